@@ -331,7 +331,7 @@ def _plan(s):
     pos = before[at] + t - (ends - rows)[at]
     held = t < ends[-1]
     slot = new[at, (pos // blk).clamp(0, width - 1)] * blk + pos % blk
-    taken = torch.where(ok, upto, 0).max()
+    taken = torch.where(ok & (need > 0), upto, 0).max()
     return {"tables": new, "free_list": ring, "free_out": torch.stack([head + taken, tail + back.sum()]),
             "row_start": row_start.int(), "kv_len": torch.where(ok, after, 0).int(),
             "status": torch.where(ok, 0, torch.where(~good, 2, torch.where(~fits, 3, 1))).int(),
