@@ -619,6 +619,184 @@ CODEC_API codec_status codec_vocos_decode(codec_vocos_t* vocos, const float* mel
                                           const int32_t* stream_ids, int32_t B, int32_t T_max, float* audio,
                                           void* stream);
 
+/*
+ * Attention operators of the codec LM: the autoregressive model in front of
+ * the decoder that reads a prompt (text, a voice sample) and emits one code
+ * frame per stream and step.  They are one attention layer's work between its
+ * q/K/V and output projections, over a cache of keys and values in blocks:
+ *   codec_lm_plan          which cache blocks and slots a call's new tokens get
+ *   codec_lm_rotate        per-head RMSNorm of queries and keys, position
+ *                          rotation, keys and values into their slots
+ *   codec_lm_prompt        causal attention of whole prompts, packed
+ *   codec_lm_prompt_paged  the same behind a context that is in the cache
+ *   codec_lm_step          attention of one token per request, with the part
+ *                          of the context that all requests share read once
+ * An object holds the shape, the rotation table and the workspace; the caches
+ * are the caller's, one pair per layer, so one object serves all layers.
+ * Independent of codec_t.
+ *
+ * All lengths, tables and slots are device memory, so a captured graph of
+ * these calls serves every step whose row count it was captured for.
+ *
+ * Cache: k_cache, v_cache [n_blocks][block_size][kv_heads][head_dim]; position
+ * p of request b is row p % block_size of block tables[b][p / block_size], and
+ * its slot is block * block_size + p % block_size.  Query head h reads K/V head
+ * h / (q_heads / kv_heads).  Cache rows at and behind a request's length are
+ * never part of a result, whatever they hold.
+ *
+ * Device data is checked where it is used, and no value of it makes a kernel
+ * read or write outside the caller's arrays; what is wrong sets a sticky bit
+ * that codec_lm_errors returns:
+ */
+#define CODEC_LM_ERR_BLOCK 1u     /* a block id outside [0, n_blocks): its keys and values read as zeros */
+#define CODEC_LM_ERR_SLOT 2u      /* a slot outside the cache (and not -1): the row was skipped */
+#define CODEC_LM_ERR_POSITION 4u  /* a position outside [0, max_positions): the row was skipped */
+#define CODEC_LM_ERR_LENGTH 8u    /* a length outside [0, table_blocks * block_size], or a row_start that falls
+                                   * or passes the row count: taken as the nearest valid value */
+#define CODEC_LM_ERR_FREE 16u     /* codec_lm_plan: the free counters do not describe a ring of n_blocks */
+#define CODEC_LM_ERR_TIMEOUT 0x80000000u /* a tensor-core kernel gave up on a bounded wait: outputs not valid */
+
+typedef enum codec_lm_type { CODEC_LM_BF16 = 0, CODEC_LM_FP16 = 1, CODEC_LM_FP32 = 2 } codec_lm_type;
+
+typedef struct codec_lm_config {
+    int32_t type;              /* of queries, keys, values, cache and outputs: CODEC_LM_BF16 or CODEC_LM_FP16 */
+    int32_t q_heads, kv_heads; /* q_heads = 1 .. 16 times kv_heads, at most 256 */
+    int32_t head_dim;          /* 64 or 128 */
+    int32_t block_size;        /* 16, 32, 64 or 128 positions */
+    int32_t n_blocks;          /* blocks of a cache; n_blocks * block_size < 2^31 - 128 */
+    int32_t table_blocks;      /* width of a block table; table_blocks * block_size <= 2^30 */
+    int32_t max_requests;      /* per call, 1 .. 4096 */
+    int32_t max_rows;          /* query rows per call, 1 .. 2^24 */
+    int32_t max_positions;     /* positions the rotation knows (0: table_blocks * block_size) */
+    int32_t rope_pairs;        /* 0: element i turns with i + head_dim / 2; 1: element 2 i with 2 i + 1 */
+    float rope_theta;          /* angle of pair i at position p: p * theta^(-2 i / head_dim) */
+    float rms_eps;
+    float scale;               /* of the scores (0: 1 / sqrt(head_dim)) */
+} codec_lm_config;
+
+typedef struct codec_lm_s codec_lm_t;
+
+/* Allocates everything on the current device.  A codec_lm_t is used by one
+ * host thread at a time and its calls go to one stream at a time (they share
+ * the workspace; graphs that hold calls of one object may not run at the same
+ * time).  Every call allocates nothing, synchronises nothing and may be
+ * captured.  Errors: CODEC_ERR_NULL, CODEC_ERR_CONFIG, CODEC_ERR_NO_DEVICE,
+ * CODEC_ERR_OOM, CODEC_ERR_CUDA. */
+CODEC_API codec_status codec_lm_create(const codec_lm_config* cfg, codec_lm_t** out);
+
+/* Synchronises the device, then frees everything. */
+CODEC_API void codec_lm_destroy(codec_lm_t* lm);
+
+/* *bits: the CODEC_LM_ERR_* bits set since they were last cleared; clear != 0
+ * clears them.  Synchronises stream.  Errors: CODEC_ERR_NULL, CODEC_ERR_CUDA. */
+CODEC_API codec_status codec_lm_errors(codec_lm_t* lm, uint32_t* bits, int32_t clear, void* stream);
+
+/*
+ * Blocks and slots for a call's new tokens, from the requests' lengths.
+ * Request b holds len_before[b] positions and is to hold len_after[b].  A
+ * request that grows gets rows for its new positions, packed in request order,
+ * and the blocks it lacks; one that shrinks (0: it ended) gives the blocks
+ * behind its new length back.  Its first shared_blocks blocks are shared_table
+ * and are never taken or given back.
+ *   free_list  int32 [n_blocks], a ring of block ids; free_in int64 [2] counts
+ *              the ids ever taken out of and put into it, so that ids
+ *              free_in[0] .. free_in[1] - 1 (mod n_blocks) are free.  Ids are
+ *              taken and put back in request order; those that are given back
+ *              here can be taken by the next call.  free_out [2]: the counts
+ *              afterwards (not the same memory as free_in).
+ *   tables     int32 [B][table_blocks]: new entries are written, and the shared
+ *              ones of a request that starts (len_before <= shared_blocks *
+ *              block_size); entries behind the new length stay as they were.
+ *   row_start  int32 [B + 1]: request b's rows are row_start[b] .. row_start[b + 1] - 1.
+ *   kv_len     int32 [B]: len_after, or 0 where status is not 0.
+ *   status     int32 [B]: 0; 1 the free blocks ran out at or before this request
+ *              (one that needs none is still served); 2 a length outside [0,
+ *              table_blocks * block_size] (no rows); 3 its rows pass max_rows.
+ *              Where it is not 0 the request's blocks stay as they were.
+ *   slots, positions  int32 [max_rows]: of each row; a row of a request that
+ *              failed has slot -1, one behind the last request slot -1 and position 0.
+ * All arrays device memory.  A repeated call with the same inputs writes the
+ * same outputs, in-place ones included.
+ * Errors (nothing enqueued): CODEC_ERR_NULL (shared_table may be NULL when
+ * shared_blocks is 0), CODEC_ERR_ARG (B or max_rows < 1, shared_blocks outside
+ * [0, table_blocks], free_out == free_in), CODEC_ERR_CAPACITY (B or max_rows
+ * above the object's); CODEC_ERR_CUDA if the launch fails.
+ */
+CODEC_API codec_status codec_lm_plan(codec_lm_t* lm, const int32_t* len_before, const int32_t* len_after, int32_t B,
+                                     int32_t* tables, const int32_t* shared_table, int32_t shared_blocks,
+                                     int32_t* free_list, const int64_t* free_in, int64_t* free_out,
+                                     int32_t* row_start, int32_t* kv_len, int32_t* status, int32_t* slots,
+                                     int32_t* positions, int32_t max_rows, void* stream);
+
+/*
+ * Queries and keys of a projection: y = x / sqrt(mean(x^2) + rms_eps) * gain
+ * over each head (gains NULL: y = x), then the rotation by the row's position;
+ * queries to q_out [rows][q_heads][head_dim], keys and values to the slots of
+ * k_dst and v_dst (a cache pair).  Computed in fp32 and rounded once.
+ *   q, k, v    rows of in_type (the object's type, or CODEC_LM_FP32), *_stride
+ *              elements apart, the heads of a row back to back
+ *   q_gain, k_gain  float [head_dim]; both or neither
+ *   positions  int32 [rows];  slots int32 [rows], different from one another:
+ *              a row of slot -1 is left out (q_out's row stays as it was).
+ *              slots NULL: row i goes to row i of k_dst, v_dst [rows][kv_heads]
+ *              [head_dim], and v and v_dst may be NULL (values stay where they are).
+ * q, k, v and the destinations 16-byte aligned, strides multiples of 16 bytes;
+ * q_out may be q itself (of the object's type, stride q_heads * head_dim), else
+ * nothing overlaps.
+ * Errors: CODEC_ERR_NULL, CODEC_ERR_ARG (rows < 0, in_type, a stride below the
+ * row or misaligned, one gain without the other), CODEC_ERR_CAPACITY (rows >
+ * max_rows), CODEC_ERR_CUDA.
+ */
+CODEC_API codec_status codec_lm_rotate(codec_lm_t* lm, const void* q, int64_t q_stride, const void* k,
+                                       int64_t k_stride, const void* v, int64_t v_stride, int32_t in_type,
+                                       int32_t rows, const float* q_gain, const float* k_gain,
+                                       const int32_t* positions, const int32_t* slots, void* q_out, void* k_dst,
+                                       void* v_dst, void* stream);
+
+/*
+ * Causal attention of B whole prompts packed back to back: row i of request b
+ * (rows row_start[b] .. row_start[b + 1] - 1) attends rows 0 .. i of the same
+ * request.  o = softmax(scale q k^T) v, lse = log(sum(exp(scale q k^T))).
+ *   q, k, v    rows of the object's type, *_stride elements apart, heads back to
+ *              back (k and v as codec_lm_rotate leaves them with slots NULL)
+ *   row_start  int32 [B + 1], device
+ *   o          rows o_stride elements apart; rows behind row_start[B] stay as
+ *              they were.  lse float [rows][q_heads], or NULL.
+ * Pointers 16-byte aligned, strides multiples of 8 elements.  o overlaps
+ * nothing else.  Scores, softmax statistics and sums are fp32; probabilities
+ * are rounded to the object's type for their product with v.
+ * Errors: CODEC_ERR_NULL, CODEC_ERR_ARG (B < 1, rows < 0, stride or alignment),
+ * CODEC_ERR_CAPACITY, CODEC_ERR_CUDA.
+ */
+CODEC_API codec_status codec_lm_prompt(codec_lm_t* lm, const void* q, int64_t q_stride, const void* k,
+                                       int64_t k_stride, const void* v, int64_t v_stride, int32_t rows,
+                                       const int32_t* row_start, int32_t B, void* o, int64_t o_stride, float* lse,
+                                       void* stream);
+
+/* The same with keys and values in a cache: request b's n rows are the last n
+ * of its kv_len[b] positions, and row i attends positions 0 .. kv_len[b] - n + i
+ * of its table (int32 [B][table_blocks]).  A row that this leaves without a key
+ * (kv_len[b] < n) gets zeros and an lse of -inf. */
+CODEC_API codec_status codec_lm_prompt_paged(codec_lm_t* lm, const void* q, int64_t q_stride, int32_t rows,
+                                             const int32_t* row_start, int32_t B, const void* k_cache,
+                                             const void* v_cache, const int32_t* tables, const int32_t* kv_len,
+                                             void* o, int64_t o_stride, float* lse, void* stream);
+
+/*
+ * One token per request: row b of q attends positions 0 .. kv_len[b] - 1 of
+ * request b (its own among them); kv_len[b] == 0: zeros, lse -inf.
+ * shared_blocks > 0: positions below shared_blocks * block_size are those of
+ * shared_table (int32 [shared_blocks], device) for every request - the entries
+ * of tables for them are not read - and their keys and values are read once
+ * for the whole batch.  A request's result does not depend on the others of
+ * the batch.  Errors as codec_lm_prompt (CODEC_ERR_ARG also for shared_blocks
+ * outside [0, table_blocks]).
+ */
+CODEC_API codec_status codec_lm_step(codec_lm_t* lm, const void* q, int64_t q_stride, int32_t B, const void* k_cache,
+                                     const void* v_cache, const int32_t* tables, const int32_t* kv_len,
+                                     const int32_t* shared_table, int32_t shared_blocks, void* o, int64_t o_stride,
+                                     float* lse, void* stream);
+
 /* Static description of a status code. */
 CODEC_API const char* codec_status_string(codec_status status);
 

@@ -123,6 +123,14 @@ class VocosConfigC(ctypes.Structure):
                 ("max_batch_frames", ctypes.c_int32), ("precision", ctypes.c_int32)]
 
 
+class LmConfigC(ctypes.Structure):
+    _fields_ = [("type", ctypes.c_int32), ("q_heads", ctypes.c_int32), ("kv_heads", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32), ("block_size", ctypes.c_int32), ("n_blocks", ctypes.c_int32),
+                ("table_blocks", ctypes.c_int32), ("max_requests", ctypes.c_int32), ("max_rows", ctypes.c_int32),
+                ("max_positions", ctypes.c_int32), ("rope_pairs", ctypes.c_int32), ("rope_theta", ctypes.c_float),
+                ("rms_eps", ctypes.c_float), ("scale", ctypes.c_float)]
+
+
 class StreamInfoC(ctypes.Structure):
     _fields_ = [("frames_decoded", ctypes.c_int64), ("error_bits", ctypes.c_uint32),
                 ("reserved", ctypes.c_int32)]
@@ -184,6 +192,14 @@ def _lib():
             "codec_vocos_destroy": (None, [_P]),
             "codec_vocos_reset": (i32, [_P, _I32P, i32, _P]),
             "codec_vocos_decode": (i32, [_P, _P, _I32P, _I32P, i32, i32, _P, _P]),
+            "codec_lm_create": (i32, [ctypes.POINTER(LmConfigC), ctypes.POINTER(_P)]),
+            "codec_lm_destroy": (None, [_P]),
+            "codec_lm_errors": (i32, [_P, ctypes.POINTER(ctypes.c_uint32), i32, _P]),
+            "codec_lm_plan": (i32, [_P, _P, _P, i32, _P, _P, i32, _P, _P, _P, _P, _P, _P, _P, _P, i32, _P]),
+            "codec_lm_rotate": (i32, [_P, _P, i64, _P, i64, _P, i64, i32, i32, _P, _P, _P, _P, _P, _P, _P, _P]),
+            "codec_lm_prompt": (i32, [_P, _P, i64, _P, i64, _P, i64, i32, _P, i32, _P, i64, _P, _P]),
+            "codec_lm_prompt_paged": (i32, [_P, _P, i64, i32, _P, i32, _P, _P, _P, _P, _P, i64, _P, _P]),
+            "codec_lm_step": (i32, [_P, _P, i64, i32, _P, _P, _P, _P, _P, i32, _P, i64, _P, _P]),
             "codec_stft_create": (i32, [ctypes.POINTER(StftConfigC), ctypes.POINTER(_P)]),
             "codec_stft_destroy": (None, [_P]),
             "codec_stft_reset": (i32, [_P, _I32P, i32, _P]),
@@ -468,6 +484,169 @@ class Stft(_Streamed):
     def decode(self, x, n_frames, spec, stream_ids=None, stream=None):
         """x: float32 CUDA [B][T_max][hop]; spec: float32 CUDA [B][T_max][2 n_bins]."""
         self._decode(x, n_frames, spec, stream_ids, stream, self.hop, 2 * self.n_bins)
+
+
+LM_TYPES = {"bf16": 0, "fp16": 1, "fp32": 2}
+LM_ERR_BLOCK, LM_ERR_SLOT, LM_ERR_POSITION, LM_ERR_LENGTH, LM_ERR_FREE = 1, 2, 4, 8, 16
+LM_ERR_TIMEOUT = 0x80000000
+
+
+class Lm:
+    """codec_lm_*: the attention operators of the codec LM in front of the
+    decoder, over a cache of keys and values in blocks.  Every tensor is a CUDA
+    tensor of the object's device (the one current here); nothing is allocated
+    or synchronised by a call, so calls may be captured into a CUDA graph.
+    dtype: "bf16" or "fp16", the type of queries, keys, values and outputs."""
+
+    def __init__(self, q_heads: int, kv_heads: int, head_dim: int, dtype: str = "bf16", block_size: int = 16,
+                 n_blocks: int = 1, table_blocks: int = 1, max_requests: int = 64, max_rows: int = 4096,
+                 max_positions: int = 0, rope_theta: float = 1e6, rope_pairs: bool = False, rms_eps: float = 1e-6,
+                 scale: float = 0.0):
+        import torch
+        if dtype not in ("bf16", "fp16"):
+            raise ValueError('dtype must be "bf16" or "fp16"')
+        c = LmConfigC(LM_TYPES[dtype], q_heads, kv_heads, head_dim, block_size, n_blocks, table_blocks, max_requests,
+                      max_rows, max_positions, int(rope_pairs), rope_theta, rms_eps, scale)
+        h = _P()
+        _check(_lib().codec_lm_create(ctypes.byref(c), ctypes.byref(h)), "codec_lm_create")
+        self._h = h
+        self.cfg_c = c
+        self.device = torch.device("cuda", torch.cuda.current_device())
+        self.dtype = torch.bfloat16 if dtype == "bf16" else torch.float16
+        self._torch = torch
+        self._cache_shape = (n_blocks, block_size, kv_heads, head_dim)
+
+    def close(self):
+        if getattr(self, "_h", None):
+            _lib().codec_lm_destroy(self._h)
+            self._h = None
+
+    def __del__(self):
+        self.close()
+
+    def _stream(self, stream):
+        return (self._torch.cuda.current_stream(self.device) if stream is None else stream).cuda_stream
+
+    def _flat(self, name, t, dtype, shape):
+        """Address of a contiguous tensor of exactly this type and shape."""
+        if t.dtype != dtype or t.device != self.device or tuple(t.shape) != shape or not t.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous {dtype} tensor {shape} on {self.device}, got {t.dtype} "
+                             f"{tuple(t.shape)} on {t.device}")
+        return t.data_ptr()
+
+    def _rows(self, name, t, heads, rows=None, dtype=None):
+        """Address and row stride of [rows][heads][head_dim] whose rows may lie apart."""
+        d = self.cfg_c.head_dim
+        if (t.dtype != (dtype or self.dtype) or t.device != self.device or t.dim() != 3 or t.shape[1] != heads
+                or t.shape[2] != d or (rows is not None and t.shape[0] != rows)):
+            raise ValueError(f"{name} must be {dtype or self.dtype} [{'rows' if rows is None else rows}][{heads}][{d}] "
+                             f"on {self.device}, got {t.dtype} {tuple(t.shape)} on {t.device}")
+        if t.shape[0] > 1:
+            stride = t.stride(0)
+        else:
+            stride = heads * d
+        if t.stride(2) != 1 or (heads > 1 and t.stride(1) != d):
+            raise ValueError(f"{name}: the heads of a row must lie back to back")
+        return t.data_ptr(), stride
+
+    def _caches(self, k_cache, v_cache):
+        return (self._flat("k_cache", k_cache, self.dtype, self._cache_shape),
+                self._flat("v_cache", v_cache, self.dtype, self._cache_shape))
+
+    def _lse(self, lse, rows):
+        return None if lse is None else self._flat("lse", lse, self._torch.float32, (rows, self.cfg_c.q_heads))
+
+    def _shared(self, shared_table):
+        n = 0 if shared_table is None else shared_table.numel()
+        return (self._flat("shared_table", shared_table, self._torch.int32, (n,)) if n else None), n
+
+    def plan(self, len_before, len_after, tables, free_list, free_in, free_out, row_start, kv_len, status, slots,
+             positions, shared_table=None, stream=None):
+        """codec_lm_plan: blocks and slots for the new tokens.  int32 len_before,
+        len_after, kv_len, status [B]; tables [B][table_blocks]; free_list
+        [n_blocks]; row_start [B + 1]; slots, positions [rows at most]; int64
+        free_in, free_out [2]; shared_table int32 [shared blocks] or None."""
+        c, i32, i64 = self.cfg_c, self._torch.int32, self._torch.int64
+        B, rows = len_before.numel(), slots.numel()
+        f = self._flat
+        shared, n_shared = self._shared(shared_table)
+        _check(_lib().codec_lm_plan(
+            self._h, f("len_before", len_before, i32, (B,)), f("len_after", len_after, i32, (B,)), B,
+            f("tables", tables, i32, (B, c.table_blocks)), shared, n_shared,
+            f("free_list", free_list, i32, (c.n_blocks,)), f("free_in", free_in, i64, (2,)),
+            f("free_out", free_out, i64, (2,)), f("row_start", row_start, i32, (B + 1,)),
+            f("kv_len", kv_len, i32, (B,)), f("status", status, i32, (B,)), f("slots", slots, i32, (rows,)),
+            f("positions", positions, i32, (rows,)), rows, self._stream(stream)), "codec_lm_plan")
+
+    def rotate(self, q, k, v, positions, slots, q_out, k_dst, v_dst, q_gain=None, k_gain=None, stream=None):
+        """codec_lm_rotate: q [rows][q_heads][head_dim], k and v [rows][kv_heads]
+        [head_dim] of the object's type or float32, rows any distance apart (views
+        of one fused projection); positions, slots int32 [rows]; q_out contiguous
+        in the object's type; k_dst, v_dst the cache.  slots None: k_dst (and v_dst,
+        or v and v_dst None) are contiguous [rows][kv_heads][head_dim]."""
+        c, t = self.cfg_c, self._torch
+        rows, fused = q.shape[0], q.dtype
+        if rows == 0:
+            return
+        if fused != self.dtype and fused != t.float32:
+            raise ValueError(f"q must be {self.dtype} or torch.float32")
+        qp, qs = self._rows("q", q, c.q_heads, None, fused)
+        kp, ks = self._rows("k", k, c.kv_heads, rows, fused)
+        vp, vs = (None, 0) if v is None else self._rows("v", v, c.kv_heads, rows, fused)
+        dst = self._cache_shape if slots is not None else (rows, c.kv_heads, c.head_dim)
+        gains = [None if g is None else self._flat("gain", g, t.float32, (c.head_dim,)) for g in (q_gain, k_gain)]
+        _check(_lib().codec_lm_rotate(
+            self._h, qp, qs, kp, ks, vp, vs, LM_TYPES["fp32"] if fused == t.float32 else c.type, rows, *gains,
+            self._flat("positions", positions, t.int32, (rows,)),
+            None if slots is None else self._flat("slots", slots, t.int32, (rows,)),
+            self._flat("q_out", q_out, self.dtype, (rows, c.q_heads, c.head_dim)),
+            self._flat("k_dst", k_dst, self.dtype, dst),
+            None if v_dst is None else self._flat("v_dst", v_dst, self.dtype, dst), self._stream(stream)),
+            "codec_lm_rotate")
+
+    def prompt(self, q, k, v, row_start, o, lse=None, stream=None):
+        """codec_lm_prompt: causal attention of packed whole prompts.  q, o
+        [rows][q_heads][head_dim], k, v [rows][kv_heads][head_dim], row_start
+        int32 [B + 1], lse float32 [rows][q_heads] or None."""
+        c = self.cfg_c
+        rows, B = q.shape[0], row_start.numel() - 1
+        if rows == 0:
+            return
+        _check(_lib().codec_lm_prompt(
+            self._h, *self._rows("q", q, c.q_heads), *self._rows("k", k, c.kv_heads, rows),
+            *self._rows("v", v, c.kv_heads, rows), rows, self._flat("row_start", row_start, self._torch.int32, (B + 1,)),
+            B, *self._rows("o", o, c.q_heads, rows), self._lse(lse, rows), self._stream(stream)), "codec_lm_prompt")
+
+    def prompt_paged(self, q, k_cache, v_cache, row_start, tables, kv_len, o, lse=None, stream=None):
+        """codec_lm_prompt_paged: the same over the cache; each request's rows are
+        the last ones of its kv_len positions."""
+        c, i32 = self.cfg_c, self._torch.int32
+        rows, B = q.shape[0], row_start.numel() - 1
+        if rows == 0:
+            return
+        _check(_lib().codec_lm_prompt_paged(
+            self._h, *self._rows("q", q, c.q_heads), rows, self._flat("row_start", row_start, i32, (B + 1,)), B,
+            *self._caches(k_cache, v_cache), self._flat("tables", tables, i32, (B, c.table_blocks)),
+            self._flat("kv_len", kv_len, i32, (B,)), *self._rows("o", o, c.q_heads, rows), self._lse(lse, rows),
+            self._stream(stream)), "codec_lm_prompt_paged")
+
+    def step(self, q, k_cache, v_cache, tables, kv_len, o, shared_table=None, lse=None, stream=None):
+        """codec_lm_step: one token per request; q, o [B][q_heads][head_dim].
+        shared_table: int32 ids of the blocks that every request starts with."""
+        c, i32 = self.cfg_c, self._torch.int32
+        B = q.shape[0]
+        shared, n_shared = self._shared(shared_table)
+        _check(_lib().codec_lm_step(
+            self._h, *self._rows("q", q, c.q_heads), B, *self._caches(k_cache, v_cache),
+            self._flat("tables", tables, i32, (B, c.table_blocks)), self._flat("kv_len", kv_len, i32, (B,)), shared,
+            n_shared, *self._rows("o", o, c.q_heads, B), self._lse(lse, B), self._stream(stream)), "codec_lm_step")
+
+    def errors(self, clear: bool = True, stream=None) -> int:
+        """codec_lm_errors: the LM_ERR_* bits set since last cleared (synchronises the stream)."""
+        bits = ctypes.c_uint32()
+        _check(_lib().codec_lm_errors(self._h, ctypes.byref(bits), 1 if clear else 0, self._stream(stream)),
+               "codec_lm_errors")
+        return bits.value
 
 
 class Codec:

@@ -1,0 +1,113 @@
+// Internal launchers of the codec LM's attention operators (lm_*.cu).
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "codec.h"
+#include "common.cuh"
+
+namespace codec {
+
+// Rows of requests and where their keys and values are.  Packed: K/V rows of
+// request b are row_start[b] ..; paged: position p is in block
+// tables[b][p / bs] of the cache.
+struct LmKeys {
+    const void* k;
+    const void* v;
+    long long k_stride, v_stride;   // packed: elements between rows
+    const int* tables;              // paged: [B][table_blocks]; null: packed
+    const int* kv_len;              // paged: [B]
+    int table_blocks;
+    int bs_shift;                   // log2(block_size)
+    int n_blocks;
+};
+
+struct LmShape {
+    int type;                       // CODEC_LM_BF16 / CODEC_LM_FP16
+    int hq, hk, group, D;
+    float scale;
+    unsigned* err;
+};
+
+struct LmPlanArgs {
+    const int* before;
+    const int* after;
+    int B;
+    int* tables;
+    const int* shared_table;
+    int shared_blocks;
+    int table_blocks, bs_shift, n_blocks;
+    int* free_list;
+    const long long* free_in;
+    long long* free_out;
+    int *row_start, *kv_len, *status, *slots, *positions;
+    int max_rows;
+    unsigned* err;
+};
+size_t lm_plan_smem(int B);
+constexpr int kLmMaxRequests = 4096;
+cudaError_t configure_lm_plan();
+cudaError_t launch_lm_plan(const LmPlanArgs& a, cudaStream_t s);
+
+struct LmRotateArgs {
+    const void *q, *k, *v;
+    long long qs, ks, vs;           // row strides, elements
+    int rows;
+    const float *q_gain, *k_gain;
+    const int *positions, *slots;
+    long long n_slots;
+    void *q_out, *k_dst, *v_dst;
+    const float2* turn;             // [max_positions][D / 2] cos, sin
+    int max_positions;
+    float eps;
+    int pairs;
+};
+cudaError_t launch_lm_rotate(const LmShape& sh, const LmRotateArgs& a, int in_type, cudaStream_t s);
+cudaError_t launch_lm_turn_table(float2* turn, int max_positions, int D, double theta, cudaStream_t s);
+
+struct LmPromptArgs {
+    const void* q;
+    long long qs;
+    int rows;
+    const int* row_start;
+    int B;
+    LmKeys keys;
+    void* o;
+    long long os;
+    float* lse;
+};
+cudaError_t launch_lm_prompt(const LmShape& sh, const LmPromptArgs& a, cudaStream_t s);
+
+struct LmStepArgs {
+    const void* q;
+    long long qs;
+    int B;
+    LmKeys keys;
+    const int* shared_table;
+    int shared_blocks;
+    void* o;
+    long long os;
+    float* lse;
+};
+cudaError_t launch_lm_step(const LmShape& sh, const LmStepArgs& a, cudaStream_t s);
+
+// Rows of request b, from a row_start that is device data: inside [0, rows]
+// and never negative in number.  False: it was not, and was bent to fit.
+__device__ __forceinline__ bool lm_rows(const int* row_start, int b, int rows, int& first, int& n)
+{
+    const int a = __ldg(row_start + b), e = __ldg(row_start + b + 1);
+    first = min(max(a, 0), rows);
+    const int end = min(max(e, first), rows);
+    n = end - first;
+    return first == a && end == e;
+}
+
+__device__ __forceinline__ bool lm_clamp_len(int& n, long long most)
+{
+    const int want = n;
+    n = (int)min(max((long long)n, 0LL), most);
+    return n == want;
+}
+
+}  // namespace codec

@@ -1,0 +1,227 @@
+// Per-head RMSNorm of queries and keys, position rotation, and the store of
+// keys and values into their cache slots, in one pass over a projection's
+// output.
+//
+// y = x / sqrt(mean(x^2) + eps) * gain, then pair (a, b) -> (a c - b s, b c + a s)
+// with the cosine and sine of the row's angle, from a table that is computed
+// in fp64 (at position 60,000 an fp32 angle would be off by 2^-9).  All in
+// fp32, one rounding at the store.
+//
+// Bound by memory: every value is read and written once.  A head is the work
+// of D / 16 lanes; each holds 8 elements of the first half and the 8 elements
+// D / 2 further, so that both rotation forms stay inside a lane, every access
+// is 16 bytes, and the norm is 2 or 3 shuffles.  A row's cosines and sines are
+// read once per warp and kept in registers over its heads.
+#include "lm.h"
+
+namespace codec {
+
+namespace {
+
+constexpr int kRotThreads = 256;
+
+template <typename T> struct Pack;      // 8 values of 16 bits
+template <> struct Pack<__nv_bfloat16> {
+    static __device__ __forceinline__ uint32_t two(float a, float b)
+    {
+        const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
+        return *reinterpret_cast<const uint32_t*>(&v);
+    }
+    static __device__ __forceinline__ float2 un(uint32_t w)
+    {
+        return __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&w));
+    }
+};
+template <> struct Pack<__half> {
+    static __device__ __forceinline__ uint32_t two(float a, float b)
+    {
+        const __half2 v = __floats2half2_rn(a, b);
+        return *reinterpret_cast<const uint32_t*>(&v);
+    }
+    static __device__ __forceinline__ float2 un(uint32_t w)
+    {
+        return __half22float2(*reinterpret_cast<const __half2*>(&w));
+    }
+};
+
+template <typename T>
+__device__ __forceinline__ void load8(const T* p, float* x)
+{
+    const uint4 w = *reinterpret_cast<const uint4*>(p);   // q may be q_out: not the read-only path
+    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+        const float2 f = Pack<T>::un(u[i]);
+        x[2 * i] = f.x;
+        x[2 * i + 1] = f.y;
+    }
+}
+__device__ __forceinline__ void load8(const float* p, float* x)
+{
+    const float4 a = *reinterpret_cast<const float4*>(p), b = *(reinterpret_cast<const float4*>(p) + 1);
+    x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
+    x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
+}
+
+template <typename T>
+__device__ __forceinline__ void store8(T* p, const float* x)
+{
+    *reinterpret_cast<uint4*>(p) = make_uint4(Pack<T>::two(x[0], x[1]), Pack<T>::two(x[2], x[3]),
+                                              Pack<T>::two(x[4], x[5]), Pack<T>::two(x[6], x[7]));
+}
+
+// Warp w of the grid: row w / parts, and every parts-th group of heads of it.
+template <typename T, typename TI, int D>
+__global__ void __launch_bounds__(kRotThreads) lm_rotate_kernel(const LmRotateArgs a, int hq, int hk, int parts,
+                                                                unsigned* err)
+{
+    constexpr int kLanes = D / 16, kGroups = 32 / kLanes;
+    const int warp = (int)((blockIdx.x * (long long)kRotThreads + threadIdx.x) >> 5);
+    const int row = warp / parts, part = warp - row * parts;
+    if (row >= a.rows) return;
+    const int lane = threadIdx.x & 31, g = lane / kLanes, c = (lane % kLanes) * 8;
+    long long slot = row;
+    if (a.slots) {
+        slot = __ldg(a.slots + row);
+        if (slot == -1) return;
+        if (slot < 0 || slot >= a.n_slots) {
+            if (lane == 0) atomicOr(err, CODEC_LM_ERR_SLOT);
+            return;
+        }
+    }
+    const int pos = __ldg(a.positions + row);
+    if (pos < 0 || pos >= a.max_positions) {
+        if (lane == 0) atomicOr(err, CODEC_LM_ERR_POSITION);
+        return;
+    }
+    // cos, sin of this lane's eight rotations: pair index c + i (halves), or
+    // c / 2 + i and D / 4 + c / 2 + i (pairs)
+    float cs[8], sn[8];
+    {
+        const float2* t = a.turn + (long long)pos * (D / 2);
+#pragma unroll
+        for (int i = 0; i < 8; i += 2) {
+            const int at = a.pairs ? (i < 4 ? c / 2 + i : D / 4 + c / 2 + i - 4) : c + i;
+            const float4 v = __ldg(reinterpret_cast<const float4*>(t + at));
+            cs[i] = v.x; sn[i] = v.y;
+            cs[i + 1] = v.z; sn[i + 1] = v.w;
+        }
+    }
+    const int heads = hq + hk + (a.v ? hk : 0);
+    for (int h0 = part * kGroups; h0 < heads; h0 += parts * kGroups) {
+        const int h = h0 + g;
+        const bool live = h < heads;
+        const bool is_q = h < hq, is_v = h >= hq + hk;
+        const TI* src = nullptr;
+        T* dst = nullptr;
+        if (live) {
+            if (is_q) {
+                src = static_cast<const TI*>(a.q) + row * a.qs + (long long)h * D;
+                dst = static_cast<T*>(a.q_out) + ((long long)row * hq + h) * D;
+            } else if (!is_v) {
+                src = static_cast<const TI*>(a.k) + row * a.ks + (long long)(h - hq) * D;
+                dst = static_cast<T*>(a.k_dst) + (slot * hk + (h - hq)) * D;
+            } else {
+                src = static_cast<const TI*>(a.v) + row * a.vs + (long long)(h - hq - hk) * D;
+                dst = static_cast<T*>(a.v_dst) + (slot * hk + (h - hq - hk)) * D;
+            }
+        }
+        float x[8] = {}, y[8] = {};
+        if (live) {
+            load8(src + c, x);
+            load8(src + D / 2 + c, y);
+        }
+        if (a.q_gain) {
+            float ss = 0.f;
+#pragma unroll
+            for (int i = 0; i < 8; i++) ss = fmaf(x[i], x[i], fmaf(y[i], y[i], ss));
+#pragma unroll
+            for (int o = kLanes / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+            if (!is_v) {
+                const float r = 1.f / sqrtf(ss * (1.f / D) + a.eps);
+                const float* gain = is_q ? a.q_gain : a.k_gain;
+                float gx[8], gy[8];
+                load8(gain + c, gx);
+                load8(gain + D / 2 + c, gy);
+#pragma unroll
+                for (int i = 0; i < 8; i++) {
+                    x[i] = x[i] * r * gx[i];
+                    y[i] = y[i] * r * gy[i];
+                }
+            }
+        }
+        if (!is_v) {
+            if (a.pairs) {
+#pragma unroll
+                for (int i = 0; i < 4; i++) {
+                    const float p = x[2 * i], q = x[2 * i + 1], u = y[2 * i], w = y[2 * i + 1];
+                    x[2 * i] = p * cs[i] - q * sn[i];
+                    x[2 * i + 1] = q * cs[i] + p * sn[i];
+                    y[2 * i] = u * cs[4 + i] - w * sn[4 + i];
+                    y[2 * i + 1] = w * cs[4 + i] + u * sn[4 + i];
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < 8; i++) {
+                    const float p = x[i], q = y[i];
+                    x[i] = p * cs[i] - q * sn[i];
+                    y[i] = q * cs[i] + p * sn[i];
+                }
+            }
+        }
+        if (live) {
+            store8(dst + c, x);
+            store8(dst + D / 2 + c, y);
+        }
+    }
+}
+
+// The angle p theta^(-2 i / D) and its cosine and sine in fp64, rounded once.
+__global__ void lm_turn_table_kernel(float2* turn, long long n, int half, double log2_theta)
+{
+    const long long u = blockIdx.x * (long long)blockDim.x + threadIdx.x;
+    if (u >= n) return;
+    const int p = (int)(u / half), i = (int)(u - (long long)p * half);
+    double s, c;
+    sincos((double)p * exp2(-log2_theta * i / half), &s, &c);
+    turn[u] = make_float2((float)c, (float)s);
+}
+
+template <typename T, typename TI, int D>
+cudaError_t launch(const LmShape& sh, const LmRotateArgs& a, cudaStream_t s)
+{
+    constexpr int kGroups = 32 / (D / 16);
+    const int heads = sh.hq + sh.hk + (a.v ? sh.hk : 0);
+    // few rows: spread a row's heads over warps until there are about 16 warps per SM
+    const int most = (heads + kGroups - 1) / kGroups;
+    int parts = 1;
+    while (parts < most && (long long)a.rows * parts < 152 * 16) parts++;
+    const long long warps = (long long)a.rows * parts;
+    const unsigned ctas = (unsigned)((warps + kRotThreads / 32 - 1) / (kRotThreads / 32));
+    lm_rotate_kernel<T, TI, D><<<ctas, kRotThreads, 0, s>>>(a, sh.hq, sh.hk, parts, sh.err);
+    return cudaGetLastError();
+}
+
+template <typename T>
+cudaError_t launch_t(const LmShape& sh, const LmRotateArgs& a, bool in32, cudaStream_t s)
+{
+    if (sh.D == 128) return in32 ? launch<T, float, 128>(sh, a, s) : launch<T, T, 128>(sh, a, s);
+    return in32 ? launch<T, float, 64>(sh, a, s) : launch<T, T, 64>(sh, a, s);
+}
+
+}  // namespace
+
+cudaError_t launch_lm_rotate(const LmShape& sh, const LmRotateArgs& a, int in_type, cudaStream_t s)
+{
+    const bool in32 = in_type == CODEC_LM_FP32;
+    return sh.type == CODEC_LM_BF16 ? launch_t<__nv_bfloat16>(sh, a, in32, s) : launch_t<__half>(sh, a, in32, s);
+}
+
+cudaError_t launch_lm_turn_table(float2* turn, int max_positions, int D, double theta, cudaStream_t s)
+{
+    const long long n = (long long)max_positions * (D / 2);
+    lm_turn_table_kernel<<<(unsigned)((n + 255) / 256), 256, 0, s>>>(turn, n, D / 2, log2(theta));
+    return cudaGetLastError();
+}
+
+}  // namespace codec

@@ -76,3 +76,33 @@ def test_create_rejects_wrong_blob_length(lib):
     st = lib.codec_create(ctypes.byref(cfg), blob.ctypes.data_as(ctypes.POINTER(ctypes.c_float)), n - 1,
                           ctypes.byref(h))
     assert st == 3 and not h.value                                         # CODEC_ERR_WEIGHTS
+
+
+def test_lm_config_and_null_checks_need_no_device(lib):
+    """codec_lm_create looks at the configuration before it looks for a device,
+    and every call at its pointers before anything else."""
+    def status(**kw):
+        c = C.LmConfigC(**{**dict(type=0, q_heads=4, kv_heads=2, head_dim=64, block_size=16, n_blocks=4,
+                                  table_blocks=2, max_requests=1, max_rows=1, rope_theta=1e4, rms_eps=1e-6), **kw})
+        h = ctypes.c_void_p()
+        s = lib.codec_lm_create(ctypes.byref(c), ctypes.byref(h))
+        if h.value:
+            lib.codec_lm_destroy(h)
+        return s
+
+    assert status() in (0, 8)                                              # CODEC_OK or CODEC_ERR_NO_DEVICE
+    for bad in (dict(type=2), dict(head_dim=32), dict(q_heads=5), dict(kv_heads=0), dict(block_size=48),
+                dict(n_blocks=0), dict(n_blocks=1 << 27), dict(table_blocks=(1 << 26) + 1), dict(max_requests=4097),
+                dict(max_rows=(1 << 24) + 1), dict(rope_pairs=2), dict(rope_theta=0.5), dict(rms_eps=float("nan")),
+                dict(scale=-1.0)):
+        assert status(**bad) == 2, bad                                     # CODEC_ERR_CONFIG
+    h = ctypes.c_void_p()
+    n = None
+    assert lib.codec_lm_create(None, ctypes.byref(h)) == 1
+    assert lib.codec_lm_plan(n, n, n, 1, n, n, 0, n, n, n, n, n, n, n, n, 1, n) == 1
+    assert lib.codec_lm_rotate(n, n, 0, n, 0, n, 0, 0, 1, n, n, n, n, n, n, n, n) == 1
+    assert lib.codec_lm_prompt(n, n, 0, n, 0, n, 0, 1, n, 1, n, 0, n, n) == 1
+    assert lib.codec_lm_prompt_paged(n, n, 0, 1, n, 1, n, n, n, n, n, 0, n, n) == 1
+    assert lib.codec_lm_step(n, n, 0, 1, n, n, n, n, n, 0, n, 0, n, n) == 1
+    bits = ctypes.c_uint32()
+    assert lib.codec_lm_errors(n, ctypes.byref(bits), 0, n) == 1

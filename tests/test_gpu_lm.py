@@ -1,0 +1,612 @@
+"""The codec LM's attention operators against their definitions in 64 bits
+(whole numbers for the plan): both types, head widths and rotation forms,
+lengths from none to several tiles, strided inputs, poisoned places that no
+row may see, device data that is wrong, and a layer's run of them together."""
+from __future__ import annotations
+
+import random
+
+import numpy as np
+import pytest
+import torch
+
+import lm_ref as R
+from streaming_tts_vocoder_gb300 import codec as C
+
+pytestmark = pytest.mark.gpu
+NAN = float("nan")
+
+
+def i32(v):
+    return torch.tensor(v, dtype=torch.int32, device="cuda")
+
+
+def f64(t):
+    return t.detach().cpu().double().numpy()
+
+
+# ---- plan -------------------------------------------------------------------
+
+def plan_case(seed, B, bs, sh, width, max_rows, free, old, new, bad=False):
+    rng = random.Random(seed)
+    before = [rng.choice([0, rng.randrange(old + 1)]) + sh * bs for _ in range(B)]
+    after = [rng.choice([0, n, n + 1, n + rng.randrange(new + 1), n // 2]) for n in before]
+    if bad:
+        for i in range(0, B, 7):
+            before[i] = rng.choice([-1, -2 ** 31, width * bs + 1, 2 ** 31 - 1])
+        for i in range(3, B, 7):
+            after[i] = rng.choice([-5, width * bs + 1, 2 ** 31 - 1])
+    counts = [max(0, -(-n // bs) - sh) if 0 <= n <= width * bs else 0 for n in before]
+    n_blocks = sh + sum(counts) + free
+    ids = list(range(n_blocks))
+    rng.shuffle(ids)
+    shared, ids = ids[:sh], ids[sh:]
+    tables = [[-7] * width for _ in range(B)]
+    for b, c in enumerate(counts):
+        if before[b] > sh * bs and c:
+            tables[b][:sh] = shared
+        tables[b][sh:sh + c], ids = ids[:c], ids[c:]
+    head = rng.randrange(10 * n_blocks + 1)
+    ring = [-9] * n_blocks
+    for i, x in enumerate(ids):
+        ring[(head + i) % n_blocks] = x
+    return before, after, tables, ring, (head, head + len(ids)), shared, n_blocks
+
+
+def run_plan(lm, before, after, tables, ring, free, shared, max_rows):
+    B = len(before)
+    t = dict(tables=i32(tables), free_list=i32(ring), free_out=torch.full((2,), -1, dtype=torch.int64, device="cuda"),
+             row_start=i32([-3] * (B + 1)), kv_len=i32([-3] * B), status=i32([-3] * B), slots=i32([-3] * max_rows),
+             positions=i32([-3] * max_rows))
+    free_in = torch.tensor(free, dtype=torch.int64, device="cuda")
+    for _ in range(2):      # a repeated call writes the same
+        lm.plan(i32(before), i32(after), t["tables"], t["free_list"], free_in, t["free_out"], t["row_start"],
+                t["kv_len"], t["status"], t["slots"], t["positions"], shared_table=i32(shared) if shared else None)
+    return {k: v.tolist() for k, v in t.items()}
+
+
+@pytest.mark.parametrize("seed,B,bs,sh,width,max_rows,free,old,new,bad", [
+    (0, 1, 16, 0, 4, 1, 3, 0, 1, False),
+    (1, 7, 16, 0, 20, 600, 90, 200, 40, False),
+    (2, 64, 16, 3, 40, 5000, 400, 500, 60, False),
+    (3, 64, 32, 0, 40, 5000, 30, 500, 200, False),       # the blocks run out
+    (4, 33, 128, 2, 9, 200, 100, 300, 100, False),       # the rows run out
+    (5, 700, 64, 1, 12, 30000, 900, 400, 100, True),     # more requests than threads, wrong lengths
+    (6, 40, 16, 5, 5, 300, 0, 0, 0, False),              # nothing free, table all shared
+])
+def test_plan(seed, B, bs, sh, width, max_rows, free, old, new, bad):
+    before, after, tables, ring, fr, shared, n_blocks = plan_case(seed, B, bs, sh, width, max_rows, free, old, new, bad)
+    lm = C.Lm(8, 8, 64, block_size=bs, n_blocks=n_blocks, table_blocks=width, max_requests=B, max_rows=max_rows)
+    got = run_plan(lm, before, after, tables, ring, fr, shared, max_rows)
+    want = R.plan(before, after, tables, ring, fr, shared, bs, max_rows)
+    for k in want:
+        assert got[k] == want[k], k
+    assert lm.errors() == 0
+
+
+def test_plan_wrong_free_counts_take_nothing():
+    lm = C.Lm(8, 8, 64, n_blocks=8, table_blocks=4, max_requests=2, max_rows=40)
+    for free in [(5, 3), (-1, 2), (0, 9)]:
+        got = run_plan(lm, [0, 3], [20, 5], [[0] * 4, [1] * 4], list(range(8)), free, [], 40)
+        assert got["status"] == [1, 0] and got["free_out"] == list(free)
+        assert got["slots"][20:22] == [19, 20] and got["slots"][:20] == [-1] * 20
+        assert lm.errors() == C.LM_ERR_FREE
+
+
+def test_plan_give_back_then_take():
+    """Blocks go round: a request ends, the next takes its blocks."""
+    lm = C.Lm(8, 8, 64, n_blocks=3, table_blocks=3, max_requests=1, max_rows=48)
+    tables, ring, free = [[-1] * 3], [2, 0, 1], (0, 3)
+    seen = []
+    for before, after in [(0, 40), (40, 0), (0, 17), (17, 48), (48, 16), (16, 0)]:
+        want = R.plan([before], [after], tables, ring, free, [], 16, 48)
+        got = run_plan(lm, [before], [after], tables, ring, free, [], 48)
+        assert got == want and got["status"] == [0]
+        tables, ring, free = got["tables"], got["free_list"], tuple(got["free_out"])
+        seen.append(free[1] - free[0])
+    assert seen == [0, 3, 1, 0, 2, 3]
+
+
+# ---- rotate -----------------------------------------------------------------
+
+@pytest.mark.parametrize("rows,hq,hk,d,dt,it,pairs,norm,far", [
+    (1, 16, 8, 128, "bf16", "bf16", False, True, 50),
+    (5, 7, 1, 128, "fp16", "fp32", True, True, 60000),
+    (67, 10, 2, 64, "bf16", "fp32", False, False, 1000),
+    (300, 3, 3, 64, "fp16", "fp16", True, False, 9),
+    (2500, 16, 16, 64, "bf16", "bf16", True, True, 30000),
+    (2600, 12, 4, 128, "fp16", "fp16", False, True, 30000),
+])
+def test_rotate(rows, hq, hk, d, dt, it, pairs, norm, far):
+    gen = torch.Generator(device="cuda").manual_seed(rows)
+    lm = C.Lm(hq, hk, d, dt, block_size=16, n_blocks=rows // 16 + 3, max_rows=rows, max_positions=far,
+              rope_theta=1e4, rope_pairs=pairs, rms_eps=1e-5)
+    r = lambda *s: torch.randn(*s, generator=gen, device="cuda")
+    fused = (r(rows, (hq + 2 * hk) * d + 8) * 3).to(R.DTYPES[it])      # rows further apart than they are wide
+    q, k, v, _ = fused.split([hq * d, hk * d, hk * d, 8], 1)
+    q, k, v = (x.unflatten(1, (-1, d)) for x in (q, k, v))
+    gq, gk = (1 + 0.1 * r(d), 1 + 0.1 * r(d)) if norm else (None, None)
+    pos = torch.randint(far, (rows,), generator=gen, device="cuda", dtype=torch.int32)
+    n_slots = (rows // 16 + 3) * 16
+    slots = torch.randperm(n_slots, generator=gen, device="cuda")[:rows].to(torch.int32)
+    skip = torch.arange(0, rows, 5, device="cuda") if rows > 5 else torch.arange(0, device="cuda")
+    slots[skip] = -1
+    T = R.DTYPES[dt]
+    qo = torch.full((rows, hq, d), 7.0, dtype=T, device="cuda")
+    kc, vc = (torch.full((n_slots // 16, 16, hk, d), 7.0, dtype=T, device="cuda") for _ in range(2))
+    lm.rotate(q, k, v, pos, slots, qo, kc, vc, q_gain=gq, k_gain=gk)
+    assert lm.errors() == 0
+    held = (slots >= 0).cpu().numpy()
+    to = slots.cpu().numpy()[held]
+    want = {}
+    for name, x, g in (("q", q, gq), ("k", k, gk)):
+        y = R.rotate(x, g, pos, 1e4, 1e-5, pairs)
+        # a rotation adds two products: their sizes bound its rounding
+        size = np.abs(f64(x)).max(-1, keepdims=True)
+        if g is not None:
+            size = size / np.sqrt((f64(x) ** 2).mean(-1, keepdims=True) + 1e-5) * 1.6
+        want[name] = y, torch.finfo(T).eps / 2 * np.abs(y) + 2 * size * 2.0 ** -20 + (2.0 ** -25 if dt == "fp16" else 0)
+    full_q = np.full((rows, hq, d), 7.0)
+    full_q[held] = want["q"][0][held]
+    tol = np.zeros_like(full_q)
+    tol[held] = np.broadcast_to(want["q"][1], full_q.shape)[held]
+    assert (np.abs(f64(qo) - full_q) <= tol).all()
+    kw, kt = np.full((n_slots, hk, d), 7.0), np.zeros((n_slots, hk, d))
+    kw[to], kt[to] = want["k"][0][held], want["k"][1][held]
+    assert (np.abs(f64(kc).reshape(kw.shape) - kw) <= kt).all()
+    vw = torch.full((n_slots, hk, d), 7.0, dtype=T, device="cuda")
+    vw[torch.from_numpy(to).cuda().long()] = v.to(T)[torch.from_numpy(held).cuda()]
+    assert torch.equal(vc.view(vw.shape), vw)
+    # rows that stay where they are; in place where the type allows it
+    pk = torch.empty(rows, hk, d, dtype=T, device="cuda")
+    qp = q.contiguous() if it == dt else torch.empty(rows, hq, d, dtype=T, device="cuda")
+    lm.rotate(qp if it == dt else q, k, None, pos, None, qp, pk, None, q_gain=gq, k_gain=gk)
+    assert torch.equal(qp[torch.from_numpy(held).cuda()], qo[torch.from_numpy(held).cuda()])
+    assert torch.equal(pk[torch.from_numpy(held).cuda()], kc.view(-1, hk, d)[torch.from_numpy(to).cuda().long()])
+
+
+def test_rotate_wrong_slots_and_positions_are_skipped():
+    lm = C.Lm(2, 2, 64, n_blocks=2, max_rows=8, max_positions=10)
+    x = torch.randn(6, 2, 64, device="cuda")
+    q = torch.zeros(6, 2, 64, dtype=torch.bfloat16, device="cuda")
+    kc, vc = (torch.zeros(2, 16, 2, 64, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    lm.rotate(x, x, x, i32([0, 1, 2, 3, 4, 5]), i32([0, 32, -2, 2 ** 31 - 1, -2 ** 31, 31]), q, kc, vc)
+    assert lm.errors() == C.LM_ERR_SLOT and lm.errors() == 0
+    assert [bool(r.any()) for r in q] == [True, False, False, False, False, True]
+    assert [bool(r.any()) for r in vc.view(32, -1)] == [True] + [False] * 30 + [True]
+    q.zero_()
+    lm.rotate(x, x, x, i32([0, 10, -1, 2 ** 31 - 1, -2 ** 31, 9]), i32([0, 1, 2, 3, 4, 5]), q, kc, vc)
+    assert lm.errors() == C.LM_ERR_POSITION
+    assert [bool(r.any()) for r in q] == [True, False, False, False, False, True]
+
+
+# ---- prompt -----------------------------------------------------------------
+
+HEADS = [(16, 16, 64), (16, 8, 128), (7, 1, 128), (10, 2, 64), (12, 4, 128), (16, 1, 64), (3, 3, 128)]
+
+
+def prompt_inputs(seed, lens, hq, hk, d, dt, extra=3, pad=8):
+    """Packed q, k, v whose rows lie `pad` elements further apart than they are
+    wide, with `extra` poisoned rows behind the last request."""
+    gen = torch.Generator(device="cuda").manual_seed(seed)
+    n = sum(lens) + extra
+    T = R.DTYPES[dt]
+    mk = lambda h, f: (torch.randn(n, h * d + pad, generator=gen, device="cuda") * f).to(T)[:, :h * d].unflatten(1, (h, d))
+    q, k, v = mk(hq, 1.5), mk(hk, 1.0), mk(hk, 1.0)
+    for t in (q, k, v):
+        t[sum(lens):] = NAN
+    starts = [sum(lens[:i]) for i in range(len(lens) + 1)]
+    return q, k, v, starts
+
+
+def check_prompt(lens, hq, hk, d, dt, scale=0.0, seed=0, mul=1.0):
+    q, k, v, starts = prompt_inputs(seed, lens, hq, hk, d, dt)
+    q.mul_(mul)
+    n = q.shape[0]
+    lm = C.Lm(hq, hk, d, dt, max_requests=len(lens), max_rows=n, scale=scale)
+    o = torch.full((n, hq, d + 8), 5.0, dtype=q.dtype, device="cuda")
+    o = o.view(n, -1)[:, :hq * d].unflatten(1, (hq, d)) if hq > 1 else o[:, :, :d]
+    lse = torch.full((n, hq), 5.0, device="cuda")
+    lm.prompt(q, k, v, i32(starts), o, lse=lse)
+    assert lm.errors() == 0
+    live = sum(lens)
+    assert (o[live:] == 5).all() and (lse[live:] == 5).all()
+    q6, k6, v6 = f64(q)[:live], f64(k), f64(v)
+    where = [(s, i) for s, e in zip(starts, starts[1:]) for i in range(e - s)]
+    ref = R.attention(q6, range(live), lambda r: (k6[where[r][0]:r + 1], v6[where[r][0]:r + 1]), hk,
+                      scale or d ** -0.5)
+    R.assert_attention(o[:live], lse[:live], ref, dt, [w[1] + 1 for w in where], d, 5.0)
+    o2 = torch.empty_like(o)
+    lm.prompt(q, k, v, i32(starts), o2)
+    assert torch.equal(o2[:live], o[:live])
+
+
+@pytest.mark.parametrize("hq,hk,d", HEADS)
+@pytest.mark.parametrize("dt", ["bf16", "fp16"])
+def test_prompt_heads(hq, hk, d, dt):
+    check_prompt([1, 0, 37, 130], hq, hk, d, dt)
+
+
+@pytest.mark.parametrize("lens", [[1], [2], [127], [128], [129], [255], [256], [257], [0, 0, 1], [64] * 9, [383, 1, 300],
+                                  [640]])
+def test_prompt_lengths(lens):
+    check_prompt(lens, 4, 2, 128, "bf16")
+    check_prompt(lens, 2, 2, 64, "fp16", seed=1)
+
+
+def test_prompt_scale_and_large_scores():
+    check_prompt([200], 4, 4, 64, "bf16", scale=0.7)
+    check_prompt([200, 50], 4, 2, 128, "fp16", mul=20.0)     # nearly one-hot rows
+
+
+def test_prompt_a_later_token_never_reaches_an_earlier_row():
+    """NaN and infinities from position 100 on leave rows 0 .. 99 the bits they had."""
+    for d, dt in ((128, "bf16"), (64, "fp16")):
+        q, k, v, starts = prompt_inputs(5, [300, 90], 4, 2, d, dt)
+        lm = C.Lm(4, 2, d, dt, max_requests=2, max_rows=q.shape[0])
+        o, o2 = (torch.zeros(q.shape, dtype=q.dtype, device="cuda") for _ in range(2))
+        lm.prompt(q, k, v, i32(starts), o)
+        k[100:300:3] = NAN
+        v[101:300:3] = NAN
+        v[100] = float("inf")
+        k[102] = float("-inf")
+        lm.prompt(q, k, v, i32(starts), o2)
+        assert torch.equal(o[:100], o2[:100]) and torch.equal(o[300:390], o2[300:390])
+        assert o2[102:300].isnan().all()
+
+
+def test_prompt_row_start_out_of_range_is_bent():
+    q, k, v, _ = prompt_inputs(6, [20], 2, 2, 64, "bf16", extra=0)
+    lm = C.Lm(2, 2, 64, max_requests=3, max_rows=20)
+    o = torch.zeros(20, 2, 64, dtype=q.dtype, device="cuda")
+    want = torch.zeros_like(o)
+    lm.prompt(q, k, v, i32([0, 20]), want)
+    assert lm.errors() == 0
+    for starts in ([0, 2 ** 31 - 1], [-4, 20], [-2 ** 31, 2 ** 31 - 1]):
+        lm.prompt(q, k, v, i32(starts), o.zero_())
+        assert lm.errors() == C.LM_ERR_LENGTH and torch.equal(o, want)
+    lm.prompt(q, k, v, i32([20, 0, -1, 5]), o.zero_())
+    assert lm.errors() == C.LM_ERR_LENGTH
+
+
+# ---- cache ------------------------------------------------------------------
+
+def cache_case(seed, lens, hk, d, dt, bs, sh=0, rows=None, mul=1.0):
+    """Caches in which every place behind a length is NaN; tables whose entries
+    behind a length are out of range."""
+    rng = random.Random(seed)
+    gen = torch.Generator(device="cuda").manual_seed(seed)
+    T = R.DTYPES[dt]
+    counts = [max(0, -(-n // bs) - sh) for n in lens]
+    n_blocks = sh + sum(counts) + 3
+    width = max(1, sh + max(counts) + 1)
+    ids = list(range(n_blocks))
+    rng.shuffle(ids)
+    shared, ids = ids[:sh], ids[sh:]
+    tables = [[2 ** 31 - 1] * width for _ in lens]
+    kc, vc = (torch.full((n_blocks, bs, hk, d), NAN, dtype=T, device="cuda") for _ in range(2))
+    for i in shared:
+        for c in (kc, vc):
+            c[i] = torch.randn(bs, hk, d, generator=gen, device="cuda").to(T)
+    for b, n in enumerate(lens):
+        tables[b][:sh] = shared
+        mine, ids = ids[:counts[b]], ids[counts[b]:]
+        tables[b][sh:sh + counts[b]] = mine
+        for j, blk in enumerate(mine):
+            left = min(bs, n - (sh + j) * bs)
+            for c in (kc, vc):
+                c[blk, :left] = torch.randn(left, hk, d, generator=gen, device="cuda").to(T) * mul
+    return kc, vc, tables, shared, n_blocks, width, gen
+
+
+def gathered(cache, table, n, bs):
+    ids = [table[j] for j in range(-(-n // bs))]
+    return f64(cache[ids].flatten(0, 1)[:n]) if n else np.zeros((0,) + tuple(cache.shape[2:]))
+
+
+def check_paged(new, kv, hq, hk, d, dt, bs, seed=0):
+    kc, vc, tables, _, n_blocks, width, gen = cache_case(seed, kv, hk, d, dt, bs)
+    n = sum(new) + 2
+    q = (torch.randn(n, hq, d, generator=gen, device="cuda") * 1.5).to(R.DTYPES[dt])
+    q[sum(new):] = NAN
+    starts = [sum(new[:i]) for i in range(len(new) + 1)]
+    lm = C.Lm(hq, hk, d, dt, block_size=bs, n_blocks=n_blocks, table_blocks=width, max_requests=len(new), max_rows=n)
+    o = torch.full((n, hq, d), 5.0, dtype=q.dtype, device="cuda")
+    lse = torch.full((n, hq), 5.0, device="cuda")
+    lm.prompt_paged(q, kc, vc, i32(starts), i32(tables), i32(kv), o, lse=lse)
+    assert lm.errors() == 0
+    live = sum(new)
+    assert (o[live:] == 5).all() and (lse[live:] == 5).all()
+    ks = [(gathered(kc, tables[b], kv[b], bs), gathered(vc, tables[b], kv[b], bs)) for b in range(len(new))]
+    where = [(b, max(0, kv[b] - new[b] + i + 1)) for b in range(len(new)) for i in range(new[b])]
+    ref = R.attention(f64(q)[:live], range(live), lambda r: tuple(x[:where[r][1]] for x in ks[where[r][0]]), hk, d ** -0.5)
+    R.assert_attention(o[:live], lse[:live], ref, dt, [w[1] for w in where], d, 5.0)
+
+
+@pytest.mark.parametrize("hq,hk,d", HEADS)
+@pytest.mark.parametrize("bs", [16, 32, 64, 128])
+def test_prompt_paged(hq, hk, d, bs):
+    dt = "bf16" if bs in (16, 64) else "fp16"
+    # whole prompt, one token behind a context, several, none, more rows than keys, keys but no rows
+    check_paged([33, 1, 70, 0, 9, 0], [33, 150, 200, 0, 4, 40], hq, hk, d, dt, bs)
+
+
+def test_prompt_paged_rows_without_keys():
+    check_paged([5, 200], [0, 64], 4, 2, 128, "bf16", 16)
+    check_paged([300], [300], 4, 1, 64, "fp16", 32)
+
+
+def check_step(kv, sh, hq, hk, d, dt, bs, seed=0, mul=1.0):
+    kc, vc, tables, shared, n_blocks, width, gen = cache_case(seed, kv, hk, d, dt, bs, sh)
+    B = len(kv)
+    q = (torch.randn(B, hq * d + 16, generator=gen, device="cuda") * 1.5 * mul).to(R.DTYPES[dt])[:, :hq * d].unflatten(1, (hq, d))
+    lm = C.Lm(hq, hk, d, dt, block_size=bs, n_blocks=n_blocks, table_blocks=width, max_requests=B, max_rows=B)
+    o = torch.full((B, hq, d), 5.0, dtype=q.dtype, device="cuda")
+    lse = torch.full((B, hq), 5.0, device="cuda")
+    own = [[-1] * sh + t[sh:] for t in tables]      # the entries of the shared blocks are not read
+    lm.step(q, kc, vc, i32(own), i32(kv), o, shared_table=i32(shared) if sh else None, lse=lse)
+    assert lm.errors() == 0
+    ks = [(gathered(kc, tables[b], n, bs), gathered(vc, tables[b], n, bs)) for b, n in enumerate(kv)]
+    ref = R.attention(f64(q), range(B), lambda r: ks[r], hk, d ** -0.5)
+    R.assert_attention(o, lse, ref, dt, kv, d, 5.0)
+    return lm, q, kc, vc, own, shared, o
+
+
+@pytest.mark.parametrize("hq,hk,d", HEADS)
+@pytest.mark.parametrize("bs", [16, 32, 64, 128])
+def test_step(hq, hk, d, bs):
+    dt = "fp16" if bs in (16, 64) else "bf16"
+    check_step([1, 0, 17, 128, 129, 260], 0, hq, hk, d, dt, bs)
+    # behind a shared part: nothing, one, several blocks; shorter than the shared part; idle
+    check_step([2 * bs, 2 * bs + 1, 2 * bs + 70, 0, bs + 3, 1], 2, hq, hk, d, dt, bs, seed=1)
+
+
+@pytest.mark.parametrize("kv,sh,bs", [([1000], 0, 16), ([2100, 5, 700], 0, 64), ([1500] * 3, 64, 16), ([700] * 70, 9, 64),
+                                      ([4200], 32, 128)])
+def test_step_long(kv, sh, bs):
+    check_step(kv, sh, 4, 2, 128, "bf16", bs)
+    check_step(kv, sh, 4, 1, 64, "fp16", bs, seed=2, mul=8.0)
+
+
+def test_step_result_does_not_depend_on_the_batch():
+    lm, q, kc, vc, own, shared, o = check_step([40 + 13 * i for i in range(20)], 2, 8, 2, 128, "bf16", 16)
+    for b in (0, 7, 19):
+        kv = i32([40 + 13 * b])
+        o1 = torch.zeros(1, 8, 128, dtype=q.dtype, device="cuda")
+        lm.step(q[b:b + 1], kc, vc, i32(own[b:b + 1]), kv, o1, shared_table=i32(shared))
+        assert torch.equal(o1[0], o[b])
+
+
+def test_bad_blocks_read_as_zeros():
+    """A table entry out of range: score 0 and value 0 for its positions, and the bit."""
+    hq, hk, d, bs = 4, 2, 64, 16
+    for bad in (-1, 7, 2 ** 31 - 1, -2 ** 31):
+        kc, vc, tables, _, n_blocks, width, gen = cache_case(9, [50, 20], hk, d, "bf16", bs)
+        if bad == 7:
+            bad = n_blocks
+        q = torch.randn(2, hq, d, generator=gen, device="cuda").to(torch.bfloat16)
+        blk = tables[0][1]
+        lm = C.Lm(hq, hk, d, block_size=bs, n_blocks=n_blocks, table_blocks=width, max_requests=2, max_rows=2)
+        o, o2 = (torch.zeros(2, hq, d, dtype=q.dtype, device="cuda") for _ in range(2))
+        wrong = [list(t) for t in tables]
+        wrong[0][1] = bad
+        run = [lambda t, o: lm.step(q, kc, vc, i32(t), i32([50, 20]), o),
+               lambda t, o: lm.prompt_paged(q, kc, vc, i32([0, 1, 2]), i32(t), i32([50, 20]), o)]
+        outs = []
+        for f in run:
+            f(wrong, o)
+            assert lm.errors() == C.LM_ERR_BLOCK
+            outs.append(o.clone())
+        kc[blk], vc[blk] = 0, 0
+        for f, got in zip(run, outs):
+            f(tables, o2)
+            assert lm.errors() == 0 and torch.equal(got, o2)
+
+
+def test_lengths_past_the_table_are_bent():
+    kc, vc, tables, _, n_blocks, width, gen = cache_case(3, [48], 2, 64, "bf16", 16)
+    tables[0][3] = tables[0][0]
+    full = width * 16
+    kc[tables[0][0]], vc[tables[0][0]] = 1, 1
+    q = torch.randn(1, 4, 64, generator=gen, device="cuda").to(torch.bfloat16)
+    lm = C.Lm(4, 2, 64, n_blocks=n_blocks, table_blocks=width, max_requests=1, max_rows=1)
+    o, want = (torch.zeros(1, 4, 64, dtype=q.dtype, device="cuda") for _ in range(2))
+    for f in (lambda n, o: lm.step(q, kc, vc, i32(tables), i32([n]), o),
+              lambda n, o: lm.prompt_paged(q, kc, vc, i32([0, 1]), i32(tables), i32([n]), o)):
+        f(full, want)
+        assert lm.errors() == 0
+        for n in (full + 1, 2 ** 31 - 1):
+            f(n, o)
+            assert lm.errors() == C.LM_ERR_LENGTH and torch.equal(o, want)
+        f(-5, o)
+        assert lm.errors() == C.LM_ERR_LENGTH and not o.any()
+
+
+# ---- together ---------------------------------------------------------------
+
+def test_layer_prompts_then_steps():
+    """As a server uses them: a shared voice prompt, requests of different
+    lengths behind it, then tokens one by one, with one captured graph for
+    every step; each step's attention against 64 bits over all keys so far."""
+    hq, hk, d, bs, B, sh = 8, 2, 128, 16, 5, 3
+    width, n_blocks, max_rows = 12, 70, 128
+    T = torch.bfloat16
+    lm = C.Lm(hq, hk, d, "bf16", block_size=bs, n_blocks=n_blocks, table_blocks=width, max_requests=B,
+              max_rows=max_rows, rope_theta=1e4)
+    gen = torch.Generator(device="cuda").manual_seed(0)
+    r = lambda *s: torch.randn(*s, generator=gen, device="cuda")
+    gq, gk = 1 + 0.1 * r(d), 1 + 0.1 * r(d)
+    kc, vc = (torch.full((n_blocks, bs, hk, d), NAN, dtype=T, device="cuda") for _ in range(2))
+    z = lambda n: torch.zeros(n, dtype=torch.int32, device="cuda")
+    tables = torch.full((B, width), -1, dtype=torch.int32, device="cuda")
+    shared = i32([69, 5, 33])
+    ids = [i for i in range(n_blocks) if i not in (69, 5, 33)]
+    ring = i32(ids + [-1] * (n_blocks - len(ids)))
+    free = [torch.tensor([0, len(ids)], device="cuda"), torch.zeros(2, dtype=torch.int64, device="cuda")]
+    keys, vals = [[] for _ in range(B)], [[] for _ in range(B)]
+
+    def project(n):
+        return (r(n, (hq + 2 * hk) * d) * 2).to(T)
+
+    def split(x):
+        return [t.unflatten(1, (-1, d)) for t in x.split([hq * d, hk * d, hk * d], 1)]
+
+    # the voice prompt: packed attention, keys and values into the shared blocks
+    n = sh * bs
+    q, k, v = split(project(n))
+    pos = torch.arange(n, dtype=torch.int32, device="cuda")
+    slots = (shared.repeat_interleave(bs) * bs + pos % bs).int()
+    qo, ko = torch.zeros(n, hq, d, dtype=T, device="cuda"), torch.zeros(n, hk, d, dtype=T, device="cuda")
+    lm.rotate(q, k, None, pos, None, qo, ko, None, q_gain=gq, k_gain=gk)
+    lm.rotate(q, k, v, pos, slots, qo, kc, vc, q_gain=gq, k_gain=gk)
+    o, o2 = torch.zeros_like(qo), torch.zeros_like(qo)
+    lm.prompt(qo, ko, v, i32([0, n]), o)
+    one = C.Lm(hq, hk, d, "bf16", block_size=bs, n_blocks=n_blocks, table_blocks=sh, max_requests=1, max_rows=n)
+    one.prompt_paged(qo, kc, vc, i32([0, n]), shared.view(1, -1), i32([n]), o2)
+    assert torch.equal(o, o2)
+    ks, vs = f64(ko), f64(v)
+
+    def check(o, qo, rows_of):
+        ref = R.attention(f64(qo), range(qo.shape[0]),
+                          lambda row: tuple(np.concatenate([s] + x[rows_of[row][0]])[:rows_of[row][1]]
+                                            for s, x in ((ks, keys), (vs, vals))), hk, d ** -0.5)
+        R.assert_attention(o, None, ref, "bf16", [n for _, n in rows_of], d, 8.0)
+
+    def collect(qo_rows, k, v, starts, slots):
+        kk = kc.view(-1, hk, d)[slots.long()]
+        for b in range(B):
+            a, e = starts[b], starts[b + 1]
+            if e > a:
+                keys[b].append(f64(kk[a:e]))
+                vals[b].append(f64(v[a:e]))
+
+    # the requests' own prompts
+    new = [20, 1, 33, 16, 7]
+    before, after = i32([n] * B), i32([n + x for x in new])
+    row_start, kv_len, status, slots, pos = z(B + 1), z(B), z(B), z(max_rows), z(max_rows)
+    lm.plan(before, after, tables, ring, free[0], free[1], row_start, kv_len, status, slots, pos, shared_table=shared)
+    q, k, v = split(project(max_rows))      # padded: the rows behind the last request are not ours
+    qo = torch.zeros(max_rows, hq, d, dtype=T, device="cuda")
+    lm.rotate(q, k, v, pos, slots, qo, kc, vc, q_gain=gq, k_gain=gk)
+    o = torch.full_like(qo, 5.0)
+    lm.prompt_paged(qo, kc, vc, row_start, tables, kv_len, o)
+    assert status.tolist() == [0] * B and (o[sum(new):] == 5).all() and not qo[sum(new):].any()
+    starts = row_start.tolist()
+    collect(qo, k, v, starts, slots)
+    rows_of = [(b, n + i + 1) for b in range(B) for i in range(new[b])]
+    check(o[:sum(new)], qo[:sum(new)], rows_of)
+
+    # one token each per step, from one graph
+    x = project(B)
+    q, k, v = split(x)
+    slots, pos, row_start = z(B), z(B), z(B + 1)
+    qo, o = torch.zeros(B, hq, d, dtype=T, device="cuda"), torch.zeros(B, hq, d, dtype=T, device="cuda")
+    before.copy_(after)
+    side = torch.cuda.Stream()
+
+    def layer():
+        lm.plan(before, after, tables, ring, free[1], free[0], row_start, kv_len, status, slots, pos,
+                shared_table=shared)
+        lm.rotate(q, k, v, pos, slots, qo, kc, vc, q_gain=gq, k_gain=gk)
+        lm.step(qo, kc, vc, tables, kv_len, o, shared_table=shared)
+
+    after.add_(1)
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph, stream=side):
+        layer()
+    lens = [n + v for v in new]
+    for step in range(20):
+        x.copy_(project(B))
+        graph.replay()
+        torch.cuda.synchronize()
+        assert status.tolist() == [0] * B and lm.errors() == 0
+        st = row_start.tolist()
+        assert st == list(range(B + 1))
+        collect(qo, k, v, st, slots)
+        lens = [v + 1 for v in lens]
+        check(o, qo, [(b, lens[b]) for b in range(B)])
+        free[1].copy_(free[0])
+        before.copy_(after)
+        after.add_(1)
+
+
+def test_two_streams_and_other_current_stream():
+    """Calls go to the stream they are given, ordered with its other work."""
+    lm = C.Lm(4, 2, 64, max_requests=1, max_rows=64)
+    q, k, v, starts = prompt_inputs(1, [64], 4, 2, 64, "bf16", extra=0)
+    want = torch.zeros(64, 4, 64, dtype=q.dtype, device="cuda")
+    lm.prompt(q, k, v, i32(starts), want)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    q2, o, rs = torch.zeros_like(q), torch.zeros_like(want), i32(starts)
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(10_000_000)
+        q2.copy_(q)
+        lm.prompt(q2, k, v, rs, o)
+    side.synchronize()
+    assert torch.equal(o, want)
+    o.zero_()
+    torch.cuda.synchronize()
+    lm.prompt(q2, k, v, rs, o, stream=side)
+    side.synchronize()
+    assert torch.equal(o, want)
+
+
+# ---- refusals ---------------------------------------------------------------
+
+def test_refusals():
+    lm = C.Lm(4, 2, 64, block_size=16, n_blocks=4, table_blocks=3, max_requests=2, max_rows=8)
+    T = torch.bfloat16
+    q = torch.zeros(8, 4, 64, dtype=T, device="cuda")
+    k = torch.zeros(8, 2, 64, dtype=T, device="cuda")
+    kc = torch.zeros(4, 16, 2, 64, dtype=T, device="cuda")
+    o, rs, tb, kv = torch.zeros_like(q), i32([0, 4, 8]), i32([[0] * 3] * 2), i32([8, 8])
+    pos, slots = i32([0] * 8), i32(list(range(8)))
+
+    def refused(kind, f, *a, **kw):
+        with pytest.raises(kind):
+            f(*a, **kw)
+
+    V, E = ValueError, C.CodecError
+    refused(V, lm.prompt, q.half(), k, k, rs, o)                        # another type
+    refused(V, lm.prompt, q.cpu(), k, k, rs, o)                         # another device
+    refused(V, lm.prompt, q[:, :2], k, k, rs, o)                        # heads missing
+    refused(V, lm.prompt, q.transpose(1, 2).contiguous().transpose(1, 2), k, k, rs, o)   # heads apart
+    refused(V, lm.prompt, q, k[:4], k, rs, o)                           # rows missing
+    refused(V, lm.prompt, q, k, k, rs.long(), o)
+    refused(V, lm.prompt, q, k, k, rs, o, lse=torch.zeros(8, 2, device="cuda"))
+    wide = torch.zeros(8 * 260 + 8, dtype=T, device="cuda")
+    refused(E, lm.prompt, wide[:8 * 260].view(8, 260)[:, :256].unflatten(1, (4, 64)), k, k, rs, o)    # stride of 520 bytes
+    refused(E, lm.prompt, wide[4:4 + 2048].view(8, 4, 64), k, k, rs, o)  # 8-byte address
+    refused(E, lm.prompt, torch.zeros(9, 4, 64, dtype=T, device="cuda"), torch.zeros(9, 2, 64, dtype=T, device="cuda"),
+            torch.zeros(9, 2, 64, dtype=T, device="cuda"), rs, torch.zeros(9, 4, 64, dtype=T, device="cuda"))
+    refused(E, lm.prompt, q, k, k, i32([0, 1, 2, 3]), o)                # three requests
+    refused(V, lm.prompt_paged, q, kc[:3], kc, rs, tb, kv, o)
+    refused(V, lm.prompt_paged, q, kc, kc, rs, tb[:, :2], kv, o)
+    refused(V, lm.prompt_paged, q, kc, kc, rs, tb, kv[:1], o)
+    refused(V, lm.step, q[:2], kc, kc.float(), tb, kv, o[:2])
+    refused(V, lm.step, q[:1], kc, kc, tb, kv, o[:1])
+    refused(E, lm.step, q[:2], kc, kc, tb, kv, o[:2], shared_table=i32([0] * 4))
+    refused(E, lm.step, q[:3], kc, kc, i32([[0] * 3] * 3), i32([1] * 3), o[:3])
+    refused(E, lm.rotate, q, k, k, pos, slots, o, kc, kc.clone(), q_gain=torch.ones(64, device="cuda"))
+    refused(E, lm.rotate, q, k, None, pos, slots, o, kc, None)          # slots without values
+    refused(V, lm.rotate, q, k.float(), k, pos, slots, o, kc, kc.clone())
+    refused(V, lm.rotate, q.half(), k.half(), k.half(), pos, slots, o, kc, kc.clone())
+    refused(V, lm.rotate, q, k, k, pos, slots, o[:, :2], kc, kc.clone())
+    free = torch.tensor([0, 4], device="cuda")
+    out = [i32([0] * 3), i32([0] * 2), i32([0] * 2), i32([0] * 8), i32([0] * 8)]
+    refused(E, lm.plan, kv, kv, tb, i32([0] * 4), free, free, *out)     # counts in place
+    refused(V, lm.plan, kv, kv, tb, i32([0] * 3), free, free.clone(), *out)
+    refused(E, lm.plan, kv, kv, tb, i32([0] * 4), free, free.clone(), *out[:3], i32([0] * 9), i32([0] * 9))
+    torch.cuda.synchronize()
+    assert lm.errors() == 0 and not o.any() and not kc.any()
+    lm.prompt(q[:0], k[:0], k[:0], rs, o[:0])                           # no rows: nothing to do
+    for bad in (dict(head_dim=96), dict(q_heads=3), dict(q_heads=34), dict(block_size=24), dict(block_size=8),
+                dict(n_blocks=0), dict(table_blocks=0), dict(max_requests=0), dict(max_requests=5000),
+                dict(max_rows=0), dict(rope_theta=1.0), dict(rms_eps=-1.0), dict(scale=NAN), dict(n_blocks=2 ** 27)):
+        with pytest.raises(C.CodecError) as e:
+            C.Lm(**{**dict(q_heads=4, kv_heads=2, head_dim=64), **bad})
+        assert e.value.status == 2, bad
+    with pytest.raises(ValueError):
+        C.Lm(4, 2, 64, "fp32")
