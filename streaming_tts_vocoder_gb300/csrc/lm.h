@@ -77,6 +77,7 @@ struct LmPromptArgs {
     long long os;
     float* lse;
 };
+cudaError_t configure_lm_prompt();
 cudaError_t launch_lm_prompt(const LmShape& sh, const LmPromptArgs& a, cudaStream_t s);
 
 struct LmStepArgs {

@@ -90,7 +90,7 @@ codec_status codec_lm_create(const codec_lm_config* cfg, codec_lm_t** out)
         return CODEC_ERR_OOM;
     }
     lm->shape = LmShape{c.type, c.q_heads, c.kv_heads, c.q_heads / c.kv_heads, c.head_dim, c.scale, lm->err};
-    if (configure_lm_plan() != cudaSuccess || cudaMemset(lm->err, 0, sizeof(unsigned)) != cudaSuccess ||
+    if (configure_lm_plan() != cudaSuccess || configure_lm_prompt() != cudaSuccess || cudaMemset(lm->err, 0, sizeof(unsigned)) != cudaSuccess ||
         launch_lm_turn_table(lm->turn, c.max_positions, c.head_dim, c.rope_theta, nullptr) != cudaSuccess ||
         cudaDeviceSynchronize() != cudaSuccess) {
         lm_free(lm);

@@ -1,4 +1,4 @@
-// Attention of the codec LM: whole prompts and single tokens.
+// Attention of the codec LM for single tokens.
 //
 // o = softmax(scale q K^T) V by one pass over the keys with the running
 // maximum m and sum l: a key of score x rescales the sums by exp(m - m') and
@@ -67,31 +67,6 @@ __device__ void attend(const LmShape& sh, const LmKeys& ks, Sources src, const T
 }
 
 template <typename T, int D>
-__global__ void lm_prompt_kernel(const LmShape sh, const LmPromptArgs a)
-{
-    const long long w = blockIdx.x * (long long)kWarps + (threadIdx.x >> 5);
-    const int row = (int)(w / sh.hq), h = (int)(w - (long long)row * sh.hq);
-    if (row >= a.rows) return;
-    for (int b = 0; b < a.B; b++) {
-        int first, n;
-        if (!lm_rows(a.row_start, b, a.rows, first, n) && (threadIdx.x & 31) == 0)
-            atomicOr(sh.err, CODEC_LM_ERR_LENGTH);
-        if (row < first || row >= first + n) continue;
-        int keys = n;
-        if (a.keys.tables) {
-            keys = __ldg(a.keys.kv_len + b);
-            if (!lm_clamp_len(keys, (long long)a.keys.table_blocks << a.keys.bs_shift))
-                atomicOr(sh.err, CODEC_LM_ERR_LENGTH);
-        }
-        attend<T, D>(sh, a.keys, Sources{nullptr, 0}, static_cast<const T*>(a.q) + row * a.qs + (long long)h * D, b,
-                     first, max(0, keys - n + (row - first) + 1), h,
-                     static_cast<T*>(a.o) + row * a.os + (long long)h * D,
-                     a.lse ? a.lse + (long long)row * sh.hq + h : nullptr);
-        return;
-    }
-}
-
-template <typename T, int D>
 __global__ void lm_step_kernel(const LmShape sh, const LmStepArgs a)
 {
     const long long w = blockIdx.x * (long long)kWarps + (threadIdx.x >> 5);
@@ -106,14 +81,6 @@ __global__ void lm_step_kernel(const LmShape sh, const LmStepArgs a)
 }
 
 template <typename T, int D>
-cudaError_t prompt(const LmShape& sh, const LmPromptArgs& a, cudaStream_t s)
-{
-    const long long n = ((long long)a.rows * sh.hq + kWarps - 1) / kWarps;
-    lm_prompt_kernel<T, D><<<(unsigned)n, 32 * kWarps, 0, s>>>(sh, a);
-    return cudaGetLastError();
-}
-
-template <typename T, int D>
 cudaError_t step(const LmShape& sh, const LmStepArgs& a, cudaStream_t s)
 {
     const long long n = ((long long)a.B * sh.hq + kWarps - 1) / kWarps;
@@ -122,12 +89,6 @@ cudaError_t step(const LmShape& sh, const LmStepArgs& a, cudaStream_t s)
 }
 
 }  // namespace
-
-cudaError_t launch_lm_prompt(const LmShape& sh, const LmPromptArgs& a, cudaStream_t s)
-{
-    if (sh.type == CODEC_LM_BF16) return sh.D == 128 ? prompt<__nv_bfloat16, 128>(sh, a, s) : prompt<__nv_bfloat16, 64>(sh, a, s);
-    return sh.D == 128 ? prompt<__half, 128>(sh, a, s) : prompt<__half, 64>(sh, a, s);
-}
 
 cudaError_t launch_lm_step(const LmShape& sh, const LmStepArgs& a, cudaStream_t s)
 {
