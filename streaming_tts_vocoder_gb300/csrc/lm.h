@@ -1,6 +1,7 @@
 // Internal launchers of the codec LM's attention operators (lm_*.cu).
 #pragma once
 
+#include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -80,6 +81,30 @@ struct LmPromptArgs {
 cudaError_t configure_lm_prompt();
 cudaError_t launch_lm_prompt(const LmShape& sh, const LmPromptArgs& a, cudaStream_t s);
 
+// Single tokens over a part of the context that all requests share: partial
+// results of splits of split_len positions, [split][B][hq][D] and [split][B][hq].
+struct LmSharedArgs {
+    const void* q;
+    long long qs;
+    int B;
+    LmKeys keys;                    // tables unused
+    const int* shared_table;
+    int shared_len, split_len;
+    float* part;
+    float* part_lse;
+};
+cudaError_t launch_lm_shared(const LmShape& sh, const LmSharedArgs& a, cudaStream_t s);
+
+// Workspace of single-token attention.
+struct LmStepSpace {
+    int chunk;                      // positions per split of a request's own part
+    int max_splits;                 // splits of a full table
+    int pre_max;                    // splits of the shared part at most
+    float *part, *part_lse;         // [max_requests][max_splits][hq][D], [..][hq]
+    float *pre, *pre_lse;           // [pre_max][max_requests][hq][D], [..][hq]
+    int* done;                      // [max_requests][hk], zero between calls
+};
+
 struct LmStepArgs {
     const void* q;
     long long qs;
@@ -90,8 +115,15 @@ struct LmStepArgs {
     void* o;
     long long os;
     float* lse;
+    LmStepSpace ws;
 };
+cudaError_t configure_lm_step();
 cudaError_t launch_lm_step(const LmShape& sh, const LmStepArgs& a, cudaStream_t s);
+
+// Tensor map of [rows][heads][D] 16-bit values, rows `stride` elements apart,
+// boxes of 64 elements x box_heads x box_rows.
+bool lm_make_map(CUtensorMap* map, int type, const void* base, int D, int heads, long long rows, long long stride,
+                 int box_heads, int box_rows);
 
 // Rows of request b, from a row_start that is device data: inside [0, rows]
 // and never negative in number.  False: it was not, and was bent to fit.

@@ -1,4 +1,5 @@
 // The codec LM's attention operators: object, argument checks, launches.
+#include <algorithm>
 #include <cmath>
 #include <new>
 
@@ -13,6 +14,7 @@ struct codec_lm_s {
     LmShape shape{};
     float2* turn = nullptr;
     unsigned* err = nullptr;
+    LmStepSpace step{};
 };
 
 namespace {
@@ -37,6 +39,11 @@ void lm_free(codec_lm_s* lm)
 {
     cudaFree(lm->turn);
     cudaFree(lm->err);
+    cudaFree(lm->step.part);
+    cudaFree(lm->step.part_lse);
+    cudaFree(lm->step.pre);
+    cudaFree(lm->step.pre_lse);
+    cudaFree(lm->step.done);
     delete lm;
 }
 
@@ -83,14 +90,30 @@ codec_status codec_lm_create(const codec_lm_config* cfg, codec_lm_t** out)
     lm->cfg = c;
     lm->device = dev;
     while ((1 << lm->bs_shift) < c.block_size) lm->bs_shift++;
+    // single tokens: splits of 256 positions, of more where a full table would have over 32 of them
+    LmStepSpace& sp = lm->step;
+    const int64_t positions = (int64_t)c.table_blocks * c.block_size;
+    for (sp.chunk = 256; positions > 32LL * sp.chunk;) sp.chunk *= 2;
+    sp.max_splits = (int)((positions + sp.chunk - 1) / sp.chunk);
+    // the shared part: about a CTA per SM, from the largest batch (so that the actual one changes no bits)
+    const int pairs = (c.max_requests + 2 * (128 / (c.q_heads / c.kv_heads)) - 1) / (2 * (128 / (c.q_heads / c.kv_heads)));
+    sp.pre_max = (int)std::max<int64_t>(1, std::min<int64_t>({32, 152 / ((int64_t)pairs * c.kv_heads), positions / 256}));
+    const size_t row = (size_t)c.max_requests * c.q_heads;
     if (cudaMalloc(&lm->turn, sizeof(float2) * (size_t)c.max_positions * (c.head_dim / 2)) != cudaSuccess ||
-        cudaMalloc(&lm->err, sizeof(unsigned)) != cudaSuccess) {
+        cudaMalloc(&lm->err, sizeof(unsigned)) != cudaSuccess ||
+        cudaMalloc(&sp.part, sizeof(float) * row * sp.max_splits * c.head_dim) != cudaSuccess ||
+        cudaMalloc(&sp.part_lse, sizeof(float) * row * sp.max_splits) != cudaSuccess ||
+        cudaMalloc(&sp.pre, sizeof(float) * row * sp.pre_max * c.head_dim) != cudaSuccess ||
+        cudaMalloc(&sp.pre_lse, sizeof(float) * row * sp.pre_max) != cudaSuccess ||
+        cudaMalloc(&sp.done, sizeof(int) * (size_t)c.max_requests * c.kv_heads) != cudaSuccess) {
         cudaGetLastError();
         lm_free(lm);
         return CODEC_ERR_OOM;
     }
     lm->shape = LmShape{c.type, c.q_heads, c.kv_heads, c.q_heads / c.kv_heads, c.head_dim, c.scale, lm->err};
-    if (configure_lm_plan() != cudaSuccess || configure_lm_prompt() != cudaSuccess || cudaMemset(lm->err, 0, sizeof(unsigned)) != cudaSuccess ||
+    if (configure_lm_plan() != cudaSuccess || configure_lm_prompt() != cudaSuccess ||
+        configure_lm_step() != cudaSuccess || cudaMemset(sp.done, 0, sizeof(int) * (size_t)c.max_requests * c.kv_heads) != cudaSuccess ||
+        cudaMemset(lm->err, 0, sizeof(unsigned)) != cudaSuccess ||
         launch_lm_turn_table(lm->turn, c.max_positions, c.head_dim, c.rope_theta, nullptr) != cudaSuccess ||
         cudaDeviceSynchronize() != cudaSuccess) {
         lm_free(lm);
@@ -114,7 +137,10 @@ codec_status codec_lm_errors(codec_lm_t* lm, uint32_t* bits, int32_t clear, void
     OnDevice on(lm->device);
     cudaStream_t cs = static_cast<cudaStream_t>(stream);
     if (!on.ok || cudaMemcpyAsync(bits, lm->err, sizeof(uint32_t), cudaMemcpyDeviceToHost, cs) != cudaSuccess ||
-        (clear && cudaMemsetAsync(lm->err, 0, sizeof(uint32_t), cs) != cudaSuccess) ||
+        (clear && (cudaMemsetAsync(lm->err, 0, sizeof(uint32_t), cs) != cudaSuccess ||
+                   // a call that gave up may have left its counts of finished units
+                   cudaMemsetAsync(lm->step.done, 0, sizeof(int) * (size_t)lm->cfg.max_requests * lm->cfg.kv_heads,
+                                   cs) != cudaSuccess)) ||
         cudaStreamSynchronize(cs) != cudaSuccess)
         return CODEC_ERR_CUDA;
     return CODEC_OK;
@@ -219,6 +245,6 @@ codec_status codec_lm_step(codec_lm_t* lm, const void* q, int64_t q_stride, int3
     OnDevice on(lm->device);
     if (!on.ok) return CODEC_ERR_CUDA;
     LmStepArgs a{q, q_stride, B, paged(lm, k_cache, v_cache, tables, kv_len), shared_table, shared_blocks, o,
-                 o_stride, lse};
+                 o_stride, lse, lm->step};
     return done(launch_lm_step(lm->shape, a, static_cast<cudaStream_t>(stream)));
 }

@@ -81,15 +81,6 @@ struct Item {
     int n[2];                   // K/V tiles of each query tile
 };
 
-__device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, uint64_t* bar, int c0, int c1, int c2)
-{
-    asm volatile(
-        "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(
-            smem_u32(dst)),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(c0), "r"(c1), "r"(c2)
-        : "memory");
-}
-
 // MN-major operand with 128-byte swizzle: 64 elements of N in a 128-byte row
 // per k; 8-row groups 1024 bytes apart (stride byte offset), the next 64
 // elements of N one half tile further (leading byte offset).
@@ -674,9 +665,11 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn()
     return fn;
 }
 
+}  // namespace
+
 // [rows][heads][D] with rows `stride` elements apart; boxes of 64 elements x
 // box_heads x box_rows, 128-byte swizzle; out-of-range rows read as zero.
-bool make_map(CUtensorMap* map, int type, const void* base, int D, int heads, long long rows, long long stride,
+bool lm_make_map(CUtensorMap* map, int type, const void* base, int D, int heads, long long rows, long long stride,
               int box_heads, int box_rows)
 {
     auto fn = encode_fn();
@@ -690,6 +683,8 @@ bool make_map(CUtensorMap* map, int type, const void* base, int D, int heads, lo
               CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
+
+namespace {
 
 // Instruction descriptor: fp32 accumulator, both operands of the given format,
 // M = 128; N columns; B MN-major or K-major.
@@ -719,9 +714,9 @@ cudaError_t launch(const LmShape& sh, const void* q, long long qs, const LmKeys&
     const long long v_stride = paged ? (long long)sh.hk * D : ks.v_stride;
     const int box = paged ? 1 << ks.bs_shift : kTile;
     CUtensorMap mq, mk, mv;
-    if (!make_map(&mq, sh.type, q, D, sh.hq, p.rows, qs, sh.group, p.tokens) ||
-        !make_map(&mk, sh.type, ks.k, D, sh.hk, key_rows, k_stride, 1, box) ||
-        !make_map(&mv, sh.type, ks.v, D, sh.hk, key_rows, v_stride, 1, box))
+    if (!lm_make_map(&mq, sh.type, q, D, sh.hq, p.rows, qs, sh.group, p.tokens) ||
+        !lm_make_map(&mk, sh.type, ks.k, D, sh.hk, key_rows, k_stride, 1, box) ||
+        !lm_make_map(&mv, sh.type, ks.v, D, sh.hk, key_rows, v_stride, 1, box))
         return cudaErrorInvalidValue;
     return launch_pdl(lm_prompt_kernel<T, D>, grid, dim3(kThreads), smem_bytes<D>(), s, mq, mk, mv, p);
 }
@@ -763,6 +758,21 @@ cudaError_t launch_lm_prompt(const LmShape& sh, const LmPromptArgs& a, cudaStrea
     const int pair = 2 * (kTile / sh.group);
     const long long items = a.rows / pair + std::min(a.rows, a.B);
     return launch_any(sh, a.q, a.qs, a.keys, p, dim3((unsigned)items, (unsigned)sh.hk), s);
+}
+
+cudaError_t launch_lm_shared(const LmShape& sh, const LmSharedArgs& a, cudaStream_t s)
+{
+    Params p{};
+    p.rows = a.B;
+    p.shared_len = a.shared_len;
+    p.split_len = a.split_len;
+    p.part = a.part;
+    p.part_lse = a.part_lse;
+    LmKeys ks = a.keys;
+    ks.tables = a.shared_table;
+    const int pair = 2 * (kTile / sh.group);
+    const dim3 grid((a.B + pair - 1) / pair, sh.hk, (a.shared_len + a.split_len - 1) / a.split_len);
+    return launch_any(sh, a.q, a.qs, ks, p, grid, s);
 }
 
 }  // namespace codec

@@ -1,99 +1,590 @@
-// Attention of the codec LM for single tokens.
+// Attention of one token per request over the cache.
 //
-// o = softmax(scale q K^T) V by one pass over the keys with the running
-// maximum m and sum l: a key of score x rescales the sums by exp(m - m') and
-// adds exp(x - m') v.  One warp per (row, query head), lanes over the head's
-// elements.
+// The part of the context that all requests share is one problem with many
+// query rows: lm_prompt.cu computes it, with partial results in fp32.  What
+// each request has of its own is read here, once, and that is the bound:
+// group x 4 flops per 4 bytes, far below the tensor pipe's balance.
+//
+// A unit of work is (request, K/V head, split of `chunk` positions).  The
+// splits lie at fixed positions, so a result's bits do not depend on the
+// batch.  CTAs walk the units in turn (their number is known on the device
+// only); a producer warp keeps a ring of 64-key K and V tiles in flight across
+// units, so the copies never pause.  Four warps take 16 keys of a tile each:
+// scores and values by m16n8k16 MMAs with the group's heads as the 16 rows
+// (padded; the instruction is not what bounds this), each warp with its own
+// running softmax, joined at the unit's end.  The CTA that finishes the last
+// unit of a (request, head) joins the partial results in split order: no
+// second launch, and no order that could change a bit.
+#include <algorithm>
+
 #include "lm.h"
+#include "tc_ptx.cuh"
 
 namespace codec {
 
 namespace {
 
-constexpr int kWarps = 4;
+constexpr int kConsumers = 4;
+constexpr int kThreads = 32 * (kConsumers + 1);
+constexpr int kKeys = 64;               // keys of a tile, 16 per consumer warp
+constexpr int kMaxStages = 6;
+constexpr uint32_t kPolls = 1u << 22;
+constexpr uint32_t kHalf = kKeys * 128; // 64 columns of a tile
 
-template <typename T> __device__ __forceinline__ float to_f(T v);
-template <> __device__ __forceinline__ float to_f(__nv_bfloat16 v) { return __bfloat162float(v); }
-template <> __device__ __forceinline__ float to_f(__half v) { return __half2float(v); }
-template <typename T> __device__ __forceinline__ T from_f(float v);
-template <> __device__ __forceinline__ __nv_bfloat16 from_f(float v) { return __float2bfloat16_rn(v); }
-template <> __device__ __forceinline__ __half from_f(float v) { return __float2half_rn(v); }
-
-struct Sources {
-    const int* shared_table;
-    int shared_blocks;
+struct Params {
+    LmShape sh;
+    int B;
+    const void* q;
+    long long qs;
+    const int* tables;
+    const int* kv_len;
+    int table_blocks, bs_shift, n_blocks;
+    int shared_len, n_pre;              // shared part: length, partial results of it
+    int chunk, max_splits;
+    int stages;
+    float c;                            // scale x log2 e
+    float* part;                        // [B][max_splits][hq][D]
+    float* part_lse;
+    const float* pre;                   // [n_pre][B][hq][D]
+    const float* pre_lse;
+    int* done;                          // [B][hk] finished units; zero between calls
+    void* o;
+    long long os;
+    float* lse;
 };
 
-// Row `row` of request b sees keys 0 .. n - 1.
-template <typename T, int D>
-__device__ void attend(const LmShape& sh, const LmKeys& ks, Sources src, const T* q, int b, long long packed0, int n,
-                       int h, T* o, float* lse)
-{
-    constexpr int E = D / 32;
-    const int lane = threadIdx.x & 31, hk = h / sh.group;
-    float x[E], acc[E] = {}, m = -INFINITY, l = 0.f;
-#pragma unroll
-    for (int i = 0; i < E; i++) x[i] = to_f(q[lane + 32 * i]) * sh.scale;
-    for (int j = 0; j < n; j++) {
-        const T *k, *v;
-        bool held = true;
-        if (ks.tables) {
-            const int blk = j >> ks.bs_shift;
-            const int id = blk < src.shared_blocks ? __ldg(src.shared_table + blk)
-                                                   : __ldg(ks.tables + (long long)b * ks.table_blocks + blk);
-            held = id >= 0 && id < ks.n_blocks;
-            if (!held && lane == 0) atomicOr(sh.err, CODEC_LM_ERR_BLOCK);
-            const long long r = ((long long)(held ? id : 0) << ks.bs_shift) + (j & ((1 << ks.bs_shift) - 1));
-            k = static_cast<const T*>(ks.k) + (r * sh.hk + hk) * D;
-            v = static_cast<const T*>(ks.v) + (r * sh.hk + hk) * D;
-        } else {
-            k = static_cast<const T*>(ks.k) + (packed0 + j) * ks.k_stride + (long long)hk * D;
-            v = static_cast<const T*>(ks.v) + (packed0 + j) * ks.v_stride + (long long)hk * D;
-        }
-        float dot = 0.f;
-#pragma unroll
-        for (int i = 0; i < E; i++) dot = fmaf(x[i], held ? to_f(k[lane + 32 * i]) : 0.f, dot);
-#pragma unroll
-        for (int s = 16; s > 0; s >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, s);
-        const float m2 = fmaxf(m, dot), f = expf(m - m2), p = expf(dot - m2);
-        l = l * f + p;
-#pragma unroll
-        for (int i = 0; i < E; i++) acc[i] = fmaf(p, held ? to_f(v[lane + 32 * i]) : 0.f, acc[i] * f);
-        m = m2;
+template <typename T> struct Mma;
+template <> struct Mma<__nv_bfloat16> {
+    static __device__ __forceinline__ uint32_t pack(float a, float b)
+    {
+        const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
+        return *reinterpret_cast<const uint32_t*>(&v);
     }
+    static __device__ __forceinline__ void run(float* d, const uint32_t* a, uint32_t b0, uint32_t b1)
+    {
+        asm volatile(
+            "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+            "{%0, %1, %2, %3};"
+            : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+    }
+};
+template <> struct Mma<__half> {
+    static __device__ __forceinline__ uint32_t pack(float a, float b)
+    {
+        const __half2 v = __floats2half2_rn(a, b);
+        return *reinterpret_cast<const uint32_t*>(&v);
+    }
+    static __device__ __forceinline__ void run(float* d, const uint32_t* a, uint32_t b0, uint32_t b1)
+    {
+        asm volatile(
+            "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+            "{%0, %1, %2, %3};"
+            : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+    }
+};
+
+__device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t* r)
+{
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+
+__device__ __forceinline__ void ldsm4_t(uint32_t addr, uint32_t* r)
+{
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+
+__device__ __forceinline__ float exp2_fast(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+__device__ __forceinline__ void consumers_sync() { asm volatile("bar.sync 1, %0;" ::"r"(32 * kConsumers) : "memory"); }
+
+struct Unit {
+    int b, hk, split, n_splits;
+    int key0, keys;             // first position, positions of the split
+    bool empty;                 // the request has no position at all
+};
+
+// The unit of index u: units run over the requests' splits, K/V heads innermost.
+__device__ __forceinline__ Unit unit_at(const Params& p, const int* first, long long u)
+{
+    Unit n;
+    const int x = (int)(u / p.sh.hk);
+    n.hk = (int)(u - (long long)x * p.sh.hk);
+    int lo = 0, hi = p.B - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (first[mid] <= x) lo = mid; else hi = mid - 1;
+    }
+    n.b = lo;
+    n.split = x - first[lo];
+    n.n_splits = first[lo + 1] - first[lo];
+    int len = __ldg(p.kv_len + lo);
+    lm_clamp_len(len, (long long)p.table_blocks << p.bs_shift);
+    n.empty = len == 0;
+    n.key0 = p.shared_len + n.split * p.chunk;
+    n.keys = min(max(len - n.key0, 0), p.chunk);
+    return n;
+}
+
+template <int D> constexpr uint32_t stage_bytes() { return 2 * kKeys * D * 2; }
+
+// [stages][K tile, V tile], then the consumers' results [4][group][D] fp32 and
+// their maxima and sums [4][16][2], the barriers, and the requests' first units.
+template <int D>
+size_t smem_bytes(int stages, int group, int B)
+{
+    return 1024 + (size_t)stages * stage_bytes<D>() + (size_t)kConsumers * group * D * 4 + kConsumers * 16 * 8 +
+           2 * kMaxStages * 8 + 64 + ((size_t)B + 1) * 4;
+}
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kThreads) lm_step_kernel(const __grid_constant__ CUtensorMap mk,
+                                                           const __grid_constant__ CUtensorMap mv,
+                                                           const __grid_constant__ Params p)
+{
+    constexpr uint32_t kTileBytes = kKeys * D * 2;
+    extern __shared__ uint8_t raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
+    const int group = p.sh.group;
+    float* res = reinterpret_cast<float*>(smem + (size_t)p.stages * stage_bytes<D>());
+    float* ml = res + kConsumers * group * D;
+    uint64_t* full = reinterpret_cast<uint64_t*>(ml + kConsumers * 16 * 2);
+    uint64_t* empty = full + kMaxStages;
+    int* flags = reinterpret_cast<int*>(empty + kMaxStages);    // abort, last, total
+    int* first = flags + 16;
+    volatile int* abort_flag = flags;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+    if (tid == 0) {
+        for (int i = 0; i < p.stages; i++) {
+            mbar_init(&full[i], 1);
+            mbar_init(&empty[i], kConsumers);
+        }
+        flags[0] = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    pdl_wait();
+    pdl_launch();
+    // units before each request: at least one per request, so that something writes its row
+    if (warp == 0) {
+        int before = 0;
+        for (int base = 0; base < p.B; base += 32) {
+            const int b = base + lane;
+            int n = 0;
+            if (b < p.B) {
+                int len = __ldg(p.kv_len + b);
+                if (!lm_clamp_len(len, (long long)p.table_blocks << p.bs_shift) && blockIdx.x == 0)
+                    atomicOr(p.sh.err, CODEC_LM_ERR_LENGTH);
+                n = max(1, (max(0, len - p.shared_len) + p.chunk - 1) / p.chunk);
+            }
+            int incl = n;
 #pragma unroll
-    for (int i = 0; i < E; i++) o[lane + 32 * i] = from_f<T>(n > 0 ? acc[i] / l : 0.f);
-    if (lse && lane == 0) *lse = n > 0 ? m + logf(l) : -INFINITY;
+            for (int o = 1; o < 32; o <<= 1) {
+                const int up = __shfl_up_sync(0xffffffffu, incl, o);
+                if (lane >= o) incl += up;
+            }
+            if (b < p.B) first[b] = before + incl - n;
+            before += __shfl_sync(0xffffffffu, incl, 31);
+        }
+        if (lane == 0) first[p.B] = before;
+    }
+    __syncthreads();
+    const long long units = (long long)first[p.B] * p.sh.hk;
+
+    if (warp == kConsumers) {
+        // -------------------------------------------------------- copies --
+        int st = 0, loads = 0;
+        uint32_t ph = 0;
+        bool ok = true;
+        if (lane == 0) {
+            prefetch_tensormap(&mk);
+            prefetch_tensormap(&mv);
+        }
+        const int box_shift = min(p.bs_shift, 6);           // keys per box: a block, or half of one of 128
+        const int per = kKeys >> box_shift;
+        for (long long u = blockIdx.x; u < units && ok; u += gridDim.x) {
+            const Unit n = unit_at(p, first, u);
+            const int* table = p.tables + (long long)n.b * p.table_blocks;
+            for (int j = 0; j * kKeys < n.keys; j++) {
+                const int here = min(per, (n.keys - j * kKeys + (1 << box_shift) - 1) >> box_shift);
+                int row = 0;
+                if (lane < here) {
+                    const int pos = n.key0 + j * kKeys + (lane << box_shift);
+                    int id = __ldg(table + (pos >> p.bs_shift));
+                    if (id < 0 || id >= p.n_blocks) {
+                        atomicOr(p.sh.err, CODEC_LM_ERR_BLOCK);
+                        row = p.n_blocks << p.bs_shift;     // behind the last row: the copy writes zeros
+                    } else {
+                        row = (id << p.bs_shift) + (pos & ((1 << p.bs_shift) - 1));
+                    }
+                }
+                ok = mbar_wait(&empty[st], ph ^ 1u, abort_flag, kPolls);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) break;
+                uint8_t* dst = smem + (size_t)st * stage_bytes<D>();
+                if (lane == 0) mbar_expect_tx(&full[st], (uint32_t)(here << box_shift) * D * 4);
+                __syncwarp();
+                if (lane < here)
+                    for (int h = 0; h < D / 64; h++) {
+                        const uint32_t at = h * kHalf + ((uint32_t)lane << box_shift) * 128;
+                        tma_load_3d(dst + at, &mk, &full[st], h * 64, n.hk, row);
+                        tma_load_3d(dst + kTileBytes + at, &mv, &full[st], h * 64, n.hk, row);
+                    }
+                loads++;
+                if (++st == p.stages) {
+                    st = 0;
+                    ph ^= 1u;
+                }
+            }
+        }
+        // every stage's last load has landed before the CTA can end
+        for (int q = 0; q < p.stages && q < loads; q++) {
+            const int last = q + ((loads - 1 - q) / p.stages) * p.stages;
+            mbar_drain(&full[q], (uint32_t)(last / p.stages) & 1u);
+        }
+    } else {
+        // ------------------------------------------------------ consumers --
+        const uint32_t base = smem_u32(smem);
+        const int r0 = lane >> 2, cp = (lane & 3) * 2;      // row (and + 8) and column pair of a fragment
+        const int m8 = lane >> 3, l8 = lane & 7;
+        // this lane's row addresses for the K (keys x 16-byte chunks) and V fragments
+        const int k_key = warp * 16 + (m8 >> 1) * 8 + l8, k_chunk = m8 & 1;
+        const int v_key = warp * 16 + (m8 & 1) * 8 + l8, v_chunk = m8 >> 1;
+        const T* q = static_cast<const T*>(p.q);
+        int st = 0;
+        uint32_t ph = 0;
+        // when a wait gives up the walk goes on without waiting (the flag is up):
+        // the warps meet at every unit's barriers whatever each of them saw
+        for (long long u = blockIdx.x; u < units; u += gridDim.x) {
+            const Unit n = unit_at(p, first, u);
+            uint32_t qf[D / 16][4];
+            {
+                const T* row = q + n.b * p.qs + (long long)n.hk * group * D;
+#pragma unroll
+                for (int k = 0; k < D / 16; k++) {
+                    const int at = k * 16 + cp;
+#pragma unroll
+                    for (int e = 0; e < 4; e++) {
+                        const int r = r0 + (e & 1) * 8, col = at + (e >> 1) * 8;
+                        qf[k][e] = r < group ? __ldg(reinterpret_cast<const uint32_t*>(row + (long long)r * D + col)) : 0u;
+                    }
+                }
+            }
+            float acc[D / 8][4];
+#pragma unroll
+            for (int i = 0; i < D / 8; i++)
+#pragma unroll
+                for (int e = 0; e < 4; e++) acc[i][e] = 0.f;
+            float ref[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+            for (int j = 0; j * kKeys < n.keys; j++) {
+                const bool ok = mbar_wait(&full[st], ph, abort_flag, kPolls);
+                if (!__all_sync(0xffffffffu, ok)) break;
+                const uint32_t kt = base + (uint32_t)st * stage_bytes<D>(), vt = kt + kTileBytes;
+                const int left = n.keys - j * kKeys - warp * 16;    // keys of the warp's 16 that exist
+                if (left > 0) {
+                    float s[2][4] = {};
+#pragma unroll
+                    for (int k = 0; k < D / 16; k++) {
+                        const int c = k * 2 + k_chunk;
+                        uint32_t f[4];
+                        ldsm4(kt + (c >> 3) * kHalf + k_key * 128 + (((c & 7) ^ (k_key & 7)) << 4), f);
+                        Mma<T>::run(s[0], qf[k], f[0], f[1]);
+                        Mma<T>::run(s[1], qf[k], f[2], f[3]);
+                    }
+                    if (left < 16) {
+#pragma unroll
+                        for (int i = 0; i < 2; i++)
+#pragma unroll
+                            for (int e = 0; e < 4; e++)
+                                if (i * 8 + cp + (e & 1) >= left) s[i][e] = -INFINITY;
+                    }
+                    float m[2];
+#pragma unroll
+                    for (int h = 0; h < 2; h++) {
+                        m[h] = fmaxf(fmaxf(s[0][2 * h], s[0][2 * h + 1]), fmaxf(s[1][2 * h], s[1][2 * h + 1]));
+                        m[h] = fmaxf(m[h], __shfl_xor_sync(0xffffffffu, m[h], 1));
+                        m[h] = fmaxf(m[h], __shfl_xor_sync(0xffffffffu, m[h], 2));
+                    }
+                    // the reference moves up by more than 8 (in log2) or not at all, as for prompts
+                    if (__any_sync(0xffffffffu, (m[0] - ref[0]) * p.c > 8.f || (m[1] - ref[1]) * p.c > 8.f)) {
+#pragma unroll
+                        for (int h = 0; h < 2; h++) {
+                            const float to = fmaxf(ref[h], m[h]);
+                            const float f = ref[h] == -INFINITY ? 0.f : exp2_fast((ref[h] - to) * p.c);
+                            ref[h] = to;
+                            l[h] *= f;
+#pragma unroll
+                            for (int i = 0; i < D / 8; i++) {
+                                acc[i][2 * h] *= f;
+                                acc[i][2 * h + 1] *= f;
+                            }
+                        }
+                    }
+                    const float b0 = ref[0] == -INFINITY ? 0.f : -ref[0] * p.c;
+                    const float b1 = ref[1] == -INFINITY ? 0.f : -ref[1] * p.c;
+                    uint32_t pf[4];
+#pragma unroll
+                    for (int i = 0; i < 2; i++) {
+                        const float x0 = exp2_fast(fmaf(s[i][0], p.c, b0)), x1 = exp2_fast(fmaf(s[i][1], p.c, b0));
+                        const float y0 = exp2_fast(fmaf(s[i][2], p.c, b1)), y1 = exp2_fast(fmaf(s[i][3], p.c, b1));
+                        l[0] += x0 + x1;
+                        l[1] += y0 + y1;
+                        pf[2 * i] = Mma<T>::pack(x0, x1);
+                        pf[2 * i + 1] = Mma<T>::pack(y0, y1);
+                    }
+                    // values behind the last key may be anything: they are cut out
+                    uint32_t mask[2] = {0xffffffffu, 0xffffffffu};
+                    if (left < 16) {
+#pragma unroll
+                        for (int i = 0; i < 2; i++)
+                            mask[i] = (i * 8 + cp < left ? 0x0000ffffu : 0u) | (i * 8 + cp + 1 < left ? 0xffff0000u : 0u);
+                    }
+#pragma unroll
+                    for (int i = 0; i < D / 16; i++) {
+                        const int c = i * 2 + v_chunk;
+                        uint32_t f[4];
+                        ldsm4_t(vt + (c >> 3) * kHalf + v_key * 128 + (((c & 7) ^ (v_key & 7)) << 4), f);
+                        if (left < 16) {
+                            f[0] &= mask[0];
+                            f[1] &= mask[1];
+                            f[2] &= mask[0];
+                            f[3] &= mask[1];
+                        }
+                        Mma<T>::run(acc[2 * i], pf, f[0], f[1]);
+                        Mma<T>::run(acc[2 * i + 1], pf, f[2], f[3]);
+                    }
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&empty[st]);
+                if (++st == p.stages) {
+                    st = 0;
+                    ph ^= 1u;
+                }
+            }
+            // join the four warps
+#pragma unroll
+            for (int h = 0; h < 2; h++) {
+                l[h] += __shfl_xor_sync(0xffffffffu, l[h], 1);
+                l[h] += __shfl_xor_sync(0xffffffffu, l[h], 2);
+                const int r = r0 + 8 * h;
+                if (r < group) {
+                    float* dst = res + ((long long)warp * group + r) * D;
+#pragma unroll
+                    for (int i = 0; i < D / 8; i++)
+                        *reinterpret_cast<float2*>(dst + i * 8 + cp) = make_float2(acc[i][2 * h], acc[i][2 * h + 1]);
+                    if ((lane & 3) == 0) {
+                        ml[(warp * 16 + r) * 2] = ref[h];
+                        ml[(warp * 16 + r) * 2 + 1] = l[h];
+                    }
+                }
+            }
+            consumers_sync();
+            const bool alone = n.n_splits == 1 && p.n_pre == 0;
+            const long long at = ((long long)n.b * p.max_splits + n.split) * p.sh.hq + n.hk * group;
+            for (int e = tid; e < group * (D / 4); e += 32 * kConsumers) {
+                const int g = e / (D / 4), d = (e - g * (D / 4)) * 4;
+                float m = -INFINITY;
+#pragma unroll
+                for (int w = 0; w < kConsumers; w++) m = fmaxf(m, ml[(w * 16 + g) * 2]);
+                float sum = 0.f;
+                float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (n.keys > 0) {
+#pragma unroll
+                    for (int w = 0; w < kConsumers; w++) {
+                        const float mw = ml[(w * 16 + g) * 2];
+                        // a warp without keys has a sum of 0 and an accumulator of 0
+                        const float f = mw == -INFINITY ? (m == -INFINITY ? 1.f : 0.f) : exp2_fast((mw - m) * p.c);
+                        const float4 x = *reinterpret_cast<const float4*>(res + ((long long)w * group + g) * D + d);
+                        sum = fmaf(f, ml[(w * 16 + g) * 2 + 1], sum);
+                        v.x = fmaf(f, x.x, v.x);
+                        v.y = fmaf(f, x.y, v.y);
+                        v.z = fmaf(f, x.z, v.z);
+                        v.w = fmaf(f, x.w, v.w);
+                    }
+                    const float inv = 1.f / sum;
+                    v = make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv);
+                }
+                const float lse = n.keys > 0 ? m * p.sh.scale + logf(sum) : -INFINITY;
+                if (alone) {
+                    const long long h = n.hk * group + g;
+                    *reinterpret_cast<uint2*>(static_cast<T*>(p.o) + n.b * p.os + h * D + d) =
+                        make_uint2(Mma<T>::pack(v.x, v.y), Mma<T>::pack(v.z, v.w));
+                    if (p.lse && d == 0) p.lse[(long long)n.b * p.sh.hq + h] = lse;
+                } else {
+                    __stcg(reinterpret_cast<float4*>(p.part + (at + g) * D + d), v);
+                    if (d == 0) __stcg(p.part_lse + at + g, lse);
+                }
+            }
+            if (alone) {
+                consumers_sync();           // res is written again
+                continue;
+            }
+            __threadfence();
+            consumers_sync();
+            if (tid == 0) {
+                int* done = p.done + (long long)n.b * p.sh.hk + n.hk;
+                const int was = n.n_splits == 1 ? 0 : atomicAdd(done, 1);
+                flags[1] = was == n.n_splits - 1;
+                if (flags[1] && n.n_splits > 1) *done = 0;
+                __threadfence();
+            }
+            consumers_sync();
+            if (!flags[1]) continue;
+            // join the partial results, the shared part's first, in order: a warp per head
+            const int parts = p.n_pre + n.n_splits;
+            for (int g = warp; g < group; g += kConsumers) {
+                const long long h = n.hk * group + g;
+                auto lse_of = [&](int i) {
+                    return i < p.n_pre
+                               ? __ldcg(p.pre_lse + ((long long)i * p.B + n.b) * p.sh.hq + h)
+                               : __ldcg(p.part_lse + ((long long)n.b * p.max_splits + (i - p.n_pre)) * p.sh.hq + h);
+                };
+                float m = -INFINITY;
+                bool nan = false;
+                for (int i = lane; i < parts; i += 32) {
+                    const float x = lse_of(i);
+                    m = fmaxf(m, x);
+                    nan |= x != x;
+                }
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+                nan = __any_sync(0xffffffffu, nan);
+                if (nan) m = NAN;
+                const float ref2 = m == -INFINITY ? 0.f : m;
+                constexpr int kE = D / 32;
+                float v[kE] = {}, sum = 0.f;
+                for (int i0 = 0; i0 < parts; i0 += 32) {
+                    float w = 0.f;
+                    if (i0 + lane < parts) w = expf(lse_of(i0 + lane) - ref2);
+                    const int cnt = min(32, parts - i0);
+#pragma unroll 4
+                    for (int i = 0; i < cnt; i++) {
+                        const float f = __shfl_sync(0xffffffffu, w, i);
+                        const int part = i0 + i;
+                        const float* src = part < p.n_pre
+                                               ? p.pre + (((long long)part * p.B + n.b) * p.sh.hq + h) * D
+                                               : p.part + (((long long)n.b * p.max_splits + (part - p.n_pre)) * p.sh.hq + h) * D;
+                        sum += f;
+                        if constexpr (kE == 4) {
+                            const float4 x = __ldcg(reinterpret_cast<const float4*>(src) + lane);
+                            if (f != 0.f) {         // a part without keys has no value, whatever is there
+                                v[0] = fmaf(f, x.x, v[0]);
+                                v[1] = fmaf(f, x.y, v[1]);
+                                v[2] = fmaf(f, x.z, v[2]);
+                                v[3] = fmaf(f, x.w, v[3]);
+                            }
+                        } else {
+                            const float2 x = __ldcg(reinterpret_cast<const float2*>(src) + lane);
+                            if (f != 0.f) {
+                                v[0] = fmaf(f, x.x, v[0]);
+                                v[1] = fmaf(f, x.y, v[1]);
+                            }
+                        }
+                    }
+                }
+                const float inv = n.empty ? 0.f : 1.f / sum;
+                T* dst = static_cast<T*>(p.o) + n.b * p.os + h * D + lane * kE;
+                if constexpr (kE == 4)
+                    *reinterpret_cast<uint2*>(dst) =
+                        make_uint2(Mma<T>::pack(v[0] * inv, v[1] * inv), Mma<T>::pack(v[2] * inv, v[3] * inv));
+                else
+                    *reinterpret_cast<uint32_t*>(dst) = Mma<T>::pack(v[0] * inv, v[1] * inv);
+                if (p.lse && lane == 0) p.lse[(long long)n.b * p.sh.hq + h] = n.empty ? -INFINITY : m + logf(sum);
+            }
+        }
+    }
+    __syncthreads();
+    if (tid == 0 && flags[0]) atomicOr(p.sh.err, CODEC_LM_ERR_TIMEOUT);
 }
 
 template <typename T, int D>
-__global__ void lm_step_kernel(const LmShape sh, const LmStepArgs a)
+cudaError_t launch(const LmShape& sh, const LmStepArgs& a, cudaStream_t s)
 {
-    const long long w = blockIdx.x * (long long)kWarps + (threadIdx.x >> 5);
-    const int b = (int)(w / sh.hq), h = (int)(w - (long long)b * sh.hq);
-    if (b >= a.B) return;
-    int keys = __ldg(a.keys.kv_len + b);
-    if (!lm_clamp_len(keys, (long long)a.keys.table_blocks << a.keys.bs_shift)) atomicOr(sh.err, CODEC_LM_ERR_LENGTH);
-    attend<T, D>(sh, a.keys, Sources{a.shared_table, a.shared_blocks},
-                 static_cast<const T*>(a.q) + b * a.qs + (long long)h * D, b, 0, keys, h,
-                 static_cast<T*>(a.o) + b * a.os + (long long)h * D,
-                 a.lse ? a.lse + (long long)b * sh.hq + h : nullptr);
-}
-
-template <typename T, int D>
-cudaError_t step(const LmShape& sh, const LmStepArgs& a, cudaStream_t s)
-{
-    const long long n = ((long long)a.B * sh.hq + kWarps - 1) / kWarps;
-    lm_step_kernel<T, D><<<(unsigned)n, 32 * kWarps, 0, s>>>(sh, a);
-    return cudaGetLastError();
+    const LmKeys& ks = a.keys;
+    Params p{};
+    p.sh = sh;
+    p.B = a.B;
+    p.q = a.q;
+    p.qs = a.qs;
+    p.tables = ks.tables;
+    p.kv_len = ks.kv_len;
+    p.table_blocks = ks.table_blocks;
+    p.bs_shift = ks.bs_shift;
+    p.n_blocks = ks.n_blocks;
+    p.shared_len = a.shared_blocks << ks.bs_shift;
+    p.chunk = a.ws.chunk;
+    p.max_splits = a.ws.max_splits;
+    p.c = (float)(sh.scale * 1.4426950408889634);
+    p.part = a.ws.part;
+    p.part_lse = a.ws.part_lse;
+    p.pre = a.ws.pre;
+    p.pre_lse = a.ws.pre_lse;
+    p.done = a.ws.done;
+    p.o = a.o;
+    p.os = a.os;
+    p.lse = a.lse;
+    if (p.shared_len > 0) {
+        LmSharedArgs c{a.q, a.qs, a.B, ks, a.shared_table, p.shared_len, 0, a.ws.pre, a.ws.pre_lse};
+        // splits by the object's shape and the shared length alone
+        const int n = std::max(1, std::min(a.ws.pre_max, p.shared_len / 256));
+        c.split_len = ((p.shared_len + n - 1) / n + 127) & ~127;
+        p.n_pre = (p.shared_len + c.split_len - 1) / c.split_len;
+        const cudaError_t e = launch_lm_shared(sh, c, s);
+        if (e != cudaSuccess) return e;
+    }
+    const int box = std::min(kKeys, 1 << ks.bs_shift);
+    CUtensorMap mk, mv;
+    const long long rows = (long long)ks.n_blocks << ks.bs_shift;
+    if (!lm_make_map(&mk, sh.type, ks.k, D, sh.hk, rows, (long long)sh.hk * D, 1, box) ||
+        !lm_make_map(&mv, sh.type, ks.v, D, sh.hk, rows, (long long)sh.hk * D, 1, box))
+        return cudaErrorInvalidValue;
+    // two CTAs per SM where two of at least two stages fit
+    constexpr size_t kSm = 228 * 1024, kOne = 227 * 1024;
+    int per_sm = 2;
+    p.stages = kMaxStages;
+    while (p.stages > 2 && per_sm * (smem_bytes<D>(p.stages, sh.group, a.B) + 1024) > kSm) p.stages--;
+    if (per_sm * (smem_bytes<D>(p.stages, sh.group, a.B) + 1024) > kSm) {
+        per_sm = 1;
+        p.stages = kMaxStages;
+        while (p.stages > 2 && smem_bytes<D>(p.stages, sh.group, a.B) > kOne) p.stages--;
+    }
+    // a unit per request and head at least, and no more CTAs than the SMs hold at once
+    const long long most = (long long)a.B * p.max_splits * sh.hk;
+    const unsigned ctas = (unsigned)std::min<long long>(152 * per_sm, most);
+    return launch_pdl(lm_step_kernel<T, D>, dim3(ctas), dim3(kThreads), smem_bytes<D>(p.stages, sh.group, a.B), s, mk,
+                      mv, p);
 }
 
 }  // namespace
 
+cudaError_t configure_lm_step()
+{
+    const void* kernels[] = {(const void*)lm_step_kernel<__nv_bfloat16, 128>, (const void*)lm_step_kernel<__nv_bfloat16, 64>,
+                             (const void*)lm_step_kernel<__half, 128>, (const void*)lm_step_kernel<__half, 64>};
+    for (const void* k : kernels) {
+        const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
+        if (e != cudaSuccess) return e;
+    }
+    return cudaSuccess;
+}
+
 cudaError_t launch_lm_step(const LmShape& sh, const LmStepArgs& a, cudaStream_t s)
 {
-    if (sh.type == CODEC_LM_BF16) return sh.D == 128 ? step<__nv_bfloat16, 128>(sh, a, s) : step<__nv_bfloat16, 64>(sh, a, s);
-    return sh.D == 128 ? step<__half, 128>(sh, a, s) : step<__half, 64>(sh, a, s);
+    if (sh.type == CODEC_LM_BF16)
+        return sh.D == 128 ? launch<__nv_bfloat16, 128>(sh, a, s) : launch<__nv_bfloat16, 64>(sh, a, s);
+    return sh.D == 128 ? launch<__half, 128>(sh, a, s) : launch<__half, 64>(sh, a, s);
 }
 
 }  // namespace codec
