@@ -496,7 +496,11 @@ class Lm:
     decoder, over a cache of keys and values in blocks.  Every tensor is a CUDA
     tensor of the object's device (the one current here); nothing is allocated
     or synchronised by a call, so calls may be captured into a CUDA graph.
-    dtype: "bf16" or "fp16", the type of queries, keys, values and outputs."""
+    dtype: "bf16" or "fp16", the type of queries, keys, values and outputs.
+    Calls go to `stream`, or else to the device's current stream.
+
+    A small call's time is this marshalling, so it looks at every tensor once
+    and in the cheapest way (about 0.3 us each)."""
 
     def __init__(self, q_heads: int, kv_heads: int, head_dim: int, dtype: str = "bf16", block_size: int = 16,
                  n_blocks: int = 1, table_blocks: int = 1, max_requests: int = 64, max_rows: int = 4096,
@@ -508,57 +512,46 @@ class Lm:
         c = LmConfigC(LM_TYPES[dtype], q_heads, kv_heads, head_dim, block_size, n_blocks, table_blocks, max_requests,
                       max_rows, max_positions, int(rope_pairs), rope_theta, rms_eps, scale)
         h = _P()
-        _check(_lib().codec_lm_create(ctypes.byref(c), ctypes.byref(h)), "codec_lm_create")
+        self._lib = lib = _lib()
+        _check(lib.codec_lm_create(ctypes.byref(c), ctypes.byref(h)), "codec_lm_create")
         self._h = h
         self.cfg_c = c
         self.device = torch.device("cuda", torch.cuda.current_device())
         self.dtype = torch.bfloat16 if dtype == "bf16" else torch.float16
-        self._torch = torch
+        self._index, self._type = self.device.index, LM_TYPES[dtype]
+        self._i32, self._i64, self._f32 = torch.int32, torch.int64, torch.float32
+        self._current = torch._C._cuda_getCurrentRawStream
+        self._hq, self._hk, self._d = q_heads, kv_heads, head_dim
+        self._width, self._n_blocks = table_blocks, n_blocks
         self._cache_shape = (n_blocks, block_size, kv_heads, head_dim)
 
     def close(self):
         if getattr(self, "_h", None):
-            _lib().codec_lm_destroy(self._h)
+            self._lib.codec_lm_destroy(self._h)
             self._h = None
 
     def __del__(self):
         self.close()
 
-    def _stream(self, stream):
-        return (self._torch.cuda.current_stream(self.device) if stream is None else stream).cuda_stream
-
     def _flat(self, name, t, dtype, shape):
         """Address of a contiguous tensor of exactly this type and shape."""
-        if t.dtype != dtype or t.device != self.device or tuple(t.shape) != shape or not t.is_contiguous():
-            raise ValueError(f"{name} must be a contiguous {dtype} tensor {shape} on {self.device}, got {t.dtype} "
-                             f"{tuple(t.shape)} on {t.device}")
-        return t.data_ptr()
+        if t.dtype is dtype and t.shape == shape and t.get_device() == self._index and t.is_contiguous():
+            return t.data_ptr()
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor {shape} on {self.device}, got {t.dtype} "
+                         f"{tuple(t.shape)}, strides {t.stride()} on {t.device}")
 
-    def _rows(self, name, t, heads, rows=None, dtype=None):
+    def _rows(self, name, t, dtype, rows, heads):
         """Address and row stride of [rows][heads][head_dim] whose rows may lie apart."""
-        d = self.cfg_c.head_dim
-        if (t.dtype != (dtype or self.dtype) or t.device != self.device or t.dim() != 3 or t.shape[1] != heads
-                or t.shape[2] != d or (rows is not None and t.shape[0] != rows)):
-            raise ValueError(f"{name} must be {dtype or self.dtype} [{'rows' if rows is None else rows}][{heads}][{d}] "
-                             f"on {self.device}, got {t.dtype} {tuple(t.shape)} on {t.device}")
-        if t.shape[0] > 1:
-            stride = t.stride(0)
-        else:
-            stride = heads * d
-        if t.stride(2) != 1 or (heads > 1 and t.stride(1) != d):
-            raise ValueError(f"{name}: the heads of a row must lie back to back")
-        return t.data_ptr(), stride
+        d = self._d
+        if t.dtype is dtype and t.shape == (rows, heads, d) and t.get_device() == self._index:
+            stride, across, inner = t.stride()
+            if inner == 1 and (across == d or heads == 1):
+                return t.data_ptr(), stride if rows > 1 else heads * d
+        raise ValueError(f"{name} must be {dtype} [{rows}][{heads}][{d}] on {self.device} with the heads of a row back "
+                         f"to back, got {t.dtype} {tuple(t.shape)}, strides {t.stride()} on {t.device}")
 
-    def _caches(self, k_cache, v_cache):
-        return (self._flat("k_cache", k_cache, self.dtype, self._cache_shape),
-                self._flat("v_cache", v_cache, self.dtype, self._cache_shape))
-
-    def _lse(self, lse, rows):
-        return None if lse is None else self._flat("lse", lse, self._torch.float32, (rows, self.cfg_c.q_heads))
-
-    def _shared(self, shared_table):
-        n = 0 if shared_table is None else shared_table.numel()
-        return (self._flat("shared_table", shared_table, self._torch.int32, (n,)) if n else None), n
+    def _optional(self, name, t, dtype, shape):
+        return None if t is None else self._flat(name, t, dtype, shape)
 
     def plan(self, len_before, len_after, tables, free_list, free_in, free_out, row_start, kv_len, status, slots,
              positions, shared_table=None, stream=None):
@@ -566,17 +559,21 @@ class Lm:
         len_after, kv_len, status [B]; tables [B][table_blocks]; free_list
         [n_blocks]; row_start [B + 1]; slots, positions [rows at most]; int64
         free_in, free_out [2]; shared_table int32 [shared blocks] or None."""
-        c, i32, i64 = self.cfg_c, self._torch.int32, self._torch.int64
+        flat, i32 = self._flat, self._i32
         B, rows = len_before.numel(), slots.numel()
-        f = self._flat
-        shared, n_shared = self._shared(shared_table)
-        _check(_lib().codec_lm_plan(
-            self._h, f("len_before", len_before, i32, (B,)), f("len_after", len_after, i32, (B,)), B,
-            f("tables", tables, i32, (B, c.table_blocks)), shared, n_shared,
-            f("free_list", free_list, i32, (c.n_blocks,)), f("free_in", free_in, i64, (2,)),
-            f("free_out", free_out, i64, (2,)), f("row_start", row_start, i32, (B + 1,)),
-            f("kv_len", kv_len, i32, (B,)), f("status", status, i32, (B,)), f("slots", slots, i32, (rows,)),
-            f("positions", positions, i32, (rows,)), rows, self._stream(stream)), "codec_lm_plan")
+        shared = 0 if shared_table is None else shared_table.numel()
+        per, two, most = (B,), (2,), (rows,)
+        status = self._lib.codec_lm_plan(
+            self._h, flat("len_before", len_before, i32, per), flat("len_after", len_after, i32, per), B,
+            flat("tables", tables, i32, (B, self._width)),
+            flat("shared_table", shared_table, i32, (shared,)) if shared else None, shared,
+            flat("free_list", free_list, i32, (self._n_blocks,)), flat("free_in", free_in, self._i64, two),
+            flat("free_out", free_out, self._i64, two), flat("row_start", row_start, i32, (B + 1,)),
+            flat("kv_len", kv_len, i32, per), flat("status", status, i32, per), flat("slots", slots, i32, most),
+            flat("positions", positions, i32, most), rows,
+            self._current(self._index) if stream is None else stream.cuda_stream)
+        if status:
+            raise CodecError(status, "codec_lm_plan")
 
     def rotate(self, q, k, v, positions, slots, q_out, k_dst, v_dst, q_gain=None, k_gain=None, stream=None):
         """codec_lm_rotate: q [rows][q_heads][head_dim], k and v [rows][kv_heads]
@@ -584,67 +581,88 @@ class Lm:
         of one fused projection); positions, slots int32 [rows]; q_out contiguous
         in the object's type; k_dst, v_dst the cache.  slots None: k_dst (and v_dst,
         or v and v_dst None) are contiguous [rows][kv_heads][head_dim]."""
-        c, t = self.cfg_c, self._torch
+        flat, i32, d, hk, dtype = self._flat, self._i32, self._d, self._hk, self.dtype
         rows, fused = q.shape[0], q.dtype
         if rows == 0:
             return
-        if fused != self.dtype and fused != t.float32:
-            raise ValueError(f"q must be {self.dtype} or torch.float32")
-        qp, qs = self._rows("q", q, c.q_heads, None, fused)
-        kp, ks = self._rows("k", k, c.kv_heads, rows, fused)
-        vp, vs = (None, 0) if v is None else self._rows("v", v, c.kv_heads, rows, fused)
-        dst = self._cache_shape if slots is not None else (rows, c.kv_heads, c.head_dim)
-        gains = [None if g is None else self._flat("gain", g, t.float32, (c.head_dim,)) for g in (q_gain, k_gain)]
-        _check(_lib().codec_lm_rotate(
-            self._h, qp, qs, kp, ks, vp, vs, LM_TYPES["fp32"] if fused == t.float32 else c.type, rows, *gains,
-            self._flat("positions", positions, t.int32, (rows,)),
-            None if slots is None else self._flat("slots", slots, t.int32, (rows,)),
-            self._flat("q_out", q_out, self.dtype, (rows, c.q_heads, c.head_dim)),
-            self._flat("k_dst", k_dst, self.dtype, dst),
-            None if v_dst is None else self._flat("v_dst", v_dst, self.dtype, dst), self._stream(stream)),
-            "codec_lm_rotate")
+        if fused is not dtype and fused is not self._f32:
+            raise ValueError(f"q must be {dtype} or torch.float32")
+        qp, qs = self._rows("q", q, fused, rows, self._hq)
+        kp, ks = self._rows("k", k, fused, rows, hk)
+        vp, vs = (None, 0) if v is None else self._rows("v", v, fused, rows, hk)
+        dst = (rows, hk, d) if slots is None else self._cache_shape
+        gain = (d,)
+        status = self._lib.codec_lm_rotate(
+            self._h, qp, qs, kp, ks, vp, vs, self._type if fused is dtype else 2, rows,
+            None if q_gain is None else flat("q_gain", q_gain, self._f32, gain),
+            None if k_gain is None else flat("k_gain", k_gain, self._f32, gain),
+            flat("positions", positions, i32, (rows,)), self._optional("slots", slots, i32, (rows,)),
+            flat("q_out", q_out, dtype, (rows, self._hq, d)), flat("k_dst", k_dst, dtype, dst),
+            self._optional("v_dst", v_dst, dtype, dst),
+            self._current(self._index) if stream is None else stream.cuda_stream)
+        if status:
+            raise CodecError(status, "codec_lm_rotate")
 
     def prompt(self, q, k, v, row_start, o, lse=None, stream=None):
         """codec_lm_prompt: causal attention of packed whole prompts.  q, o
         [rows][q_heads][head_dim], k, v [rows][kv_heads][head_dim], row_start
         int32 [B + 1], lse float32 [rows][q_heads] or None."""
-        c = self.cfg_c
+        rows_of, dtype = self._rows, self.dtype
         rows, B = q.shape[0], row_start.numel() - 1
         if rows == 0:
             return
-        _check(_lib().codec_lm_prompt(
-            self._h, *self._rows("q", q, c.q_heads), *self._rows("k", k, c.kv_heads, rows),
-            *self._rows("v", v, c.kv_heads, rows), rows, self._flat("row_start", row_start, self._torch.int32, (B + 1,)),
-            B, *self._rows("o", o, c.q_heads, rows), self._lse(lse, rows), self._stream(stream)), "codec_lm_prompt")
+        qp, qs = rows_of("q", q, dtype, rows, self._hq)
+        kp, ks = rows_of("k", k, dtype, rows, self._hk)
+        vp, vs = rows_of("v", v, dtype, rows, self._hk)
+        op, os = rows_of("o", o, dtype, rows, self._hq)
+        status = self._lib.codec_lm_prompt(
+            self._h, qp, qs, kp, ks, vp, vs, rows, self._flat("row_start", row_start, self._i32, (B + 1,)), B, op, os,
+            self._optional("lse", lse, self._f32, (rows, self._hq)),
+            self._current(self._index) if stream is None else stream.cuda_stream)
+        if status:
+            raise CodecError(status, "codec_lm_prompt")
 
     def prompt_paged(self, q, k_cache, v_cache, row_start, tables, kv_len, o, lse=None, stream=None):
         """codec_lm_prompt_paged: the same over the cache; each request's rows are
         the last ones of its kv_len positions."""
-        c, i32 = self.cfg_c, self._torch.int32
+        flat, dtype, i32 = self._flat, self.dtype, self._i32
         rows, B = q.shape[0], row_start.numel() - 1
         if rows == 0:
             return
-        _check(_lib().codec_lm_prompt_paged(
-            self._h, *self._rows("q", q, c.q_heads), rows, self._flat("row_start", row_start, i32, (B + 1,)), B,
-            *self._caches(k_cache, v_cache), self._flat("tables", tables, i32, (B, c.table_blocks)),
-            self._flat("kv_len", kv_len, i32, (B,)), *self._rows("o", o, c.q_heads, rows), self._lse(lse, rows),
-            self._stream(stream)), "codec_lm_prompt_paged")
+        qp, qs = self._rows("q", q, dtype, rows, self._hq)
+        op, os = self._rows("o", o, dtype, rows, self._hq)
+        status = self._lib.codec_lm_prompt_paged(
+            self._h, qp, qs, rows, flat("row_start", row_start, i32, (B + 1,)), B,
+            flat("k_cache", k_cache, dtype, self._cache_shape), flat("v_cache", v_cache, dtype, self._cache_shape),
+            flat("tables", tables, i32, (B, self._width)), flat("kv_len", kv_len, i32, (B,)), op, os,
+            self._optional("lse", lse, self._f32, (rows, self._hq)),
+            self._current(self._index) if stream is None else stream.cuda_stream)
+        if status:
+            raise CodecError(status, "codec_lm_prompt_paged")
 
     def step(self, q, k_cache, v_cache, tables, kv_len, o, shared_table=None, lse=None, stream=None):
         """codec_lm_step: one token per request; q, o [B][q_heads][head_dim].
         shared_table: int32 ids of the blocks that every request starts with."""
-        c, i32 = self.cfg_c, self._torch.int32
+        flat, dtype, i32 = self._flat, self.dtype, self._i32
         B = q.shape[0]
-        shared, n_shared = self._shared(shared_table)
-        _check(_lib().codec_lm_step(
-            self._h, *self._rows("q", q, c.q_heads), B, *self._caches(k_cache, v_cache),
-            self._flat("tables", tables, i32, (B, c.table_blocks)), self._flat("kv_len", kv_len, i32, (B,)), shared,
-            n_shared, *self._rows("o", o, c.q_heads, B), self._lse(lse, B), self._stream(stream)), "codec_lm_step")
+        shared = 0 if shared_table is None else shared_table.numel()
+        qp, qs = self._rows("q", q, dtype, B, self._hq)
+        op, os = self._rows("o", o, dtype, B, self._hq)
+        status = self._lib.codec_lm_step(
+            self._h, qp, qs, B, flat("k_cache", k_cache, dtype, self._cache_shape),
+            flat("v_cache", v_cache, dtype, self._cache_shape), flat("tables", tables, i32, (B, self._width)),
+            flat("kv_len", kv_len, i32, (B,)),
+            flat("shared_table", shared_table, i32, (shared,)) if shared else None, shared, op, os,
+            self._optional("lse", lse, self._f32, (B, self._hq)),
+            self._current(self._index) if stream is None else stream.cuda_stream)
+        if status:
+            raise CodecError(status, "codec_lm_step")
 
     def errors(self, clear: bool = True, stream=None) -> int:
         """codec_lm_errors: the LM_ERR_* bits set since last cleared (synchronises the stream)."""
         bits = ctypes.c_uint32()
-        _check(_lib().codec_lm_errors(self._h, ctypes.byref(bits), 1 if clear else 0, self._stream(stream)),
+        _check(self._lib.codec_lm_errors(self._h, ctypes.byref(bits), 1 if clear else 0,
+                                         self._current(self._index) if stream is None else stream.cuda_stream),
                "codec_lm_errors")
         return bits.value
 
