@@ -124,6 +124,33 @@ __device__ __forceinline__ float exp2_fast(float x)
     return y;
 }
 
+// Two fp32 operations per instruction, on register pairs.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c)
+{
+    float2 d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;"
+        : "=l"(*reinterpret_cast<uint64_t*>(&d))
+        : "l"(*reinterpret_cast<const uint64_t*>(&a)), "l"(*reinterpret_cast<const uint64_t*>(&b)),
+          "l"(*reinterpret_cast<const uint64_t*>(&c)));
+    return d;
+}
+
+__device__ __forceinline__ float2 add2(float2 a, float2 b)
+{
+    float2 d;
+    asm("add.rn.f32x2 %0, %1, %2;"
+        : "=l"(*reinterpret_cast<uint64_t*>(&d))
+        : "l"(*reinterpret_cast<const uint64_t*>(&a)), "l"(*reinterpret_cast<const uint64_t*>(&b)));
+    return d;
+}
+
+__device__ __forceinline__ float max3(float a, float b, float c)
+{
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+
 template <typename T> struct Two;
 template <> struct Two<__nv_bfloat16> {
     static constexpr uint32_t kFormat = 1;              // MMA operand format
@@ -153,13 +180,13 @@ __device__ __forceinline__ uint32_t not_finite(uint32_t w)
     return ((w & Two<T>::kExp) + Two<T>::kOne) & 0x80008000u;
 }
 
-template <int D> constexpr int stages() { return D == 128 ? 4 : 8; }
+template <int D> constexpr int stages() { return D == 128 ? 5 : 8; }
 
 struct Shared {
     uint64_t q_full, drain;
     uint64_t full[kMaxStages], empty[kMaxStages];
     uint64_t raw[kMaxStages], clean[kMaxStages];    // V tiles that are cleaned before use: landed, cleaned
-    uint64_t s_full[2], p_full[2], o_full[2];
+    uint64_t s_full[2], p_full[2][2], o_full[2];
     uint32_t tmem;
     int abort;
     Item item;
@@ -171,9 +198,10 @@ struct Shared {
 };
 
 template <int D> constexpr uint32_t tile_bytes() { return kTile * D * 2; }
+static_assert(sizeof(Shared) <= 227 * 1024 - 7 * 32768, "five stages of 32 KB beside two query tiles");
 template <int D> constexpr size_t smem_bytes()
 {
-    return 1024 + (size_t)(2 + stages<D>()) * tile_bytes<D>() + sizeof(Shared);
+    return (size_t)(2 + stages<D>()) * tile_bytes<D>() + sizeof(Shared);
 }
 
 // Finds the CTA's request and query rows: item x of the requests' tile pairs,
@@ -239,8 +267,7 @@ __global__ void __launch_bounds__(kThreads, 1) lm_prompt_kernel(const __grid_con
     constexpr uint32_t kBytes = tile_bytes<D>();
     constexpr int kHalves = D / 64;
     constexpr uint32_t kTmem = 512;
-    extern __shared__ uint8_t raw[];
-    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
+    extern __shared__ __align__(1024) uint8_t smem[];
     uint8_t* sq = smem;                                 // two query tiles
     uint8_t* skv = smem + 2 * kBytes;                   // ring: K tile, V tile, K tile, ...
     Shared& s = *reinterpret_cast<Shared*>(skv + (size_t)kStages * kBytes);
@@ -258,7 +285,8 @@ __global__ void __launch_bounds__(kThreads, 1) lm_prompt_kernel(const __grid_con
         }
         for (int i = 0; i < 2; i++) {
             mbar_init(&s.s_full[i], 1);
-            mbar_init(&s.p_full[i], 4);
+            mbar_init(&s.p_full[i][0], 4);
+            mbar_init(&s.p_full[i][1], 4);
             mbar_init(&s.o_full[i], 1);
         }
         s.abort = 0;
@@ -411,7 +439,7 @@ __global__ void __launch_bounds__(kThreads, 1) lm_prompt_kernel(const __grid_con
             if (n_max > 0) mbar_drain(&s.q_full, 0);
         } else if (warp == 1) {
             // -------------------------------------------------------- MMAs --
-            if (lane == 0 && n_max > 0) {
+            if (n_max > 0 && elect_one()) {
                 const uint32_t q_addr = smem_u32(sq), kv_addr = smem_u32(skv);
                 uint32_t full_ph = 0, clean_ph = 0;     // parity of each stage's barriers
                 auto landed = [&](int st) {
@@ -428,10 +456,10 @@ __global__ void __launch_bounds__(kThreads, 1) lm_prompt_kernel(const __grid_con
                     }
                     mma_commit(&s.s_full[i]);
                 };
-                auto value = [&](int i, int st, bool more) {    // O_i += P_i V
+                auto value = [&](int i, int st, int half, bool more) {  // O_i += P_i V over 64 keys
                     const uint64_t b0 = sdesc_mn_sw128(kv_addr + st * kBytes);
 #pragma unroll
-                    for (int k = 0; k < kTile / 16; k++)
+                    for (int k = half * 4; k < half * 4 + 4; k++)
                         mma_f16_ta(tmem + 256 + i * 128, tmem + i * 128 + k * 8, b0 + (uint64_t)((k * 2048) >> 4),
                                    p.idesc_o, more || k > 0);
                 };
@@ -460,9 +488,12 @@ __global__ void __launch_bounds__(kThreads, 1) lm_prompt_kernel(const __grid_con
                     }
                     for (int i = 0; i < 2 && ok; i++) {
                         if (j < it.n[i]) {
-                            if (!(ok = mbar_wait(&s.p_full[i], j & 1, abort_flag, kPolls))) break;
+                            if (!(ok = mbar_wait(&s.p_full[i][0], j & 1, abort_flag, kPolls))) break;
                             tc_fence_after();
-                            value(i, sv, j > 0);
+                            value(i, sv, 0, j > 0);
+                            if (!(ok = mbar_wait(&s.p_full[i][1], j & 1, abort_flag, kPolls))) break;
+                            tc_fence_after();
+                            value(i, sv, 1, true);
                             if (j + 1 == it.n[i]) mma_commit(&s.o_full[i]);
                         }
                         if (j + 1 < it.n[i]) score(i, sk);
@@ -540,15 +571,18 @@ __global__ void __launch_bounds__(kThreads, 1) lm_prompt_kernel(const __grid_con
 #pragma unroll
                 for (int q = 0; q < kTile; q++) x[q] = q < see ? x[q] : -INFINITY;
             }
-            float m0 = x[0], m1 = x[1], m2 = x[2], m3 = x[3];
+            float m0 = max3(x[0], x[1], x[2]), m1 = max3(x[3], x[4], x[5]), m2 = max3(x[6], x[7], x[8]),
+                  m3 = max3(x[9], x[10], x[11]);
 #pragma unroll
-            for (int q = 4; q < kTile; q += 4) {
-                m0 = fmaxf(m0, x[q]);
-                m1 = fmaxf(m1, x[q + 1]);
-                m2 = fmaxf(m2, x[q + 2]);
-                m3 = fmaxf(m3, x[q + 3]);
+            for (int q = 12; q < 124; q += 8) {
+                m0 = max3(m0, x[q], x[q + 1]);
+                m1 = max3(m1, x[q + 2], x[q + 3]);
+                m2 = max3(m2, x[q + 4], x[q + 5]);
+                m3 = max3(m3, x[q + 6], x[q + 7]);
             }
-            const float m = fmaxf(fmaxf(m0, m1), fmaxf(m2, m3));
+            m0 = max3(m0, x[124], x[125]);
+            m1 = max3(m1, x[126], x[127]);
+            const float m = max3(fmaxf(m0, m1), m2, m3);
             if (j == 0) {
                 ref = m == -INFINITY ? 0.f : m;
             } else if (__any_sync(0xffffffffu, (m - ref) * p.c > 8.f)) {
@@ -566,29 +600,31 @@ __global__ void __launch_bounds__(kThreads, 1) lm_prompt_kernel(const __grid_con
                     tmem_st32(to + q, a);
                 }
             }
-            const float base = -ref * p.c;
-            float l0 = 0.f, l1 = 0.f, l2 = 0.f, l3 = 0.f;
+            const float2 c2 = make_float2(p.c, p.c), base = make_float2(-ref * p.c, -ref * p.c);
+            float2 l0 = make_float2(0.f, 0.f), l1 = l0;
 #pragma unroll
             for (int q = 0; q < kTile; q += 64) {
                 uint32_t w[32];
 #pragma unroll
                 for (int e = 0; e < 64; e += 4) {
-                    const float a = exp2_fast(fmaf(x[q + e], p.c, base)), b = exp2_fast(fmaf(x[q + e + 1], p.c, base));
-                    const float c = exp2_fast(fmaf(x[q + e + 2], p.c, base)), d = exp2_fast(fmaf(x[q + e + 3], p.c, base));
-                    l0 += a;
-                    l1 += b;
-                    l2 += c;
-                    l3 += d;
-                    w[e / 2] = Two<T>::pack(a, b);
-                    w[e / 2 + 1] = Two<T>::pack(c, d);
+                    float2 a = fma2(make_float2(x[q + e], x[q + e + 1]), c2, base);
+                    float2 b = fma2(make_float2(x[q + e + 2], x[q + e + 3]), c2, base);
+                    a = make_float2(exp2_fast(a.x), exp2_fast(a.y));
+                    b = make_float2(exp2_fast(b.x), exp2_fast(b.y));
+                    l0 = add2(l0, a);
+                    l1 = add2(l1, b);
+                    w[e / 2] = Two<T>::pack(a.x, a.y);
+                    w[e / 2 + 1] = Two<T>::pack(b.x, b.y);
                 }
+                // half of the keys: their products start while the other half is worked on
                 tmem_st32(ts + q / 2, w);
+                tmem_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&s.p_full[i][q / 64]);
             }
-            l += (l0 + l1) + (l2 + l3);
-            tmem_wait_st();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&s.p_full[i]);
+            l0 = add2(l0, l1);
+            l += l0.x + l0.y;
         }
         if (ok && n > 0) {
             ok = mbar_wait(&s.o_full[i], 0, abort_flag, kPolls);
