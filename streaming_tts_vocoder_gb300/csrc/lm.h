@@ -77,7 +77,14 @@ struct LmPromptArgs {
     void* o;
     long long os;
     float* lse;
+    void* list;                     // workspace: lm_list_items() x 16 bytes, and their number
+    int* list_n;
 };
+// Pairs of query tiles that `rows` rows of at most B requests can make.
+inline long long lm_list_items(int rows, int B, int group)
+{
+    return rows / (2 * (128 / group)) + (rows < B ? rows : B);
+}
 cudaError_t configure_lm_prompt();
 cudaError_t launch_lm_prompt(const LmShape& sh, const LmPromptArgs& a, cudaStream_t s);
 

@@ -15,6 +15,8 @@ struct codec_lm_s {
     float2* turn = nullptr;
     unsigned* err = nullptr;
     LmStepSpace step{};
+    void* list = nullptr;           // prompt attention's items
+    int* list_n = nullptr;
 };
 
 namespace {
@@ -44,6 +46,8 @@ void lm_free(codec_lm_s* lm)
     cudaFree(lm->step.pre);
     cudaFree(lm->step.pre_lse);
     cudaFree(lm->step.done);
+    cudaFree(lm->list);
+    cudaFree(lm->list_n);
     delete lm;
 }
 
@@ -105,6 +109,9 @@ codec_status codec_lm_create(const codec_lm_config* cfg, codec_lm_t** out)
         cudaMalloc(&sp.part_lse, sizeof(float) * row * sp.max_splits) != cudaSuccess ||
         cudaMalloc(&sp.pre, sizeof(float) * row * sp.pre_max * c.head_dim) != cudaSuccess ||
         cudaMalloc(&sp.pre_lse, sizeof(float) * row * sp.pre_max) != cudaSuccess ||
+        cudaMalloc(&lm->list, 16 * (size_t)(lm_list_items(c.max_rows, c.max_requests, c.q_heads / c.kv_heads) + 1)) !=
+            cudaSuccess ||
+        cudaMalloc(&lm->list_n, sizeof(int)) != cudaSuccess ||
         cudaMalloc(&sp.done, sizeof(int) * (size_t)c.max_requests * c.kv_heads) != cudaSuccess) {
         cudaGetLastError();
         lm_free(lm);
@@ -206,7 +213,8 @@ codec_status codec_lm_prompt(codec_lm_t* lm, const void* q, int64_t q_stride, co
     if (rows == 0) return CODEC_OK;
     OnDevice on(lm->device);
     if (!on.ok) return CODEC_ERR_CUDA;
-    LmPromptArgs a{q, q_stride, rows, row_start, B, LmKeys{k, v, k_stride, v_stride}, o, o_stride, lse};
+    LmPromptArgs a{q, q_stride, rows, row_start, B, LmKeys{k, v, k_stride, v_stride}, o, o_stride, lse,
+                   lm->list, lm->list_n};
     return done(launch_lm_prompt(lm->shape, a, static_cast<cudaStream_t>(stream)));
 }
 
@@ -225,7 +233,8 @@ codec_status codec_lm_prompt_paged(codec_lm_t* lm, const void* q, int64_t q_stri
     if (rows == 0) return CODEC_OK;
     OnDevice on(lm->device);
     if (!on.ok) return CODEC_ERR_CUDA;
-    LmPromptArgs a{q, q_stride, rows, row_start, B, paged(lm, k_cache, v_cache, tables, kv_len), o, o_stride, lse};
+    LmPromptArgs a{q, q_stride, rows, row_start, B, paged(lm, k_cache, v_cache, tables, kv_len), o, o_stride, lse,
+                   lm->list, lm->list_n};
     return done(launch_lm_prompt(lm->shape, a, static_cast<cudaStream_t>(stream)));
 }
 

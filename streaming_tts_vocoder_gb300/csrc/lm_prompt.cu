@@ -18,15 +18,20 @@
 // (it overwrites its scores there) and V in its natural layout as the MN-major
 // operand.  TMEM: two score tiles of 128 columns and two accumulators of D.
 //
-// Roles (384 threads, one CTA per SM):
-//   warp 0      copies: Q once, then K and V tiles through a ring of stages;
-//               paged keys one box per cache block, one block per lane
+// Work: an item is a pair of query tiles of one request and K/V head.  Few
+// items: one CTA each.  More than there are SMs: one CTA per SM walks a list
+// of them, longest first, that a small kernel makes from the lengths; copies
+// and MMAs of the next item then run while the last one is written.
+//
+// Roles (384 threads, one CTA per SM), each walking the items by itself:
+//   warp 0      copies: Q, then K and V tiles through a ring of stages; paged
+//               keys one box per cache block, one block per lane
 //   warp 1      TMEM and MMA issue: the MMAs of one tile run while the
 //               softmax of the other does
 //   warps 2, 3  V tiles that hold keys some row may not see: rows nobody sees
 //               are zeroed, and so is what is not finite (0 x NaN is NaN, so a
-//               probability of zero would not keep it out); where it was is
-//               noted, and the rows that do see it get it back at the end
+//               probability of zero would not keep it out); the rows that do
+//               see it get it back at the end
 //   warps 4-11  softmax, four warps per tile; they also rescale the
 //               accumulator and write the result
 // Every wait is bounded: when one expires the CTA raises the error bit, stops,
@@ -50,6 +55,7 @@ constexpr uint32_t kHalfBytes = kTile * 128;    // 64 columns of a tile: 128 row
 constexpr int kMaxStages = 8;
 constexpr uint32_t kPolls = 1u << 22;
 constexpr int kNone = 0x7fffffff;
+constexpr int kSms = 152;
 
 struct Params {
     LmShape sh;
@@ -61,6 +67,10 @@ struct Params {
     int table_blocks, bs_shift, n_blocks;
     int shared_len, split_len;  // shared part: its length, and keys per blockIdx.z
     int tokens;                 // tokens per query tile: 128 / group
+    const void* v;              // values, for what is not finite
+    long long v_stride;
+    const int4* list;           // items (request, first query row, tokens, keys of the first token); null: by blockIdx
+    const int* list_n;
     float c;                    // scale x log2 e
     uint32_t idesc_s, idesc_o;
     void* o;
@@ -70,11 +80,12 @@ struct Params {
     float* part_lse;            // [split][rows][hq]
 };
 
-// What the CTA works on; filled once.
+// A pair of query tiles.
 struct Item {
-    int b;                      // request
+    int b, hk;                  // request, K/V head
     int q0;                     // first query row
     int ntok;                   // tokens of the two tiles that exist
+    int first;                  // prompts: keys of the first token, each later one sees one more (may be < 1)
     int key0;                   // packed: row of key 0; else key 0's position
     int end;                    // keys at or behind it: seen by no row
     int free_from;              // keys below it: seen by every row that sees any
@@ -113,6 +124,23 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t* r)
         "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
         "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31]), "r"(taddr)
         : "memory");
+}
+
+// Eight columns of this warp's lanes times f (few registers: the scores are live around it).
+__device__ __forceinline__ void tmem_scale8(uint32_t taddr, float f)
+{
+    float a[8];
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=f"(a[0]), "=f"(a[1]), "=f"(a[2]), "=f"(a[3]), "=f"(a[4]), "=f"(a[5]), "=f"(a[6]), "=f"(a[7])
+        : "r"(taddr)
+        : "memory");
+#pragma unroll
+    for (int e = 0; e < 8; e++) a[e] *= f;
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%8], {%0, %1, %2, %3, %4, %5, %6, %7};" ::"f"(a[0]), "f"(a[1]),
+                 "f"(a[2]), "f"(a[3]), "f"(a[4]), "f"(a[5]), "f"(a[6]), "f"(a[7]), "r"(taddr)
+                 : "memory");
 }
 
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
@@ -160,7 +188,6 @@ template <> struct Two<__nv_bfloat16> {
         const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
         return *reinterpret_cast<const uint32_t*>(&v);
     }
-    static __device__ __forceinline__ float one(uint32_t h) { return __uint_as_float(h << 16); }
 };
 template <> struct Two<__half> {
     static constexpr uint32_t kFormat = 0;
@@ -170,7 +197,6 @@ template <> struct Two<__half> {
         const __half2 v = __floats2half2_rn(a, b);
         return *reinterpret_cast<const uint32_t*>(&v);
     }
-    static __device__ __forceinline__ float one(uint32_t h) { return __half2float(__ushort_as_half((unsigned short)h)); }
 };
 
 // Which of a word's two values is not finite, as bits 15 and 31.
@@ -183,18 +209,17 @@ __device__ __forceinline__ uint32_t not_finite(uint32_t w)
 template <int D> constexpr int stages() { return D == 128 ? 5 : 8; }
 
 struct Shared {
-    uint64_t q_full, drain;
+    uint64_t drain;
     uint64_t full[kMaxStages], empty[kMaxStages];
     uint64_t raw[kMaxStages], clean[kMaxStages];    // V tiles that are cleaned before use: landed, cleaned
-    uint64_t s_full[2], p_full[2][2], o_full[2];
+    uint64_t q_full[2], q_empty[2], s_full[2], p_full[2][2], o_full[2], o_empty[2];
     uint32_t tmem;
     int abort;
-    Item item;
-    int any_bad;
     int scan[kThreads / 32];
     int found;
-    int lim[2 * kTile];         // keys each token sees
-    int bad[3][128];            // first key whose value in this column is NaN, +inf, -inf
+    Item item;                  // without a list
+    int written[2];             // softmax warps of each query tile that are done with an item, summed
+    int dirty[2];               // 1 + the last even / odd item with a value that is not finite in a cleaned tile
 };
 
 template <int D> constexpr uint32_t tile_bytes() { return kTile * D * 2; }
@@ -206,7 +231,7 @@ template <int D> constexpr size_t smem_bytes()
 
 // Finds the CTA's request and query rows: item x of the requests' tile pairs,
 // in request order, each request's last (longest) pair first.  All threads.
-__device__ bool find_item(const Params& p, Shared& s)
+__device__ void find_item(const Params& p, Shared& s)
 {
     const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
     const int pair = 2 * p.tokens;
@@ -239,22 +264,92 @@ __device__ bool find_item(const Params& p, Shared& s)
             s.item.b = b;
             s.item.q0 = first + t * pair;
             s.item.ntok = min(pair, n - t * pair);
-            s.item.key0 = p.tables ? 0 : first;
             int keys = n;
             if (p.tables) {
                 keys = __ldg(p.kv_len + b);
                 if (!lm_clamp_len(keys, (long long)p.table_blocks << p.bs_shift))
                     atomicOr(p.sh.err, CODEC_LM_ERR_LENGTH);
             }
-            // the first token's keys (others see one more each), before the clamp at 0
-            s.item.end = keys - n + t * pair + 1;
+            s.item.first = keys - n + t * pair + 1;
             s.found = 1;
         }
         before += total;
         __syncthreads();
         if (s.found && !report) break;
     }
-    return s.found != 0;
+}
+
+// Keys that token t of an item sees, from key0 on.
+__device__ __forceinline__ int keys_of(const Params& p, const Item& it, int t)
+{
+    if (p.row_start) return max(0, it.first + t);
+    int n = __ldg(p.kv_len + it.q0 + t);
+    lm_clamp_len(n, (long long)p.table_blocks << p.bs_shift);
+    return min(max(min(n, p.shared_len) - it.key0, 0), p.split_len);
+}
+
+// What follows from a prompt item's rows and its first token's keys.
+__device__ __forceinline__ void derive(const Params& p, Item& it)
+{
+    const int most0 = max(0, it.first + min(it.ntok, p.tokens) - 1);
+    const int most1 = it.ntok > p.tokens ? max(0, it.first + it.ntok - 1) : 0;
+    it.key0 = p.tables ? 0 : it.q0 - (it.first - 1);
+    it.end = max(most0, most1);
+    it.free_from = it.end > 0 ? max(1, it.first) : kNone;
+    it.n[0] = (most0 + kTile - 1) / kTile;
+    it.n[1] = (most1 + kTile - 1) / kTile;
+}
+
+// The CTA's items, one after the other: each role has a walk of its own.
+struct Walk {
+    int k = 0;                  // items so far
+    int count;                  // of the list, with heads
+    __device__ __forceinline__ Walk(const Params& p) : count(p.list ? __ldg(p.list_n) * p.sh.hk : 0) {}
+    __device__ __forceinline__ bool next(const Params& p, const Shared& s, Item& it)
+    {
+        if (!p.list) {
+            if (k++ || !s.found) return false;
+            it = s.item;
+            return true;
+        }
+        // rounds alternate their direction, so that no CTA gets the longer item of each
+        const long long w = (long long)k * gridDim.x + (k & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+        k++;
+        if (w >= count) {
+            // the last round may go backwards: a CTA without an item in it has none in any later one
+            return false;
+        }
+        const int x = (int)w / p.sh.hk;
+        const int4 e = __ldg(p.list + x);
+        it.hk = (int)w - x * p.sh.hk;
+        it.b = e.x;
+        it.q0 = e.y;
+        it.ntok = e.z;
+        it.first = e.w;
+        derive(p, it);
+        return true;
+    }
+};
+
+// Sum of the values of a column that are not finite, over keys lo .. hi - 1 of
+// an item (rare: read from global memory one by one).
+template <typename T>
+__device__ __noinline__ float not_finite_sum(const Params& p, const Item& it, int col, int lo, int hi)
+{
+    const T* v = static_cast<const T*>(p.v) + (long long)it.hk * p.sh.D + col;
+    float sum = 0.f;
+    for (int k = lo; k < hi; k++) {
+        long long row = it.key0 + k;
+        if (p.tables) {
+            const int* table = p.tables + (p.row_start ? (long long)it.b * p.table_blocks : 0LL);
+            const int id = __ldg(table + (row >> p.bs_shift));
+            if (id < 0 || id >= p.n_blocks) continue;
+            row = ((long long)id << p.bs_shift) + (row & ((1 << p.bs_shift) - 1));
+        }
+        const float x = (float)v[row * p.v_stride];
+        if (!isfinite(x)) sum += x;
+    }
+    return sum;
 }
 
 template <typename T, int D>
@@ -272,10 +367,8 @@ __global__ void __launch_bounds__(kThreads, 1) lm_prompt_kernel(const __grid_con
     uint8_t* skv = smem + 2 * kBytes;                   // ring: K tile, V tile, K tile, ...
     Shared& s = *reinterpret_cast<Shared*>(skv + (size_t)kStages * kBytes);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int hk = blockIdx.y;
 
     if (tid == 0) {
-        mbar_init(&s.q_full, 1);
         mbar_init(&s.drain, 1);
         for (int i = 0; i < kStages; i++) {
             mbar_init(&s.full[i], 1);
@@ -284,68 +377,24 @@ __global__ void __launch_bounds__(kThreads, 1) lm_prompt_kernel(const __grid_con
             mbar_init(&s.clean[i], 2);
         }
         for (int i = 0; i < 2; i++) {
+            mbar_init(&s.q_full[i], 1);
+            mbar_init(&s.q_empty[i], 1);
             mbar_init(&s.s_full[i], 1);
             mbar_init(&s.p_full[i][0], 4);
             mbar_init(&s.p_full[i][1], 4);
             mbar_init(&s.o_full[i], 1);
+            mbar_init(&s.o_empty[i], 4);
+            s.dirty[i] = 0;
         }
         s.abort = 0;
-        s.any_bad = 0;
         s.found = 0;
+        s.written[0] = s.written[1] = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        prefetch_tensormap(&mq);
+        prefetch_tensormap(&mk);
+        prefetch_tensormap(&mv);
     }
-    for (int i = tid; i < 3 * 128; i += kThreads) (&s.bad[0][0])[i] = kNone;
-    __syncthreads();
-    pdl_wait();
-    pdl_launch();
-
-    // ---- what to work on ----
-    if (p.row_start) {
-        if (!find_item(p, s)) return;       // the same for all threads, and before TMEM is taken
-        const int first = s.item.end;
-        __syncthreads();
-        for (int t = tid; t < 2 * kTile; t += kThreads)
-            s.lim[t] = t < s.item.ntok ? max(0, first + t) : 0;
-    } else {
-        const int q0 = blockIdx.x * 2 * p.tokens, k0 = blockIdx.z * p.split_len;
-        const int ntok = min(2 * p.tokens, p.rows - q0);
-        for (int t = tid; t < 2 * kTile; t += kThreads) {
-            int n = 0;
-            if (t < ntok) {
-                n = __ldg(p.kv_len + q0 + t);
-                lm_clamp_len(n, (long long)p.table_blocks << p.bs_shift);
-                n = min(max(min(n, p.shared_len) - k0, 0), p.split_len);
-            }
-            s.lim[t] = n;
-        }
-        if (tid == 0) {
-            s.item.b = 0;
-            s.item.q0 = q0;
-            s.item.ntok = ntok;
-            s.item.key0 = k0;
-        }
-    }
-    __syncthreads();
-    if (warp == 0) {                        // the largest and the smallest number of keys but none
-        int most[2] = {0, 0}, least = kNone;
-        for (int t = lane; t < s.item.ntok; t += 32) {
-            const int n = s.lim[t], i = t >= p.tokens;
-            most[i] = max(most[i], n);
-            if (n > 0) least = min(least, n);
-        }
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) {
-            most[0] = max(most[0], __shfl_xor_sync(0xffffffffu, most[0], o));
-            most[1] = max(most[1], __shfl_xor_sync(0xffffffffu, most[1], o));
-            least = min(least, __shfl_xor_sync(0xffffffffu, least, o));
-        }
-        if (lane == 0) {
-            s.item.end = max(most[0], most[1]);
-            s.item.free_from = least;
-            s.item.n[0] = (most[0] + kTile - 1) / kTile;
-            s.item.n[1] = (most[1] + kTile - 1) / kTile;
-        }
-    } else if (warp == 1) {
+    if (warp == 1) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&s.tmem)),
                      "r"(kTmem)
                      : "memory");
@@ -354,154 +403,235 @@ __global__ void __launch_bounds__(kThreads, 1) lm_prompt_kernel(const __grid_con
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const Item it = s.item;
     const uint32_t tmem = s.tmem;
+    // the set-up above touches no global memory that an earlier kernel writes
+    pdl_wait();
+    pdl_launch();
+
+    if (!p.list) {
+        if (p.row_start) {
+            find_item(p, s);
+            if (tid == 0 && s.found) {
+                s.item.hk = blockIdx.y;
+                derive(p, s.item);
+            }
+        } else if (warp == 0) {
+            // a shared part: the largest and the smallest number of keys but none
+            Item it;
+            it.b = 0;
+            it.hk = blockIdx.y;
+            it.q0 = blockIdx.x * 2 * p.tokens;
+            it.ntok = min(2 * p.tokens, p.rows - it.q0);
+            it.key0 = blockIdx.z * p.split_len;
+            it.first = 0;
+            int most[2] = {0, 0}, least = kNone;
+            for (int t = lane; t < it.ntok; t += 32) {
+                const int n = keys_of(p, it, t);
+                if (t < p.tokens) most[0] = max(most[0], n); else most[1] = max(most[1], n);
+                if (n > 0) least = min(least, n);
+            }
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) {
+                most[0] = max(most[0], __shfl_xor_sync(0xffffffffu, most[0], o));
+                most[1] = max(most[1], __shfl_xor_sync(0xffffffffu, most[1], o));
+                least = min(least, __shfl_xor_sync(0xffffffffu, least, o));
+            }
+            it.end = max(most[0], most[1]);
+            it.free_from = least;
+            it.n[0] = (most[0] + kTile - 1) / kTile;
+            it.n[1] = (most[1] + kTile - 1) / kTile;
+            if (lane == 0) {
+                s.item = it;
+                s.found = 1;
+            }
+        }
+        __syncthreads();
+    }
     volatile int* abort_flag = &s.abort;
-    const int n_max = max(it.n[0], it.n[1]);
-    // tiles from here on hold keys that some row does not see
-    const int first_masked = it.free_from / kTile;
+    Walk walk(p);
+    Item it;
 
     if (warp < 4) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 72;" ::: "memory");
         if (warp == 0) {
             // ------------------------------------------------------ copies --
             int st = 0;
-            uint32_t ph = 0;
-            uint32_t full_n = 0, raw_n = 0, full_any = 0, raw_any = 0;  // uses of each stage's barriers: parity, any
-            bool ok = true;
-            if (n_max > 0 && lane == 0) {
-                prefetch_tensormap(&mq);
-                prefetch_tensormap(&mk);
-                prefetch_tensormap(&mv);
-                const int tiles = it.n[1] > 0 ? 2 : 1;
-                const int g = p.sh.group;
-                mbar_expect_tx(&s.q_full, (uint32_t)(tiles * p.tokens * g * D * 2));
-                for (int i = 0; i < tiles; i++)
-                    for (int h = 0; h < kHalves; h++)
-                        tma_load_3d(sq + i * kBytes + h * kHalfBytes, &mq, &s.q_full, h * 64, hk * g,
-                                    it.q0 + i * p.tokens);
-            }
+            uint32_t ph = 0, q_n = 0;                   // stage and its round; uses of the query tiles (parity)
+            uint32_t full_n = 0, raw_n = 0, full_any = 0, raw_any = 0, q_any = 0;  // uses of the barriers: parity, any
             const int per = kTile >> p.bs_shift;        // cache blocks per tile
-            const int* table = p.tables + (p.row_start ? (long long)it.b * p.table_blocks : 0LL) +
-                               (it.key0 >> p.bs_shift);
-            const int blocks = (it.end + (1 << p.bs_shift) - 1) >> p.bs_shift;
-            int next = 0;
-            if (p.tables && lane < min(per, blocks)) next = __ldg(table + lane);
-            for (int j = 0; j < n_max && ok; j++) {
-                int id = next;
-                const int here = p.tables ? min(per, blocks - j * per) : 1;
+            const int g = p.sh.group;
+            bool ok = true;
+            while (ok && walk.next(p, s, it)) {
+                const int n_max = max(it.n[0], it.n[1]);
+                const int first_masked = it.free_from / kTile;
+                const int* table = nullptr;
+                int blocks = 0, next = 0;
                 if (p.tables) {
-                    const int at = (j + 1) * per + lane;
-                    if (lane < per && at < blocks) next = __ldg(table + at);
-                    if (lane < here && (id < 0 || id >= p.n_blocks)) {
-                        atomicOr(p.sh.err, CODEC_LM_ERR_BLOCK);
-                        id = p.n_blocks;                // behind the last row: the copy writes zeros
-                    }
+                    table = p.tables + (p.row_start ? (long long)it.b * p.table_blocks : 0LL) + (it.key0 >> p.bs_shift);
+                    blocks = (it.end + (1 << p.bs_shift) - 1) >> p.bs_shift;
+                    if (lane < min(per, blocks)) next = __ldg(table + lane);
                 }
-                for (int kv = 0; kv < 2; kv++) {
-                    ok = mbar_wait(&s.empty[st], ph ^ 1u, abort_flag, kPolls);
+                for (int i = 0; i < 2 && ok; i++) {
+                    if (it.n[i] == 0) continue;
+                    ok = mbar_wait(&s.q_empty[i], (q_n >> i & 1u) ^ 1u, abort_flag, kPolls);
                     ok = __all_sync(0xffffffffu, ok);
                     if (!ok) break;
-                    uint8_t* dst = skv + (size_t)st * kBytes;
-                    const CUtensorMap* map = kv ? &mv : &mk;
-                    const bool clean = kv && j >= first_masked;
-                    uint64_t* bar = clean ? &s.raw[st] : &s.full[st];
-                    if (clean) {
-                        raw_n ^= 1u << st;
-                        raw_any |= 1u << st;
-                    } else {
-                        full_n ^= 1u << st;
-                        full_any |= 1u << st;
-                    }
-                    if (lane == 0)
-                        mbar_expect_tx(bar, p.tables ? (uint32_t)(here << p.bs_shift) * D * 2 : kBytes);
-                    __syncwarp();
-                    if (p.tables) {
-                        if (lane < here)
-                            for (int h = 0; h < kHalves; h++)
-                                tma_load_3d(dst + h * kHalfBytes + ((uint32_t)lane << p.bs_shift) * 128, map,
-                                            bar, h * 64, hk, id << p.bs_shift);
-                    } else if (lane == 0) {
+                    q_n ^= 1u << i;
+                    q_any |= 1u << i;
+                    if (elect_one()) {
+                        mbar_expect_tx(&s.q_full[i], (uint32_t)(p.tokens * g * D * 2));
                         for (int h = 0; h < kHalves; h++)
-                            tma_load_3d(dst + h * kHalfBytes, map, bar, h * 64, hk, it.key0 + j * kTile);
+                            tma_load_3d(sq + i * kBytes + h * kHalfBytes, &mq, &s.q_full[i], h * 64, it.hk * g,
+                                        it.q0 + i * p.tokens);
                     }
-                    if (++st == kStages) {
-                        st = 0;
-                        ph ^= 1u;
+                    __syncwarp();
+                }
+                for (int j = 0; j < n_max && ok; j++) {
+                    int id = next;
+                    const int here = p.tables ? min(per, blocks - j * per) : 1;
+                    if (p.tables) {
+                        const int at = (j + 1) * per + lane;
+                        if (lane < per && at < blocks) next = __ldg(table + at);
+                        if (lane < here && (id < 0 || id >= p.n_blocks)) {
+                            atomicOr(p.sh.err, CODEC_LM_ERR_BLOCK);
+                            id = p.n_blocks;            // behind the last row: the copy writes zeros
+                        }
+                    }
+                    for (int kv = 0; kv < 2; kv++) {
+                        ok = mbar_wait(&s.empty[st], ph ^ 1u, abort_flag, kPolls);
+                        ok = __all_sync(0xffffffffu, ok);
+                        if (!ok) break;
+                        uint8_t* dst = skv + (size_t)st * kBytes;
+                        const CUtensorMap* map = kv ? &mv : &mk;
+                        const bool clean = kv && j >= first_masked;
+                        uint64_t* bar = clean ? &s.raw[st] : &s.full[st];
+                        if (clean) {
+                            raw_n ^= 1u << st;
+                            raw_any |= 1u << st;
+                        } else {
+                            full_n ^= 1u << st;
+                            full_any |= 1u << st;
+                        }
+                        if (p.tables) {
+                            if (lane == 0) mbar_expect_tx(bar, (uint32_t)(here << p.bs_shift) * D * 2);
+                            __syncwarp();
+                            if (lane < here)
+                                for (int h = 0; h < kHalves; h++)
+                                    tma_load_3d(dst + h * kHalfBytes + ((uint32_t)lane << p.bs_shift) * 128, map, bar,
+                                                h * 64, it.hk, id << p.bs_shift);
+                        } else if (elect_one()) {
+                            mbar_expect_tx(bar, kBytes);
+                            for (int h = 0; h < kHalves; h++)
+                                tma_load_3d(dst + h * kHalfBytes, map, bar, h * 64, it.hk, it.key0 + j * kTile);
+                        }
+                        __syncwarp();
+                        if (++st == kStages) {
+                            st = 0;
+                            ph ^= 1u;
+                        }
                     }
                 }
             }
-            // every stage's last load has landed before the CTA can end
+            // every last load has landed before the CTA can end
             for (int q = 0; q < kStages; q++) {
                 if (full_any >> q & 1u) mbar_drain(&s.full[q], (full_n >> q & 1u) ^ 1u);
                 if (raw_any >> q & 1u) mbar_drain(&s.raw[q], (raw_n >> q & 1u) ^ 1u);
             }
-            if (n_max > 0) mbar_drain(&s.q_full, 0);
+            for (int i = 0; i < 2; i++)
+                if (q_any >> i & 1u) mbar_drain(&s.q_full[i], (q_n >> i & 1u) ^ 1u);
         } else if (warp == 1) {
             // -------------------------------------------------------- MMAs --
-            if (n_max > 0 && elect_one()) {
+            if (elect_one()) {
                 const uint32_t q_addr = smem_u32(sq), kv_addr = smem_u32(skv);
                 uint32_t full_ph = 0, clean_ph = 0;     // parity of each stage's barriers
-                auto landed = [&](int st) {
-                    const bool in = mbar_wait(&s.full[st], full_ph >> st & 1u, abort_flag, kPolls);
-                    full_ph ^= 1u << st;
+                uint32_t tile_ph = 0, item_ph = 0;      // of each query tile's: per K/V tile, per item
+                int st = 0;
+                auto landed = [&](int stage) {
+                    const bool in = mbar_wait(&s.full[stage], full_ph >> stage & 1u, abort_flag, kPolls);
+                    full_ph ^= 1u << stage;
+                    tc_fence_after();
                     return in;
                 };
-                auto score = [&](int i, int st) {       // S_i = Q_i K^T
-                    const uint64_t a0 = sdesc_sw128(q_addr + i * kBytes), b0 = sdesc_sw128(kv_addr + st * kBytes);
+                auto score = [&](int i, int stage, bool last) {         // S_i = Q_i K^T
+                    const uint64_t a0 = sdesc_sw128(q_addr + i * kBytes), b0 = sdesc_sw128(kv_addr + stage * kBytes);
 #pragma unroll
                     for (int k = 0; k < D / 16; k++) {
                         const uint64_t off = (uint64_t)(((k >> 2) * kHalfBytes + (k & 3) * 32) >> 4);
                         mma_f16(tmem + i * 128, a0 + off, b0 + off, p.idesc_s, k > 0);
                     }
                     mma_commit(&s.s_full[i]);
+                    if (last) mma_commit(&s.q_empty[i]);
                 };
-                auto value = [&](int i, int st, int half, bool more) {  // O_i += P_i V over 64 keys
-                    const uint64_t b0 = sdesc_mn_sw128(kv_addr + st * kBytes);
+                auto value = [&](int i, int stage, int half, bool more) {   // O_i += P_i V over 64 keys
+                    const uint64_t b0 = sdesc_mn_sw128(kv_addr + stage * kBytes);
 #pragma unroll
                     for (int k = half * 4; k < half * 4 + 4; k++)
                         mma_f16_ta(tmem + 256 + i * 128, tmem + i * 128 + k * 8, b0 + (uint64_t)((k * 2048) >> 4),
                                    p.idesc_o, more || k > 0);
                 };
-                bool ok = mbar_wait(&s.q_full, 0, abort_flag, kPolls) && landed(0);
-                if (ok) {
-                    tc_fence_after();
-                    for (int i = 0; i < 2; i++)
-                        if (it.n[i] > 0) score(i, 0);
-                    mma_commit(&s.empty[0]);
-                }
-                int st = 1;                             // stage of V_j; K_{j+1} is in the one after it
-                for (int j = 0; j < n_max && ok; j++) {
-                    const int sv = st;
-                    if (j < first_masked) {
-                        ok = landed(sv);
-                    } else {
-                        ok = mbar_wait(&s.clean[sv], clean_ph >> sv & 1u, abort_flag, kPolls);
-                        clean_ph ^= 1u << sv;
-                    }
-                    if (!ok) break;
+                bool ok = true;
+                while (ok && walk.next(p, s, it)) {
+                    const int n_max = max(it.n[0], it.n[1]);
+                    if (n_max == 0) continue;
+                    const int first_masked = it.free_from / kTile;
+                    const int sk0 = st;
                     if (++st == kStages) st = 0;
-                    const int sk = st;
-                    if (j + 1 < n_max) {
-                        if (!(ok = landed(sk))) break;
-                        if (++st == kStages) st = 0;
-                    }
+                    if (!(ok = landed(sk0))) break;
                     for (int i = 0; i < 2 && ok; i++) {
-                        if (j < it.n[i]) {
-                            if (!(ok = mbar_wait(&s.p_full[i][0], j & 1, abort_flag, kPolls))) break;
-                            tc_fence_after();
-                            value(i, sv, 0, j > 0);
-                            if (!(ok = mbar_wait(&s.p_full[i][1], j & 1, abort_flag, kPolls))) break;
-                            tc_fence_after();
-                            value(i, sv, 1, true);
-                            if (j + 1 == it.n[i]) mma_commit(&s.o_full[i]);
-                        }
-                        if (j + 1 < it.n[i]) score(i, sk);
+                        if (it.n[i] == 0) continue;
+                        ok = mbar_wait(&s.q_full[i], item_ph >> i & 1u, abort_flag, kPolls);
+                        tc_fence_after();
+                        if (ok) score(i, sk0, it.n[i] == 1);
                     }
                     if (!ok) break;
-                    mma_commit(&s.empty[sv]);
-                    if (j + 1 < n_max) mma_commit(&s.empty[sk]);
+                    mma_commit(&s.empty[sk0]);
+                    for (int j = 0; j < n_max && ok; j++) {
+                        const int sv = st;
+                        if (++st == kStages) st = 0;
+                        if (j < first_masked) {
+                            ok = landed(sv);
+                        } else {
+                            ok = mbar_wait(&s.clean[sv], clean_ph >> sv & 1u, abort_flag, kPolls);
+                            clean_ph ^= 1u << sv;
+                            tc_fence_after();
+                        }
+                        if (!ok) break;
+                        const int sk = st;              // K_{j+1}
+                        const bool more = j + 1 < n_max;
+                        if (more && ++st == kStages) st = 0;
+                        bool here = false;              // K_{j+1} has landed
+                        for (int i = 0; i < 2 && ok; i++) {
+                            if (j < it.n[i]) {
+                                const uint32_t ph = tile_ph >> i & 1u;
+                                ok = mbar_wait(&s.p_full[i][0], ph, abort_flag, kPolls);
+                                // the last item's result has been read
+                                if (ok && j == 0)
+                                    ok = mbar_wait(&s.o_empty[i], (item_ph >> i & 1u) ^ 1u, abort_flag, kPolls);
+                                if (!ok) break;
+                                tc_fence_after();
+                                value(i, sv, 0, j > 0);
+                                if (!(ok = mbar_wait(&s.p_full[i][1], ph, abort_flag, kPolls))) break;
+                                tc_fence_after();
+                                value(i, sv, 1, true);
+                                tile_ph ^= 1u << i;
+                                if (j + 1 == it.n[i]) mma_commit(&s.o_full[i]);
+                            }
+                            if (j + 1 < it.n[i]) {
+                                if (!here) {
+                                    if (!(ok = landed(sk))) break;
+                                    here = true;
+                                }
+                                score(i, sk, j + 2 == it.n[i]);
+                            }
+                        }
+                        if (!ok) break;
+                        mma_commit(&s.empty[sv]);
+                        if (more) mma_commit(&s.empty[sk]);
+                    }
+                    for (int i = 0; i < 2; i++)
+                        if (it.n[i] > 0) item_ph ^= 1u << i;
                 }
+                // all issued MMAs complete before TMEM is released
                 mma_commit(&s.drain);
                 mbar_drain(&s.drain, 0);
             }
@@ -510,38 +640,44 @@ __global__ void __launch_bounds__(kThreads, 1) lm_prompt_kernel(const __grid_con
             // ------------------------------- values that not every row sees --
             const int t = (warp - 2) * 32 + lane;
             uint32_t raw_ph = 0;                        // parity of each stage's raw barrier
-            for (int j = first_masked; j < n_max; j++) {
-                const int st = (2 * j + 1) % kStages;
-                const bool ok = mbar_wait(&s.raw[st], raw_ph >> st & 1u, abort_flag, kPolls);
-                raw_ph ^= 1u << st;
-                if (!__all_sync(0xffffffffu, ok)) break;
-                uint8_t* v = skv + (size_t)st * kBytes;
-                const int live = min(kTile, it.end - j * kTile);
-                for (int e = t; e < kTile * D / 8; e += 64) {       // 16 bytes: 8 values of a key
-                    const int r = (e >> 3) & (kTile - 1), h = e / (8 * kTile);
-                    uint4* at = reinterpret_cast<uint4*>(v + e * 16);
-                    if (r >= live) {
-                        *at = make_uint4(0, 0, 0, 0);
-                        continue;
-                    }
-                    uint4 w = *at;
-                    uint32_t u[4] = {w.x, w.y, w.z, w.w};
-                    if (not_finite<T>(u[0]) | not_finite<T>(u[1]) | not_finite<T>(u[2]) | not_finite<T>(u[3])) {
-                        const int col = h * 64 + (((e & 7) ^ (r & 7)) << 3), key = j * kTile + r;
-                        for (int i = 0; i < 8; i++) {
-                            const uint32_t bits = (u[i >> 1] >> (16 * (i & 1))) & 0xffffu;
-                            if (not_finite<T>(bits) == 0) continue;
-                            const float f = Two<T>::one(bits);
-                            atomicMin(&s.bad[f != f ? 0 : f > 0.f ? 1 : 2][col + i], key);
-                            u[i >> 1] &= i & 1 ? 0x0000ffffu : 0xffff0000u;
+            int load0 = 0;                              // stage of the item's first load
+            bool ok = true;
+            while (ok && walk.next(p, s, it)) {
+                const int n_max = max(it.n[0], it.n[1]);
+                for (int j = it.free_from / kTile; j < n_max; j++) {
+                    const int st = (load0 + 2 * j + 1) % kStages;
+                    ok = mbar_wait(&s.raw[st], raw_ph >> st & 1u, abort_flag, kPolls);
+                    raw_ph ^= 1u << st;
+                    ok = __all_sync(0xffffffffu, ok);
+                    if (!ok) break;
+                    uint8_t* v = skv + (size_t)st * kBytes;
+                    const int live = min(kTile, it.end - j * kTile);
+                    for (int e = t; e < kTile * D / 8; e += 64) {       // 16 bytes: 8 values of a key
+                        const int r = (e >> 3) & (kTile - 1);
+                        uint4* at = reinterpret_cast<uint4*>(v + e * 16);
+                        if (r >= live) {
+                            *at = make_uint4(0, 0, 0, 0);
+                            continue;
                         }
-                        *at = make_uint4(u[0], u[1], u[2], u[3]);
-                        s.any_bad = 1;
+                        const uint4 w = *at;
+                        const uint32_t b0 = not_finite<T>(w.x), b1 = not_finite<T>(w.y), b2 = not_finite<T>(w.z),
+                                       b3 = not_finite<T>(w.w);
+                        if (b0 | b1 | b2 | b3) {
+                            auto keep = [](uint32_t x, uint32_t bad) {
+                                return x & ((bad & 0x8000u ? 0u : 0xffffu) | (bad & 0x80000000u ? 0u : 0xffff0000u));
+                            };
+                            *at = make_uint4(keep(w.x, b0), keep(w.y, b1), keep(w.z, b2), keep(w.w, b3));
+                            // the note of the item before the last one has been read by now
+                            volatile int* written = s.written;
+                            for (uint32_t i = 0; i < kPolls && min(written[0], written[1]) < 4 * (walk.k - 2) && !*abort_flag; i++) {}
+                            *reinterpret_cast<volatile int*>(&s.dirty[walk.k & 1]) = walk.k;
+                        }
                     }
+                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&s.clean[st]);
                 }
-                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&s.clean[st]);
+                load0 = (load0 + 2 * n_max) % kStages;
             }
         }
     } else {
@@ -550,94 +686,93 @@ __global__ void __launch_bounds__(kThreads, 1) lm_prompt_kernel(const __grid_con
         const int i = (warp >> 2) - 1;                  // query tile
         const int r = (warp & 3) * 32 + lane;           // row of it
         const int g = r % p.sh.group, tok = i * p.tokens + r / p.sh.group;
-        const bool live = r < p.tokens * p.sh.group && tok < it.ntok;
-        const int lim = live ? s.lim[tok] : 0;
-        const int n = it.n[i];
         const uint32_t lane_base = tmem + ((uint32_t)((warp & 3) * 32) << 16);
         const uint32_t ts = lane_base + i * 128, to = lane_base + 256 + i * 128;
-        float ref = 0.f, l = 0.f;
+        uint32_t tile_ph = 0, item_ph = 0;
         bool ok = true;
-        for (int j = 0; j < n; j++) {
-            ok = mbar_wait(&s.s_full[i], j & 1, abort_flag, kPolls);
-            ok = __all_sync(0xffffffffu, ok);
+        while (ok && walk.next(p, s, it)) {
+            const bool live = r < p.tokens * p.sh.group && tok < it.ntok;
+            const int lim = live ? keys_of(p, it, tok) : 0;
+            const int n = it.n[i];
+            // tiles from here on hold keys that some row does not see
+            const int first_masked = it.free_from / kTile;
+            float ref = 0.f, l = 0.f;
+            for (int j = 0; j < n; j++) {
+                ok = mbar_wait(&s.s_full[i], tile_ph, abort_flag, kPolls);
+                tile_ph ^= 1u;
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) break;
+                tc_fence_after();
+                float x[kTile];
+#pragma unroll
+                for (int q = 0; q < kTile; q += 32) tmem_ld32_async(ts + q, reinterpret_cast<uint32_t*>(x) + q);
+                tmem_wait_ld();
+                if (j >= first_masked) {
+                    const int see = lim - j * kTile;
+#pragma unroll
+                    for (int q = 0; q < kTile; q++) x[q] = q < see ? x[q] : -INFINITY;
+                }
+                float m0 = max3(x[0], x[1], x[2]), m1 = max3(x[3], x[4], x[5]), m2 = max3(x[6], x[7], x[8]),
+                      m3 = max3(x[9], x[10], x[11]);
+#pragma unroll
+                for (int q = 12; q < 124; q += 8) {
+                    m0 = max3(m0, x[q], x[q + 1]);
+                    m1 = max3(m1, x[q + 2], x[q + 3]);
+                    m2 = max3(m2, x[q + 4], x[q + 5]);
+                    m3 = max3(m3, x[q + 6], x[q + 7]);
+                }
+                m0 = max3(m0, x[124], x[125]);
+                m1 = max3(m1, x[126], x[127]);
+                const float m = max3(fmaxf(m0, m1), m2, m3);
+                if (j == 0) {
+                    ref = m == -INFINITY ? 0.f : m;
+                } else if (__any_sync(0xffffffffu, (m - ref) * p.c > 8.f)) {
+                    // the accumulator rests: its last product ran before these scores
+                    const float to_ref = fmaxf(ref, m), f = exp2_fast((ref - to_ref) * p.c);
+                    l *= f;
+                    ref = to_ref;
+#pragma unroll 1
+                    for (int q = 0; q < D; q += 8) tmem_scale8(to + q, f);
+                }
+                const float2 c2 = make_float2(p.c, p.c), base = make_float2(-ref * p.c, -ref * p.c);
+                float2 l0 = make_float2(0.f, 0.f), l1 = l0;
+#pragma unroll
+                for (int q = 0; q < kTile; q += 64) {
+                    uint32_t w[32];
+#pragma unroll
+                    for (int e = 0; e < 64; e += 4) {
+                        float2 a = fma2(make_float2(x[q + e], x[q + e + 1]), c2, base);
+                        float2 b = fma2(make_float2(x[q + e + 2], x[q + e + 3]), c2, base);
+                        a = make_float2(exp2_fast(a.x), exp2_fast(a.y));
+                        b = make_float2(exp2_fast(b.x), exp2_fast(b.y));
+                        l0 = add2(l0, a);
+                        l1 = add2(l1, b);
+                        w[e / 2] = Two<T>::pack(a.x, a.y);
+                        w[e / 2 + 1] = Two<T>::pack(b.x, b.y);
+                    }
+                    // half of the keys: their products start while the other half is worked on
+                    tmem_st32(ts + q / 2, w);
+                    tmem_wait_st();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&s.p_full[i][q / 64]);
+                }
+                l0 = add2(l0, l1);
+                l += l0.x + l0.y;
+            }
+            if (ok && n > 0) {
+                ok = mbar_wait(&s.o_full[i], item_ph, abort_flag, kPolls);
+                item_ph ^= 1u;
+                ok = __all_sync(0xffffffffu, ok);
+                tc_fence_after();
+            }
             if (!ok) break;
-            tc_fence_after();
-            float x[kTile];
-#pragma unroll
-            for (int q = 0; q < kTile; q += 32) tmem_ld32_async(ts + q, reinterpret_cast<uint32_t*>(x) + q);
-            tmem_wait_ld();
-            if (j >= first_masked) {
-                const int see = lim - j * kTile;
-#pragma unroll
-                for (int q = 0; q < kTile; q++) x[q] = q < see ? x[q] : -INFINITY;
-            }
-            float m0 = max3(x[0], x[1], x[2]), m1 = max3(x[3], x[4], x[5]), m2 = max3(x[6], x[7], x[8]),
-                  m3 = max3(x[9], x[10], x[11]);
-#pragma unroll
-            for (int q = 12; q < 124; q += 8) {
-                m0 = max3(m0, x[q], x[q + 1]);
-                m1 = max3(m1, x[q + 2], x[q + 3]);
-                m2 = max3(m2, x[q + 4], x[q + 5]);
-                m3 = max3(m3, x[q + 6], x[q + 7]);
-            }
-            m0 = max3(m0, x[124], x[125]);
-            m1 = max3(m1, x[126], x[127]);
-            const float m = max3(fmaxf(m0, m1), m2, m3);
-            if (j == 0) {
-                ref = m == -INFINITY ? 0.f : m;
-            } else if (__any_sync(0xffffffffu, (m - ref) * p.c > 8.f)) {
-                // the accumulator rests: its last product ran before these scores
-                const float to_ref = fmaxf(ref, m), f = exp2_fast((ref - to_ref) * p.c);
-                l *= f;
-                ref = to_ref;
-#pragma unroll
-                for (int q = 0; q < D; q += 32) {
-                    uint32_t a[32];
-                    tmem_ld32_async(to + q, a);
-                    tmem_wait_ld();
-#pragma unroll
-                    for (int e = 0; e < 32; e++) a[e] = __float_as_uint(__uint_as_float(a[e]) * f);
-                    tmem_st32(to + q, a);
-                }
-            }
-            const float2 c2 = make_float2(p.c, p.c), base = make_float2(-ref * p.c, -ref * p.c);
-            float2 l0 = make_float2(0.f, 0.f), l1 = l0;
-#pragma unroll
-            for (int q = 0; q < kTile; q += 64) {
-                uint32_t w[32];
-#pragma unroll
-                for (int e = 0; e < 64; e += 4) {
-                    float2 a = fma2(make_float2(x[q + e], x[q + e + 1]), c2, base);
-                    float2 b = fma2(make_float2(x[q + e + 2], x[q + e + 3]), c2, base);
-                    a = make_float2(exp2_fast(a.x), exp2_fast(a.y));
-                    b = make_float2(exp2_fast(b.x), exp2_fast(b.y));
-                    l0 = add2(l0, a);
-                    l1 = add2(l1, b);
-                    w[e / 2] = Two<T>::pack(a.x, a.y);
-                    w[e / 2 + 1] = Two<T>::pack(b.x, b.y);
-                }
-                // half of the keys: their products start while the other half is worked on
-                tmem_st32(ts + q / 2, w);
-                tmem_wait_st();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&s.p_full[i][q / 64]);
-            }
-            l0 = add2(l0, l1);
-            l += l0.x + l0.y;
-        }
-        if (ok && n > 0) {
-            ok = mbar_wait(&s.o_full[i], 0, abort_flag, kPolls);
-            ok = __all_sync(0xffffffffu, ok);
-            tc_fence_after();
-        }
-        if (ok) {
             const float inv = lim > 0 ? 1.f / l : 0.f;
-            const int h = hk * p.sh.group + g;
+            const int h = it.hk * p.sh.group + g;
             const long long row = it.q0 + tok;
-            const bool fix = s.any_bad != 0 && lim > 0;
-            const float lse = lim > 0 ? ref * p.sh.scale + logf(l) : -INFINITY;
+            const bool fix = *reinterpret_cast<volatile int*>(&s.dirty[walk.k & 1]) == walk.k && lim > 0;
             if (live) {
+                const float lse = lim > 0 ? ref * p.sh.scale + logf(l) : -INFINITY;
                 if (p.part)
                     p.part_lse[((long long)blockIdx.z * p.rows + row) * p.sh.hq + h] = lse;
                 else if (p.lse)
@@ -649,16 +784,19 @@ __global__ void __launch_bounds__(kThreads, 1) lm_prompt_kernel(const __grid_con
                 if (n > 0) {                            // the same for the warp
                     tmem_ld32_async(to + q, a);
                     tmem_wait_ld();
+                    if (q + 32 == D) {                  // the accumulator is free for the next item
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&s.o_empty[i]);
+                    }
                 }
                 float f[32];
 #pragma unroll
                 for (int e = 0; e < 32; e++) f[e] = lim > 0 ? __uint_as_float(a[e]) * inv : 0.f;
                 if (fix) {
-                    for (int e = 0; e < 32; e++) {
-                        const bool nan = s.bad[0][q + e] < lim, up = s.bad[1][q + e] < lim, down = s.bad[2][q + e] < lim;
-                        if (nan || (up && down)) f[e] = NAN;
-                        else if (up || down) f[e] += up ? INFINITY : -INFINITY;
-                    }
+#pragma unroll
+                    for (int e = 0; e < 32; e++)
+                        f[e] += not_finite_sum<T>(p, it, q + e, first_masked * kTile, lim);
                 }
                 if (!live) continue;
                 if (p.part) {
@@ -675,6 +813,8 @@ __global__ void __launch_bounds__(kThreads, 1) lm_prompt_kernel(const __grid_con
                                             Two<T>::pack(f[8 * e + 6], f[8 * e + 7]));
                 }
             }
+            __syncwarp();
+            if (lane == 0) atomicAdd(&s.written[i], 1);
         }
         tc_fence_before();
     }
@@ -683,6 +823,87 @@ __global__ void __launch_bounds__(kThreads, 1) lm_prompt_kernel(const __grid_con
     if (warp == 1) {
         tc_fence_after();
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmem));
+    }
+}
+
+// The items of a call, from the device's lengths: requests by their keys,
+// most first (in request order where there are many), each request's last pair
+// of tiles first.  One CTA.
+constexpr int kListThreads = 512;
+constexpr int kListSort = 512;          // requests that are sorted (by counting)
+
+__global__ void __launch_bounds__(kListThreads) lm_list_kernel(const Params p, int4* list, int* list_n)
+{
+    __shared__ int keys[kListSort];
+    __shared__ unsigned short order[kLmMaxRequests];
+    __shared__ int start[kLmMaxRequests + 1];
+    __shared__ int warp_sum[kListThreads / 32];
+    __shared__ int carry;
+    const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
+    const int pair = 2 * p.tokens;
+    pdl_wait();
+    pdl_launch();
+    auto rows_and_keys = [&](int b, int& first, int& n, bool report) {
+        const bool good = lm_rows(p.row_start, b, p.rows, first, n);
+        int k = n;
+        bool len = true;
+        if (p.tables) {
+            k = __ldg(p.kv_len + b);
+            len = lm_clamp_len(k, (long long)p.table_blocks << p.bs_shift);
+        }
+        if (report && !(good && len)) atomicOr(p.sh.err, CODEC_LM_ERR_LENGTH);
+        return k;
+    };
+    const bool sorted = p.B <= kListSort;
+    if (tid == 0) carry = 0;
+    for (int b = tid; b < p.B; b += kListThreads) {
+        int first, n;
+        const int k = rows_and_keys(b, first, n, true);
+        if (sorted) keys[b] = n > 0 ? k : -1; else order[b] = (unsigned short)b;
+    }
+    __syncthreads();
+    if (sorted && tid < p.B) {
+        int rank = 0;
+        for (int c = 0; c < p.B; c++) rank += keys[c] > keys[tid] || (keys[c] == keys[tid] && c < tid);
+        order[rank] = (unsigned short)tid;
+    }
+    __syncthreads();
+    for (int base = 0; base < p.B; base += kListThreads) {
+        const int x = base + tid;
+        int tiles = 0, first, n;
+        if (x < p.B) {
+            lm_rows(p.row_start, order[x], p.rows, first, n);
+            tiles = (n + pair - 1) / pair;
+        }
+        int incl = tiles;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int up = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += up;
+        }
+        if (lane == 31) warp_sum[w] = incl;
+        __syncthreads();
+        int at = carry;
+        for (int i = 0; i < w; i++) at += warp_sum[i];
+        if (x < p.B) start[x] = at + incl - tiles;
+        __syncthreads();
+        if (tid == kListThreads - 1) carry = at + incl;
+        __syncthreads();
+    }
+    // row_starts that overlap could make more items than there is room for
+    const int total = min(carry, p.rows / pair + min(p.rows, p.B));
+    if (tid == 0) *list_n = total;
+    for (int e = tid; e < total; e += kListThreads) {
+        int lo = 0, hi = p.B - 1;
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) >> 1;
+            if (start[mid] <= e) lo = mid; else hi = mid - 1;
+        }
+        int first, n;
+        const int b = order[lo];
+        const int k = rows_and_keys(b, first, n, false);
+        const int t = (n + pair - 1) / pair - 1 - (e - start[lo]);
+        list[e] = make_int4(b, first + t * pair, min(pair, n - t * pair), k - n + t * pair + 1);
     }
 }
 
@@ -732,7 +953,7 @@ uint32_t idesc(uint32_t format, int N, bool b_mn)
 
 template <typename T, int D>
 cudaError_t launch(const LmShape& sh, const void* q, long long qs, const LmKeys& ks, Params& p, dim3 grid,
-                   cudaStream_t s)
+                   cudaStream_t s, int4* list, int* list_n)
 {
     p.sh = sh;
     p.tokens = kTile / sh.group;
@@ -749,21 +970,30 @@ cudaError_t launch(const LmShape& sh, const void* q, long long qs, const LmKeys&
     const long long k_stride = paged ? (long long)sh.hk * D : ks.k_stride;
     const long long v_stride = paged ? (long long)sh.hk * D : ks.v_stride;
     const int box = paged ? 1 << ks.bs_shift : kTile;
+    p.v = ks.v;
+    p.v_stride = v_stride;
     CUtensorMap mq, mk, mv;
     if (!lm_make_map(&mq, sh.type, q, D, sh.hq, p.rows, qs, sh.group, p.tokens) ||
         !lm_make_map(&mk, sh.type, ks.k, D, sh.hk, key_rows, k_stride, 1, box) ||
         !lm_make_map(&mv, sh.type, ks.v, D, sh.hk, key_rows, v_stride, 1, box))
         return cudaErrorInvalidValue;
+    if (list) {
+        const cudaError_t e = launch_pdl(lm_list_kernel, dim3(1), dim3(kListThreads), 0, s, p, list, list_n);
+        if (e != cudaSuccess) return e;
+        p.list = list;
+        p.list_n = list_n;
+    }
     return launch_pdl(lm_prompt_kernel<T, D>, grid, dim3(kThreads), smem_bytes<D>(), s, mq, mk, mv, p);
 }
 
 cudaError_t launch_any(const LmShape& sh, const void* q, long long qs, const LmKeys& ks, Params& p, dim3 grid,
-                       cudaStream_t s)
+                       cudaStream_t s, int4* list = nullptr, int* list_n = nullptr)
 {
     if (sh.type == CODEC_LM_BF16)
-        return sh.D == 128 ? launch<__nv_bfloat16, 128>(sh, q, qs, ks, p, grid, s)
-                           : launch<__nv_bfloat16, 64>(sh, q, qs, ks, p, grid, s);
-    return sh.D == 128 ? launch<__half, 128>(sh, q, qs, ks, p, grid, s) : launch<__half, 64>(sh, q, qs, ks, p, grid, s);
+        return sh.D == 128 ? launch<__nv_bfloat16, 128>(sh, q, qs, ks, p, grid, s, list, list_n)
+                           : launch<__nv_bfloat16, 64>(sh, q, qs, ks, p, grid, s, list, list_n);
+    return sh.D == 128 ? launch<__half, 128>(sh, q, qs, ks, p, grid, s, list, list_n)
+                       : launch<__half, 64>(sh, q, qs, ks, p, grid, s, list, list_n);
 }
 
 }  // namespace
@@ -791,9 +1021,9 @@ cudaError_t launch_lm_prompt(const LmShape& sh, const LmPromptArgs& a, cudaStrea
     p.os = a.os;
     p.lse = a.lse;
     // pairs of query tiles: at most one partly filled pair per request
-    const int pair = 2 * (kTile / sh.group);
-    const long long items = a.rows / pair + std::min(a.rows, a.B);
-    return launch_any(sh, a.q, a.qs, a.keys, p, dim3((unsigned)items, (unsigned)sh.hk), s);
+    const long long items = lm_list_items(a.rows, a.B, sh.group);
+    if (items * sh.hk <= kSms) return launch_any(sh, a.q, a.qs, a.keys, p, dim3((unsigned)items, (unsigned)sh.hk), s);
+    return launch_any(sh, a.q, a.qs, a.keys, p, dim3(kSms), s, static_cast<int4*>(a.list), a.list_n);
 }
 
 cudaError_t launch_lm_shared(const LmShape& sh, const LmSharedArgs& a, cudaStream_t s)
