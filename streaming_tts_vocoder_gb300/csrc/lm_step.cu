@@ -8,13 +8,15 @@
 // A unit of work is (request, K/V head, split of `chunk` positions).  The
 // splits lie at fixed positions, so a result's bits do not depend on the
 // batch.  CTAs walk the units in turn (their number is known on the device
-// only); a producer warp keeps a ring of 64-key K and V tiles in flight across
-// units, so the copies never pause.  Four warps take 16 keys of a tile each:
-// scores and values by m16n8k16 MMAs with the group's heads as the 16 rows
-// (padded; the instruction is not what bounds this), each warp with its own
-// running softmax, joined at the unit's end.  The CTA that finishes the last
-// unit of a (request, head) joins the partial results in split order: no
-// second launch, and no order that could change a bit.
+// only); a producer warp keeps a ring of 64-key K and V tiles (the unit's
+// queries with the first) in flight across units, so the copies never pause.
+// Four warps take 16 keys of a tile each: scores and values by m16n8k16 MMAs
+// with the group's heads as the 16 rows (padded; the instruction is not what
+// bounds this), each warp with its own running softmax, joined at the unit's
+// end.  Partial results are joined in split order: by the CTA that finishes
+// the last unit of a (request, head) where no CTA has more than one unit, else
+// by a kernel of its own - the fence, the counter and the join cost a CTA
+// about 6,000 cycles, a third of a unit's time when one walks many.
 #include <algorithm>
 
 #include "lm.h"
@@ -42,6 +44,8 @@ struct Params {
     int shared_len, n_pre;              // shared part: length, partial results of it
     int chunk, max_splits;
     int stages;
+    int join;                           // partial results are joined here
+    int after_shared;                   // the shared part's kernel is running: nothing here needs its results
     float c;                            // scale x log2 e
     float* part;                        // [B][max_splits][hq][D]
     float* part_lse;
@@ -130,7 +134,7 @@ __device__ __forceinline__ Unit unit_at(const Params& p, const int* first, long 
     n.b = lo;
     n.split = x - first[lo];
     n.n_splits = first[lo + 1] - first[lo];
-    int len = __ldg(p.kv_len + lo);
+    int len = __ldcg(p.kv_len + lo);
     lm_clamp_len(len, (long long)p.table_blocks << p.bs_shift);
     n.empty = len == 0;
     n.key0 = p.shared_len + n.split * p.chunk;
@@ -138,15 +142,100 @@ __device__ __forceinline__ Unit unit_at(const Params& p, const int* first, long 
     return n;
 }
 
-template <int D> constexpr uint32_t stage_bytes() { return 2 * kKeys * D * 2; }
+// K tile, V tile, and the group's queries.
+template <int D>
+__host__ __device__ constexpr uint32_t stage_bytes(int group)
+{
+    return 2 * kKeys * D * 2 + ((group * D * 2 + 1023) & ~1023);
+}
+// A consumer's results lie [group][D + 8], so that the rows of a fragment fall into different banks.
+template <int D> constexpr int kPitch = D + 8;
 
-// [stages][K tile, V tile], then the consumers' results [4][group][D] fp32 and
-// their maxima and sums [4][16][2], the barriers, and the requests' first units.
+// [stages], then the consumers' results [4][group][pitch] fp32 and their
+// maxima and sums [4][16][2], the barriers, and the requests' first units.
 template <int D>
 size_t smem_bytes(int stages, int group, int B)
 {
-    return 1024 + (size_t)stages * stage_bytes<D>() + (size_t)kConsumers * group * D * 4 + kConsumers * 16 * 8 +
+    return 1024 + (size_t)stages * stage_bytes<D>(group) + (size_t)kConsumers * group * kPitch<D> * 4 + kConsumers * 16 * 8 +
            2 * kMaxStages * 8 + 64 + ((size_t)B + 1) * 4;
+}
+
+// Joins the partial results of (request, head), the shared part's first, in
+// order.  One warp; empty: the request has no position at all.
+template <typename T, int D>
+__device__ __forceinline__ void join_parts(const Params& p, int b, int h, int n_splits, bool empty, int lane)
+{
+    const int parts = p.n_pre + n_splits;
+    const long long shared_row = (long long)b * p.sh.hq + h, own_row = (long long)b * p.max_splits * p.sh.hq + h;
+    auto row_of = [&](int i) {
+        return i < p.n_pre ? (long long)i * p.B * p.sh.hq + shared_row : (long long)(i - p.n_pre) * p.sh.hq + own_row;
+    };
+    auto lse_of = [&](int i) { return __ldcg((i < p.n_pre ? p.pre_lse : p.part_lse) + row_of(i)); };
+    float m = -INFINITY;
+    bool nan = false;
+    const float mine = lane < parts ? lse_of(lane) : -INFINITY;
+    for (int i = lane; i < parts; i += 32) {
+        const float x = i < 32 ? mine : lse_of(i);
+        m = fmaxf(m, x);
+        nan |= x != x;
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    if (__any_sync(0xffffffffu, nan)) m = NAN;
+    const float ref = m == -INFINITY ? 0.f : m;
+    constexpr int kE = D / 32;
+    float v[kE] = {}, sum = 0.f;
+    for (int i0 = 0; i0 < parts; i0 += 32) {
+        float w = 0.f;
+        if (i0 + lane < parts) w = expf((i0 == 0 ? mine : lse_of(i0 + lane)) - ref);
+        const int cnt = min(32, parts - i0);
+#pragma unroll 8
+        for (int i = 0; i < cnt; i++) {
+            const float f = __shfl_sync(0xffffffffu, w, i);
+            const float* src = (i0 + i < p.n_pre ? p.pre : p.part) + row_of(i0 + i) * D;
+            float x[kE];
+            if constexpr (kE == 4) {
+                const float4 y = __ldcg(reinterpret_cast<const float4*>(src) + lane);
+                x[0] = y.x; x[1] = y.y; x[2] = y.z; x[3] = y.w;
+            } else {
+                const float2 y = __ldcg(reinterpret_cast<const float2*>(src) + lane);
+                x[0] = y.x; x[1] = y.y;
+            }
+            sum += f;
+#pragma unroll
+            for (int e = 0; e < kE; e++)
+                v[e] = f != 0.f ? fmaf(f, x[e], v[e]) : v[e];   // a part without keys has no value
+        }
+    }
+    const float inv = empty ? 0.f : 1.f / sum;
+    T* dst = static_cast<T*>(p.o) + b * p.os + (long long)h * D + lane * kE;
+    if constexpr (kE == 4)
+        *reinterpret_cast<uint2*>(dst) =
+            make_uint2(Mma<T>::pack(v[0] * inv, v[1] * inv), Mma<T>::pack(v[2] * inv, v[3] * inv));
+    else
+        *reinterpret_cast<uint32_t*>(dst) = Mma<T>::pack(v[0] * inv, v[1] * inv);
+    if (p.lse && lane == 0) p.lse[(long long)b * p.sh.hq + h] = empty ? -INFINITY : m + logf(sum);
+}
+
+__device__ __forceinline__ int splits_of(const Params& p, int len)
+{
+    return max(1, (max(0, len - p.shared_len) + p.chunk - 1) / p.chunk);
+}
+
+// A warp per (request, head) whose result is in parts.
+template <typename T, int D>
+__global__ void __launch_bounds__(128) lm_join_kernel(const __grid_constant__ Params p)
+{
+    pdl_wait();
+    pdl_launch();
+    const long long w = blockIdx.x * 4LL + (threadIdx.x >> 5);
+    const int b = (int)(w / p.sh.hq), h = (int)(w - (long long)b * p.sh.hq);
+    if (b >= p.B) return;
+    int len = __ldg(p.kv_len + b);
+    lm_clamp_len(len, (long long)p.table_blocks << p.bs_shift);
+    const int n = splits_of(p, len);
+    if (n == 1 && p.n_pre == 0) return;         // written by its unit
+    join_parts<T, D>(p, b, h, n, len == 0, threadIdx.x & 31);
 }
 
 template <typename T, int D>
@@ -158,8 +247,9 @@ __global__ void __launch_bounds__(kThreads) lm_step_kernel(const __grid_constant
     extern __shared__ uint8_t raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
     const int group = p.sh.group;
-    float* res = reinterpret_cast<float*>(smem + (size_t)p.stages * stage_bytes<D>());
-    float* ml = res + kConsumers * group * D;
+    const uint32_t pitch = stage_bytes<D>(group);
+    float* res = reinterpret_cast<float*>(smem + (size_t)p.stages * pitch);
+    float* ml = res + kConsumers * group * kPitch<D>;
     uint64_t* full = reinterpret_cast<uint64_t*>(ml + kConsumers * 16 * 2);
     uint64_t* empty = full + kMaxStages;
     int* flags = reinterpret_cast<int*>(empty + kMaxStages);    // abort, last, total
@@ -175,7 +265,9 @@ __global__ void __launch_bounds__(kThreads) lm_step_kernel(const __grid_constant
         flags[0] = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
-    pdl_wait();
+    // behind the shared part's kernel there is nothing to wait for: what this one
+    // reads was complete when that one passed its own wait (and is read from L2)
+    if (!p.after_shared) pdl_wait();
     pdl_launch();
     // units before each request: at least one per request, so that something writes its row
     if (warp == 0) {
@@ -184,10 +276,10 @@ __global__ void __launch_bounds__(kThreads) lm_step_kernel(const __grid_constant
             const int b = base + lane;
             int n = 0;
             if (b < p.B) {
-                int len = __ldg(p.kv_len + b);
+                int len = __ldcg(p.kv_len + b);
                 if (!lm_clamp_len(len, (long long)p.table_blocks << p.bs_shift) && blockIdx.x == 0)
                     atomicOr(p.sh.err, CODEC_LM_ERR_LENGTH);
-                n = max(1, (max(0, len - p.shared_len) + p.chunk - 1) / p.chunk);
+                n = splits_of(p, len);
             }
             int incl = n;
 #pragma unroll
@@ -217,12 +309,13 @@ __global__ void __launch_bounds__(kThreads) lm_step_kernel(const __grid_constant
         for (long long u = blockIdx.x; u < units && ok; u += gridDim.x) {
             const Unit n = unit_at(p, first, u);
             const int* table = p.tables + (long long)n.b * p.table_blocks;
+            const T* q = static_cast<const T*>(p.q) + n.b * p.qs + (long long)n.hk * group * D;
             for (int j = 0; j * kKeys < n.keys; j++) {
                 const int here = min(per, (n.keys - j * kKeys + (1 << box_shift) - 1) >> box_shift);
                 int row = 0;
                 if (lane < here) {
                     const int pos = n.key0 + j * kKeys + (lane << box_shift);
-                    int id = __ldg(table + (pos >> p.bs_shift));
+                    int id = __ldcg(table + (pos >> p.bs_shift));
                     if (id < 0 || id >= p.n_blocks) {
                         atomicOr(p.sh.err, CODEC_LM_ERR_BLOCK);
                         row = p.n_blocks << p.bs_shift;     // behind the last row: the copy writes zeros
@@ -233,8 +326,12 @@ __global__ void __launch_bounds__(kThreads) lm_step_kernel(const __grid_constant
                 ok = mbar_wait(&empty[st], ph ^ 1u, abort_flag, kPolls);
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break;
-                uint8_t* dst = smem + (size_t)st * stage_bytes<D>();
-                if (lane == 0) mbar_expect_tx(&full[st], (uint32_t)(here << box_shift) * D * 4);
+                uint8_t* dst = smem + (size_t)st * pitch;
+                if (lane == 0) {
+                    const uint32_t q_bytes = j == 0 ? group * D * 2 : 0;
+                    mbar_expect_tx(&full[st], (uint32_t)(here << box_shift) * D * 4 + q_bytes);
+                    if (q_bytes) bulk_load(dst + 2 * kTileBytes, q, &full[st], q_bytes);
+                }
                 __syncwarp();
                 if (lane < here)
                     for (int h = 0; h < D / 64; h++) {
@@ -262,7 +359,6 @@ __global__ void __launch_bounds__(kThreads) lm_step_kernel(const __grid_constant
         // this lane's row addresses for the K (keys x 16-byte chunks) and V fragments
         const int k_key = warp * 16 + (m8 >> 1) * 8 + l8, k_chunk = m8 & 1;
         const int v_key = warp * 16 + (m8 & 1) * 8 + l8, v_chunk = m8 >> 1;
-        const T* q = static_cast<const T*>(p.q);
         int st = 0;
         uint32_t ph = 0;
         // when a wait gives up the walk goes on without waiting (the flag is up):
@@ -270,18 +366,6 @@ __global__ void __launch_bounds__(kThreads) lm_step_kernel(const __grid_constant
         for (long long u = blockIdx.x; u < units; u += gridDim.x) {
             const Unit n = unit_at(p, first, u);
             uint32_t qf[D / 16][4];
-            {
-                const T* row = q + n.b * p.qs + (long long)n.hk * group * D;
-#pragma unroll
-                for (int k = 0; k < D / 16; k++) {
-                    const int at = k * 16 + cp;
-#pragma unroll
-                    for (int e = 0; e < 4; e++) {
-                        const int r = r0 + (e & 1) * 8, col = at + (e >> 1) * 8;
-                        qf[k][e] = r < group ? __ldg(reinterpret_cast<const uint32_t*>(row + (long long)r * D + col)) : 0u;
-                    }
-                }
-            }
             float acc[D / 8][4];
 #pragma unroll
             for (int i = 0; i < D / 8; i++)
@@ -291,7 +375,12 @@ __global__ void __launch_bounds__(kThreads) lm_step_kernel(const __grid_constant
             for (int j = 0; j * kKeys < n.keys; j++) {
                 const bool ok = mbar_wait(&full[st], ph, abort_flag, kPolls);
                 if (!__all_sync(0xffffffffu, ok)) break;
-                const uint32_t kt = base + (uint32_t)st * stage_bytes<D>(), vt = kt + kTileBytes;
+                const uint32_t kt = base + (uint32_t)st * pitch, vt = kt + kTileBytes;
+                if (j == 0) {       // rows behind the group's repeat its last: nobody reads them
+                    const uint32_t qt = vt + kTileBytes + min((m8 & 1) * 8 + l8, group - 1) * D * 2 + (m8 >> 1) * 16;
+#pragma unroll
+                    for (int k = 0; k < D / 16; k++) ldsm4(qt + k * 32, qf[k]);
+                }
                 const int left = n.keys - j * kKeys - warp * 16;    // keys of the warp's 16 that exist
                 if (left > 0) {
                     float s[2][4] = {};
@@ -380,7 +469,7 @@ __global__ void __launch_bounds__(kThreads) lm_step_kernel(const __grid_constant
                 l[h] += __shfl_xor_sync(0xffffffffu, l[h], 2);
                 const int r = r0 + 8 * h;
                 if (r < group) {
-                    float* dst = res + ((long long)warp * group + r) * D;
+                    float* dst = res + (warp * group + r) * kPitch<D>;
 #pragma unroll
                     for (int i = 0; i < D / 8; i++)
                         *reinterpret_cast<float2*>(dst + i * 8 + cp) = make_float2(acc[i][2 * h], acc[i][2 * h + 1]);
@@ -406,7 +495,7 @@ __global__ void __launch_bounds__(kThreads) lm_step_kernel(const __grid_constant
                         const float mw = ml[(w * 16 + g) * 2];
                         // a warp without keys has a sum of 0 and an accumulator of 0
                         const float f = mw == -INFINITY ? (m == -INFINITY ? 1.f : 0.f) : exp2_fast((mw - m) * p.c);
-                        const float4 x = *reinterpret_cast<const float4*>(res + ((long long)w * group + g) * D + d);
+                        const float4 x = *reinterpret_cast<const float4*>(res + (w * group + g) * kPitch<D> + d);
                         sum = fmaf(f, ml[(w * 16 + g) * 2 + 1], sum);
                         v.x = fmaf(f, x.x, v.x);
                         v.y = fmaf(f, x.y, v.y);
@@ -427,7 +516,7 @@ __global__ void __launch_bounds__(kThreads) lm_step_kernel(const __grid_constant
                     if (d == 0) __stcg(p.part_lse + at + g, lse);
                 }
             }
-            if (alone) {
+            if (alone || !p.join) {
                 consumers_sync();           // res is written again
                 continue;
             }
@@ -435,78 +524,20 @@ __global__ void __launch_bounds__(kThreads) lm_step_kernel(const __grid_constant
             consumers_sync();
             if (tid == 0) {
                 int* done = p.done + (long long)n.b * p.sh.hk + n.hk;
-                const int was = n.n_splits == 1 ? 0 : atomicAdd(done, 1);
-                flags[1] = was == n.n_splits - 1;
+                flags[1] = n.n_splits == 1 || atomicAdd(done, 1) == n.n_splits - 1;
                 if (flags[1] && n.n_splits > 1) *done = 0;
                 __threadfence();
             }
             consumers_sync();
             if (!flags[1]) continue;
-            // join the partial results, the shared part's first, in order: a warp per head
-            const int parts = p.n_pre + n.n_splits;
-            for (int g = warp; g < group; g += kConsumers) {
-                const long long h = n.hk * group + g;
-                auto lse_of = [&](int i) {
-                    return i < p.n_pre
-                               ? __ldcg(p.pre_lse + ((long long)i * p.B + n.b) * p.sh.hq + h)
-                               : __ldcg(p.part_lse + ((long long)n.b * p.max_splits + (i - p.n_pre)) * p.sh.hq + h);
-                };
-                float m = -INFINITY;
-                bool nan = false;
-                for (int i = lane; i < parts; i += 32) {
-                    const float x = lse_of(i);
-                    m = fmaxf(m, x);
-                    nan |= x != x;
-                }
-#pragma unroll
-                for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-                nan = __any_sync(0xffffffffu, nan);
-                if (nan) m = NAN;
-                const float ref2 = m == -INFINITY ? 0.f : m;
-                constexpr int kE = D / 32;
-                float v[kE] = {}, sum = 0.f;
-                for (int i0 = 0; i0 < parts; i0 += 32) {
-                    float w = 0.f;
-                    if (i0 + lane < parts) w = expf(lse_of(i0 + lane) - ref2);
-                    const int cnt = min(32, parts - i0);
-#pragma unroll 4
-                    for (int i = 0; i < cnt; i++) {
-                        const float f = __shfl_sync(0xffffffffu, w, i);
-                        const int part = i0 + i;
-                        const float* src = part < p.n_pre
-                                               ? p.pre + (((long long)part * p.B + n.b) * p.sh.hq + h) * D
-                                               : p.part + (((long long)n.b * p.max_splits + (part - p.n_pre)) * p.sh.hq + h) * D;
-                        sum += f;
-                        if constexpr (kE == 4) {
-                            const float4 x = __ldcg(reinterpret_cast<const float4*>(src) + lane);
-                            if (f != 0.f) {         // a part without keys has no value, whatever is there
-                                v[0] = fmaf(f, x.x, v[0]);
-                                v[1] = fmaf(f, x.y, v[1]);
-                                v[2] = fmaf(f, x.z, v[2]);
-                                v[3] = fmaf(f, x.w, v[3]);
-                            }
-                        } else {
-                            const float2 x = __ldcg(reinterpret_cast<const float2*>(src) + lane);
-                            if (f != 0.f) {
-                                v[0] = fmaf(f, x.x, v[0]);
-                                v[1] = fmaf(f, x.y, v[1]);
-                            }
-                        }
-                    }
-                }
-                const float inv = n.empty ? 0.f : 1.f / sum;
-                T* dst = static_cast<T*>(p.o) + n.b * p.os + h * D + lane * kE;
-                if constexpr (kE == 4)
-                    *reinterpret_cast<uint2*>(dst) =
-                        make_uint2(Mma<T>::pack(v[0] * inv, v[1] * inv), Mma<T>::pack(v[2] * inv, v[3] * inv));
-                else
-                    *reinterpret_cast<uint32_t*>(dst) = Mma<T>::pack(v[0] * inv, v[1] * inv);
-                if (p.lse && lane == 0) p.lse[(long long)n.b * p.sh.hq + h] = n.empty ? -INFINITY : m + logf(sum);
-            }
+            for (int g = warp; g < group; g += kConsumers)
+                join_parts<T, D>(p, n.b, n.hk * group + g, n.n_splits, n.empty, lane);
         }
     }
     __syncthreads();
     if (tid == 0 && flags[0]) atomicOr(p.sh.err, CODEC_LM_ERR_TIMEOUT);
+    // this kernel's end is its predecessors' too
+    if (p.after_shared) pdl_wait();
 }
 
 template <typename T, int D>
@@ -563,8 +594,13 @@ cudaError_t launch(const LmShape& sh, const LmStepArgs& a, cudaStream_t s)
     // a unit per request and head at least, and no more CTAs than the SMs hold at once
     const long long most = (long long)a.B * p.max_splits * sh.hk;
     const unsigned ctas = (unsigned)std::min<long long>(152 * per_sm, most);
-    return launch_pdl(lm_step_kernel<T, D>, dim3(ctas), dim3(kThreads), smem_bytes<D>(p.stages, sh.group, a.B), s, mk,
-                      mv, p);
+    p.after_shared = p.n_pre > 0;
+    // joined in this kernel where a CTA has one unit at most and needs no other kernel's results
+    p.join = most <= ctas && p.n_pre == 0;
+    const cudaError_t e = launch_pdl(lm_step_kernel<T, D>, dim3(ctas), dim3(kThreads), smem_bytes<D>(p.stages, sh.group, a.B), s, mk,
+                                     mv, p);
+    if (e != cudaSuccess || p.join || (p.n_pre == 0 && p.max_splits == 1)) return e;
+    return launch_pdl(lm_join_kernel<T, D>, dim3((unsigned)(((long long)a.B * sh.hq + 3) / 4)), dim3(128), 0, s, p);
 }
 
 }  // namespace
