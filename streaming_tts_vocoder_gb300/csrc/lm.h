@@ -110,6 +110,7 @@ struct LmStepSpace {
     float *part, *part_lse;         // [max_requests][max_splits][hq][D], [..][hq]
     float *pre, *pre_lse;           // [pre_max][max_requests][hq][D], [..][hq]
     int* done;                      // [max_requests][hk], zero between calls
+    int* taken;                     // the same (behind done)
 };
 
 struct LmStepArgs {

@@ -94,14 +94,21 @@ codec_status codec_lm_create(const codec_lm_config* cfg, codec_lm_t** out)
     lm->cfg = c;
     lm->device = dev;
     while ((1 << lm->bs_shift) < c.block_size) lm->bs_shift++;
-    // single tokens: splits of 256 positions, of more where a full table would have over 32 of them
+    // Single tokens: splits as short as 64 positions where the largest batch
+    // would not fill the SMs twice with longer ones, then of 256, then of as
+    // many as leave a full table 64.
     LmStepSpace& sp = lm->step;
     const int64_t positions = (int64_t)c.table_blocks * c.block_size;
-    for (sp.chunk = 256; positions > 32LL * sp.chunk;) sp.chunk *= 2;
+    const int64_t heads = (int64_t)c.max_requests * c.kv_heads;
+    for (sp.chunk = 64; (sp.chunk < 256 && heads * ((positions + sp.chunk - 1) / sp.chunk) > 304) ||
+                        positions > 64LL * sp.chunk;)
+        sp.chunk *= 2;
     sp.max_splits = (int)((positions + sp.chunk - 1) / sp.chunk);
-    // the shared part: about a CTA per SM, from the largest batch (so that the actual one changes no bits)
-    const int pairs = (c.max_requests + 2 * (128 / (c.q_heads / c.kv_heads)) - 1) / (2 * (128 / (c.q_heads / c.kv_heads)));
-    sp.pre_max = (int)std::max<int64_t>(1, std::min<int64_t>({32, 152 / ((int64_t)pairs * c.kv_heads), positions / 256}));
+    // The shared part: 64 CTAs (the rest of the SMs stream the requests' own
+    // parts meanwhile), by the largest batch, so that the actual one changes no bits.
+    const int tokens = 2 * (128 / (c.q_heads / c.kv_heads));
+    const int64_t pairs = (c.max_requests + tokens - 1) / tokens;
+    sp.pre_max = (int)std::max<int64_t>(1, std::min<int64_t>({32, 64 / (pairs * c.kv_heads), positions / 128}));
     const size_t row = (size_t)c.max_requests * c.q_heads;
     if (cudaMalloc(&lm->turn, sizeof(float2) * (size_t)c.max_positions * (c.head_dim / 2)) != cudaSuccess ||
         cudaMalloc(&lm->err, sizeof(unsigned)) != cudaSuccess ||
@@ -112,14 +119,15 @@ codec_status codec_lm_create(const codec_lm_config* cfg, codec_lm_t** out)
         cudaMalloc(&lm->list, 16 * (size_t)(lm_list_items(c.max_rows, c.max_requests, c.q_heads / c.kv_heads) + 1)) !=
             cudaSuccess ||
         cudaMalloc(&lm->list_n, sizeof(int)) != cudaSuccess ||
-        cudaMalloc(&sp.done, sizeof(int) * (size_t)c.max_requests * c.kv_heads) != cudaSuccess) {
+        cudaMalloc(&sp.done, sizeof(int) * ((size_t)c.max_requests * c.kv_heads + 1)) != cudaSuccess) {
         cudaGetLastError();
         lm_free(lm);
         return CODEC_ERR_OOM;
     }
+    sp.taken = sp.done + (size_t)c.max_requests * c.kv_heads;
     lm->shape = LmShape{c.type, c.q_heads, c.kv_heads, c.q_heads / c.kv_heads, c.head_dim, c.scale, lm->err};
     if (configure_lm_plan() != cudaSuccess || configure_lm_prompt() != cudaSuccess ||
-        configure_lm_step() != cudaSuccess || cudaMemset(sp.done, 0, sizeof(int) * (size_t)c.max_requests * c.kv_heads) != cudaSuccess ||
+        configure_lm_step() != cudaSuccess || cudaMemset(sp.done, 0, sizeof(int) * ((size_t)c.max_requests * c.kv_heads + 1)) != cudaSuccess ||
         cudaMemset(lm->err, 0, sizeof(unsigned)) != cudaSuccess ||
         launch_lm_turn_table(lm->turn, c.max_positions, c.head_dim, c.rope_theta, nullptr) != cudaSuccess ||
         cudaDeviceSynchronize() != cudaSuccess) {
@@ -146,7 +154,7 @@ codec_status codec_lm_errors(codec_lm_t* lm, uint32_t* bits, int32_t clear, void
     if (!on.ok || cudaMemcpyAsync(bits, lm->err, sizeof(uint32_t), cudaMemcpyDeviceToHost, cs) != cudaSuccess ||
         (clear && (cudaMemsetAsync(lm->err, 0, sizeof(uint32_t), cs) != cudaSuccess ||
                    // a call that gave up may have left its counts of finished units
-                   cudaMemsetAsync(lm->step.done, 0, sizeof(int) * (size_t)lm->cfg.max_requests * lm->cfg.kv_heads,
+                   cudaMemsetAsync(lm->step.done, 0, sizeof(int) * ((size_t)lm->cfg.max_requests * lm->cfg.kv_heads + 1),
                                    cs) != cudaSuccess)) ||
         cudaStreamSynchronize(cs) != cudaSuccess)
         return CODEC_ERR_CUDA;

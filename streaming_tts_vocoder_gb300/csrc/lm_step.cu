@@ -7,9 +7,11 @@
 //
 // A unit of work is (request, K/V head, split of `chunk` positions).  The
 // splits lie at fixed positions, so a result's bits do not depend on the
-// batch.  CTAs walk the units in turn (their number is known on the device
-// only); a producer warp keeps a ring of 64-key K and V tiles (the unit's
-// queries with the first) in flight across units, so the copies never pause.
+// batch.  The units' number is known on the device only: a CTA's producer warp
+// takes one after the other from a counter (CTAs start late where the shared
+// part's kernel holds their SM) and keeps a ring of 64-key K and V tiles, the
+// unit's queries with the first, in flight across units, so the copies never
+// pause.
 // Four warps take 16 keys of a tile each: scores and values by m16n8k16 MMAs
 // with the group's heads as the 16 rows (padded; the instruction is not what
 // bounds this), each warp with its own running softmax, joined at the unit's
@@ -52,6 +54,7 @@ struct Params {
     const float* pre;                   // [n_pre][B][hq][D]
     const float* pre_lse;
     int* done;                          // [B][hk] finished units; zero between calls
+    int* taken;                         // units taken from the counter (null: unit = blockIdx, + gridDim, ..); zero between calls
     void* o;
     long long os;
     float* lse;
@@ -114,6 +117,20 @@ __device__ __forceinline__ float exp2_fast(float x)
 
 __device__ __forceinline__ void consumers_sync() { asm volatile("bar.sync 1, %0;" ::"r"(32 * kConsumers) : "memory"); }
 
+__device__ __forceinline__ bool consumers_all(bool ok)
+{
+    uint32_t all;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.u32 p, %1, 0;\n\t"
+        "bar.red.and.pred q, 1, %2, p;\n\t"
+        "selp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(all)
+        : "r"((uint32_t)ok), "n"(32 * kConsumers)
+        : "memory");
+    return all != 0;
+}
+
 struct Unit {
     int b, hk, split, n_splits;
     int key0, keys;             // first position, positions of the split
@@ -121,11 +138,12 @@ struct Unit {
 };
 
 // The unit of index u: units run over the requests' splits, K/V heads innermost.
-__device__ __forceinline__ Unit unit_at(const Params& p, const int* first, long long u)
+// first, lens: the requests' first units and lengths.
+__device__ __forceinline__ Unit unit_at(const Params& p, const int* first, const int* lens, int u)
 {
     Unit n;
-    const int x = (int)(u / p.sh.hk);
-    n.hk = (int)(u - (long long)x * p.sh.hk);
+    const int x = u / p.sh.hk;
+    n.hk = u - x * p.sh.hk;
     int lo = 0, hi = p.B - 1;
     while (lo < hi) {
         const int mid = (lo + hi + 1) >> 1;
@@ -134,8 +152,7 @@ __device__ __forceinline__ Unit unit_at(const Params& p, const int* first, long 
     n.b = lo;
     n.split = x - first[lo];
     n.n_splits = first[lo + 1] - first[lo];
-    int len = __ldcg(p.kv_len + lo);
-    lm_clamp_len(len, (long long)p.table_blocks << p.bs_shift);
+    const int len = lens[lo];
     n.empty = len == 0;
     n.key0 = p.shared_len + n.split * p.chunk;
     n.keys = min(max(len - n.key0, 0), p.chunk);
@@ -152,12 +169,13 @@ __host__ __device__ constexpr uint32_t stage_bytes(int group)
 template <int D> constexpr int kPitch = D + 8;
 
 // [stages], then the consumers' results [4][group][pitch] fp32 and their
-// maxima and sums [4][16][2], the barriers, and the requests' first units.
+// maxima and sums [4][16][2], the barriers, and the requests' first units and
+// lengths.
 template <int D>
 size_t smem_bytes(int stages, int group, int B)
 {
     return 1024 + (size_t)stages * stage_bytes<D>(group) + (size_t)kConsumers * group * kPitch<D> * 4 + kConsumers * 16 * 8 +
-           2 * kMaxStages * 8 + 64 + ((size_t)B + 1) * 4;
+           2 * kMaxStages * 8 + 64 + (2 * (size_t)B + 1) * 4;
 }
 
 // Joins the partial results of (request, head), the shared part's first, in
@@ -228,6 +246,7 @@ __global__ void __launch_bounds__(128) lm_join_kernel(const __grid_constant__ Pa
 {
     pdl_wait();
     pdl_launch();
+    if (blockIdx.x == 0 && threadIdx.x == 0 && p.taken) *p.taken = 0;
     const long long w = blockIdx.x * 4LL + (threadIdx.x >> 5);
     const int b = (int)(w / p.sh.hq), h = (int)(w - (long long)b * p.sh.hq);
     if (b >= p.B) return;
@@ -252,8 +271,10 @@ __global__ void __launch_bounds__(kThreads) lm_step_kernel(const __grid_constant
     float* ml = res + kConsumers * group * kPitch<D>;
     uint64_t* full = reinterpret_cast<uint64_t*>(ml + kConsumers * 16 * 2);
     uint64_t* empty = full + kMaxStages;
-    int* flags = reinterpret_cast<int*>(empty + kMaxStages);    // abort, last, total
+    int* flags = reinterpret_cast<int*>(empty + kMaxStages);    // abort, last one of a (request, head)
+    int* unit_of = flags + 2;                                   // unit whose first tile a stage holds
     int* first = flags + 16;
+    int* lens = first + p.B + 1;
     volatile int* abort_flag = flags;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
@@ -280,6 +301,7 @@ __global__ void __launch_bounds__(kThreads) lm_step_kernel(const __grid_constant
                 if (!lm_clamp_len(len, (long long)p.table_blocks << p.bs_shift) && blockIdx.x == 0)
                     atomicOr(p.sh.err, CODEC_LM_ERR_LENGTH);
                 n = splits_of(p, len);
+                lens[b] = len;
             }
             int incl = n;
 #pragma unroll
@@ -293,7 +315,7 @@ __global__ void __launch_bounds__(kThreads) lm_step_kernel(const __grid_constant
         if (lane == 0) first[p.B] = before;
     }
     __syncthreads();
-    const long long units = (long long)first[p.B] * p.sh.hk;
+    const int units = first[p.B] * p.sh.hk;
 
     if (warp == kConsumers) {
         // -------------------------------------------------------- copies --
@@ -306,12 +328,18 @@ __global__ void __launch_bounds__(kThreads) lm_step_kernel(const __grid_constant
         }
         const int box_shift = min(p.bs_shift, 6);           // keys per box: a block, or half of one of 128
         const int per = kKeys >> box_shift;
-        for (long long u = blockIdx.x; u < units && ok; u += gridDim.x) {
-            const Unit n = unit_at(p, first, u);
+        int u = blockIdx.x;
+        while (ok) {
+            int next = u + gridDim.x;
+            if (p.taken && lane == 0) next = atomicAdd(p.taken, 1) + gridDim.x;     // needed when this unit's copies are out
+            if (u >= units) u = -1;
+            Unit n{};
+            if (u >= 0) n = unit_at(p, first, lens, u);
             const int* table = p.tables + (long long)n.b * p.table_blocks;
             const T* q = static_cast<const T*>(p.q) + n.b * p.qs + (long long)n.hk * group * D;
-            for (int j = 0; j * kKeys < n.keys; j++) {
-                const int here = min(per, (n.keys - j * kKeys + (1 << box_shift) - 1) >> box_shift);
+            // a unit without keys, and the end, take a stage without copies
+            for (int j = 0; j == 0 || j * kKeys < n.keys; j++) {
+                const int here = max(0, min(per, (n.keys - j * kKeys + (1 << box_shift) - 1) >> box_shift));
                 int row = 0;
                 if (lane < here) {
                     const int pos = n.key0 + j * kKeys + (lane << box_shift);
@@ -328,7 +356,8 @@ __global__ void __launch_bounds__(kThreads) lm_step_kernel(const __grid_constant
                 if (!ok) break;
                 uint8_t* dst = smem + (size_t)st * pitch;
                 if (lane == 0) {
-                    const uint32_t q_bytes = j == 0 ? group * D * 2 : 0;
+                    const uint32_t q_bytes = j == 0 && here > 0 ? group * D * 2 : 0;
+                    if (j == 0) unit_of[st] = u;
                     mbar_expect_tx(&full[st], (uint32_t)(here << box_shift) * D * 4 + q_bytes);
                     if (q_bytes) bulk_load(dst + 2 * kTileBytes, q, &full[st], q_bytes);
                 }
@@ -345,6 +374,8 @@ __global__ void __launch_bounds__(kThreads) lm_step_kernel(const __grid_constant
                     ph ^= 1u;
                 }
             }
+            if (u < 0) break;
+            u = __shfl_sync(0xffffffffu, next, 0);
         }
         // every stage's last load has landed before the CTA can end
         for (int q = 0; q < p.stages && q < loads; q++) {
@@ -361,10 +392,13 @@ __global__ void __launch_bounds__(kThreads) lm_step_kernel(const __grid_constant
         const int v_key = warp * 16 + (m8 & 1) * 8 + l8, v_chunk = m8 >> 1;
         int st = 0;
         uint32_t ph = 0;
-        // when a wait gives up the walk goes on without waiting (the flag is up):
-        // the warps meet at every unit's barriers whatever each of them saw
-        for (long long u = blockIdx.x; u < units; u += gridDim.x) {
-            const Unit n = unit_at(p, first, u);
+        // when a wait gives up inside a unit its warps still meet at the unit's
+        // barriers; at the next unit they all leave
+        while (true) {
+            if (!consumers_all(mbar_wait(&full[st], ph, abort_flag, kPolls))) break;
+            const int u = *reinterpret_cast<volatile int*>(unit_of + st);
+            if (u < 0) break;
+            const Unit n = unit_at(p, first, lens, u);
             uint32_t qf[D / 16][4];
             float acc[D / 8][4];
 #pragma unroll
@@ -372,11 +406,11 @@ __global__ void __launch_bounds__(kThreads) lm_step_kernel(const __grid_constant
 #pragma unroll
                 for (int e = 0; e < 4; e++) acc[i][e] = 0.f;
             float ref[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
-            for (int j = 0; j * kKeys < n.keys; j++) {
-                const bool ok = mbar_wait(&full[st], ph, abort_flag, kPolls);
+            for (int j = 0; j == 0 || j * kKeys < n.keys; j++) {
+                const bool ok = j == 0 || mbar_wait(&full[st], ph, abort_flag, kPolls);
                 if (!__all_sync(0xffffffffu, ok)) break;
                 const uint32_t kt = base + (uint32_t)st * pitch, vt = kt + kTileBytes;
-                if (j == 0) {       // rows behind the group's repeat its last: nobody reads them
+                if (j == 0 && n.keys > 0) {     // rows behind the group's repeat its last: nobody reads them
                     const uint32_t qt = vt + kTileBytes + min((m8 & 1) * 8 + l8, group - 1) * D * 2 + (m8 >> 1) * 16;
 #pragma unroll
                     for (int k = 0; k < D / 16; k++) ldsm4(qt + k * 32, qf[k]);
@@ -569,7 +603,7 @@ cudaError_t launch(const LmShape& sh, const LmStepArgs& a, cudaStream_t s)
     if (p.shared_len > 0) {
         LmSharedArgs c{a.q, a.qs, a.B, ks, a.shared_table, p.shared_len, 0, a.ws.pre, a.ws.pre_lse};
         // splits by the object's shape and the shared length alone
-        const int n = std::max(1, std::min(a.ws.pre_max, p.shared_len / 256));
+        const int n = std::max(1, std::min(a.ws.pre_max, p.shared_len / 128));
         c.split_len = ((p.shared_len + n - 1) / n + 127) & ~127;
         p.n_pre = (p.shared_len + c.split_len - 1) / c.split_len;
         const cudaError_t e = launch_lm_shared(sh, c, s);
@@ -597,9 +631,11 @@ cudaError_t launch(const LmShape& sh, const LmStepArgs& a, cudaStream_t s)
     p.after_shared = p.n_pre > 0;
     // joined in this kernel where a CTA has one unit at most and needs no other kernel's results
     p.join = most <= ctas && p.n_pre == 0;
+    const bool two = !p.join && (p.n_pre > 0 || p.max_splits > 1);
+    p.taken = two ? a.ws.taken : nullptr;
     const cudaError_t e = launch_pdl(lm_step_kernel<T, D>, dim3(ctas), dim3(kThreads), smem_bytes<D>(p.stages, sh.group, a.B), s, mk,
                                      mv, p);
-    if (e != cudaSuccess || p.join || (p.n_pre == 0 && p.max_splits == 1)) return e;
+    if (e != cudaSuccess || !two) return e;
     return launch_pdl(lm_join_kernel<T, D>, dim3((unsigned)(((long long)a.B * sh.hq + 3) / 4)), dim3(128), 0, s, p);
 }
 
