@@ -77,8 +77,8 @@ struct LmPromptArgs {
     void* o;
     long long os;
     float* lse;
-    void* list;                     // workspace: lm_list_items() x 16 bytes, and their number
-    int* list_n;
+    void* list;                     // workspace: lm_list_items() x 16 bytes, their number and how many are taken
+    int* list_n;                    // [2]
 };
 // Pairs of query tiles that `rows` rows of at most B requests can make.
 inline long long lm_list_items(int rows, int B, int group)

@@ -16,7 +16,7 @@ struct codec_lm_s {
     unsigned* err = nullptr;
     LmStepSpace step{};
     void* list = nullptr;           // prompt attention's items
-    int* list_n = nullptr;
+    int* list_n = nullptr;          // their number, and how many are taken
 };
 
 namespace {
@@ -118,7 +118,7 @@ codec_status codec_lm_create(const codec_lm_config* cfg, codec_lm_t** out)
         cudaMalloc(&sp.pre_lse, sizeof(float) * row * sp.pre_max) != cudaSuccess ||
         cudaMalloc(&lm->list, 16 * (size_t)(lm_list_items(c.max_rows, c.max_requests, c.q_heads / c.kv_heads) + 1)) !=
             cudaSuccess ||
-        cudaMalloc(&lm->list_n, sizeof(int)) != cudaSuccess ||
+        cudaMalloc(&lm->list_n, 2 * sizeof(int)) != cudaSuccess ||
         cudaMalloc(&sp.done, sizeof(int) * ((size_t)c.max_requests * c.kv_heads + 1)) != cudaSuccess) {
         cudaGetLastError();
         lm_free(lm);

@@ -23,8 +23,8 @@
 // of them, longest first, that a small kernel makes from the lengths; copies
 // and MMAs of the next item then run while the last one is written.
 //
-// Roles (384 threads, one CTA per SM), each walking the items by itself:
-//   warp 0      copies: Q, then K and V tiles through a ring of stages; paged
+// Roles (384 threads, one CTA per SM):
+//   warp 0      takes the items from a counter; copies: Q, then K and V tiles through a ring of stages; paged
 //               keys one box per cache block, one block per lane
 //   warp 1      TMEM and MMA issue: the MMAs of one tile run while the
 //               softmax of the other does
@@ -71,6 +71,7 @@ struct Params {
     long long v_stride;
     const int4* list;           // items (request, first query row, tokens, keys of the first token); null: by blockIdx
     const int* list_n;
+    int* taken;                 // items taken from the list
     float c;                    // scale x log2 e
     uint32_t idesc_s, idesc_o;
     void* o;
@@ -206,13 +207,18 @@ __device__ __forceinline__ uint32_t not_finite(uint32_t w)
     return ((w & Two<T>::kExp) + Two<T>::kOne) & 0x80008000u;
 }
 
-template <int D> constexpr int stages() { return D == 128 ? 5 : 8; }
+template <int D> constexpr int stages() { return D == 128 ? 4 : 7; }
+constexpr int kWork = 4;                // items handed out ahead
+constexpr uint32_t kStageOut = 4096;    // per softmax warp: 32 rows of 128 bytes on their way out
 
 struct Shared {
     uint64_t drain;
     uint64_t full[kMaxStages], empty[kMaxStages];
     uint64_t raw[kMaxStages], clean[kMaxStages];    // V tiles that are cleaned before use: landed, cleaned
     uint64_t q_full[2], q_empty[2], s_full[2], p_full[2][2], o_full[2], o_empty[2];
+    uint64_t work_full[kWork], work_empty[kWork];
+    int4 work[kWork];
+    int work_hk[kWork];         // K/V head; -1: no more
     uint32_t tmem;
     int abort;
     int scan[kThreads / 32];
@@ -223,11 +229,11 @@ struct Shared {
 };
 
 template <int D> constexpr uint32_t tile_bytes() { return kTile * D * 2; }
-static_assert(sizeof(Shared) <= 227 * 1024 - 7 * 32768, "five stages of 32 KB beside two query tiles");
 template <int D> constexpr size_t smem_bytes()
 {
-    return (size_t)(2 + stages<D>()) * tile_bytes<D>() + sizeof(Shared);
+    return (size_t)(2 + stages<D>()) * tile_bytes<D>() + 8 * kStageOut + sizeof(Shared);
 }
+static_assert(smem_bytes<128>() <= 227 * 1024 && smem_bytes<64>() <= 227 * 1024, "shared memory");
 
 // Finds the CTA's request and query rows: item x of the requests' tile pairs,
 // in request order, each request's last (longest) pair first.  All threads.
@@ -300,34 +306,57 @@ __device__ __forceinline__ void derive(const Params& p, Item& it)
     it.n[1] = (most1 + kTile - 1) / kTile;
 }
 
-// The CTA's items, one after the other: each role has a walk of its own.
+// The CTA's items, one after the other.  The copy warp takes them from a
+// counter and hands them on; each other role waits for them by itself.
 struct Walk {
     int k = 0;                  // items so far
-    int count;                  // of the list, with heads
-    __device__ __forceinline__ Walk(const Params& p) : count(p.list ? __ldg(p.list_n) * p.sh.hk : 0) {}
-    __device__ __forceinline__ bool next(const Params& p, const Shared& s, Item& it)
+
+    __device__ __forceinline__ bool set(const Params& p, Item& it, int4 e, int hk)
     {
-        if (!p.list) {
-            if (k++ || !s.found) return false;
-            it = s.item;
-            return true;
-        }
-        // rounds alternate their direction, so that no CTA gets the longer item of each
-        const long long w = (long long)k * gridDim.x + (k & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
-        k++;
-        if (w >= count) {
-            // the last round may go backwards: a CTA without an item in it has none in any later one
-            return false;
-        }
-        const int x = (int)w / p.sh.hk;
-        const int4 e = __ldg(p.list + x);
-        it.hk = (int)w - x * p.sh.hk;
+        if (hk < 0) return false;
+        it.hk = hk;
         it.b = e.x;
         it.q0 = e.y;
         it.ntok = e.z;
         it.first = e.w;
         derive(p, it);
         return true;
+    }
+    // The copy warp hands out (e, hk).
+    __device__ __forceinline__ bool hand_out(const Params& p, Shared& s, int4 e, int hk, Item& it, int lane)
+    {
+        if (!p.list) {
+            if (k++ || !s.found) return false;
+            it = s.item;
+            return true;
+        }
+        const int slot = k % kWork;
+        const bool ok = mbar_wait(&s.work_empty[slot], (uint32_t)(k / kWork & 1) ^ 1u, &s.abort, kPolls);
+        k++;
+        if (!__all_sync(0xffffffffu, ok)) return false;
+        if (lane == 0) {
+            s.work[slot] = e;
+            s.work_hk[slot] = hk;
+            mbar_arrive(&s.work_full[slot]);
+        }
+        return set(p, it, e, hk);
+    }
+    // Every other role; arrives: one thread of each waiting warp.
+    __device__ __forceinline__ bool next(const Params& p, Shared& s, Item& it, bool arrives)
+    {
+        if (!p.list) {
+            if (k++ || !s.found) return false;
+            it = s.item;
+            return true;
+        }
+        const int slot = k % kWork;
+        const bool ok = mbar_wait(&s.work_full[slot], (uint32_t)(k / kWork & 1), &s.abort, kPolls);
+        k++;
+        if (!ok) return false;
+        const int4 e = s.work[slot];
+        const int hk = s.work_hk[slot];
+        if (arrives) mbar_arrive(&s.work_empty[slot]);
+        return set(p, it, e, hk);
     }
 };
 
@@ -365,7 +394,8 @@ __global__ void __launch_bounds__(kThreads, 1) lm_prompt_kernel(const __grid_con
     extern __shared__ __align__(1024) uint8_t smem[];
     uint8_t* sq = smem;                                 // two query tiles
     uint8_t* skv = smem + 2 * kBytes;                   // ring: K tile, V tile, K tile, ...
-    Shared& s = *reinterpret_cast<Shared*>(skv + (size_t)kStages * kBytes);
+    uint8_t* sout = skv + (size_t)kStages * kBytes;     // rows on their way out
+    Shared& s = *reinterpret_cast<Shared*>(sout + 8 * kStageOut);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
     if (tid == 0) {
@@ -385,6 +415,10 @@ __global__ void __launch_bounds__(kThreads, 1) lm_prompt_kernel(const __grid_con
             mbar_init(&s.o_full[i], 1);
             mbar_init(&s.o_empty[i], 4);
             s.dirty[i] = 0;
+        }
+        for (int i = 0; i < kWork; i++) {
+            mbar_init(&s.work_full[i], 1);
+            mbar_init(&s.work_empty[i], 11);            // MMA thread, 2 cleaning and 8 softmax warps
         }
         s.abort = 0;
         s.found = 0;
@@ -448,7 +482,7 @@ __global__ void __launch_bounds__(kThreads, 1) lm_prompt_kernel(const __grid_con
         __syncthreads();
     }
     volatile int* abort_flag = &s.abort;
-    Walk walk(p);
+    Walk walk;
     Item it;
 
     if (warp < 4) {
@@ -461,7 +495,24 @@ __global__ void __launch_bounds__(kThreads, 1) lm_prompt_kernel(const __grid_con
             const int per = kTile >> p.bs_shift;        // cache blocks per tile
             const int g = p.sh.group;
             bool ok = true;
-            while (ok && walk.next(p, s, it)) {
+            int4 entry = make_int4(0, 0, 0, 0);
+            int entry_hk = -1;
+            const int count = p.list ? __ldg(p.list_n) * p.sh.hk : 0;
+            auto fetch = [&](int w) {
+                entry_hk = -1;
+                if (w < count) {
+                    entry_hk = w % p.sh.hk;
+                    entry = __ldg(p.list + w / p.sh.hk);
+                }
+            };
+            if (p.list) fetch(blockIdx.x);
+            while (ok && walk.hand_out(p, s, entry, entry_hk, it, lane)) {
+                // the next one: needed when this one's copies are out
+                if (p.list) {
+                    int w = 0;
+                    if (lane == 0) w = atomicAdd(p.taken, 1) + gridDim.x;
+                    fetch(__shfl_sync(0xffffffffu, w, 0));
+                }
                 const int n_max = max(it.n[0], it.n[1]);
                 const int first_masked = it.free_from / kTile;
                 const int* table = nullptr;
@@ -570,7 +621,7 @@ __global__ void __launch_bounds__(kThreads, 1) lm_prompt_kernel(const __grid_con
                                    p.idesc_o, more || k > 0);
                 };
                 bool ok = true;
-                while (ok && walk.next(p, s, it)) {
+                while (ok && walk.next(p, s, it, true)) {
                     const int n_max = max(it.n[0], it.n[1]);
                     if (n_max == 0) continue;
                     const int first_masked = it.free_from / kTile;
@@ -642,7 +693,7 @@ __global__ void __launch_bounds__(kThreads, 1) lm_prompt_kernel(const __grid_con
             uint32_t raw_ph = 0;                        // parity of each stage's raw barrier
             int load0 = 0;                              // stage of the item's first load
             bool ok = true;
-            while (ok && walk.next(p, s, it)) {
+            while (ok && __all_sync(0xffffffffu, walk.next(p, s, it, lane == 0))) {
                 const int n_max = max(it.n[0], it.n[1]);
                 for (int j = it.free_from / kTile; j < n_max; j++) {
                     const int st = (load0 + 2 * j + 1) % kStages;
@@ -690,7 +741,7 @@ __global__ void __launch_bounds__(kThreads, 1) lm_prompt_kernel(const __grid_con
         const uint32_t ts = lane_base + i * 128, to = lane_base + 256 + i * 128;
         uint32_t tile_ph = 0, item_ph = 0;
         bool ok = true;
-        while (ok && walk.next(p, s, it)) {
+        while (ok && __all_sync(0xffffffffu, walk.next(p, s, it, lane == 0))) {
             const bool live = r < p.tokens * p.sh.group && tok < it.ntok;
             const int lim = live ? keys_of(p, it, tok) : 0;
             const int n = it.n[i];
@@ -778,39 +829,67 @@ __global__ void __launch_bounds__(kThreads, 1) lm_prompt_kernel(const __grid_con
                 else if (p.lse)
                     p.lse[row * p.sh.hq + h] = lse;
             }
+            // A row per lane would touch 32 lines with every store; so 32 rows of 128
+            // bytes go through shared memory (16-byte chunks swizzled by the row) and
+            // leave as four whole rows per store.  Rolled loops: this runs once per
+            // item, and unrolled it came from beyond the instruction cache each time.
+            uint8_t* out = sout + (size_t)(warp - 4) * kStageOut;
+            const unsigned rows = __ballot_sync(0xffffffffu, live);
+            const unsigned long long mine = reinterpret_cast<unsigned long long>(
+                p.part ? static_cast<void*>(p.part + (((long long)blockIdx.z * p.rows + row) * p.sh.hq + h) * D)
+                       : static_cast<void*>(static_cast<T*>(p.o) + row * p.os + (long long)h * D));
+            const int step = p.part ? 32 : 64;          // columns in 128 bytes
+#pragma unroll 1
+            for (int q = 0; q < D; q += step) {
+#pragma unroll 1
+                for (int c = 0; c < step; c += 32) {
+                    uint32_t a[32] = {};
+                    if (n > 0) {                        // the same for the warp
+                        tmem_ld32_async(to + q + c, a);
+                        tmem_wait_ld();
+                    }
+                    float f[32];
 #pragma unroll
-            for (int q = 0; q < D; q += 32) {
-                uint32_t a[32] = {};
-                if (n > 0) {                            // the same for the warp
-                    tmem_ld32_async(to + q, a);
-                    tmem_wait_ld();
-                    if (q + 32 == D) {                  // the accumulator is free for the next item
-                        tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(&s.o_empty[i]);
+                    for (int e = 0; e < 32; e++) f[e] = lim > 0 ? __uint_as_float(a[e]) * inv : 0.f;
+                    if (p.part) {
+#pragma unroll
+                        for (int e = 0; e < 8; e++)
+                            *reinterpret_cast<float4*>(out + lane * 128 + ((e ^ (lane & 7)) << 4)) =
+                                make_float4(f[4 * e], f[4 * e + 1], f[4 * e + 2], f[4 * e + 3]);
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 4; e++)
+                            *reinterpret_cast<uint4*>(out + lane * 128 + (((c / 8 + e) ^ (lane & 7)) << 4)) =
+                                make_uint4(Two<T>::pack(f[8 * e], f[8 * e + 1]), Two<T>::pack(f[8 * e + 2], f[8 * e + 3]),
+                                           Two<T>::pack(f[8 * e + 4], f[8 * e + 5]),
+                                           Two<T>::pack(f[8 * e + 6], f[8 * e + 7]));
                     }
                 }
-                float f[32];
-#pragma unroll
-                for (int e = 0; e < 32; e++) f[e] = lim > 0 ? __uint_as_float(a[e]) * inv : 0.f;
-                if (fix) {
-#pragma unroll
-                    for (int e = 0; e < 32; e++)
-                        f[e] += not_finite_sum<T>(p, it, q + e, first_masked * kTile, lim);
+                __syncwarp();
+                if (q + step >= D && n > 0) {           // the accumulator is free for the next item
+                    tc_fence_before();
+                    if (lane == 0) mbar_arrive(&s.o_empty[i]);
                 }
-                if (!live) continue;
-                if (p.part) {
-                    float4* dst = reinterpret_cast<float4*>(
-                        p.part + (((long long)blockIdx.z * p.rows + row) * p.sh.hq + h) * D + q);
 #pragma unroll
-                    for (int e = 0; e < 8; e++) dst[e] = make_float4(f[4 * e], f[4 * e + 1], f[4 * e + 2], f[4 * e + 3]);
-                } else {
-                    uint4* dst = reinterpret_cast<uint4*>(static_cast<T*>(p.o) + row * p.os + (long long)h * D + q);
-#pragma unroll
-                    for (int e = 0; e < 4; e++)
-                        dst[e] = make_uint4(Two<T>::pack(f[8 * e], f[8 * e + 1]), Two<T>::pack(f[8 * e + 2], f[8 * e + 3]),
-                                            Two<T>::pack(f[8 * e + 4], f[8 * e + 5]),
-                                            Two<T>::pack(f[8 * e + 6], f[8 * e + 7]));
+                for (int e = 0; e < 8; e++) {
+                    const int from = 4 * e + (lane >> 3), chunk = lane & 7;
+                    const unsigned long long dst = __shfl_sync(0xffffffffu, mine, from);
+                    if (rows >> from & 1u)
+                        *reinterpret_cast<uint4*>(dst + (p.part ? q * 4 : q * 2) + chunk * 16) =
+                            *reinterpret_cast<const uint4*>(out + from * 128 + ((chunk ^ (from & 7)) << 4));
+                }
+                __syncwarp();
+            }
+            if (fix) {
+                // a finite sum plus what is not finite is the latter
+#pragma unroll 1
+                for (int c = 0; c < D; c++) {
+                    const float x = not_finite_sum<T>(p, it, c, first_masked * kTile, lim);
+                    if (x == 0.f) continue;
+                    if (p.part)
+                        reinterpret_cast<float*>(mine)[c] = x;
+                    else
+                        reinterpret_cast<T*>(mine)[c] = (T)x;
                 }
             }
             __syncwarp();
@@ -832,7 +911,7 @@ __global__ void __launch_bounds__(kThreads, 1) lm_prompt_kernel(const __grid_con
 constexpr int kListThreads = 512;
 constexpr int kListSort = 512;          // requests that are sorted (by counting)
 
-__global__ void __launch_bounds__(kListThreads) lm_list_kernel(const Params p, int4* list, int* list_n)
+__global__ void __launch_bounds__(kListThreads) lm_list_kernel(const Params p, int4* list, int* list_n, int* taken)
 {
     __shared__ int keys[kListSort];
     __shared__ unsigned short order[kLmMaxRequests];
@@ -892,7 +971,10 @@ __global__ void __launch_bounds__(kListThreads) lm_list_kernel(const Params p, i
     }
     // row_starts that overlap could make more items than there is room for
     const int total = min(carry, p.rows / pair + min(p.rows, p.B));
-    if (tid == 0) *list_n = total;
+    if (tid == 0) {
+        *list_n = total;
+        *taken = 0;
+    }
     for (int e = tid; e < total; e += kListThreads) {
         int lo = 0, hi = p.B - 1;
         while (lo < hi) {
@@ -978,10 +1060,11 @@ cudaError_t launch(const LmShape& sh, const void* q, long long qs, const LmKeys&
         !lm_make_map(&mv, sh.type, ks.v, D, sh.hk, key_rows, v_stride, 1, box))
         return cudaErrorInvalidValue;
     if (list) {
-        const cudaError_t e = launch_pdl(lm_list_kernel, dim3(1), dim3(kListThreads), 0, s, p, list, list_n);
+        const cudaError_t e = launch_pdl(lm_list_kernel, dim3(1), dim3(kListThreads), 0, s, p, list, list_n, list_n + 1);
         if (e != cudaSuccess) return e;
         p.list = list;
         p.list_n = list_n;
+        p.taken = list_n + 1;
     }
     return launch_pdl(lm_prompt_kernel<T, D>, grid, dim3(kThreads), smem_bytes<D>(), s, mq, mk, mv, p);
 }
