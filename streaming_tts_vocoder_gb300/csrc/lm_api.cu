@@ -94,21 +94,22 @@ codec_status codec_lm_create(const codec_lm_config* cfg, codec_lm_t** out)
     lm->cfg = c;
     lm->device = dev;
     while ((1 << lm->bs_shift) < c.block_size) lm->bs_shift++;
-    // Single tokens: splits as short as 64 positions where the largest batch
-    // would not fill the SMs twice with longer ones, then of 256, then of as
-    // many as leave a full table 64.
+    // Single tokens: splits of 64 positions, of up to 512 as long as the largest
+    // batch over full tables still makes eight for every CTA that fits the GPU,
+    // and of as many as leave a full table 64.
     LmStepSpace& sp = lm->step;
     const int64_t positions = (int64_t)c.table_blocks * c.block_size;
     const int64_t heads = (int64_t)c.max_requests * c.kv_heads;
-    for (sp.chunk = 64; (sp.chunk < 256 && heads * ((positions + sp.chunk - 1) / sp.chunk) > 304) ||
-                        positions > 64LL * sp.chunk;)
+    sp.chunk = 64;
+    while ((sp.chunk < 512 && heads * ((positions + 2 * sp.chunk - 1) / (2 * sp.chunk)) >= 8 * 304) ||
+           positions > 64LL * sp.chunk)
         sp.chunk *= 2;
     sp.max_splits = (int)((positions + sp.chunk - 1) / sp.chunk);
     // The shared part: 64 CTAs (the rest of the SMs stream the requests' own
     // parts meanwhile), by the largest batch, so that the actual one changes no bits.
     const int tokens = 2 * (128 / (c.q_heads / c.kv_heads));
     const int64_t pairs = (c.max_requests + tokens - 1) / tokens;
-    sp.pre_max = (int)std::max<int64_t>(1, std::min<int64_t>({32, 64 / (pairs * c.kv_heads), positions / 128}));
+    sp.pre_max = (int)std::max<int64_t>(1, std::min<int64_t>({32, 64 / (pairs * c.kv_heads), positions / 256}));
     const size_t row = (size_t)c.max_requests * c.q_heads;
     if (cudaMalloc(&lm->turn, sizeof(float2) * (size_t)c.max_positions * (c.head_dim / 2)) != cudaSuccess ||
         cudaMalloc(&lm->err, sizeof(unsigned)) != cudaSuccess ||

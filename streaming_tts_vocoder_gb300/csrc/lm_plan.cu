@@ -21,44 +21,30 @@ namespace codec {
 
 namespace {
 
-constexpr int kPlanThreads = 512;
-constexpr int kPlanRows = 2048;     // rows that make another CTA worth its running sums
+constexpr int kPlanThreads = 1024;
+constexpr int kPlanRows = 4096;     // rows that make another CTA worth its running sums
 
-struct Scan {
-    long long warp[kPlanThreads / 32];
-    long long carry;
+struct Sums {
+    long long rows, take, give;
+    __device__ __forceinline__ Sums operator+(const Sums& o) const { return {rows + o.rows, take + o.take, give + o.give}; }
 };
 
-// Exclusive running sum over the block of one value per thread, on top of
-// *carry, which then grows by the block's total.
-__device__ __forceinline__ long long block_sum(Scan& s, long long v)
+__device__ __forceinline__ Sums warp_sums(Sums v)       // inclusive
 {
-    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-    long long incl = v;
+    const int lane = threadIdx.x & 31;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const long long up = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o) incl += up;
+        const Sums up = {__shfl_up_sync(0xffffffffu, v.rows, o), __shfl_up_sync(0xffffffffu, v.take, o),
+                         __shfl_up_sync(0xffffffffu, v.give, o)};
+        if (lane >= o) v = v + up;
     }
-    if (lane == 31) s.warp[w] = incl;
-    __syncthreads();
-    long long before = s.carry, total = 0;
-    for (int i = 0; i < kPlanThreads / 32; i++) {
-        if (i < w) before += s.warp[i];
-        total += s.warp[i];
-    }
-    __syncthreads();
-    if (threadIdx.x == 0) s.carry += total;
-    __syncthreads();
-    return before + incl - v;
+    return v;
 }
 
 __device__ __forceinline__ int owned(int n, int shift, int shared)
 {
     return max(0, (int)(((long long)n + (1 << shift) - 1) >> shift) - shared);
 }
-
-__device__ __forceinline__ int ring_at(long long i, int n) { return (int)(i % n); }
 
 // Largest b in [0, B) with a[b] <= x (a[0] <= x, a nondecreasing).
 __device__ __forceinline__ int last_le(const int* a, int B, long long x)
@@ -71,81 +57,81 @@ __device__ __forceinline__ int last_le(const int* a, int B, long long x)
     return lo;
 }
 
-__global__ void __launch_bounds__(kPlanThreads) lm_plan_kernel(const LmPlanArgs a)
+// vec: slots and positions lie on 16 bytes.
+__global__ void __launch_bounds__(kPlanThreads) lm_plan_kernel(const LmPlanArgs a, int vec)
 {
     extern __shared__ int sm[];
     int* row0 = sm;                 // first row of each request (clamped to max_rows)
     int* take0 = row0 + a.B;        // blocks taken by those before it
     int* give0 = take0 + a.B;       // blocks given back by those before it
     unsigned char* st = reinterpret_cast<unsigned char*>(give0 + a.B);
-    __shared__ Scan s;
-    __shared__ long long rows_all, take_all, give_all;
-    const int tid = threadIdx.x;
+    __shared__ Sums warp_total[kPlanThreads / 32];
+    __shared__ Sums carry;
+    __shared__ long long take_all, give_all;
+    const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
     const bool first_cta = blockIdx.x == 0;
-    const long long most = (long long)a.table_blocks << a.bs_shift;
+    const int most = a.table_blocks << a.bs_shift;
 
     const long long head = a.free_in[0], tail = a.free_in[1];
     const bool ring_ok = head >= 0 && tail >= head && tail - head <= a.n_blocks;
     const long long n_free = ring_ok ? tail - head : 0;
     const long long room = ring_ok ? a.n_blocks - n_free : 0;   // ids that can be put back
+    const int head_at = ring_ok ? (int)(head % a.n_blocks) : 0, tail_at = ring_ok ? (int)(tail % a.n_blocks) : 0;
+    auto ring = [&](int at, long long i) {                      // i < n_blocks
+        const long long x = at + i;
+        return (int)(x >= a.n_blocks ? x - a.n_blocks : x);
+    };
 
-    // rows
-    if (tid == 0) s.carry = 0;
+    // All three sums at once.  Requests that grow are served up to the first
+    // whose rows or blocks do not fit (later ones that need some fit no better),
+    // so the sums need not leave anybody out.
+    if (tid == 0) {
+        carry = {0, 0, 0};
+        take_all = give_all = LLONG_MAX;
+    }
     __syncthreads();
     for (int base = 0; base < a.B; base += kPlanThreads) {
         const int b = base + tid;
-        int rows = 0;
+        Sums own{0, 0, 0};
         bool good = true;
         if (b < a.B) {
             const int n0 = __ldg(a.before + b), n1 = __ldg(a.after + b);
             good = n0 >= 0 && n1 >= 0 && n0 <= most && n1 <= most;
-            rows = good ? max(0, n1 - n0) : 0;
+            if (good) {
+                const int more = owned(n1, a.bs_shift, a.shared_blocks) - owned(n0, a.bs_shift, a.shared_blocks);
+                own = {max(0, n1 - n0), max(0, more), max(0, -more)};
+            }
         }
-        const long long at = block_sum(s, rows);
+        Sums at = warp_sums(own);
+        if (lane == 31) warp_total[w] = at;
+        __syncthreads();
+        if (w == 0) {
+            const Sums v = warp_sums(warp_total[lane]);
+            warp_total[lane] = carry + v;                       // everything up to that warp
+        }
+        __syncthreads();
+        const Sums before = w > 0 ? warp_total[w - 1] : carry;
+        at = before + at;                                       // up to and with this request
         if (b < a.B) {
-            row0[b] = (int)min(at, (long long)a.max_rows);
-            st[b] = !good ? 2 : at + rows > a.max_rows ? 3 : 0;
+            int status = 0;
+            if (!good) status = 2;
+            else if (at.rows > a.max_rows) status = 3;          // and so for every request behind it
+            else if (own.take > 0 && at.take > n_free) status = 1;
+            st[b] = status;
+            row0[b] = (int)min(at.rows - own.rows, (long long)a.max_rows);
+            const long long t = at.take - own.take;
+            take0[b] = (int)min(t, n_free);
+            give0[b] = (int)min(at.give - own.give, (long long)INT_MAX);
+            if (status != 0 && own.take > 0) atomicMin(&take_all, t);
+            if (status == 3) atomicMin(&give_all, at.give - own.give);
         }
+        __syncthreads();
+        if (tid == 0) carry = warp_total[kPlanThreads / 32 - 1];
+        __syncthreads();
     }
-    if (tid == 0) {
-        rows_all = min(s.carry, (long long)a.max_rows);
-        s.carry = 0;
-    }
-    __syncthreads();
-    // blocks taken: a request is served while the sum up to it fits
-    for (int base = 0; base < a.B; base += kPlanThreads) {
-        const int b = base + tid;
-        int need = 0;
-        if (b < a.B && st[b] == 0)
-            need = max(0, owned(__ldg(a.after + b), a.bs_shift, a.shared_blocks) -
-                              owned(__ldg(a.before + b), a.bs_shift, a.shared_blocks));
-        const long long at = block_sum(s, need);
-        if (b < a.B) {
-            if (need > 0 && at + need > n_free) st[b] = 1;
-            take0[b] = (int)min(at, n_free);
-        }
-    }
-    // the sums of those served: the first one that is not ends the count
-    if (tid == 0) {
-        take_all = min(s.carry, n_free);
-        s.carry = 0;
-    }
-    __syncthreads();
-    for (int b = tid; b < a.B; b += kPlanThreads)
-        if (st[b] == 1) atomicMin(&take_all, (long long)take0[b]);
-    __syncthreads();
-    // blocks given back
-    for (int base = 0; base < a.B; base += kPlanThreads) {
-        const int b = base + tid;
-        int back = 0;
-        if (b < a.B && st[b] == 0)
-            back = max(0, owned(__ldg(a.before + b), a.bs_shift, a.shared_blocks) -
-                              owned(__ldg(a.after + b), a.bs_shift, a.shared_blocks));
-        const long long at = block_sum(s, back);
-        if (b < a.B) give0[b] = (int)min(at, (long long)INT_MAX);
-    }
-    if (tid == 0) give_all = min(s.carry, room);
-    __syncthreads();
+    const int rows_all = (int)min(carry.rows, (long long)a.max_rows);
+    const int taken = (int)min(min(take_all, carry.take), n_free);
+    const int given = (int)min(min(give_all, carry.give), room);
 
     if (first_cta) {
         for (int b = tid; b < a.B; b += kPlanThreads) {
@@ -154,61 +140,85 @@ __global__ void __launch_bounds__(kPlanThreads) lm_plan_kernel(const LmPlanArgs 
             a.kv_len[b] = st[b] == 0 ? __ldg(a.after + b) : 0;
         }
         if (tid == 0) {
-            a.row_start[a.B] = (int)rows_all;
-            a.free_out[0] = head + take_all;
-            a.free_out[1] = tail + give_all;
+            a.row_start[a.B] = rows_all;
+            a.free_out[0] = head + taken;
+            a.free_out[1] = tail + given;
             if (!ring_ok) atomicOr(a.err, CODEC_LM_ERR_FREE);
         }
     }
 
-    const long long t0 = (long long)blockIdx.x * kPlanThreads + tid, step = (long long)gridDim.x * kPlanThreads;
+    const int t0 = blockIdx.x * kPlanThreads + tid, step = gridDim.x * kPlanThreads;
     // table entries of the blocks taken
-    for (long long e = t0; e < take_all; e += step) {
+    for (int e = t0; e < taken; e += step) {
         const int b = last_le(take0, a.B, e);
-        const int j = a.shared_blocks + owned(__ldg(a.before + b), a.bs_shift, a.shared_blocks) + (int)(e - take0[b]);
-        a.tables[(long long)b * a.table_blocks + j] = a.free_list[ring_at(head + e, a.n_blocks)];
+        const int j = a.shared_blocks + owned(__ldg(a.before + b), a.bs_shift, a.shared_blocks) + (e - take0[b]);
+        a.tables[(long long)b * a.table_blocks + j] = a.free_list[ring(head_at, e)];
     }
     // blocks given back
-    for (long long e = t0; e < give_all; e += step) {
+    for (int e = t0; e < given; e += step) {
         const int b = last_le(give0, a.B, e);
-        const int j = a.shared_blocks + owned(__ldg(a.after + b), a.bs_shift, a.shared_blocks) + (int)(e - give0[b]);
-        a.free_list[ring_at(tail + e, a.n_blocks)] = a.tables[(long long)b * a.table_blocks + j];
+        const int j = a.shared_blocks + owned(__ldg(a.after + b), a.bs_shift, a.shared_blocks) + (e - give0[b]);
+        a.free_list[ring(tail_at, e)] = a.tables[(long long)b * a.table_blocks + j];
     }
     // the shared blocks of requests that start
     if (a.shared_blocks > 0) {
         const long long shared_len = (long long)a.shared_blocks << a.bs_shift;
-        for (long long e = t0; e < (long long)a.B * a.shared_blocks; e += step) {
-            const int b = (int)(e / a.shared_blocks), j = (int)(e - (long long)b * a.shared_blocks);
+        for (int b = blockIdx.x * (kPlanThreads / 32) + w; b < a.B; b += gridDim.x * (kPlanThreads / 32)) {
             const int n0 = __ldg(a.before + b);
-            if (st[b] == 0 && n0 <= shared_len && __ldg(a.after + b) > n0)
+            if (st[b] != 0 || n0 > shared_len || __ldg(a.after + b) <= n0) continue;
+            for (int j = lane; j < a.shared_blocks; j += 32)
                 a.tables[(long long)b * a.table_blocks + j] = __ldg(a.shared_table + j);
         }
     }
-    // rows
-    for (long long t = t0; t < a.max_rows; t += step) {
-        int slot = -1, pos = 0;
-        if (t < rows_all) {
-            const int b = last_le(row0, a.B, t);
-            const int n0 = __ldg(a.before + b);
-            pos = n0 + (int)(t - row0[b]);
-            if (st[b] == 0) {
-                const int j = pos >> a.bs_shift;
-                const int own = a.shared_blocks + owned(n0, a.bs_shift, a.shared_blocks);
-                int id;
-                if (j >= own)
-                    id = a.free_list[ring_at(head + take0[b] + (j - own), a.n_blocks)];
-                else if (j < a.shared_blocks && n0 <= ((long long)a.shared_blocks << a.bs_shift))
-                    id = __ldg(a.shared_table + j);
-                else
-                    id = a.tables[(long long)b * a.table_blocks + j];
-                if (id >= 0 && id < a.n_blocks)
-                    slot = (id << a.bs_shift) + (pos & ((1 << a.bs_shift) - 1));
-                else
-                    atomicOr(a.err, CODEC_LM_ERR_BLOCK);
+    // rows, four in a row per thread
+    for (long long t4 = 4LL * t0; t4 < a.max_rows; t4 += 4LL * step) {
+        int slot[4], pos[4];
+        int b = t4 < rows_all ? last_le(row0, a.B, t4) : a.B;
+        int n0 = 0, r0 = 0, end = 0, own = 0, status = 0;
+        auto request = [&]() {
+            n0 = __ldg(a.before + b);
+            r0 = row0[b];
+            end = b + 1 < a.B ? row0[b + 1] : rows_all;
+            own = a.shared_blocks + owned(n0, a.bs_shift, a.shared_blocks);
+            status = st[b];
+        };
+        if (b < a.B) request();
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+            const int t = (int)t4 + i;
+            slot[i] = -1;
+            pos[i] = 0;
+            if (t >= rows_all) continue;
+            if (t >= end) {
+                b = last_le(row0, a.B, t);
+                request();
             }
+            pos[i] = n0 + (t - r0);
+            if (status != 0) continue;
+            const int j = pos[i] >> a.bs_shift;
+            int id;
+            if (j >= own)
+                id = a.free_list[ring(head_at, take0[b] + (j - own))];
+            else if (j < a.shared_blocks && n0 <= (a.shared_blocks << a.bs_shift))
+                id = __ldg(a.shared_table + j);
+            else
+                id = a.tables[(long long)b * a.table_blocks + j];
+            if (id >= 0 && id < a.n_blocks)
+                slot[i] = (id << a.bs_shift) + (pos[i] & ((1 << a.bs_shift) - 1));
+            else
+                atomicOr(a.err, CODEC_LM_ERR_BLOCK);
         }
-        a.slots[t] = slot;
-        a.positions[t] = pos;
+        if (vec && t4 + 4 <= a.max_rows) {
+            *reinterpret_cast<int4*>(a.slots + t4) = make_int4(slot[0], slot[1], slot[2], slot[3]);
+            *reinterpret_cast<int4*>(a.positions + t4) = make_int4(pos[0], pos[1], pos[2], pos[3]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; i++)
+                if (t4 + i < a.max_rows) {
+                    a.slots[t4 + i] = slot[i];
+                    a.positions[t4 + i] = pos[i];
+                }
+        }
     }
 }
 
@@ -226,7 +236,8 @@ cudaError_t configure_lm_plan()
 cudaError_t launch_lm_plan(const LmPlanArgs& a, cudaStream_t s)
 {
     const int ctas = min(152, (a.max_rows + kPlanRows - 1) / kPlanRows);
-    lm_plan_kernel<<<ctas, kPlanThreads, lm_plan_smem(a.B), s>>>(a);
+    const int vec = ((reinterpret_cast<uintptr_t>(a.slots) | reinterpret_cast<uintptr_t>(a.positions)) & 15) == 0;
+    lm_plan_kernel<<<ctas, kPlanThreads, lm_plan_smem(a.B), s>>>(a, vec);
     return cudaGetLastError();
 }
 

@@ -838,47 +838,57 @@ __global__ void __launch_bounds__(kThreads, 1) lm_prompt_kernel(const __grid_con
             const unsigned long long mine = reinterpret_cast<unsigned long long>(
                 p.part ? static_cast<void*>(p.part + (((long long)blockIdx.z * p.rows + row) * p.sh.hq + h) * D)
                        : static_cast<void*>(static_cast<T*>(p.o) + row * p.os + (long long)h * D));
-            const int step = p.part ? 32 : 64;          // columns in 128 bytes
-#pragma unroll 1
-            for (int q = 0; q < D; q += step) {
-#pragma unroll 1
-                for (int c = 0; c < step; c += 32) {
-                    uint32_t a[32] = {};
-                    if (n > 0) {                        // the same for the warp
-                        tmem_ld32_async(to + q + c, a);
-                        tmem_wait_ld();
-                    }
-                    float f[32];
-#pragma unroll
-                    for (int e = 0; e < 32; e++) f[e] = lim > 0 ? __uint_as_float(a[e]) * inv : 0.f;
-                    if (p.part) {
-#pragma unroll
-                        for (int e = 0; e < 8; e++)
-                            *reinterpret_cast<float4*>(out + lane * 128 + ((e ^ (lane & 7)) << 4)) =
-                                make_float4(f[4 * e], f[4 * e + 1], f[4 * e + 2], f[4 * e + 3]);
-                    } else {
-#pragma unroll
-                        for (int e = 0; e < 4; e++)
-                            *reinterpret_cast<uint4*>(out + lane * 128 + (((c / 8 + e) ^ (lane & 7)) << 4)) =
-                                make_uint4(Two<T>::pack(f[8 * e], f[8 * e + 1]), Two<T>::pack(f[8 * e + 2], f[8 * e + 3]),
-                                           Two<T>::pack(f[8 * e + 4], f[8 * e + 5]),
-                                           Two<T>::pack(f[8 * e + 6], f[8 * e + 7]));
-                    }
-                }
+            auto flush = [&](int byte) {
                 __syncwarp();
-                if (q + step >= D && n > 0) {           // the accumulator is free for the next item
-                    tc_fence_before();
-                    if (lane == 0) mbar_arrive(&s.o_empty[i]);
-                }
+                uint4 v[8];
+                unsigned long long dst[8];
 #pragma unroll
                 for (int e = 0; e < 8; e++) {
-                    const int from = 4 * e + (lane >> 3), chunk = lane & 7;
-                    const unsigned long long dst = __shfl_sync(0xffffffffu, mine, from);
-                    if (rows >> from & 1u)
-                        *reinterpret_cast<uint4*>(dst + (p.part ? q * 4 : q * 2) + chunk * 16) =
-                            *reinterpret_cast<const uint4*>(out + from * 128 + ((chunk ^ (from & 7)) << 4));
+                    const int from = 4 * e + (lane >> 3);
+                    v[e] = *reinterpret_cast<const uint4*>(out + from * 128 + (((lane & 7) ^ (from & 7)) << 4));
+                    dst[e] = __shfl_sync(0xffffffffu, mine, from) + byte + (lane & 7) * 16;
                 }
+#pragma unroll
+                for (int e = 0; e < 8; e++)
+                    if (rows >> (4 * e + (lane >> 3)) & 1u) *reinterpret_cast<uint4*>(dst[e]) = v[e];
                 __syncwarp();
+            };
+#pragma unroll 1
+            for (int q = 0; q < D; q += 64) {
+                uint32_t a[64] = {};
+                if (n > 0) {                            // the same for the warp
+                    tmem_ld32_async(to + q, a);
+                    tmem_ld32_async(to + q + 32, a + 32);
+                    tmem_wait_ld();
+                    if (q + 64 == D) {                  // the accumulator is free for the next item
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&s.o_empty[i]);
+                    }
+                }
+                float f[64];
+#pragma unroll
+                for (int e = 0; e < 64; e++) f[e] = lim > 0 ? __uint_as_float(a[e]) * inv : 0.f;
+                auto put = [&](int chunk, uint4 v) {
+                    *reinterpret_cast<uint4*>(out + lane * 128 + ((chunk ^ (lane & 7)) << 4)) = v;
+                };
+                if (p.part) {
+#pragma unroll
+                    for (int c = 0; c < 64; c += 32) {
+#pragma unroll
+                        for (int e = 0; e < 8; e++)
+                            put(e, make_uint4(__float_as_uint(f[c + 4 * e]), __float_as_uint(f[c + 4 * e + 1]),
+                                              __float_as_uint(f[c + 4 * e + 2]), __float_as_uint(f[c + 4 * e + 3])));
+                        flush((q + c) * 4);
+                    }
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 8; e++)
+                        put(e, make_uint4(Two<T>::pack(f[8 * e], f[8 * e + 1]), Two<T>::pack(f[8 * e + 2], f[8 * e + 3]),
+                                          Two<T>::pack(f[8 * e + 4], f[8 * e + 5]),
+                                          Two<T>::pack(f[8 * e + 6], f[8 * e + 7])));
+                    flush(q * 2);
+                }
             }
             if (fix) {
                 // a finite sum plus what is not finite is the latter

@@ -189,9 +189,26 @@ __device__ __forceinline__ void join_parts(const Params& p, int b, int h, int n_
         return i < p.n_pre ? (long long)i * p.B * p.sh.hq + shared_row : (long long)(i - p.n_pre) * p.sh.hq + own_row;
     };
     auto lse_of = [&](int i) { return __ldcg((i < p.n_pre ? p.pre_lse : p.part_lse) + row_of(i)); };
+    constexpr int kE = D / 32;
+    auto part_of = [&](int i, float* x) {
+        const float* src = (i < p.n_pre ? p.pre : p.part) + row_of(i) * D;
+        if constexpr (kE == 4) {
+            const float4 y = __ldcg(reinterpret_cast<const float4*>(src) + lane);
+            x[0] = y.x; x[1] = y.y; x[2] = y.z; x[3] = y.w;
+        } else {
+            const float2 y = __ldcg(reinterpret_cast<const float2*>(src) + lane);
+            x[0] = y.x; x[1] = y.y;
+        }
+    };
+    // the first parts are on their way while the weights are worked out
+    constexpr int kAhead = 4;
+    const float mine = lane < parts ? lse_of(lane) : -INFINITY;
+    float ahead[kAhead][kE];
+#pragma unroll
+    for (int i = 0; i < kAhead; i++)
+        if (i < parts) part_of(i, ahead[i]);
     float m = -INFINITY;
     bool nan = false;
-    const float mine = lane < parts ? lse_of(lane) : -INFINITY;
     for (int i = lane; i < parts; i += 32) {
         const float x = i < 32 ? mine : lse_of(i);
         m = fmaxf(m, x);
@@ -201,28 +218,26 @@ __device__ __forceinline__ void join_parts(const Params& p, int b, int h, int n_
     for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
     if (__any_sync(0xffffffffu, nan)) m = NAN;
     const float ref = m == -INFINITY ? 0.f : m;
-    constexpr int kE = D / 32;
     float v[kE] = {}, sum = 0.f;
+    float w = lane < parts ? expf(mine - ref) : 0.f;
+    auto add = [&](float f, const float* x) {
+        sum += f;
+#pragma unroll
+        for (int e = 0; e < kE; e++) v[e] = f != 0.f ? fmaf(f, x[e], v[e]) : v[e];  // a part without keys has no value
+    };
+#pragma unroll
+    for (int i = 0; i < kAhead; i++) {
+        const float f = __shfl_sync(0xffffffffu, w, i);
+        if (i < parts) add(f, ahead[i]);
+    }
     for (int i0 = 0; i0 < parts; i0 += 32) {
-        float w = 0.f;
-        if (i0 + lane < parts) w = expf((i0 == 0 ? mine : lse_of(i0 + lane)) - ref);
+        if (i0 > 0) w = i0 + lane < parts ? expf(lse_of(i0 + lane) - ref) : 0.f;
         const int cnt = min(32, parts - i0);
 #pragma unroll 8
-        for (int i = 0; i < cnt; i++) {
-            const float f = __shfl_sync(0xffffffffu, w, i);
-            const float* src = (i0 + i < p.n_pre ? p.pre : p.part) + row_of(i0 + i) * D;
+        for (int i = i0 == 0 ? kAhead : 0; i < cnt; i++) {
             float x[kE];
-            if constexpr (kE == 4) {
-                const float4 y = __ldcg(reinterpret_cast<const float4*>(src) + lane);
-                x[0] = y.x; x[1] = y.y; x[2] = y.z; x[3] = y.w;
-            } else {
-                const float2 y = __ldcg(reinterpret_cast<const float2*>(src) + lane);
-                x[0] = y.x; x[1] = y.y;
-            }
-            sum += f;
-#pragma unroll
-            for (int e = 0; e < kE; e++)
-                v[e] = f != 0.f ? fmaf(f, x[e], v[e]) : v[e];   // a part without keys has no value
+            part_of(i0 + i, x);
+            add(__shfl_sync(0xffffffffu, w, i), x);
         }
     }
     const float inv = empty ? 0.f : 1.f / sum;
@@ -241,13 +256,15 @@ __device__ __forceinline__ int splits_of(const Params& p, int len)
 }
 
 // A warp per (request, head) whose result is in parts.
+constexpr int kJoinThreads = 256;
+
 template <typename T, int D>
-__global__ void __launch_bounds__(128) lm_join_kernel(const __grid_constant__ Params p)
+__global__ void __launch_bounds__(kJoinThreads, 6) lm_join_kernel(const __grid_constant__ Params p)
 {
     pdl_wait();
     pdl_launch();
     if (blockIdx.x == 0 && threadIdx.x == 0 && p.taken) *p.taken = 0;
-    const long long w = blockIdx.x * 4LL + (threadIdx.x >> 5);
+    const long long w = blockIdx.x * (kJoinThreads / 32LL) + (threadIdx.x >> 5);
     const int b = (int)(w / p.sh.hq), h = (int)(w - (long long)b * p.sh.hq);
     if (b >= p.B) return;
     int len = __ldg(p.kv_len + b);
@@ -258,7 +275,7 @@ __global__ void __launch_bounds__(128) lm_join_kernel(const __grid_constant__ Pa
 }
 
 template <typename T, int D>
-__global__ void __launch_bounds__(kThreads) lm_step_kernel(const __grid_constant__ CUtensorMap mk,
+__global__ void __launch_bounds__(kThreads, 2) lm_step_kernel(const __grid_constant__ CUtensorMap mk,
                                                            const __grid_constant__ CUtensorMap mv,
                                                            const __grid_constant__ Params p)
 {
@@ -290,6 +307,8 @@ __global__ void __launch_bounds__(kThreads) lm_step_kernel(const __grid_constant
     // reads was complete when that one passed its own wait (and is read from L2)
     if (!p.after_shared) pdl_wait();
     pdl_launch();
+    int unit0 = blockIdx.x;                 // of the copy warp's lane 0
+    if (p.taken && warp == kConsumers && lane == 0) unit0 = atomicAdd(p.taken, 1);
     // units before each request: at least one per request, so that something writes its row
     if (warp == 0) {
         int before = 0;
@@ -328,10 +347,10 @@ __global__ void __launch_bounds__(kThreads) lm_step_kernel(const __grid_constant
         }
         const int box_shift = min(p.bs_shift, 6);           // keys per box: a block, or half of one of 128
         const int per = kKeys >> box_shift;
-        int u = blockIdx.x;
+        int u = __shfl_sync(0xffffffffu, unit0, 0);
         while (ok) {
             int next = u + gridDim.x;
-            if (p.taken && lane == 0) next = atomicAdd(p.taken, 1) + gridDim.x;     // needed when this unit's copies are out
+            if (p.taken && lane == 0 && u < units) next = atomicAdd(p.taken, 1);    // needed when this unit's copies are out
             if (u >= units) u = -1;
             Unit n{};
             if (u >= 0) n = unit_at(p, first, lens, u);
@@ -603,7 +622,7 @@ cudaError_t launch(const LmShape& sh, const LmStepArgs& a, cudaStream_t s)
     if (p.shared_len > 0) {
         LmSharedArgs c{a.q, a.qs, a.B, ks, a.shared_table, p.shared_len, 0, a.ws.pre, a.ws.pre_lse};
         // splits by the object's shape and the shared length alone
-        const int n = std::max(1, std::min(a.ws.pre_max, p.shared_len / 128));
+        const int n = std::max(1, std::min(a.ws.pre_max, p.shared_len / 256));
         c.split_len = ((p.shared_len + n - 1) / n + 127) & ~127;
         p.n_pre = (p.shared_len + c.split_len - 1) / c.split_len;
         const cudaError_t e = launch_lm_shared(sh, c, s);
@@ -636,7 +655,8 @@ cudaError_t launch(const LmShape& sh, const LmStepArgs& a, cudaStream_t s)
     const cudaError_t e = launch_pdl(lm_step_kernel<T, D>, dim3(ctas), dim3(kThreads), smem_bytes<D>(p.stages, sh.group, a.B), s, mk,
                                      mv, p);
     if (e != cudaSuccess || !two) return e;
-    return launch_pdl(lm_join_kernel<T, D>, dim3((unsigned)(((long long)a.B * sh.hq + 3) / 4)), dim3(128), 0, s, p);
+    return launch_pdl(lm_join_kernel<T, D>, dim3((unsigned)(((long long)a.B * sh.hq + kJoinThreads / 32 - 1) / (kJoinThreads / 32))),
+                      dim3(kJoinThreads), 0, s, p);
 }
 
 }  // namespace
