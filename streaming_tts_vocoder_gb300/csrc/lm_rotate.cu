@@ -10,15 +10,19 @@
 // Bound by memory: every value is read and written once.  A head is the work
 // of D / 16 lanes; each holds 8 elements of the first half and the 8 elements
 // D / 2 further, so that both rotation forms stay inside a lane, every access
-// is 16 bytes, and the norm is 2 or 3 shuffles.  A row's cosines and sines are
-// read once per warp and kept in registers over its heads.
+// is 16 bytes, and the norm is 2 or 3 shuffles.  A warp takes a row (or a part
+// of its heads, when there are few rows): cosines, sines and a gain stay in
+// registers over its heads, and kUnroll groups of heads are loaded (and kept
+// as they lie in memory) before the first is worked on.  32,768 rows of 48
+// heads of 128: 127 us, 6.35 TB/s; with two groups ahead 153, with eight 202,
+// at three CTAs of 256 threads 129, at eight of 128 (registers spilled) 169.
 #include "lm.h"
 
 namespace codec {
 
 namespace {
 
-constexpr int kRotThreads = 256;
+constexpr int kRotThreads = 128;
 
 template <typename T> struct Pack;      // 8 values of 16 bits
 template <> struct Pack<__nv_bfloat16> {
@@ -44,24 +48,35 @@ template <> struct Pack<__half> {
     }
 };
 
-template <typename T>
-__device__ __forceinline__ void load8(const T* p, float* x)
-{
-    const uint4 w = *reinterpret_cast<const uint4*>(p);   // q may be q_out: not the read-only path
-    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+// Eight values as they lie in memory (a projection's output may be q_out
+// itself, so not by the read-only path), and in fp32.
+template <typename T> struct Raw {
+    uint4 w;
+    __device__ __forceinline__ void load(const T* p) { w = *reinterpret_cast<const uint4*>(p); }
+    __device__ __forceinline__ void get(float* x) const
+    {
+        const uint32_t u[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-    for (int i = 0; i < 4; i++) {
-        const float2 f = Pack<T>::un(u[i]);
-        x[2 * i] = f.x;
-        x[2 * i + 1] = f.y;
+        for (int i = 0; i < 4; i++) {
+            const float2 f = Pack<T>::un(u[i]);
+            x[2 * i] = f.x;
+            x[2 * i + 1] = f.y;
+        }
     }
-}
-__device__ __forceinline__ void load8(const float* p, float* x)
-{
-    const float4 a = *reinterpret_cast<const float4*>(p), b = *(reinterpret_cast<const float4*>(p) + 1);
-    x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
-    x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
-}
+};
+template <> struct Raw<float> {
+    float4 a, b;
+    __device__ __forceinline__ void load(const float* p)
+    {
+        a = *reinterpret_cast<const float4*>(p);
+        b = *(reinterpret_cast<const float4*>(p) + 1);
+    }
+    __device__ __forceinline__ void get(float* x) const
+    {
+        x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
+        x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
+    }
+};
 
 template <typename T>
 __device__ __forceinline__ void store8(T* p, const float* x)
@@ -70,16 +85,87 @@ __device__ __forceinline__ void store8(T* p, const float* x)
                                               Pack<T>::two(x[4], x[5]), Pack<T>::two(x[6], x[7]));
 }
 
+// Heads first, first + kGroups step, .. of a row: norm (gain not null) and
+// rotation (turn).  src, dst: the row's heads back to back.
+template <typename T, typename TI, int D, bool kTurn>
+__device__ __forceinline__ void heads_of(const TI* src, T* dst, int heads, int part, int parts, const float* gain,
+                                         float eps, int pairs, const float* cs, const float* sn)
+{
+    constexpr int kLanes = D / 16, kGroups = 32 / kLanes, kUnroll = sizeof(TI) == 4 ? 2 : 4;
+    const int lane = threadIdx.x & 31, g = lane / kLanes, c = (lane % kLanes) * 8;
+    float gx[8], gy[8];
+    if (kTurn && gain) {
+        Raw<float> r;
+        r.load(gain + c);
+        r.get(gx);
+        r.load(gain + D / 2 + c);
+        r.get(gy);
+    }
+    for (int h0 = part * kGroups + g; h0 - g < heads; h0 += parts * kGroups * kUnroll) {
+        Raw<TI> rx[kUnroll], ry[kUnroll];
+#pragma unroll
+        for (int u = 0; u < kUnroll; u++) {
+            const int h = h0 + u * parts * kGroups;
+            const TI* at = src + (long long)min(h, heads - 1) * D + c;
+            rx[u].load(at);
+            ry[u].load(at + D / 2);
+        }
+#pragma unroll
+        for (int u = 0; u < kUnroll; u++) {
+            const int h = h0 + u * parts * kGroups;
+            if (u > 0 && h - g >= heads) break;
+            float x[8], y[8];
+            rx[u].get(x);
+            ry[u].get(y);
+            if (kTurn && gain) {
+                float ss = 0.f;
+#pragma unroll
+                for (int i = 0; i < 8; i++) ss = fmaf(x[i], x[i], fmaf(y[i], y[i], ss));
+#pragma unroll
+                for (int o = kLanes / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+                const float r = 1.f / sqrtf(ss * (1.f / D) + eps);
+#pragma unroll
+                for (int i = 0; i < 8; i++) {
+                    x[i] = x[i] * r * gx[i];
+                    y[i] = y[i] * r * gy[i];
+                }
+            }
+            if (kTurn && pairs) {
+#pragma unroll
+                for (int i = 0; i < 4; i++) {
+                    const float p = x[2 * i], q = x[2 * i + 1], v = y[2 * i], w = y[2 * i + 1];
+                    x[2 * i] = p * cs[i] - q * sn[i];
+                    x[2 * i + 1] = q * cs[i] + p * sn[i];
+                    y[2 * i] = v * cs[4 + i] - w * sn[4 + i];
+                    y[2 * i + 1] = w * cs[4 + i] + v * sn[4 + i];
+                }
+            } else if (kTurn) {
+#pragma unroll
+                for (int i = 0; i < 8; i++) {
+                    const float p = x[i], q = y[i];
+                    x[i] = p * cs[i] - q * sn[i];
+                    y[i] = q * cs[i] + p * sn[i];
+                }
+            }
+            if (h < heads) {
+                store8(dst + (long long)h * D + c, x);
+                store8(dst + (long long)h * D + D / 2 + c, y);
+            }
+        }
+    }
+}
+
 // Warp w of the grid: row w / parts, and every parts-th group of heads of it.
 template <typename T, typename TI, int D>
-__global__ void __launch_bounds__(kRotThreads) lm_rotate_kernel(const LmRotateArgs a, int hq, int hk, int parts,
+__global__ void __launch_bounds__(kRotThreads, 5) lm_rotate_kernel(const LmRotateArgs a, int hq, int hk, int parts,
                                                                 unsigned* err)
 {
-    constexpr int kLanes = D / 16, kGroups = 32 / kLanes;
+    constexpr int kLanes = D / 16;
     const int warp = (int)((blockIdx.x * (long long)kRotThreads + threadIdx.x) >> 5);
-    const int row = warp / parts, part = warp - row * parts;
+    const int row = parts == 1 ? warp : warp / parts, part = warp - row * parts;
     if (row >= a.rows) return;
-    const int lane = threadIdx.x & 31, g = lane / kLanes, c = (lane % kLanes) * 8;
+    const int lane = threadIdx.x & 31, c = (lane % kLanes) * 8;
+    const int pos = __ldg(a.positions + row);
     long long slot = row;
     if (a.slots) {
         slot = __ldg(a.slots + row);
@@ -89,7 +175,6 @@ __global__ void __launch_bounds__(kRotThreads) lm_rotate_kernel(const LmRotateAr
             return;
         }
     }
-    const int pos = __ldg(a.positions + row);
     if (pos < 0 || pos >= a.max_positions) {
         if (lane == 0) atomicOr(err, CODEC_LM_ERR_POSITION);
         return;
@@ -97,83 +182,23 @@ __global__ void __launch_bounds__(kRotThreads) lm_rotate_kernel(const LmRotateAr
     // cos, sin of this lane's eight rotations: pair index c + i (halves), or
     // c / 2 + i and D / 4 + c / 2 + i (pairs)
     float cs[8], sn[8];
-    {
-        const float2* t = a.turn + (long long)pos * (D / 2);
+    const float2* t = a.turn + (long long)pos * (D / 2);
 #pragma unroll
-        for (int i = 0; i < 8; i += 2) {
-            const int at = a.pairs ? (i < 4 ? c / 2 + i : D / 4 + c / 2 + i - 4) : c + i;
-            const float4 v = __ldg(reinterpret_cast<const float4*>(t + at));
-            cs[i] = v.x; sn[i] = v.y;
-            cs[i + 1] = v.z; sn[i + 1] = v.w;
-        }
+    for (int i = 0; i < 8; i += 2) {
+        const int at = a.pairs ? (i < 4 ? c / 2 + i : D / 4 + c / 2 + i - 4) : c + i;
+        const float4 v = __ldg(reinterpret_cast<const float4*>(t + at));
+        cs[i] = v.x;
+        sn[i] = v.y;
+        cs[i + 1] = v.z;
+        sn[i + 1] = v.w;
     }
-    const int heads = hq + hk + (a.v ? hk : 0);
-    for (int h0 = part * kGroups; h0 < heads; h0 += parts * kGroups) {
-        const int h = h0 + g;
-        const bool live = h < heads;
-        const bool is_q = h < hq, is_v = h >= hq + hk;
-        const TI* src = nullptr;
-        T* dst = nullptr;
-        if (live) {
-            if (is_q) {
-                src = static_cast<const TI*>(a.q) + row * a.qs + (long long)h * D;
-                dst = static_cast<T*>(a.q_out) + ((long long)row * hq + h) * D;
-            } else if (!is_v) {
-                src = static_cast<const TI*>(a.k) + row * a.ks + (long long)(h - hq) * D;
-                dst = static_cast<T*>(a.k_dst) + (slot * hk + (h - hq)) * D;
-            } else {
-                src = static_cast<const TI*>(a.v) + row * a.vs + (long long)(h - hq - hk) * D;
-                dst = static_cast<T*>(a.v_dst) + (slot * hk + (h - hq - hk)) * D;
-            }
-        }
-        float x[8] = {}, y[8] = {};
-        if (live) {
-            load8(src + c, x);
-            load8(src + D / 2 + c, y);
-        }
-        if (a.q_gain) {
-            float ss = 0.f;
-#pragma unroll
-            for (int i = 0; i < 8; i++) ss = fmaf(x[i], x[i], fmaf(y[i], y[i], ss));
-#pragma unroll
-            for (int o = kLanes / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-            if (!is_v) {
-                const float r = 1.f / sqrtf(ss * (1.f / D) + a.eps);
-                const float* gain = is_q ? a.q_gain : a.k_gain;
-                float gx[8], gy[8];
-                load8(gain + c, gx);
-                load8(gain + D / 2 + c, gy);
-#pragma unroll
-                for (int i = 0; i < 8; i++) {
-                    x[i] = x[i] * r * gx[i];
-                    y[i] = y[i] * r * gy[i];
-                }
-            }
-        }
-        if (!is_v) {
-            if (a.pairs) {
-#pragma unroll
-                for (int i = 0; i < 4; i++) {
-                    const float p = x[2 * i], q = x[2 * i + 1], u = y[2 * i], w = y[2 * i + 1];
-                    x[2 * i] = p * cs[i] - q * sn[i];
-                    x[2 * i + 1] = q * cs[i] + p * sn[i];
-                    y[2 * i] = u * cs[4 + i] - w * sn[4 + i];
-                    y[2 * i + 1] = w * cs[4 + i] + u * sn[4 + i];
-                }
-            } else {
-#pragma unroll
-                for (int i = 0; i < 8; i++) {
-                    const float p = x[i], q = y[i];
-                    x[i] = p * cs[i] - q * sn[i];
-                    y[i] = q * cs[i] + p * sn[i];
-                }
-            }
-        }
-        if (live) {
-            store8(dst + c, x);
-            store8(dst + D / 2 + c, y);
-        }
-    }
+    heads_of<T, TI, D, true>(static_cast<const TI*>(a.q) + row * a.qs, static_cast<T*>(a.q_out) + (long long)row * hq * D,
+                             hq, part, parts, a.q_gain, a.eps, a.pairs, cs, sn);
+    heads_of<T, TI, D, true>(static_cast<const TI*>(a.k) + row * a.ks, static_cast<T*>(a.k_dst) + slot * hk * D, hk,
+                             part, parts, a.k_gain, a.eps, a.pairs, cs, sn);
+    if (a.v)
+        heads_of<T, TI, D, false>(static_cast<const TI*>(a.v) + row * a.vs, static_cast<T*>(a.v_dst) + slot * hk * D,
+                                  hk, part, parts, nullptr, 0.f, 0, cs, sn);
 }
 
 // The angle p theta^(-2 i / D) and its cosine and sine in fp64, rounded once.
@@ -191,9 +216,8 @@ template <typename T, typename TI, int D>
 cudaError_t launch(const LmShape& sh, const LmRotateArgs& a, cudaStream_t s)
 {
     constexpr int kGroups = 32 / (D / 16);
-    const int heads = sh.hq + sh.hk + (a.v ? sh.hk : 0);
     // few rows: spread a row's heads over warps until there are about 16 warps per SM
-    const int most = (heads + kGroups - 1) / kGroups;
+    const int most = (sh.hq + kGroups - 1) / kGroups;
     int parts = 1;
     while (parts < most && (long long)a.rows * parts < 152 * 16) parts++;
     const long long warps = (long long)a.rows * parts;
