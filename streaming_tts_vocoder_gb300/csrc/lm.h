@@ -67,6 +67,15 @@ struct LmRotateArgs {
 cudaError_t launch_lm_rotate(const LmShape& sh, const LmRotateArgs& a, int in_type, cudaStream_t s);
 cudaError_t launch_lm_turn_table(float2* turn, int max_positions, int D, double theta, cudaStream_t s);
 
+// Workspace of prompt attention.
+constexpr int kLmSlots = 256;       // pieces of items that are cut, with their K/V heads
+struct LmPromptSpace {
+    void* list;                     // [items + kLmSlots] x 32 bytes
+    int* counts;                    // [3]
+    void* joins;                    // [kLmSlots] x 16 bytes
+    float *piece, *piece_lse;       // [kLmSlots][256][D], [kLmSlots][256]
+};
+
 struct LmPromptArgs {
     const void* q;
     long long qs;
@@ -77,11 +86,10 @@ struct LmPromptArgs {
     void* o;
     long long os;
     float* lse;
-    void* list;                     // workspace: lm_list_items() x 16 bytes, their number and how many are taken
-    int* list_n;                    // [2]
+    LmPromptSpace ws;
 };
 // Pairs of query tiles that `rows` rows of at most B requests can make.
-inline long long lm_list_items(int rows, int B, int group)
+__host__ __device__ inline long long lm_list_items(int rows, int B, int group)
 {
     return rows / (2 * (128 / group)) + (rows < B ? rows : B);
 }

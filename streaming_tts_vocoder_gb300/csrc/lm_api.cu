@@ -15,8 +15,7 @@ struct codec_lm_s {
     float2* turn = nullptr;
     unsigned* err = nullptr;
     LmStepSpace step{};
-    void* list = nullptr;           // prompt attention's items
-    int* list_n = nullptr;          // their number, and how many are taken
+    LmPromptSpace prompt{};
 };
 
 namespace {
@@ -46,8 +45,11 @@ void lm_free(codec_lm_s* lm)
     cudaFree(lm->step.pre);
     cudaFree(lm->step.pre_lse);
     cudaFree(lm->step.done);
-    cudaFree(lm->list);
-    cudaFree(lm->list_n);
+    cudaFree(lm->prompt.list);
+    cudaFree(lm->prompt.counts);
+    cudaFree(lm->prompt.joins);
+    cudaFree(lm->prompt.piece);
+    cudaFree(lm->prompt.piece_lse);
     delete lm;
 }
 
@@ -110,6 +112,8 @@ codec_status codec_lm_create(const codec_lm_config* cfg, codec_lm_t** out)
     const int tokens = 2 * (128 / (c.q_heads / c.kv_heads));
     const int64_t pairs = (c.max_requests + tokens - 1) / tokens;
     sp.pre_max = (int)std::max<int64_t>(1, std::min<int64_t>({32, 64 / (pairs * c.kv_heads), positions / 256}));
+    LmPromptSpace& pr = lm->prompt;
+    const size_t items = (size_t)lm_list_items(c.max_rows, c.max_requests, c.q_heads / c.kv_heads) + kLmSlots;
     const size_t row = (size_t)c.max_requests * c.q_heads;
     if (cudaMalloc(&lm->turn, sizeof(float2) * (size_t)c.max_positions * (c.head_dim / 2)) != cudaSuccess ||
         cudaMalloc(&lm->err, sizeof(unsigned)) != cudaSuccess ||
@@ -117,9 +121,10 @@ codec_status codec_lm_create(const codec_lm_config* cfg, codec_lm_t** out)
         cudaMalloc(&sp.part_lse, sizeof(float) * row * sp.max_splits) != cudaSuccess ||
         cudaMalloc(&sp.pre, sizeof(float) * row * sp.pre_max * c.head_dim) != cudaSuccess ||
         cudaMalloc(&sp.pre_lse, sizeof(float) * row * sp.pre_max) != cudaSuccess ||
-        cudaMalloc(&lm->list, 16 * (size_t)(lm_list_items(c.max_rows, c.max_requests, c.q_heads / c.kv_heads) + 1)) !=
-            cudaSuccess ||
-        cudaMalloc(&lm->list_n, 2 * sizeof(int)) != cudaSuccess ||
+        cudaMalloc(&pr.list, 32 * items) != cudaSuccess || cudaMalloc(&pr.counts, 3 * sizeof(int)) != cudaSuccess ||
+        cudaMalloc(&pr.joins, 16 * kLmSlots) != cudaSuccess ||
+        cudaMalloc(&pr.piece, sizeof(float) * kLmSlots * 256 * c.head_dim) != cudaSuccess ||
+        cudaMalloc(&pr.piece_lse, sizeof(float) * kLmSlots * 256) != cudaSuccess ||
         cudaMalloc(&sp.done, sizeof(int) * ((size_t)c.max_requests * c.kv_heads + 1)) != cudaSuccess) {
         cudaGetLastError();
         lm_free(lm);
@@ -223,7 +228,7 @@ codec_status codec_lm_prompt(codec_lm_t* lm, const void* q, int64_t q_stride, co
     OnDevice on(lm->device);
     if (!on.ok) return CODEC_ERR_CUDA;
     LmPromptArgs a{q, q_stride, rows, row_start, B, LmKeys{k, v, k_stride, v_stride}, o, o_stride, lse,
-                   lm->list, lm->list_n};
+                   lm->prompt};
     return done(launch_lm_prompt(lm->shape, a, static_cast<cudaStream_t>(stream)));
 }
 
@@ -243,7 +248,7 @@ codec_status codec_lm_prompt_paged(codec_lm_t* lm, const void* q, int64_t q_stri
     OnDevice on(lm->device);
     if (!on.ok) return CODEC_ERR_CUDA;
     LmPromptArgs a{q, q_stride, rows, row_start, B, paged(lm, k_cache, v_cache, tables, kv_len), o, o_stride, lse,
-                   lm->list, lm->list_n};
+                   lm->prompt};
     return done(launch_lm_prompt(lm->shape, a, static_cast<cudaStream_t>(stream)));
 }
 

@@ -21,7 +21,10 @@
 // Work: an item is a pair of query tiles of one request and K/V head.  Few
 // items: one CTA each.  More than there are SMs: one CTA per SM walks a list
 // of them, longest first, that a small kernel makes from the lengths; copies
-// and MMAs of the next item then run while the last one is written.
+// and MMAs of the next item then run while the last one is written.  Where the
+// longest items would keep a few SMs busy long after the others, they are cut
+// along the keys: the pieces leave partial results in fp32, which a third
+// kernel joins in order.
 //
 // Roles (384 threads, one CTA per SM):
 //   warp 0      takes the items from a counter; copies: Q, then K and V tiles through a ring of stages; paged
@@ -43,6 +46,7 @@
 #include <mutex>
 
 #include "lm.h"
+#include "lm_join.cuh"
 #include "tc_ptx.cuh"
 
 namespace codec {
@@ -69,9 +73,12 @@ struct Params {
     int tokens;                 // tokens per query tile: 128 / group
     const void* v;              // values, for what is not finite
     long long v_stride;
-    const int4* list;           // items (request, first query row, tokens, keys of the first token); null: by blockIdx
-    const int* list_n;
-    int* taken;                 // items taken from the list
+    const int4* list;           // items, two each (see Entry); null: by blockIdx
+    int* counts;                // items of the list, items taken from it, items to join
+    int4* joins;                // of each: first query row, tokens, first slot, pieces
+    int split;                  // items may be cut along the keys
+    float* piece;               // pieces' results: [slot][2 x 128 rows][D], normalised, fp32
+    float* piece_lse;
     float c;                    // scale x log2 e
     uint32_t idesc_s, idesc_o;
     void* o;
@@ -81,13 +88,21 @@ struct Params {
     float* part_lse;            // [split][rows][hq]
 };
 
-// A pair of query tiles.
+// An item as the list holds it.
+struct Entry {
+    int4 rows;                  // request, first query row, tokens, keys of the first token
+    int4 keys;                  // first K/V tile, tiles, first slot of the piece (of K/V head 0; -1: whole)
+};
+
+// A pair of query tiles, or a piece of one along the keys.
 struct Item {
     int b, hk;                  // request, K/V head
     int q0;                     // first query row
     int ntok;                   // tokens of the two tiles that exist
     int first;                  // prompts: keys of the first token, each later one sees one more (may be < 1)
     int key0;                   // packed: row of key 0; else key 0's position
+    int cap;                    // keys of the piece at most
+    int slot;                   // where a piece's result goes; -1: the item is whole
     int end;                    // keys at or behind it: seen by no row
     int free_from;              // keys below it: seen by every row that sees any
     int n[2];                   // K/V tiles of each query tile
@@ -217,7 +232,7 @@ struct Shared {
     uint64_t raw[kMaxStages], clean[kMaxStages];    // V tiles that are cleaned before use: landed, cleaned
     uint64_t q_full[2], q_empty[2], s_full[2], p_full[2][2], o_full[2], o_empty[2];
     uint64_t work_full[kWork], work_empty[kWork];
-    int4 work[kWork];
+    Entry work[kWork];
     int work_hk[kWork];         // K/V head; -1: no more
     uint32_t tmem;
     int abort;
@@ -288,20 +303,24 @@ __device__ void find_item(const Params& p, Shared& s)
 // Keys that token t of an item sees, from key0 on.
 __device__ __forceinline__ int keys_of(const Params& p, const Item& it, int t)
 {
-    if (p.row_start) return max(0, it.first + t);
+    if (p.row_start) return min(it.cap, max(0, it.first + t));
     int n = __ldg(p.kv_len + it.q0 + t);
     lm_clamp_len(n, (long long)p.table_blocks << p.bs_shift);
     return min(max(min(n, p.shared_len) - it.key0, 0), p.split_len);
 }
 
 // What follows from a prompt item's rows and its first token's keys.
-__device__ __forceinline__ void derive(const Params& p, Item& it)
+__device__ __forceinline__ void derive(const Params& p, Item& it, int4 keys)
 {
-    const int most0 = max(0, it.first + min(it.ntok, p.tokens) - 1);
-    const int most1 = it.ntok > p.tokens ? max(0, it.first + it.ntok - 1) : 0;
-    it.key0 = p.tables ? 0 : it.q0 - (it.first - 1);
+    const int skip = keys.x * kTile;
+    it.key0 = (p.tables ? 0 : it.q0 - (it.first - 1)) + skip;
+    it.first -= skip;
+    it.cap = keys.y < kNone / kTile ? keys.y * kTile : kNone;
+    it.slot = keys.z < 0 ? -1 : keys.z + it.hk;
+    const int most0 = min(it.cap, max(0, it.first + min(it.ntok, p.tokens) - 1));
+    const int most1 = it.ntok > p.tokens ? min(it.cap, max(0, it.first + it.ntok - 1)) : 0;
     it.end = max(most0, most1);
-    it.free_from = it.end > 0 ? max(1, it.first) : kNone;
+    it.free_from = it.end > 0 ? min(it.cap, max(1, it.first)) : kNone;
     it.n[0] = (most0 + kTile - 1) / kTile;
     it.n[1] = (most1 + kTile - 1) / kTile;
 }
@@ -311,19 +330,19 @@ __device__ __forceinline__ void derive(const Params& p, Item& it)
 struct Walk {
     int k = 0;                  // items so far
 
-    __device__ __forceinline__ bool set(const Params& p, Item& it, int4 e, int hk)
+    __device__ __forceinline__ bool set(const Params& p, Item& it, const Entry& e, int hk)
     {
         if (hk < 0) return false;
         it.hk = hk;
-        it.b = e.x;
-        it.q0 = e.y;
-        it.ntok = e.z;
-        it.first = e.w;
-        derive(p, it);
+        it.b = e.rows.x;
+        it.q0 = e.rows.y;
+        it.ntok = e.rows.z;
+        it.first = e.rows.w;
+        derive(p, it, e.keys);
         return true;
     }
     // The copy warp hands out (e, hk).
-    __device__ __forceinline__ bool hand_out(const Params& p, Shared& s, int4 e, int hk, Item& it, int lane)
+    __device__ __forceinline__ bool hand_out(const Params& p, Shared& s, const Entry& e, int hk, Item& it, int lane)
     {
         if (!p.list) {
             if (k++ || !s.found) return false;
@@ -353,7 +372,7 @@ struct Walk {
         const bool ok = mbar_wait(&s.work_full[slot], (uint32_t)(k / kWork & 1), &s.abort, kPolls);
         k++;
         if (!ok) return false;
-        const int4 e = s.work[slot];
+        const Entry e = s.work[slot];
         const int hk = s.work_hk[slot];
         if (arrives) mbar_arrive(&s.work_empty[slot]);
         return set(p, it, e, hk);
@@ -447,7 +466,7 @@ __global__ void __launch_bounds__(kThreads, 1) lm_prompt_kernel(const __grid_con
             find_item(p, s);
             if (tid == 0 && s.found) {
                 s.item.hk = blockIdx.y;
-                derive(p, s.item);
+                derive(p, s.item, make_int4(0, kNone, -1, 0));
             }
         } else if (warp == 0) {
             // a shared part: the largest and the smallest number of keys but none
@@ -458,6 +477,8 @@ __global__ void __launch_bounds__(kThreads, 1) lm_prompt_kernel(const __grid_con
             it.ntok = min(2 * p.tokens, p.rows - it.q0);
             it.key0 = blockIdx.z * p.split_len;
             it.first = 0;
+            it.cap = kNone;
+            it.slot = -1;
             int most[2] = {0, 0}, least = kNone;
             for (int t = lane; t < it.ntok; t += 32) {
                 const int n = keys_of(p, it, t);
@@ -495,14 +516,15 @@ __global__ void __launch_bounds__(kThreads, 1) lm_prompt_kernel(const __grid_con
             const int per = kTile >> p.bs_shift;        // cache blocks per tile
             const int g = p.sh.group;
             bool ok = true;
-            int4 entry = make_int4(0, 0, 0, 0);
+            Entry entry{};
             int entry_hk = -1;
-            const int count = p.list ? __ldg(p.list_n) * p.sh.hk : 0;
+            const int count = p.list ? __ldcg(p.counts) * p.sh.hk : 0;
             auto fetch = [&](int w) {
                 entry_hk = -1;
                 if (w < count) {
                     entry_hk = w % p.sh.hk;
-                    entry = __ldg(p.list + w / p.sh.hk);
+                    entry.rows = __ldg(p.list + 2 * (w / p.sh.hk));
+                    entry.keys = __ldg(p.list + 2 * (w / p.sh.hk) + 1);
                 }
             };
             if (p.list) fetch(blockIdx.x);
@@ -510,7 +532,7 @@ __global__ void __launch_bounds__(kThreads, 1) lm_prompt_kernel(const __grid_con
                 // the next one: needed when this one's copies are out
                 if (p.list) {
                     int w = 0;
-                    if (lane == 0) w = atomicAdd(p.taken, 1) + gridDim.x;
+                    if (lane == 0) w = atomicAdd(p.counts + 1, 1) + gridDim.x;
                     fetch(__shfl_sync(0xffffffffu, w, 0));
                 }
                 const int n_max = max(it.n[0], it.n[1]);
@@ -824,7 +846,9 @@ __global__ void __launch_bounds__(kThreads, 1) lm_prompt_kernel(const __grid_con
             const bool fix = *reinterpret_cast<volatile int*>(&s.dirty[walk.k & 1]) == walk.k && lim > 0;
             if (live) {
                 const float lse = lim > 0 ? ref * p.sh.scale + logf(l) : -INFINITY;
-                if (p.part)
+                if (it.slot >= 0)
+                    p.piece_lse[((long long)it.slot * 2 + i) * kTile + r] = lse;
+                else if (p.part)
                     p.part_lse[((long long)blockIdx.z * p.rows + row) * p.sh.hq + h] = lse;
                 else if (p.lse)
                     p.lse[row * p.sh.hq + h] = lse;
@@ -835,8 +859,10 @@ __global__ void __launch_bounds__(kThreads, 1) lm_prompt_kernel(const __grid_con
             // item, and unrolled it came from beyond the instruction cache each time.
             uint8_t* out = sout + (size_t)(warp - 4) * kStageOut;
             const unsigned rows = __ballot_sync(0xffffffffu, live);
+            const bool fp32 = p.part || it.slot >= 0;
             const unsigned long long mine = reinterpret_cast<unsigned long long>(
-                p.part ? static_cast<void*>(p.part + (((long long)blockIdx.z * p.rows + row) * p.sh.hq + h) * D)
+                it.slot >= 0 ? static_cast<void*>(p.piece + (((long long)it.slot * 2 + i) * kTile + r) * D)
+                : p.part ? static_cast<void*>(p.part + (((long long)blockIdx.z * p.rows + row) * p.sh.hq + h) * D)
                        : static_cast<void*>(static_cast<T*>(p.o) + row * p.os + (long long)h * D));
             auto flush = [&](int byte) {
                 __syncwarp();
@@ -872,7 +898,7 @@ __global__ void __launch_bounds__(kThreads, 1) lm_prompt_kernel(const __grid_con
                 auto put = [&](int chunk, uint4 v) {
                     *reinterpret_cast<uint4*>(out + lane * 128 + ((chunk ^ (lane & 7)) << 4)) = v;
                 };
-                if (p.part) {
+                if (fp32) {
 #pragma unroll
                     for (int c = 0; c < 64; c += 32) {
 #pragma unroll
@@ -896,7 +922,7 @@ __global__ void __launch_bounds__(kThreads, 1) lm_prompt_kernel(const __grid_con
                 for (int c = 0; c < D; c++) {
                     const float x = not_finite_sum<T>(p, it, c, first_masked * kTile, lim);
                     if (x == 0.f) continue;
-                    if (p.part)
+                    if (fp32)
                         reinterpret_cast<float*>(mine)[c] = x;
                     else
                         reinterpret_cast<T*>(mine)[c] = (T)x;
@@ -917,17 +943,21 @@ __global__ void __launch_bounds__(kThreads, 1) lm_prompt_kernel(const __grid_con
 
 // The items of a call, from the device's lengths: requests by their keys,
 // most first (in request order where there are many), each request's last pair
-// of tiles first.  One CTA.
+// of tiles first.  With p.split, items of more than 5/4 of an SM's share of the
+// call's tiles are cut into pieces of about that share (at least kMinPiece
+// tiles: an item costs as much as three tiles besides them).  One CTA.
 constexpr int kListThreads = 512;
 constexpr int kListSort = 512;          // requests that are sorted (by counting)
+constexpr int kMinPiece = 6;
 
-__global__ void __launch_bounds__(kListThreads) lm_list_kernel(const Params p, int4* list, int* list_n, int* taken)
+__global__ void __launch_bounds__(kListThreads) lm_list_kernel(const Params p, int4* list)
 {
     __shared__ int keys[kListSort];
     __shared__ unsigned short order[kLmMaxRequests];
     __shared__ int start[kLmMaxRequests + 1];
-    __shared__ int warp_sum[kListThreads / 32];
-    __shared__ int carry;
+    __shared__ int warp_sum[3][kListThreads / 32];
+    __shared__ int carry[3];
+    __shared__ unsigned long long work;
     const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
     const int pair = 2 * p.tokens;
     pdl_wait();
@@ -943,8 +973,37 @@ __global__ void __launch_bounds__(kListThreads) lm_list_kernel(const Params p, i
         if (report && !(good && len)) atomicOr(p.sh.err, CODEC_LM_ERR_LENGTH);
         return k;
     };
+    // running sums over the block of up to three values, on top of carry (which grows)
+    auto scan = [&](int* v, int count) {
+        int incl[3];
+        for (int c = 0; c < count; c++) {
+            incl[c] = v[c];
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int up = __shfl_up_sync(0xffffffffu, incl[c], o);
+                if (lane >= o) incl[c] += up;
+            }
+            if (lane == 31) warp_sum[c][w] = incl[c];
+        }
+        __syncthreads();
+        int total[3];
+        for (int c = 0; c < count; c++) {
+            int at = carry[c];
+            total[c] = at;
+            for (int i = 0; i < kListThreads / 32; i++) {
+                if (i < w) at += warp_sum[c][i];
+                total[c] += warp_sum[c][i];
+            }
+            v[c] = at + incl[c] - v[c];         // exclusive
+        }
+        __syncthreads();
+        if (tid == 0)
+            for (int c = 0; c < count; c++) carry[c] = total[c];
+        __syncthreads();
+    };
     const bool sorted = p.B <= kListSort;
-    if (tid == 0) carry = 0;
+    if (tid < 3) carry[tid] = 0;
+    if (tid == 0) work = 0;
     for (int b = tid; b < p.B; b += kListThreads) {
         int first, n;
         const int k = rows_and_keys(b, first, n, true);
@@ -964,28 +1023,13 @@ __global__ void __launch_bounds__(kListThreads) lm_list_kernel(const Params p, i
             lm_rows(p.row_start, order[x], p.rows, first, n);
             tiles = (n + pair - 1) / pair;
         }
-        int incl = tiles;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int up = __shfl_up_sync(0xffffffffu, incl, o);
-            if (lane >= o) incl += up;
-        }
-        if (lane == 31) warp_sum[w] = incl;
-        __syncthreads();
-        int at = carry;
-        for (int i = 0; i < w; i++) at += warp_sum[i];
-        if (x < p.B) start[x] = at + incl - tiles;
-        __syncthreads();
-        if (tid == kListThreads - 1) carry = at + incl;
-        __syncthreads();
+        scan(&tiles, 1);
+        if (x < p.B) start[x] = tiles;
     }
     // row_starts that overlap could make more items than there is room for
-    const int total = min(carry, p.rows / pair + min(p.rows, p.B));
-    if (tid == 0) {
-        *list_n = total;
-        *taken = 0;
-    }
-    for (int e = tid; e < total; e += kListThreads) {
+    const int total = min(carry[0], (int)lm_list_items(p.rows, p.B, p.sh.group));
+    // the item of number e, and its K/V tiles
+    auto item = [&](int e, int4& rows) {
         int lo = 0, hi = p.B - 1;
         while (lo < hi) {
             const int mid = (lo + hi + 1) >> 1;
@@ -995,7 +1039,93 @@ __global__ void __launch_bounds__(kListThreads) lm_list_kernel(const Params p, i
         const int b = order[lo];
         const int k = rows_and_keys(b, first, n, false);
         const int t = (n + pair - 1) / pair - 1 - (e - start[lo]);
-        list[e] = make_int4(b, first + t * pair, min(pair, n - t * pair), k - n + t * pair + 1);
+        rows = make_int4(b, first + t * pair, min(pair, n - t * pair), k - n + t * pair + 1);
+        return (max(0, rows.w + rows.z - 1) + kTile - 1) / kTile;
+    };
+    if (!p.split) {
+        for (int e = tid; e < total; e += kListThreads) {
+            int4 rows;
+            item(e, rows);
+            list[2 * e] = rows;
+            list[2 * e + 1] = make_int4(0, kNone, -1, 0);
+        }
+        if (tid == 0) {
+            p.counts[0] = total;
+            p.counts[1] = 0;
+        }
+        return;
+    }
+    unsigned long long mine = 0;
+    for (int e = tid; e < total; e += kListThreads) {
+        int4 rows;
+        mine += item(e, rows);
+    }
+    if (mine) atomicAdd(&work, mine);           // whole numbers: any order
+    __syncthreads();
+    const int share = (int)min(max((work * p.sh.hk + kSms - 1) / kSms, (unsigned long long)kMinPiece), 1ull << 24);
+    if (tid < 3) carry[tid] = 0;
+    __syncthreads();
+    for (int base = 0; base < total; base += kListThreads) {
+        const int e = base + tid;
+        int4 rows;
+        int tiles = 0, pieces = 0;
+        if (e < total) {
+            tiles = item(e, rows);
+            pieces = tiles > share + share / 4 ? (tiles + share / 2) / share : 1;
+        }
+        int v[3] = {pieces, pieces > 1 ? pieces * p.sh.hk : 0, pieces > 1 ? 1 : 0};
+        scan(v, 3);
+        if (e >= total) continue;
+        // the shares bound the slots; should they not, the item stays whole (and keeps its places)
+        const bool cut = pieces > 1 && v[1] + pieces * p.sh.hk <= kLmSlots;
+        const int len = cut ? (tiles + pieces - 1) / pieces : kNone;
+        for (int c = 0; c < pieces; c++) {
+            const bool live = cut ? c * len < tiles : c == 0;
+            list[2 * (v[0] + c)] = live ? rows : make_int4(rows.x, rows.y, 0, 0);
+            list[2 * (v[0] + c) + 1] = cut && live ? make_int4(c * len, len, v[1] + c * p.sh.hk, 0) : make_int4(0, kNone, -1, 0);
+        }
+        if (pieces > 1) p.joins[v[2]] = make_int4(rows.y, cut ? rows.z : 0, v[1], cut ? (tiles + len - 1) / len : 0);
+    }
+    if (tid == 0) {
+        p.counts[0] = carry[0];
+        p.counts[1] = 0;
+        p.counts[2] = carry[2];
+    }
+}
+
+// Joins the pieces of items that were cut: a warp per row.
+constexpr int kPieceThreads = 256;
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kPieceThreads, 4) lm_pieces_kernel(const __grid_constant__ Params p)
+{
+    pdl_wait();
+    pdl_launch();
+    const int lane = threadIdx.x & 31, group = p.sh.group;
+    const long long total = (long long)__ldcg(p.counts + 2) * p.sh.hk * 2 * kTile;
+    const long long warps = gridDim.x * (kPieceThreads / 32LL);
+    for (long long x = blockIdx.x * (kPieceThreads / 32LL) + (threadIdx.x >> 5); x < total; x += warps) {
+        const int r = (int)(x % (2 * kTile));
+        const int y = (int)(x / (2 * kTile)), hk = y % p.sh.hk;
+        const int4 j = __ldcg(p.joins + y / p.sh.hk);
+        const int i = r / kTile, in = r % kTile, tok = i * p.tokens + in / group;
+        if (in >= p.tokens * group || tok >= j.y) continue;
+        auto row_of = [&](int c) { return (long long)(j.z + c * p.sh.hk + hk) * 2 * kTile + r; };
+        constexpr int kE = D / 32;
+        float v[kE], lse;
+        // a row that sees nothing has an lse of -inf in every piece; its first piece holds key 0 of all others
+        const bool empty = __ldcg(p.piece_lse + row_of(0)) == -INFINITY;
+        join_row<kE>(
+            j.w, empty, [&](int c) { return __ldcg(p.piece_lse + row_of(c)); },
+            [&](int c, float* f) { row_part<kE>(p.piece + row_of(c) * D, f); }, v, lse);
+        const long long row = j.x + tok;
+        const int h = hk * group + in % group;
+        T* dst = static_cast<T*>(p.o) + row * p.os + (long long)h * D + lane * kE;
+        if constexpr (kE == 4)
+            *reinterpret_cast<uint2*>(dst) = make_uint2(Two<T>::pack(v[0], v[1]), Two<T>::pack(v[2], v[3]));
+        else
+            *reinterpret_cast<uint32_t*>(dst) = Two<T>::pack(v[0], v[1]);
+        if (p.lse && lane == 0) p.lse[row * p.sh.hq + h] = lse;
     }
 }
 
@@ -1045,7 +1175,7 @@ uint32_t idesc(uint32_t format, int N, bool b_mn)
 
 template <typename T, int D>
 cudaError_t launch(const LmShape& sh, const void* q, long long qs, const LmKeys& ks, Params& p, dim3 grid,
-                   cudaStream_t s, int4* list, int* list_n)
+                   cudaStream_t s, int4* list)
 {
     p.sh = sh;
     p.tokens = kTile / sh.group;
@@ -1069,24 +1199,25 @@ cudaError_t launch(const LmShape& sh, const void* q, long long qs, const LmKeys&
         !lm_make_map(&mk, sh.type, ks.k, D, sh.hk, key_rows, k_stride, 1, box) ||
         !lm_make_map(&mv, sh.type, ks.v, D, sh.hk, key_rows, v_stride, 1, box))
         return cudaErrorInvalidValue;
+    cudaError_t e = cudaSuccess;
     if (list) {
-        const cudaError_t e = launch_pdl(lm_list_kernel, dim3(1), dim3(kListThreads), 0, s, p, list, list_n, list_n + 1);
+        e = launch_pdl(lm_list_kernel, dim3(1), dim3(kListThreads), 0, s, p, list);
         if (e != cudaSuccess) return e;
         p.list = list;
-        p.list_n = list_n;
-        p.taken = list_n + 1;
     }
-    return launch_pdl(lm_prompt_kernel<T, D>, grid, dim3(kThreads), smem_bytes<D>(), s, mq, mk, mv, p);
+    e = launch_pdl(lm_prompt_kernel<T, D>, grid, dim3(kThreads), smem_bytes<D>(), s, mq, mk, mv, p);
+    if (e != cudaSuccess || !p.split) return e;
+    return launch_pdl(lm_pieces_kernel<T, D>, dim3(2 * kSms), dim3(kPieceThreads), 0, s, p);
 }
 
 cudaError_t launch_any(const LmShape& sh, const void* q, long long qs, const LmKeys& ks, Params& p, dim3 grid,
-                       cudaStream_t s, int4* list = nullptr, int* list_n = nullptr)
+                       cudaStream_t s, int4* list = nullptr)
 {
     if (sh.type == CODEC_LM_BF16)
-        return sh.D == 128 ? launch<__nv_bfloat16, 128>(sh, q, qs, ks, p, grid, s, list, list_n)
-                           : launch<__nv_bfloat16, 64>(sh, q, qs, ks, p, grid, s, list, list_n);
-    return sh.D == 128 ? launch<__half, 128>(sh, q, qs, ks, p, grid, s, list, list_n)
-                       : launch<__half, 64>(sh, q, qs, ks, p, grid, s, list, list_n);
+        return sh.D == 128 ? launch<__nv_bfloat16, 128>(sh, q, qs, ks, p, grid, s, list)
+                           : launch<__nv_bfloat16, 64>(sh, q, qs, ks, p, grid, s, list);
+    return sh.D == 128 ? launch<__half, 128>(sh, q, qs, ks, p, grid, s, list)
+                       : launch<__half, 64>(sh, q, qs, ks, p, grid, s, list);
 }
 
 }  // namespace
@@ -1113,10 +1244,20 @@ cudaError_t launch_lm_prompt(const LmShape& sh, const LmPromptArgs& a, cudaStrea
     p.o = a.o;
     p.os = a.os;
     p.lse = a.lse;
-    // pairs of query tiles: at most one partly filled pair per request
-    const long long items = lm_list_items(a.rows, a.B, sh.group);
-    if (items * sh.hk <= kSms) return launch_any(sh, a.q, a.qs, a.keys, p, dim3((unsigned)items, (unsigned)sh.hk), s);
-    return launch_any(sh, a.q, a.qs, a.keys, p, dim3(kSms), s, static_cast<int4*>(a.list), a.list_n);
+    // Pairs of query tiles: at most one partly filled pair per request.  Cutting
+    // pays where they are few for the SMs and their keys many (which a context
+    // in the cache may be): a call of one request of 64 tokens behind 32,768
+    // positions is otherwise eight items.
+    const long long items = lm_list_items(a.rows, a.B, sh.group) * sh.hk;
+    const bool cut = (a.keys.tables || a.rows > 1024) && items <= 4 * kSms;
+    if (items <= kSms && !cut)
+        return launch_any(sh, a.q, a.qs, a.keys, p, dim3((unsigned)(items / sh.hk), (unsigned)sh.hk), s);
+    p.split = cut;
+    p.counts = a.ws.counts;
+    p.joins = static_cast<int4*>(a.ws.joins);
+    p.piece = a.ws.piece;
+    p.piece_lse = a.ws.piece_lse;
+    return launch_any(sh, a.q, a.qs, a.keys, p, dim3(kSms), s, static_cast<int4*>(a.ws.list));
 }
 
 cudaError_t launch_lm_shared(const LmShape& sh, const LmSharedArgs& a, cudaStream_t s)

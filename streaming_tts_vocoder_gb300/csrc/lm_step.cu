@@ -22,6 +22,7 @@
 #include <algorithm>
 
 #include "lm.h"
+#include "lm_join.cuh"
 #include "tc_ptx.cuh"
 
 namespace codec {
@@ -188,66 +189,17 @@ __device__ __forceinline__ void join_parts(const Params& p, int b, int h, int n_
     auto row_of = [&](int i) {
         return i < p.n_pre ? (long long)i * p.B * p.sh.hq + shared_row : (long long)(i - p.n_pre) * p.sh.hq + own_row;
     };
-    auto lse_of = [&](int i) { return __ldcg((i < p.n_pre ? p.pre_lse : p.part_lse) + row_of(i)); };
     constexpr int kE = D / 32;
-    auto part_of = [&](int i, float* x) {
-        const float* src = (i < p.n_pre ? p.pre : p.part) + row_of(i) * D;
-        if constexpr (kE == 4) {
-            const float4 y = __ldcg(reinterpret_cast<const float4*>(src) + lane);
-            x[0] = y.x; x[1] = y.y; x[2] = y.z; x[3] = y.w;
-        } else {
-            const float2 y = __ldcg(reinterpret_cast<const float2*>(src) + lane);
-            x[0] = y.x; x[1] = y.y;
-        }
-    };
-    // the first parts are on their way while the weights are worked out
-    constexpr int kAhead = 4;
-    const float mine = lane < parts ? lse_of(lane) : -INFINITY;
-    float ahead[kAhead][kE];
-#pragma unroll
-    for (int i = 0; i < kAhead; i++)
-        if (i < parts) part_of(i, ahead[i]);
-    float m = -INFINITY;
-    bool nan = false;
-    for (int i = lane; i < parts; i += 32) {
-        const float x = i < 32 ? mine : lse_of(i);
-        m = fmaxf(m, x);
-        nan |= x != x;
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    if (__any_sync(0xffffffffu, nan)) m = NAN;
-    const float ref = m == -INFINITY ? 0.f : m;
-    float v[kE] = {}, sum = 0.f;
-    float w = lane < parts ? expf(mine - ref) : 0.f;
-    auto add = [&](float f, const float* x) {
-        sum += f;
-#pragma unroll
-        for (int e = 0; e < kE; e++) v[e] = f != 0.f ? fmaf(f, x[e], v[e]) : v[e];  // a part without keys has no value
-    };
-#pragma unroll
-    for (int i = 0; i < kAhead; i++) {
-        const float f = __shfl_sync(0xffffffffu, w, i);
-        if (i < parts) add(f, ahead[i]);
-    }
-    for (int i0 = 0; i0 < parts; i0 += 32) {
-        if (i0 > 0) w = i0 + lane < parts ? expf(lse_of(i0 + lane) - ref) : 0.f;
-        const int cnt = min(32, parts - i0);
-#pragma unroll 8
-        for (int i = i0 == 0 ? kAhead : 0; i < cnt; i++) {
-            float x[kE];
-            part_of(i0 + i, x);
-            add(__shfl_sync(0xffffffffu, w, i), x);
-        }
-    }
-    const float inv = empty ? 0.f : 1.f / sum;
+    float v[kE], lse;
+    join_row<kE>(
+        parts, empty, [&](int i) { return __ldcg((i < p.n_pre ? p.pre_lse : p.part_lse) + row_of(i)); },
+        [&](int i, float* x) { row_part<kE>((i < p.n_pre ? p.pre : p.part) + row_of(i) * D, x); }, v, lse);
     T* dst = static_cast<T*>(p.o) + b * p.os + (long long)h * D + lane * kE;
     if constexpr (kE == 4)
-        *reinterpret_cast<uint2*>(dst) =
-            make_uint2(Mma<T>::pack(v[0] * inv, v[1] * inv), Mma<T>::pack(v[2] * inv, v[3] * inv));
+        *reinterpret_cast<uint2*>(dst) = make_uint2(Mma<T>::pack(v[0], v[1]), Mma<T>::pack(v[2], v[3]));
     else
-        *reinterpret_cast<uint32_t*>(dst) = Mma<T>::pack(v[0] * inv, v[1] * inv);
-    if (p.lse && lane == 0) p.lse[(long long)b * p.sh.hq + h] = empty ? -INFINITY : m + logf(sum);
+        *reinterpret_cast<uint32_t*>(dst) = Mma<T>::pack(v[0], v[1]);
+    if (p.lse && lane == 0) p.lse[(long long)b * p.sh.hq + h] = lse;
 }
 
 __device__ __forceinline__ int splits_of(const Params& p, int len)
@@ -259,7 +211,7 @@ __device__ __forceinline__ int splits_of(const Params& p, int len)
 constexpr int kJoinThreads = 256;
 
 template <typename T, int D>
-__global__ void __launch_bounds__(kJoinThreads, 6) lm_join_kernel(const __grid_constant__ Params p)
+__global__ void __launch_bounds__(kJoinThreads, 4) lm_join_kernel(const __grid_constant__ Params p)
 {
     pdl_wait();
     pdl_launch();

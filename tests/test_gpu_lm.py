@@ -336,6 +336,23 @@ def test_prompt_paged_rows_without_keys():
     check_paged([300], [300], 4, 1, 64, "fp16", 32)
 
 
+@pytest.mark.parametrize("new,kv,hq,hk,d,bs", [
+    ([3], [9000], 4, 2, 128, 16),               # one request behind a long context: cut along the keys
+    ([70, 1, 33], [5000, 8200, 700], 4, 1, 64, 64),
+    ([260], [4100], 2, 2, 128, 128),            # several pairs of tiles, each cut
+    ([40, 5], [3, 6000], 16, 1, 64, 32),        # one with rows that see nothing, one cut
+])
+def test_prompt_paged_long_context(new, kv, hq, hk, d, bs):
+    check_paged(new, kv, hq, hk, d, "bf16", bs, seed=3)
+    check_paged(new, kv, hq, hk, d, "fp16", bs, seed=4)
+
+
+def test_prompt_cut_along_the_keys():
+    """Packed prompts whose items are few and long."""
+    check_prompt([2100], 4, 1, 64, "fp16")
+    check_prompt([1500, 30, 1], 2, 2, 128, "bf16")
+
+
 def check_step(kv, sh, hq, hk, d, dt, bs, seed=0, mul=1.0):
     kc, vc, tables, shared, n_blocks, width, gen = cache_case(seed, kv, hk, d, dt, bs, sh)
     B = len(kv)
