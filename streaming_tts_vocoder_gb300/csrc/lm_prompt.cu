@@ -108,24 +108,35 @@ struct Item {
     int n[2];                   // K/V tiles of each query tile
 };
 
-// MN-major operand with 128-byte swizzle: 64 elements of N in a 128-byte row
-// per k; 8-row groups 1024 bytes apart (stride byte offset), the next 64
-// elements of N one half tile further (leading byte offset).
-__device__ __forceinline__ uint64_t sdesc_mn_sw128(uint32_t saddr)
+// Operand descriptors, low words (address and leading byte offset; the high
+// word is the same for all: 8-row groups 1024 bytes apart, descriptor version,
+// 128-byte swizzle).  K-major: as sdesc_sw128.  MN-major: 64 elements of N in a
+// 128-byte row per k, the next 64 one half tile further (leading byte offset).
+constexpr uint32_t kDescHigh = (1024u >> 4) | (1u << 14) | (2u << 29);
+__device__ __forceinline__ uint32_t desc_k(uint32_t saddr) { return (saddr >> 4) | (1u << 16); }
+__device__ __forceinline__ uint32_t desc_mn(uint32_t saddr) { return (saddr >> 4) | ((kHalfBytes >> 4) << 16); }
+
+// D[tmem] (+)= A[shared] x B[shared]
+__device__ __forceinline__ void mma_ss(uint32_t d_tmem, uint32_t a, uint32_t b, uint32_t idesc, uint32_t accumulate)
 {
-    return (uint64_t)((saddr & 0x3FFFFu) >> 4) | ((uint64_t)(kHalfBytes >> 4) << 16) | ((uint64_t)(1024 >> 4) << 32) |
-           ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b64 da, db;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "mov.b64 da, {%1, %5};\n\tmov.b64 db, {%2, %5};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, p;\n\t}" ::"r"(d_tmem),
+        "r"(a), "r"(b), "r"(idesc), "r"(accumulate), "r"(kDescHigh)
+        : "memory");
 }
 
 // D[tmem] (+)= A[tmem] x B[shared]
-__device__ __forceinline__ void mma_f16_ta(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
-                                           uint32_t accumulate)
+__device__ __forceinline__ void mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint32_t b, uint32_t idesc, uint32_t accumulate)
 {
     asm volatile(
-        "{\n\t.reg .pred p;\n\t"
+        "{\n\t.reg .pred p;\n\t.reg .b64 db;\n\t"
         "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
-        "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
+        "mov.b64 db, {%2, %5};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %3, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_tmem), "r"(b), "r"(idesc), "r"(accumulate), "r"(kDescHigh)
         : "memory");
 }
 
@@ -232,8 +243,7 @@ struct Shared {
     uint64_t raw[kMaxStages], clean[kMaxStages];    // V tiles that are cleaned before use: landed, cleaned
     uint64_t q_full[2], q_empty[2], s_full[2], p_full[2][2], o_full[2], o_empty[2];
     uint64_t work_full[kWork], work_empty[kWork];
-    Entry work[kWork];
-    int work_hk[kWork];         // K/V head; -1: no more
+    Item work[kWork];           // hk -1: no more
     uint32_t tmem;
     int abort;
     int scan[kThreads / 32];
@@ -326,56 +336,45 @@ __device__ __forceinline__ void derive(const Params& p, Item& it, int4 keys)
 }
 
 // The CTA's items, one after the other.  The copy warp takes them from a
-// counter and hands them on; each other role waits for them by itself.
+// counter and hands them on in shared memory (few registers: each role reads
+// what it needs); each other role waits for them by itself.
 struct Walk {
     int k = 0;                  // items so far
 
-    __device__ __forceinline__ bool set(const Params& p, Item& it, const Entry& e, int hk)
+    // The copy warp hands out (e, hk); null: that was the end.
+    __device__ __forceinline__ const Item* hand_out(const Params& p, Shared& s, const Entry& e, int hk, int lane)
     {
-        if (hk < 0) return false;
-        it.hk = hk;
-        it.b = e.rows.x;
-        it.q0 = e.rows.y;
-        it.ntok = e.rows.z;
-        it.first = e.rows.w;
-        derive(p, it, e.keys);
-        return true;
-    }
-    // The copy warp hands out (e, hk).
-    __device__ __forceinline__ bool hand_out(const Params& p, Shared& s, const Entry& e, int hk, Item& it, int lane)
-    {
-        if (!p.list) {
-            if (k++ || !s.found) return false;
-            it = s.item;
-            return true;
-        }
+        if (!p.list) return k++ || !s.found ? nullptr : &s.item;
         const int slot = k % kWork;
         const bool ok = mbar_wait(&s.work_empty[slot], (uint32_t)(k / kWork & 1) ^ 1u, &s.abort, kPolls);
         k++;
-        if (!__all_sync(0xffffffffu, ok)) return false;
+        if (!__all_sync(0xffffffffu, ok)) return nullptr;
+        Item& it = s.work[slot];
         if (lane == 0) {
-            s.work[slot] = e;
-            s.work_hk[slot] = hk;
+            it.hk = hk;
+            it.b = e.rows.x;
+            it.q0 = e.rows.y;
+            it.ntok = e.rows.z;
+            it.first = e.rows.w;
+            derive(p, it, e.keys);
             mbar_arrive(&s.work_full[slot]);
         }
-        return set(p, it, e, hk);
+        __syncwarp();
+        return hk < 0 ? nullptr : &it;
     }
-    // Every other role; arrives: one thread of each waiting warp.
-    __device__ __forceinline__ bool next(const Params& p, Shared& s, Item& it, bool arrives)
+    // Every other role.
+    __device__ __forceinline__ const Item* next(const Params& p, Shared& s)
     {
-        if (!p.list) {
-            if (k++ || !s.found) return false;
-            it = s.item;
-            return true;
-        }
+        if (!p.list) return k++ || !s.found ? nullptr : &s.item;
         const int slot = k % kWork;
         const bool ok = mbar_wait(&s.work_full[slot], (uint32_t)(k / kWork & 1), &s.abort, kPolls);
         k++;
-        if (!ok) return false;
-        const Entry e = s.work[slot];
-        const int hk = s.work_hk[slot];
-        if (arrives) mbar_arrive(&s.work_empty[slot]);
-        return set(p, it, e, hk);
+        return !ok || s.work[slot].hk < 0 ? nullptr : &s.work[slot];
+    }
+    // and when it needs the item no longer: one thread of each waiting warp.
+    __device__ __forceinline__ void done(const Params& p, Shared& s)
+    {
+        if (p.list) mbar_arrive(&s.work_empty[(k - 1) % kWork]);
     }
 };
 
@@ -504,7 +503,6 @@ __global__ void __launch_bounds__(kThreads, 1) lm_prompt_kernel(const __grid_con
     }
     volatile int* abort_flag = &s.abort;
     Walk walk;
-    Item it;
 
     if (warp < 4) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 72;" ::: "memory");
@@ -528,7 +526,10 @@ __global__ void __launch_bounds__(kThreads, 1) lm_prompt_kernel(const __grid_con
                 }
             };
             if (p.list) fetch(blockIdx.x);
-            while (ok && walk.hand_out(p, s, entry, entry_hk, it, lane)) {
+            while (ok) {
+                const Item* const item = walk.hand_out(p, s, entry, entry_hk, lane);
+                if (!item) break;
+                const Item& it = *item;
                 // the next one: needed when this one's copies are out
                 if (p.list) {
                     int w = 0;
@@ -626,35 +627,39 @@ __global__ void __launch_bounds__(kThreads, 1) lm_prompt_kernel(const __grid_con
                     return in;
                 };
                 auto score = [&](int i, int stage, bool last) {         // S_i = Q_i K^T
-                    const uint64_t a0 = sdesc_sw128(q_addr + i * kBytes), b0 = sdesc_sw128(kv_addr + stage * kBytes);
+                    const uint32_t a0 = desc_k(q_addr + i * kBytes), b0 = desc_k(kv_addr + stage * kBytes);
 #pragma unroll
                     for (int k = 0; k < D / 16; k++) {
-                        const uint64_t off = (uint64_t)(((k >> 2) * kHalfBytes + (k & 3) * 32) >> 4);
-                        mma_f16(tmem + i * 128, a0 + off, b0 + off, p.idesc_s, k > 0);
+                        const uint32_t off = ((k >> 2) * kHalfBytes + (k & 3) * 32) >> 4;
+                        mma_ss(tmem + i * 128, a0 + off, b0 + off, p.idesc_s, k > 0);
                     }
                     mma_commit(&s.s_full[i]);
                     if (last) mma_commit(&s.q_empty[i]);
                 };
                 auto value = [&](int i, int stage, int half, bool more) {   // O_i += P_i V over 64 keys
-                    const uint64_t b0 = sdesc_mn_sw128(kv_addr + stage * kBytes);
+                    const uint32_t b0 = desc_mn(kv_addr + stage * kBytes);
 #pragma unroll
                     for (int k = half * 4; k < half * 4 + 4; k++)
-                        mma_f16_ta(tmem + 256 + i * 128, tmem + i * 128 + k * 8, b0 + (uint64_t)((k * 2048) >> 4),
-                                   p.idesc_o, more || k > 0);
+                        mma_ts(tmem + 256 + i * 128, tmem + i * 128 + k * 8, b0 + ((k * 2048) >> 4), p.idesc_o,
+                               more || k > 0);
                 };
                 bool ok = true;
-                while (ok && walk.next(p, s, it, true)) {
-                    const int n_max = max(it.n[0], it.n[1]);
+                while (ok) {
+                    const Item* const item = walk.next(p, s);
+                    if (!item) break;
+                    const int n0 = item->n[0], n1 = item->n[1], first_masked = item->free_from / kTile;
+                    walk.done(p, s);
+                    const int n_max = max(n0, n1);
                     if (n_max == 0) continue;
-                    const int first_masked = it.free_from / kTile;
                     const int sk0 = st;
                     if (++st == kStages) st = 0;
                     if (!(ok = landed(sk0))) break;
-                    for (int i = 0; i < 2 && ok; i++) {
-                        if (it.n[i] == 0) continue;
+#pragma unroll
+                    for (int i = 0; i < 2; i++) {
+                        if ((i ? n1 : n0) == 0 || !ok) continue;
                         ok = mbar_wait(&s.q_full[i], item_ph >> i & 1u, abort_flag, kPolls);
                         tc_fence_after();
-                        if (ok) score(i, sk0, it.n[i] == 1);
+                        if (ok) score(i, sk0, (i ? n1 : n0) == 1);
                     }
                     if (!ok) break;
                     mma_commit(&s.empty[sk0]);
@@ -673,8 +678,10 @@ __global__ void __launch_bounds__(kThreads, 1) lm_prompt_kernel(const __grid_con
                         const bool more = j + 1 < n_max;
                         if (more && ++st == kStages) st = 0;
                         bool here = false;              // K_{j+1} has landed
-                        for (int i = 0; i < 2 && ok; i++) {
-                            if (j < it.n[i]) {
+#pragma unroll
+                        for (int i = 0; i < 2; i++) {
+                            if (!ok) break;
+                            if (j < (i ? n1 : n0)) {
                                 const uint32_t ph = tile_ph >> i & 1u;
                                 ok = mbar_wait(&s.p_full[i][0], ph, abort_flag, kPolls);
                                 // the last item's result has been read
@@ -687,14 +694,14 @@ __global__ void __launch_bounds__(kThreads, 1) lm_prompt_kernel(const __grid_con
                                 tc_fence_after();
                                 value(i, sv, 1, true);
                                 tile_ph ^= 1u << i;
-                                if (j + 1 == it.n[i]) mma_commit(&s.o_full[i]);
+                                if (j + 1 == (i ? n1 : n0)) mma_commit(&s.o_full[i]);
                             }
-                            if (j + 1 < it.n[i]) {
+                            if (j + 1 < (i ? n1 : n0)) {
                                 if (!here) {
                                     if (!(ok = landed(sk))) break;
                                     here = true;
                                 }
-                                score(i, sk, j + 2 == it.n[i]);
+                                score(i, sk, j + 2 == (i ? n1 : n0));
                             }
                         }
                         if (!ok) break;
@@ -702,7 +709,7 @@ __global__ void __launch_bounds__(kThreads, 1) lm_prompt_kernel(const __grid_con
                         if (more) mma_commit(&s.empty[sk]);
                     }
                     for (int i = 0; i < 2; i++)
-                        if (it.n[i] > 0) item_ph ^= 1u << i;
+                        if ((i ? n1 : n0) > 0) item_ph ^= 1u << i;
                 }
                 // all issued MMAs complete before TMEM is released
                 mma_commit(&s.drain);
@@ -715,16 +722,20 @@ __global__ void __launch_bounds__(kThreads, 1) lm_prompt_kernel(const __grid_con
             uint32_t raw_ph = 0;                        // parity of each stage's raw barrier
             int load0 = 0;                              // stage of the item's first load
             bool ok = true;
-            while (ok && __all_sync(0xffffffffu, walk.next(p, s, it, lane == 0))) {
-                const int n_max = max(it.n[0], it.n[1]);
-                for (int j = it.free_from / kTile; j < n_max; j++) {
+            while (ok) {
+                const Item* const item = walk.next(p, s);
+                if (!__all_sync(0xffffffffu, item != nullptr)) break;
+                const int n_max = max(item->n[0], item->n[1]), first_masked = item->free_from / kTile, end = item->end;
+                __syncwarp();
+                if (lane == 0) walk.done(p, s);
+                for (int j = first_masked; j < n_max; j++) {
                     const int st = (load0 + 2 * j + 1) % kStages;
                     ok = mbar_wait(&s.raw[st], raw_ph >> st & 1u, abort_flag, kPolls);
                     raw_ph ^= 1u << st;
                     ok = __all_sync(0xffffffffu, ok);
                     if (!ok) break;
                     uint8_t* v = skv + (size_t)st * kBytes;
-                    const int live = min(kTile, it.end - j * kTile);
+                    const int live = min(kTile, end - j * kTile);
                     for (int e = t; e < kTile * D / 8; e += 64) {       // 16 bytes: 8 values of a key
                         const int r = (e >> 3) & (kTile - 1);
                         uint4* at = reinterpret_cast<uint4*>(v + e * 16);
@@ -763,7 +774,10 @@ __global__ void __launch_bounds__(kThreads, 1) lm_prompt_kernel(const __grid_con
         const uint32_t ts = lane_base + i * 128, to = lane_base + 256 + i * 128;
         uint32_t tile_ph = 0, item_ph = 0;
         bool ok = true;
-        while (ok && __all_sync(0xffffffffu, walk.next(p, s, it, lane == 0))) {
+        while (ok) {
+            const Item* const item = walk.next(p, s);
+            if (!__all_sync(0xffffffffu, item != nullptr)) break;
+            const Item& it = *item;
             const bool live = r < p.tokens * p.sh.group && tok < it.ntok;
             const int lim = live ? keys_of(p, it, tok) : 0;
             const int n = it.n[i];
@@ -929,7 +943,10 @@ __global__ void __launch_bounds__(kThreads, 1) lm_prompt_kernel(const __grid_con
                 }
             }
             __syncwarp();
-            if (lane == 0) atomicAdd(&s.written[i], 1);
+            if (lane == 0) {
+                atomicAdd(&s.written[i], 1);
+                walk.done(p, s);
+            }
         }
         tc_fence_before();
     }
@@ -1245,11 +1262,12 @@ cudaError_t launch_lm_prompt(const LmShape& sh, const LmPromptArgs& a, cudaStrea
     p.os = a.os;
     p.lse = a.lse;
     // Pairs of query tiles: at most one partly filled pair per request.  Cutting
-    // pays where they are few for the SMs and their keys many (which a context
-    // in the cache may be): a call of one request of 64 tokens behind 32,768
-    // positions is otherwise eight items.
+    // along the keys pays where items are few for the SMs and their keys may be
+    // many: 64 tokens behind 32,768 positions are otherwise eight items.  (It
+    // costs about 10 us: 16 paged prompts of 144 items, 58 us whole, took 67 cut.)
     const long long items = lm_list_items(a.rows, a.B, sh.group) * sh.hk;
-    const bool cut = (a.keys.tables || a.rows > 1024) && items <= 4 * kSms;
+    const bool cut = a.keys.tables ? items <= kSms && ((long long)a.keys.table_blocks << a.keys.bs_shift) > 2048
+                                   : items <= 2 * kSms && a.rows > 2048;
     if (items <= kSms && !cut)
         return launch_any(sh, a.q, a.qs, a.keys, p, dim3((unsigned)(items / sh.hk), (unsigned)sh.hk), s);
     p.split = cut;
