@@ -8,13 +8,13 @@
 namespace codec {
 
 // lse_of(i): a part's lse; part_of(i, x): this lane's columns of a part.
-// empty: the row sees nothing (v = 0, lse = -inf).
-template <int kE, typename Lse, typename Part>
+// empty: the row sees nothing (v = 0, lse = -inf).  kAhead: parts that are read
+// before their weights are known.
+template <int kE, int kAhead, typename Lse, typename Part>
 __device__ __forceinline__ void join_row(int parts, bool empty, Lse lse_of, Part part_of, float* v, float& lse)
 {
     const int lane = threadIdx.x & 31;
     // the first parts are on their way while the weights are worked out
-    constexpr int kAhead = 4;
     const float mine = lane < parts ? lse_of(lane) : -INFINITY;
     float ahead[kAhead][kE];
 #pragma unroll

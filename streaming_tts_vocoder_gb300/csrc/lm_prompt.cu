@@ -1132,7 +1132,7 @@ __global__ void __launch_bounds__(kPieceThreads, 4) lm_pieces_kernel(const __gri
         float v[kE], lse;
         // a row that sees nothing has an lse of -inf in every piece; its first piece holds key 0 of all others
         const bool empty = __ldcg(p.piece_lse + row_of(0)) == -INFINITY;
-        join_row<kE>(
+        join_row<kE, 4>(
             j.w, empty, [&](int c) { return __ldcg(p.piece_lse + row_of(c)); },
             [&](int c, float* f) { row_part<kE>(p.piece + row_of(c) * D, f); }, v, lse);
         const long long row = j.x + tok;

@@ -179,24 +179,31 @@ __global__ void __launch_bounds__(kRotThreads, 5) lm_rotate_kernel(const LmRotat
         if (lane == 0) atomicOr(err, CODEC_LM_ERR_POSITION);
         return;
     }
+    // queries, keys and values: all here, or one of them by blockIdx.y
+    const bool all = gridDim.y == 1;
     // cos, sin of this lane's eight rotations: pair index c + i (halves), or
     // c / 2 + i and D / 4 + c / 2 + i (pairs)
-    float cs[8], sn[8];
-    const float2* t = a.turn + (long long)pos * (D / 2);
+    float cs[8] = {}, sn[8] = {};
+    if (blockIdx.y < 2) {
+        const float2* t = a.turn + (long long)pos * (D / 2);
 #pragma unroll
-    for (int i = 0; i < 8; i += 2) {
-        const int at = a.pairs ? (i < 4 ? c / 2 + i : D / 4 + c / 2 + i - 4) : c + i;
-        const float4 v = __ldg(reinterpret_cast<const float4*>(t + at));
-        cs[i] = v.x;
-        sn[i] = v.y;
-        cs[i + 1] = v.z;
-        sn[i + 1] = v.w;
+        for (int i = 0; i < 8; i += 2) {
+            const int at = a.pairs ? (i < 4 ? c / 2 + i : D / 4 + c / 2 + i - 4) : c + i;
+            const float4 v = __ldg(reinterpret_cast<const float4*>(t + at));
+            cs[i] = v.x;
+            sn[i] = v.y;
+            cs[i + 1] = v.z;
+            sn[i + 1] = v.w;
+        }
     }
-    heads_of<T, TI, D, true>(static_cast<const TI*>(a.q) + row * a.qs, static_cast<T*>(a.q_out) + (long long)row * hq * D,
-                             hq, part, parts, a.q_gain, a.eps, a.pairs, cs, sn);
-    heads_of<T, TI, D, true>(static_cast<const TI*>(a.k) + row * a.ks, static_cast<T*>(a.k_dst) + slot * hk * D, hk,
-                             part, parts, a.k_gain, a.eps, a.pairs, cs, sn);
-    if (a.v)
+    if (blockIdx.y == 0)
+        heads_of<T, TI, D, true>(static_cast<const TI*>(a.q) + row * a.qs,
+                                 static_cast<T*>(a.q_out) + (long long)row * hq * D, hq, part, parts, a.q_gain, a.eps,
+                                 a.pairs, cs, sn);
+    if (all || blockIdx.y == 1)
+        heads_of<T, TI, D, true>(static_cast<const TI*>(a.k) + row * a.ks, static_cast<T*>(a.k_dst) + slot * hk * D,
+                                 hk, part, parts, a.k_gain, a.eps, a.pairs, cs, sn);
+    if (a.v && (all || blockIdx.y == 2))
         heads_of<T, TI, D, false>(static_cast<const TI*>(a.v) + row * a.vs, static_cast<T*>(a.v_dst) + slot * hk * D,
                                   hk, part, parts, nullptr, 0.f, 0, cs, sn);
 }
@@ -222,7 +229,10 @@ cudaError_t launch(const LmShape& sh, const LmRotateArgs& a, cudaStream_t s)
     while (parts < most && (long long)a.rows * parts < 152 * 16) parts++;
     const long long warps = (long long)a.rows * parts;
     const unsigned ctas = (unsigned)((warps + kRotThreads / 32 - 1) / (kRotThreads / 32));
-    lm_rotate_kernel<T, TI, D><<<ctas, kRotThreads, 0, s>>>(a, sh.hq, sh.hk, parts, sh.err);
+    // Up to eight rows per resident warp (five CTAs of four per SM) queries, keys
+    // and values go to warps of their own: shorter warps leave a shorter tail.
+    const unsigned kinds = a.rows < 8 * 152 * 20 ? (a.v ? 3 : 2) : 1;
+    lm_rotate_kernel<T, TI, D><<<dim3(ctas, kinds), kRotThreads, 0, s>>>(a, sh.hq, sh.hk, parts, sh.err);
     return cudaGetLastError();
 }
 

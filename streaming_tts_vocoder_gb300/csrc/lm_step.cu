@@ -47,7 +47,6 @@ struct Params {
     int shared_len, n_pre;              // shared part: length, partial results of it
     int chunk, max_splits;
     int stages;
-    int join;                           // partial results are joined here
     int after_shared;                   // the shared part's kernel is running: nothing here needs its results
     float c;                            // scale x log2 e
     float* part;                        // [B][max_splits][hq][D]
@@ -181,7 +180,7 @@ size_t smem_bytes(int stages, int group, int B)
 
 // Joins the partial results of (request, head), the shared part's first, in
 // order.  One warp; empty: the request has no position at all.
-template <typename T, int D>
+template <typename T, int D, int kAhead>
 __device__ __forceinline__ void join_parts(const Params& p, int b, int h, int n_splits, bool empty, int lane)
 {
     const int parts = p.n_pre + n_splits;
@@ -191,7 +190,7 @@ __device__ __forceinline__ void join_parts(const Params& p, int b, int h, int n_
     };
     constexpr int kE = D / 32;
     float v[kE], lse;
-    join_row<kE>(
+    join_row<kE, kAhead>(
         parts, empty, [&](int i) { return __ldcg((i < p.n_pre ? p.pre_lse : p.part_lse) + row_of(i)); },
         [&](int i, float* x) { row_part<kE>((i < p.n_pre ? p.pre : p.part) + row_of(i) * D, x); }, v, lse);
     T* dst = static_cast<T*>(p.o) + b * p.os + (long long)h * D + lane * kE;
@@ -223,10 +222,12 @@ __global__ void __launch_bounds__(kJoinThreads, 4) lm_join_kernel(const __grid_c
     lm_clamp_len(len, (long long)p.table_blocks << p.bs_shift);
     const int n = splits_of(p, len);
     if (n == 1 && p.n_pre == 0) return;         // written by its unit
-    join_parts<T, D>(p, b, h, n, len == 0, threadIdx.x & 31);
+    join_parts<T, D, 4>(p, b, h, n, len == 0, threadIdx.x & 31);
 }
 
-template <typename T, int D>
+// kJoin: partial results are joined here (an instance of its own: the join's
+// registers would make the main loop spill).
+template <typename T, int D, bool kJoin>
 __global__ void __launch_bounds__(kThreads, 2) lm_step_kernel(const __grid_constant__ CUtensorMap mk,
                                                            const __grid_constant__ CUtensorMap mv,
                                                            const __grid_constant__ Params p)
@@ -521,22 +522,26 @@ __global__ void __launch_bounds__(kThreads, 2) lm_step_kernel(const __grid_const
                     if (d == 0) __stcg(p.part_lse + at + g, lse);
                 }
             }
-            if (alone || !p.join) {
+            if (alone || !kJoin) {
                 consumers_sync();           // res is written again
                 continue;
             }
-            __threadfence();
             consumers_sync();
             if (tid == 0) {
+                // releases the CTA's results (ordered before it by the barrier) and
+                // acquires those of the others
                 int* done = p.done + (long long)n.b * p.sh.hk + n.hk;
-                flags[1] = n.n_splits == 1 || atomicAdd(done, 1) == n.n_splits - 1;
+                int was = 0;
+                if (n.n_splits > 1)
+                    asm volatile("atom.acq_rel.gpu.global.add.s32 %0, [%1], 1;" : "=r"(was) : "l"(done) : "memory");
+                flags[1] = was == n.n_splits - 1;
                 if (flags[1] && n.n_splits > 1) *done = 0;
-                __threadfence();
             }
             consumers_sync();
             if (!flags[1]) continue;
-            for (int g = warp; g < group; g += kConsumers)
-                join_parts<T, D>(p, n.b, n.hk * group + g, n.n_splits, n.empty, lane);
+            if constexpr (kJoin)
+                for (int g = warp; g < group; g += kConsumers)
+                    join_parts<T, D, 12>(p, n.b, n.hk * group + g, n.n_splits, n.empty, lane);
         }
     }
     __syncthreads();
@@ -601,10 +606,9 @@ cudaError_t launch(const LmShape& sh, const LmStepArgs& a, cudaStream_t s)
     const unsigned ctas = (unsigned)std::min<long long>(152 * per_sm, most);
     p.after_shared = p.n_pre > 0;
     // joined in this kernel where a CTA has one unit at most and needs no other kernel's results
-    p.join = most <= ctas && p.n_pre == 0;
-    const bool two = !p.join && (p.n_pre > 0 || p.max_splits > 1);
+    const bool join = most <= ctas && p.n_pre == 0, two = !join && (p.n_pre > 0 || p.max_splits > 1);
     p.taken = two ? a.ws.taken : nullptr;
-    const cudaError_t e = launch_pdl(lm_step_kernel<T, D>, dim3(ctas), dim3(kThreads), smem_bytes<D>(p.stages, sh.group, a.B), s, mk,
+    const cudaError_t e = launch_pdl(join ? lm_step_kernel<T, D, true> : lm_step_kernel<T, D, false>, dim3(ctas), dim3(kThreads), smem_bytes<D>(p.stages, sh.group, a.B), s, mk,
                                      mv, p);
     if (e != cudaSuccess || !two) return e;
     return launch_pdl(lm_join_kernel<T, D>, dim3((unsigned)(((long long)a.B * sh.hq + kJoinThreads / 32 - 1) / (kJoinThreads / 32))),
@@ -615,8 +619,11 @@ cudaError_t launch(const LmShape& sh, const LmStepArgs& a, cudaStream_t s)
 
 cudaError_t configure_lm_step()
 {
-    const void* kernels[] = {(const void*)lm_step_kernel<__nv_bfloat16, 128>, (const void*)lm_step_kernel<__nv_bfloat16, 64>,
-                             (const void*)lm_step_kernel<__half, 128>, (const void*)lm_step_kernel<__half, 64>};
+    const void* kernels[] = {
+        (const void*)lm_step_kernel<__nv_bfloat16, 128, false>, (const void*)lm_step_kernel<__nv_bfloat16, 64, false>,
+        (const void*)lm_step_kernel<__half, 128, false>,        (const void*)lm_step_kernel<__half, 64, false>,
+        (const void*)lm_step_kernel<__nv_bfloat16, 128, true>,  (const void*)lm_step_kernel<__nv_bfloat16, 64, true>,
+        (const void*)lm_step_kernel<__half, 128, true>,         (const void*)lm_step_kernel<__half, 64, true>};
     for (const void* k : kernels) {
         const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
         if (e != cudaSuccess) return e;
