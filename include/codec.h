@@ -688,7 +688,8 @@ CODEC_API codec_status codec_lm_create(const codec_lm_config* cfg, codec_lm_t** 
 CODEC_API void codec_lm_destroy(codec_lm_t* lm);
 
 /* *bits: the CODEC_LM_ERR_* bits set since they were last cleared; clear != 0
- * clears them.  Synchronises stream.  Errors: CODEC_ERR_NULL, CODEC_ERR_CUDA. */
+ * clears them, and what a call that gave up on a wait left in the workspace.
+ * Synchronises stream.  Errors: CODEC_ERR_NULL, CODEC_ERR_CUDA. */
 CODEC_API codec_status codec_lm_errors(codec_lm_t* lm, uint32_t* bits, int32_t clear, void* stream);
 
 /*

@@ -108,6 +108,7 @@ struct LmSharedArgs {
     float* part;
     float* part_lse;
 };
+long long lm_shared_ctas(const LmShape& sh, const LmSharedArgs& a);
 cudaError_t launch_lm_shared(const LmShape& sh, const LmSharedArgs& a, cudaStream_t s);
 
 // Workspace of single-token attention.

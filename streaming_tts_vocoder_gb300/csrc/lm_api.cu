@@ -104,7 +104,10 @@ codec_status codec_lm_create(const codec_lm_config* cfg, codec_lm_t** out)
     const int64_t heads = (int64_t)c.max_requests * c.kv_heads;
     sp.chunk = 64;
     while ((sp.chunk < 512 && heads * ((positions + 2 * sp.chunk - 1) / (2 * sp.chunk)) >= 8 * 304) ||
-           positions > 64LL * sp.chunk)
+           positions > 64LL * sp.chunk ||
+           // and the partial results of full tables stay within 2 GB
+           (sp.chunk < positions && heads * (c.q_heads / c.kv_heads) * ((positions + sp.chunk - 1) / sp.chunk) *
+                                            c.head_dim > (1LL << 29)))
         sp.chunk *= 2;
     sp.max_splits = (int)((positions + sp.chunk - 1) / sp.chunk);
     // The shared part: 64 CTAs (the rest of the SMs stream the requests' own

@@ -57,7 +57,7 @@ constexpr int kThreads = 384;
 constexpr int kTile = 128;                  // rows of a query tile, keys of a K/V tile
 constexpr uint32_t kHalfBytes = kTile * 128;    // 64 columns of a tile: 128 rows of 128 bytes
 constexpr int kMaxStages = 8;
-constexpr uint32_t kPolls = 1u << 22;
+constexpr uint32_t kPolls = 1u << 26;         // a second or more: an item of 10^5 tiles takes a tenth of one
 constexpr int kNone = 0x7fffffff;
 constexpr int kSms = 152;
 
@@ -814,8 +814,10 @@ __global__ void __launch_bounds__(kThreads, 1) lm_prompt_kernel(const __grid_con
                 if (j == 0) {
                     ref = m == -INFINITY ? 0.f : m;
                 } else if (__any_sync(0xffffffffu, (m - ref) * p.c > 8.f)) {
-                    // the accumulator rests: its last product ran before these scores
-                    const float to_ref = fmaxf(ref, m), f = exp2_fast((ref - to_ref) * p.c);
+                    // Only the rows that need it move (times 1 changes nothing): a row's bits
+                    // do not depend on its neighbours.  The accumulator rests: its last
+                    // product ran before these scores.
+                    const float to_ref = (m - ref) * p.c > 8.f ? m : ref, f = exp2_fast((ref - to_ref) * p.c);
                     l *= f;
                     ref = to_ref;
 #pragma unroll 1
@@ -1278,6 +1280,18 @@ cudaError_t launch_lm_prompt(const LmShape& sh, const LmPromptArgs& a, cudaStrea
     return launch_any(sh, a.q, a.qs, a.keys, p, dim3(kSms), s, static_cast<int4*>(a.ws.list));
 }
 
+static dim3 shared_grid(const LmShape& sh, const LmSharedArgs& a)
+{
+    const int pair = 2 * (kTile / sh.group);
+    return dim3((a.B + pair - 1) / pair, sh.hk, (a.shared_len + a.split_len - 1) / a.split_len);
+}
+
+long long lm_shared_ctas(const LmShape& sh, const LmSharedArgs& a)
+{
+    const dim3 g = shared_grid(sh, a);
+    return (long long)g.x * g.y * g.z;
+}
+
 cudaError_t launch_lm_shared(const LmShape& sh, const LmSharedArgs& a, cudaStream_t s)
 {
     Params p{};
@@ -1288,8 +1302,7 @@ cudaError_t launch_lm_shared(const LmShape& sh, const LmSharedArgs& a, cudaStrea
     p.part_lse = a.part_lse;
     LmKeys ks = a.keys;
     ks.tables = a.shared_table;
-    const int pair = 2 * (kTile / sh.group);
-    const dim3 grid((a.B + pair - 1) / pair, sh.hk, (a.shared_len + a.split_len - 1) / a.split_len);
+    const dim3 grid = shared_grid(sh, a);
     return launch_any(sh, a.q, a.qs, ks, p, grid, s);
 }
 

@@ -33,7 +33,7 @@ constexpr int kConsumers = 4;
 constexpr int kThreads = 32 * (kConsumers + 1);
 constexpr int kKeys = 64;               // keys of a tile, 16 per consumer warp
 constexpr int kMaxStages = 6;
-constexpr uint32_t kPolls = 1u << 22;
+constexpr uint32_t kPolls = 1u << 25;
 constexpr uint32_t kHalf = kKeys * 128; // 64 columns of a tile
 
 struct Params {
@@ -576,12 +576,16 @@ cudaError_t launch(const LmShape& sh, const LmStepArgs& a, cudaStream_t s)
     p.o = a.o;
     p.os = a.os;
     p.lse = a.lse;
+    bool after_shared = false;
     if (p.shared_len > 0) {
         LmSharedArgs c{a.q, a.qs, a.B, ks, a.shared_table, p.shared_len, 0, a.ws.pre, a.ws.pre_lse};
         // splits by the object's shape and the shared length alone
         const int n = std::max(1, std::min(a.ws.pre_max, p.shared_len / 256));
         c.split_len = ((p.shared_len + n - 1) / n + 127) & ~127;
         p.n_pre = (p.shared_len + c.split_len - 1) / c.split_len;
+        // beside the shared part only while that one's CTAs all fit the GPU at once:
+        // then none of them can wait for an SM that this kernel's CTAs hold
+        after_shared = lm_shared_ctas(sh, c) <= 152;
         const cudaError_t e = launch_lm_shared(sh, c, s);
         if (e != cudaSuccess) return e;
     }
@@ -604,7 +608,7 @@ cudaError_t launch(const LmShape& sh, const LmStepArgs& a, cudaStream_t s)
     // a unit per request and head at least, and no more CTAs than the SMs hold at once
     const long long most = (long long)a.B * p.max_splits * sh.hk;
     const unsigned ctas = (unsigned)std::min<long long>(152 * per_sm, most);
-    p.after_shared = p.n_pre > 0;
+    p.after_shared = after_shared;
     // joined in this kernel where a CTA has one unit at most and needs no other kernel's results
     const bool join = most <= ctas && p.n_pre == 0, two = !join && (p.n_pre > 0 || p.max_splits > 1);
     p.taken = two ? a.ws.taken : nullptr;

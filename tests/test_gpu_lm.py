@@ -394,6 +394,115 @@ def test_step_result_does_not_depend_on_the_batch():
         assert torch.equal(o1[0], o[b])
 
 
+@pytest.mark.parametrize("hq,hk,d,dt", [(8, 2, 128, "bf16"), (4, 4, 64, "fp16")])
+def test_step_behind_many_shared_tiles_does_not_depend_on_the_batch(hq, hk, d, dt):
+    """Scores large enough that running references move in every tile: each
+    request's must move for its own sake alone."""
+    kv = [1100 + 37 * i for i in range(30)] + [700, 0, 3]
+    lm, q, kc, vc, own, shared, o = check_step(kv, 66, hq, hk, d, dt, 16, seed=5, mul=8.0)
+    for b in (0, 11, 29, 30, 32):
+        o1 = torch.zeros(1, hq, d, dtype=q.dtype, device="cuda")
+        lm.step(q[b:b + 1], kc, vc, i32(own[b:b + 1]), i32([kv[b]]), o1, shared_table=i32(shared))
+        assert torch.equal(o1[0], o[b])
+    back = list(range(len(kv)))[::-1]           # other neighbours, other order
+    o2 = torch.zeros_like(o)
+    lm.step(q[back], kc, vc, i32([own[b] for b in back]), i32([kv[b] for b in back]), o2, shared_table=i32(shared))
+    assert torch.equal(o2, o[back])
+
+
+def test_step_short_request_does_not_see_the_rest_of_the_shared_part():
+    kc, vc, tables, shared, n_blocks, width, gen = cache_case(7, [300, 300, 300], 2, 128, "bf16", 16, 12)
+    q = torch.randn(3, 4, 128, generator=gen, device="cuda").to(torch.bfloat16)
+    lm = C.Lm(4, 2, 128, n_blocks=n_blocks, table_blocks=width, max_requests=3, max_rows=3)
+    o, o2 = torch.zeros_like(q), torch.zeros_like(q)
+    lm.step(q, kc, vc, i32(tables), i32([50, 300, 130]), o, shared_table=i32(shared))
+    kc[shared[10]] = NAN
+    vc[shared[10], ::2] = float("inf")
+    vc[shared[10], 1::2] = NAN
+    lm.step(q, kc, vc, i32(tables), i32([50, 300, 130]), o2, shared_table=i32(shared))
+    assert torch.equal(o2[::2], o[::2]) and o2[1].isnan().all()
+
+
+def test_many_requests():
+    rng = random.Random(1)
+    check_prompt([rng.choice([0, 1, 2, 5, 9, 40]) for _ in range(700)], 4, 2, 64, "bf16")       # too many to sort
+    lens = [0] * 1000
+    for i in rng.sample(range(1000), 20):
+        lens[i] = rng.randrange(1, 5)
+    check_prompt(lens, 2, 2, 64, "fp16")        # fewer rows than requests
+    check_step([rng.choice([0, 1, 7, 90]) for _ in range(600)], 0, 2, 1, 64, "bf16", 16)
+    check_step([32 + rng.choice([0, 1, 7, 90]) for _ in range(1500)], 2, 2, 1, 64, "fp16", 16)
+
+
+def test_graph_of_prompts_follows_the_lengths():
+    """One captured call, replayed with other lengths in the same rows: packed
+    with a list of items, and behind the cache with pieces."""
+    q, k, v, _ = prompt_inputs(8, [3000], 4, 2, 64, "bf16", extra=0)
+    for paged in (False, True):
+        bs, width = 64, 60
+        lm = C.Lm(4, 2, 64, block_size=bs, n_blocks=60, table_blocks=width, max_requests=3, max_rows=3000)
+        eager = C.Lm(4, 2, 64, block_size=bs, n_blocks=60, table_blocks=width, max_requests=3, max_rows=3000)
+        gen = torch.Generator(device="cuda").manual_seed(0)
+        kc, vc = (torch.randn(60, bs, 2, 64, generator=gen, device="cuda").to(torch.bfloat16) for _ in range(2))
+        tables = torch.randint(60, (3, width), generator=gen, device="cuda", dtype=torch.int32)
+        rows, kv, o = i32([0, 0, 0, 0]), i32([0, 0, 0]), torch.zeros(3000, 4, 64, dtype=q.dtype, device="cuda")
+
+        def call(lm, o):
+            if paged:
+                lm.prompt_paged(q[:200], kc, vc, rows, tables, kv, o[:200])
+            else:
+                lm.prompt(q, k, v, rows, o)
+
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            call(lm, o)
+        for starts, lens in (([0, 1, 1, 100], [3000, 9, 3840]), ([0, 70, 71, 200], [70, 1, 2500]),
+                             ([0, 0, 0, 0], [5, 5, 5])):
+            rows.copy_(i32(starts))
+            kv.copy_(i32(lens))
+            want = torch.full_like(o, 3.0)
+            call(eager, want)
+            o.fill_(3.0)
+            graph.replay()
+            torch.cuda.synchronize()
+            assert torch.equal(o, want) and lm.errors() == 0 and eager.errors() == 0
+            assert (o[starts[-1]:] == 3).all() and not (o[:starts[-1]] == 3).all(-1).any()
+
+
+def test_cache_beyond_32_bits():
+    """Blocks whose elements lie past 2^32, and a slot to the last of them."""
+    hq, hk, d, bs = 16, 8, 128, 128
+    n_blocks = 2 ** 32 // (bs * hk * d) + 40
+    T = torch.bfloat16
+    kc, vc = (torch.empty(n_blocks, bs, hk, d, dtype=T, device="cuda") for _ in range(2))
+    kc[:8], vc[:8] = NAN, NAN                   # where a wrapped offset would read
+    ids = [n_blocks - 1, n_blocks - 30, n_blocks - 2]
+    gen = torch.Generator(device="cuda").manual_seed(4)
+    for i in ids:
+        for c in (kc, vc):
+            c[i] = torch.randn(bs, hk, d, generator=gen, device="cuda").to(T)
+    lm = C.Lm(hq, hk, d, block_size=bs, n_blocks=n_blocks, table_blocks=3, max_requests=2, max_rows=64)
+    x = (torch.randn(1, (hq + 2 * hk) * d, generator=gen, device="cuda")).to(T)
+    q, k, v = (t.unflatten(1, (-1, d)) for t in x.split([hq * d, hk * d, hk * d], 1))
+    qo = torch.zeros(1, hq, d, dtype=T, device="cuda")
+    last = n_blocks * bs - 1
+    lm.rotate(q, k, v, i32([0]), i32([last]), qo, kc, vc)       # position 0 turns by nothing
+    assert torch.equal(kc.view(-1, hk, d)[last], k[0]) and torch.equal(vc.view(-1, hk, d)[last], v[0])
+    kv, tables = [384, 200], [ids, ids]
+    ks, vs = (f64(c[ids].flatten(0, 1)) for c in (kc, vc))
+    q = torch.randn(12, hq, d, generator=gen, device="cuda").to(T)
+    o = torch.zeros_like(q)
+    lm.prompt_paged(q, kc, vc, i32([0, 10, 12]), i32(tables), i32(kv), o)
+    n = [375 + i for i in range(10)] + [199, 200]
+    ref = R.attention(f64(q), range(12), lambda r: (ks[:n[r]], vs[:n[r]]), hk, d ** -0.5)
+    R.assert_attention(o, None, ref, "bf16", n, d, 5.0)
+    for sh in (0, 1):
+        lm.step(q[:2], kc, vc, i32(tables), i32(kv), o[:2], shared_table=i32(ids[:sh]) if sh else None)
+        ref = R.attention(f64(q[:2]), range(2), lambda r: (ks[:kv[r]], vs[:kv[r]]), hk, d ** -0.5)
+        R.assert_attention(o[:2], None, ref, "bf16", kv, d, 5.0)
+    assert lm.errors() == 0
+
+
 def test_bad_blocks_read_as_zeros():
     """A table entry out of range: score 0 and value 0 for its positions, and the bit."""
     hq, hk, d, bs = 4, 2, 64, 16
