@@ -971,7 +971,7 @@ constexpr int kMinPiece = 6;
 
 __global__ void __launch_bounds__(kListThreads) lm_list_kernel(const Params p, int4* list)
 {
-    __shared__ int keys[kListSort];
+    __shared__ int keys[kListSort], row0[kListSort], nrow[kListSort];
     __shared__ unsigned short order[kLmMaxRequests];
     __shared__ int start[kLmMaxRequests + 1];
     __shared__ int warp_sum[3][kListThreads / 32];
@@ -1026,7 +1026,13 @@ __global__ void __launch_bounds__(kListThreads) lm_list_kernel(const Params p, i
     for (int b = tid; b < p.B; b += kListThreads) {
         int first, n;
         const int k = rows_and_keys(b, first, n, true);
-        if (sorted) keys[b] = n > 0 ? k : -1; else order[b] = (unsigned short)b;
+        if (sorted) {
+            keys[b] = n > 0 ? k : -1;
+            row0[b] = first;
+            nrow[b] = n;
+        } else {
+            order[b] = (unsigned short)b;
+        }
     }
     __syncthreads();
     if (sorted && tid < p.B) {
@@ -1039,7 +1045,7 @@ __global__ void __launch_bounds__(kListThreads) lm_list_kernel(const Params p, i
         const int x = base + tid;
         int tiles = 0, first, n;
         if (x < p.B) {
-            lm_rows(p.row_start, order[x], p.rows, first, n);
+            if (sorted) n = nrow[order[x]]; else lm_rows(p.row_start, order[x], p.rows, first, n);
             tiles = (n + pair - 1) / pair;
         }
         scan(&tiles, 1);
@@ -1054,9 +1060,15 @@ __global__ void __launch_bounds__(kListThreads) lm_list_kernel(const Params p, i
             const int mid = (lo + hi + 1) >> 1;
             if (start[mid] <= e) lo = mid; else hi = mid - 1;
         }
-        int first, n;
+        int first, n, k;
         const int b = order[lo];
-        const int k = rows_and_keys(b, first, n, false);
+        if (sorted) {
+            first = row0[b];
+            n = nrow[b];
+            k = keys[b];
+        } else {
+            k = rows_and_keys(b, first, n, false);
+        }
         const int t = (n + pair - 1) / pair - 1 - (e - start[lo]);
         rows = make_int4(b, first + t * pair, min(pair, n - t * pair), k - n + t * pair + 1);
         return (max(0, rows.w + rows.z - 1) + kTile - 1) / kTile;
@@ -1074,22 +1086,23 @@ __global__ void __launch_bounds__(kListThreads) lm_list_kernel(const Params p, i
         }
         return;
     }
-    unsigned long long mine = 0;
-    for (int e = tid; e < total; e += kListThreads) {
-        int4 rows;
-        mine += item(e, rows);
+    int4 rows = make_int4(0, 0, 0, 0);
+    int tiles = tid < total ? item(tid, rows) : 0;      // the first round's, kept
+    unsigned long long mine = tiles;
+    for (int e = tid + kListThreads; e < total; e += kListThreads) {
+        int4 other;
+        mine += item(e, other);
     }
     if (mine) atomicAdd(&work, mine);           // whole numbers: any order
-    __syncthreads();
-    const int share = (int)min(max((work * p.sh.hk + kSms - 1) / kSms, (unsigned long long)kMinPiece), 1ull << 24);
     if (tid < 3) carry[tid] = 0;
     __syncthreads();
+    const int share = (int)min(max((work * p.sh.hk + kSms - 1) / kSms, (unsigned long long)kMinPiece),
+                               1ull << 24);
     for (int base = 0; base < total; base += kListThreads) {
         const int e = base + tid;
-        int4 rows;
-        int tiles = 0, pieces = 0;
+        int pieces = 0;
         if (e < total) {
-            tiles = item(e, rows);
+            if (base > 0) tiles = item(e, rows);
             pieces = tiles > share + share / 4 ? (tiles + share / 2) / share : 1;
         }
         int v[3] = {pieces, pieces > 1 ? pieces * p.sh.hk : 0, pieces > 1 ? 1 : 0};
@@ -1265,8 +1278,9 @@ cudaError_t launch_lm_prompt(const LmShape& sh, const LmPromptArgs& a, cudaStrea
     p.lse = a.lse;
     // Pairs of query tiles: at most one partly filled pair per request.  Cutting
     // along the keys pays where items are few for the SMs and their keys may be
-    // many: 64 tokens behind 32,768 positions are otherwise eight items.  (It
-    // costs about 10 us: 16 paged prompts of 144 items, 58 us whole, took 67 cut.)
+    // many: 64 tokens behind 32,768 positions, eight items, take 44 us cut and 373
+    // whole.  It costs about 10 us: 16 paged prompts of 144 items take 57 us whole
+    // and 63 cut, with two pieces for each SM 69.
     const long long items = lm_list_items(a.rows, a.B, sh.group) * sh.hk;
     const bool cut = a.keys.tables ? items <= kSms && ((long long)a.keys.table_blocks << a.keys.bs_shift) > 2048
                                    : items <= 2 * kSms && a.rows > 2048;
