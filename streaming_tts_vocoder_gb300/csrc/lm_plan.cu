@@ -71,6 +71,8 @@ __global__ void __launch_bounds__(kPlanThreads) lm_plan_kernel(const LmPlanArgs 
     const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
     const bool first_cta = blockIdx.x == 0;
     const int most = a.table_blocks << a.bs_shift;
+    pdl_wait();
+    pdl_launch();
 
     const long long head = a.free_in[0], tail = a.free_in[1];
     const bool ring_ok = head >= 0 && tail >= head && tail - head <= a.n_blocks;
@@ -237,8 +239,7 @@ cudaError_t launch_lm_plan(const LmPlanArgs& a, cudaStream_t s)
 {
     const int ctas = min(152, (a.max_rows + kPlanRows - 1) / kPlanRows);
     const int vec = ((reinterpret_cast<uintptr_t>(a.slots) | reinterpret_cast<uintptr_t>(a.positions)) & 15) == 0;
-    lm_plan_kernel<<<ctas, kPlanThreads, lm_plan_smem(a.B), s>>>(a, vec);
-    return cudaGetLastError();
+    return launch_pdl(lm_plan_kernel, dim3(ctas), dim3(kPlanThreads), lm_plan_smem(a.B), s, a, vec);
 }
 
 }  // namespace codec

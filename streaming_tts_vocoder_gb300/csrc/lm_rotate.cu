@@ -163,6 +163,8 @@ __global__ void __launch_bounds__(kRotThreads, 5) lm_rotate_kernel(const LmRotat
     constexpr int kLanes = D / 16;
     const int warp = (int)((blockIdx.x * (long long)kRotThreads + threadIdx.x) >> 5);
     const int row = parts == 1 ? warp : warp / parts, part = warp - row * parts;
+    pdl_wait();
+    pdl_launch();
     if (row >= a.rows) return;
     const int lane = threadIdx.x & 31, c = (lane % kLanes) * 8;
     const int pos = __ldg(a.positions + row);
@@ -232,8 +234,8 @@ cudaError_t launch(const LmShape& sh, const LmRotateArgs& a, cudaStream_t s)
     // Up to eight rows per resident warp (five CTAs of four per SM) queries, keys
     // and values go to warps of their own: shorter warps leave a shorter tail.
     const unsigned kinds = a.rows < 8 * 152 * 20 ? (a.v ? 3 : 2) : 1;
-    lm_rotate_kernel<T, TI, D><<<dim3(ctas, kinds), kRotThreads, 0, s>>>(a, sh.hq, sh.hk, parts, sh.err);
-    return cudaGetLastError();
+    return launch_pdl(lm_rotate_kernel<T, TI, D>, dim3(ctas, kinds), dim3(kRotThreads), 0, s, a, sh.hq, sh.hk, parts,
+                      sh.err);
 }
 
 template <typename T>
