@@ -664,7 +664,7 @@ typedef struct codec_lm_config {
     int32_t head_dim;          /* 64 or 128 */
     int32_t block_size;        /* 16, 32, 64 or 128 positions */
     int32_t n_blocks;          /* blocks of a cache; n_blocks * block_size < 2^31 - 128 */
-    int32_t table_blocks;      /* width of a block table; table_blocks * block_size <= 2^30 */
+    int32_t table_blocks;      /* width of a block table; table_blocks * block_size <= 2^25 */
     int32_t max_requests;      /* per call, 1 .. 4096 */
     int32_t max_rows;          /* query rows per call, 1 .. 2^24 */
     int32_t max_positions;     /* positions the rotation knows (0: table_blocks * block_size) */
@@ -716,11 +716,12 @@ CODEC_API codec_status codec_lm_errors(codec_lm_t* lm, uint32_t* bits, int32_t c
  *              Where it is not 0 the request's blocks stay as they were.
  *   slots, positions  int32 [max_rows]: of each row; a row of a request that
  *              failed has slot -1, one behind the last request slot -1 and position 0.
- * All arrays device memory.  A repeated call with the same inputs writes the
+ * All arrays device memory; kv_len is neither len_before nor len_after (they
+ * are read while it is written).  A repeated call with the same inputs writes the
  * same outputs, in-place ones included.
  * Errors (nothing enqueued): CODEC_ERR_NULL (shared_table may be NULL when
  * shared_blocks is 0), CODEC_ERR_ARG (B or max_rows < 1, shared_blocks outside
- * [0, table_blocks], free_out == free_in), CODEC_ERR_CAPACITY (B or max_rows
+ * [0, table_blocks], free_out == free_in, kv_len one of the lengths), CODEC_ERR_CAPACITY (B or max_rows
  * above the object's); CODEC_ERR_CUDA if the launch fails.
  */
 CODEC_API codec_status codec_lm_plan(codec_lm_t* lm, const int32_t* len_before, const int32_t* len_after, int32_t B,
@@ -742,11 +743,11 @@ CODEC_API codec_status codec_lm_plan(codec_lm_t* lm, const int32_t* len_before, 
  *              slots NULL: row i goes to row i of k_dst, v_dst [rows][kv_heads]
  *              [head_dim], and v and v_dst may be NULL (values stay where they are).
  * q, k, v and the destinations 16-byte aligned, strides multiples of 16 bytes;
- * q_out may be q itself (of the object's type, stride q_heads * head_dim), else
- * nothing overlaps.
+ * q_out may be q itself (of the object's type, stride q_heads * head_dim), and
+ * without slots k_dst may be k and v_dst v in the same way; else nothing overlaps.
  * Errors: CODEC_ERR_NULL, CODEC_ERR_ARG (rows < 0, in_type, a stride below the
- * row or misaligned, one gain without the other), CODEC_ERR_CAPACITY (rows >
- * max_rows), CODEC_ERR_CUDA.
+ * row or misaligned, one gain without the other, another way in place), CODEC_ERR_CAPACITY
+ * (rows > max_rows), CODEC_ERR_CUDA.
  */
 CODEC_API codec_status codec_lm_rotate(codec_lm_t* lm, const void* q, int64_t q_stride, const void* k,
                                        int64_t k_stride, const void* v, int64_t v_stride, int32_t in_type,
@@ -766,8 +767,8 @@ CODEC_API codec_status codec_lm_rotate(codec_lm_t* lm, const void* q, int64_t q_
  * Pointers 16-byte aligned, strides multiples of 8 elements.  o overlaps
  * nothing else.  Scores, softmax statistics and sums are fp32; probabilities
  * are rounded to the object's type for their product with v.
- * Errors: CODEC_ERR_NULL, CODEC_ERR_ARG (B < 1, rows < 0, stride or alignment),
- * CODEC_ERR_CAPACITY, CODEC_ERR_CUDA.
+ * Errors: CODEC_ERR_NULL, CODEC_ERR_ARG (B < 1, rows < 0, stride or alignment, o an
+ * input), CODEC_ERR_CAPACITY, CODEC_ERR_CUDA.
  */
 CODEC_API codec_status codec_lm_prompt(codec_lm_t* lm, const void* q, int64_t q_stride, const void* k,
                                        int64_t k_stride, const void* v, int64_t v_stride, int32_t rows,
@@ -790,7 +791,7 @@ CODEC_API codec_status codec_lm_prompt_paged(codec_lm_t* lm, const void* q, int6
  * shared_table (int32 [shared_blocks], device) for every request - the entries
  * of tables for them are not read - and their keys and values are read once
  * for the whole batch.  A request's result does not depend on the others of
- * the batch.  Errors as codec_lm_prompt (CODEC_ERR_ARG also for shared_blocks
+ * the batch.  o overlaps nothing else.  Errors as codec_lm_prompt (CODEC_ERR_ARG also for shared_blocks
  * outside [0, table_blocks]).
  */
 CODEC_API codec_status codec_lm_step(codec_lm_t* lm, const void* q, int64_t q_stride, int32_t B, const void* k_cache,

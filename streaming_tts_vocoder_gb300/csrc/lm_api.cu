@@ -80,7 +80,7 @@ codec_status codec_lm_create(const codec_lm_config* cfg, codec_lm_t** out)
         c.q_heads / c.kv_heads > 16 ||
         (c.block_size != 16 && c.block_size != 32 && c.block_size != 64 && c.block_size != 128) || c.n_blocks < 1 ||
         (int64_t)c.n_blocks * c.block_size >= (1LL << 31) - 128 || c.table_blocks < 1 ||
-        (int64_t)c.table_blocks * c.block_size > (1LL << 30) || c.max_requests < 1 || c.max_requests > kLmMaxRequests ||
+        (int64_t)c.table_blocks * c.block_size > (1LL << 25) || c.max_requests < 1 || c.max_requests > kLmMaxRequests ||
         c.max_rows < 1 || c.max_rows > (1 << 24) || c.max_positions < 0 || c.max_positions > (1 << 30) ||
         (c.rope_pairs != 0 && c.rope_pairs != 1) || !(c.rope_theta > 1.f) || !std::isfinite(c.rope_theta) ||
         !(c.rms_eps >= 0.f) || !std::isfinite(c.rms_eps) || !(c.scale >= 0.f) || !std::isfinite(c.scale))
@@ -179,7 +179,8 @@ codec_status codec_lm_plan(codec_lm_t* lm, const int32_t* len_before, const int3
         !free_in || !free_out || !row_start || !kv_len || !status || !slots || !positions)
         return CODEC_ERR_NULL;
     const codec_lm_config& c = lm->cfg;
-    if (B < 1 || max_rows < 1 || shared_blocks < 0 || shared_blocks > c.table_blocks || free_in == free_out)
+    if (B < 1 || max_rows < 1 || shared_blocks < 0 || shared_blocks > c.table_blocks || free_in == free_out ||
+        kv_len == len_before || kv_len == len_after)
         return CODEC_ERR_ARG;
     if (B > c.max_requests || max_rows > c.max_rows) return CODEC_ERR_CAPACITY;
     OnDevice on(lm->device);
@@ -204,7 +205,9 @@ codec_status codec_lm_rotate(codec_lm_t* lm, const void* q, int64_t q_stride, co
         !row_ok(q, q_stride, nq, size) || !row_ok(k, k_stride, nk, size) ||
         (v && (!row_ok(v, v_stride, nk, size) || !aligned16(v_dst))) || !aligned16(q_out) || !aligned16(k_dst) ||
         (q_gain && (!aligned16(q_gain) || !aligned16(k_gain))) ||
-        (q == q_out && (in_type != c.type || q_stride != nq)))
+        (q == q_out && (in_type != c.type || q_stride != nq)) ||
+        (k == k_dst && (slots || in_type != c.type || k_stride != nk)) ||
+        (v && v == v_dst && (slots || in_type != c.type || v_stride != nk)))
         return CODEC_ERR_ARG;
     if (rows > c.max_rows) return CODEC_ERR_CAPACITY;
     if (rows == 0) return CODEC_OK;
@@ -224,7 +227,7 @@ codec_status codec_lm_prompt(codec_lm_t* lm, const void* q, int64_t q_stride, co
     const codec_lm_config& c = lm->cfg;
     const int64_t nq = (int64_t)c.q_heads * c.head_dim, nk = (int64_t)c.kv_heads * c.head_dim;
     if (B < 1 || rows < 0 || !row_ok(q, q_stride, nq, 2) || !row_ok(k, k_stride, nk, 2) ||
-        !row_ok(v, v_stride, nk, 2) || !row_ok(o, o_stride, nq, 2))
+        !row_ok(v, v_stride, nk, 2) || !row_ok(o, o_stride, nq, 2) || o == q || o == k || o == v)
         return CODEC_ERR_ARG;
     if (B > c.max_requests || rows > c.max_rows) return CODEC_ERR_CAPACITY;
     if (rows == 0) return CODEC_OK;
@@ -244,7 +247,7 @@ codec_status codec_lm_prompt_paged(codec_lm_t* lm, const void* q, int64_t q_stri
     const codec_lm_config& c = lm->cfg;
     const int64_t nq = (int64_t)c.q_heads * c.head_dim;
     if (B < 1 || rows < 0 || !row_ok(q, q_stride, nq, 2) || !aligned16(k_cache) || !aligned16(v_cache) ||
-        !row_ok(o, o_stride, nq, 2))
+        !row_ok(o, o_stride, nq, 2) || o == q || o == k_cache || o == v_cache)
         return CODEC_ERR_ARG;
     if (B > c.max_requests || rows > c.max_rows) return CODEC_ERR_CAPACITY;
     if (rows == 0) return CODEC_OK;
@@ -265,7 +268,8 @@ codec_status codec_lm_step(codec_lm_t* lm, const void* q, int64_t q_stride, int3
     const codec_lm_config& c = lm->cfg;
     const int64_t nq = (int64_t)c.q_heads * c.head_dim;
     if (B < 1 || shared_blocks < 0 || shared_blocks > c.table_blocks || !row_ok(q, q_stride, nq, 2) ||
-        !aligned16(k_cache) || !aligned16(v_cache) || !row_ok(o, o_stride, nq, 2))
+        !aligned16(k_cache) || !aligned16(v_cache) || !row_ok(o, o_stride, nq, 2) || o == q || o == k_cache ||
+        o == v_cache)
         return CODEC_ERR_ARG;
     if (B > c.max_requests) return CODEC_ERR_CAPACITY;
     OnDevice on(lm->device);

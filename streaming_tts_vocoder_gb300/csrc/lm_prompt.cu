@@ -57,7 +57,7 @@ constexpr int kThreads = 384;
 constexpr int kTile = 128;                  // rows of a query tile, keys of a K/V tile
 constexpr uint32_t kHalfBytes = kTile * 128;    // 64 columns of a tile: 128 rows of 128 bytes
 constexpr int kMaxStages = 8;
-constexpr uint32_t kPolls = 1u << 26;         // a second or more: an item of 10^5 tiles takes a tenth of one
+constexpr uint32_t kPolls = 1u << 26;         // a second or more; the longest table, 2^18 tiles, takes a fifth of one
 constexpr int kNone = 0x7fffffff;
 constexpr int kSms = 152;
 
@@ -75,7 +75,7 @@ struct Params {
     long long v_stride;
     const int4* list;           // items, two each (see Entry); null: by blockIdx
     int* counts;                // items of the list, items taken from it, items to join
-    int4* joins;                // of each: first query row, tokens, first slot, pieces
+    int4* joins;                // of each: first query row, tokens, first slot and pieces << 16, keys of the first token
     int split;                  // items may be cut along the keys
     float* piece;               // pieces' results: [slot][2 x 128 rows][D], normalised, fp32
     float* piece_lse;
@@ -272,7 +272,12 @@ __device__ void find_item(const Params& p, Shared& s)
         const int b = base + tid;
         int first = 0, n = 0, tiles = 0;
         if (b < p.B) {
-            if (!lm_rows(p.row_start, b, p.rows, first, n) && report) atomicOr(p.sh.err, CODEC_LM_ERR_LENGTH);
+            bool good = lm_rows(p.row_start, b, p.rows, first, n);
+            if (report && p.tables) {
+                int keys = __ldg(p.kv_len + b);
+                good &= lm_clamp_len(keys, (long long)p.table_blocks << p.bs_shift);
+            }
+            if (report && !good) atomicOr(p.sh.err, CODEC_LM_ERR_LENGTH);
             tiles = (n + pair - 1) / pair;
         }
         int incl = tiles;
@@ -298,8 +303,7 @@ __device__ void find_item(const Params& p, Shared& s)
             int keys = n;
             if (p.tables) {
                 keys = __ldg(p.kv_len + b);
-                if (!lm_clamp_len(keys, (long long)p.table_blocks << p.bs_shift))
-                    atomicOr(p.sh.err, CODEC_LM_ERR_LENGTH);
+                lm_clamp_len(keys, (long long)p.table_blocks << p.bs_shift);
             }
             s.item.first = keys - n + t * pair + 1;
             s.found = 1;
@@ -812,7 +816,8 @@ __global__ void __launch_bounds__(kThreads, 1) lm_prompt_kernel(const __grid_con
                 m1 = max3(m1, x[126], x[127]);
                 const float m = max3(fmaxf(m0, m1), m2, m3);
                 if (j == 0) {
-                    ref = m == -INFINITY ? 0.f : m;
+                    // scores of -inf alone so far: below whatever comes
+                    ref = m == -INFINITY ? -1e30f : m;
                 } else if (__any_sync(0xffffffffu, (m - ref) * p.c > 8.f)) {
                     // Only the rows that need it move (times 1 changes nothing): a row's bits
                     // do not depend on its neighbours.  The accumulator rests: its last
@@ -1116,7 +1121,8 @@ __global__ void __launch_bounds__(kListThreads) lm_list_kernel(const Params p, i
             list[2 * (v[0] + c)] = live ? rows : make_int4(rows.x, rows.y, 0, 0);
             list[2 * (v[0] + c) + 1] = cut && live ? make_int4(c * len, len, v[1] + c * p.sh.hk, 0) : make_int4(0, kNone, -1, 0);
         }
-        if (pieces > 1) p.joins[v[2]] = make_int4(rows.y, cut ? rows.z : 0, v[1], cut ? (tiles + len - 1) / len : 0);
+        if (pieces > 1)
+            p.joins[v[2]] = make_int4(rows.y, cut ? rows.z : 0, v[1] | (cut ? (tiles + len - 1) / len : 0) << 16, rows.w);
     }
     if (tid == 0) {
         p.counts[0] = carry[0];
@@ -1142,13 +1148,11 @@ __global__ void __launch_bounds__(kPieceThreads, 4) lm_pieces_kernel(const __gri
         const int4 j = __ldcg(p.joins + y / p.sh.hk);
         const int i = r / kTile, in = r % kTile, tok = i * p.tokens + in / group;
         if (in >= p.tokens * group || tok >= j.y) continue;
-        auto row_of = [&](int c) { return (long long)(j.z + c * p.sh.hk + hk) * 2 * kTile + r; };
+        auto row_of = [&](int c) { return (long long)((j.z & 0xffff) + c * p.sh.hk + hk) * 2 * kTile + r; };
         constexpr int kE = D / 32;
         float v[kE], lse;
-        // a row that sees nothing has an lse of -inf in every piece; its first piece holds key 0 of all others
-        const bool empty = __ldcg(p.piece_lse + row_of(0)) == -INFINITY;
         join_row<kE, 4>(
-            j.w, empty, [&](int c) { return __ldcg(p.piece_lse + row_of(c)); },
+            j.z >> 16, j.w + tok <= 0, [&](int c) { return __ldcg(p.piece_lse + row_of(c)); },
             [&](int c, float* f) { row_part<kE>(p.piece + row_of(c) * D, f); }, v, lse);
         const long long row = j.x + tok;
         const int h = hk * group + in % group;

@@ -736,3 +736,87 @@ def test_refusals():
         assert e.value.status == 2, bad
     with pytest.raises(ValueError):
         C.Lm(4, 2, 64, "fp32")
+
+
+# ---- places that a user may share, and scores without a finite one -----------
+
+def test_outputs_in_place_are_refused_or_right():
+    lm = C.Lm(4, 2, 64, block_size=16, n_blocks=4, table_blocks=3, max_requests=2, max_rows=8)
+    T = torch.bfloat16
+    x = torch.randn(8, 8, 64, device="cuda").to(T)
+    q, k, v = x[:, :4].contiguous(), x[:, 4:6].contiguous(), x[:, 6:].contiguous()
+    kc = torch.zeros(4, 16, 2, 64, dtype=T, device="cuda")
+    before, after, kv = i32([0, 0]), i32([4, 4]), i32([0, 0])
+    pos, slots = i32(list(range(8))), i32(list(range(8)))
+    free = torch.tensor([0, 4], device="cuda")
+    for a, b, c in ((before, after, before), (before, after, after), (kv, kv, kv)):
+        with pytest.raises(C.CodecError) as e:
+            lm.plan(a, b, i32([[0] * 3] * 2), i32(range(4)), free, free.clone(), i32([0] * 3), c, i32([0] * 2),
+                    i32([0] * 8), i32([0] * 8))
+        assert e.value.status == 4
+    square = C.Lm(2, 2, 64, block_size=16, n_blocks=4, table_blocks=3, max_requests=2, max_rows=8)
+    rs, tb = i32([0, 4, 8]), i32([[0] * 3] * 2)
+    for call in (lambda: lm.prompt(q, k, v, rs, q), lambda: square.prompt(q[:, :2].contiguous(), k, v, rs, k),
+                 lambda: square.prompt(q[:, :2].contiguous(), k, v, rs, v),
+                 lambda: lm.prompt_paged(q, kc, kc, rs, tb, i32([8, 8]), q),
+                 lambda: lm.step(q[:2], kc, kc, tb, i32([8, 8]), q[:2]),
+                 lambda: lm.rotate(q, kc.view(-1, 2, 64)[:8], v, pos, slots, torch.empty_like(q), kc, kc.clone()),
+                 lambda: lm.rotate(q, k, kc.view(-1, 2, 64)[:8], pos, slots, torch.empty_like(q), kc.clone(), kc)):
+        with pytest.raises(C.CodecError) as e:
+            call()
+        assert e.value.status == 4
+    # without slots in place
+    qo, ko, vo = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
+    lm.rotate(q, k, v, pos, None, qo, ko, vo)
+    lm.rotate(q, k, v, pos, None, q, k, v)
+    assert torch.equal(q, qo) and torch.equal(k, ko) and torch.equal(v, vo)
+    for bad in (dict(table_blocks=2 ** 21 + 1, n_blocks=4, block_size=16),):
+        with pytest.raises(C.CodecError) as e:
+            C.Lm(4, 2, 64, **bad)
+        assert e.value.status == 2
+
+
+def test_length_out_of_range_is_told_without_rows_too():
+    lm = C.Lm(4, 2, 64, block_size=16, n_blocks=4, table_blocks=3, max_requests=2, max_rows=8)
+    q = torch.zeros(8, 4, 64, dtype=torch.bfloat16, device="cuda")
+    kc = torch.zeros(4, 16, 2, 64, dtype=torch.bfloat16, device="cuda")
+    lm.prompt_paged(q, kc, kc, i32([0, 8, 8]), i32([[0] * 3] * 2), i32([8, 49]), torch.zeros_like(q))
+    assert lm.errors() == C.LM_ERR_LENGTH
+
+
+@pytest.mark.parametrize("n,hq,hk,d,cut", [(300, 4, 2, 128, False), (2100, 4, 1, 64, True)])
+def test_scores_of_minus_infinity_have_no_weight(n, hq, hk, d, cut):
+    """Keys that score -inf for every row, more than a tile of them, in front of
+    keys whose scores lie far below zero: only the latter count."""
+    T, skip, bs = torch.bfloat16, 130, 16
+    gen = torch.Generator(device="cuda").manual_seed(n)
+    r = lambda *s: torch.randn(*s, generator=gen, device="cuda")
+    q = (2 + 0.1 * r(n, hq, d)).to(T)
+    k, v = (-12 + 0.1 * r(n, hk, d)).to(T), r(n, hk, d).to(T)
+    k[:skip] = -float("inf")
+    k6, v6 = f64(k), f64(v)
+
+    def check(o, rows):         # rows: of q
+        ref = R.attention(f64(q)[rows], range(len(rows)), lambda i: (k6[skip:rows[i] + 1], v6[skip:rows[i] + 1]), hk, d ** -0.5)
+        R.assert_attention(o, None, ref, "bf16", [x + 1 for x in rows], d, 5.0)
+
+    blocks = -(-n // bs)
+    lm = C.Lm(hq, hk, d, block_size=bs, n_blocks=blocks, table_blocks=blocks, max_requests=3, max_rows=n)
+    rows = list(range(skip, n)) if not cut else list(range(skip, n, 61))
+    o, o2 = torch.zeros_like(q), torch.zeros_like(q)
+    lm.prompt(q, k, v, i32([0, n]), o)
+    check(o[rows], rows)
+    assert o[:skip].isnan().all()
+    kc, vc = (torch.zeros(blocks, bs, hk, d, dtype=T, device="cuda") for _ in range(2))
+    kc.view(-1, hk, d)[:n], vc.view(-1, hk, d)[:n] = k, v
+    table = i32([list(range(blocks))])
+    lm.prompt_paged(q, kc, vc, i32([0, n]), table, i32([n]), o2)
+    check(o2[rows], rows)
+    three = i32([n - 1, n - 100, skip])
+    for shared in (None, table[0, :10].contiguous()):
+        o3 = torch.zeros(3, hq, d, dtype=T, device="cuda")
+        qs = q[[n - 2, n - 101, skip - 1]].contiguous()
+        lm.step(qs, kc, vc, table.expand(3, -1).contiguous(), three, o3, shared_table=shared)
+        check(o3[:2], [n - 2, n - 101])
+        assert o3[2].isnan().all()
+    assert lm.errors() == 0
