@@ -96,14 +96,22 @@ codec_status codec_lm_create(const codec_lm_config* cfg, codec_lm_t** out)
     lm->cfg = c;
     lm->device = dev;
     while ((1 << lm->bs_shift) < c.block_size) lm->bs_shift++;
-    // Single tokens: splits of 64 positions, of up to 512 as long as the largest
-    // batch over full tables still makes eight for every CTA that fits the GPU,
-    // and of as many as leave a full table 64.
+    // Single tokens: splits of 64 positions, of up to 256 as long as the largest
+    // batch over full tables still makes one for every CTA that fits the GPU (304),
+    // of up to 512 as long as it makes eight, and of as many as leave a full table
+    // 64.  A split costs about 2 us whatever it holds, an idle SM more: 16 requests
+    // of 3,000 to 4,000 positions take 47 us in splits of 256 and 52 in 128, 64 of up
+    // to 500 behind a shared part 17.5 in 256 and 19 in 512.  Tables of up to 512
+    // positions are not split where the requests' heads alone occupy most SMs, and
+    // then nothing is joined: 64 requests of 200 to 250 positions 12.7 us, in
+    // splits of 64 22.4.
     LmStepSpace& sp = lm->step;
     const int64_t positions = (int64_t)c.table_blocks * c.block_size;
     const int64_t heads = (int64_t)c.max_requests * c.kv_heads;
     sp.chunk = 64;
-    while ((sp.chunk < 512 && heads * ((positions + 2 * sp.chunk - 1) / (2 * sp.chunk)) >= 8 * 304) ||
+    if (heads >= 152 && positions <= 512) sp.chunk = 512;
+    while ((sp.chunk < 512 && heads * ((positions + 2 * sp.chunk - 1) / (2 * sp.chunk)) >=
+                                  (sp.chunk < 256 ? 1 : 8) * 304) ||
            positions > 64LL * sp.chunk ||
            // and the partial results of full tables stay within 2 GB
            (sp.chunk < positions && heads * (c.q_heads / c.kv_heads) * ((positions + sp.chunk - 1) / sp.chunk) *
