@@ -5,6 +5,8 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include <algorithm>
+
 #include "codec.h"
 #include "common.cuh"
 
@@ -112,10 +114,19 @@ long long lm_shared_ctas(const LmShape& sh, const LmSharedArgs& a);
 cudaError_t launch_lm_shared(const LmShape& sh, const LmSharedArgs& a, cudaStream_t s);
 
 // Workspace of single-token attention.
+// Splits of a shared part of `len` positions whose every split takes `ctas`: 256
+// positions at least while all of them make at most 64 CTAs (the rest of the SMs
+// stream the requests' own parts meanwhile), 128 while they make at most 32.
+// 64 CTAs of one tile each: 1,024 positions, 8 heads 23.5 us, 32 of two 18.8.
+inline int lm_shared_splits(long long ctas, long long len)
+{
+    const long long wide = std::min<long long>({32, 64 / ctas, len / 256}), narrow = std::min<long long>({8, 32 / ctas, len / 128});
+    return (int)std::max<long long>({1, wide, narrow});
+}
 struct LmStepSpace {
     int chunk;                      // positions per split of a request's own part
     int max_splits;                 // splits of a full table
-    int pre_max;                    // splits of the shared part at most
+    int shared_ctas;                // of each split of the shared part, with max_requests
     float *part, *part_lse;         // [max_requests][max_splits][hq][D], [..][hq]
     float *pre, *pre_lse;           // [pre_max][max_requests][hq][D], [..][hq]
     int* done;                      // [max_requests][hk], zero between calls

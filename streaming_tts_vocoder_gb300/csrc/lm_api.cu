@@ -118,11 +118,11 @@ codec_status codec_lm_create(const codec_lm_config* cfg, codec_lm_t** out)
                                             c.head_dim > (1LL << 29)))
         sp.chunk *= 2;
     sp.max_splits = (int)((positions + sp.chunk - 1) / sp.chunk);
-    // The shared part: 64 CTAs (the rest of the SMs stream the requests' own
-    // parts meanwhile), by the largest batch, so that the actual one changes no bits.
+    // The shared part's splits: by the largest batch, so that the actual one changes no bits.
     const int tokens = 2 * (128 / (c.q_heads / c.kv_heads));
     const int64_t pairs = (c.max_requests + tokens - 1) / tokens;
-    sp.pre_max = (int)std::max<int64_t>(1, std::min<int64_t>({32, 64 / (pairs * c.kv_heads), positions / 256}));
+    sp.shared_ctas = (int)(pairs * c.kv_heads);
+    const int pre_max = lm_shared_splits(sp.shared_ctas, positions);
     LmPromptSpace& pr = lm->prompt;
     const size_t items = (size_t)lm_list_items(c.max_rows, c.max_requests, c.q_heads / c.kv_heads) + kLmSlots;
     const size_t row = (size_t)c.max_requests * c.q_heads;
@@ -130,8 +130,8 @@ codec_status codec_lm_create(const codec_lm_config* cfg, codec_lm_t** out)
         cudaMalloc(&lm->err, sizeof(unsigned)) != cudaSuccess ||
         cudaMalloc(&sp.part, sizeof(float) * row * sp.max_splits * c.head_dim) != cudaSuccess ||
         cudaMalloc(&sp.part_lse, sizeof(float) * row * sp.max_splits) != cudaSuccess ||
-        cudaMalloc(&sp.pre, sizeof(float) * row * sp.pre_max * c.head_dim) != cudaSuccess ||
-        cudaMalloc(&sp.pre_lse, sizeof(float) * row * sp.pre_max) != cudaSuccess ||
+        cudaMalloc(&sp.pre, sizeof(float) * row * pre_max * c.head_dim) != cudaSuccess ||
+        cudaMalloc(&sp.pre_lse, sizeof(float) * row * pre_max) != cudaSuccess ||
         cudaMalloc(&pr.list, 32 * items) != cudaSuccess || cudaMalloc(&pr.counts, 3 * sizeof(int)) != cudaSuccess ||
         cudaMalloc(&pr.joins, 16 * kLmSlots) != cudaSuccess ||
         cudaMalloc(&pr.piece, sizeof(float) * kLmSlots * 256 * c.head_dim) != cudaSuccess ||

@@ -594,7 +594,7 @@ cudaError_t launch(const LmShape& sh, const LmStepArgs& a, cudaStream_t s)
     if (p.shared_len > 0) {
         LmSharedArgs c{a.q, a.qs, a.B, ks, a.shared_table, p.shared_len, 0, a.ws.pre, a.ws.pre_lse};
         // splits by the object's shape and the shared length alone
-        const int n = std::max(1, std::min(a.ws.pre_max, p.shared_len / 256));
+        const int n = lm_shared_splits(a.ws.shared_ctas, p.shared_len);
         c.split_len = ((p.shared_len + n - 1) / n + 127) & ~127;
         p.n_pre = (p.shared_len + c.split_len - 1) / c.split_len;
         // beside the shared part only while that one's CTAs all fit the GPU at once:
