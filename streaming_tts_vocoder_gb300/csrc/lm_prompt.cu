@@ -520,26 +520,21 @@ __global__ void __launch_bounds__(kThreads, 1) lm_prompt_kernel(const __grid_con
             bool ok = true;
             Entry entry{};
             int entry_hk = -1;
-            const int count = p.list ? __ldcg(p.counts) * p.sh.hk : 0;
-            auto fetch = [&](int w) {
-                entry_hk = -1;
-                if (w < count) {
-                    entry_hk = w % p.sh.hk;
-                    entry.rows = __ldg(p.list + 2 * (w / p.sh.hk));
-                    entry.keys = __ldg(p.list + 2 * (w / p.sh.hk) + 1);
-                }
+            int count = 0, taken = 0;                   // taken: lane 0's, from the counter
+            auto fetch = [&](int w) {                   // the list has room for a grid of items
+                entry_hk = w % p.sh.hk;
+                entry.rows = __ldg(p.list + 2 * (w / p.sh.hk));
+                entry.keys = __ldg(p.list + 2 * (w / p.sh.hk) + 1);
             };
-            if (p.list) fetch(blockIdx.x);
+            if (p.list) {
+                count = __ldcg(p.counts) * p.sh.hk;
+                fetch(blockIdx.x);
+                if ((int)blockIdx.x >= count) entry_hk = -1;
+            }
             while (ok) {
                 const Item* const item = walk.hand_out(p, s, entry, entry_hk, lane);
                 if (!item) break;
                 const Item& it = *item;
-                // the next one: needed when this one's copies are out
-                if (p.list) {
-                    int w = 0;
-                    if (lane == 0) w = atomicAdd(p.counts + 1, 1) + gridDim.x;
-                    fetch(__shfl_sync(0xffffffffu, w, 0));
-                }
                 const int n_max = max(it.n[0], it.n[1]);
                 const int first_masked = it.free_from / kTile;
                 const int* table = nullptr;
@@ -564,6 +559,8 @@ __global__ void __launch_bounds__(kThreads, 1) lm_prompt_kernel(const __grid_con
                     }
                     __syncwarp();
                 }
+                // the next item: taken while this one's first copies are on their way
+                if (p.list && lane == 0) taken = atomicAdd(p.counts + 1, 1) + gridDim.x;
                 for (int j = 0; j < n_max && ok; j++) {
                     int id = next;
                     const int here = p.tables ? min(per, blocks - j * per) : 1;
@@ -608,6 +605,11 @@ __global__ void __launch_bounds__(kThreads, 1) lm_prompt_kernel(const __grid_con
                             ph ^= 1u;
                         }
                     }
+                }
+                if (p.list) {
+                    taken = __shfl_sync(0xffffffffu, taken, 0);
+                    entry_hk = -1;
+                    if (taken < count) fetch(taken);
                 }
             }
             // every last load has landed before the CTA can end
