@@ -57,7 +57,7 @@ constexpr int kThreads = 384;
 constexpr int kTile = 128;                  // rows of a query tile, keys of a K/V tile
 constexpr uint32_t kHalfBytes = kTile * 128;    // 64 columns of a tile: 128 rows of 128 bytes
 constexpr int kMaxStages = 8;
-constexpr uint32_t kPolls = 1u << 26;         // a second or more; the longest table, 2^18 tiles, takes a fifth of one
+constexpr uint32_t kPolls = 1u << 20;         // 1.5 us each where nothing arrives; the longest table, 2^18 tiles, takes 0.4 s
 constexpr int kNone = 0x7fffffff;
 constexpr int kSms = 152;
 

@@ -33,7 +33,7 @@ constexpr int kConsumers = 4;
 constexpr int kThreads = 32 * (kConsumers + 1);
 constexpr int kKeys = 64;               // keys of a tile, 16 per consumer warp
 constexpr int kMaxStages = 6;
-constexpr uint32_t kPolls = 1u << 25;
+constexpr uint32_t kPolls = 1u << 20;   // 1.5 us each where nothing arrives
 constexpr uint32_t kHalf = kKeys * 128; // 64 columns of a tile
 
 struct Params {
@@ -334,20 +334,26 @@ __global__ void __launch_bounds__(kThreads, 2) lm_step_kernel(const __grid_const
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break;
                 uint8_t* dst = smem + (size_t)st * pitch;
-                if (lane == 0) {
+                // one thread issues them all (lanes that each issue their own take turns)
+                int rows[4];
+#pragma unroll
+                for (int b = 0; b < 4; b++) rows[b] = __shfl_sync(0xffffffffu, row, b);
+                if (elect_one()) {
                     const uint32_t q_bytes = j == 0 && here > 0 ? group * D * 2 : 0;
                     if (j == 0)
                         unit_of[st] = make_int4(u < 0 ? -1 : n.b | (n.empty ? 1 << 30 : 0), n.hk, n.split | n.n_splits << 16, n.keys);
                     mbar_expect_tx(&full[st], (uint32_t)(here << box_shift) * D * 4 + q_bytes);
                     if (q_bytes) bulk_load(dst + 2 * kTileBytes, q, &full[st], q_bytes);
+#pragma unroll
+                    for (int b = 0; b < 4; b++)
+                        if (b < here)
+                            for (int h = 0; h < D / 64; h++) {
+                                const uint32_t at = h * kHalf + ((uint32_t)b << box_shift) * 128;
+                                tma_load_3d(dst + at, &mk, &full[st], h * 64, n.hk, rows[b]);
+                                tma_load_3d(dst + kTileBytes + at, &mv, &full[st], h * 64, n.hk, rows[b]);
+                            }
                 }
                 __syncwarp();
-                if (lane < here)
-                    for (int h = 0; h < D / 64; h++) {
-                        const uint32_t at = h * kHalf + ((uint32_t)lane << box_shift) * 128;
-                        tma_load_3d(dst + at, &mk, &full[st], h * 64, n.hk, row);
-                        tma_load_3d(dst + kTileBytes + at, &mv, &full[st], h * 64, n.hk, row);
-                    }
                 loads++;
                 if (++st == p.stages) {
                     st = 0;
