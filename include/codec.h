@@ -789,8 +789,8 @@ CODEC_API codec_status codec_lm_prompt_paged(codec_lm_t* lm, const void* q, int6
  * request b (its own among them); kv_len[b] == 0: zeros, lse -inf.
  * shared_blocks > 0: positions below shared_blocks * block_size are those of
  * shared_table (int32 [shared_blocks], device) for every request - the entries
- * of tables for them are not read - and their keys and values are read once
- * for the whole batch.  A request's result does not depend on the others of
+ * of tables for them are not read - and where they are many their scores and
+ * sums are computed for the whole batch at once.  A request's result does not depend on the others of
  * the batch.  o overlaps nothing else.  Errors as codec_lm_prompt (CODEC_ERR_ARG also for shared_blocks
  * outside [0, table_blocks]).
  */

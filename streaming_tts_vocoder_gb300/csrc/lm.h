@@ -127,6 +127,7 @@ struct LmStepSpace {
     int chunk;                      // positions per split of a request's own part
     int max_splits;                 // splits of a full table
     int shared_ctas;                // of each split of the shared part, with max_requests
+    long long heads;                // max_requests x kv_heads
     float *part, *part_lse;         // [max_requests][max_splits][hq][D], [..][hq]
     float *pre, *pre_lse;           // [pre_max][max_requests][hq][D], [..][hq]
     int* done;                      // [max_requests][hk], zero between calls

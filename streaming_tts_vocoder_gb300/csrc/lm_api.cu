@@ -122,6 +122,7 @@ codec_status codec_lm_create(const codec_lm_config* cfg, codec_lm_t** out)
     const int tokens = 2 * (128 / (c.q_heads / c.kv_heads));
     const int64_t pairs = (c.max_requests + tokens - 1) / tokens;
     sp.shared_ctas = (int)(pairs * c.kv_heads);
+    sp.heads = heads;
     const int pre_max = lm_shared_splits(sp.shared_ctas, positions);
     LmPromptSpace& pr = lm->prompt;
     const size_t items = (size_t)lm_list_items(c.max_rows, c.max_requests, c.q_heads / c.kv_heads) + kLmSlots;

@@ -44,6 +44,8 @@ struct Params {
     const int* tables;
     const int* kv_len;
     int table_blocks, bs_shift, n_blocks;
+    const int* lead;                    // a short shared part: the blocks of the first lead_len positions
+    int lead_len;
     int shared_len, n_pre;              // shared part: length, partial results of it
     int chunk, max_splits;
     int stages;
@@ -314,7 +316,10 @@ __global__ void __launch_bounds__(kThreads, 2) lm_step_kernel(const __grid_const
             const T* q = static_cast<const T*>(p.q) + n.b * p.qs + (long long)n.hk * group * D;
             auto boxes = [&](int j) { return max(0, min(per, (n.keys - j * kKeys + (1 << box_shift) - 1) >> box_shift)); };
             auto position = [&](int j) { return n.key0 + j * kKeys + (lane << box_shift); };
-            auto block = [&](int j) { return lane < boxes(j) ? __ldcg(table + (position(j) >> p.bs_shift)) : 0; };
+            auto block = [&](int j) {
+                const int pos = position(j);
+                return lane < boxes(j) ? __ldcg((pos < p.lead_len ? p.lead : table) + (pos >> p.bs_shift)) : 0;
+            };
             int id_ahead = block(0);
             // a unit without keys, and the end, take a stage without copies
             for (int j = 0; j == 0 || j * kKeys < n.keys; j++) {
@@ -597,6 +602,17 @@ cudaError_t launch(const LmShape& sh, const LmStepArgs& a, cudaStream_t s)
     p.os = a.os;
     p.lse = a.lse;
     bool after_shared = false;
+    // A short shared part is read by every request, from L2 for all but the first:
+    // no second kernel, and nothing to join with.  Device time as a part of its own
+    // and so: 3 requests, 1 head, 32 positions 10.4 and 7.4 us; 32, 8, 256 11.7 and
+    // 9.4; 32, 1, 1,024 14.6 and 11.0; but 16, 8, 512 11.9 and 13.5; 8, 1, 4,096 13.8
+    // and 18.8.  By the largest batch, so that the actual one changes no bits.
+    const long long most_short = p.shared_len <= 256 ? 65536 : p.shared_len <= 1024 ? 32768 : 0;
+    if (a.ws.heads == sh.hk || a.ws.heads * p.shared_len <= most_short) {
+        p.lead = a.shared_table;
+        p.lead_len = p.shared_len;
+        p.shared_len = 0;
+    }
     if (p.shared_len > 0) {
         LmSharedArgs c{a.q, a.qs, a.B, ks, a.shared_table, p.shared_len, 0, a.ws.pre, a.ws.pre_lse};
         // splits by the object's shape and the shared length alone

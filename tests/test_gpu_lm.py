@@ -820,3 +820,57 @@ def test_scores_of_minus_infinity_have_no_weight(n, hq, hk, d, cut):
         check(o3[:2], [n - 2, n - 101])
         assert o3[2].isnan().all()
     assert lm.errors() == 0
+
+
+@pytest.mark.parametrize("kv,sh,bs,hq,hk", [
+    ([700], 40, 16, 4, 2),                                  # one request shares with nobody: many blocks read as its own
+    ([2000, 10, 1030, 0, 33], 64, 16, 4, 1),                # up to 1,024 shared positions of few heads
+    ([300] * 20 + [100, 256, 257, 0, 255], 2, 128, 8, 2),   # short shared part
+    ([260 + i for i in range(40)], 16, 16, 16, 8),          # one more head, and it is a part of its own
+    ([520 + i for i in range(17)], 32, 16, 8, 4),
+])
+def test_step_short_and_long_shared_parts(kv, sh, bs, hq, hk):
+    lm, q, kc, vc, own, shared, o = check_step(kv, sh, hq, hk, 128, "bf16", bs, seed=len(kv))
+    check_step(kv, sh, hq, hk, 64, "fp16", bs, seed=len(kv) + 1, mul=4.0)
+    b = len(kv) // 2
+    o1 = torch.zeros(1, hq, 128, dtype=q.dtype, device="cuda")
+    lm.step(q[b:b + 1], kc, vc, i32(own[b:b + 1]), i32([kv[b]]), o1, shared_table=i32(shared))
+    assert torch.equal(o1[0], o[b])
+    # a block of the shared part that is none reads as zeros wherever it is read from
+    wrong = list(shared)
+    wrong[0] = -1
+    kc2, vc2 = kc.clone(), vc.clone()
+    kc2[shared[0]], vc2[shared[0]] = 0, 0
+    o2, o3 = torch.zeros_like(o), torch.zeros_like(o)
+    lm.step(q, kc, vc, i32(own), i32(kv), o2, shared_table=i32(wrong))
+    assert lm.errors() == C.LM_ERR_BLOCK
+    lm.step(q, kc2, vc2, i32(own), i32(kv), o3, shared_table=i32(shared))
+    assert torch.equal(o2, o3) and lm.errors() == 0
+
+
+@pytest.mark.parametrize("B,width", [(1, 1), (33, 1), (153, 30), (1025, 2), (1100, 40), (4096, 2)])
+def test_step_many_requests_of_few_positions(B, width):
+    """Units are looked up 32 requests at a time: one, two and three rounds of it,
+    with tables that are split and tables that are not."""
+    rng = random.Random(B)
+    kv = [rng.choice([0, 1, 15, 16, 17, width * 16]) if rng.random() < 0.2 else rng.randrange(1, 30) % (width * 16 + 1)
+          for _ in range(B)]
+    n_blocks, d = 64, 64
+    gen = torch.Generator(device="cuda").manual_seed(B)
+    kc, vc = (torch.randn(n_blocks, 16, 2, d, generator=gen, device="cuda").to(torch.bfloat16) for _ in range(2))
+    tables = [[rng.randrange(n_blocks) for _ in range(width)] for _ in range(B)]     # requests may share blocks
+    q = (torch.randn(B, 4, d, generator=gen, device="cuda") * 1.5).to(torch.bfloat16)
+    lm = C.Lm(4, 2, d, n_blocks=n_blocks, table_blocks=width, max_requests=B, max_rows=B)
+    o, lse = torch.full_like(q, 5.0), torch.full((B, 4), 5.0, device="cuda")
+    lm.step(q, kc, vc, i32(tables), i32(kv), o, lse=lse)
+    assert lm.errors() == 0
+    k6, v6 = f64(kc), f64(vc)
+    rows = sorted({0, B - 1, *rng.sample(range(B), min(B, 200))})
+
+    def keys_of(i):
+        b = rows[i]
+        ids = tables[b][:-(-kv[b] // 16)]
+        return tuple(x[ids].reshape(-1, 2, d)[:kv[b]] for x in (k6, v6))
+
+    ref = R.attention(f64(q)[rows], range(len(rows)), keys_of, 2, d ** -0.5)
+    R.assert_attention(o[rows], lse[rows], ref, "bf16", [kv[b] for b in rows], d, 5.0)
