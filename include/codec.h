@@ -629,8 +629,8 @@ CODEC_API codec_status codec_vocos_decode(codec_vocos_t* vocos, const float* mel
  *                          rotation, keys and values into their slots
  *   codec_lm_prompt        causal attention of whole prompts, packed
  *   codec_lm_prompt_paged  the same behind a context that is in the cache
- *   codec_lm_step          attention of one token per request, with the part
- *                          of the context that all requests share read once
+ *   codec_lm_step          attention of one token per request, with the part of
+ *                          the context that all requests share done for all at once
  * An object holds the shape, the rotation table and the workspace; the caches
  * are the caller's, one pair per layer, so one object serves all layers.
  * Independent of codec_t.

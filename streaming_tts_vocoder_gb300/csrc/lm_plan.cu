@@ -13,6 +13,11 @@
 // different requests; and the ring positions read, head .. head + taken, lie
 // before the ones written, tail .. tail + given back, which are at most n_blocks
 // ahead of head (any beyond are dropped: they were given back twice).
+//
+// Bound by latency: 64 requests of one token each take 7.0 us, 1,000 that start
+// with 475,000 rows 7.7 us (3.9 MB: 0.6 us).  A launch is 2.3 of it, the rest the
+// chain of dependent steps: counters and lengths from memory, the sums, the
+// look-up of a row's request, its block's id, the store.
 #include <climits>
 
 #include "lm.h"
