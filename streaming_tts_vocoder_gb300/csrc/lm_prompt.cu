@@ -88,6 +88,7 @@ struct Params {
     int* counts;                // items of the list, items taken from it, items to join
     int4* joins;                // of each: first query row, tokens, first slot and pieces << 16, keys of the first token
     int split;                  // items may be cut along the keys
+    int most_cut;               // so many of them at most (with their K/V heads)
     float* piece;               // pieces' results: [slot][2 x 128 rows][D], normalised, fp32
     float* piece_lse;
     float c;                    // scale x log2 e
@@ -1256,7 +1257,10 @@ cudaError_t launch(const LmShape& sh, const void* q, long long qs, const LmKeys&
     }
     e = launch_pdl(lm_prompt_kernel<T, D>, grid, dim3(kThreads), smem_bytes<D>(), s, mq, mk, mv, p);
     if (e != cudaSuccess || !p.split) return e;
-    return launch_pdl(lm_pieces_kernel<T, D>, dim3(2 * kSms), dim3(kPieceThreads), 0, s, p);
+    // a row per warp where they fit: four rows per warp in turn, 608 CTAs less, took
+    // 40 instead of 34 us for 670 tokens behind 6,000 positions, eight K/V heads
+    const int ctas = std::min(8 * kSms, p.most_cut * 2 * kTile / (kPieceThreads / 32));
+    return launch_pdl(lm_pieces_kernel<T, D>, dim3(ctas), dim3(kPieceThreads), 0, s, p);
 }
 
 cudaError_t launch_any(const LmShape& sh, const void* q, long long qs, const LmKeys& ks, Params& p, dim3 grid,
@@ -1304,6 +1308,7 @@ cudaError_t launch_lm_prompt(const LmShape& sh, const LmPromptArgs& a, cudaStrea
     if (items <= kSms && !cut)
         return launch_any(sh, a.q, a.qs, a.keys, p, dim3((unsigned)(items / sh.hk), (unsigned)sh.hk), s);
     p.split = cut;
+    p.most_cut = (int)std::min<long long>(items, kLmSlots / 2);
     p.counts = a.ws.counts;
     p.joins = static_cast<int4*>(a.ws.joins);
     p.piece = a.ws.piece;
