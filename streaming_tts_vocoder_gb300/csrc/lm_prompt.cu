@@ -571,8 +571,6 @@ __global__ void __launch_bounds__(kThreads, 1) lm_prompt_kernel(const __grid_con
                     }
                     __syncwarp();
                 }
-                // the next item: taken while this one's first copies are on their way
-                if (p.list && lane == 0) taken = atomicAdd(p.counts + 1, 1) + gridDim.x;
                 for (int j = 0; j < n_max && ok; j++) {
                     int id = next;
                     const int here = p.tables ? min(per, blocks - j * per) : 1;
@@ -618,7 +616,10 @@ __global__ void __launch_bounds__(kThreads, 1) lm_prompt_kernel(const __grid_con
                         }
                     }
                 }
+                // The next item, two tiles ahead of its use.  No sooner: a CTA in the midst of
+                // a long item would hold one that others could have begun.
                 if (p.list) {
+                    if (lane == 0) taken = atomicAdd(p.counts + 1, 1) + gridDim.x;
                     taken = __shfl_sync(0xffffffffu, taken, 0);
                     entry_hk = -1;
                     if (taken < count) fetch(taken);
@@ -1112,7 +1113,9 @@ __global__ void __launch_bounds__(kListThreads) lm_list_kernel(const Params p, i
         int4 other;
         mine += item(e, other);
     }
-    if (mine) atomicAdd(&work, mine);           // whole numbers: any order
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
+    if (lane == 0 && mine) atomicAdd(&work, mine);      // whole numbers: any order
     if (tid < 3) carry[tid] = 0;
     __syncthreads();
     const int share = (int)min(max((work * p.sh.hk + kSms - 1) / kSms, (unsigned long long)kMinPiece),
