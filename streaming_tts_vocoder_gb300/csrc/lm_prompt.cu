@@ -1302,9 +1302,9 @@ cudaError_t launch_lm_prompt(const LmShape& sh, const LmPromptArgs& a, cudaStrea
     p.lse = a.lse;
     // Pairs of query tiles: at most one partly filled pair per request.  Cutting
     // along the keys pays where items are few for the SMs and their keys may be
-    // many: 64 tokens behind 32,768 positions, eight items, take 44 us cut and 373
-    // whole.  It costs about 10 us: 16 paged prompts of 144 items take 57 us whole
-    // and 63 cut, with two pieces for each SM 69.
+    // many: 64 tokens behind 32,768 positions, eight items, take 43 us cut and 373
+    // whole.  It costs about 5 us: 20 requests of 18 tokens behind 300 to 3,150
+    // positions, 160 items, take 48 us whole and 52 cut.
     const long long items = lm_list_items(a.rows, a.B, sh.group) * sh.hk;
     const bool cut = a.keys.tables ? items <= kSms && ((long long)a.keys.table_blocks << a.keys.bs_shift) > 2048
                                    : items <= 2 * kSms && a.rows > 2048;
