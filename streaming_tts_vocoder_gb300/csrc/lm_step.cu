@@ -8,8 +8,8 @@
 // A unit of work is (request, K/V head, split of `chunk` positions).  The
 // splits lie at fixed positions, so a result's bits do not depend on the
 // batch.  The units' number is known on the device only: a CTA's producer warp
-// takes one after the other from a counter (CTAs start late where the shared
-// part's kernel holds their SM) and keeps a ring of 64-key K and V tiles, the
+// takes one after the other, from a counter where that pays (CTAs start late
+// where the shared part's kernel holds their SM), and keeps a ring of 64-key K and V tiles, the
 // unit's queries with the first, in flight across units, so the copies never
 // pause.
 // Four warps take 16 keys of a tile each: scores and values by m16n8k16 MMAs
@@ -653,6 +653,9 @@ cudaError_t launch(const LmShape& sh, const LmStepArgs& a, cudaStream_t s)
     p.after_shared = after_shared;
     // joined in this kernel where a CTA has one unit at most and needs no other kernel's results
     const bool join = most <= ctas && p.n_pre == 0, two = !join && (p.n_pre > 0 || p.max_splits > 1);
+    // Units from the counter where requests are split or the shared part holds SMs (300
+    // of 500 to 600 positions 113 us, by blockIdx 121; 64 behind a shared 1,024 16.2 and
+    // 19.3), else by blockIdx, which is there at once (64 of up to 250: 9.3, 10.6 counted).
     p.taken = two ? a.ws.taken : nullptr;
     const cudaError_t e = launch_pdl(join ? lm_step_kernel<T, D, true> : lm_step_kernel<T, D, false>, dim3(ctas), dim3(kThreads), smem_bytes<D>(p.stages, sh.group, a.B), s, mk,
                                      mv, p);
