@@ -984,10 +984,11 @@ __global__ void __launch_bounds__(kThreads, 1) lm_prompt_kernel(const __grid_con
 // most first (in request order where there are many), each request's last pair
 // of tiles first.  With p.split, items of more than 5/4 of an SM's share of the
 // call's tiles are cut into pieces of about that share (at least kMinPiece
-// tiles: an item costs as much as three tiles besides them).  One CTA.
+// tiles: an item costs as much as three tiles besides them; with six two requests of
+// 64 tokens behind 1,936 positions take 24.0 us, with four 22.6).  One CTA.
 constexpr int kListThreads = 512;
 constexpr int kListSort = 512;          // requests that are sorted (by counting)
-constexpr int kMinPiece = 6;
+constexpr int kMinPiece = 4;
 
 __global__ void __launch_bounds__(kListThreads) lm_list_kernel(const Params p, int4* list)
 {
@@ -1304,9 +1305,12 @@ cudaError_t launch_lm_prompt(const LmShape& sh, const LmPromptArgs& a, cudaStrea
     // along the keys pays where items are few for the SMs and their keys may be
     // many: 64 tokens behind 32,768 positions, eight items, take 43 us cut and 373
     // whole.  It costs about 5 us: 20 requests of 18 tokens behind 300 to 3,150
-    // positions, 160 items, take 48 us whole and 52 cut.
+    // positions, 160 items, take 48 us whole and 52 cut.  The fewer the items, the
+    // sooner: 2 requests of 64 tokens behind 1,136 positions, 16 items, 23.1 and 21.3;
+    // 4 of 100 behind 1,000, 32 items (56 at most), 24.0 and 26.6.
     const long long items = lm_list_items(a.rows, a.B, sh.group) * sh.hk;
-    const bool cut = a.keys.tables ? items <= kSms && ((long long)a.keys.table_blocks << a.keys.bs_shift) > 2048
+    const bool cut = a.keys.tables ? items <= kSms && ((long long)a.keys.table_blocks << a.keys.bs_shift) >
+                                                          (items <= 48 ? 1024 : 2048)
                                    : items <= 2 * kSms && a.rows > 2048;
     if (items <= kSms && !cut)
         return launch_any(sh, a.q, a.qs, a.keys, p, dim3((unsigned)(items / sh.hk), (unsigned)sh.hk), s);

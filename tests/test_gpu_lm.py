@@ -874,3 +874,14 @@ def test_step_many_requests_of_few_positions(B, width):
 
     ref = R.attention(f64(q)[rows], range(len(rows)), keys_of, 2, d ** -0.5)
     R.assert_attention(o[rows], lse[rows], ref, "bf16", [kv[b] for b in rows], d, 5.0)
+
+
+@pytest.mark.parametrize("new,kv,hq,hk,d,bs", [
+    ([64, 64], [1200, 1100], 4, 2, 128, 16),            # just long enough to be cut, four tiles a piece
+    ([33, 1, 70, 9], [497, 1990, 0, 1200], 10, 2, 64, 128),
+    ([300, 2], [1300, 515], 7, 1, 128, 32),
+    ([130], [1024], 4, 1, 128, 64),                     # just not
+])
+def test_prompt_paged_middling_context(new, kv, hq, hk, d, bs):
+    check_paged(new, kv, hq, hk, d, "bf16", bs, seed=5)
+    check_paged(new, kv, hq, hk, d, "fp16", bs, seed=6)
