@@ -1072,6 +1072,7 @@ __global__ void __launch_bounds__(kListThreads) lm_list_kernel(const Params p, i
         scan(&tiles, 1);
         if (x < p.B) start[x] = tiles;
     }
+    __syncthreads();                            // item() reads every warp's starts
     // row_starts that overlap could make more items than there is room for
     const int total = min(carry[0], (int)lm_list_items(p.rows, p.B, p.sh.group));
     // the item of number e, and its K/V tiles
@@ -1117,6 +1118,7 @@ __global__ void __launch_bounds__(kListThreads) lm_list_kernel(const Params p, i
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
     if (lane == 0 && mine) atomicAdd(&work, mine);      // whole numbers: any order
+    __syncthreads();                            // every thread has its total: carry begins anew
     if (tid < 3) carry[tid] = 0;
     __syncthreads();
     const int share = (int)min(max((work * p.sh.hk + kSms - 1) / kSms, (unsigned long long)kMinPiece),

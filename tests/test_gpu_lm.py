@@ -885,3 +885,68 @@ def test_step_many_requests_of_few_positions(B, width):
 def test_prompt_paged_middling_context(new, kv, hq, hk, d, bs):
     check_paged(new, kv, hq, hk, d, "bf16", bs, seed=5)
     check_paged(new, kv, hq, hk, d, "fp16", bs, seed=6)
+
+
+def tile_pairs(lens, hq, hk):
+    """Pairs of query tiles that the prompts make, over all K/V heads."""
+    pair = 2 * (128 // (hq // hk))
+    return hk * sum(-(-n // pair) for n in lens)
+
+
+@pytest.mark.parametrize("B", [33, 64, 200, 511, 512])
+def test_prompt_list_of_many_sorted_requests(B):
+    """More items than SMs and more requests than a warp has lanes, few enough to
+    be ordered by their keys: whichever warp wrote a request's place in the
+    list, each request's rows come out as alone."""
+    rng = random.Random(B)
+    hq, hk, d = 16, 8, 64
+    lens = [rng.choice([0, 1, 2, 7, 30, 90]) for _ in range(B)]
+    lens[rng.randrange(B)] = 300
+    assert tile_pairs(lens, hq, hk) > 152
+    check_prompt(lens, 2, 2, d, "fp16", seed=B)         # the definition, few heads
+    q, k, v, starts = prompt_inputs(B, lens, hq, hk, d, "bf16", extra=2)
+    n = q.shape[0]
+    lm = C.Lm(hq, hk, d, max_requests=B, max_rows=n)
+    one = C.Lm(hq, hk, d, max_requests=1, max_rows=300)
+    o, lse = torch.full((n, hq, d), 5.0, dtype=q.dtype, device="cuda"), torch.full((n, hq), 5.0, device="cuda")
+    lm.prompt(q, k, v, i32(starts), o, lse=lse)
+    for b in range(B):
+        x, y = starts[b], starts[b + 1]
+        if y > x:
+            want, want_lse = torch.zeros_like(o[x:y]), torch.zeros_like(lse[x:y])
+            one.prompt(q[x:y], k[x:y], v[x:y], i32([0, y - x]), want, lse=want_lse)
+            assert torch.equal(o[x:y], want) and torch.equal(lse[x:y], want_lse), b
+    assert (o[starts[-1]:] == 5).all() and (lse[starts[-1]:] == 5).all() and lm.errors() == 0
+
+
+@pytest.mark.parametrize("B,bs", [(33, 16), (150, 64), (512, 32)])
+def test_prompt_paged_list_of_many_sorted_requests(B, bs):
+    rng = random.Random(B)
+    kv = [rng.choice([1, 5, 40, 130, 260]) for _ in range(B)]
+    new = [min(n, rng.choice([0, 1, 3, 20])) for n in kv]
+    assert tile_pairs([1] * B, 8, 8) > 152
+    check_paged(new, kv, 8, 8, 64, "bf16", bs, seed=B)
+
+
+@pytest.mark.parametrize("paged", [False, True])
+def test_row_starts_that_overlap_stay_inside_the_outputs(paged):
+    """Row starts that go back and forth name rows many times over: more items
+    than a call can have.  The bit, and nothing written outside."""
+    hq, hk, d, B, rows = 4, 4, 64, 60, 700
+    T = torch.bfloat16
+    gen = torch.Generator(device="cuda").manual_seed(0)
+    r = lambda *s: torch.randn(*s, generator=gen, device="cuda").to(T)
+    q, k, v = r(rows, hq, d), r(rows, hk, d), r(rows, hk, d)
+    kc, vc = r(64, 16, hk, d), r(64, 16, hk, d)
+    tables = torch.randint(64, (B, 50), generator=gen, device="cuda", dtype=torch.int32)
+    lm = C.Lm(hq, hk, d, n_blocks=64, table_blocks=50, max_requests=B, max_rows=rows)
+    guard = torch.full((3 * rows, hq, d), 5.0, dtype=T, device="cuda")
+    lse = torch.full((3 * rows, hq), 5.0, device="cuda")
+    for starts in ([0, rows] * 30 + [0], [rows - i for i in range(B + 1)], [2 ** 31 - 1, -2 ** 31] * 30 + [rows]):
+        call = ((lambda: lm.prompt_paged(q, kc, vc, i32(starts), tables, i32([800] * B), guard[rows:2 * rows],
+                                         lse=lse[rows:2 * rows])) if paged else
+                (lambda: lm.prompt(q, k, v, i32(starts), guard[rows:2 * rows], lse=lse[rows:2 * rows])))
+        call()
+        assert lm.errors() == C.LM_ERR_LENGTH
+        assert (guard[:rows] == 5).all() and (guard[2 * rows:] == 5).all()
+        assert (lse[:rows] == 5).all() and (lse[2 * rows:] == 5).all()
