@@ -953,15 +953,16 @@ __global__ void __launch_bounds__(kThreads, 1) lm_prompt_kernel(const __grid_con
                 }
             }
             if (fix) {
-                // a finite sum plus what is not finite is the latter
+                // added to what the other tiles and the row's statistics gave, which may be an
+                // infinity or NaN already
 #pragma unroll 1
                 for (int c = 0; c < D; c++) {
                     const float x = not_finite_sum<T>(p, it, c, first_masked * kTile, lim);
                     if (x == 0.f) continue;
                     if (fp32)
-                        reinterpret_cast<float*>(mine)[c] = x;
+                        reinterpret_cast<float*>(mine)[c] += x;
                     else
-                        reinterpret_cast<T*>(mine)[c] = (T)x;
+                        reinterpret_cast<T*>(mine)[c] = (T)((float)reinterpret_cast<T*>(mine)[c] + x);
                 }
             }
             __syncwarp();

@@ -950,3 +950,104 @@ def test_row_starts_that_overlap_stay_inside_the_outputs(paged):
         assert lm.errors() == C.LM_ERR_LENGTH
         assert (guard[:rows] == 5).all() and (guard[2 * rows:] == 5).all()
         assert (lse[:rows] == 5).all() and (lse[2 * rows:] == 5).all()
+
+
+# ---- values that are not finite, where they are seen -------------------------
+
+def check_not_finite(got, q, rows, keys_of, hk, dt, n_keys, d):
+    """NaN and infinities exactly where the definition has them (probabilities
+    that are zero for the type do not occur here), all else within the bound."""
+    with np.errstate(invalid="ignore"):
+        want = R.attention(q, rows, keys_of, hk, d ** -0.5)[0]
+    clean = R.attention(q, rows, lambda i: tuple(np.nan_to_num(x, nan=0.0, posinf=0.0, neginf=0.0) for x in keys_of(i)),
+                        hk, d ** -0.5)
+    g = f64(got)
+    odd = ~np.isfinite(want)
+    assert odd.any() and (~odd).any()
+    wrong = ~(np.isfinite(g) == ~odd) | (np.isnan(g) != np.isnan(want)) | (np.isinf(want) & (g != want))
+    assert not wrong.any(), f"{wrong.sum()} of {odd.sum()}, first {np.argwhere(wrong)[:4].tolist()}: {g[wrong][:4]} for {want[wrong][:4]}"
+    patched = torch.from_numpy(np.where(odd, clean[0], g)).to(got.dtype)
+    R.assert_attention(patched, None, clean, dt, n_keys, d, 6.0)
+
+
+def poison(v, at):
+    """Values of an early and a late key: one column NaN early and an infinity
+    late, one with both infinities, one with the same twice, some with one."""
+    inf = float("inf")
+    early, late = at
+    v[early, ..., 0], v[late, ..., 0] = NAN, inf
+    v[early, ..., 1], v[late, ..., 1] = inf, -inf
+    v[early, ..., 2], v[late, ..., 2] = -inf, -inf
+    v[late, ..., 3] = NAN
+    v[early, ..., 4] = inf
+    v[late, ..., 5] = inf
+    v[late - 1, ..., 6], v[late, ..., 6] = -inf, inf
+
+
+@pytest.mark.parametrize("dt,d,hq,hk,lens", [
+    ("bf16", 128, 4, 2, [300, 290]),            # an item per CTA
+    ("fp16", 64, 3, 3, [300, 290]),
+    ("bf16", 128, 8, 8, [290] * 12),            # a list
+    ("fp16", 64, 4, 1, [2100, 290]),            # cut along the keys
+])
+@pytest.mark.parametrize("paged", [False, True])
+def test_values_that_are_not_finite_come_out_as_defined(dt, d, hq, hk, lens, paged):
+    bs = 16
+    q, k, v, starts = prompt_inputs(11, lens, hq, hk, d, dt, extra=0)
+    q.mul_(0.5)
+    for b, x in enumerate(starts[:-1]):
+        n = lens[b]
+        poison(v[x:x + n], (5, n - 20))
+    k[starts[1] + 9] = NAN                      # every row of the second request from its tenth on
+    n = sum(lens)
+    blocks = sum(-(-x // bs) for x in lens)
+    lm = C.Lm(hq, hk, d, dt, block_size=bs, n_blocks=blocks, table_blocks=max(130, -(-max(lens) // bs)),
+              max_requests=len(lens), max_rows=n)
+    o = torch.zeros(n, hq, d, dtype=q.dtype, device="cuda")
+    if paged:
+        kc, vc = (torch.full((blocks, bs, hk, d), NAN, dtype=q.dtype, device="cuda") for _ in range(2))
+        tables = torch.full((len(lens), lm._width), -1, dtype=torch.int32)
+        at = 0
+        for b, x in enumerate(starts[:-1]):
+            kc.view(-1, hk, d)[at * bs:at * bs + lens[b]] = k[x:x + lens[b]]
+            vc.view(-1, hk, d)[at * bs:at * bs + lens[b]] = v[x:x + lens[b]]
+            c = -(-lens[b] // bs)
+            tables[b, :c] = torch.arange(at, at + c)
+            at += c
+        lm.prompt_paged(q.contiguous(), kc, vc, i32(starts), tables.cuda(), i32(lens), o)
+    else:
+        lm.prompt(q, k, v, i32(starts), o)
+    assert lm.errors() == 0
+    where = [(s, s + i + 1) for s, e in zip(starts, starts[1:]) for i in range(e - s)]
+    rows = sorted({r for s, e in zip(starts, starts[1:]) for r in (s, s + 4, s + 5, s + 12, s + 127, s + 128, e - 23, e - 22,
+                                                                    e - 21, e - 20, e - 19, e - 1)})
+    k6, v6 = f64(k), f64(v)
+    check_not_finite(o[rows], f64(q)[rows], range(len(rows)),
+                     lambda i: (k6[where[rows[i]][0]:where[rows[i]][1]], v6[where[rows[i]][0]:where[rows[i]][1]]), hk, dt,
+                     [where[r][1] - where[r][0] for r in rows], d)
+
+
+@pytest.mark.parametrize("dt,d,hq,hk", [("bf16", 128, 4, 2), ("fp16", 64, 3, 3)])
+@pytest.mark.parametrize("sh", [0, 128])
+def test_step_values_that_are_not_finite_come_out_as_defined(dt, d, hq, hk, sh):
+    """The shared part as rows of one product (some requests end inside it), and
+    each request's own part."""
+    bs = 16
+    kv = [2100, 2300, 2048, 1000, 40, 2040, 3, 0, 2200]
+    kc, vc, tables, shared, n_blocks, width, gen = cache_case(21, kv, hk, d, dt, bs, sh)
+    if sh:
+        flat = vc[shared].flatten(0, 1)
+        poison(flat, (5, 990))
+        poison(flat, (1500, 2044))
+        vc[shared] = flat.unflatten(0, (sh, bs))
+    for b in (0, 8):                                            # in their own parts too
+        blk = tables[b][kv[b] // bs - 1]
+        vc[blk, 3, :, 1], vc[blk, 4, :, 7], vc[blk, 4, :, 8] = -float("inf"), NAN, float("inf")
+    kc[tables[1][2200 // bs], 2] = NAN
+    q = torch.randn(len(kv), hq, d, generator=gen, device="cuda").mul_(0.75).to(R.DTYPES[dt])
+    lm = C.Lm(hq, hk, d, dt, block_size=bs, n_blocks=n_blocks, table_blocks=width, max_requests=len(kv), max_rows=9)
+    o = torch.zeros_like(q)
+    lm.step(q, kc, vc, i32(tables), i32(kv), o, shared_table=i32(shared) if sh else None)
+    assert lm.errors() == 0
+    ks = [(gathered(kc, tables[b], n, bs), gathered(vc, tables[b], n, bs)) for b, n in enumerate(kv)]
+    check_not_finite(o, f64(q), range(len(kv)), lambda b: ks[b], hk, dt, kv, d)
