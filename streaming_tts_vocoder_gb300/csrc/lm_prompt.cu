@@ -394,25 +394,56 @@ struct Walk {
     }
 };
 
-// Sum of the values of a column that are not finite, over keys lo .. hi - 1 of
-// an item (rare: read from global memory one by one).
-template <typename T>
-__device__ __noinline__ float not_finite_sum(const Params& p, const Item& it, int col, int lo, int hi)
+// Adds to a warp's rows (dst: this lane's, T or fp32; lim: the keys it sees) the values
+// that are not finite of its keys lo .. lim - 1 of an item.  Rare, and read from
+// global memory: once for the warp, D / 32 columns per lane, each row taking the
+// sum where its last key is in.  One infinity a head among 8,192 shared positions,
+// 64 requests: 0.3 ms on top (48 with a column at a time, every row reading its keys anew).
+template <typename T, int D>
+__device__ __noinline__ void add_not_finite(const Params& p, const Item& it, int lo, int lim, unsigned long long dst,
+                                            bool fp32)
 {
-    const T* v = static_cast<const T*>(p.v) + (long long)it.hk * p.sh.D + col;
-    float sum = 0.f;
-    for (int k = lo; k < hi; k++) {
-        long long row = it.key0 + k;
-        if (p.tables) {
-            const int* table = p.tables + (p.row_start ? (long long)it.b * p.table_blocks : 0LL);
-            const int id = __ldg(table + (row >> p.bs_shift));
-            if (id < 0 || id >= p.n_blocks) continue;
-            row = ((long long)id << p.bs_shift) + (row & ((1 << p.bs_shift) - 1));
+    constexpr int kE = D / 32;
+    const int col = (threadIdx.x & 31) * kE;
+    const T* v = static_cast<const T*>(p.v) + (long long)it.hk * D + col;
+    const int* table = p.tables ? p.tables + (p.row_start ? (long long)it.b * p.table_blocks : 0LL) : nullptr;
+    float sum[kE] = {};
+    for (int k = lo;;) {
+        const int next = __reduce_min_sync(0xffffffffu, lim > k ? lim : kNone);
+        if (next == kNone) break;
+#pragma unroll 8
+        for (int x = k; x < next; x++) {
+            long long row = it.key0 + x;
+            bool in = true;
+            if (table) {
+                const int id = __ldg(table + (row >> p.bs_shift));
+                in = id >= 0 && id < p.n_blocks;
+                row = ((long long)id << p.bs_shift) + (row & ((1 << p.bs_shift) - 1));
+            }
+            alignas(8) T y[kE] = {};
+            if constexpr (kE == 4) {
+                if (in) *reinterpret_cast<uint2*>(y) = *reinterpret_cast<const uint2*>(v + row * p.v_stride);
+            } else {
+                if (in) *reinterpret_cast<uint32_t*>(y) = *reinterpret_cast<const uint32_t*>(v + row * p.v_stride);
+            }
+#pragma unroll
+            for (int e = 0; e < kE; e++) sum[e] += isfinite((float)y[e]) ? 0.f : (float)y[e];
         }
-        const float x = (float)v[row * p.v_stride];
-        if (!isfinite(x)) sum += x;
+        k = next;
+        unsigned rows = __ballot_sync(0xffffffffu, lim == next);
+        while (rows) {
+            const unsigned long long to = __shfl_sync(0xffffffffu, dst, __ffs(rows) - 1);
+            rows &= rows - 1;
+#pragma unroll
+            for (int e = 0; e < kE; e++) {
+                if (sum[e] == 0.f) continue;
+                if (fp32)
+                    reinterpret_cast<float*>(to)[col + e] += sum[e];
+                else
+                    reinterpret_cast<T*>(to)[col + e] = (T)((float)reinterpret_cast<T*>(to)[col + e] + sum[e]);
+            }
+        }
     }
-    return sum;
 }
 
 template <typename T, int D>
@@ -770,9 +801,10 @@ __global__ void __launch_bounds__(kThreads, 1) lm_prompt_kernel(const __grid_con
                                 return x & ((bad & 0x8000u ? 0u : 0xffffu) | (bad & 0x80000000u ? 0u : 0xffff0000u));
                             };
                             *at = make_uint4(keep(w.x, b0), keep(w.y, b1), keep(w.z, b2), keep(w.w, b3));
-                            // the note of the item before the last one has been read by now
+                            // the note of the item before the last one has been read by now, or soon is
                             volatile int* written = s.written;
-                            for (uint32_t i = 0; i < kPolls && min(written[0], written[1]) < 4 * (walk.k - 2) && !*abort_flag; i++) {}
+                            for (uint32_t i = 0; min(written[0], written[1]) < 4 * (walk.k - 2) && !*abort_flag; i++)
+                                if (i >= kPolls) *abort_flag = 1;
                             *reinterpret_cast<volatile int*>(&s.dirty[walk.k & 1]) = walk.k;
                         }
                     }
@@ -952,19 +984,8 @@ __global__ void __launch_bounds__(kThreads, 1) lm_prompt_kernel(const __grid_con
                     flush(q * 2);
                 }
             }
-            if (fix) {
-                // added to what the other tiles and the row's statistics gave, which may be an
-                // infinity or NaN already
-#pragma unroll 1
-                for (int c = 0; c < D; c++) {
-                    const float x = not_finite_sum<T>(p, it, c, first_masked * kTile, lim);
-                    if (x == 0.f) continue;
-                    if (fp32)
-                        reinterpret_cast<float*>(mine)[c] += x;
-                    else
-                        reinterpret_cast<T*>(mine)[c] = (T)((float)reinterpret_cast<T*>(mine)[c] + x);
-                }
-            }
+            // added to what the other tiles and the row's statistics gave, which may be an infinity or NaN already
+            if (__any_sync(0xffffffffu, fix)) add_not_finite<T, D>(p, it, first_masked * kTile, fix ? lim : 0, mine, fp32);
             __syncwarp();
             if (lane == 0) {
                 atomicAdd(&s.written[i], 1);
