@@ -443,13 +443,14 @@ __global__ void __launch_bounds__(kThreads, 2) lm_step_kernel(const __grid_const
                         m[h] = fmaxf(m[h], __shfl_xor_sync(0xffffffffu, m[h], 1));
                         m[h] = fmaxf(m[h], __shfl_xor_sync(0xffffffffu, m[h], 2));
                     }
-                    // the reference moves up by more than 8 (in log2) or not at all, as for prompts
+                    // a row's reference moves up by more than 8 (in log2) or not at all, for its own
+                    // scores alone, as for prompts (times 1 changes nothing)
                     if (__any_sync(0xffffffffu, (m[0] - ref[0]) * p.c > 8.f || (m[1] - ref[1]) * p.c > 8.f)) {
 #pragma unroll
                         for (int h = 0; h < 2; h++) {
-                            const float to = fmaxf(ref[h], m[h]);
-                            const float f = ref[h] == -INFINITY ? 0.f : exp2_fast((ref[h] - to) * p.c);
-                            ref[h] = to;
+                            const bool up = (m[h] - ref[h]) * p.c > 8.f;
+                            const float f = !up ? 1.f : ref[h] == -INFINITY ? 0.f : exp2_fast((ref[h] - m[h]) * p.c);
+                            ref[h] = up ? m[h] : ref[h];
                             l[h] *= f;
 #pragma unroll
                             for (int i = 0; i < D / 8; i++) {

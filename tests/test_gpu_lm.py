@@ -1082,3 +1082,26 @@ def test_one_infinity_among_many_shared_positions_costs_little():
     vc[7, 3, :, 0] = float("inf")
     assert ms() < 40 * without
     assert o[:-1, :, 0].isposinf().all() and o[:, :, 1:].isfinite().all() and o[-1].isfinite().all()
+
+
+@pytest.mark.parametrize("dt,hq,hk,d", [("bf16", 16, 8, 128), ("fp16", 32, 8, 64)])
+def test_step_a_head_does_not_depend_on_the_others_of_its_group(dt, hq, hk, d):
+    """Units of eight tiles in which running references move often: a head's
+    moves for its own scores alone, so its bits are the same beside others."""
+    B, bs = 20, 32
+    kv = [500 - 7 * i for i in range(B)]
+    kc, vc, tables, _, n_blocks, width, gen = cache_case(31, kv, hk, d, dt, bs)
+    assert width * bs > 500 and width * bs <= 512 + bs
+    tables = [t[:16] for t in tables]
+    r = lambda: torch.randn(B, hk, hq // hk, d, generator=gen, device="cuda")
+    q, q2 = r() * 12, r() * 12
+    q2[:, :, 0] = q[:, :, 0]
+    lm = C.Lm(hq, hk, d, dt, block_size=bs, n_blocks=n_blocks, table_blocks=16, max_requests=B, max_rows=B)
+    outs = []
+    for x in (q, q2):
+        x = x.to(R.DTYPES[dt]).view(B, hq, d)
+        o, lse = torch.zeros_like(x), torch.zeros(B, hq, device="cuda")
+        lm.step(x, kc, vc, i32(tables), i32(kv), o, lse=lse)
+        outs.append((o.view(B, hk, -1, d)[:, :, 0], lse.view(B, hk, -1)[:, :, 0]))
+    assert lm.errors() == 0
+    assert torch.equal(outs[0][0], outs[1][0]) and torch.equal(outs[0][1], outs[1][1])
