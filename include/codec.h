@@ -692,6 +692,16 @@ CODEC_API void codec_lm_destroy(codec_lm_t* lm);
  * Synchronises stream.  Errors: CODEC_ERR_NULL, CODEC_ERR_CUDA. */
 CODEC_API codec_status codec_lm_errors(codec_lm_t* lm, uint32_t* bits, int32_t clear, void* stream);
 
+/* Every wait of the attention kernels is bounded (2^20 polls, 1.6 s): a kernel
+ * that gives up on one stops cleanly and sets CODEC_LM_ERR_TIMEOUT, and once
+ * codec_lm_errors has cleared it the next calls are right again.  This verifies
+ * that path: with polls != 0, in the calls made from here on one warp of each CTA
+ * waits that many polls (2^20 at most) for a barrier that no role arrives on
+ * (codec_lm_step: in units of more than 64 positions), so the kernels give up on
+ * any input and the outputs are not valid.  0: off.  Captured graphs keep what they were
+ * captured with.  Errors: CODEC_ERR_NULL. */
+CODEC_API codec_status codec_lm_set_unarrived_wait(codec_lm_t* lm, uint32_t polls);
+
 /*
  * Blocks and slots for a call's new tokens, from the requests' lengths.
  * Request b holds len_before[b] positions and is to hold len_after[b].  A

@@ -195,6 +195,7 @@ def _lib():
             "codec_lm_create": (i32, [ctypes.POINTER(LmConfigC), ctypes.POINTER(_P)]),
             "codec_lm_destroy": (None, [_P]),
             "codec_lm_errors": (i32, [_P, ctypes.POINTER(ctypes.c_uint32), i32, _P]),
+            "codec_lm_set_unarrived_wait": (i32, [_P, ctypes.c_uint32]),
             "codec_lm_plan": (i32, [_P, _P, _P, i32, _P, _P, i32, _P, _P, _P, _P, _P, _P, _P, _P, i32, _P]),
             "codec_lm_rotate": (i32, [_P, _P, i64, _P, i64, _P, i64, i32, i32, _P, _P, _P, _P, _P, _P, _P, _P]),
             "codec_lm_prompt": (i32, [_P, _P, i64, _P, i64, _P, i64, i32, _P, i32, _P, i64, _P, _P]),
@@ -695,6 +696,11 @@ class Lm:
                                          self._current(self._index) if stream is None else stream.cuda_stream),
                "codec_lm_errors")
         return bits.value
+
+    def set_unarrived_wait(self, polls: int):
+        """codec_lm_set_unarrived_wait: one warp per CTA waits `polls` polls for
+        nothing, to verify that waits are bounded; 0: off."""
+        _check(self._lib.codec_lm_set_unarrived_wait(self._h, polls), "codec_lm_set_unarrived_wait")
 
 
 class Codec:

@@ -31,7 +31,12 @@ struct LmShape {
     int hq, hk, group, D;
     float scale;
     unsigned* err;
+    unsigned unarrived;             // != 0: one warp per CTA waits so many polls for a barrier that nothing arrives on
 };
+// Polls of a wait before it gives up: 1.5 us each where nothing arrives; the longest
+// table, 2^18 tiles of 128 keys, takes 0.4 s.  A constant: as a kernel argument it
+// made prompts of 6,904 and 9,000 tokens 688 us instead of 654.
+constexpr unsigned kLmPolls = 1u << 20;
 
 struct LmPlanArgs {
     const int* before;

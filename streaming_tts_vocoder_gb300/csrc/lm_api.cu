@@ -143,7 +143,7 @@ codec_status codec_lm_create(const codec_lm_config* cfg, codec_lm_t** out)
         return CODEC_ERR_OOM;
     }
     sp.taken = sp.done + (size_t)c.max_requests * c.kv_heads;
-    lm->shape = LmShape{c.type, c.q_heads, c.kv_heads, c.q_heads / c.kv_heads, c.head_dim, c.scale, lm->err};
+    lm->shape = LmShape{c.type, c.q_heads, c.kv_heads, c.q_heads / c.kv_heads, c.head_dim, c.scale, lm->err, 0};
     if (configure_lm_plan() != cudaSuccess || configure_lm_prompt() != cudaSuccess ||
         configure_lm_step() != cudaSuccess || cudaMemset(sp.done, 0, sizeof(int) * ((size_t)c.max_requests * c.kv_heads + 1)) != cudaSuccess ||
         cudaMemset(lm->err, 0, sizeof(unsigned)) != cudaSuccess ||
@@ -176,6 +176,13 @@ codec_status codec_lm_errors(codec_lm_t* lm, uint32_t* bits, int32_t clear, void
                                    cs) != cudaSuccess)) ||
         cudaStreamSynchronize(cs) != cudaSuccess)
         return CODEC_ERR_CUDA;
+    return CODEC_OK;
+}
+
+codec_status codec_lm_set_unarrived_wait(codec_lm_t* lm, uint32_t polls)
+{
+    if (!lm) return CODEC_ERR_NULL;
+    lm->shape.unarrived = std::min(polls, kLmPolls);
     return CODEC_OK;
 }
 

@@ -68,7 +68,6 @@ constexpr int kThreads = 384;
 constexpr int kTile = 128;                  // rows of a query tile, keys of a K/V tile
 constexpr uint32_t kHalfBytes = kTile * 128;    // 64 columns of a tile: 128 rows of 128 bytes
 constexpr int kMaxStages = 8;
-constexpr uint32_t kPolls = 1u << 20;         // 1.5 us each where nothing arrives; the longest table, 2^18 tiles, takes 0.4 s
 constexpr int kNone = 0x7fffffff;
 constexpr int kSms = 152;
 
@@ -253,6 +252,7 @@ struct Shared {
     uint64_t drain;
     uint64_t full[kMaxStages], empty[kMaxStages];
     uint64_t raw[kMaxStages], clean[kMaxStages];    // V tiles that are cleaned before use: landed, cleaned
+    uint64_t never;             // nothing arrives (see LmShape::unarrived)
     uint64_t q_full[2], q_empty[2], s_full[2], p_full[2][2], o_full[2], o_empty[2];
     uint64_t work_full[kWork], work_empty[kWork];
     Item work[kWork];           // hk -1: no more
@@ -362,7 +362,7 @@ struct Walk {
     {
         if (!p.list) return k++ || !s.found ? nullptr : &s.item;
         const int slot = k % kWork;
-        const bool ok = mbar_wait(&s.work_empty[slot], (uint32_t)(k / kWork & 1) ^ 1u, &s.abort, kPolls);
+        const bool ok = mbar_wait(&s.work_empty[slot], (uint32_t)(k / kWork & 1) ^ 1u, &s.abort, kLmPolls);
         k++;
         if (!__all_sync(0xffffffffu, ok)) return nullptr;
         Item& it = s.work[slot];
@@ -383,7 +383,7 @@ struct Walk {
     {
         if (!p.list) return k++ || !s.found ? nullptr : &s.item;
         const int slot = k % kWork;
-        const bool ok = mbar_wait(&s.work_full[slot], (uint32_t)(k / kWork & 1), &s.abort, kPolls);
+        const bool ok = mbar_wait(&s.work_full[slot], (uint32_t)(k / kWork & 1), &s.abort, kLmPolls);
         k++;
         return !ok || s.work[slot].hk < 0 ? nullptr : &s.work[slot];
     }
@@ -465,6 +465,7 @@ __global__ void __launch_bounds__(kThreads, 1) lm_prompt_kernel(const __grid_con
 
     if (tid == 0) {
         mbar_init(&s.drain, 1);
+        mbar_init(&s.never, 1);
         for (int i = 0; i < kStages; i++) {
             mbar_init(&s.full[i], 1);
             mbar_init(&s.empty[i], 1);
@@ -589,7 +590,7 @@ __global__ void __launch_bounds__(kThreads, 1) lm_prompt_kernel(const __grid_con
                 }
                 for (int i = 0; i < 2 && ok; i++) {
                     if (it.n[i] == 0) continue;
-                    ok = mbar_wait(&s.q_empty[i], (q_n >> i & 1u) ^ 1u, abort_flag, kPolls);
+                    ok = mbar_wait(&s.q_empty[i], (q_n >> i & 1u) ^ 1u, abort_flag, kLmPolls);
                     ok = __all_sync(0xffffffffu, ok);
                     if (!ok) break;
                     q_n ^= 1u << i;
@@ -614,7 +615,7 @@ __global__ void __launch_bounds__(kThreads, 1) lm_prompt_kernel(const __grid_con
                         }
                     }
                     for (int kv = 0; kv < 2; kv++) {
-                        ok = mbar_wait(&s.empty[st], ph ^ 1u, abort_flag, kPolls);
+                        ok = mbar_wait(&s.empty[st], ph ^ 1u, abort_flag, kLmPolls);
                         ok = __all_sync(0xffffffffu, ok);
                         if (!ok) break;
                         uint8_t* dst = skv + (size_t)st * kBytes;
@@ -671,7 +672,7 @@ __global__ void __launch_bounds__(kThreads, 1) lm_prompt_kernel(const __grid_con
                 uint32_t tile_ph = 0, item_ph = 0;      // of each query tile's: per K/V tile, per item
                 int st = 0;
                 auto landed = [&](int stage) {
-                    const bool in = mbar_wait(&s.full[stage], full_ph >> stage & 1u, abort_flag, kPolls);
+                    const bool in = mbar_wait(&s.full[stage], full_ph >> stage & 1u, abort_flag, kLmPolls);
                     full_ph ^= 1u << stage;
                     tc_fence_after();
                     return in;
@@ -707,7 +708,7 @@ __global__ void __launch_bounds__(kThreads, 1) lm_prompt_kernel(const __grid_con
 #pragma unroll
                     for (int i = 0; i < 2; i++) {
                         if ((i ? n1 : n0) == 0 || !ok) continue;
-                        ok = mbar_wait(&s.q_full[i], item_ph >> i & 1u, abort_flag, kPolls);
+                        ok = mbar_wait(&s.q_full[i], item_ph >> i & 1u, abort_flag, kLmPolls);
                         tc_fence_after();
                         if (ok) score(i, sk0, (i ? n1 : n0) == 1);
                     }
@@ -719,7 +720,7 @@ __global__ void __launch_bounds__(kThreads, 1) lm_prompt_kernel(const __grid_con
                         if (j < first_masked) {
                             ok = landed(sv);
                         } else {
-                            ok = mbar_wait(&s.clean[sv], clean_ph >> sv & 1u, abort_flag, kPolls);
+                            ok = mbar_wait(&s.clean[sv], clean_ph >> sv & 1u, abort_flag, kLmPolls);
                             clean_ph ^= 1u << sv;
                             tc_fence_after();
                         }
@@ -733,14 +734,14 @@ __global__ void __launch_bounds__(kThreads, 1) lm_prompt_kernel(const __grid_con
                             if (!ok) break;
                             if (j < (i ? n1 : n0)) {
                                 const uint32_t ph = tile_ph >> i & 1u;
-                                ok = mbar_wait(&s.p_full[i][0], ph, abort_flag, kPolls);
+                                ok = mbar_wait(&s.p_full[i][0], ph, abort_flag, kLmPolls);
                                 // the last item's result has been read
                                 if (ok && j == 0)
-                                    ok = mbar_wait(&s.o_empty[i], (item_ph >> i & 1u) ^ 1u, abort_flag, kPolls);
+                                    ok = mbar_wait(&s.o_empty[i], (item_ph >> i & 1u) ^ 1u, abort_flag, kLmPolls);
                                 if (!ok) break;
                                 tc_fence_after();
                                 value(i, sv, 0, j > 0);
-                                if (!(ok = mbar_wait(&s.p_full[i][1], ph, abort_flag, kPolls))) break;
+                                if (!(ok = mbar_wait(&s.p_full[i][1], ph, abort_flag, kLmPolls))) break;
                                 tc_fence_after();
                                 value(i, sv, 1, true);
                                 tile_ph ^= 1u << i;
@@ -780,7 +781,7 @@ __global__ void __launch_bounds__(kThreads, 1) lm_prompt_kernel(const __grid_con
                 if (lane == 0) walk.done(p, s);
                 for (int j = first_masked; j < n_max; j++) {
                     const int st = (load0 + 2 * j + 1) % kStages;
-                    ok = mbar_wait(&s.raw[st], raw_ph >> st & 1u, abort_flag, kPolls);
+                    ok = mbar_wait(&s.raw[st], raw_ph >> st & 1u, abort_flag, kLmPolls);
                     raw_ph ^= 1u << st;
                     ok = __all_sync(0xffffffffu, ok);
                     if (!ok) break;
@@ -804,7 +805,7 @@ __global__ void __launch_bounds__(kThreads, 1) lm_prompt_kernel(const __grid_con
                             // the note of the item before the last one has been read by now, or soon is
                             volatile int* written = s.written;
                             for (uint32_t i = 0; min(written[0], written[1]) < 4 * (walk.k - 2) && !*abort_flag; i++)
-                                if (i >= kPolls) *abort_flag = 1;
+                                if (i >= kLmPolls) *abort_flag = 1;
                             *reinterpret_cast<volatile int*>(&s.dirty[walk.k & 1]) = walk.k;
                         }
                     }
@@ -824,7 +825,8 @@ __global__ void __launch_bounds__(kThreads, 1) lm_prompt_kernel(const __grid_con
         const uint32_t lane_base = tmem + ((uint32_t)((warp & 3) * 32) << 16);
         const uint32_t ts = lane_base + i * 128, to = lane_base + 256 + i * 128;
         uint32_t tile_ph = 0, item_ph = 0;
-        bool ok = true;
+        bool ok = !p.sh.unarrived || warp != 4 || mbar_wait(&s.never, 0, abort_flag, p.sh.unarrived);
+        ok = __all_sync(0xffffffffu, ok);
         while (ok) {
             const Item* const item = walk.next(p, s);
             if (!__all_sync(0xffffffffu, item != nullptr)) break;
@@ -836,7 +838,7 @@ __global__ void __launch_bounds__(kThreads, 1) lm_prompt_kernel(const __grid_con
             const int first_masked = it.free_from / kTile;
             float ref = 0.f, l = 0.f;
             for (int j = 0; j < n; j++) {
-                ok = mbar_wait(&s.s_full[i], tile_ph, abort_flag, kPolls);
+                ok = mbar_wait(&s.s_full[i], tile_ph, abort_flag, kLmPolls);
                 tile_ph ^= 1u;
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break;
@@ -902,7 +904,7 @@ __global__ void __launch_bounds__(kThreads, 1) lm_prompt_kernel(const __grid_con
                 l += l0.x + l0.y;
             }
             if (ok && n > 0) {
-                ok = mbar_wait(&s.o_full[i], item_ph, abort_flag, kPolls);
+                ok = mbar_wait(&s.o_full[i], item_ph, abort_flag, kLmPolls);
                 item_ph ^= 1u;
                 ok = __all_sync(0xffffffffu, ok);
                 tc_fence_after();

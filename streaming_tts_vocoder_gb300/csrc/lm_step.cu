@@ -39,7 +39,6 @@ constexpr int kConsumers = 4;
 constexpr int kThreads = 32 * (kConsumers + 1);
 constexpr int kKeys = 64;               // keys of a tile, 16 per consumer warp
 constexpr int kMaxStages = 6;
-constexpr uint32_t kPolls = 1u << 20;   // 1.5 us each where nothing arrives
 constexpr uint32_t kHalf = kKeys * 128; // 64 columns of a tile
 
 struct Params {
@@ -252,6 +251,7 @@ __global__ void __launch_bounds__(kThreads, 2) lm_step_kernel(const __grid_const
     uint64_t* full = reinterpret_cast<uint64_t*>(ml + kConsumers * 16 * 2);
     uint64_t* empty = full + kMaxStages;
     int* flags = reinterpret_cast<int*>(empty + kMaxStages);    // abort, last one of a (request, head)
+    uint64_t* never = reinterpret_cast<uint64_t*>(flags + 2);   // nothing arrives (see LmShape::unarrived)
     // the unit whose first tile a stage holds: request (-1: no more), K/V head, split and splits << 16, positions
     int4* unit_of = reinterpret_cast<int4*>(flags + 4);
     int* first = reinterpret_cast<int*>(unit_of + kMaxStages);
@@ -264,6 +264,7 @@ __global__ void __launch_bounds__(kThreads, 2) lm_step_kernel(const __grid_const
             mbar_init(&full[i], 1);
             mbar_init(&empty[i], kConsumers);
         }
+        mbar_init(never, 1);
         flags[0] = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
@@ -341,7 +342,7 @@ __global__ void __launch_bounds__(kThreads, 2) lm_step_kernel(const __grid_const
                         row = (id << p.bs_shift) + (pos & ((1 << p.bs_shift) - 1));
                     }
                 }
-                ok = mbar_wait(&empty[st], ph ^ 1u, abort_flag, kPolls);
+                ok = mbar_wait(&empty[st], ph ^ 1u, abort_flag, kLmPolls);
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break;
                 uint8_t* dst = smem + (size_t)st * pitch;
@@ -389,10 +390,12 @@ __global__ void __launch_bounds__(kThreads, 2) lm_step_kernel(const __grid_const
         const int v_key = warp * 16 + (m8 & 1) * 8 + l8, v_chunk = m8 >> 1;
         int st = 0;
         uint32_t ph = 0;
-        // when a wait gives up inside a unit its warps still meet at the unit's
-        // barriers; at the next unit they all leave
+        // When a wait gives up inside a unit its warps still meet at the unit's
+        // barriers; at the next unit they all leave, whatever has landed by then: the
+        // warps may stand at different stages, and not each of those holds a unit's start.
+        bool gave_up = false;
         while (true) {
-            if (!consumers_all(mbar_wait(&full[st], ph, abort_flag, kPolls))) break;
+            if (!consumers_all(!gave_up && mbar_wait(&full[st], ph, abort_flag, kLmPolls))) break;
             const int4 unit = unit_of[st];
             if (unit.x < 0) break;
             Unit n;
@@ -410,8 +413,12 @@ __global__ void __launch_bounds__(kThreads, 2) lm_step_kernel(const __grid_const
                 for (int e = 0; e < 4; e++) acc[i][e] = 0.f;
             float ref[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
             for (int j = 0; j == 0 || j * kKeys < n.keys; j++) {
-                const bool ok = j == 0 || mbar_wait(&full[st], ph, abort_flag, kPolls);
-                if (!__all_sync(0xffffffffu, ok)) break;
+                // (unarrived: one warp's second tile never comes)
+                const bool ok = j == 0 || (p.sh.unarrived && warp == 0 && j == 1
+                                               ? mbar_wait(never, 0, abort_flag, p.sh.unarrived)
+                                               : mbar_wait(&full[st], ph, abort_flag, kLmPolls));
+                gave_up = !__all_sync(0xffffffffu, ok);
+                if (gave_up) break;
                 const uint32_t kt = base + (uint32_t)st * pitch, vt = kt + kTileBytes;
                 if (j == 0 && n.keys > 0) {     // rows behind the group's repeat its last: nobody reads them
                     const uint32_t qt = vt + kTileBytes + min((m8 & 1) * 8 + l8, group - 1) * D * 2 + (m8 >> 1) * 16;

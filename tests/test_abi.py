@@ -106,3 +106,7 @@ def test_lm_config_and_null_checks_need_no_device(lib):
     assert lib.codec_lm_step(n, n, 0, 1, n, n, n, n, n, 0, n, 0, n, n) == 1
     bits = ctypes.c_uint32()
     assert lib.codec_lm_errors(n, ctypes.byref(bits), 0, n) == 1
+
+
+def test_lm_unarrived_wait_needs_an_object(lib):
+    assert lib.codec_lm_set_unarrived_wait(None, 0) == 1

@@ -1105,3 +1105,45 @@ def test_step_a_head_does_not_depend_on_the_others_of_its_group(dt, hq, hk, d):
         outs.append((o.view(B, hk, -1, d)[:, :, 0], lse.view(B, hk, -1)[:, :, 0]))
     assert lm.errors() == 0
     assert torch.equal(outs[0][0], outs[1][0]) and torch.equal(outs[0][1], outs[1][1])
+
+
+# ---- waits that run out -------------------------------------------------------
+
+@pytest.mark.parametrize("form", ["prompt", "list", "cut", "step joined inside", "step joined after", "shared"])
+def test_bounded_waits_run_out_report_and_recover(form):
+    """One warp per CTA waits for a barrier that nothing arrives on while the
+    other roles are at work: the kernels stop cleanly, the bit is set, and after
+    it is cleared the same call gives its bits again."""
+    T, hq, hk, d, bs = torch.bfloat16, 8, 4, 128, 16
+    gen = torch.Generator(device="cuda").manual_seed(6)
+    r = lambda *s: torch.randn(*s, generator=gen, device="cuda").to(T)
+    if form in ("prompt", "list"):
+        lens = [400, 30] if form == "prompt" else [150] * 60
+        n = sum(lens)
+        q, k, v = r(n, hq, d), r(n, hk, d), r(n, hk, d)
+        starts = i32([sum(lens[:i]) for i in range(len(lens) + 1)])
+        lm = C.Lm(hq, hk, d, max_requests=len(lens), max_rows=n)
+        call = lambda o: lm.prompt(q, k, v, starts, o)
+    else:
+        B, width = (1, 313) if form == "step joined inside" else (2, 300) if form == "cut" else (40, 120)
+        kc, vc = r(400, bs, hk, d), r(400, bs, hk, d)
+        tables = torch.randint(400, (B, width), generator=gen, device="cuda", dtype=torch.int32)
+        kv = i32([width * bs - 5 * b for b in range(B)])
+        n = 70 if form == "cut" else B
+        q = r(n, hq, d)
+        lm = C.Lm(hq, hk, d, n_blocks=400, table_blocks=width, max_requests=B, max_rows=n)
+        shared = tables[0, :80].contiguous() if form == "shared" else None
+        starts = i32([0, 40, 70])
+        call = ((lambda o: lm.prompt_paged(q, kc, vc, starts, tables, kv, o)) if form == "cut" else
+                (lambda o: lm.step(q, kc, vc, tables, kv, o, shared_table=shared)))
+    want, o = torch.zeros_like(q), torch.zeros_like(q)
+    call(want)
+    assert lm.errors() == 0 and want.any()
+    for _ in range(2):
+        lm.set_unarrived_wait(1000)
+        call(o)
+        bits = lm.errors()
+        lm.set_unarrived_wait(0)
+        assert bits == C.LM_ERR_TIMEOUT
+        call(o.zero_())
+        assert lm.errors() == 0 and torch.equal(o, want)
