@@ -722,10 +722,16 @@ CODEC_API codec_status codec_lm_set_unarrived_wait(codec_lm_t* lm, uint32_t poll
  *   kv_len     int32 [B]: len_after, or 0 where status is not 0.
  *   status     int32 [B]: 0; 1 the free blocks ran out at or before this request
  *              (one that needs none is still served); 2 a length outside [0,
- *              table_blocks * block_size] (no rows); 3 its rows pass max_rows.
- *              Where it is not 0 the request's blocks stay as they were.
+ *              table_blocks * block_size] (no rows); 3 the rows up to and with
+ *              this request's pass max_rows, and so they do for every request
+ *              behind it, those without rows among them.  Where it is not 0 the
+ *              request's blocks stay as they were: it gets none and gives none
+ *              back, and its kv_len is 0 in this call even if it did not change.
  *   slots, positions  int32 [max_rows]: of each row; a row of a request that
  *              failed has slot -1, one behind the last request slot -1 and position 0.
+ *              Positions inside the shared blocks have the same slots for every
+ *              request, so of requests that start there (len_before < shared_blocks *
+ *              block_size) a call has one, whose rows fill the blocks.
  * All arrays device memory; kv_len is neither len_before nor len_after (they
  * are read while it is written).  A repeated call with the same inputs writes the
  * same outputs, in-place ones included.

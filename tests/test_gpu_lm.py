@@ -1147,3 +1147,39 @@ def test_bounded_waits_run_out_report_and_recover(form):
         assert bits == C.LM_ERR_TIMEOUT
         call(o.zero_())
         assert lm.errors() == 0 and torch.equal(o, want)
+
+
+# ---- plans of more requests than a CTA has threads -----------------------------
+
+@pytest.mark.parametrize("seed,B,bs,sh,width,max_rows,free,old,new,bad", [
+    (10, 1024, 16, 0, 30, 20000, 3000, 300, 40, False),
+    (11, 1025, 16, 2, 30, 20000, 3000, 300, 40, False),
+    (12, 2049, 32, 1, 20, 90000, 400, 400, 60, True),       # the blocks run out behind the first thousand
+    (13, 3000, 16, 0, 12, 11000, 9000, 100, 40, False),     # the rows run out in the third
+    (14, 4096, 128, 3, 9, 400000, 9000, 500, 300, True),
+])
+def test_plan_of_many_requests(seed, B, bs, sh, width, max_rows, free, old, new, bad):
+    before, after, tables, ring, fr, shared, n_blocks = plan_case(seed, B, bs, sh, width, max_rows, free, old, new, bad)
+    lm = C.Lm(8, 8, 64, block_size=bs, n_blocks=n_blocks, table_blocks=width, max_requests=B, max_rows=max_rows)
+    got = run_plan(lm, before, after, tables, ring, fr, shared, max_rows)
+    want = R.plan(before, after, tables, ring, fr, shared, bs, max_rows)
+    for k in want:
+        assert got[k] == want[k], k
+    assert lm.errors() == 0
+    stop = {12: 1, 13: 3}.get(seed)
+    if stop:
+        assert want["status"].index(stop) > 1024
+
+
+def test_plan_rows_that_do_not_fit_leave_all_behind_them():
+    """The third request's rows pass max_rows: it, one that ended, one that did
+    not change and one that grows are all left as they were."""
+    lm = C.Lm(8, 8, 64, n_blocks=12, table_blocks=4, max_requests=6, max_rows=20)
+    before, after = [16, 30, 0, 40, 20, 5], [17, 16, 20, 0, 20, 6]
+    tables = [[0, -1, -1, -1], [1, 2, -1, -1], [-1] * 4, [3, 4, 5, -1], [6, 7, -1, -1], [8, -1, -1, -1]]
+    got = run_plan(lm, before, after, tables, [9, 10, 11] + [-1] * 9, (0, 3), [], 20)
+    assert got["status"] == [0, 0, 3, 3, 3, 3] and got["kv_len"] == [17, 16, 0, 0, 0, 0]
+    assert got["free_out"] == [1, 4] and got["free_list"][3] == 2
+    assert got["row_start"] == [0, 1, 1, 20, 20, 20, 20]
+    assert got["tables"] == [[0, 9, -1, -1]] + tables[1:] and lm.errors() == 0
+    assert got["slots"] == [9 * 16] + [-1] * 19 and got["positions"] == [16] + list(range(19))
