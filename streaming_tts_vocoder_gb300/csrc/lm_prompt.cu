@@ -1132,48 +1132,38 @@ __global__ void __launch_bounds__(kListThreads) lm_list_kernel(const Params p, i
         }
         return;
     }
+    // a call whose items may be cut has at most 2 kSms of them: one per thread
     int4 rows = make_int4(0, 0, 0, 0);
-    int tiles = tid < total ? item(tid, rows) : 0;      // the first round's, kept
-    unsigned long long mine = tiles;
-    for (int e = tid + kListThreads; e < total; e += kListThreads) {
-        int4 other;
-        mine += item(e, other);
-    }
+    const int tiles = tid < total ? item(tid, rows) : 0;
+    unsigned long long sum = tiles;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
-    if (lane == 0 && mine) atomicAdd(&work, mine);      // whole numbers: any order
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    if (lane == 0 && sum) atomicAdd(&work, sum);        // whole numbers: any order
     __syncthreads();                            // every thread has its total: carry begins anew
     if (tid < 3) carry[tid] = 0;
     __syncthreads();
     const int share = (int)min(max((work * p.sh.hk + kSms - 1) / kSms, (unsigned long long)kMinPiece),
                                1ull << 24);
-    for (int base = 0; base < total; base += kListThreads) {
-        const int e = base + tid;
-        int pieces = 0;
-        if (e < total) {
-            if (base > 0) tiles = item(e, rows);
-            pieces = tiles > share + share / 4 ? (tiles + share / 2) / share : 1;
-        }
-        int v[3] = {pieces, pieces > 1 ? pieces * p.sh.hk : 0, pieces > 1 ? 1 : 0};
-        scan(v, 3);
-        if (e >= total) continue;
-        // the shares bound the slots; should they not, the item stays whole (and keeps its places)
-        const bool cut = pieces > 1 && v[1] + pieces * p.sh.hk <= kLmSlots;
-        const int len = cut ? (tiles + pieces - 1) / pieces : kNone;
-        for (int c = 0; c < pieces; c++) {
-            const bool live = cut ? c * len < tiles : c == 0;
-            list[2 * (v[0] + c)] = live ? rows : make_int4(rows.x, rows.y, 0, 0);
-            list[2 * (v[0] + c) + 1] = cut && live ? make_int4(c * len, len, v[1] + c * p.sh.hk, 0) : make_int4(0, kNone, -1, 0);
-        }
-        if (pieces > 1)
-            p.joins[v[2]] = make_int4(rows.y, cut ? rows.z : 0, v[1] | (cut ? (tiles + len - 1) / len : 0) << 16, rows.w);
-    }
+    const int pieces = tid >= total ? 0 : tiles > share + share / 4 ? (tiles + share / 2) / share : 1;
+    int v[3] = {pieces, pieces > 1 ? pieces * p.sh.hk : 0, pieces > 1 ? 1 : 0};
+    scan(v, 3);
     if (tid == 0) {
         p.counts[0] = carry[0];
         p.counts[1] = 0;
         p.counts[2] = carry[2];
     }
+    // the shares bound the slots; should they not, the item stays whole (and keeps its places)
+    const bool cut = pieces > 1 && v[1] + pieces * p.sh.hk <= kLmSlots;
+    const int len = cut ? (tiles + pieces - 1) / pieces : kNone;
+    for (int c = 0; c < pieces; c++) {
+        const bool live = cut ? c * len < tiles : c == 0;
+        list[2 * (v[0] + c)] = live ? rows : make_int4(rows.x, rows.y, 0, 0);
+        list[2 * (v[0] + c) + 1] = cut && live ? make_int4(c * len, len, v[1] + c * p.sh.hk, 0) : make_int4(0, kNone, -1, 0);
+    }
+    if (pieces > 1)
+        p.joins[v[2]] = make_int4(rows.y, cut ? rows.z : 0, v[1] | (cut ? (tiles + len - 1) / len : 0) << 16, rows.w);
 }
+static_assert(2 * kSms <= kListThreads, "a thread per item that may be cut");
 
 // Joins the pieces of items that were cut: a warp per row.
 constexpr int kPieceThreads = 256;
