@@ -231,9 +231,12 @@ cudaError_t launch(const LmShape& sh, const LmRotateArgs& a, cudaStream_t s)
     while (parts < most && (long long)a.rows * parts < 152 * 16) parts++;
     const long long warps = (long long)a.rows * parts;
     const unsigned ctas = (unsigned)((warps + kRotThreads / 32 - 1) / (kRotThreads / 32));
-    // Up to eight rows per resident warp (five CTAs of four per SM) queries, keys
-    // and values go to warps of their own: shorter warps leave a shorter tail.
-    const unsigned kinds = a.rows < 8 * 152 * 20 ? (a.v ? 3 : 2) : 1;
+    // While every group of heads has a warp of its own, queries, keys and values go
+    // to different warps: 64 rows of 16 / 16 heads of 64 2.4 us (in turn 3.2), of 32 / 8
+    // of 128 2.9 (3.2), 500 rows of 16 / 16 3.1 (3.6).  Beyond that the warps' set-up
+    // costs more than it spreads: 500 rows of 32 / 8 6.2 (5.2), 2,000 rows 10.4 (10.1)
+    // and 8.0 (7.4), 16,000 70 (65) and 41 (38); 4,097 rows 17.0 (18.9) and 9.6 (9.3).
+    const unsigned kinds = (long long)a.rows * most <= 152 * 16 ? (a.v ? 3 : 2) : 1;
     return launch_pdl(lm_rotate_kernel<T, TI, D>, dim3(ctas, kinds), dim3(kRotThreads), 0, s, a, sh.hq, sh.hk, parts,
                       sh.err);
 }
