@@ -1322,11 +1322,14 @@ cudaError_t launch_lm_prompt(const LmShape& sh, const LmPromptArgs& a, cudaStrea
     // many: 64 tokens behind 32,768 positions, eight items, take 43 us cut and 373
     // whole.  It costs about 5 us: 20 requests of 18 tokens behind 300 to 3,150
     // positions, 160 items, take 48 us whole and 52 cut.  The fewer the items, the
-    // sooner: 2 requests of 64 tokens behind 1,136 positions, 16 items, 23.1 and 21.3;
-    // 4 of 100 behind 1,000, 32 items (56 at most), 24.0 and 26.6.
+    // sooner: tables of more than 1,280 positions where they are at most 48 (whole and
+    // cut, 16 / 8 heads of 128: 1 token behind 1,299 positions 22.2 and 17.9 us, 4 of 60
+    // behind 1,240 25.2 and 24.0; but 300 behind 730 23.2 and 27.8, 2 of 200 behind 890
+    // 24.6 and 28.7, 60 behind 1,030 20.1 and 21.4), else of more than 2,048 (4 of 200
+    // behind 1,800, 80 items, 34.2 and 35.5).
     const long long items = lm_list_items(a.rows, a.B, sh.group) * sh.hk;
     const bool cut = a.keys.tables ? items <= kSms && ((long long)a.keys.table_blocks << a.keys.bs_shift) >
-                                                          (items <= 48 ? 1024 : 2048)
+                                                          (items <= 48 ? 1280 : 2048)
                                    : items <= 2 * kSms && a.rows > 2048;
     if (items <= kSms && !cut)
         return launch_any(sh, a.q, a.qs, a.keys, p, dim3((unsigned)(items / sh.hk), (unsigned)sh.hk), s);
