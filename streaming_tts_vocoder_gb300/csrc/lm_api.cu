@@ -20,14 +20,16 @@ struct codec_lm_s {
 
 namespace {
 
-// Calls run on the object's device, whichever is current.
+// Calls run on the object's device, whichever is current.  It is set even where it
+// is current already: that binds its context to a host thread that has made no CUDA
+// call yet, and the driver encodes no tensor map without one.
 struct OnDevice {
     int was = -1;
     bool ok = false;
     explicit OnDevice(int device)
     {
         if (cudaGetDevice(&was) != cudaSuccess) return;
-        ok = was == device || cudaSetDevice(device) == cudaSuccess;
+        ok = cudaSetDevice(device) == cudaSuccess;
         if (was == device) was = -1;
     }
     ~OnDevice()

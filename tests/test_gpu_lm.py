@@ -5,6 +5,7 @@ row may see, device data that is wrong, and a layer's run of them together."""
 from __future__ import annotations
 
 import random
+import threading
 
 import numpy as np
 import pytest
@@ -1183,3 +1184,46 @@ def test_plan_rows_that_do_not_fit_leave_all_behind_them():
     assert got["row_start"] == [0, 1, 1, 20, 20, 20, 20]
     assert got["tables"] == [[0, 9, -1, -1]] + tables[1:] and lm.errors() == 0
     assert got["slots"] == [9 * 16] + [-1] * 19 and got["positions"] == [16] + list(range(19))
+
+
+@pytest.mark.parametrize("call", ["plan", "rotate", "prompt", "prompt_paged", "step", "errors"])
+def test_first_call_of_a_new_host_thread(call):
+    """A thread that has made no CUDA call before has no context bound yet."""
+    hq, hk, d = 4, 2, 64
+    T = torch.bfloat16
+    gen = torch.Generator(device="cuda").manual_seed(3)
+    r = lambda *s: torch.randn(*s, generator=gen, device="cuda").to(T)
+    q, k, v, kc, vc = r(20, hq, d), r(20, hk, d), r(20, hk, d), r(8, 16, hk, d), r(8, 16, hk, d)
+    starts, tables, kv = i32([0, 9, 20]), i32([[0, 1, 2], [3, 4, 5]]), i32([33, 48])
+    lm = C.Lm(hq, hk, d, n_blocks=8, table_blocks=3, max_requests=2, max_rows=20)
+    stream = torch.cuda.current_stream()
+    free = torch.tensor([0, 8], device="cuda")
+
+    def run(o):
+        z = lambda n: torch.zeros(n, dtype=torch.int32, device="cuda")
+        out, ring = [z(3), z(2), z(2), z(20), z(20)], i32(range(8))
+        qo, kd, vd, t = torch.zeros_like(q), torch.zeros_like(kc), torch.zeros_like(vc), tables.clone()
+        pos, before, after, counts = i32(range(20)), i32([5, 0]), i32([9, 7]), torch.zeros_like(free)
+        torch.cuda.synchronize()
+        return {"plan": lambda: (lm.plan(before, after, t, ring, free, counts, *out, stream=stream), out[3]),
+                "rotate": lambda: (lm.rotate(q, k, v, pos, pos, qo, kd, vd, stream=stream), qo),
+                "prompt": lambda: (lm.prompt(q, k, v, starts, o, stream=stream), o),
+                "prompt_paged": lambda: (lm.prompt_paged(q, kc, vc, starts, tables, kv, o, stream=stream), o),
+                "step": lambda: (lm.step(q[:2], kc, vc, tables, kv, o[:2], stream=stream), o),
+                "errors": lambda: (None, torch.tensor(lm.errors(stream=stream)))}[call]
+
+    want = run(torch.zeros_like(q))()[1]
+    got, f = [], run(torch.zeros_like(q))
+
+    def work():
+        try:
+            got.append(f()[1])
+        except Exception as e:      # told by the other thread
+            got.append(e)
+
+    t = threading.Thread(target=work)
+    t.start()
+    t.join()
+    torch.cuda.synchronize()
+    assert torch.is_tensor(got[0]), got[0]
+    assert torch.equal(got[0], want) and lm.errors() == 0
