@@ -806,8 +806,11 @@ CODEC_API codec_status codec_lm_prompt_paged(codec_lm_t* lm, const void* q, int6
  * shared_blocks > 0: positions below shared_blocks * block_size are those of
  * shared_table (int32 [shared_blocks], device) for every request - the entries
  * of tables for them are not read - and where they are many their scores and
- * sums are computed for the whole batch at once.  A request's result does not depend on the others of
- * the batch.  o overlaps nothing else.  Errors as codec_lm_prompt (CODEC_ERR_ARG also for shared_blocks
+ * sums are computed for the whole batch at once.  Whether they are many goes by
+ * max_requests, the heads and the shared length, not by B: a request's result does
+ * not depend on the others of the batch, and an object made for many requests takes
+ * the longer way (three kernels, 4 to 5 us) for one as well.  o overlaps nothing
+ * else.  Errors as codec_lm_prompt (CODEC_ERR_ARG also for shared_blocks
  * outside [0, table_blocks]).
  */
 CODEC_API codec_status codec_lm_step(codec_lm_t* lm, const void* q, int64_t q_stride, int32_t B, const void* k_cache,

@@ -268,8 +268,11 @@ __global__ void __launch_bounds__(kThreads, 2) lm_step_kernel(const __grid_const
         flags[0] = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
-    // behind the shared part's kernel there is nothing to wait for: what this one
-    // reads was complete when that one passed its own wait (and is read from L2)
+    // Behind the shared part's kernel there is nothing to wait for: what this one
+    // reads was complete when that one passed its own wait.  It has to come from L2
+    // all the same, as this SM's L1 may hold it from before: lengths and tables by
+    // __ldcg, queries by bulk copies, keys and values by TMA, nothing by plain or
+    // read-only loads.
     if (!p.after_shared) pdl_wait();
     pdl_launch();
     int unit0 = blockIdx.x;                 // of the copy warp's lane 0
