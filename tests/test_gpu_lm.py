@@ -1227,3 +1227,83 @@ def test_first_call_of_a_new_host_thread(call):
     torch.cuda.synchronize()
     assert torch.is_tensor(got[0]), got[0]
     assert torch.equal(got[0], want) and lm.errors() == 0
+
+
+# ---- captured calls and several streams ----------------------------------------
+
+def test_graph_of_steps_behind_a_long_shared_part_follows_the_lengths():
+    """Rotation, shared part, own parts and join in one graph: nothing of the
+    last replay's queries, lengths or cache may be seen by the next."""
+    hq, hk, d, bs, sh, B = 16, 8, 128, 16, 96, 40
+    T, width, n_blocks = torch.bfloat16, sh + 12, 200
+    gen = torch.Generator(device="cuda").manual_seed(12)
+    r = lambda *s: torch.randn(*s, generator=gen, device="cuda")
+    kc, vc = r(n_blocks, bs, hk, d).to(T), r(n_blocks, bs, hk, d).to(T)
+    tables = torch.randint(n_blocks, (B, width), generator=gen, device="cuda", dtype=torch.int32)
+    shared = torch.randperm(n_blocks, generator=gen, device="cuda")[:sh].to(torch.int32)
+    mk = lambda: C.Lm(hq, hk, d, n_blocks=n_blocks, table_blocks=width, max_requests=B, max_rows=B)
+    lm, eager = mk(), mk()
+    x = torch.zeros(B, (hq + 2 * hk) * d, dtype=T, device="cuda")
+    q, k, v = (t.unflatten(1, (-1, d)) for t in x.split([hq * d, hk * d, hk * d], 1))
+    pos, slots, kv = (torch.zeros(B, dtype=torch.int32, device="cuda") for _ in range(3))
+    qo, o = torch.zeros(B, hq, d, dtype=T, device="cuda"), torch.zeros(B, hq, d, dtype=T, device="cuda")
+
+    def layer(lm, kc, vc, qo, o):
+        lm.rotate(q, k, v, pos, slots, qo, kc, vc)
+        lm.step(qo, kc, vc, tables, kv, o, shared_table=shared)
+
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        layer(lm, kc, vc, qo, o)
+    for i in range(12):
+        x.copy_((r(B, (hq + 2 * hk) * d) * 3).to(T))
+        kv.copy_(torch.randint(0, width * bs + 1, (B,), generator=gen, device="cuda") * (torch.arange(B, device="cuda") % 5 != i % 5))
+        pos.copy_(torch.randint(width * bs, (B,), generator=gen, device="cuda"))
+        slots.copy_(torch.randperm(n_blocks * bs, generator=gen, device="cuda")[:B])
+        kc2, vc2, want = kc.clone(), vc.clone(), torch.zeros_like(o)
+        torch.cuda.synchronize()
+        layer(eager, kc2, vc2, torch.zeros_like(qo), want)
+        torch.cuda.synchronize()
+        graph.replay()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(kc, kc2) and torch.equal(vc, vc2) and torch.equal(o, want), i
+    assert lm.errors() == 0 and eager.errors() == 0
+
+
+def test_objects_on_streams_of_their_own_run_at_once():
+    """Prompts, steps behind a shared part and prompts behind the cache, each
+    object on its own stream and host thread: each gives the bits it gives alone."""
+    hq, hk, d = 16, 8, 128
+    T = torch.bfloat16
+    gen = torch.Generator(device="cuda").manual_seed(8)
+    r = lambda *s: torch.randn(*s, generator=gen, device="cuda").to(T)
+    lens = [60, 900, 300, 500] * 3
+    n = sum(lens)
+    q, k, v, starts = r(n, hq, d), r(n, hk, d), r(n, hk, d), i32([sum(lens[:i]) for i in range(13)])
+    kc, vc = r(300, 16, hk, d), r(300, 16, hk, d)
+    tables = torch.randint(300, (30, 110), generator=gen, device="cuda", dtype=torch.int32)
+    shared, kv = tables[0, :80].contiguous(), i32([1281 + 11 * i for i in range(30)])
+    mk = lambda: C.Lm(hq, hk, d, n_blocks=300, table_blocks=110, max_requests=30, max_rows=n)
+    two, tables2, kv2 = i32([0, 40, 90]), tables[:2].contiguous(), kv[:2].contiguous()
+    calls = [lambda lm, o, s: lm.prompt(q, k, v, starts, o, stream=s),
+             lambda lm, o, s: lm.step(q[:30], kc, vc, tables, kv, o[:30], shared_table=shared, stream=s),
+             lambda lm, o, s: lm.prompt_paged(q[:90], kc, vc, two, tables2, kv2, o[:90], stream=s)]
+    wants, lms = [], [mk() for _ in calls]
+    for f, lm in zip(calls, lms):
+        wants.append(torch.zeros_like(q))
+        f(lm, wants[-1], torch.cuda.current_stream())
+    outs = [[torch.zeros_like(q) for _ in range(8)] for _ in calls]
+    streams = [torch.cuda.Stream() for _ in calls]
+    torch.cuda.synchronize()
+
+    def work(i):
+        for o in outs[i]:
+            calls[i](lms[i], o, streams[i])
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(3)]
+    [t.start() for t in threads]
+    [t.join() for t in threads]
+    torch.cuda.synchronize()
+    for want, out, lm in zip(wants, outs, lms):
+        assert want.any() and all(torch.equal(o, want) for o in out) and lm.errors() == 0
