@@ -42,8 +42,8 @@
 //
 // What bounds it.  Long prompts: a pair of tiles takes about 2,800 cycles per 128
 // keys where its MMAs need 2,048; 6,904 and 9,000 tokens of 32 / 8 heads of 128 in
-// bf16 take 700 us, 1,500 TFLOP/s (80 % of a large library GEMM), the tensor pipe
-// 71 % active.  A warp's softmax of a tile is 1,100 cycles, and a tile's scores
+// bf16 take 711 us, 1,480 TFLOP/s (79 % of a large library GEMM), the tensor pipe
+// 70 % active.  A warp's softmax of a tile is 1,100 cycles, and a tile's scores
 // cannot be made before its last probabilities have been used, as these lie over
 // them: two tiles in turn hide most of that.  Ragged and short ones: an item costs
 // 8,000 cycles besides its tiles - the last product with V 2,400, the result 4,900

@@ -21,8 +21,8 @@
 // about 6,000 cycles, a third of a unit's time when one walks many.
 //
 // Long contexts: HBM.  256 requests of 32 / 8 heads of 128 in bf16 with 420,000
-// positions of their own behind 8,192 shared ones take 277 us, 6.3 TB/s (95 % of
-// the rate of a copy); two CTAs per SM keep six stages of 32 KB in flight.  Short ones: the latency of a unit, about 3,300
+// positions of their own behind 8,192 shared ones take 277 to 282 us, 6.2 to 6.3
+// TB/s (94 % of the rate of a copy); two CTAs per SM keep six stages of 32 KB in flight.  Short ones: the latency of a unit, about 3,300
 // cycles of its consumers for a tile (its scores and sums half of that, the
 // four warps' join the rest), and two launches where results are joined.
 #include <algorithm>
