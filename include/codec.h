@@ -631,6 +631,12 @@ CODEC_API codec_status codec_vocos_decode(codec_vocos_t* vocos, const float* mel
  *   codec_lm_prompt_paged  the same behind a context that is in the cache
  *   codec_lm_step          attention of one token per request, with the part of
  *                          the context that all requests share done for all at once
+ *   codec_lm_store_q4, codec_lm_load_q4, codec_lm_step_q4
+ *                          the same over a cache that holds 4 bits a value
+ *   codec_lm_beams         which beams go on with which tokens
+ *   codec_lm_fork, codec_lm_compact, codec_lm_copy
+ *                          blocks that several rows hold: rows that go on from
+ *                          others, held blocks moved together, blocks copied
  * An object holds the shape, the rotation table and the workspace; the caches
  * are the caller's, one pair per layer, so one object serves all layers.
  * Independent of codec_t.
@@ -654,6 +660,7 @@ CODEC_API codec_status codec_vocos_decode(codec_vocos_t* vocos, const float* mel
 #define CODEC_LM_ERR_LENGTH 8u    /* a length outside [0, table_blocks * block_size], or a row_start that falls
                                    * or passes the row count: taken as the nearest valid value */
 #define CODEC_LM_ERR_FREE 16u     /* codec_lm_plan: the free counters do not describe a ring of n_blocks */
+#define CODEC_LM_ERR_OWNERS 32u   /* codec_lm_fork: fewer owners counted than rows that hold a block */
 #define CODEC_LM_ERR_TIMEOUT 0x80000000u /* a tensor-core kernel gave up on a bounded wait: outputs not valid */
 
 typedef enum codec_lm_type { CODEC_LM_BF16 = 0, CODEC_LM_FP16 = 1, CODEC_LM_FP32 = 2 } codec_lm_type;
@@ -817,6 +824,147 @@ CODEC_API codec_status codec_lm_step(codec_lm_t* lm, const void* q, int64_t q_st
                                      const void* v_cache, const int32_t* tables, const int32_t* kv_len,
                                      const int32_t* shared_table, int32_t shared_blocks, void* o, int64_t o_stride,
                                      float* lse, void* stream);
+
+/*
+ * The cache in 4 bits: uint8 [n_blocks][kv_heads][block_size * head_dim * 5 / 8],
+ * 5 bits a value in all.  32 values of a head make a group: with lo and hi the
+ * least and the largest of them, low = fp16(lo), scale = fp16((hi - lo) * (1 / 15)),
+ * a value's code is rint((x - low) * (1 / scale)) within 0 .. 15 (0 where scale
+ * is 0), each step in fp32, and stands for low + scale * code.  Values beyond
+ * +-65504 count as that; a group that holds one that is not finite stands for
+ * NaN, all of it.
+ * Layout: tiles of 16 positions of one head, 10 * head_dim bytes each.  G =
+ * head_dim / 32; position p of the tile; value i of the head, g = i / 32, e = i % 32:
+ *   keys    code: byte p * head_dim / 2 + (e / 8 * G + g) * 4 + e % 8 / 2, upper half for odd e;
+ *           fp16 scale and low: bytes 8 * head_dim + (p * G + g) * 4 and + 2
+ *   values  a = p / 8, t = p % 8 / 2, b = p % 2;
+ *           code: byte a * 4 * head_dim + (e / 4 * 4 + t) * 4 * G + g * 4 + b * 2 + e % 4 / 2, upper half for odd e;
+ *           fp16 scale: byte 8 * head_dim + ((t * G + g) * 4 + 2 * a + b) * 2, low: head_dim bytes further
+ * (what one thread of the attention takes lies together).  A position's bytes
+ * are its own: rows of one call may lie in the same block.
+ *
+ * codec_lm_store_q4: keys and values of rows (in_type, strides and slots as for
+ * codec_lm_rotate; different slots; -1: left out) into their slots.
+ * Errors: CODEC_ERR_NULL, CODEC_ERR_ARG (rows < 0, in_type, a stride below the row or
+ * misaligned, caches not on 16 bytes or the same), CODEC_ERR_CAPACITY, CODEC_ERR_CUDA.
+ */
+CODEC_API codec_status codec_lm_store_q4(codec_lm_t* lm, const void* k, int64_t k_stride, const void* v,
+                                         int64_t v_stride, int32_t in_type, int32_t rows, const int32_t* slots,
+                                         void* k_cache, void* v_cache, void* stream);
+
+/*
+ * Blocks of the cache in 4 bits back in the object's type, for a prompt's
+ * attention behind them: block src[i] to block dst[i] of k_dst, v_dst [dst_blocks]
+ * [block_size][kv_heads][head_dim], i < n (int32, device; dst different from one
+ * another; src of -1: left out).  A whole block each: positions that nothing was
+ * stored to hold what their bytes stand for.  fp16 results beyond 65504 are cut
+ * to that.  An id out of range is left out and sets CODEC_LM_ERR_BLOCK.
+ * Errors: CODEC_ERR_NULL, CODEC_ERR_ARG (n < 0, dst_blocks < 1 or too many for
+ * 2^31 - 128 positions, alignment of 16 bytes, one of the destinations a cache
+ * or the other one), CODEC_ERR_CUDA.
+ */
+CODEC_API codec_status codec_lm_load_q4(codec_lm_t* lm, const void* k_cache, const void* v_cache, const int32_t* src,
+                                        const int32_t* dst, int32_t n, void* k_dst, void* v_dst, int32_t dst_blocks,
+                                        void* stream);
+
+/* codec_lm_step over the cache in 4 bits.  Queries and outputs are of the
+ * object's type; scores, sums and the codes' products are fp32, probabilities
+ * (with a value group's scale) fp16.  Errors as codec_lm_step. */
+CODEC_API codec_status codec_lm_step_q4(codec_lm_t* lm, const void* q, int64_t q_stride, int32_t B,
+                                        const void* k_cache, const void* v_cache, const int32_t* tables,
+                                        const int32_t* kv_len, const int32_t* shared_table, int32_t shared_blocks,
+                                        void* o, int64_t o_stride, float* lse, void* stream);
+
+/*
+ * Beam search's selection.  logits [rows][vocab] (in_type, rows `stride` elements
+ * apart), rows = groups * beams; sums float [rows]: the log-probability of each
+ * beam so far; ended int32 [rows].  A beam's candidates are its tokens, with
+ * sums + logit - log(sum(exp(logits of the row))); one whose ended is not 0 has
+ * itself alone, with end_token and the sum it has.  Each group's best `beams`
+ * candidates become its rows, best first; of equal ones the lower beam's, then
+ * the lower token.  Candidates are compared as 64-bit arithmetic finds them
+ * (within 1e-8), whatever their type.
+ *   sums_out float, parents (a row), tokens, ended_out (1: the token is
+ *              end_token) int32 [rows].  A row that no candidate is left for:
+ *              sum -inf, parent -1, token -1, ended 1.
+ * -inf is a logit like others; a beam whose sum is not finite, or whose logits
+ * hold a NaN, +inf or nothing but -inf, offers nothing, and neither does a
+ * candidate of -inf.  Outputs are not inputs.
+ * Errors: CODEC_ERR_NULL, CODEC_ERR_ARG (groups < 1, beams outside [1, 32], vocab
+ * outside [2, 2^24], stride < vocab or above 2^32, in_type none of the three, logits not on
+ * its size, end_token outside [-1, vocab); -1: none ends), CODEC_ERR_CAPACITY (rows
+ * above max_requests), CODEC_ERR_CUDA.
+ */
+CODEC_API codec_status codec_lm_beams(codec_lm_t* lm, const void* logits, int64_t stride, int32_t in_type,
+                                      int32_t groups, int32_t beams, int32_t vocab, const float* sums,
+                                      const int32_t* ended, int32_t end_token, float* sums_out, int32_t* parents,
+                                      int32_t* tokens, int32_t* ended_out, void* stream);
+
+/*
+ * Rows that go on from others (beams, samples of one prompt): row b becomes row
+ * parents[b] as it was, -1: it ends.  Blocks that are full are held by all rows
+ * that go on with them; a last block that is not full goes to the first of its
+ * row's children, and the others get a block each to copy it to (copy_src,
+ * copy_dst: codec_lm_copy does it, for every layer's caches).  A block that no row
+ * holds any more goes back to the free ones, in ascending order of ids.
+ *   parents    int32 [B];  len int32 [B]: positions of each row before
+ *   tables     int32 [B][table_blocks] before; tables_out: after, entries behind
+ *              a row's length stay as they were
+ *   shared_blocks  the first blocks of every row are nobody's: copied as entries,
+ *              neither counted nor given back (as for codec_lm_plan)
+ *   owners     int32 [n_blocks] before: rows that hold the block beyond the first (0
+ *              for one that codec_lm_plan has handed out, or a free one); owners_out: after
+ *   free_list, free_in, free_out  as for codec_lm_plan; ids that are given back
+ *              here can be taken by the next call
+ *   kv_len     int32 [B]: the row's length after, 0 where it ended or status is not 0
+ *   status     int32 [B]: 0; 1 the free blocks ran out at or before this row, which
+ *              needs one (it ends); 2 a parent outside [-1, B), or the parent's length
+ *              outside [0, table_blocks * block_size] (it ends, and such a parent
+ *              holds nothing)
+ *   copy_src, copy_dst  int32 [B], copies int32 [1]: the first `copies` entries
+ *              are written, in order of rows
+ * Rows whose last blocks are held by others too may grow (codec_lm_plan) but not
+ * shrink, and end by codec_lm_fork.  All arrays device memory; no array is another.
+ * A repeated call with the same inputs writes the same outputs.
+ * Errors: CODEC_ERR_NULL, CODEC_ERR_ARG (B < 1, shared_blocks outside [0, table_blocks],
+ * an output that is an input), CODEC_ERR_CAPACITY, CODEC_ERR_CUDA.
+ */
+CODEC_API codec_status codec_lm_fork(codec_lm_t* lm, const int32_t* parents, const int32_t* len, int32_t B,
+                                     const int32_t* tables, int32_t* tables_out, int32_t shared_blocks,
+                                     const int32_t* owners, int32_t* owners_out, int32_t* free_list,
+                                     const int64_t* free_in, int64_t* free_out, int32_t* kv_len, int32_t* status,
+                                     int32_t* copy_src, int32_t* copy_dst, int32_t* copies, void* stream);
+
+/*
+ * Moves the blocks in use to the front: with U blocks held (by the B rows of len
+ * positions, or shared), those with ids of U and above go to the free ids below
+ * U, lowest to lowest.  tables_out (entries behind a row's length stay as they
+ * were), shared_out, owners_out follow; free_list becomes U, U + 1, .. n_blocks - 1
+ * and free_out 0 and n_blocks - U.  copy_src, copy_dst int32 [n_blocks / 2]: the
+ * first copies[0] are written, ascending, for codec_lm_copy (no destination is a
+ * source).  A block that no row holds is free here, whatever the ring said.
+ * owners may be NULL (then owners_out is too).  An id outside [0, n_blocks) stays
+ * as it is and sets CODEC_LM_ERR_BLOCK; a length out of range is bent.
+ * Arrays, errors as codec_lm_fork.
+ */
+CODEC_API codec_status codec_lm_compact(codec_lm_t* lm, const int32_t* len, int32_t B, const int32_t* tables,
+                                        int32_t* tables_out, const int32_t* shared_table, int32_t* shared_out,
+                                        int32_t shared_blocks, const int32_t* owners, int32_t* owners_out,
+                                        int32_t* free_list, int64_t* free_out, int32_t* copy_src, int32_t* copy_dst,
+                                        int32_t* copies, void* stream);
+
+/*
+ * Copies block src[i] to block dst[i], i < min(copies[0], n), in each of n_caches
+ * caches (a host array of device pointers; [n_blocks][block_bytes] each, of any
+ * type).  src, dst int32 [n], copies int32 [1], device; copies NULL: n.  No block is
+ * both source and destination, none twice a destination.  An id out of range is
+ * left out and sets CODEC_LM_ERR_BLOCK.
+ * Errors: CODEC_ERR_NULL, CODEC_ERR_ARG (n < 0, n_caches outside [1, 256], block_bytes
+ * not a positive multiple of 16 or above 2^28, a cache not on 16 bytes), CODEC_ERR_CUDA.
+ */
+CODEC_API codec_status codec_lm_copy(codec_lm_t* lm, void* const* caches, int32_t n_caches, int64_t block_bytes,
+                                     const int32_t* src, const int32_t* dst, int32_t n, const int32_t* copies,
+                                     void* stream);
 
 /* Static description of a status code. */
 CODEC_API const char* codec_status_string(codec_status status);

@@ -201,6 +201,13 @@ def _lib():
             "codec_lm_prompt": (i32, [_P, _P, i64, _P, i64, _P, i64, i32, _P, i32, _P, i64, _P, _P]),
             "codec_lm_prompt_paged": (i32, [_P, _P, i64, i32, _P, i32, _P, _P, _P, _P, _P, i64, _P, _P]),
             "codec_lm_step": (i32, [_P, _P, i64, i32, _P, _P, _P, _P, _P, i32, _P, i64, _P, _P]),
+            "codec_lm_store_q4": (i32, [_P, _P, i64, _P, i64, i32, i32, _P, _P, _P, _P]),
+            "codec_lm_load_q4": (i32, [_P, _P, _P, _P, _P, i32, _P, _P, i32, _P]),
+            "codec_lm_step_q4": (i32, [_P, _P, i64, i32, _P, _P, _P, _P, _P, i32, _P, i64, _P, _P]),
+            "codec_lm_beams": (i32, [_P, _P, i64, i32, i32, i32, i32, _P, _P, i32, _P, _P, _P, _P, _P]),
+            "codec_lm_fork": (i32, [_P, _P, _P, i32, _P, _P, i32, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P]),
+            "codec_lm_compact": (i32, [_P, _P, i32, _P, _P, _P, _P, i32, _P, _P, _P, _P, _P, _P, _P, _P]),
+            "codec_lm_copy": (i32, [_P, ctypes.POINTER(_P), i32, i64, _P, _P, i32, _P, _P]),
             "codec_stft_create": (i32, [ctypes.POINTER(StftConfigC), ctypes.POINTER(_P)]),
             "codec_stft_destroy": (None, [_P]),
             "codec_stft_reset": (i32, [_P, _I32P, i32, _P]),
@@ -488,7 +495,7 @@ class Stft(_Streamed):
 
 
 LM_TYPES = {"bf16": 0, "fp16": 1, "fp32": 2}
-LM_ERR_BLOCK, LM_ERR_SLOT, LM_ERR_POSITION, LM_ERR_LENGTH, LM_ERR_FREE = 1, 2, 4, 8, 16
+LM_ERR_BLOCK, LM_ERR_SLOT, LM_ERR_POSITION, LM_ERR_LENGTH, LM_ERR_FREE, LM_ERR_OWNERS = 1, 2, 4, 8, 16, 32
 LM_ERR_TIMEOUT = 0x80000000
 
 
@@ -527,6 +534,11 @@ class Lm:
         self._plan, self._rotate, self._prompt = lib.codec_lm_plan, lib.codec_lm_rotate, lib.codec_lm_prompt
         self._prompt_paged, self._step = lib.codec_lm_prompt_paged, lib.codec_lm_step
         self._cache_shape = (n_blocks, block_size, kv_heads, head_dim)
+        self._store_q4, self._load_q4, self._step_q4 = lib.codec_lm_store_q4, lib.codec_lm_load_q4, lib.codec_lm_step_q4
+        self._beams, self._fork, self._compact, self._copy = (lib.codec_lm_beams, lib.codec_lm_fork,
+                                                              lib.codec_lm_compact, lib.codec_lm_copy)
+        self._logit_types = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
+        self._u8, self._q4_shape = torch.uint8, (n_blocks, kv_heads, block_size * head_dim * 5 // 8)
 
     def close(self):
         if getattr(self, "_h", None):
@@ -688,6 +700,138 @@ class Lm:
             self._current(self._index) if stream is None else stream.cuda_stream)
         if bad:
             raise CodecError(bad, "codec_lm_step")
+
+    def store_q4(self, k, v, slots, k_cache, v_cache, stream=None):
+        """codec_lm_store_q4: k and v [rows][kv_heads][head_dim] of the object's
+        type or float32, rows any distance apart, into slots (int32 [rows]) of
+        the caches in 4 bits: uint8 [n_blocks][kv_heads][block_size * head_dim * 5 / 8]."""
+        flat, fused, rows = self._flat, k.dtype, k.shape[0]
+        if rows == 0:
+            return
+        if fused is not self.dtype and fused is not self._f32:
+            raise ValueError(f"k must be {self.dtype} or torch.float32")
+        heads = (rows, self._hk, self._d)
+        bad = self._store_q4(
+            self._h, k.data_ptr(), self._stride("k", k, fused, heads), v.data_ptr(),
+            self._stride("v", v, fused, heads), self._type if fused is self.dtype else 2, rows,
+            flat("slots", slots, self._i32, (rows,)), flat("k_cache", k_cache, self._u8, self._q4_shape),
+            flat("v_cache", v_cache, self._u8, self._q4_shape),
+            self._current(self._index) if stream is None else stream.cuda_stream)
+        if bad:
+            raise CodecError(bad, "codec_lm_store_q4")
+
+    def load_q4(self, k_cache, v_cache, src, dst, k_dst, v_dst, stream=None):
+        """codec_lm_load_q4: blocks src (int32 [n]) of the caches in 4 bits to blocks
+        dst of k_dst, v_dst [any number][block_size][kv_heads][head_dim]."""
+        flat, i32, n = self._flat, self._i32, src.numel()
+        if n == 0:
+            return
+        shape = (k_dst.shape[0], *self._cache_shape[1:])
+        bad = self._load_q4(
+            self._h, flat("k_cache", k_cache, self._u8, self._q4_shape),
+            flat("v_cache", v_cache, self._u8, self._q4_shape), flat("src", src, i32, (n,)), flat("dst", dst, i32, (n,)),
+            n, flat("k_dst", k_dst, self.dtype, shape), flat("v_dst", v_dst, self.dtype, shape), shape[0],
+            self._current(self._index) if stream is None else stream.cuda_stream)
+        if bad:
+            raise CodecError(bad, "codec_lm_load_q4")
+
+    def step_q4(self, q, k_cache, v_cache, tables, kv_len, o, shared_table=None, lse=None, stream=None):
+        """codec_lm_step_q4: `step` over the caches in 4 bits."""
+        flat, dtype, i32 = self._flat, self.dtype, self._i32
+        B = q.shape[0]
+        shared = 0 if shared_table is None else shared_table.numel()
+        wide = (B, self._hq, self._d)
+        bad = self._step_q4(
+            self._h, q.data_ptr(), self._stride("q", q, dtype, wide), B,
+            flat("k_cache", k_cache, self._u8, self._q4_shape), flat("v_cache", v_cache, self._u8, self._q4_shape),
+            flat("tables", tables, i32, (B, self._width)), flat("kv_len", kv_len, i32, (B,)),
+            flat("shared_table", shared_table, i32, (shared,)) if shared else None, shared, o.data_ptr(),
+            self._stride("o", o, dtype, wide), None if lse is None else flat("lse", lse, self._f32, (B, self._hq)),
+            self._current(self._index) if stream is None else stream.cuda_stream)
+        if bad:
+            raise CodecError(bad, "codec_lm_step_q4")
+
+    def beams(self, logits, beams, sums, ended, end_token, sums_out, parents, tokens, ended_out, stream=None):
+        """codec_lm_beams: the best `beams` continuations of each group of as many
+        rows.  logits [rows][vocab] of bfloat16, float16 or float32, rows any
+        distance apart; sums, sums_out float32 [rows]; ended, parents, tokens,
+        ended_out int32 [rows]; end_token -1: none ends."""
+        flat, i32, f32 = self._flat, self._i32, self._f32
+        if logits.dim() != 2 or logits.dtype not in self._logit_types or logits.get_device() != self._index or (
+                logits.shape[1] > 1 and logits.stride(1) != 1):
+            raise ValueError(f"logits must be bfloat16, float16 or float32 [rows][vocab] on {self.device}, values of a "
+                             f"row back to back, got {logits.dtype} {tuple(logits.shape)}, strides {logits.stride()}")
+        rows, vocab = logits.shape
+        if beams < 1 or rows % beams:
+            raise ValueError(f"{rows} rows are not groups of {beams} beams")
+        per = (rows,)
+        bad = self._beams(
+            self._h, logits.data_ptr(), logits.stride(0) if rows > 1 else vocab, self._logit_types[logits.dtype],
+            rows // beams, beams, vocab, flat("sums", sums, f32, per), flat("ended", ended, i32, per), end_token,
+            flat("sums_out", sums_out, f32, per), flat("parents", parents, i32, per), flat("tokens", tokens, i32, per),
+            flat("ended_out", ended_out, i32, per), self._current(self._index) if stream is None else stream.cuda_stream)
+        if bad:
+            raise CodecError(bad, "codec_lm_beams")
+
+    def fork(self, parents, kv_len, tables, tables_out, owners, owners_out, free_list, free_in, free_out, kv_out,
+             status, copy_src, copy_dst, copies, shared_blocks=0, stream=None):
+        """codec_lm_fork: row b goes on as row parents[b].  int32 parents, kv_len,
+        kv_out, status, copy_src, copy_dst [B]; tables, tables_out
+        [B][table_blocks]; owners, owners_out, free_list [n_blocks]; copies [1];
+        int64 free_in, free_out [2]."""
+        flat, i32, B = self._flat, self._i32, parents.numel()
+        per, wide, ring, two = (B,), (B, self._width), self._ring_shape, (2,)
+        bad = self._fork(
+            self._h, flat("parents", parents, i32, per), flat("kv_len", kv_len, i32, per), B,
+            flat("tables", tables, i32, wide), flat("tables_out", tables_out, i32, wide), shared_blocks,
+            flat("owners", owners, i32, ring), flat("owners_out", owners_out, i32, ring),
+            flat("free_list", free_list, i32, ring), flat("free_in", free_in, self._i64, two),
+            flat("free_out", free_out, self._i64, two), flat("kv_out", kv_out, i32, per),
+            flat("status", status, i32, per), flat("copy_src", copy_src, i32, per), flat("copy_dst", copy_dst, i32, per),
+            flat("copies", copies, i32, (1,)), self._current(self._index) if stream is None else stream.cuda_stream)
+        if bad:
+            raise CodecError(bad, "codec_lm_fork")
+
+    def compact(self, kv_len, tables, tables_out, owners, owners_out, free_list, free_out, copy_src, copy_dst, copies,
+                shared_table=None, shared_out=None, stream=None):
+        """codec_lm_compact: blocks in use to the front.  Shapes as for `fork`;
+        copy_src, copy_dst int32 [n_blocks // 2]; owners, owners_out or both None."""
+        flat, i32, B = self._flat, self._i32, kv_len.numel()
+        wide, ring, half = (B, self._width), self._ring_shape, (self._ring_shape[0] // 2,)
+        shared = 0 if shared_table is None else shared_table.numel()
+        bad = self._compact(
+            self._h, flat("kv_len", kv_len, i32, (B,)), B, flat("tables", tables, i32, wide),
+            flat("tables_out", tables_out, i32, wide),
+            flat("shared_table", shared_table, i32, (shared,)) if shared else None,
+            flat("shared_out", shared_out, i32, (shared,)) if shared else None, shared,
+            None if owners is None else flat("owners", owners, i32, ring),
+            None if owners_out is None else flat("owners_out", owners_out, i32, ring),
+            flat("free_list", free_list, i32, ring), flat("free_out", free_out, self._i64, (2,)),
+            flat("copy_src", copy_src, i32, half), flat("copy_dst", copy_dst, i32, half),
+            flat("copies", copies, i32, (1,)), self._current(self._index) if stream is None else stream.cuda_stream)
+        if bad:
+            raise CodecError(bad, "codec_lm_compact")
+
+    def copy_blocks(self, caches, src, dst, copies=None, stream=None):
+        """codec_lm_copy: blocks src to blocks dst (int32 [n]; the first copies[0],
+        or all) in each of `caches`, contiguous tensors [n_blocks][..] of one
+        number of bytes a block."""
+        n, size = src.numel(), 0
+        at = (_P * max(1, len(caches)))()
+        for i, t in enumerate(caches):
+            per = t.numel() // self._ring_shape[0] * t.element_size() if t.dim() > 1 else 0
+            if t.shape[:1] != self._ring_shape or t.get_device() != self._index or not t.is_contiguous() or per != (
+                    size or per) or per == 0:
+                raise ValueError(f"caches must be contiguous tensors [{self._ring_shape[0]}][..] on {self.device} with "
+                                 f"the same bytes a block, got {t.dtype} {tuple(t.shape)}, strides {t.stride()}")
+            size = per
+            at[i] = t.data_ptr()
+        bad = self._copy(self._h, at, len(caches), size, self._flat("src", src, self._i32, (n,)),
+                         self._flat("dst", dst, self._i32, (n,)), n,
+                         None if copies is None else self._flat("copies", copies, self._i32, (1,)),
+                         self._current(self._index) if stream is None else stream.cuda_stream)
+        if bad:
+            raise CodecError(bad, "codec_lm_copy")
 
     def errors(self, clear: bool = True, stream=None) -> int:
         """codec_lm_errors: the LM_ERR_* bits set since last cleared (synchronises the stream)."""

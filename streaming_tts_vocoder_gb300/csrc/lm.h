@@ -154,6 +154,99 @@ struct LmStepArgs {
 cudaError_t configure_lm_step();
 cudaError_t launch_lm_step(const LmShape& sh, const LmStepArgs& a, cudaStream_t s);
 
+// Single tokens over the cache in 4 bits (keys.k, keys.v: its bytes).
+cudaError_t launch_lm_step_q4(const LmShape& sh, const LmStepArgs& a, cudaStream_t s);
+
+struct LmStoreQ4Args {
+    const void *k, *v;
+    long long ks, vs;               // row strides, elements
+    int rows;
+    const int* slots;
+    long long n_slots;
+    int bs_shift;
+    void *k_cache, *v_cache;
+};
+cudaError_t launch_lm_store_q4(const LmShape& sh, const LmStoreQ4Args& a, int in_type, cudaStream_t s);
+
+struct LmLoadQ4Args {
+    const void *k_cache, *v_cache;
+    const int *src, *dst;
+    int n, bs_shift, n_blocks, dst_blocks;
+    void *k_dst, *v_dst;
+};
+cudaError_t launch_lm_load_q4(const LmShape& sh, const LmLoadQ4Args& a, cudaStream_t s);
+
+struct LmForkArgs {
+    const int *parents, *len;
+    int B;
+    const int* tables;
+    int* tables_out;
+    int shared_blocks, table_blocks, bs_shift, n_blocks;
+    const int* owners;
+    int* owners_out;
+    int* free_list;
+    const long long* free_in;
+    long long* free_out;
+    int *kv_len, *status, *copy_src, *copy_dst, *copies;
+    unsigned* err;
+};
+struct LmCompactArgs {
+    const int* len;
+    int B;
+    const int* tables;
+    int* tables_out;
+    const int* shared_table;
+    int* shared_out;
+    int shared_blocks, table_blocks, bs_shift, n_blocks;
+    const int* owners;
+    int* owners_out;
+    int* free_list;
+    long long* free_out;
+    int *copy_src, *copy_dst, *copies;
+    int* map;                       // workspace [n_blocks]
+    unsigned* err;
+};
+constexpr int kLmMaxCaches = 256;
+struct LmCopyArgs {
+    const int *src, *dst, *copies;
+    int n, n_caches, n_blocks;
+    long long block_bytes;
+    unsigned* err;
+    void* caches[kLmMaxCaches];
+};
+cudaError_t configure_lm_pages();
+cudaError_t launch_lm_fork(const LmForkArgs& a, cudaStream_t s);
+cudaError_t launch_lm_compact(const LmCompactArgs& a, cudaStream_t s);
+cudaError_t launch_lm_copy(const LmCopyArgs& a, cudaStream_t s);
+
+// Beam search: the best candidates of a part of a row, and its maximum and sum.
+constexpr int kLmMaxBeams = 32;
+struct LmBeamPart {
+    double sum;                     // of exp(x - top)
+    float top;
+    int pad;
+};
+struct LmBeamSpace {
+    int parts;                      // that the workspace holds
+    LmBeamPart* part;               // [parts]
+    uint2* best;                    // [parts][kLmMaxBeams]: logit's bits (fp32), token
+};
+inline int lm_beam_parts(int max_requests) { return max_requests + 152 * 32; }
+
+struct LmBeamArgs {
+    const void* logits;
+    long long stride;
+    int type;
+    int groups, beams, vocab;
+    const float* sums;
+    const int* ended;
+    int end_token;
+    float* sums_out;
+    int *parents, *tokens, *ended_out;
+    LmBeamSpace ws;
+};
+cudaError_t launch_lm_beams(const LmBeamArgs& a, cudaStream_t s);
+
 // Tensor map of [rows][heads][D] 16-bit values, rows `stride` elements apart,
 // boxes of 64 elements x box_heads x box_rows.
 bool lm_make_map(CUtensorMap* map, int type, const void* base, int D, int heads, long long rows, long long stride,

@@ -16,6 +16,8 @@ struct codec_lm_s {
     unsigned* err = nullptr;
     LmStepSpace step{};
     LmPromptSpace prompt{};
+    LmBeamSpace beam{};
+    int* block_map = nullptr;
 };
 
 namespace {
@@ -52,6 +54,9 @@ void lm_free(codec_lm_s* lm)
     cudaFree(lm->prompt.joins);
     cudaFree(lm->prompt.piece);
     cudaFree(lm->prompt.piece_lse);
+    cudaFree(lm->beam.part);
+    cudaFree(lm->beam.best);
+    cudaFree(lm->block_map);
     delete lm;
 }
 
@@ -126,6 +131,8 @@ codec_status codec_lm_create(const codec_lm_config* cfg, codec_lm_t** out)
     sp.shared_ctas = (int)(pairs * c.kv_heads);
     sp.heads = heads;
     const int pre_max = lm_shared_splits(sp.shared_ctas, positions);
+    LmBeamSpace& bm = lm->beam;
+    bm.parts = lm_beam_parts(c.max_requests);
     LmPromptSpace& pr = lm->prompt;
     const size_t items = (size_t)lm_list_items(c.max_rows, c.max_requests, c.q_heads / c.kv_heads) + kLmSlots;
     const size_t row = (size_t)c.max_requests * c.q_heads;
@@ -139,6 +146,9 @@ codec_status codec_lm_create(const codec_lm_config* cfg, codec_lm_t** out)
         cudaMalloc(&pr.joins, 16 * kLmSlots) != cudaSuccess ||
         cudaMalloc(&pr.piece, sizeof(float) * kLmSlots * 256 * c.head_dim) != cudaSuccess ||
         cudaMalloc(&pr.piece_lse, sizeof(float) * kLmSlots * 256) != cudaSuccess ||
+        cudaMalloc(&bm.part, sizeof(LmBeamPart) * bm.parts) != cudaSuccess ||
+        cudaMalloc(&bm.best, sizeof(uint2) * kLmMaxBeams * (size_t)bm.parts) != cudaSuccess ||
+        cudaMalloc(&lm->block_map, sizeof(int) * (size_t)c.n_blocks) != cudaSuccess ||
         cudaMalloc(&sp.done, sizeof(int) * ((size_t)c.max_requests * c.kv_heads + 1)) != cudaSuccess) {
         cudaGetLastError();
         lm_free(lm);
@@ -147,7 +157,7 @@ codec_status codec_lm_create(const codec_lm_config* cfg, codec_lm_t** out)
     sp.taken = sp.done + (size_t)c.max_requests * c.kv_heads;
     lm->shape = LmShape{c.type, c.q_heads, c.kv_heads, c.q_heads / c.kv_heads, c.head_dim, c.scale, lm->err, 0};
     if (configure_lm_plan() != cudaSuccess || configure_lm_prompt() != cudaSuccess ||
-        configure_lm_step() != cudaSuccess || cudaMemset(sp.done, 0, sizeof(int) * ((size_t)c.max_requests * c.kv_heads + 1)) != cudaSuccess ||
+        configure_lm_step() != cudaSuccess || configure_lm_pages() != cudaSuccess || cudaMemset(sp.done, 0, sizeof(int) * ((size_t)c.max_requests * c.kv_heads + 1)) != cudaSuccess ||
         cudaMemset(lm->err, 0, sizeof(unsigned)) != cudaSuccess ||
         launch_lm_turn_table(lm->turn, c.max_positions, c.head_dim, c.rope_theta, nullptr) != cudaSuccess ||
         cudaDeviceSynchronize() != cudaSuccess) {
@@ -295,4 +305,153 @@ codec_status codec_lm_step(codec_lm_t* lm, const void* q, int64_t q_stride, int3
     LmStepArgs a{q, q_stride, B, paged(lm, k_cache, v_cache, tables, kv_len), shared_table, shared_blocks, o,
                  o_stride, lse, lm->step};
     return done(launch_lm_step(lm->shape, a, static_cast<cudaStream_t>(stream)));
+}
+
+codec_status codec_lm_store_q4(codec_lm_t* lm, const void* k, int64_t k_stride, const void* v, int64_t v_stride,
+                               int32_t in_type, int32_t rows, const int32_t* slots, void* k_cache, void* v_cache,
+                               void* stream)
+{
+    if (!lm || !k || !v || !slots || !k_cache || !v_cache) return CODEC_ERR_NULL;
+    const codec_lm_config& c = lm->cfg;
+    const int64_t nk = (int64_t)c.kv_heads * c.head_dim;
+    const int size = in_type == CODEC_LM_FP32 ? 4 : 2;
+    if (rows < 0 || (in_type != c.type && in_type != CODEC_LM_FP32) || !row_ok(k, k_stride, nk, size) ||
+        !row_ok(v, v_stride, nk, size) || !aligned16(k_cache) || !aligned16(v_cache) || k_cache == v_cache ||
+        k == k_cache || k == v_cache || v == k_cache || v == v_cache)
+        return CODEC_ERR_ARG;
+    if (rows > c.max_rows) return CODEC_ERR_CAPACITY;
+    if (rows == 0) return CODEC_OK;
+    OnDevice on(lm->device);
+    if (!on.ok) return CODEC_ERR_CUDA;
+    LmStoreQ4Args a{k, v, k_stride, v_stride, rows, slots, (int64_t)c.n_blocks * c.block_size, lm->bs_shift, k_cache,
+                    v_cache};
+    return done(launch_lm_store_q4(lm->shape, a, in_type, static_cast<cudaStream_t>(stream)));
+}
+
+codec_status codec_lm_load_q4(codec_lm_t* lm, const void* k_cache, const void* v_cache, const int32_t* src,
+                              const int32_t* dst, int32_t n, void* k_dst, void* v_dst, int32_t dst_blocks,
+                              void* stream)
+{
+    if (!lm || !k_cache || !v_cache || !src || !dst || !k_dst || !v_dst) return CODEC_ERR_NULL;
+    const codec_lm_config& c = lm->cfg;
+    if (n < 0 || dst_blocks < 1 || (int64_t)dst_blocks * c.block_size >= (1LL << 31) - 128 || !aligned16(k_cache) ||
+        !aligned16(v_cache) || !aligned16(k_dst) || !aligned16(v_dst) || k_dst == v_dst || k_dst == k_cache ||
+        k_dst == v_cache || v_dst == k_cache || v_dst == v_cache)
+        return CODEC_ERR_ARG;
+    if (n == 0) return CODEC_OK;
+    OnDevice on(lm->device);
+    if (!on.ok) return CODEC_ERR_CUDA;
+    LmLoadQ4Args a{k_cache, v_cache, src, dst, n, lm->bs_shift, c.n_blocks, dst_blocks, k_dst, v_dst};
+    return done(launch_lm_load_q4(lm->shape, a, static_cast<cudaStream_t>(stream)));
+}
+
+codec_status codec_lm_step_q4(codec_lm_t* lm, const void* q, int64_t q_stride, int32_t B, const void* k_cache,
+                              const void* v_cache, const int32_t* tables, const int32_t* kv_len,
+                              const int32_t* shared_table, int32_t shared_blocks, void* o, int64_t o_stride,
+                              float* lse, void* stream)
+{
+    if (!lm || !q || !k_cache || !v_cache || !tables || !kv_len || (shared_blocks > 0 && !shared_table) || !o)
+        return CODEC_ERR_NULL;
+    const codec_lm_config& c = lm->cfg;
+    const int64_t nq = (int64_t)c.q_heads * c.head_dim;
+    if (B < 1 || shared_blocks < 0 || shared_blocks > c.table_blocks || !row_ok(q, q_stride, nq, 2) ||
+        !aligned16(k_cache) || !aligned16(v_cache) || !row_ok(o, o_stride, nq, 2) || o == q || o == k_cache ||
+        o == v_cache)
+        return CODEC_ERR_ARG;
+    if (B > c.max_requests) return CODEC_ERR_CAPACITY;
+    OnDevice on(lm->device);
+    if (!on.ok) return CODEC_ERR_CUDA;
+    LmStepArgs a{q, q_stride, B, paged(lm, k_cache, v_cache, tables, kv_len), shared_table, shared_blocks, o,
+                 o_stride, lse, lm->step};
+    return done(launch_lm_step_q4(lm->shape, a, static_cast<cudaStream_t>(stream)));
+}
+
+codec_status codec_lm_beams(codec_lm_t* lm, const void* logits, int64_t stride, int32_t in_type, int32_t groups,
+                            int32_t beams, int32_t vocab, const float* sums, const int32_t* ended, int32_t end_token,
+                            float* sums_out, int32_t* parents, int32_t* tokens, int32_t* ended_out, void* stream)
+{
+    if (!lm || !logits || !sums || !ended || !sums_out || !parents || !tokens || !ended_out) return CODEC_ERR_NULL;
+    const codec_lm_config& c = lm->cfg;
+    const bool typed = in_type == CODEC_LM_BF16 || in_type == CODEC_LM_FP16 || in_type == CODEC_LM_FP32;
+    const uintptr_t size = in_type == CODEC_LM_FP32 ? 4 : 2;
+    if (!typed || groups < 1 || beams < 1 || beams > kLmMaxBeams || vocab < 2 || vocab > (1 << 24) || stride < vocab ||
+        stride > (1LL << 32) || reinterpret_cast<uintptr_t>(logits) % size || end_token < -1 || end_token >= vocab ||
+        sums_out == sums || ended_out == ended || parents == ended || tokens == ended)
+        return CODEC_ERR_ARG;
+    if ((int64_t)groups * beams > c.max_requests) return CODEC_ERR_CAPACITY;
+    OnDevice on(lm->device);
+    if (!on.ok) return CODEC_ERR_CUDA;
+    LmBeamArgs a{logits, stride, in_type, groups, beams, vocab, sums, ended, end_token, sums_out, parents, tokens,
+                 ended_out, lm->beam};
+    return done(launch_lm_beams(a, static_cast<cudaStream_t>(stream)));
+}
+
+codec_status codec_lm_fork(codec_lm_t* lm, const int32_t* parents, const int32_t* len, int32_t B,
+                           const int32_t* tables, int32_t* tables_out, int32_t shared_blocks, const int32_t* owners,
+                           int32_t* owners_out, int32_t* free_list, const int64_t* free_in, int64_t* free_out,
+                           int32_t* kv_len, int32_t* status, int32_t* copy_src, int32_t* copy_dst, int32_t* copies,
+                           void* stream)
+{
+    if (!lm || !parents || !len || !tables || !tables_out || !owners || !owners_out || !free_list || !free_in ||
+        !free_out || !kv_len || !status || !copy_src || !copy_dst || !copies)
+        return CODEC_ERR_NULL;
+    const codec_lm_config& c = lm->cfg;
+    if (B < 1 || shared_blocks < 0 || shared_blocks > c.table_blocks || tables == tables_out || owners == owners_out ||
+        free_in == free_out || kv_len == len || kv_len == parents || status == len || status == parents)
+        return CODEC_ERR_ARG;
+    if (B > c.max_requests) return CODEC_ERR_CAPACITY;
+    OnDevice on(lm->device);
+    if (!on.ok) return CODEC_ERR_CUDA;
+    LmForkArgs a{parents, len, B, tables, tables_out, shared_blocks, c.table_blocks, lm->bs_shift, c.n_blocks, owners,
+                 owners_out, free_list, reinterpret_cast<const long long*>(free_in),
+                 reinterpret_cast<long long*>(free_out), kv_len, status, copy_src, copy_dst, copies, lm->err};
+    return done(launch_lm_fork(a, static_cast<cudaStream_t>(stream)));
+}
+
+codec_status codec_lm_compact(codec_lm_t* lm, const int32_t* len, int32_t B, const int32_t* tables,
+                              int32_t* tables_out, const int32_t* shared_table, int32_t* shared_out,
+                              int32_t shared_blocks, const int32_t* owners, int32_t* owners_out, int32_t* free_list,
+                              int64_t* free_out, int32_t* copy_src, int32_t* copy_dst, int32_t* copies, void* stream)
+{
+    if (!lm || !len || !tables || !tables_out || (shared_blocks > 0 && (!shared_table || !shared_out)) || !free_list ||
+        !free_out || (lm->cfg.n_blocks > 1 && (!copy_src || !copy_dst)) || !copies || !owners != !owners_out)
+        return CODEC_ERR_NULL;
+    const codec_lm_config& c = lm->cfg;
+    if (B < 1 || shared_blocks < 0 || shared_blocks > c.table_blocks || tables == tables_out ||
+        (owners && owners == owners_out) || (shared_blocks > 0 && shared_table == shared_out))
+        return CODEC_ERR_ARG;
+    if (B > c.max_requests) return CODEC_ERR_CAPACITY;
+    OnDevice on(lm->device);
+    if (!on.ok) return CODEC_ERR_CUDA;
+    LmCompactArgs a{len, B, tables, tables_out, shared_table, shared_out, shared_blocks, c.table_blocks, lm->bs_shift,
+                    c.n_blocks, owners, owners_out, free_list, reinterpret_cast<long long*>(free_out), copy_src,
+                    copy_dst, copies, lm->block_map, lm->err};
+    return done(launch_lm_compact(a, static_cast<cudaStream_t>(stream)));
+}
+
+codec_status codec_lm_copy(codec_lm_t* lm, void* const* caches, int32_t n_caches, int64_t block_bytes,
+                           const int32_t* src, const int32_t* dst, int32_t n, const int32_t* copies, void* stream)
+{
+    if (!lm || !caches || !src || !dst) return CODEC_ERR_NULL;
+    if (n < 0 || n_caches < 1 || n_caches > kLmMaxCaches || block_bytes < 16 || block_bytes % 16 ||
+        block_bytes > (1LL << 28))
+        return CODEC_ERR_ARG;
+    LmCopyArgs a{};
+    for (int i = 0; i < n_caches; i++) {
+        if (!caches[i]) return CODEC_ERR_NULL;
+        if (!aligned16(caches[i])) return CODEC_ERR_ARG;
+        a.caches[i] = caches[i];
+    }
+    if (n == 0) return CODEC_OK;
+    OnDevice on(lm->device);
+    if (!on.ok) return CODEC_ERR_CUDA;
+    a.src = src;
+    a.dst = dst;
+    a.copies = copies;
+    a.n = n;
+    a.n_caches = n_caches;
+    a.n_blocks = lm->cfg.n_blocks;
+    a.block_bytes = block_bytes;
+    a.err = lm->err;
+    return done(launch_lm_copy(a, static_cast<cudaStream_t>(stream)));
 }

@@ -1,0 +1,238 @@
+// Keys and values into the cache in 4 bits, and blocks of it back in 16.
+#include "lm.h"
+#include "lm_q4.cuh"
+
+namespace codec {
+
+namespace {
+
+constexpr int kThreads = 128;
+
+__device__ __forceinline__ void load8(const float* p, float* x)
+{
+    const float4 a = *reinterpret_cast<const float4*>(p), b = *(reinterpret_cast<const float4*>(p) + 1);
+    x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
+    x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
+}
+__device__ __forceinline__ float2 unpack2(uint32_t w, const __half*)
+{
+    return __half22float2(*reinterpret_cast<const __half2*>(&w));
+}
+__device__ __forceinline__ float2 unpack2(uint32_t w, const __nv_bfloat16*)
+{
+    return __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&w));
+}
+template <typename T>
+__device__ __forceinline__ void load8(const T* p, float* x)
+{
+    const uint4 w = *reinterpret_cast<const uint4*>(p);
+    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+        const float2 f = unpack2(u[i], p);
+        x[2 * i] = f.x;
+        x[2 * i + 1] = f.y;
+    }
+}
+
+// Codes of 8 values, four lanes a group.  The steps and their roundings are the
+// format's: no contraction, no approximate reciprocal.
+__device__ __forceinline__ uint32_t encode(const float* in, __half& scale, __half& low)
+{
+    const int lane = threadIdx.x & 31;
+    float x[8], lo = INFINITY, hi = -INFINITY;
+    bool good = true;
+#pragma unroll
+    for (int i = 0; i < 8; i++) {
+        good &= fabsf(in[i]) < INFINITY;
+        x[i] = fminf(fmaxf(in[i], -65504.f), 65504.f);
+        lo = fminf(lo, x[i]);
+        hi = fmaxf(hi, x[i]);
+    }
+#pragma unroll
+    for (int o = 1; o < 4; o <<= 1) {
+        lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, o));
+        hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, o));
+    }
+    good = (__ballot_sync(0xffffffffu, !good) >> (lane & 28) & 15u) == 0;
+    scale = __float2half_rn(__fmul_rn(__fsub_rn(hi, lo), 1.f / 15.f));
+    low = __float2half_rn(lo);
+    const float s = __half2float(scale), l = __half2float(low);
+    const float inv = __frcp_rn(s);
+    uint32_t word = 0;
+#pragma unroll
+    for (int i = 0; i < 8; i++) {
+        const float c = fminf(fmaxf(rintf(__fmul_rn(__fsub_rn(x[i], l), inv)), 0.f), 15.f);
+        word |= (uint32_t)c << (4 * i);
+    }
+    if (!good) scale = low = __ushort_as_half(0x7fff);
+    return good && s > 0.f ? word : 0u;
+}
+
+struct StoreArgs {
+    const void *k, *v;
+    long long ks, vs;
+    int rows, hk, bs_shift, parts;
+    const int* slots;
+    long long n_slots;
+    uint8_t *k_cache, *v_cache;
+    unsigned* err;
+};
+
+// Warp w of the grid: row w / parts, and every parts-th set of 256 / D heads of
+// it; keys or values by blockIdx.y.
+template <typename TI, int D>
+__global__ void __launch_bounds__(kThreads) lm_store_q4_kernel(const StoreArgs a)
+{
+    using Tile = Q4Tile<D>;
+    constexpr int kLanes = D / 8, kHeads = 32 / kLanes;
+    const int warp = (int)((blockIdx.x * (long long)kThreads + threadIdx.x) >> 5);
+    const int row = warp / a.parts, part = warp - row * a.parts;
+    pdl_wait();
+    pdl_launch();
+    if (row >= a.rows) return;
+    const int lane = threadIdx.x & 31, c = lane % kLanes, g = c >> 2, t = c & 3;
+    const int slot = __ldg(a.slots + row);
+    if (slot == -1) return;
+    if (slot < 0 || slot >= a.n_slots) {
+        if (lane == 0) atomicOr(a.err, CODEC_LM_ERR_SLOT);
+        return;
+    }
+    const bool values = blockIdx.y == 1;
+    const TI* src = static_cast<const TI*>(values ? a.v : a.k) + row * (values ? a.vs : a.ks) + c * 8;
+    const int block = slot >> a.bs_shift, pos = slot & ((1 << a.bs_shift) - 1), p = pos & 15;
+    const long long head_bytes = (long long)Tile::kBytes << (a.bs_shift - 4);
+    uint8_t* base = (values ? a.v_cache : a.k_cache) + (long long)block * a.hk * head_bytes + (pos >> 4) * Tile::kBytes;
+    for (int h0 = part * kHeads; h0 < a.hk; h0 += a.parts * kHeads) {
+        const int h = h0 + lane / kLanes;
+        float x[8];
+        load8(src + (long long)min(h, a.hk - 1) * D, x);
+        __half scale, low;
+        const uint32_t word = encode(x, scale, low);
+        if (h >= a.hk) continue;
+        uint8_t* tile = base + h * head_bytes;
+        if (!values) {
+            *reinterpret_cast<uint32_t*>(tile + Tile::k_word(p, t, g)) = word;
+            if (t == 0) *reinterpret_cast<__half2*>(tile + Tile::k_param(p, g)) = __halves2half2(scale, low);
+        } else {
+            *reinterpret_cast<uint16_t*>(tile + Tile::v_pair(p, 2 * t, g)) = (uint16_t)word;
+            *reinterpret_cast<uint16_t*>(tile + Tile::v_pair(p, 2 * t + 1, g)) = (uint16_t)(word >> 16);
+            if (t == 0) {
+                *reinterpret_cast<__half*>(tile + Tile::v_scale(p, g)) = scale;
+                *reinterpret_cast<__half*>(tile + Tile::v_scale(p, g) + D) = low;
+            }
+        }
+    }
+}
+
+struct LoadArgs {
+    const uint8_t *k_cache, *v_cache;
+    const int *src, *dst;
+    int n, hk, bs_shift, n_blocks, dst_blocks;
+    void *k_dst, *v_dst;
+    unsigned* err;
+};
+
+__device__ __forceinline__ uint32_t pack2(float a, float b, const __nv_bfloat16*)
+{
+    const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&v);
+}
+__device__ __forceinline__ uint32_t pack2(float a, float b, const __half*)
+{
+    // low + 15 scale may pass fp16's largest by the scale's rounding (NaN stays)
+    const __half2 v = __floats2half2_rn(a > 65504.f ? 65504.f : a, b > 65504.f ? 65504.f : b);
+    return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+// A warp per tile of 16 positions; keys or values by blockIdx.y.
+template <typename T, int D>
+__global__ void __launch_bounds__(kThreads) lm_load_q4_kernel(const LoadArgs a)
+{
+    using Tile = Q4Tile<D>;
+    constexpr int kLanes = D / 8, kRows = 32 / kLanes;
+    const int lane = threadIdx.x & 31, c = lane % kLanes, g = c >> 2, t = c & 3;
+    const bool values = blockIdx.y == 1;
+    const uint8_t* cache = values ? a.v_cache : a.k_cache;
+    T* out = static_cast<T*>(values ? a.v_dst : a.k_dst);
+    pdl_wait();
+    pdl_launch();
+    const int tiles = 1 << (a.bs_shift - 4);
+    const long long all = (long long)a.n * a.hk * tiles;
+    for (long long w = (blockIdx.x * (long long)kThreads + threadIdx.x) >> 5; w < all;
+         w += gridDim.x * (long long)(kThreads / 32)) {
+        const int tile = (int)(w % tiles), i = (int)(w / tiles / a.hk), h = (int)(w / tiles - (long long)i * a.hk);
+        const int from = __ldg(a.src + i), to = __ldg(a.dst + i);
+        if (from == -1) continue;
+        if (from < 0 || from >= a.n_blocks || to < 0 || to >= a.dst_blocks) {
+            if (lane == 0) atomicOr(a.err, CODEC_LM_ERR_BLOCK);
+            continue;
+        }
+        const uint8_t* at = cache + (((long long)from * a.hk + h) * tiles + tile) * Tile::kBytes;
+        T* row = out + ((((long long)to << a.bs_shift) + tile * 16) * a.hk + h) * D + c * 8;
+#pragma unroll
+        for (int p0 = 0; p0 < 16; p0 += kRows) {
+            const int p = p0 + lane / kLanes;
+            uint32_t word;
+            float scale, low;
+            if (!values) {
+                word = __ldg(reinterpret_cast<const uint32_t*>(at + Tile::k_word(p, t, g)));
+                const float2 f = __half22float2(__ldg(reinterpret_cast<const __half2*>(at + Tile::k_param(p, g))));
+                scale = f.x;
+                low = f.y;
+            } else {
+                word = __ldg(reinterpret_cast<const uint16_t*>(at + Tile::v_pair(p, 2 * t, g))) |
+                       (uint32_t)__ldg(reinterpret_cast<const uint16_t*>(at + Tile::v_pair(p, 2 * t + 1, g))) << 16;
+                scale = __half2float(__ldg(reinterpret_cast<const __half*>(at + Tile::v_scale(p, g))));
+                low = __half2float(__ldg(reinterpret_cast<const __half*>(at + Tile::v_scale(p, g) + D)));
+            }
+            uint32_t o[4];
+#pragma unroll
+            for (int j = 0; j < 4; j++)
+                o[j] = pack2(fmaf(scale, (float)(word >> (8 * j) & 15u), low),
+                             fmaf(scale, (float)(word >> (8 * j + 4) & 15u), low), row);
+            *reinterpret_cast<uint4*>(row + (long long)p * a.hk * D) = make_uint4(o[0], o[1], o[2], o[3]);
+        }
+    }
+}
+
+template <typename TI>
+cudaError_t store_t(const LmShape& sh, StoreArgs& a, cudaStream_t s)
+{
+    const int most = (sh.hk * sh.D + 255) / 256;    // sets of heads
+    a.parts = 1;
+    while (a.parts < most && (long long)a.rows * a.parts < 152 * 16) a.parts++;
+    const long long warps = (long long)a.rows * a.parts;
+    const dim3 grid((unsigned)((warps + kThreads / 32 - 1) / (kThreads / 32)), 2);
+    return launch_pdl(sh.D == 128 ? lm_store_q4_kernel<TI, 128> : lm_store_q4_kernel<TI, 64>, grid, dim3(kThreads), 0,
+                      s, a);
+}
+
+template <typename T>
+cudaError_t load_t(const LmShape& sh, const LoadArgs& a, cudaStream_t s)
+{
+    const long long warps = ((long long)a.n * sh.hk) << (a.bs_shift - 4);
+    const dim3 grid((unsigned)std::min<long long>((warps + kThreads / 32 - 1) / (kThreads / 32), 152 * 32), 2);
+    return launch_pdl(sh.D == 128 ? lm_load_q4_kernel<T, 128> : lm_load_q4_kernel<T, 64>, grid, dim3(kThreads), 0, s,
+                      a);
+}
+
+}  // namespace
+
+cudaError_t launch_lm_store_q4(const LmShape& sh, const LmStoreQ4Args& x, int in_type, cudaStream_t s)
+{
+    StoreArgs a{x.k, x.v, x.ks, x.vs, x.rows, sh.hk, x.bs_shift, 1, x.slots, x.n_slots,
+                static_cast<uint8_t*>(x.k_cache), static_cast<uint8_t*>(x.v_cache), sh.err};
+    return in_type == CODEC_LM_FP32   ? store_t<float>(sh, a, s)
+           : in_type == CODEC_LM_BF16 ? store_t<__nv_bfloat16>(sh, a, s)
+                                      : store_t<__half>(sh, a, s);
+}
+
+cudaError_t launch_lm_load_q4(const LmShape& sh, const LmLoadQ4Args& x, cudaStream_t s)
+{
+    const LoadArgs a{static_cast<const uint8_t*>(x.k_cache), static_cast<const uint8_t*>(x.v_cache), x.src, x.dst, x.n,
+                     sh.hk, x.bs_shift, x.n_blocks, x.dst_blocks, x.k_dst, x.v_dst, sh.err};
+    return sh.type == CODEC_LM_BF16 ? load_t<__nv_bfloat16>(sh, a, s) : load_t<__half>(sh, a, s);
+}
+
+}  // namespace codec
