@@ -136,8 +136,17 @@ struct LmStepSpace {
     float *part, *part_lse;         // [max_requests][max_splits][hq][D], [..][hq]
     float *pre, *pre_lse;           // [pre_max][max_requests][hq][D], [..][hq]
     int* done;                      // [max_requests][hk], zero between calls
-    int* taken;                     // the same (behind done)
+    int* taken;                     // the same (behind done), of own and of shared parts in 4 bits
+    unsigned char* zeros;           // a stage of positions in 4 bits that stand for zero
 };
+constexpr int kLmZeroBytes = 64 * 128 * 5 / 8;
+// Splits of a shared part in 4 bits: about 2,000 units with the largest batch
+// (a unit: the heads of 16 / group requests of one K/V head), of 256 positions at least.
+inline int lm_shared_splits_q4(long long max_requests, int hk, int group, long long len)
+{
+    const long long per = 16 / group, units = (max_requests + per - 1) / per * hk;
+    return (int)std::max<long long>(1, std::min<long long>({32, 2048 / units, len / 256}));
+}
 
 struct LmStepArgs {
     const void* q;
@@ -155,6 +164,7 @@ cudaError_t configure_lm_step();
 cudaError_t launch_lm_step(const LmShape& sh, const LmStepArgs& a, cudaStream_t s);
 
 // Single tokens over the cache in 4 bits (keys.k, keys.v: its bytes).
+cudaError_t configure_lm_step_q4();
 cudaError_t launch_lm_step_q4(const LmShape& sh, const LmStepArgs& a, cudaStream_t s);
 
 struct LmStoreQ4Args {

@@ -49,6 +49,7 @@ void lm_free(codec_lm_s* lm)
     cudaFree(lm->step.pre);
     cudaFree(lm->step.pre_lse);
     cudaFree(lm->step.done);
+    cudaFree(lm->step.zeros);
     cudaFree(lm->prompt.list);
     cudaFree(lm->prompt.counts);
     cudaFree(lm->prompt.joins);
@@ -130,7 +131,8 @@ codec_status codec_lm_create(const codec_lm_config* cfg, codec_lm_t** out)
     const int64_t pairs = (c.max_requests + tokens - 1) / tokens;
     sp.shared_ctas = (int)(pairs * c.kv_heads);
     sp.heads = heads;
-    const int pre_max = lm_shared_splits(sp.shared_ctas, positions);
+    const int pre_max = std::max(lm_shared_splits(sp.shared_ctas, positions),
+                                 lm_shared_splits_q4(c.max_requests, c.kv_heads, c.q_heads / c.kv_heads, positions));
     LmBeamSpace& bm = lm->beam;
     bm.parts = lm_beam_parts(c.max_requests);
     LmPromptSpace& pr = lm->prompt;
@@ -149,7 +151,8 @@ codec_status codec_lm_create(const codec_lm_config* cfg, codec_lm_t** out)
         cudaMalloc(&bm.part, sizeof(LmBeamPart) * bm.parts) != cudaSuccess ||
         cudaMalloc(&bm.best, sizeof(uint2) * kLmMaxBeams * (size_t)bm.parts) != cudaSuccess ||
         cudaMalloc(&lm->block_map, sizeof(int) * (size_t)c.n_blocks) != cudaSuccess ||
-        cudaMalloc(&sp.done, sizeof(int) * ((size_t)c.max_requests * c.kv_heads + 1)) != cudaSuccess) {
+        cudaMalloc(&sp.zeros, kLmZeroBytes) != cudaSuccess ||
+        cudaMalloc(&sp.done, sizeof(int) * ((size_t)c.max_requests * c.kv_heads + 2)) != cudaSuccess) {
         cudaGetLastError();
         lm_free(lm);
         return CODEC_ERR_OOM;
@@ -157,7 +160,8 @@ codec_status codec_lm_create(const codec_lm_config* cfg, codec_lm_t** out)
     sp.taken = sp.done + (size_t)c.max_requests * c.kv_heads;
     lm->shape = LmShape{c.type, c.q_heads, c.kv_heads, c.q_heads / c.kv_heads, c.head_dim, c.scale, lm->err, 0};
     if (configure_lm_plan() != cudaSuccess || configure_lm_prompt() != cudaSuccess ||
-        configure_lm_step() != cudaSuccess || configure_lm_pages() != cudaSuccess || cudaMemset(sp.done, 0, sizeof(int) * ((size_t)c.max_requests * c.kv_heads + 1)) != cudaSuccess ||
+        configure_lm_step() != cudaSuccess || configure_lm_step_q4() != cudaSuccess || configure_lm_pages() != cudaSuccess || cudaMemset(sp.done, 0, sizeof(int) * ((size_t)c.max_requests * c.kv_heads + 2)) != cudaSuccess ||
+        cudaMemset(sp.zeros, 0, kLmZeroBytes) != cudaSuccess ||
         cudaMemset(lm->err, 0, sizeof(unsigned)) != cudaSuccess ||
         launch_lm_turn_table(lm->turn, c.max_positions, c.head_dim, c.rope_theta, nullptr) != cudaSuccess ||
         cudaDeviceSynchronize() != cudaSuccess) {
@@ -184,7 +188,7 @@ codec_status codec_lm_errors(codec_lm_t* lm, uint32_t* bits, int32_t clear, void
     if (!on.ok || cudaMemcpyAsync(bits, lm->err, sizeof(uint32_t), cudaMemcpyDeviceToHost, cs) != cudaSuccess ||
         (clear && (cudaMemsetAsync(lm->err, 0, sizeof(uint32_t), cs) != cudaSuccess ||
                    // a call that gave up may have left its counts of finished units
-                   cudaMemsetAsync(lm->step.done, 0, sizeof(int) * ((size_t)lm->cfg.max_requests * lm->cfg.kv_heads + 1),
+                   cudaMemsetAsync(lm->step.done, 0, sizeof(int) * ((size_t)lm->cfg.max_requests * lm->cfg.kv_heads + 2),
                                    cs) != cudaSuccess)) ||
         cudaStreamSynchronize(cs) != cudaSuccess)
         return CODEC_ERR_CUDA;
