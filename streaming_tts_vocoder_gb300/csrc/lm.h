@@ -114,6 +114,7 @@ struct LmSharedArgs {
     int shared_len, split_len;
     float* part;
     float* part_lse;
+    const float* row_c = nullptr;   // fp16 queries, each (row, head) with a factor c of its own
 };
 long long lm_shared_ctas(const LmShape& sh, const LmSharedArgs& a);
 cudaError_t launch_lm_shared(const LmShape& sh, const LmSharedArgs& a, cudaStream_t s);
@@ -137,16 +138,17 @@ struct LmStepSpace {
     float *pre, *pre_lse;           // [pre_max][max_requests][hq][D], [..][hq]
     int* done;                      // [max_requests][hk], zero between calls
     int* taken;                     // the same (behind done), of own and of shared parts in 4 bits
-    unsigned char* zeros;           // a stage of positions in 4 bits that stand for zero
+    int chunk_q4, max_splits_q4;    // chunk and max_splits over the cache in 4 bits
+    unsigned char* zeros;           // two tiles of 16 positions in 4 bits that stand for zero
+    // A shared part in 4 bits, as halves: at most shared_q4 positions [shared_q4][hk][D],
+    // the queries [max_requests][hq][D] and their factors, and the numbers 0, 1, ..
+    int shared_q4;
+    void *k16, *v16, *q16;
+    float* row_c;
+    int* count;
 };
-constexpr int kLmZeroBytes = 64 * 128 * 5 / 8;
-// Splits of a shared part in 4 bits: about 2,000 units with the largest batch
-// (a unit: the heads of 16 / group requests of one K/V head), of 256 positions at least.
-inline int lm_shared_splits_q4(long long max_requests, int hk, int group, long long len)
-{
-    const long long per = 16 / group, units = (max_requests + per - 1) / per * hk;
-    return (int)std::max<long long>(1, std::min<long long>({32, 2048 / units, len / 256}));
-}
+constexpr int kLmZeroBytes = 2 * 16 * 128 * 5 / 8;
+constexpr int kLmSharedQ4 = 32768;
 
 struct LmStepArgs {
     const void* q;
@@ -185,6 +187,22 @@ struct LmLoadQ4Args {
     void *k_dst, *v_dst;
 };
 cudaError_t launch_lm_load_q4(const LmShape& sh, const LmLoadQ4Args& a, cudaStream_t s);
+
+// Blocks 0 .. n - 1 of table in halves to k16, v16 [n][block][hk][D] (zeros for an id
+// out of range), and queries [B][hq][D] of the object's type in halves to q16, each
+// head times a power of two, with scale log2(e) / that in row_c.
+struct LmHalvesArgs {
+    const void *k_cache, *v_cache;
+    const int* table;
+    int n, bs_shift, n_blocks;
+    const void* q;
+    long long qs;
+    int B;
+    void *k16, *v16, *q16;
+    float* row_c;
+};
+cudaError_t launch_lm_halves_q4(const LmShape& sh, const LmHalvesArgs& a, cudaStream_t s);
+cudaError_t launch_lm_count(int* count, int n, cudaStream_t s);     // 0, 1, .. n - 1
 
 struct LmForkArgs {
     const int *parents, *len;

@@ -50,6 +50,11 @@ void lm_free(codec_lm_s* lm)
     cudaFree(lm->step.pre_lse);
     cudaFree(lm->step.done);
     cudaFree(lm->step.zeros);
+    cudaFree(lm->step.k16);
+    cudaFree(lm->step.v16);
+    cudaFree(lm->step.q16);
+    cudaFree(lm->step.row_c);
+    cudaFree(lm->step.count);
     cudaFree(lm->prompt.list);
     cudaFree(lm->prompt.counts);
     cudaFree(lm->prompt.joins);
@@ -126,13 +131,24 @@ codec_status codec_lm_create(const codec_lm_config* cfg, codec_lm_t** out)
                                             c.head_dim > (1LL << 29)))
         sp.chunk *= 2;
     sp.max_splits = (int)((positions + sp.chunk - 1) / sp.chunk);
+    // In 4 bits a split is one warp's: of 32 positions, of up to 1,024 as long as full
+    // tables still make eight for every warp that fits the GPU (2,432), and of as many as
+    // leave a full table 128.
+    sp.chunk_q4 = 32;
+    while ((sp.chunk_q4 < 1024 && heads * ((positions + 2 * sp.chunk_q4 - 1) / (2 * sp.chunk_q4)) >= 8 * 2432) ||
+           positions > 128LL * sp.chunk_q4 ||
+           (sp.chunk_q4 < positions && heads * (c.q_heads / c.kv_heads) * ((positions + sp.chunk_q4 - 1) / sp.chunk_q4) *
+                                               c.head_dim > (1LL << 29)))
+        sp.chunk_q4 *= 2;
+    sp.max_splits_q4 = (int)((positions + sp.chunk_q4 - 1) / sp.chunk_q4);
+    const size_t most_splits = std::max(sp.max_splits, sp.max_splits_q4);
     // The shared part's splits: by the largest batch, so that the actual one changes no bits.
     const int tokens = 2 * (128 / (c.q_heads / c.kv_heads));
     const int64_t pairs = (c.max_requests + tokens - 1) / tokens;
     sp.shared_ctas = (int)(pairs * c.kv_heads);
     sp.heads = heads;
-    const int pre_max = std::max(lm_shared_splits(sp.shared_ctas, positions),
-                                 lm_shared_splits_q4(c.max_requests, c.kv_heads, c.q_heads / c.kv_heads, positions));
+    const int pre_max = lm_shared_splits(sp.shared_ctas, positions);
+    sp.shared_q4 = (int)std::min<int64_t>(positions, kLmSharedQ4);
     LmBeamSpace& bm = lm->beam;
     bm.parts = lm_beam_parts(c.max_requests);
     LmPromptSpace& pr = lm->prompt;
@@ -140,8 +156,8 @@ codec_status codec_lm_create(const codec_lm_config* cfg, codec_lm_t** out)
     const size_t row = (size_t)c.max_requests * c.q_heads;
     if (cudaMalloc(&lm->turn, sizeof(float2) * (size_t)c.max_positions * (c.head_dim / 2)) != cudaSuccess ||
         cudaMalloc(&lm->err, sizeof(unsigned)) != cudaSuccess ||
-        cudaMalloc(&sp.part, sizeof(float) * row * sp.max_splits * c.head_dim) != cudaSuccess ||
-        cudaMalloc(&sp.part_lse, sizeof(float) * row * sp.max_splits) != cudaSuccess ||
+        cudaMalloc(&sp.part, sizeof(float) * row * most_splits * c.head_dim) != cudaSuccess ||
+        cudaMalloc(&sp.part_lse, sizeof(float) * row * most_splits) != cudaSuccess ||
         cudaMalloc(&sp.pre, sizeof(float) * row * pre_max * c.head_dim) != cudaSuccess ||
         cudaMalloc(&sp.pre_lse, sizeof(float) * row * pre_max) != cudaSuccess ||
         cudaMalloc(&pr.list, 32 * items) != cudaSuccess || cudaMalloc(&pr.counts, 3 * sizeof(int)) != cudaSuccess ||
@@ -152,6 +168,11 @@ codec_status codec_lm_create(const codec_lm_config* cfg, codec_lm_t** out)
         cudaMalloc(&bm.best, sizeof(uint2) * kLmMaxBeams * (size_t)bm.parts) != cudaSuccess ||
         cudaMalloc(&lm->block_map, sizeof(int) * (size_t)c.n_blocks) != cudaSuccess ||
         cudaMalloc(&sp.zeros, kLmZeroBytes) != cudaSuccess ||
+        cudaMalloc(&sp.k16, 2 * (size_t)sp.shared_q4 * c.kv_heads * c.head_dim) != cudaSuccess ||
+        cudaMalloc(&sp.v16, 2 * (size_t)sp.shared_q4 * c.kv_heads * c.head_dim) != cudaSuccess ||
+        cudaMalloc(&sp.q16, 2 * row * c.head_dim) != cudaSuccess ||
+        cudaMalloc(&sp.row_c, sizeof(float) * row) != cudaSuccess ||
+        cudaMalloc(&sp.count, sizeof(int) * (sp.shared_q4 / c.block_size)) != cudaSuccess ||
         cudaMalloc(&sp.done, sizeof(int) * ((size_t)c.max_requests * c.kv_heads + 2)) != cudaSuccess) {
         cudaGetLastError();
         lm_free(lm);
@@ -162,6 +183,7 @@ codec_status codec_lm_create(const codec_lm_config* cfg, codec_lm_t** out)
     if (configure_lm_plan() != cudaSuccess || configure_lm_prompt() != cudaSuccess ||
         configure_lm_step() != cudaSuccess || configure_lm_step_q4() != cudaSuccess || configure_lm_pages() != cudaSuccess || cudaMemset(sp.done, 0, sizeof(int) * ((size_t)c.max_requests * c.kv_heads + 2)) != cudaSuccess ||
         cudaMemset(sp.zeros, 0, kLmZeroBytes) != cudaSuccess ||
+        launch_lm_count(sp.count, sp.shared_q4 / c.block_size, nullptr) != cudaSuccess ||
         cudaMemset(lm->err, 0, sizeof(unsigned)) != cudaSuccess ||
         launch_lm_turn_table(lm->turn, c.max_positions, c.head_dim, c.rope_theta, nullptr) != cudaSuccess ||
         cudaDeviceSynchronize() != cudaSuccess) {

@@ -97,6 +97,7 @@ struct Params {
     float* lse;
     float* part;                // shared part: [split][rows][hq][D], normalised, fp32
     float* part_lse;            // [split][rows][hq]
+    const float* row_c;         // shared part: c of each (row, head) instead (kRowScale)
 };
 
 // An item as the list holds it.
@@ -446,7 +447,9 @@ __device__ __noinline__ void add_not_finite(const Params& p, const Item& it, int
     }
 }
 
-template <typename T, int D>
+// kRowScale: queries are times a power of two of their own, which row_c undoes (an
+// instance of its own: a register more).
+template <typename T, int D, bool kRowScale = false>
 __global__ void __launch_bounds__(kThreads, 1) lm_prompt_kernel(const __grid_constant__ CUtensorMap mq,
                                                                 const __grid_constant__ CUtensorMap mk,
                                                                 const __grid_constant__ CUtensorMap mv,
@@ -837,6 +840,9 @@ __global__ void __launch_bounds__(kThreads, 1) lm_prompt_kernel(const __grid_con
             // tiles from here on hold keys that some row does not see
             const int first_masked = it.free_from / kTile;
             float ref = 0.f, l = 0.f;
+            float c = p.c;
+            if constexpr (kRowScale)
+                if (live) c = __ldcg(p.row_c + ((long long)it.q0 + tok) * p.sh.hq + it.hk * p.sh.group + g);
             for (int j = 0; j < n; j++) {
                 ok = mbar_wait(&s.s_full[i], tile_ph, abort_flag, kLmPolls);
                 tile_ph ^= 1u;
@@ -867,17 +873,17 @@ __global__ void __launch_bounds__(kThreads, 1) lm_prompt_kernel(const __grid_con
                 if (j == 0) {
                     // scores of -inf alone so far: below whatever comes
                     ref = m == -INFINITY ? -1e30f : m;
-                } else if (__any_sync(0xffffffffu, (m - ref) * p.c > 8.f)) {
+                } else if (__any_sync(0xffffffffu, (m - ref) * c > 8.f)) {
                     // Only the rows that need it move (times 1 changes nothing): a row's bits
                     // do not depend on its neighbours.  The accumulator rests: its last
                     // product ran before these scores.
-                    const float to_ref = (m - ref) * p.c > 8.f ? m : ref, f = exp2_fast((ref - to_ref) * p.c);
+                    const float to_ref = (m - ref) * c > 8.f ? m : ref, f = exp2_fast((ref - to_ref) * c);
                     l *= f;
                     ref = to_ref;
 #pragma unroll 1
                     for (int q = 0; q < D; q += 8) tmem_scale8(to + q, f);
                 }
-                const float2 c2 = make_float2(p.c, p.c), base = make_float2(-ref * p.c, -ref * p.c);
+                const float2 c2 = make_float2(c, c), base = make_float2(-ref * c, -ref * c);
                 float2 l0 = make_float2(0.f, 0.f), l1 = l0;
 #pragma unroll
                 for (int q = 0; q < kTile; q += 64) {
@@ -915,7 +921,7 @@ __global__ void __launch_bounds__(kThreads, 1) lm_prompt_kernel(const __grid_con
             const long long row = it.q0 + tok;
             const bool fix = *reinterpret_cast<volatile int*>(&s.dirty[walk.k & 1]) == walk.k && lim > 0;
             if (live) {
-                const float lse = lim > 0 ? ref * p.sh.scale + logf(l) : -INFINITY;
+                const float lse = lim > 0 ? ref * (kRowScale ? c * 0.6931471805599453f : p.sh.scale) + logf(l) : -INFINITY;
                 if (it.slot >= 0)
                     p.piece_lse[((long long)it.slot * 2 + i) * kTile + r] = lse;
                 else if (p.part)
@@ -1243,7 +1249,7 @@ uint32_t idesc(uint32_t format, int N, bool b_mn)
            ((uint32_t)(kTile >> 4) << 24);
 }
 
-template <typename T, int D>
+template <typename T, int D, bool kRowScale = false>
 cudaError_t launch(const LmShape& sh, const void* q, long long qs, const LmKeys& ks, Params& p, dim3 grid,
                    cudaStream_t s, int4* list)
 {
@@ -1275,7 +1281,7 @@ cudaError_t launch(const LmShape& sh, const void* q, long long qs, const LmKeys&
         if (e != cudaSuccess) return e;
         p.list = list;
     }
-    e = launch_pdl(lm_prompt_kernel<T, D>, grid, dim3(kThreads), smem_bytes<D>(), s, mq, mk, mv, p);
+    e = launch_pdl(lm_prompt_kernel<T, D, kRowScale>, grid, dim3(kThreads), smem_bytes<D>(), s, mq, mk, mv, p);
     if (e != cudaSuccess || !p.split) return e;
     // a row per warp where they fit: four rows per warp in turn, 608 CTAs less, took
     // 40 instead of 34 us for 670 tokens behind 6,000 positions, eight K/V heads
@@ -1300,7 +1306,9 @@ cudaError_t configure_lm_prompt()
     const std::pair<const void*, size_t> kernels[] = {{(const void*)lm_prompt_kernel<__nv_bfloat16, 128>, smem_bytes<128>()},
                                                       {(const void*)lm_prompt_kernel<__nv_bfloat16, 64>, smem_bytes<64>()},
                                                       {(const void*)lm_prompt_kernel<__half, 128>, smem_bytes<128>()},
-                                                      {(const void*)lm_prompt_kernel<__half, 64>, smem_bytes<64>()}};
+                                                      {(const void*)lm_prompt_kernel<__half, 64>, smem_bytes<64>()},
+                                                      {(const void*)lm_prompt_kernel<__half, 128, true>, smem_bytes<128>()},
+                                                      {(const void*)lm_prompt_kernel<__half, 64, true>, smem_bytes<64>()}};
     for (const auto& k : kernels) {
         const cudaError_t e = cudaFuncSetAttribute(k.first, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)k.second);
         if (e != cudaSuccess) return e;
@@ -1365,6 +1373,10 @@ cudaError_t launch_lm_shared(const LmShape& sh, const LmSharedArgs& a, cudaStrea
     LmKeys ks = a.keys;
     ks.tables = a.shared_table;
     const dim3 grid = shared_grid(sh, a);
+    p.row_c = a.row_c;
+    if (a.row_c)
+        return sh.D == 128 ? launch<__half, 128, true>(sh, a.q, a.qs, ks, p, grid, s, nullptr)
+                           : launch<__half, 64, true>(sh, a.q, a.qs, ks, p, grid, s, nullptr);
     return launch_any(sh, a.q, a.qs, ks, p, grid, s);
 }
 

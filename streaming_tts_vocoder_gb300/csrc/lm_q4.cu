@@ -145,13 +145,44 @@ __device__ __forceinline__ uint32_t pack2(float a, float b, const __half*)
     return *reinterpret_cast<const uint32_t*>(&v);
 }
 
-// A warp per tile of 16 positions; keys or values by blockIdx.y.
+// A tile of 16 positions (null: zeros) to rows of the same head `stride` elements
+// apart; row: this lane's eight elements of the first.  A whole warp.
 template <typename T, int D>
-__global__ void __launch_bounds__(kThreads) lm_load_q4_kernel(const LoadArgs a)
+__device__ __forceinline__ void decode(const uint8_t* at, bool values, T* row, long long stride)
 {
     using Tile = Q4Tile<D>;
     constexpr int kLanes = D / 8, kRows = 32 / kLanes;
     const int lane = threadIdx.x & 31, c = lane % kLanes, g = c >> 2, t = c & 3;
+#pragma unroll
+    for (int p0 = 0; p0 < 16; p0 += kRows) {
+        const int p = p0 + lane / kLanes;
+        uint32_t word = 0;
+        float scale = 0.f, low = 0.f;
+        if (at && !values) {
+            word = __ldg(reinterpret_cast<const uint32_t*>(at + Tile::k_word(p, t, g)));
+            const float2 f = __half22float2(__ldg(reinterpret_cast<const __half2*>(at + Tile::k_param(p, g))));
+            scale = f.x;
+            low = f.y;
+        } else if (at) {
+            word = __ldg(reinterpret_cast<const uint16_t*>(at + Tile::v_pair(p, 2 * t, g))) |
+                   (uint32_t)__ldg(reinterpret_cast<const uint16_t*>(at + Tile::v_pair(p, 2 * t + 1, g))) << 16;
+            scale = __half2float(__ldg(reinterpret_cast<const __half*>(at + Tile::v_scale(p, g))));
+            low = __half2float(__ldg(reinterpret_cast<const __half*>(at + Tile::v_scale(p, g) + D)));
+        }
+        uint32_t o[4];
+#pragma unroll
+        for (int j = 0; j < 4; j++)
+            o[j] = pack2(fmaf(scale, (float)(word >> (8 * j) & 15u), low),
+                         fmaf(scale, (float)(word >> (8 * j + 4) & 15u), low), row);
+        *reinterpret_cast<uint4*>(row + p * stride) = make_uint4(o[0], o[1], o[2], o[3]);
+    }
+}
+
+// A warp per tile of 16 positions; keys or values by blockIdx.y.
+template <typename T, int D>
+__global__ void __launch_bounds__(kThreads) lm_load_q4_kernel(const LoadArgs a)
+{
+    const int lane = threadIdx.x & 31;
     const bool values = blockIdx.y == 1;
     const uint8_t* cache = values ? a.v_cache : a.k_cache;
     T* out = static_cast<T*>(values ? a.v_dst : a.k_dst);
@@ -168,32 +199,68 @@ __global__ void __launch_bounds__(kThreads) lm_load_q4_kernel(const LoadArgs a)
             if (lane == 0) atomicOr(a.err, CODEC_LM_ERR_BLOCK);
             continue;
         }
-        const uint8_t* at = cache + (((long long)from * a.hk + h) * tiles + tile) * Tile::kBytes;
-        T* row = out + ((((long long)to << a.bs_shift) + tile * 16) * a.hk + h) * D + c * 8;
-#pragma unroll
-        for (int p0 = 0; p0 < 16; p0 += kRows) {
-            const int p = p0 + lane / kLanes;
-            uint32_t word;
-            float scale, low;
-            if (!values) {
-                word = __ldg(reinterpret_cast<const uint32_t*>(at + Tile::k_word(p, t, g)));
-                const float2 f = __half22float2(__ldg(reinterpret_cast<const __half2*>(at + Tile::k_param(p, g))));
-                scale = f.x;
-                low = f.y;
-            } else {
-                word = __ldg(reinterpret_cast<const uint16_t*>(at + Tile::v_pair(p, 2 * t, g))) |
-                       (uint32_t)__ldg(reinterpret_cast<const uint16_t*>(at + Tile::v_pair(p, 2 * t + 1, g))) << 16;
-                scale = __half2float(__ldg(reinterpret_cast<const __half*>(at + Tile::v_scale(p, g))));
-                low = __half2float(__ldg(reinterpret_cast<const __half*>(at + Tile::v_scale(p, g) + D)));
-            }
-            uint32_t o[4];
-#pragma unroll
-            for (int j = 0; j < 4; j++)
-                o[j] = pack2(fmaf(scale, (float)(word >> (8 * j) & 15u), low),
-                             fmaf(scale, (float)(word >> (8 * j + 4) & 15u), low), row);
-            *reinterpret_cast<uint4*>(row + (long long)p * a.hk * D) = make_uint4(o[0], o[1], o[2], o[3]);
-        }
+        decode<T, D>(cache + (((long long)from * a.hk + h) * tiles + tile) * Q4Tile<D>::kBytes, values,
+                     out + ((((long long)to << a.bs_shift) + tile * 16) * a.hk + h) * D + lane % (D / 8) * 8,
+                     (long long)a.hk * D);
     }
+}
+
+// See LmHalvesArgs.  blockIdx.y: keys, values, queries (a warp per row and head).
+template <int D>
+__global__ void __launch_bounds__(kThreads) lm_halves_q4_kernel(const LmHalvesArgs a, int hq, int hk, int bf16, float scale,
+                                                             unsigned* err)
+{
+    const int lane = threadIdx.x & 31;
+    const long long first = (blockIdx.x * (long long)kThreads + threadIdx.x) >> 5, step = gridDim.x * (long long)(kThreads / 32);
+    pdl_wait();
+    pdl_launch();
+    if (blockIdx.y < 2) {
+        const bool values = blockIdx.y == 1;
+        const uint8_t* cache = static_cast<const uint8_t*>(values ? a.v_cache : a.k_cache);
+        __half* out = static_cast<__half*>(values ? a.v16 : a.k16);
+        const int tiles = 1 << (a.bs_shift - 4);
+        for (long long w = first; w < (long long)a.n * hk * tiles; w += step) {
+            const int tile = (int)(w % tiles), i = (int)(w / tiles / hk), h = (int)(w / tiles - (long long)i * hk);
+            const int from = __ldg(a.table + i);
+            const bool good = from >= 0 && from < a.n_blocks;
+            if (!good && lane == 0) atomicOr(err, CODEC_LM_ERR_BLOCK);
+            decode<__half, D>(good ? cache + (((long long)from * hk + h) * tiles + tile) * Q4Tile<D>::kBytes : nullptr, values,
+                              out + ((((long long)i << a.bs_shift) + tile * 16) * hk + h) * D + lane % (D / 8) * 8,
+                              (long long)hk * D);
+        }
+        return;
+    }
+    constexpr int kE = D / 32;
+    for (long long w = first; w < (long long)a.B * hq; w += step) {
+        const int b = (int)(w / hq), h = (int)(w - (long long)b * hq);
+        const uint32_t* row = reinterpret_cast<const uint32_t*>(static_cast<const uint16_t*>(a.q) + b * a.qs + (long long)h * D) +
+                              lane * (kE / 2);
+        float2 x[kE / 2];
+        float top = 0.f;
+#pragma unroll
+        for (int e = 0; e < kE / 2; e++) {
+            const uint32_t u = row[e];
+            x[e] = bf16 ? unpack2(u, static_cast<const __nv_bfloat16*>(nullptr)) : unpack2(u, static_cast<const __half*>(nullptr));
+            top = fmaxf(top, fmaxf(fabsf(x[e].x), fabsf(x[e].y)));
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+        const int lift = q4_query_lift(top);
+        const float m = __int_as_float((127 + lift) << 23);
+        uint32_t* to = reinterpret_cast<uint32_t*>(static_cast<__half*>(a.q16) + w * D) + lane * (kE / 2);
+#pragma unroll
+        for (int e = 0; e < kE / 2; e++) {
+            const __half2 v = __floats2half2_rn(x[e].x * m, x[e].y * m);
+            to[e] = *reinterpret_cast<const uint32_t*>(&v);
+        }
+        if (lane == 0) a.row_c[w] = q4_query_factor(scale, lift);
+    }
+}
+
+__global__ void lm_count_kernel(int* count, int n)
+{
+    const int i = blockIdx.x * blockDim.x + threadIdx.x;
+    if (i < n) count[i] = i;
 }
 
 template <typename TI>
@@ -233,6 +300,20 @@ cudaError_t launch_lm_load_q4(const LmShape& sh, const LmLoadQ4Args& x, cudaStre
     const LoadArgs a{static_cast<const uint8_t*>(x.k_cache), static_cast<const uint8_t*>(x.v_cache), x.src, x.dst, x.n,
                      sh.hk, x.bs_shift, x.n_blocks, x.dst_blocks, x.k_dst, x.v_dst, sh.err};
     return sh.type == CODEC_LM_BF16 ? load_t<__nv_bfloat16>(sh, a, s) : load_t<__half>(sh, a, s);
+}
+
+cudaError_t launch_lm_halves_q4(const LmShape& sh, const LmHalvesArgs& a, cudaStream_t s)
+{
+    const long long warps = std::max(((long long)a.n * sh.hk) << (a.bs_shift - 4), (long long)a.B * sh.hq);
+    const dim3 grid((unsigned)std::min<long long>((warps + kThreads / 32 - 1) / (kThreads / 32), 152 * 16), 3);
+    return launch_pdl(sh.D == 128 ? lm_halves_q4_kernel<128> : lm_halves_q4_kernel<64>, grid, dim3(kThreads), 0, s, a, sh.hq,
+                      sh.hk, (int)(sh.type == CODEC_LM_BF16), (float)(sh.scale * 1.4426950408889634), sh.err);
+}
+
+cudaError_t launch_lm_count(int* count, int n, cudaStream_t s)
+{
+    lm_count_kernel<<<(n + 255) / 256, 256, 0, s>>>(count, n);
+    return cudaGetLastError();
 }
 
 }  // namespace codec

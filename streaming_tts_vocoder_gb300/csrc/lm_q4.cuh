@@ -28,4 +28,18 @@ struct Q4Tile {
     }
 };
 
+// Queries as halves: times 2^lift, which brings a head's largest element to 2^14 ..
+// 2^15, so exact but for what lies 2^34 below (what is not finite stays so); and
+// the factor that undoes it with the scale.
+__device__ __forceinline__ int q4_query_lift(float top)
+{
+    const int e = (int)(__float_as_uint(top) >> 23);
+    return e == 255 ? 0 : min(127 + 14 - e, 100);
+}
+// Neither bound is met by scores that differ.
+__device__ __forceinline__ float q4_query_factor(float c, int lift)
+{
+    return fmaxf(fminf(c * __int_as_float((127 - lift) << 23), 1e31f), 1e-30f);
+}
+
 }  // namespace codec

@@ -144,14 +144,27 @@ def cache_q4(seed, lens, hk, d, bs, sh=0, v_mul=1.0):
     return kc, vc, tables, shared, n_blocks, width
 
 
-def step_reference(q, kc, vc, tables, lens, shared, hk, d, bs, scale=None):
+def as_halves(most, hk, shared_len):
+    """Positions of the shared part that the batch has in common as halves: none
+    where every request reads it itself (a short one, or an object for one request)."""
+    short = 65536 if shared_len <= 256 else 32768 if shared_len <= 1024 else 0
+    return 0 if most == 1 or most * hk * shared_len <= short else min(shared_len, 32768)
+
+
+def step_reference(q, kc, vc, tables, lens, shared, hk, d, bs, scale=None, most=1):
     sh = len(shared)
     parts = [Q.values(c.cpu().numpy(), bs, d, keys, parts=True) for c, keys in ((kc, True), (vc, False))]
+    halves = as_halves(most, hk, sh * bs)
 
     def keys_of(b):
         n = lens[b]
         ids = [(shared + tables[b][sh:])[j] for j in range(-(-n // bs))]
-        return [x[ids].reshape(-1, hk, d)[:n] for pair in parts for x in pair]
+        got = []
+        for low, rest in parts:
+            low, rest = (x[ids].reshape(-1, hk, d)[:n].copy() for x in (low, rest))
+            rest[:halves] = (low[:halves] + rest[:halves]).astype(np.float16).astype(np.float64) - low[:halves]
+            got += [low, rest]
+        return got
 
     return Q.step(f64(q), keys_of, hk, scale or d ** -0.5)
 
@@ -170,7 +183,7 @@ def check_step(lens, sh, hq, hk, d, dt, bs, seed=0, mul=1.0, v_mul=1.0, most=Non
     run = lambda o, lse: lm.step_q4(q, kc, vc, i32(own), i32(lens), o, shared_table=i32(shared) if sh else None, lse=lse)
     run(o, lse)
     assert lm.errors() == 0
-    ref = step_reference(q, kc, vc, tables, lens, shared, hk, d, bs, scale)
+    ref = step_reference(q, kc, vc, tables, lens, shared, hk, d, bs, scale, most or B)
     Q.assert_step(o, lse, ref, dt, d, 6.0 * v_mul)
     o2 = torch.zeros(B, hq, d, dtype=q.dtype, device="cuda")
     run(o2, None)
@@ -265,14 +278,15 @@ def test_step_many_requests():
     check_step([40, 700, 3], 0, 8, 2, 128, "bf16", 16, most=4096)
 
 
-def test_step_what_is_not_finite_reaches_its_own_rows():
+@pytest.mark.parametrize("most", [3, 4096])      # every request reads the shared part, or it is worked on for all
+def test_step_what_is_not_finite_reaches_its_own_rows(most):
     """A NaN in a request's own key makes its results NaN, one in a value its
     group's columns; one in the shared part reaches those who see it."""
     hq, hk, d, bs, sh = 4, 2, 128, 16, 12
     lens = [300, 50, 200]
     kc, vc, tables, shared, n_blocks, width = cache_q4(8, lens, hk, d, bs, sh)
     q = torch.randn(3, hq, d, device="cuda", generator=torch.Generator(device="cuda").manual_seed(8)).bfloat16()
-    lm = C.Lm(hq, hk, d, block_size=bs, n_blocks=n_blocks, table_blocks=width, max_requests=3, max_rows=8)
+    lm = C.Lm(hq, hk, d, block_size=bs, n_blocks=n_blocks, table_blocks=width, max_requests=most, max_rows=8)
 
     def run():
         o = torch.zeros_like(q)
@@ -295,9 +309,17 @@ def test_step_what_is_not_finite_reaches_its_own_rows():
     lm.store_q4(x, torch.ones_like(x), i32([at]), kc, vc)
     got = run()
     assert torch.equal(got[1:], want[1:]) and got[0, :2].isnan().all() and not got[0, 2:].isnan().any()
-    lm.store_q4(x, torch.ones_like(x), i32([shared[5] * bs + 1]), kc, vc)        # position 81: behind request 1's end
+    lm.store_q4(y, y, i32([at]), kc, vc)
+    y[0, 1, 70] = 1.0
+    lm.store_q4(y, y, i32([at]), kc, vc)
+    place, want = i32([shared[5] * bs + 1]), run()              # position 81: behind request 1's end
+    lm.store_q4(x, torch.ones_like(x), place, kc, vc)
     got = run()
-    assert torch.equal(got[1], want[1]) and got[2, :2].isnan().all() and not got[2, 2:].isnan().any()
+    assert torch.equal(got[1], want[1]) and got[::2, :2].isnan().all() and not got[::2, 2:].isnan().any()
+    x[0, 0, 3], y[0, 0, 100] = 1.0, -INF                        # group 3 of head 0
+    lm.store_q4(x, y, place, kc, vc)
+    bad = run().isnan()
+    assert torch.equal(run()[1], want[1]) and bad[::2, :2, 96:].all() and bad.sum() == 2 * 2 * 32
     assert lm.errors() == 0
 
 
@@ -318,6 +340,28 @@ def test_step_bad_blocks_read_as_zeros():
         want = torch.zeros_like(q)
         lm.step_q4(q, kc, vc, i32(tables), i32(lens), want)
         assert lm.errors() == 0 and all(torch.equal(o, want) for o in outs)
+
+
+@pytest.mark.parametrize("most", [2, 4096])
+def test_step_bad_shared_blocks_read_as_zeros(most):
+    hq, hk, d, bs, lens = 8, 2, 64, 32, [300, 200]
+    kc, vc, tables, shared, n_blocks, width = cache_q4(12, lens, hk, d, bs, 6)
+    q = torch.randn(2, hq, d, device="cuda", generator=torch.Generator(device="cuda").manual_seed(9)).bfloat16()
+    lm = C.Lm(hq, hk, d, block_size=bs, n_blocks=n_blocks, table_blocks=width, max_requests=most, max_rows=2)
+    o, want = torch.zeros_like(q), torch.zeros_like(q)
+    for bad in (-1, n_blocks, 2 ** 31 - 1):
+        lm.step_q4(q, kc, vc, i32(tables), i32(lens), o, shared_table=i32(shared[:3] + [bad] + shared[4:]))
+        assert lm.errors() == C.LM_ERR_BLOCK
+    kc[shared[3]], vc[shared[3]] = 0, 0
+    lm.step_q4(q, kc, vc, i32(tables), i32(lens), want, shared_table=i32(shared))
+    assert lm.errors() == 0 and torch.equal(o, want)
+
+
+def test_step_behind_more_than_is_worked_on_for_all():
+    """A shared part of more positions than the workspace holds: the rest is read
+    by every request."""
+    hq, hk, d, bs, sh = 2, 1, 64, 128, 32768 // 128 + 3
+    check_step([sh * bs + 5, sh * bs + 300, 33000, 20000, 0], sh, hq, hk, d, "bf16", bs, seed=13, most=64)
 
 
 def test_step_lengths_past_the_table_are_bent():
