@@ -247,19 +247,19 @@ cudaError_t launch_lm_fork(const LmForkArgs& a, cudaStream_t s);
 cudaError_t launch_lm_compact(const LmCompactArgs& a, cudaStream_t s);
 cudaError_t launch_lm_copy(const LmCopyArgs& a, cudaStream_t s);
 
-// Beam search: the best candidates of a part of a row, and its maximum and sum.
+// Beam search: the best candidates of a part of a row, its log(sum(exp(x))) and maximum.
 constexpr int kLmMaxBeams = 32;
 struct LmBeamPart {
-    double sum;                     // of exp(x - top)
+    double lse;
     float top;
     int pad;
 };
 struct LmBeamSpace {
     int parts;                      // that the workspace holds
     LmBeamPart* part;               // [parts]
-    uint2* best;                    // [parts][kLmMaxBeams]: logit's bits (fp32), token
+    uint2* best;                    // [parts][beams]: logit's bits (fp32), token, best first
 };
-inline int lm_beam_parts(int max_requests) { return max_requests + 152 * 32; }
+inline int lm_beam_parts(int max_requests) { return max_requests + 152 * 8; }
 
 struct LmBeamArgs {
     const void* logits;
@@ -273,6 +273,7 @@ struct LmBeamArgs {
     int *parents, *tokens, *ended_out;
     LmBeamSpace ws;
 };
+cudaError_t configure_lm_beams();
 cudaError_t launch_lm_beams(const LmBeamArgs& a, cudaStream_t s);
 
 // Tensor map of [rows][heads][D] 16-bit values, rows `stride` elements apart,

@@ -181,7 +181,8 @@ codec_status codec_lm_create(const codec_lm_config* cfg, codec_lm_t** out)
     sp.taken = sp.done + (size_t)c.max_requests * c.kv_heads;
     lm->shape = LmShape{c.type, c.q_heads, c.kv_heads, c.q_heads / c.kv_heads, c.head_dim, c.scale, lm->err, 0};
     if (configure_lm_plan() != cudaSuccess || configure_lm_prompt() != cudaSuccess ||
-        configure_lm_step() != cudaSuccess || configure_lm_step_q4() != cudaSuccess || configure_lm_pages() != cudaSuccess || cudaMemset(sp.done, 0, sizeof(int) * ((size_t)c.max_requests * c.kv_heads + 2)) != cudaSuccess ||
+        configure_lm_step() != cudaSuccess || configure_lm_step_q4() != cudaSuccess || configure_lm_pages() != cudaSuccess || configure_lm_beams() != cudaSuccess ||
+        cudaMemset(sp.done, 0, sizeof(int) * ((size_t)c.max_requests * c.kv_heads + 2)) != cudaSuccess ||
         cudaMemset(sp.zeros, 0, kLmZeroBytes) != cudaSuccess ||
         launch_lm_count(sp.count, sp.shared_q4 / c.block_size, nullptr) != cudaSuccess ||
         cudaMemset(lm->err, 0, sizeof(unsigned)) != cudaSuccess ||

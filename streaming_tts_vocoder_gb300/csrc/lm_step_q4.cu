@@ -24,12 +24,16 @@
 // own.  A long part that all requests share is first turned into halves and then
 // the prompt kernel's work, as over a cache of 16 bits.
 #include <algorithm>
+#include <type_traits>
 
 #include "lm.h"
 #include "lm_join.cuh"
 #include "lm_q4.cuh"
 #include "tc_ptx.cuh"
 
+#ifndef CT
+#define CT 3
+#endif
 namespace codec {
 
 namespace {
@@ -114,16 +118,27 @@ __device__ __forceinline__ uint32_t times(uint32_t a, uint32_t b)
     return *reinterpret_cast<const uint32_t*>(&v);
 }
 
-// N words at a shared address (a multiple of 4 N bytes).
-template <int N>
+// N words at a shared address (a multiple of 4 N bytes) and kOff bytes.
+template <int N, int kOff>
 __device__ __forceinline__ void lds(uint32_t at, uint32_t* w)
 {
     if constexpr (N == 4)
-        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(at) : "memory");
+        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4 + %5];"
+                     : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                     : "r"(at), "n"(kOff)
+                     : "memory");
     else if constexpr (N == 2)
-        asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(at) : "memory");
+        asm volatile("ld.shared.v2.b32 {%0, %1}, [%2 + %3];" : "=r"(w[0]), "=r"(w[1]) : "r"(at), "n"(kOff) : "memory");
     else
-        asm volatile("ld.shared.b32 %0, [%1];" : "=r"(w[0]) : "r"(at) : "memory");
+        asm volatile("ld.shared.b32 %0, [%1 + %2];" : "=r"(w[0]) : "r"(at), "n"(kOff) : "memory");
+}
+
+// f(0), .. f(N - 1) with constants.
+template <int N, typename F>
+__device__ __forceinline__ void each(F f)
+{
+    f(std::integral_constant<int, 0>());
+    if constexpr (N == 2) f(std::integral_constant<int, 1>());
 }
 
 struct Unit {
@@ -220,7 +235,7 @@ __global__ void __launch_bounds__(kJoinThreads, 4) lm_join_q4_kernel(const __gri
 
 // NT: sets of eight columns.  kJoin: partial results are joined here.
 template <int D, int NT, bool kJoin>
-__global__ void __launch_bounds__(kThreads, 3) lm_step_q4_kernel(const __grid_constant__ Params p)
+__global__ void __launch_bounds__(kThreads, NT == 1 ? CT : 3) lm_step_q4_kernel(const __grid_constant__ Params p)
 {
     using Tile = Q4Tile<D>;
     constexpr int G = Tile::G, kAt = NT == 1 ? 2 : 1;       // tiles worked on at once
@@ -356,9 +371,8 @@ __global__ void __launch_bounds__(kThreads, 3) lm_step_q4_kernel(const __grid_co
     const uint32_t base = smem_u32(ring);
     // this lane's places in a tile: a key's codes and (scale, low), the low of group t, values' codes,
     // their scales, and their lows of group r
-    const uint32_t k_at = r * (D / 2) + t * 4 * G, kp_at = Tile::kParams + r * 4 * G;
-    const uint32_t kl_at = Tile::kParams + (r * G + min(t, G - 1)) * 4, v_at = lane * 4 * G;
-    const uint32_t vs_at = Tile::kParams + t * 8 * G, vl_at = Tile::kParams + D + (t * G + min(r, G - 1)) * 8;
+    const uint32_t k_at = r * (D / 2) + t * 4 * G, kp_at = r * 4 * G, kl_at = (r * G + min(t, G - 1)) * 4;
+    const uint32_t v_at = lane * 4 * G, vs_at = t * 8 * G, vl_at = (t * G + min(r, G - 1)) * 8;
     int st = 0, done = 0;
     uint32_t ph = 0;
     bool gave_up = false;
@@ -459,24 +473,19 @@ __global__ void __launch_bounds__(kThreads, 3) lm_step_q4_kernel(const __grid_co
 #pragma unroll 1
                 for (int w = 0; w < kTiles && at + 16 * w < n.keys; w += kAt) {
                     const int here = at + 16 * w;
-                    const uint32_t kt = base + (uint32_t)st * kStage + w * kTile, vt = kt + kTiles * kTile;
+                    const uint32_t kt = base + (uint32_t)st * kStage + w * kTile;
                     float s[kAt][NT][4];
-                    uint32_t sc[kAt][2 * G], vl[kAt][2];
-#pragma unroll
-                    for (int i = 0; i < kAt; i++) {
+                    // scores
+                    each<kAt>([&](auto I) {
+                        constexpr int i = I, kOff = i * kTile, kP = kOff + Tile::kParams;
                         uint32_t ka[G], kb[G], pa[G], pb[G], la, lb;
-                        lds<G>(kt + i * kTile + k_at, ka);
-                        lds<G>(kt + i * kTile + k_at + 4 * D, kb);
-                        lds<1>(kt + i * kTile + kl_at, &la);
-                        lds<1>(kt + i * kTile + kl_at + 32 * G, &lb);
-                        lds<G>(kt + i * kTile + kp_at, pa);
-                        lds<G>(kt + i * kTile + kp_at + 32 * G, pb);
-                        // values: scales and lows of keys 2 t, 2 t + 1 and of those 8 further; later their codes
-                        lds<4>(vt + i * kTile + vs_at, sc[i]);
-                        if constexpr (G == 4) lds<4>(vt + i * kTile + vs_at + 16, sc[i] + 4);
-                        lds<2>(vt + i * kTile + vl_at, vl[i]);
+                        lds<G, kOff>(kt + k_at, ka);
+                        lds<G, kOff + 4 * D>(kt + k_at, kb);
+                        lds<1, kP>(kt + kl_at, &la);
+                        lds<1, kP + 32 * G>(kt + kl_at, &lb);
+                        lds<G, kP>(kt + kp_at, pa);
+                        lds<G, kP + 32 * G>(kt + kp_at, pb);
                         if (G < 4 && t >= G) la = lb = 0u;
-                        if (r >= G) vl[i][0] = vl[i][1] = 0u;
                         la = __byte_perm(la, 0, 0x3232);
                         lb = __byte_perm(lb, 0, 0x3232);
 #pragma unroll
@@ -501,7 +510,16 @@ __global__ void __launch_bounds__(kThreads, 3) lm_step_q4_kernel(const __grid_co
                                 s[i][x][3] = fmaf(sb, d[3], s[i][x][3]);
                             }
                         }
-                    }
+                    });
+                    // values: scales and lows of keys 2 t, 2 t + 1 and of those 8 further
+                    uint32_t sc[kAt][2 * G], vl[kAt][2];
+                    each<kAt>([&](auto I) {
+                        constexpr int i = I, kP = (kTiles + i) * kTile + Tile::kParams;
+                        lds<4, kP>(kt + vs_at, sc[i]);
+                        if constexpr (G == 4) lds<4, kP + 16>(kt + vs_at, sc[i] + 4);
+                        lds<2, kP + D>(kt + vl_at, vl[i]);
+                        if (r >= G) vl[i][0] = vl[i][1] = 0u;
+                    });
                     if (here + 16 * kAt > n.keys) {
                         // what lies behind the last key may be anything
 #pragma unroll
@@ -577,11 +595,11 @@ __global__ void __launch_bounds__(kThreads, 3) lm_step_q4_kernel(const __grid_co
                                 low[x][h] *= f;
                             }
                     }
-#pragma unroll
-                    for (int i = 0; i < kAt; i++) {
+                    each<kAt>([&](auto I) {
+                        constexpr int i = I, kOff = (kTiles + i) * kTile;
                         uint32_t va[G], vb[G], f0[NT], f1[NT];
-                        lds<G>(vt + i * kTile + v_at, va);
-                        lds<G>(vt + i * kTile + v_at + 4 * D, vb);
+                        lds<G, kOff>(kt + v_at, va);
+                        lds<G, kOff + 4 * D>(kt + v_at, vb);
 #pragma unroll
                         for (int x = 0; x < NT; x++) {
                             const float p0 = exp2_fast(fmaf(s[i][x][0], cf[x][0], bias[x][0])), p1 = exp2_fast(fmaf(s[i][x][1], cf[x][1], bias[x][1]));
@@ -603,7 +621,7 @@ __global__ void __launch_bounds__(kThreads, 3) lm_step_q4_kernel(const __grid_co
                                 mma(acc[x][g][1], a2, a3, b2, b3, g0, g1);
                             }
                         }
-                    }
+                    });
                 }
             }
             __syncwarp();
@@ -749,7 +767,7 @@ cudaError_t launch(const LmShape& sh, const LmStepArgs& a, cudaStream_t s)
     }
     const bool wide = sh.group > 8;
     int per_sm = 1;
-    fit<D>(p, 3, per_sm);
+    fit<D>(p, wide ? 3 : CT, per_sm);
     // a unit per request and head at least, and no more CTAs than the SMs hold at once
     const long long most = (long long)a.B * p.max_splits * sh.hk;
     const unsigned ctas = (unsigned)std::min<long long>(152 * per_sm, (most + kWarps - 1) / kWarps);
