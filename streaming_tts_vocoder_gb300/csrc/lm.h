@@ -247,12 +247,12 @@ cudaError_t launch_lm_fork(const LmForkArgs& a, cudaStream_t s);
 cudaError_t launch_lm_compact(const LmCompactArgs& a, cudaStream_t s);
 cudaError_t launch_lm_copy(const LmCopyArgs& a, cudaStream_t s);
 
-// Beam search: the best candidates of a part of a row, its log(sum(exp(x))) and maximum.
+// Beam search: the best candidates of a part of a row, its maximum and sum.
 constexpr int kLmMaxBeams = 32;
 struct LmBeamPart {
-    double lse;
+    double sum;                     // of 2^(x log2 e - c)
     float top;
-    int pad;
+    int c;
 };
 struct LmBeamSpace {
     int parts;                      // that the workspace holds

@@ -8,8 +8,8 @@
 // then a search of the lanes' maxima, largest first, for values that belong into
 // the list of the best; a lane's values are read once more for it, 64 by the
 // whole warp.  The second launch joins the parts and picks among a group's rows by
-// sums + x - log(sum), in fp64: lists are sorted, so a thread per list and a
-// reduction over their heads for each candidate.
+// sums + x - log(sum), in fp64: lists are sorted, so a warp looks at their heads
+// alone for each candidate, as whole numbers of the same order (three reductions).
 //
 // What decides between rows is the logarithm, and sums of exponentials in fp32
 // are off by up to kNear.  Where two neighbours of the result (or the last and
@@ -19,19 +19,24 @@
 
 #include "lm.h"
 
+#ifndef RB
+#define RB 8
+#endif
 namespace codec {
 
 namespace {
 
 constexpr int kThreads = 256;
-// Two rows' errors: of 2^-22 by ex2, 16 additions and a product rounded by 2^-24 of
-// at most 20 each.
-constexpr float kNear = 6e-6f;
+// A row's logarithm is off by 2^-22 at most for ex2, 2^-24 for each of 16 additions
+// and of the product with log2 e (times up to 20); of either sign, they come to 1e-7.
+constexpr float kNear = 2e-6f;
+constexpr double kLog2eOff = 1.4426950408889634f / 1.4426950408889634074 - 1.;    // of log2 e as a float, relative
 constexpr int kLists = 256;                 // of a group: beams x parts of a row
 
 constexpr int kRowWarps = 4;
 constexpr int kRowThreads = 32 * kRowWarps;
 constexpr int kVectors = 8;                 // of 16 bytes a lane: a chunk of a row is 4 KB
+constexpr int kWindow = 8;                  // chunks whose best are looked for at once
 
 __device__ __forceinline__ float to_float(float x) { return x; }
 __device__ __forceinline__ float to_float(__half x) { return __half2float(x); }
@@ -122,18 +127,32 @@ __device__ __forceinline__ int ordered(float x)
     return i >= 0 ? i : i ^ 0x7fffffff;
 }
 
-// Row blockIdx.x, part blockIdx.y of it: the chunks of which a warp takes every
-// kRowWarps-th.
+// 2^(c - most), 0 where c is none or far below.
+__device__ __forceinline__ float power_of_two(int c, int most)
+{
+    return c == INT_MIN || c < most - 126 ? 0.f : __int_as_float((127 + c - most) << 23);
+}
+
+// hi + lo += y with the rounding error kept.
+__device__ __forceinline__ void add_kept(float& hi, float& lo, float y)
+{
+    const float t = __fadd_rn(hi, y), b = __fsub_rn(t, hi);
+    lo += __fadd_rn(__fsub_rn(hi, __fsub_rn(t, b)), __fsub_rn(y, b));
+    hi = t;
+}
+
+// Row blockIdx.x, part blockIdx.y of it: chunks of which a warp takes every
+// kRowWarps-th, kWindow at a time.
 template <typename T>
-__global__ void __launch_bounds__(kRowThreads) lm_beam_rows_kernel(const LmBeamArgs a)
+__global__ void __launch_bounds__(kRowThreads, RB) lm_beam_rows_kernel(const LmBeamArgs a)
 {
     using V = Vector<T>;
     constexpr int kChunk = kVectors * 32 * V::N;
     constexpr float kLog2e = 1.4426950408889634f;
-    __shared__ float list_x[kRowThreads];
+    __shared__ float list_x[kRowThreads], tops[kRowWarps][kWindow][32];
     __shared__ int list_i[kRowThreads];
-    __shared__ double part_l[kRowWarps];
-    __shared__ float part_top[kRowWarps];
+    __shared__ float part_hi[kRowWarps], part_lo[kRowWarps], part_top[kRowWarps];
+    __shared__ int part_c[kRowWarps];
     const int row = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, K = a.beams;
     pdl_wait();
     pdl_launch();
@@ -153,86 +172,107 @@ __global__ void __launch_bounds__(kRowThreads) lm_beam_rows_kernel(const LmBeamA
     float top = -INFINITY, hi = 0.f, lo = 0.f;  // of the warp; this lane's sum
     int C = INT_MIN;
     bool bad = false;
-    for (int c = blockIdx.y * each + warp; c < last; c += kRowWarps) {
-        const int v0 = c * kChunk + lane * V::N;
-        uint4 raw[kVectors];
-        if (c * kChunk >= lead && (c + 1) * kChunk <= end) {
+    for (int c0 = blockIdx.y * each + warp; c0 < last && !bad; c0 += kRowWarps * kWindow) {
+        int n = 0;                              // chunks of the window
+        for (int c = c0; n < kWindow && c < last; c += kRowWarps, n++) {
+            const int v0 = c * kChunk + lane * V::N;
+            uint4 raw[kVectors];
+            if (c * kChunk >= lead && (c + 1) * kChunk <= end) {
 #pragma unroll
-            for (int i = 0; i < kVectors; i++)
-                raw[i] = __ldg(reinterpret_cast<const uint4*>(base + v0 + i * 32 * V::N));
-        } else {
+                for (int i = 0; i < kVectors; i++)
+                    raw[i] = __ldg(reinterpret_cast<const uint4*>(base + v0 + i * 32 * V::N));
+            } else {
+                // the row's first or last: vectors that pass its ends value by value
+#pragma unroll
+                for (int i = 0; i < kVectors; i++) {
+                    const int v1 = v0 + i * 32 * V::N;
+                    if (v1 >= lead && v1 + V::N <= end) {
+                        raw[i] = __ldg(reinterpret_cast<const uint4*>(base + v1));
+                    } else {
+                        alignas(16) T e[V::N];
+#pragma unroll
+                        for (int j = 0; j < V::N; j++) e[j] = v1 + j >= lead && v1 + j < end ? base[v1 + j] : minus_infinity<T>();
+                        raw[i] = *reinterpret_cast<const uint4*>(e);
+                    }
+                }
+            }
+            float mine = V::top(raw[0]);
+#pragma unroll
+            for (int i = 1; i < kVectors; i++) mine = max_nan(mine, V::top(raw[i]));
+            bad = __any_sync(0xffffffffu, !(mine < INFINITY));
+            if (bad) break;
+            tops[warp][n][lane] = mine;
+            const int most = __reduce_max_sync(0xffffffffu, ordered(mine));
+            const float chunk_top = __int_as_float(most >= 0 ? most : most ^ 0x7fffffff);
+            if (chunk_top == -INFINITY) continue;
+            if (chunk_top > top) {
+                top = chunk_top;
+                const int now = (int)ceilf(top * kLog2e);
+                const float f = power_of_two(C, now);
+                hi *= f;
+                lo *= f;
+                C = now;
+            }
+            const float2 c2 = make_float2(-(float)C, -(float)C), log2e = make_float2(kLog2e, kLog2e);
+            float2 sum[2] = {};
 #pragma unroll
             for (int i = 0; i < kVectors; i++) {
-                alignas(16) T e[V::N];
+                float y[V::N];
+                V::get(raw[i], y);
 #pragma unroll
-                for (int j = 0; j < V::N; j++) {
-                    const int v = v0 + i * 32 * V::N + j;
-                    e[j] = v >= lead && v < end ? base[v] : minus_infinity<T>();
+                for (int j = 0; j < V::N; j += 2) {
+                    float2 e = __ffma2_rn(make_float2(y[j], y[j + 1]), log2e, c2);
+                    e = make_float2(exp2_fast(e.x), exp2_fast(e.y));
+                    sum[j / 2 & 1] = __fadd2_rn(sum[j / 2 & 1], e);
                 }
-                raw[i] = *reinterpret_cast<const uint4*>(e);
             }
+            add_kept(hi, lo, (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y));
         }
-        float mine = V::top(raw[0]);
+        if (bad) break;
+        // The window's (lane, chunk) with the largest values first, until none can
+        // hold one that belongs into the list.
+        float mx[kWindow];
 #pragma unroll
-        for (int i = 1; i < kVectors; i++) mine = max_nan(mine, V::top(raw[i]));
-        bad |= !(mine < INFINITY);
-        if (__any_sync(0xffffffffu, bad)) break;
-        const int key = ordered(mine), most = __reduce_max_sync(0xffffffffu, key);
-        const float chunk_top = __int_as_float(most >= 0 ? most : most ^ 0x7fffffff);
-        if (chunk_top == -INFINITY) continue;
-        if (chunk_top > top) {
-            top = chunk_top;
-            const int now = (int)ceilf(top * kLog2e);
-            const float f = C == INT_MIN ? 0.f : C - now < -126 ? 0.f : __int_as_float((127 + C - now) << 23);
-            hi *= f;
-            lo *= f;
-            C = now;
-        }
-        const float minus_c = -(float)C;
-        float sum[4] = {};
+        for (int j = 0; j < kWindow; j++) mx[j] = j < n ? tops[warp][j][lane] : -INFINITY;
+        for (int turn = 0; turn < 32 * kWindow; turn++) {
+            float mine = mx[0];
+            int which = 0;
 #pragma unroll
-        for (int i = 0; i < kVectors; i++) {
-            float y[V::N];
-            V::get(raw[i], y);
-#pragma unroll
-            for (int j = 0; j < V::N; j++) sum[j & 3] += exp2_fast(fmaf(y[j], kLog2e, minus_c));
-        }
-        // added with the rounding error kept
-        const float s = (sum[0] + sum[1]) + (sum[2] + sum[3]), t = __fadd_rn(hi, s), b = __fsub_rn(t, hi);
-        lo += __fadd_rn(__fsub_rn(hi, __fsub_rn(t, b)), __fsub_rn(s, b));
-        hi = t;
-        // lanes with values that belong into the list, the largest first (equal ones
-        // only where a value may come before those of the list)
-        int pending = key;
-        for (int lanes = 0; lanes < 32; lanes++) {
-            const int k = __reduce_max_sync(0xffffffffu, pending);
+            for (int j = 1; j < kWindow; j++)
+                if (mx[j] > mine) {
+                    mine = mx[j];
+                    which = j;
+                }
+            const int key = ordered(mine), k = __reduce_max_sync(0xffffffffu, key);
             const float y = __int_as_float(k >= 0 ? k : k ^ 0x7fffffff);
-            if (y == -INFINITY || y < least || (y == least && c * kChunk - lead > least_i)) break;
-            const int from = __ffs(__ballot_sync(0xffffffffu, pending == k)) - 1;
-            if (lane == from) pending = INT_MIN;
+            if (y == -INFINITY || y < least) break;
+            const int from = __ffs(__ballot_sync(0xffffffffu, key == k)) - 1;
+            const int c = c0 + kRowWarps * __shfl_sync(0xffffffffu, which, from);
+#pragma unroll
+            for (int j = 0; j < kWindow; j++)
+                if (lane == from && j == which) mx[j] = -INFINITY;
+            if (y == least && c * kChunk - lead > least_i) continue;    // equal ones only before those of the list
             // its values: V::N / 4 for each lane
             constexpr int kE = V::N / 4;
             const int at = c * kChunk + ((lane >> 2) * 32 + from) * V::N + (lane & 3) * kE;
+            float z[kE];
+#pragma unroll
+            for (int j = 0; j < kE; j++) z[j] = at + j >= lead && at + j < end ? to_float(base[at + j]) : -INFINITY;
 #pragma unroll
             for (int j = 0; j < kE; j++) {
-                const int v = at + j;
-                const float z = v >= lead && v < end ? to_float(base[v]) : -INFINITY;
-                unsigned in = __ballot_sync(0xffffffffu, z > -INFINITY && ahead(z, v - lead, least, least_i));
+                unsigned in = __ballot_sync(0xffffffffu, z[j] > -INFINITY && ahead(z[j], at + j - lead, least, least_i));
+                if (in == 0) continue;
                 while (in) {
                     const int who = __ffs(in) - 1;
                     in &= in - 1;
-                    const float nx = __shfl_sync(0xffffffffu, z, who);
-                    const int ni = __shfl_sync(0xffffffffu, v - lead, who);
-                    const unsigned before = __ballot_sync(0xffffffffu, ahead(best_x, best_i, nx, ni));
+                    const float nx = __shfl_sync(0xffffffffu, z[j], who);
+                    const int ni = __shfl_sync(0xffffffffu, at + j - lead, who);
+                    const int place = __popc(__ballot_sync(0xffffffffu, ahead(best_x, best_i, nx, ni)));
                     const float ux = __shfl_up_sync(0xffffffffu, best_x, 1);
                     const int ui = __shfl_up_sync(0xffffffffu, best_i, 1);
-                    const int place = __popc(before);
-                    if (lane > place) {
-                        best_x = ux;
-                        best_i = ui;
-                    } else if (lane == place) {
-                        best_x = nx;
-                        best_i = ni;
+                    if (lane >= place) {
+                        best_x = lane == place ? nx : ux;
+                        best_i = lane == place ? ni : ui;
                     }
                 }
                 least = __shfl_sync(0xffffffffu, best_x, K - 1);
@@ -240,15 +280,17 @@ __global__ void __launch_bounds__(kRowThreads) lm_beam_rows_kernel(const LmBeamA
             }
         }
     }
-    bad = __any_sync(0xffffffffu, bad);
     list_x[tid] = lane < K ? best_x : -INFINITY;
     list_i[tid] = lane < K ? best_i : INT_MAX;
-    double l = (double)hi + (double)lo;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+    for (int o = 16; o > 0; o >>= 1) {
+        lo += __shfl_xor_sync(0xffffffffu, lo, o);
+        add_kept(hi, lo, __shfl_xor_sync(0xffffffffu, hi, o));
+    }
     if (lane == 0) {
-        // kLog2e is 1.33e-8 of itself too small
-        part_l[warp] = top == -INFINITY ? -INFINITY : ((double)C + log2(l)) * 0.6931471805599453 + 1.3349623e-8 * (double)top;
+        part_hi[warp] = hi;
+        part_lo[warp] = lo;
+        part_c[warp] = C;
         part_top[warp] = bad ? NAN : top;
     }
     __syncthreads();
@@ -256,23 +298,27 @@ __global__ void __launch_bounds__(kRowThreads) lm_beam_rows_kernel(const LmBeamA
     // the warps' lists: a value's place is the number of those before it
     const float mx = list_x[tid];
     const int mi = list_i[tid];
-    if (lane < K && mx > -INFINITY) {
-        int place = 0;
+    if (mx > -INFINITY) {
+        int place = lane;
         for (int w = 0; w < kRowWarps; w++)
-            for (int j = 0; j < K; j++) place += ahead(list_x[w * 32 + j], list_i[w * 32 + j], mx, mi);
+            if (w != warp)
+                for (int j = 0; j < K && ahead(list_x[w * 32 + j], list_i[w * 32 + j], mx, mi); j++) place++;
         if (place < K) a.ws.best[at * K + place] = make_uint2(__float_as_uint(mx), (unsigned)mi);
     }
     // places that nothing takes
-    const int there = __syncthreads_count(lane < K && mx > -INFINITY);
+    const int there = __syncthreads_count(mx > -INFINITY);
     if (tid >= there && tid < K) a.ws.best[at * K + tid] = make_uint2(__float_as_uint(-INFINITY), (unsigned)INT_MAX);
     if (tid == 0) {
+        int most = part_c[0];
         float m = part_top[0];
-        for (int w = 1; w < kRowWarps; w++) m = max_nan(m, part_top[w]);
-        double sum = 0., most = part_l[0];
-        for (int w = 1; w < kRowWarps; w++) most = fmax(most, part_l[w]);
-        if (most > -INFINITY)
-            for (int w = 0; w < kRowWarps; w++) sum += exp(part_l[w] - most);
-        a.ws.part[at] = LmBeamPart{most > -INFINITY ? most + log(sum) : most, m, 0};
+        for (int w = 1; w < kRowWarps; w++) {
+            m = max_nan(m, part_top[w]);
+            most = max(most, part_c[w]);
+        }
+        double sum = 0.;
+        for (int w = 0; w < kRowWarps; w++)
+            sum += ((double)part_hi[w] + (double)part_lo[w]) * power_of_two(part_c[w], most);
+        a.ws.part[at] = LmBeamPart{sum, m, most};
     }
 }
 
@@ -321,9 +367,10 @@ __global__ void __launch_bounds__(kThreads) lm_beam_pick_kernel(const LmBeamArgs
     extern __shared__ uint2 list[];
     __shared__ double base[kLmMaxBeams];        // sums - log(sum(exp)), or the sum of an ended beam
     __shared__ float top[kLmMaxBeams];
+    __shared__ int power[kLmMaxBeams];
     __shared__ int kind[kLmMaxBeams];           // 0: offers nothing, 1: tokens, 2: itself
-    __shared__ double ws[2][kThreads / 32], sums[kThreads / 32], got[kLmMaxBeams + 1];
-    __shared__ int wi[2][kThreads / 32], got_i[kLmMaxBeams + 1];
+    __shared__ double sums[kThreads / 32], got[kLmMaxBeams + 1];
+    __shared__ int got_i[kLmMaxBeams + 1];
     __shared__ float2 table[64];
     __shared__ unsigned again;
     const int K = a.beams, row0 = blockIdx.x * K, lists = K * parts;
@@ -333,92 +380,96 @@ __global__ void __launch_bounds__(kThreads) lm_beam_pick_kernel(const LmBeamArgs
     for (int e = tid; e < lists * K; e += kThreads) list[e] = __ldcg(a.ws.best + (long long)row0 * parts * K + e);
     for (int r = warp; r < K; r += kThreads / 32) {
         const int row = row0 + r;
-        const float sum = __ldg(a.sums + row);
-        const bool there = fabsf(sum) < INFINITY, end = __ldg(a.ended + row) != 0;
-        double l = 0.;
         float m = -INFINITY;
-        if (there && !end) {
-            double most = -INFINITY;
+        double l = 0.;
+        int most = INT_MIN;
+        if (offers(a, row)) {
+            const LmBeamPart* part = a.ws.part + (long long)row * parts;
             for (int i = lane; i < parts; i += 32) {
-                const LmBeamPart* p = a.ws.part + (long long)row * parts + i;
-                m = max_nan(m, __ldcg(&p->top));
-                most = fmax(most, __ldcg(&p->lse));
+                m = max_nan(m, __ldcg(&part[i].top));
+                most = max(most, __ldcg(&part[i].c));
             }
-            for (int o = 16; o > 0; o >>= 1) {
+            most = __reduce_max_sync(0xffffffffu, most);
+            for (int i = lane; i < parts; i += 32) l += __ldcg(&part[i].sum) * power_of_two(__ldcg(&part[i].c), most);
+            for (int o = parts > 1 ? 16 : 0; o > 0; o >>= 1) {
                 m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
-                most = fmax(most, __shfl_xor_sync(0xffffffffu, most, o));
-            }
-            if (fabsf(m) < INFINITY) {
-                for (int i = lane; i < parts; i += 32) l += exp(__ldcg(&a.ws.part[(long long)row * parts + i].lse) - most);
-                for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
-                l = most + log(l);
+                l += __shfl_xor_sync(0xffffffffu, l, o);
             }
         }
         if (lane == 0) {
             top[r] = m;
-            kind[r] = !there ? 0 : end ? 2 : fabsf(m) < INFINITY ? 1 : 0;
-            base[r] = end ? (double)sum : (double)sum - l;
+            base[r] = l;
+            power[r] = most;
         }
     }
     if (tid == 0) again = 0;
     __syncthreads();
-    // this thread's list: its row, and its head's score and index (row of the group, token)
-    const int r = min(tid / parts, K - 1);
-    int at = 0;
-    double s = -INFINITY;
-    int i = INT_MAX;
-    auto head = [&]() {
-        s = -INFINITY;
-        i = INT_MAX;
-        if (tid >= lists || at == K) return;
-        if (kind[r] == 1) {
-            const uint2 c = list[tid * K + at];
-            const float x = __uint_as_float(c.x);
-            if (x > -INFINITY) {
-                s = base[r] + (double)x;
-                i = r * a.vocab + (int)c.y;
-            }
-        } else if (kind[r] == 2 && tid == r * parts && at == 0) {
-            s = base[r];
-            i = r * a.vocab + max(a.end_token, 0);
-        }
-    };
+    // a lane per row: fp64 is slow, and a logarithm costs a warp what it costs a lane
+    if (tid < K) {
+        const float sum = __ldg(a.sums + row0 + tid), m = top[tid];
+        const bool there = fabsf(sum) < INFINITY, itself = __ldg(a.ended + row0 + tid) != 0;
+        kind[tid] = !there ? 0 : itself ? 2 : fabsf(m) < INFINITY ? 1 : 0;
+        // sums of 2^(x log2 e - c), with a log2 e that is 1.33e-8 of itself too small or large
+        base[tid] = kind[tid] != 1 ? (double)sum
+                                   : (double)sum - ((log(base[tid]) + power[tid] * 0.69314718055994531) - kLog2eOff * (double)m);
+    }
+    __syncthreads();
     for (int round = 0; round < 2; round++) {
-        at = 0;
-        head();
-        // one more than are wanted, to see how near it is
-        for (int k = 0; k <= K; k++) {
-            double best = s;
-            int best_i = i;
+        // The first warp picks: lane l has lists l, l + 32, .., each at its `at`-th
+        // entry, and the best of their heads as whole numbers of the same order.
+        if (warp == 0) {
+            int at[kLists / 32] = {};
+            unsigned hi = 0, lo = 0;
+            int best_i = INT_MAX, which = 0;
+            auto look = [&]() {
+                unsigned long long key = 0;
+                best_i = INT_MAX;
 #pragma unroll
-            for (int o = 16; o > 0; o >>= 1) {
-                const double y = __shfl_xor_sync(0xffffffffu, best, o);
-                const int j = __shfl_xor_sync(0xffffffffu, best_i, o);
-                if (ahead(y, j, best, best_i)) {
-                    best = y;
-                    best_i = j;
+                for (int j = 0; j < kLists / 32; j++) {
+                    const int l = lane + 32 * j;
+                    if (l >= lists || at[j] == K) continue;
+                    const int r = l / parts;
+                    double s = -INFINITY;
+                    int i = INT_MAX;
+                    if (kind[r] == 1) {
+                        const uint2 c = list[l * K + at[j]];
+                        if (__uint_as_float(c.x) > -INFINITY) {
+                            s = base[r] + (double)__uint_as_float(c.x);
+                            i = r * a.vocab + (int)c.y;
+                        }
+                    } else if (kind[r] == 2 && l == r * parts && at[j] == 0) {
+                        s = base[r];
+                        i = r * a.vocab + max(a.end_token, 0);
+                    }
+                    if (i == INT_MAX) continue;
+                    const long long bits = __double_as_longlong(s);
+                    const unsigned long long k = bits < 0 ? ~(unsigned long long)bits : (unsigned long long)bits | 1ULL << 63;
+                    if (best_i == INT_MAX || k > key || (k == key && i < best_i)) {
+                        key = k;
+                        best_i = i;
+                        which = j;
+                    }
                 }
-            }
-            if (lane == 0) {
-                ws[k & 1][warp] = best;
-                wi[k & 1][warp] = best_i;
-            }
-            __syncthreads();                    // two sets: the next round writes the other
-            best = ws[k & 1][0];
-            best_i = wi[k & 1][0];
+                hi = (unsigned)(key >> 32);
+                lo = (unsigned)key;
+            };
+            look();
+            // one more than are wanted, to see how near it is
+            for (int k = 0; k <= K; k++) {
+                const unsigned top_hi = __reduce_max_sync(0xffffffffu, best_i == INT_MAX ? 0u : hi);
+                const unsigned top_lo = __reduce_max_sync(0xffffffffu, best_i != INT_MAX && hi == top_hi ? lo : 0u);
+                const int winner = __reduce_min_sync(0xffffffffu, hi == top_hi && lo == top_lo ? best_i : INT_MAX);
+                if (lane == 0) {
+                    const unsigned long long key = (unsigned long long)top_hi << 32 | top_lo;
+                    got[k] = __longlong_as_double((long long)(key >> 63 ? key & ~(1ULL << 63) : ~key));
+                    got_i[k] = winner;
+                }
+                if (winner != INT_MAX && best_i == winner) {
 #pragma unroll
-            for (int w = 1; w < kThreads / 32; w++)
-                if (ahead(ws[k & 1][w], wi[k & 1][w], best, best_i)) {
-                    best = ws[k & 1][w];
-                    best_i = wi[k & 1][w];
+                    for (int j = 0; j < kLists / 32; j++)
+                        if (j == which) at[j]++;
+                    look();
                 }
-            if (tid == 0) {
-                got[k] = best;
-                got_i[k] = best_i;
-            }
-            if (i == best_i && i != INT_MAX) {
-                at++;
-                head();
             }
         }
         __syncthreads();
