@@ -36,7 +36,7 @@ constexpr int kLists = 256;                 // of a group: beams x parts of a ro
 constexpr int kRowWarps = 4;
 constexpr int kRowThreads = 32 * kRowWarps;
 constexpr int kVectors = 8;                 // of 16 bytes a lane: a chunk of a row is 4 KB
-constexpr int kWindow = 8;                  // chunks whose best are looked for at once
+constexpr int kWindow = 16;                 // chunks of each warp whose best are looked for at once
 
 __device__ __forceinline__ float to_float(float x) { return x; }
 __device__ __forceinline__ float to_float(__half x) { return __half2float(x); }
@@ -69,10 +69,14 @@ __device__ __forceinline__ float max_nan(float a, float b)
 template <typename T> struct Vector;
 template <> struct Vector<float> {
     static constexpr int N = 4;
-    static __device__ __forceinline__ float top(uint4 v)
+    // the largest (NaN if one is) of vectors: pairwise, then of the last
+    using Two = float2;
+    static __device__ __forceinline__ Two top(uint4 v)
     {
-        return max_nan(max_nan(__uint_as_float(v.x), __uint_as_float(v.y)), max_nan(__uint_as_float(v.z), __uint_as_float(v.w)));
+        return make_float2(max_nan(__uint_as_float(v.x), __uint_as_float(v.y)), max_nan(__uint_as_float(v.z), __uint_as_float(v.w)));
     }
+    static __device__ __forceinline__ Two max(Two a, Two b) { return make_float2(max_nan(a.x, b.x), max_nan(a.y, b.y)); }
+    static __device__ __forceinline__ float2 split(Two a) { return a; }
     static __device__ __forceinline__ void get(uint4 v, float* x)
     {
         x[0] = __uint_as_float(v.x); x[1] = __uint_as_float(v.y); x[2] = __uint_as_float(v.z); x[3] = __uint_as_float(v.w);
@@ -81,11 +85,13 @@ template <> struct Vector<float> {
 template <> struct Vector<__nv_bfloat16> {
     static constexpr int N = 8;
     static __device__ __forceinline__ __nv_bfloat162 two(uint32_t w) { return *reinterpret_cast<const __nv_bfloat162*>(&w); }
-    static __device__ __forceinline__ float top(uint4 v)
+    using Two = __nv_bfloat162;
+    static __device__ __forceinline__ Two top(uint4 v)
     {
-        const float2 f = __bfloat1622float2(__hmax2_nan(__hmax2_nan(two(v.x), two(v.y)), __hmax2_nan(two(v.z), two(v.w))));
-        return max_nan(f.x, f.y);
+        return __hmax2_nan(__hmax2_nan(two(v.x), two(v.y)), __hmax2_nan(two(v.z), two(v.w)));
     }
+    static __device__ __forceinline__ Two max(Two a, Two b) { return __hmax2_nan(a, b); }
+    static __device__ __forceinline__ float2 split(Two a) { return __bfloat1622float2(a); }
     static __device__ __forceinline__ void get(uint4 v, float* x)
     {
         const uint32_t w[4] = {v.x, v.y, v.z, v.w};
@@ -99,11 +105,13 @@ template <> struct Vector<__nv_bfloat16> {
 template <> struct Vector<__half> {
     static constexpr int N = 8;
     static __device__ __forceinline__ __half2 two(uint32_t w) { return *reinterpret_cast<const __half2*>(&w); }
-    static __device__ __forceinline__ float top(uint4 v)
+    using Two = __half2;
+    static __device__ __forceinline__ Two top(uint4 v)
     {
-        const float2 f = __half22float2(__hmax2_nan(__hmax2_nan(two(v.x), two(v.y)), __hmax2_nan(two(v.z), two(v.w))));
-        return max_nan(f.x, f.y);
+        return __hmax2_nan(__hmax2_nan(two(v.x), two(v.y)), __hmax2_nan(two(v.z), two(v.w)));
     }
+    static __device__ __forceinline__ Two max(Two a, Two b) { return __hmax2_nan(a, b); }
+    static __device__ __forceinline__ float2 split(Two a) { return __half22float2(a); }
     static __device__ __forceinline__ void get(uint4 v, float* x)
     {
         const uint32_t w[4] = {v.x, v.y, v.z, v.w};
@@ -141,16 +149,15 @@ __device__ __forceinline__ void add_kept(float& hi, float& lo, float y)
     hi = t;
 }
 
-// Row blockIdx.x, part blockIdx.y of it: chunks of which a warp takes every
-// kRowWarps-th, kWindow at a time.
+// Row blockIdx.x, part blockIdx.y of it: windows of chunks, of which a warp takes
+// every kRowWarps-th.
 template <typename T>
 __global__ void __launch_bounds__(kRowThreads, RB) lm_beam_rows_kernel(const LmBeamArgs a)
 {
     using V = Vector<T>;
     constexpr int kChunk = kVectors * 32 * V::N;
     constexpr float kLog2e = 1.4426950408889634f;
-    __shared__ float list_x[kRowThreads], tops[kRowWarps][kWindow][32];
-    __shared__ int list_i[kRowThreads];
+    __shared__ float tops[kRowWarps][kWindow][32];
     __shared__ float part_hi[kRowWarps], part_lo[kRowWarps], part_top[kRowWarps];
     __shared__ int part_c[kRowWarps];
     const int row = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, K = a.beams;
@@ -165,17 +172,19 @@ __global__ void __launch_bounds__(kRowThreads, RB) lm_beam_rows_kernel(const LmB
     const int last = min(chunks, ((int)blockIdx.y + 1) * each);
     const T* base = x - lead;
 
-    float best_x = -INFINITY;                   // lane i < K: the i-th best
-    int best_i = INT_MAX;
-    float least = -INFINITY;                    // the K-th
-    int least_i = INT_MAX;
+    // of the first warp: lane i < K has the i-th best so far; the K-th
+    float best_x = -INFINITY, least = -INFINITY;
+    int best_i = INT_MAX, least_i = INT_MAX;
     float top = -INFINITY, hi = 0.f, lo = 0.f;  // of the warp; this lane's sum
     int C = INT_MIN;
     bool bad = false;
-    for (int c0 = blockIdx.y * each + warp; c0 < last && !bad; c0 += kRowWarps * kWindow) {
-        int n = 0;                              // chunks of the window
-        for (int c = c0; n < kWindow && c < last; c += kRowWarps, n++) {
+    for (int c0 = blockIdx.y * each; c0 < last; c0 += kRowWarps * kWindow) {
+        for (int n = 0; n < kWindow; n++) tops[warp][n][lane] = -INFINITY;
+        for (int n = 0, c = c0 + warp; n < kWindow && c < last && !bad; c += kRowWarps, n++) {
             const int v0 = c * kChunk + lane * V::N;
+            // the warp's next chunk to L2: a line of 128 bytes a lane
+            if (c + kRowWarps < last)
+                asm volatile("prefetch.global.L2 [%0];" ::"l"(base + min((c + kRowWarps) * kChunk + lane * (128 / (int)sizeof(T)), end - 1)));
             uint4 raw[kVectors];
             if (c * kChunk >= lead && (c + 1) * kChunk <= end) {
 #pragma unroll
@@ -196,9 +205,10 @@ __global__ void __launch_bounds__(kRowThreads, RB) lm_beam_rows_kernel(const LmB
                     }
                 }
             }
-            float mine = V::top(raw[0]);
+            typename V::Two pair = V::top(raw[0]);
 #pragma unroll
-            for (int i = 1; i < kVectors; i++) mine = max_nan(mine, V::top(raw[i]));
+            for (int i = 1; i < kVectors; i++) pair = V::max(pair, V::top(raw[i]));
+            const float mine = max_nan(V::split(pair).x, V::split(pair).y);
             bad = __any_sync(0xffffffffu, !(mine < INFINITY));
             if (bad) break;
             tops[warp][n][lane] = mine;
@@ -228,29 +238,54 @@ __global__ void __launch_bounds__(kRowThreads, RB) lm_beam_rows_kernel(const LmB
             }
             add_kept(hi, lo, (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y));
         }
-        if (bad) break;
-        // The window's (lane, chunk) with the largest values first, until none can
-        // hold one that belongs into the list.
-        float mx[kWindow];
-#pragma unroll
-        for (int j = 0; j < kWindow; j++) mx[j] = j < n ? tops[warp][j][lane] : -INFINITY;
-        for (int turn = 0; turn < 32 * kWindow; turn++) {
-            float mine = mx[0];
+        if (__syncthreads_or(bad)) {
+            bad = true;
+            break;
+        }
+        // The first warp takes the window's (lane, chunk) with the largest values first,
+        // until none can hold one that belongs into the list.
+        float mx[kRowWarps];                    // of this lane's chunks of each warp, and which
+        int of[kRowWarps];
+        auto look = [&](int w) {
+            float m = tops[w][0][lane];
             int which = 0;
 #pragma unroll
-            for (int j = 1; j < kWindow; j++)
-                if (mx[j] > mine) {
-                    mine = mx[j];
-                    which = j;
+            for (int j = 1; j < kWindow; j++) {
+                const float y = tops[w][j][lane];
+                which = y > m ? j : which;
+                m = fmaxf(m, y);
+            }
+#pragma unroll
+            for (int j = 0; j < kRowWarps; j++)
+                if (j == w) {
+                    mx[j] = m;
+                    of[j] = which;
                 }
+        };
+        if (warp == 0) {
+#pragma unroll
+            for (int w = 0; w < kRowWarps; w++) look(w);
+        }
+        for (int turn = 0; turn < 32 * kRowWarps * kWindow && warp == 0; turn++) {
+            float mine = mx[0];
+            int at_w = 0, at_j = of[0];
+#pragma unroll
+            for (int w = 1; w < kRowWarps; w++) {
+                at_j = mx[w] > mine ? of[w] : at_j;
+                at_w = mx[w] > mine ? w : at_w;
+                mine = fmaxf(mine, mx[w]);
+            }
             const int key = ordered(mine), k = __reduce_max_sync(0xffffffffu, key);
             const float y = __int_as_float(k >= 0 ? k : k ^ 0x7fffffff);
             if (y == -INFINITY || y < least) break;
             const int from = __ffs(__ballot_sync(0xffffffffu, key == k)) - 1;
-            const int c = c0 + kRowWarps * __shfl_sync(0xffffffffu, which, from);
-#pragma unroll
-            for (int j = 0; j < kWindow; j++)
-                if (lane == from && j == which) mx[j] = -INFINITY;
+            const int w = __shfl_sync(0xffffffffu, at_w, from), j0 = __shfl_sync(0xffffffffu, at_j, from);
+            const int c = c0 + w + kRowWarps * j0;
+            if (lane == from) {
+                tops[w][j0][lane] = -INFINITY;
+                look(w);
+            }
+            __syncwarp();
             if (y == least && c * kChunk - lead > least_i) continue;    // equal ones only before those of the list
             // its values: V::N / 4 for each lane
             constexpr int kE = V::N / 4;
@@ -279,9 +314,8 @@ __global__ void __launch_bounds__(kRowThreads, RB) lm_beam_rows_kernel(const LmB
                 least_i = __shfl_sync(0xffffffffu, best_i, K - 1);
             }
         }
+        __syncthreads();                        // tops are written again
     }
-    list_x[tid] = lane < K ? best_x : -INFINITY;
-    list_i[tid] = lane < K ? best_i : INT_MAX;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
         lo += __shfl_xor_sync(0xffffffffu, lo, o);
@@ -295,19 +329,7 @@ __global__ void __launch_bounds__(kRowThreads, RB) lm_beam_rows_kernel(const LmB
     }
     __syncthreads();
     const long long at = (long long)row * gridDim.y + blockIdx.y;
-    // the warps' lists: a value's place is the number of those before it
-    const float mx = list_x[tid];
-    const int mi = list_i[tid];
-    if (mx > -INFINITY) {
-        int place = lane;
-        for (int w = 0; w < kRowWarps; w++)
-            if (w != warp)
-                for (int j = 0; j < K && ahead(list_x[w * 32 + j], list_i[w * 32 + j], mx, mi); j++) place++;
-        if (place < K) a.ws.best[at * K + place] = make_uint2(__float_as_uint(mx), (unsigned)mi);
-    }
-    // places that nothing takes
-    const int there = __syncthreads_count(mx > -INFINITY);
-    if (tid >= there && tid < K) a.ws.best[at * K + tid] = make_uint2(__float_as_uint(-INFINITY), (unsigned)INT_MAX);
+    if (tid < K) a.ws.best[at * K + tid] = make_uint2(__float_as_uint(best_x), (unsigned)best_i);
     if (tid == 0) {
         int most = part_c[0];
         float m = part_top[0];
@@ -322,15 +344,37 @@ __global__ void __launch_bounds__(kRowThreads, RB) lm_beam_rows_kernel(const LmB
     }
 }
 
-// log(sum(exp(x))) of a row to about 1e-9, by the whole CTA.  exp(d) = 2^k 2^(j / 64)
-// (1 + p): the power of two of the table in two floats, p a short series of what
-// is left (at most ln 2 / 128), terms added with their rounding errors kept.
-template <typename T>
-__device__ double exact_log_sum(const T* x, int n, float top, const float2* table, double* sm)
+// exp(d + e) as 2^k 2^(j / 64) (1 + p): k, the power of two of the table (two floats),
+// and p, a short series of what is left (at most ln 2 / 128).  e: a small rest of d.
+__device__ __forceinline__ float2 exp_parts(float d, float e, const float2* table, float& p, float& scale)
 {
     constexpr float kInv = 92.332482616893656f;             // 64 / ln 2
     constexpr float kHi = 0x1.62cp-7f;                      // ln 2 / 64: 11 bits, and the rest
-    const float lo = (float)(0.010830424696249145 - (double)kHi);
+    constexpr float kLo = (float)(0.010830424696249145 - (double)kHi);
+    const float m = rintf(d * kInv);
+    const float r = fmaf(-m, kLo, fmaf(-m, kHi, d)) + e;
+    p = r * fmaf(r, fmaf(r, fmaf(r, 1.f / 24.f, 1.f / 6.f), 0.5f), 1.f);
+    const int im = (int)m;
+    scale = __int_as_float(((im >> 6) + 127) << 23);
+    return table[im & 63];
+}
+
+// log(s) to about 1e-9, s in 2^-64 .. 2^64: fp32's, and how far s is from its exponential
+// (log() itself takes some 2 us, fp64 being slow).
+__device__ __forceinline__ double log_of(double s, const float2* table)
+{
+    const float y = logf((float)s);
+    float p, scale;
+    const float2 t = exp_parts(-y, 0.f, table, p, scale);
+    const double off = fma(s, ((double)t.x + (double)t.y) * (1. + (double)p) * (double)scale, -1.);
+    return (double)y + off * (1. - 0.5 * off);
+}
+
+// log(sum(exp(x))) of a row to about 1e-9, by the whole CTA: terms added with their
+// rounding errors kept.
+template <typename T>
+__device__ double exact_log_sum(const T* x, int n, float top, const float2* table, double* sm)
+{
     const int tid = threadIdx.x;
     float s = 0.f, c = 0.f;
     for (int v = tid; v < n; v += kThreads) {
@@ -339,12 +383,8 @@ __device__ double exact_log_sum(const T* x, int n, float top, const float2* tabl
         if (!(d > -80.f)) continue;                         // nothing beside the maximum's 1
         const float u = __fsub_rn(d, y), w = __fsub_rn(d, u);
         const float e = __fadd_rn(__fsub_rn(y, w), __fsub_rn(-top, u));     // what d was rounded by
-        const float m = rintf(d * kInv);
-        const float r = fmaf(-m, lo, fmaf(-m, kHi, d)) + e;
-        const float p = r * fmaf(r, fmaf(r, fmaf(r, 1.f / 24.f, 1.f / 6.f), 0.5f), 1.f);
-        const int im = (int)m;
-        const float scale = __int_as_float(((im >> 6) + 127) << 23);
-        const float2 t = table[im & 63];
+        float p, scale;
+        const float2 t = exp_parts(d, e, table, p, scale);
         const float h = t.x * scale, l = fmaf(t.x, p, t.y) * scale;
         const float now = __fadd_rn(s, h), b = __fsub_rn(now, s);
         c += __fadd_rn(__fsub_rn(s, __fsub_rn(now, b)), __fsub_rn(h, b)) + l;
@@ -357,14 +397,15 @@ __device__ double exact_log_sum(const T* x, int n, float top, const float2* tabl
     __syncthreads();
     sum = 0.;
     for (int w = 0; w < kThreads / 32; w++) sum += sm[w];
-    return (double)top + log(sum);
+    return (double)top + log_of(sum, table);
 }
 
-// One group.  Dynamic shared memory: the lists, [K x parts][K].
+// One group.  Dynamic shared memory: the lists' scores as whole numbers of the same
+// order and their indexes (row of the group, token), [K x parts][K] each.
 template <typename T>
 __global__ void __launch_bounds__(kThreads) lm_beam_pick_kernel(const LmBeamArgs a, int parts)
 {
-    extern __shared__ uint2 list[];
+    extern __shared__ unsigned long long keys[];
     __shared__ double base[kLmMaxBeams];        // sums - log(sum(exp)), or the sum of an ended beam
     __shared__ float top[kLmMaxBeams];
     __shared__ int power[kLmMaxBeams];
@@ -375,26 +416,34 @@ __global__ void __launch_bounds__(kThreads) lm_beam_pick_kernel(const LmBeamArgs
     __shared__ unsigned again;
     const int K = a.beams, row0 = blockIdx.x * K, lists = K * parts;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    int* index = reinterpret_cast<int*>(keys + lists * K);
+    if (tid < 64) {
+        const double t = exp2(tid / 64.);
+        table[tid] = make_float2((float)t, (float)(t - (double)(float)t));
+    }
     pdl_wait();
     pdl_launch();
-    for (int e = tid; e < lists * K; e += kThreads) list[e] = __ldcg(a.ws.best + (long long)row0 * parts * K + e);
+    const uint2* best = a.ws.best + (long long)row0 * parts * K;
+    // on their way meanwhile
+    const uint2 ahead_of = tid < lists * K ? __ldcg(best + tid) : uint2{};
+    const float sum = tid < K ? __ldg(a.sums + row0 + tid) : 0.f;
+    const bool itself = tid < K && __ldg(a.ended + row0 + tid) != 0;
     for (int r = warp; r < K; r += kThreads / 32) {
         const int row = row0 + r;
+        // (a row that offers nothing wrote nothing: what is found there is not used)
         float m = -INFINITY;
         double l = 0.;
         int most = INT_MIN;
-        if (offers(a, row)) {
-            const LmBeamPart* part = a.ws.part + (long long)row * parts;
-            for (int i = lane; i < parts; i += 32) {
-                m = max_nan(m, __ldcg(&part[i].top));
-                most = max(most, __ldcg(&part[i].c));
-            }
-            most = __reduce_max_sync(0xffffffffu, most);
-            for (int i = lane; i < parts; i += 32) l += __ldcg(&part[i].sum) * power_of_two(__ldcg(&part[i].c), most);
-            for (int o = parts > 1 ? 16 : 0; o > 0; o >>= 1) {
-                m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
-                l += __shfl_xor_sync(0xffffffffu, l, o);
-            }
+        const LmBeamPart* part = a.ws.part + (long long)row * parts;
+        for (int i = lane; i < parts; i += 32) {
+            m = max_nan(m, __ldcg(&part[i].top));
+            most = max(most, __ldcg(&part[i].c));
+        }
+        most = __reduce_max_sync(0xffffffffu, most);
+        for (int i = lane; i < parts; i += 32) l += __ldcg(&part[i].sum) * power_of_two(__ldcg(&part[i].c), most);
+        for (int o = parts > 1 ? 16 : 0; o > 0; o >>= 1) {
+            m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
+            l += __shfl_xor_sync(0xffffffffu, l, o);
         }
         if (lane == 0) {
             top[r] = m;
@@ -404,19 +453,36 @@ __global__ void __launch_bounds__(kThreads) lm_beam_pick_kernel(const LmBeamArgs
     }
     if (tid == 0) again = 0;
     __syncthreads();
-    // a lane per row: fp64 is slow, and a logarithm costs a warp what it costs a lane
     if (tid < K) {
-        const float sum = __ldg(a.sums + row0 + tid), m = top[tid];
-        const bool there = fabsf(sum) < INFINITY, itself = __ldg(a.ended + row0 + tid) != 0;
+        const float m = top[tid];
+        const bool there = fabsf(sum) < INFINITY;
         kind[tid] = !there ? 0 : itself ? 2 : fabsf(m) < INFINITY ? 1 : 0;
         // sums of 2^(x log2 e - c), with a log2 e that is 1.33e-8 of itself too small or large
         base[tid] = kind[tid] != 1 ? (double)sum
-                                   : (double)sum - ((log(base[tid]) + power[tid] * 0.69314718055994531) - kLog2eOff * (double)m);
+                                   : (double)sum - ((log_of(base[tid], table) + power[tid] * 0.69314718055994531) - kLog2eOff * (double)m);
     }
     __syncthreads();
     for (int round = 0; round < 2; round++) {
+        for (int e = tid; e < lists * K; e += kThreads) {
+            const uint2 c = e == tid ? ahead_of : __ldcg(best + e);
+            const int l = e / K, r = l / parts;
+            const float x = __uint_as_float(c.x);
+            int i = INT_MAX;
+            double s = 0.;
+            if (kind[r] == 1 && x > -INFINITY) {
+                s = base[r] + (double)x;
+                i = r * a.vocab + (int)c.y;
+            } else if (kind[r] == 2 && e == r * parts * K) {
+                s = base[r];
+                i = r * a.vocab + max(a.end_token, 0);
+            }
+            const long long bits = __double_as_longlong(s);
+            keys[e] = bits < 0 ? ~(unsigned long long)bits : (unsigned long long)bits | 1ULL << 63;
+            index[e] = i;
+        }
+        __syncthreads();
         // The first warp picks: lane l has lists l, l + 32, .., each at its `at`-th
-        // entry, and the best of their heads as whole numbers of the same order.
+        // entry, and the best of their heads.
         if (warp == 0) {
             int at[kLists / 32] = {};
             unsigned hi = 0, lo = 0;
@@ -426,25 +492,12 @@ __global__ void __launch_bounds__(kThreads) lm_beam_pick_kernel(const LmBeamArgs
                 best_i = INT_MAX;
 #pragma unroll
                 for (int j = 0; j < kLists / 32; j++) {
+                    if (32 * j >= lists) break;
                     const int l = lane + 32 * j;
                     if (l >= lists || at[j] == K) continue;
-                    const int r = l / parts;
-                    double s = -INFINITY;
-                    int i = INT_MAX;
-                    if (kind[r] == 1) {
-                        const uint2 c = list[l * K + at[j]];
-                        if (__uint_as_float(c.x) > -INFINITY) {
-                            s = base[r] + (double)__uint_as_float(c.x);
-                            i = r * a.vocab + (int)c.y;
-                        }
-                    } else if (kind[r] == 2 && l == r * parts && at[j] == 0) {
-                        s = base[r];
-                        i = r * a.vocab + max(a.end_token, 0);
-                    }
-                    if (i == INT_MAX) continue;
-                    const long long bits = __double_as_longlong(s);
-                    const unsigned long long k = bits < 0 ? ~(unsigned long long)bits : (unsigned long long)bits | 1ULL << 63;
-                    if (best_i == INT_MAX || k > key || (k == key && i < best_i)) {
+                    const int i = index[l * K + at[j]];
+                    const unsigned long long k = keys[l * K + at[j]];
+                    if (i != INT_MAX && (best_i == INT_MAX || k > key || (k == key && i < best_i))) {
                         key = k;
                         best_i = i;
                         which = j;
@@ -483,12 +536,8 @@ __global__ void __launch_bounds__(kThreads) lm_beam_pick_kernel(const LmBeamArgs
         // and all that lie as near to the last one
         for (int e = tid; e < lists * K; e += kThreads) {
             const int row = e / K / parts;
-            if (kind[row] == 1 && fabs(base[row] + (double)__uint_as_float(list[e].x) - got[K - 1]) < kNear)
+            if (kind[row] == 1 && fabs(base[row] + (double)__uint_as_float(__ldcg(best + e).x) - got[K - 1]) < kNear)
                 atomicOr(&again, 1u << row);
-        }
-        if (tid < 64) {
-            const double t = exp2(tid / 64.);
-            table[tid] = make_float2((float)t, (float)(t - (double)(float)t));
         }
         __syncthreads();
         for (int q = 0; q < K; q++)
@@ -521,7 +570,7 @@ cudaError_t launch(const LmBeamArgs& a, cudaStream_t s)
     const int parts = (int)std::max<long long>(1, std::min<long long>({152 * 8 / rows, chunks / kRowWarps, kLists / a.beams}));
     const cudaError_t e = launch_pdl(lm_beam_rows_kernel<T>, dim3(rows, parts), dim3(kRowThreads), 0, s, a);
     if (e != cudaSuccess) return e;
-    return launch_pdl(lm_beam_pick_kernel<T>, dim3(a.groups), dim3(kThreads), sizeof(uint2) * a.beams * parts * a.beams, s, a,
+    return launch_pdl(lm_beam_pick_kernel<T>, dim3(a.groups), dim3(kThreads), (sizeof(unsigned long long) + sizeof(int)) * a.beams * parts * a.beams, s, a,
                       parts);
 }
 
@@ -529,7 +578,7 @@ template <typename T>
 cudaError_t configure()
 {
     return cudaFuncSetAttribute(lm_beam_pick_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                (int)sizeof(uint2) * kLists * kLmMaxBeams);
+                                (int)(sizeof(unsigned long long) + sizeof(int)) * kLists * kLmMaxBeams);
 }
 
 }  // namespace
