@@ -35,38 +35,55 @@ __device__ __forceinline__ void load8(const T* p, float* x)
     }
 }
 
-// Codes of 8 values, four lanes a group.  The steps and their roundings are the
-// format's: no contraction, no approximate reciprocal.
-__device__ __forceinline__ uint32_t encode(const float* in, __half& scale, __half& low)
+__device__ __forceinline__ float min_nan(float a, float b)
 {
-    const int lane = threadIdx.x & 31;
-    float x[8], lo = INFINITY, hi = -INFINITY;
-    bool good = true;
+    float y;
+    asm("min.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
+    return y;
+}
+__device__ __forceinline__ float max_nan(float a, float b)
+{
+    float y;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
+    return y;
+}
+
+// Codes of 8 values, four lanes a group.  The steps and their roundings are the
+// format's: no contraction, no approximate reciprocal.  A value beyond +-65504 needs
+// no cut of its own (its code is 0 or 15 as that one's is), and what is not finite
+// shows in the least and the largest.
+__device__ __forceinline__ uint32_t encode(const float* x, __half& scale, __half& low)
+{
+    float lo = x[0], hi = x[0];
 #pragma unroll
-    for (int i = 0; i < 8; i++) {
-        good &= fabsf(in[i]) < INFINITY;
-        x[i] = fminf(fmaxf(in[i], -65504.f), 65504.f);
-        lo = fminf(lo, x[i]);
-        hi = fmaxf(hi, x[i]);
+    for (int i = 1; i < 8; i++) {
+        lo = min_nan(lo, x[i]);
+        hi = max_nan(hi, x[i]);
     }
 #pragma unroll
     for (int o = 1; o < 4; o <<= 1) {
-        lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, o));
-        hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, o));
+        lo = min_nan(lo, __shfl_xor_sync(0xffffffffu, lo, o));
+        hi = max_nan(hi, __shfl_xor_sync(0xffffffffu, hi, o));
     }
-    good = (__ballot_sync(0xffffffffu, !good) >> (lane & 28) & 15u) == 0;
+    const bool good = fabsf(lo) < INFINITY && fabsf(hi) < INFINITY;
+    lo = fminf(fmaxf(lo, -65504.f), 65504.f);
+    hi = fminf(fmaxf(hi, -65504.f), 65504.f);
     scale = __float2half_rn(__fmul_rn(__fsub_rn(hi, lo), 1.f / 15.f));
     low = __float2half_rn(lo);
     const float s = __half2float(scale), l = __half2float(low);
     const float inv = __frcp_rn(s);
-    uint32_t word = 0;
+    // a number of 0 .. 15 and 1.5 x 2^23 is rounded to a whole one, which then stands in
+    // the last bits; what the others' bits add to the word is taken off at the end
+    constexpr float kWhole = 12582912.f;
+    uint32_t word = 0, rest = 0;
 #pragma unroll
     for (int i = 0; i < 8; i++) {
-        const float c = fminf(fmaxf(rintf(__fmul_rn(__fsub_rn(x[i], l), inv)), 0.f), 15.f);
-        word |= (uint32_t)c << (4 * i);
+        const float c = fminf(fmaxf(__fmul_rn(__fsub_rn(x[i], l), inv), 0.f), 15.f);
+        word += __float_as_uint(__fadd_rn(c, kWhole)) << (4 * i);
+        rest += 0x4b400000u << (4 * i);
     }
     if (!good) scale = low = __ushort_as_half(0x7fff);
-    return good && s > 0.f ? word : 0u;
+    return good && s > 0.f ? word - rest : 0u;
 }
 
 struct StoreArgs {
@@ -146,35 +163,54 @@ __device__ __forceinline__ uint32_t pack2(float a, float b, const __half*)
 }
 
 // A tile of 16 positions (null: zeros) to rows of the same head `stride` elements
-// apart; row: this lane's eight elements of the first.  A whole warp.
+// apart; row: this lane's eight elements of the first.  A whole warp; buf: a tile's
+// bytes of its own in shared memory.  Codes as they lie at the lowest bits of halves
+// are that many times 2^-24, four bits further 2^-20, and the scale makes up for it.
 template <typename T, int D>
-__device__ __forceinline__ void decode(const uint8_t* at, bool values, T* row, long long stride)
+__device__ __forceinline__ void decode(const uint8_t* at, bool values, T* row, long long stride, uint4* buf)
 {
     using Tile = Q4Tile<D>;
-    constexpr int kLanes = D / 8, kRows = 32 / kLanes;
+    constexpr int kLanes = D / 8, kRows = 32 / kLanes, kVectors = Tile::kBytes / 16;
     const int lane = threadIdx.x & 31, c = lane % kLanes, g = c >> 2, t = c & 3;
+    uint4 v[(kVectors + 31) / 32];
+#pragma unroll
+    for (int i = 0; i < (kVectors + 31) / 32; i++) {
+        const int x = lane + 32 * i;
+        v[i] = at && x < kVectors ? __ldg(reinterpret_cast<const uint4*>(at) + x) : uint4{};
+    }
+    __syncwarp();                       // buf may still be read
+#pragma unroll
+    for (int i = 0; i < (kVectors + 31) / 32; i++)
+        if (lane + 32 * i < kVectors) buf[lane + 32 * i] = v[i];
+    __syncwarp();
+    const uint8_t* tile = reinterpret_cast<const uint8_t*>(buf);
 #pragma unroll
     for (int p0 = 0; p0 < 16; p0 += kRows) {
         const int p = p0 + lane / kLanes;
-        uint32_t word = 0;
-        float scale = 0.f, low = 0.f;
-        if (at && !values) {
-            word = __ldg(reinterpret_cast<const uint32_t*>(at + Tile::k_word(p, t, g)));
-            const float2 f = __half22float2(__ldg(reinterpret_cast<const __half2*>(at + Tile::k_param(p, g))));
+        uint32_t word;
+        float scale, low;
+        if (!values) {
+            word = *reinterpret_cast<const uint32_t*>(tile + Tile::k_word(p, t, g));
+            const float2 f = __half22float2(*reinterpret_cast<const __half2*>(tile + Tile::k_param(p, g)));
             scale = f.x;
             low = f.y;
-        } else if (at) {
-            word = __ldg(reinterpret_cast<const uint16_t*>(at + Tile::v_pair(p, 2 * t, g))) |
-                   (uint32_t)__ldg(reinterpret_cast<const uint16_t*>(at + Tile::v_pair(p, 2 * t + 1, g))) << 16;
-            scale = __half2float(__ldg(reinterpret_cast<const __half*>(at + Tile::v_scale(p, g))));
-            low = __half2float(__ldg(reinterpret_cast<const __half*>(at + Tile::v_scale(p, g) + D)));
+        } else {
+            word = *reinterpret_cast<const uint16_t*>(tile + Tile::v_pair(p, 2 * t, g)) |
+                   (uint32_t)*reinterpret_cast<const uint16_t*>(tile + Tile::v_pair(p, 2 * t + 1, g)) << 16;
+            scale = __half2float(*reinterpret_cast<const __half*>(tile + Tile::v_scale(p, g)));
+            low = __half2float(*reinterpret_cast<const __half*>(tile + Tile::v_scale(p, g) + D));
         }
-        uint32_t o[4];
+        const float s0 = scale * 0x1p24f, s1 = scale * 0x1p20f;
+        float x[8];
 #pragma unroll
-        for (int j = 0; j < 4; j++)
-            o[j] = pack2(fmaf(scale, (float)(word >> (8 * j) & 15u), low),
-                         fmaf(scale, (float)(word >> (8 * j + 4) & 15u), low), row);
-        *reinterpret_cast<uint4*>(row + p * stride) = make_uint4(o[0], o[1], o[2], o[3]);
+        for (int j = 0; j < 4; j++) {   // codes j and j + 4
+            const uint32_t two = (j < 2 ? word : word >> 8) & (j & 1 ? 0x00f000f0u : 0x000f000fu);
+            const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&two));
+            x[j] = fmaf(j & 1 ? s1 : s0, f.x, low);
+            x[j + 4] = fmaf(j & 1 ? s1 : s0, f.y, low);
+        }
+        *reinterpret_cast<uint4*>(row + p * stride) =
+            make_uint4(pack2(x[0], x[1], row), pack2(x[2], x[3], row), pack2(x[4], x[5], row), pack2(x[6], x[7], row));
     }
 }
 
@@ -182,6 +218,7 @@ __device__ __forceinline__ void decode(const uint8_t* at, bool values, T* row, l
 template <typename T, int D>
 __global__ void __launch_bounds__(kThreads) lm_load_q4_kernel(const LoadArgs a)
 {
+    __shared__ uint4 buf[kThreads / 32][Q4Tile<D>::kBytes / 16];
     const int lane = threadIdx.x & 31;
     const bool values = blockIdx.y == 1;
     const uint8_t* cache = values ? a.v_cache : a.k_cache;
@@ -201,7 +238,7 @@ __global__ void __launch_bounds__(kThreads) lm_load_q4_kernel(const LoadArgs a)
         }
         decode<T, D>(cache + (((long long)from * a.hk + h) * tiles + tile) * Q4Tile<D>::kBytes, values,
                      out + ((((long long)to << a.bs_shift) + tile * 16) * a.hk + h) * D + lane % (D / 8) * 8,
-                     (long long)a.hk * D);
+                     (long long)a.hk * D, buf[threadIdx.x >> 5]);
     }
 }
 
@@ -210,6 +247,7 @@ template <int D>
 __global__ void __launch_bounds__(kThreads) lm_halves_q4_kernel(const LmHalvesArgs a, int hq, int hk, int bf16, float scale,
                                                              unsigned* err)
 {
+    __shared__ uint4 buf[kThreads / 32][Q4Tile<D>::kBytes / 16];
     const int lane = threadIdx.x & 31;
     const long long first = (blockIdx.x * (long long)kThreads + threadIdx.x) >> 5, step = gridDim.x * (long long)(kThreads / 32);
     pdl_wait();
@@ -226,7 +264,7 @@ __global__ void __launch_bounds__(kThreads) lm_halves_q4_kernel(const LmHalvesAr
             if (!good && lane == 0) atomicOr(err, CODEC_LM_ERR_BLOCK);
             decode<__half, D>(good ? cache + (((long long)from * hk + h) * tiles + tile) * Q4Tile<D>::kBytes : nullptr, values,
                               out + ((((long long)i << a.bs_shift) + tile * 16) * hk + h) * D + lane % (D / 8) * 8,
-                              (long long)hk * D);
+                              (long long)hk * D, buf[threadIdx.x >> 5]);
         }
         return;
     }
