@@ -8,12 +8,6 @@ namespace {
 
 constexpr int kThreads = 128;
 
-__device__ __forceinline__ void load8(const float* p, float* x)
-{
-    const float4 a = *reinterpret_cast<const float4*>(p), b = *(reinterpret_cast<const float4*>(p) + 1);
-    x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
-    x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
-}
 __device__ __forceinline__ float2 unpack2(uint32_t w, const __half*)
 {
     return __half22float2(*reinterpret_cast<const __half2*>(&w));
@@ -22,29 +16,47 @@ __device__ __forceinline__ float2 unpack2(uint32_t w, const __nv_bfloat16*)
 {
     return __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&w));
 }
-template <typename T>
-__device__ __forceinline__ void load8(const T* p, float* x)
-{
-    const uint4 w = *reinterpret_cast<const uint4*>(p);
-    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-    for (int i = 0; i < 4; i++) {
-        const float2 f = unpack2(u[i], p);
-        x[2 * i] = f.x;
-        x[2 * i + 1] = f.y;
-    }
-}
 
-__device__ __forceinline__ float min_nan(float a, float b)
+// Eight values as they lie in memory, and in fp32.
+template <typename T> struct Raw {
+    uint4 w;
+    __device__ __forceinline__ void load(const T* p) { w = *reinterpret_cast<const uint4*>(p); }
+    __device__ __forceinline__ void get(float* x) const
+    {
+        const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+            const float2 f = unpack2(u[i], static_cast<const T*>(nullptr));
+            x[2 * i] = f.x;
+            x[2 * i + 1] = f.y;
+        }
+    }
+};
+template <> struct Raw<float> {
+    float4 a, b;
+    __device__ __forceinline__ void load(const float* p)
+    {
+        a = *reinterpret_cast<const float4*>(p);
+        b = *(reinterpret_cast<const float4*>(p) + 1);
+    }
+    __device__ __forceinline__ void get(float* x) const
+    {
+        x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
+        x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
+    }
+};
+
+// NaN if one is.
+__device__ __forceinline__ float min_nan(float a, float b, float c)
 {
     float y;
-    asm("min.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
+    asm("min.NaN.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
     return y;
 }
-__device__ __forceinline__ float max_nan(float a, float b)
+__device__ __forceinline__ float max_nan(float a, float b, float c)
 {
     float y;
-    asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
+    asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
     return y;
 }
 
@@ -54,16 +66,12 @@ __device__ __forceinline__ float max_nan(float a, float b)
 // shows in the least and the largest.
 __device__ __forceinline__ uint32_t encode(const float* x, __half& scale, __half& low)
 {
-    float lo = x[0], hi = x[0];
-#pragma unroll
-    for (int i = 1; i < 8; i++) {
-        lo = min_nan(lo, x[i]);
-        hi = max_nan(hi, x[i]);
-    }
+    float lo = min_nan(min_nan(x[0], x[1], x[2]), min_nan(x[3], x[4], x[5]), min_nan(x[6], x[6], x[7]));
+    float hi = max_nan(max_nan(x[0], x[1], x[2]), max_nan(x[3], x[4], x[5]), max_nan(x[6], x[6], x[7]));
 #pragma unroll
     for (int o = 1; o < 4; o <<= 1) {
-        lo = min_nan(lo, __shfl_xor_sync(0xffffffffu, lo, o));
-        hi = max_nan(hi, __shfl_xor_sync(0xffffffffu, hi, o));
+        lo = min_nan(lo, lo, __shfl_xor_sync(0xffffffffu, lo, o));
+        hi = max_nan(hi, hi, __shfl_xor_sync(0xffffffffu, hi, o));
     }
     const bool good = fabsf(lo) < INFINITY && fabsf(hi) < INFINITY;
     lo = fminf(fmaxf(lo, -65504.f), 65504.f);
@@ -75,12 +83,15 @@ __device__ __forceinline__ uint32_t encode(const float* x, __half& scale, __half
     // a number of 0 .. 15 and 1.5 x 2^23 is rounded to a whole one, which then stands in
     // the last bits; what the others' bits add to the word is taken off at the end
     constexpr float kWhole = 12582912.f;
+    const float2 minus = make_float2(-l, -l), by = make_float2(inv, inv), whole = make_float2(kWhole, kWhole);
     uint32_t word = 0, rest = 0;
 #pragma unroll
-    for (int i = 0; i < 8; i++) {
-        const float c = fminf(fmaxf(__fmul_rn(__fsub_rn(x[i], l), inv), 0.f), 15.f);
-        word += __float_as_uint(__fadd_rn(c, kWhole)) << (4 * i);
-        rest += 0x4b400000u << (4 * i);
+    for (int i = 0; i < 8; i += 2) {
+        float2 c = __fmul2_rn(__fadd2_rn(make_float2(x[i], x[i + 1]), minus), by);
+        c = __fadd2_rn(make_float2(fminf(fmaxf(c.x, 0.f), 15.f), fminf(fmaxf(c.y, 0.f), 15.f)), whole);
+        word += __float_as_uint(c.x) << (4 * i);
+        word += __float_as_uint(c.y) << (4 * i + 4);
+        rest += (0x4b400000u << (4 * i)) + (0x4b400000u << (4 * i + 4));
     }
     if (!good) scale = low = __ushort_as_half(0x7fff);
     return good && s > 0.f ? word - rest : 0u;
@@ -120,23 +131,33 @@ __global__ void __launch_bounds__(kThreads) lm_store_q4_kernel(const StoreArgs a
     const int block = slot >> a.bs_shift, pos = slot & ((1 << a.bs_shift) - 1), p = pos & 15;
     const long long head_bytes = (long long)Tile::kBytes << (a.bs_shift - 4);
     uint8_t* base = (values ? a.v_cache : a.k_cache) + (long long)block * a.hk * head_bytes + (pos >> 4) * Tile::kBytes;
-    for (int h0 = part * kHeads; h0 < a.hk; h0 += a.parts * kHeads) {
-        const int h = h0 + lane / kLanes;
-        float x[8];
-        load8(src + (long long)min(h, a.hk - 1) * D, x);
-        __half scale, low;
-        const uint32_t word = encode(x, scale, low);
-        if (h >= a.hk) continue;
-        uint8_t* tile = base + h * head_bytes;
-        if (!values) {
-            *reinterpret_cast<uint32_t*>(tile + Tile::k_word(p, t, g)) = word;
-            if (t == 0) *reinterpret_cast<__half2*>(tile + Tile::k_param(p, g)) = __halves2half2(scale, low);
-        } else {
-            *reinterpret_cast<uint16_t*>(tile + Tile::v_pair(p, 2 * t, g)) = (uint16_t)word;
-            *reinterpret_cast<uint16_t*>(tile + Tile::v_pair(p, 2 * t + 1, g)) = (uint16_t)(word >> 16);
-            if (t == 0) {
-                *reinterpret_cast<__half*>(tile + Tile::v_scale(p, g)) = scale;
-                *reinterpret_cast<__half*>(tile + Tile::v_scale(p, g) + D) = low;
+    // kUnroll sets of heads are loaded before the first is worked on
+    constexpr int kUnroll = sizeof(TI) == 4 ? 2 : 4;
+    const int step = a.parts * kHeads;
+    for (int h0 = part * kHeads; h0 < a.hk; h0 += kUnroll * step) {
+        Raw<TI> raw[kUnroll];
+#pragma unroll
+        for (int u = 0; u < kUnroll; u++) raw[u].load(src + (long long)min(h0 + u * step + lane / kLanes, a.hk - 1) * D);
+#pragma unroll
+        for (int u = 0; u < kUnroll; u++) {
+            const int h = h0 + u * step + lane / kLanes;
+            if (u > 0 && h0 + u * step >= a.hk) break;
+            float x[8];
+            raw[u].get(x);
+            __half scale, low;
+            const uint32_t word = encode(x, scale, low);
+            if (h >= a.hk) continue;
+            uint8_t* tile = base + h * head_bytes;
+            if (!values) {
+                *reinterpret_cast<uint32_t*>(tile + Tile::k_word(p, t, g)) = word;
+                if (t == 0) *reinterpret_cast<__half2*>(tile + Tile::k_param(p, g)) = __halves2half2(scale, low);
+            } else {
+                *reinterpret_cast<uint16_t*>(tile + Tile::v_pair(p, 2 * t, g)) = (uint16_t)word;
+                *reinterpret_cast<uint16_t*>(tile + Tile::v_pair(p, 2 * t + 1, g)) = (uint16_t)(word >> 16);
+                if (t == 0) {
+                    *reinterpret_cast<__half*>(tile + Tile::v_scale(p, g)) = scale;
+                    *reinterpret_cast<__half*>(tile + Tile::v_scale(p, g) + D) = low;
+                }
             }
         }
     }
