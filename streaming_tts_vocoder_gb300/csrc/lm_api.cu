@@ -131,15 +131,22 @@ codec_status codec_lm_create(const codec_lm_config* cfg, codec_lm_t** out)
                                             c.head_dim > (1LL << 29)))
         sp.chunk *= 2;
     sp.max_splits = (int)((positions + sp.chunk - 1) / sp.chunk);
-    // In 4 bits a split is one warp's: of 32 positions, of up to 1,024 as long as full
-    // tables still make eight for every warp that fits the GPU (2,432), and of as many as
-    // leave a full table 128.
+    // In 4 bits a split is one warp's, and 1,824 of them run at once: about as long as
+    // makes one for each from full tables, of 32 positions at least and 256 at most (512
+    // from 4,096 a warp on), at most 64 of a table, and none where the heads alone
+    // occupy three warps an SM and a table makes two.  Requests x positions (16 / 8
+    // heads of 128), us with splits of 32, 64, 128, 256, 512: 1 x 700 9.5, 9.5, 11.0, 14.5,
+    // 22.0; 1 x 9,000 39.7, 22.5, 18.6, 18.1, 23.5; 16 x 3,000 to 3,750 56.6, 39.0, 29.3,
+    // 23.9, 27.2; 64 of 1 to 1,500 (16 / 16 of 64) 24.3, 17.9, 18.5, 17.2, 23.5; 256 of 500
+    // to 4,000 (32 / 8) 457, 306, 216, 172, 155; 64 x 250 21.1, 19.7, 15.1, whole 13.5.
+    const int64_t each = heads * positions / 1824;
     sp.chunk_q4 = 32;
-    while ((sp.chunk_q4 < 1024 && heads * ((positions + 2 * sp.chunk_q4 - 1) / (2 * sp.chunk_q4)) >= 8 * 2432) ||
-           positions > 128LL * sp.chunk_q4 ||
+    while ((sp.chunk_q4 < each && sp.chunk_q4 < (each >= 4096 ? 512 : 256)) || positions > 64LL * sp.chunk_q4 ||
+           // and the partial results of full tables stay within 2 GB
            (sp.chunk_q4 < positions && heads * (c.q_heads / c.kv_heads) * ((positions + sp.chunk_q4 - 1) / sp.chunk_q4) *
                                                c.head_dim > (1LL << 29)))
         sp.chunk_q4 *= 2;
+    if (heads >= 3 * 152 && positions <= 2 * sp.chunk_q4) sp.chunk_q4 *= 2;
     sp.max_splits_q4 = (int)((positions + sp.chunk_q4 - 1) / sp.chunk_q4);
     const size_t most_splits = std::max(sp.max_splits, sp.max_splits_q4);
     // The shared part's splits: by the largest batch, so that the actual one changes no bits.

@@ -19,9 +19,7 @@
 // warp's: it takes units from a counter, keeps a ring of stages of 32 keys in
 // flight across them by bulk copies of its own, and shares nothing with other
 // warps, so there is no barrier but the one that a stage's copies complete.
-// Partial results are joined in order: by the warp that finishes the last unit of
-// a (request, head) where no warp has more than one unit, else by a kernel of its
-// own.  A long part that all requests share is first turned into halves and then
+// Partial results are joined in order by a kernel of its own.  A long part that all requests share is first turned into halves and then
 // the prompt kernel's work, as over a cache of 16 bits.
 #include <algorithm>
 #include <type_traits>
@@ -31,9 +29,6 @@
 #include "lm_q4.cuh"
 #include "tc_ptx.cuh"
 
-#ifndef CT
-#define CT 3
-#endif
 namespace codec {
 
 namespace {
@@ -43,6 +38,7 @@ constexpr int kThreads = 32 * kWarps;
 constexpr int kTiles = 2;                   // of a stage, of keys and as many of values
 constexpr int kKeys = 16 * kTiles;
 constexpr int kMaxStages = 6;
+template <int D, int NT> constexpr int kCtas = D == 128 && NT == 2 ? 2 : 3;    // per SM, what the registers allow
 // A probability of the reference is 2^kLift; the reference follows when a score
 // passes it by more than kSlack (both log2), so that a probability times a scale
 // below 2 stays below 2^15.
@@ -69,7 +65,6 @@ struct Params {
     float* part_lse;
     const float* pre;                   // [n_pre][B][hq][D]
     const float* pre_lse;
-    int* done;                          // [B][hk] finished units; zero between calls
     int* taken;                         // units taken (null: unit = blockIdx, + gridDim, ..); zero between calls
     void* o;
     long long os;
@@ -213,15 +208,15 @@ __device__ __forceinline__ void join_parts(const Params& p, int b, int h, int n_
 }
 
 // A warp per (request, head) whose result is in parts.
-constexpr int kJoinThreads = 256;
+constexpr int kJoinThreads = 128;
 
 template <int D>
-__global__ void __launch_bounds__(kJoinThreads, 4) lm_join_q4_kernel(const __grid_constant__ Params p)
+__global__ void __launch_bounds__(kJoinThreads) lm_join_q4_kernel(const __grid_constant__ Params p)
 {
     pdl_wait();
     pdl_launch();
     if (blockIdx.x == 0 && threadIdx.x == 0) {
-        *p.taken = 0;
+        if (p.taken) *p.taken = 0;
     }
     const long long w = blockIdx.x * (kJoinThreads / 32LL) + (threadIdx.x >> 5);
     const int b = (int)(w / p.sh.hq), h = (int)(w - (long long)b * p.sh.hq);
@@ -230,12 +225,12 @@ __global__ void __launch_bounds__(kJoinThreads, 4) lm_join_q4_kernel(const __gri
     lm_clamp_len(len, (long long)p.table_blocks << p.bs_shift);
     const int n = splits_of(p, len);
     if (n == 1 && p.n_pre == 0) return;         // written by its unit
-    join_parts<D, 4>(p, b, h, n, len == 0, threadIdx.x & 31);
+    join_parts<D, 16>(p, b, h, n, len == 0, threadIdx.x & 31);
 }
 
-// NT: sets of eight columns.  kJoin: partial results are joined here.
-template <int D, int NT, bool kJoin>
-__global__ void __launch_bounds__(kThreads, NT == 1 ? CT : 3) lm_step_q4_kernel(const __grid_constant__ Params p)
+// NT: sets of eight columns.
+template <int D, int NT>
+__global__ void __launch_bounds__(kThreads, kCtas<D, NT>) lm_step_q4_kernel(const __grid_constant__ Params p)
 {
     using Tile = Q4Tile<D>;
     constexpr int G = Tile::G, kAt = NT == 1 ? 2 : 1;       // tiles worked on at once
@@ -669,20 +664,6 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? CT : 3) lm_step_q4_kernel(
                         p.lse[(long long)b * p.sh.hq + head] = lse;
                 }
             }
-        if constexpr (kJoin) {
-            if (alone) continue;
-            __syncwarp();
-            // releases the warp's results (ordered before it by the barrier) and acquires those of the others
-            int was = 0;
-            if (lane == 0 && n.n_splits > 1) {
-                int* count = p.done + (long long)n.b * p.sh.hk + n.hk;
-                asm volatile("atom.acq_rel.gpu.global.add.s32 %0, [%1], 1;" : "=r"(was) : "l"(count) : "memory");
-                if (was == n.n_splits - 1) *count = 0;
-            }
-            was = __shfl_sync(0xffffffffu, was, 0);
-            if (was != n.n_splits - 1) continue;
-            for (int g = 0; g < group; g++) join_parts<D, 4>(p, n.b, n.hk * group + g, n.n_splits, n.empty, lane);
-        }
     }
     // every copy that is out has landed before the CTA can end
     for (int i = done; i < issued; i++) mbar_drain(&full[i % S], (uint32_t)(i / S) & 1u);
@@ -732,7 +713,6 @@ cudaError_t launch(const LmShape& sh, const LmStepArgs& a, cudaStream_t s)
     p.part_lse = a.ws.part_lse;
     p.pre = a.ws.pre;
     p.pre_lse = a.ws.pre_lse;
-    p.done = a.ws.done;
     p.o = a.o;
     p.os = a.os;
     p.lse = a.lse;
@@ -767,15 +747,14 @@ cudaError_t launch(const LmShape& sh, const LmStepArgs& a, cudaStream_t s)
     }
     const bool wide = sh.group > 8;
     int per_sm = 1;
-    fit<D>(p, wide ? 3 : CT, per_sm);
+    fit<D>(p, wide ? kCtas<D, 2> : kCtas<D, 1>, per_sm);
     // a unit per request and head at least, and no more CTAs than the SMs hold at once
     const long long most = (long long)a.B * p.max_splits * sh.hk;
     const unsigned ctas = (unsigned)std::min<long long>(152 * per_sm, (most + kWarps - 1) / kWarps);
-    // joined in this kernel where a warp has one unit at most and needs no other kernel's results
-    const bool join = most <= (long long)ctas * kWarps && p.n_pre == 0, two = !join && (p.n_pre > 0 || p.max_splits > 1);
-    p.taken = two ? a.ws.taken : nullptr;
-    auto kernel = wide ? (join ? lm_step_q4_kernel<D, 2, true> : lm_step_q4_kernel<D, 2, false>)
-                       : (join ? lm_step_q4_kernel<D, 1, true> : lm_step_q4_kernel<D, 1, false>);
+    const bool two = p.n_pre > 0 || p.max_splits > 1;
+    // from the counter where a warp has more than one
+    p.taken = two && most > (long long)ctas * kWarps ? a.ws.taken : nullptr;
+    auto kernel = wide ? lm_step_q4_kernel<D, 2> : lm_step_q4_kernel<D, 1>;
     const cudaError_t e = launch_pdl(kernel, dim3(ctas), dim3(kThreads), smem_bytes<D>(p.stages, a.B), s, p);
     if (e != cudaSuccess || !two) return e;
     return launch_pdl(lm_join_q4_kernel<D>, dim3((unsigned)(((long long)a.B * sh.hq + kJoinThreads / 32 - 1) / (kJoinThreads / 32))),
@@ -785,8 +764,7 @@ cudaError_t launch(const LmShape& sh, const LmStepArgs& a, cudaStream_t s)
 template <int D>
 cudaError_t configure()
 {
-    const void* kernels[] = {(const void*)lm_step_q4_kernel<D, 1, false>, (const void*)lm_step_q4_kernel<D, 1, true>,
-                             (const void*)lm_step_q4_kernel<D, 2, false>, (const void*)lm_step_q4_kernel<D, 2, true>};
+    const void* kernels[] = {(const void*)lm_step_q4_kernel<D, 1>, (const void*)lm_step_q4_kernel<D, 2>};
     for (const void* k : kernels) {
         const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
         if (e != cudaSuccess) return e;
