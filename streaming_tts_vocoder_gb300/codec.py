@@ -705,49 +705,65 @@ class Lm:
         """codec_lm_store_q4: k and v [rows][kv_heads][head_dim] of the object's
         type or float32, rows any distance apart, into slots (int32 [rows]) of
         the caches in 4 bits: uint8 [n_blocks][kv_heads][block_size * head_dim * 5 / 8]."""
-        flat, fused, rows = self._flat, k.dtype, k.shape[0]
+        i32, u8, at, fused, rows, cache = self._i32, self._u8, self._index, k.dtype, k.shape[0], self._q4_shape
         if rows == 0:
             return
         if fused is not self.dtype and fused is not self._f32:
             raise ValueError(f"k must be {self.dtype} or torch.float32")
-        heads = (rows, self._hk, self._d)
+        heads, per = (rows, self._hk, self._d), (rows,)
+        if not (slots.dtype is i32 and slots.shape == per and slots.get_device() == at and slots.is_contiguous()
+                and k_cache.dtype is u8 and k_cache.shape == cache and k_cache.get_device() == at and
+                k_cache.is_contiguous() and v_cache.dtype is u8 and v_cache.shape == cache and
+                v_cache.get_device() == at and v_cache.is_contiguous()):
+            self._say(("slots", slots, i32, per), ("k_cache", k_cache, u8, cache), ("v_cache", v_cache, u8, cache))
         bad = self._store_q4(
             self._h, k.data_ptr(), self._stride("k", k, fused, heads), v.data_ptr(),
-            self._stride("v", v, fused, heads), self._type if fused is self.dtype else 2, rows,
-            flat("slots", slots, self._i32, (rows,)), flat("k_cache", k_cache, self._u8, self._q4_shape),
-            flat("v_cache", v_cache, self._u8, self._q4_shape),
-            self._current(self._index) if stream is None else stream.cuda_stream)
+            self._stride("v", v, fused, heads), self._type if fused is self.dtype else 2, rows, slots.data_ptr(),
+            k_cache.data_ptr(), v_cache.data_ptr(), self._current(at) if stream is None else stream.cuda_stream)
         if bad:
             raise CodecError(bad, "codec_lm_store_q4")
 
     def load_q4(self, k_cache, v_cache, src, dst, k_dst, v_dst, stream=None):
         """codec_lm_load_q4: blocks src (int32 [n]) of the caches in 4 bits to blocks
         dst of k_dst, v_dst [any number][block_size][kv_heads][head_dim]."""
-        flat, i32, n = self._flat, self._i32, src.numel()
+        i32, u8, dtype, at, n, cache = self._i32, self._u8, self.dtype, self._index, src.numel(), self._q4_shape
         if n == 0:
             return
-        shape = (k_dst.shape[0], *self._cache_shape[1:])
+        per, shape = (n,), (k_dst.shape[0], *self._cache_shape[1:])
+        if not (k_cache.dtype is u8 and k_cache.shape == cache and k_cache.get_device() == at and
+                k_cache.is_contiguous() and v_cache.dtype is u8 and v_cache.shape == cache and
+                v_cache.get_device() == at and v_cache.is_contiguous() and src.dtype is i32 and src.shape == per
+                and src.get_device() == at and src.is_contiguous() and dst.dtype is i32 and dst.shape == per and
+                dst.get_device() == at and dst.is_contiguous() and k_dst.dtype is dtype and k_dst.shape == shape
+                and k_dst.get_device() == at and k_dst.is_contiguous() and v_dst.dtype is dtype and v_dst.shape ==
+                shape and v_dst.get_device() == at and v_dst.is_contiguous()):
+            self._say(("k_cache", k_cache, u8, cache), ("v_cache", v_cache, u8, cache), ("src", src, i32, per),
+                      ("dst", dst, i32, per), ("k_dst", k_dst, dtype, shape), ("v_dst", v_dst, dtype, shape))
         bad = self._load_q4(
-            self._h, flat("k_cache", k_cache, self._u8, self._q4_shape),
-            flat("v_cache", v_cache, self._u8, self._q4_shape), flat("src", src, i32, (n,)), flat("dst", dst, i32, (n,)),
-            n, flat("k_dst", k_dst, self.dtype, shape), flat("v_dst", v_dst, self.dtype, shape), shape[0],
-            self._current(self._index) if stream is None else stream.cuda_stream)
+            self._h, k_cache.data_ptr(), v_cache.data_ptr(), src.data_ptr(), dst.data_ptr(), n, k_dst.data_ptr(),
+            v_dst.data_ptr(), shape[0], self._current(at) if stream is None else stream.cuda_stream)
         if bad:
             raise CodecError(bad, "codec_lm_load_q4")
 
     def step_q4(self, q, k_cache, v_cache, tables, kv_len, o, shared_table=None, lse=None, stream=None):
         """codec_lm_step_q4: `step` over the caches in 4 bits."""
-        flat, dtype, i32 = self._flat, self.dtype, self._i32
+        flat, dtype, i32, u8, at, cache = self._flat, self.dtype, self._i32, self._u8, self._index, self._q4_shape
         B = q.shape[0]
         shared = 0 if shared_table is None else shared_table.numel()
-        wide = (B, self._hq, self._d)
+        wide, table, per = (B, self._hq, self._d), (B, self._width), (B,)
+        if not (k_cache.dtype is u8 and k_cache.shape == cache and k_cache.get_device() == at and
+                k_cache.is_contiguous() and v_cache.dtype is u8 and v_cache.shape == cache and
+                v_cache.get_device() == at and v_cache.is_contiguous() and tables.dtype is i32 and tables.shape ==
+                table and tables.get_device() == at and tables.is_contiguous() and kv_len.dtype is i32 and
+                kv_len.shape == per and kv_len.get_device() == at and kv_len.is_contiguous()):
+            self._say(("k_cache", k_cache, u8, cache), ("v_cache", v_cache, u8, cache), ("tables", tables, i32,
+                      table), ("kv_len", kv_len, i32, per))
         bad = self._step_q4(
-            self._h, q.data_ptr(), self._stride("q", q, dtype, wide), B,
-            flat("k_cache", k_cache, self._u8, self._q4_shape), flat("v_cache", v_cache, self._u8, self._q4_shape),
-            flat("tables", tables, i32, (B, self._width)), flat("kv_len", kv_len, i32, (B,)),
-            flat("shared_table", shared_table, i32, (shared,)) if shared else None, shared, o.data_ptr(),
-            self._stride("o", o, dtype, wide), None if lse is None else flat("lse", lse, self._f32, (B, self._hq)),
-            self._current(self._index) if stream is None else stream.cuda_stream)
+            self._h, q.data_ptr(), self._stride("q", q, dtype, wide), B, k_cache.data_ptr(), v_cache.data_ptr(),
+            tables.data_ptr(), kv_len.data_ptr(), flat("shared_table", shared_table, i32, (shared,)) if shared else None,
+            shared, o.data_ptr(), self._stride("o", o, dtype, wide),
+            None if lse is None else flat("lse", lse, self._f32, (B, self._hq)),
+            self._current(at) if stream is None else stream.cuda_stream)
         if bad:
             raise CodecError(bad, "codec_lm_step_q4")
 
@@ -756,8 +772,8 @@ class Lm:
         rows.  logits [rows][vocab] of bfloat16, float16 or float32, rows any
         distance apart; sums, sums_out float32 [rows]; ended, parents, tokens,
         ended_out int32 [rows]; end_token -1: none ends."""
-        flat, i32, f32 = self._flat, self._i32, self._f32
-        if logits.dim() != 2 or logits.dtype not in self._logit_types or logits.get_device() != self._index or (
+        i32, f32, at = self._i32, self._f32, self._index
+        if logits.dim() != 2 or logits.dtype not in self._logit_types or logits.get_device() != at or (
                 logits.shape[1] > 1 and logits.stride(1) != 1):
             raise ValueError(f"logits must be bfloat16, float16 or float32 [rows][vocab] on {self.device}, values of a "
                              f"row back to back, got {logits.dtype} {tuple(logits.shape)}, strides {logits.stride()}")
@@ -765,11 +781,21 @@ class Lm:
         if beams < 1 or rows % beams:
             raise ValueError(f"{rows} rows are not groups of {beams} beams")
         per = (rows,)
+        if not (sums.dtype is f32 and sums.shape == per and sums.get_device() == at and sums.is_contiguous() and
+                ended.dtype is i32 and ended.shape == per and ended.get_device() == at and ended.is_contiguous()
+                and sums_out.dtype is f32 and sums_out.shape == per and sums_out.get_device() == at and
+                sums_out.is_contiguous() and parents.dtype is i32 and parents.shape == per and
+                parents.get_device() == at and parents.is_contiguous() and tokens.dtype is i32 and tokens.shape ==
+                per and tokens.get_device() == at and tokens.is_contiguous() and ended_out.dtype is i32 and
+                ended_out.shape == per and ended_out.get_device() == at and ended_out.is_contiguous()):
+            self._say(("sums", sums, f32, per), ("ended", ended, i32, per), ("sums_out", sums_out, f32, per),
+                      ("parents", parents, i32, per), ("tokens", tokens, i32, per), ("ended_out", ended_out, i32,
+                      per))
         bad = self._beams(
             self._h, logits.data_ptr(), logits.stride(0) if rows > 1 else vocab, self._logit_types[logits.dtype],
-            rows // beams, beams, vocab, flat("sums", sums, f32, per), flat("ended", ended, i32, per), end_token,
-            flat("sums_out", sums_out, f32, per), flat("parents", parents, i32, per), flat("tokens", tokens, i32, per),
-            flat("ended_out", ended_out, i32, per), self._current(self._index) if stream is None else stream.cuda_stream)
+            rows // beams, beams, vocab, sums.data_ptr(), ended.data_ptr(), end_token, sums_out.data_ptr(),
+            parents.data_ptr(), tokens.data_ptr(), ended_out.data_ptr(),
+            self._current(at) if stream is None else stream.cuda_stream)
         if bad:
             raise CodecError(bad, "codec_lm_beams")
 
@@ -779,16 +805,37 @@ class Lm:
         kv_out, status, copy_src, copy_dst [B]; tables, tables_out
         [B][table_blocks]; owners, owners_out, free_list [n_blocks]; copies [1];
         int64 free_in, free_out [2]."""
-        flat, i32, B = self._flat, self._i32, parents.numel()
-        per, wide, ring, two = (B,), (B, self._width), self._ring_shape, (2,)
+        i32, i64, at, B = self._i32, self._i64, self._index, parents.numel()
+        per, wide, ring, two, one = (B,), (B, self._width), self._ring_shape, (2,), (1,)
+        if not (parents.dtype is i32 and parents.shape == per and parents.get_device() == at and
+                parents.is_contiguous() and kv_len.dtype is i32 and kv_len.shape == per and kv_len.get_device() ==
+                at and kv_len.is_contiguous() and tables.dtype is i32 and tables.shape == wide and
+                tables.get_device() == at and tables.is_contiguous() and tables_out.dtype is i32 and
+                tables_out.shape == wide and tables_out.get_device() == at and tables_out.is_contiguous() and
+                owners.dtype is i32 and owners.shape == ring and owners.get_device() == at and
+                owners.is_contiguous() and owners_out.dtype is i32 and owners_out.shape == ring and
+                owners_out.get_device() == at and owners_out.is_contiguous() and free_list.dtype is i32 and
+                free_list.shape == ring and free_list.get_device() == at and free_list.is_contiguous() and
+                free_in.dtype is i64 and free_in.shape == two and free_in.get_device() == at and
+                free_in.is_contiguous() and free_out.dtype is i64 and free_out.shape == two and
+                free_out.get_device() == at and free_out.is_contiguous() and kv_out.dtype is i32 and kv_out.shape
+                == per and kv_out.get_device() == at and kv_out.is_contiguous() and status.dtype is i32 and
+                status.shape == per and status.get_device() == at and status.is_contiguous() and copy_src.dtype is
+                i32 and copy_src.shape == per and copy_src.get_device() == at and copy_src.is_contiguous() and
+                copy_dst.dtype is i32 and copy_dst.shape == per and copy_dst.get_device() == at and
+                copy_dst.is_contiguous() and copies.dtype is i32 and copies.shape == one and copies.get_device()
+                == at and copies.is_contiguous()):
+            self._say(("parents", parents, i32, per), ("kv_len", kv_len, i32, per), ("tables", tables, i32, wide),
+                      ("tables_out", tables_out, i32, wide), ("owners", owners, i32, ring), ("owners_out",
+                      owners_out, i32, ring), ("free_list", free_list, i32, ring), ("free_in", free_in, i64, two),
+                      ("free_out", free_out, i64, two), ("kv_out", kv_out, i32, per), ("status", status, i32, per),
+                      ("copy_src", copy_src, i32, per), ("copy_dst", copy_dst, i32, per), ("copies", copies, i32,
+                      one))
         bad = self._fork(
-            self._h, flat("parents", parents, i32, per), flat("kv_len", kv_len, i32, per), B,
-            flat("tables", tables, i32, wide), flat("tables_out", tables_out, i32, wide), shared_blocks,
-            flat("owners", owners, i32, ring), flat("owners_out", owners_out, i32, ring),
-            flat("free_list", free_list, i32, ring), flat("free_in", free_in, self._i64, two),
-            flat("free_out", free_out, self._i64, two), flat("kv_out", kv_out, i32, per),
-            flat("status", status, i32, per), flat("copy_src", copy_src, i32, per), flat("copy_dst", copy_dst, i32, per),
-            flat("copies", copies, i32, (1,)), self._current(self._index) if stream is None else stream.cuda_stream)
+            self._h, parents.data_ptr(), kv_len.data_ptr(), B, tables.data_ptr(), tables_out.data_ptr(), shared_blocks,
+            owners.data_ptr(), owners_out.data_ptr(), free_list.data_ptr(), free_in.data_ptr(), free_out.data_ptr(),
+            kv_out.data_ptr(), status.data_ptr(), copy_src.data_ptr(), copy_dst.data_ptr(), copies.data_ptr(),
+            self._current(at) if stream is None else stream.cuda_stream)
         if bad:
             raise CodecError(bad, "codec_lm_fork")
 
@@ -796,19 +843,32 @@ class Lm:
                 shared_table=None, shared_out=None, stream=None):
         """codec_lm_compact: blocks in use to the front.  Shapes as for `fork`;
         copy_src, copy_dst int32 [n_blocks // 2]; owners, owners_out or both None."""
-        flat, i32, B = self._flat, self._i32, kv_len.numel()
-        wide, ring, half = (B, self._width), self._ring_shape, (self._ring_shape[0] // 2,)
+        flat, i32, i64, at, B = self._flat, self._i32, self._i64, self._index, kv_len.numel()
+        per, wide, ring, half = (B,), (B, self._width), self._ring_shape, (self._ring_shape[0] // 2,)
+        two, one = (2,), (1,)
         shared = 0 if shared_table is None else shared_table.numel()
+        if not (kv_len.dtype is i32 and kv_len.shape == per and kv_len.get_device() == at and
+                kv_len.is_contiguous() and tables.dtype is i32 and tables.shape == wide and tables.get_device() ==
+                at and tables.is_contiguous() and tables_out.dtype is i32 and tables_out.shape == wide and
+                tables_out.get_device() == at and tables_out.is_contiguous() and free_list.dtype is i32 and
+                free_list.shape == ring and free_list.get_device() == at and free_list.is_contiguous() and
+                free_out.dtype is i64 and free_out.shape == two and free_out.get_device() == at and
+                free_out.is_contiguous() and copy_src.dtype is i32 and copy_src.shape == half and
+                copy_src.get_device() == at and copy_src.is_contiguous() and copy_dst.dtype is i32 and
+                copy_dst.shape == half and copy_dst.get_device() == at and copy_dst.is_contiguous() and
+                copies.dtype is i32 and copies.shape == one and copies.get_device() == at and
+                copies.is_contiguous()):
+            self._say(("kv_len", kv_len, i32, per), ("tables", tables, i32, wide), ("tables_out", tables_out, i32,
+                      wide), ("free_list", free_list, i32, ring), ("free_out", free_out, i64, two), ("copy_src",
+                      copy_src, i32, half), ("copy_dst", copy_dst, i32, half), ("copies", copies, i32, one))
         bad = self._compact(
-            self._h, flat("kv_len", kv_len, i32, (B,)), B, flat("tables", tables, i32, wide),
-            flat("tables_out", tables_out, i32, wide),
+            self._h, kv_len.data_ptr(), B, tables.data_ptr(), tables_out.data_ptr(),
             flat("shared_table", shared_table, i32, (shared,)) if shared else None,
             flat("shared_out", shared_out, i32, (shared,)) if shared else None, shared,
             None if owners is None else flat("owners", owners, i32, ring),
-            None if owners_out is None else flat("owners_out", owners_out, i32, ring),
-            flat("free_list", free_list, i32, ring), flat("free_out", free_out, self._i64, (2,)),
-            flat("copy_src", copy_src, i32, half), flat("copy_dst", copy_dst, i32, half),
-            flat("copies", copies, i32, (1,)), self._current(self._index) if stream is None else stream.cuda_stream)
+            None if owners_out is None else flat("owners_out", owners_out, i32, ring), free_list.data_ptr(),
+            free_out.data_ptr(), copy_src.data_ptr(), copy_dst.data_ptr(), copies.data_ptr(),
+            self._current(at) if stream is None else stream.cuda_stream)
         if bad:
             raise CodecError(bad, "codec_lm_compact")
 
@@ -816,20 +876,17 @@ class Lm:
         """codec_lm_copy: blocks src to blocks dst (int32 [n]; the first copies[0],
         or all) in each of `caches`, contiguous tensors [n_blocks][..] of one
         number of bytes a block."""
-        n, size = src.numel(), 0
-        at = (_P * max(1, len(caches)))()
-        for i, t in enumerate(caches):
-            per = t.numel() // self._ring_shape[0] * t.element_size() if t.dim() > 1 else 0
-            if t.shape[:1] != self._ring_shape or t.get_device() != self._index or not t.is_contiguous() or per != (
-                    size or per) or per == 0:
-                raise ValueError(f"caches must be contiguous tensors [{self._ring_shape[0]}][..] on {self.device} with "
-                                 f"the same bytes a block, got {t.dtype} {tuple(t.shape)}, strides {t.stride()}")
-            size = per
-            at[i] = t.data_ptr()
-        bad = self._copy(self._h, at, len(caches), size, self._flat("src", src, self._i32, (n,)),
-                         self._flat("dst", dst, self._i32, (n,)), n,
+        n, at, (blocks,) = src.numel(), self._index, self._ring_shape
+        size = caches[0].nbytes if caches else 0
+        ptrs = [t.data_ptr() for t in caches if t.nbytes == size and t.shape[0] == blocks and t.get_device() == at
+                and t.is_contiguous()]
+        if len(ptrs) != len(caches):
+            raise ValueError(f"caches must be contiguous tensors [{blocks}][..] on {self.device} with the same bytes a "
+                             f"block, got {[(t.dtype, tuple(t.shape), t.stride()) for t in caches]}")
+        bad = self._copy(self._h, (_P * max(1, len(ptrs)))(*ptrs), len(ptrs), size // blocks,
+                         self._flat("src", src, self._i32, (n,)), self._flat("dst", dst, self._i32, (n,)), n,
                          None if copies is None else self._flat("copies", copies, self._i32, (1,)),
-                         self._current(self._index) if stream is None else stream.cuda_stream)
+                         self._current(at) if stream is None else stream.cuda_stream)
         if bad:
             raise CodecError(bad, "codec_lm_copy")
 

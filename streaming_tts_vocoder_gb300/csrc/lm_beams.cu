@@ -19,9 +19,6 @@
 
 #include "lm.h"
 
-#ifndef RB
-#define RB 8
-#endif
 namespace codec {
 
 namespace {
@@ -152,7 +149,7 @@ __device__ __forceinline__ void add_kept(float& hi, float& lo, float y)
 // Row blockIdx.x, part blockIdx.y of it: windows of chunks, of which a warp takes
 // every kRowWarps-th.
 template <typename T>
-__global__ void __launch_bounds__(kRowThreads, RB) lm_beam_rows_kernel(const LmBeamArgs a)
+__global__ void __launch_bounds__(kRowThreads, 8) lm_beam_rows_kernel(const LmBeamArgs a)
 {
     using V = Vector<T>;
     constexpr int kChunk = kVectors * 32 * V::N;

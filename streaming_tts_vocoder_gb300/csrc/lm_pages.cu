@@ -3,9 +3,9 @@
 //
 // fork and compact are integer work with an order: what is counted for a block
 // has to be complete before blocks are given out or back, and those are listed by
-// ascending id.  One cluster of eight CTAs does each call in one launch, with the
-// cluster's barrier between the phases; sums are the only atomics, so no order
-// shows in a result.
+// ascending id.  One cluster of CTAs does each call in one launch, with the cluster's
+// barrier between the phases; sums are the only atomics, so no order shows in a
+// result.
 #include <climits>
 
 #include "lm.h"
@@ -16,7 +16,6 @@ namespace {
 
 constexpr int kPageThreads = 1024;
 constexpr int kPageCtas = 8;
-constexpr int kAll = kPageThreads * kPageCtas;
 
 __device__ __forceinline__ void cluster_barrier()
 {
@@ -61,15 +60,30 @@ __device__ __forceinline__ int cta_incl(int v, int* sm, int& total)
     return at + sm[w];
 }
 
-// Entries of the tables that are in use, shared among the cluster's warps:
-// f(row, entry) for the count(row) first ones of each.
-template <typename Count, typename F>
-__device__ __forceinline__ void entries(int B, int rank, Count count, F f)
+// Entries of the tables that are in use, shared among the cluster's warps: use(row,
+// entry, load(row, entry)) for the count(row) first ones of each.  A warp loads
+// those of four rows before it uses one (each load alone costs its whole latency).
+template <typename Count, typename Load, typename Use>
+__device__ __forceinline__ void entries(int B, Count count, Load load, Use use)
 {
-    const int w = rank * (kPageThreads / 32) + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-    for (int b = w; b < B; b += kAll / 32) {
-        const int n = count(b);
-        for (int j = lane; j < n; j += 32) f(b, j);
+    constexpr int kRows = 4;
+    const int w = blockIdx.x * (kPageThreads / 32) + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+    const int warps = gridDim.x * (kPageThreads / 32);
+    for (int b0 = w; b0 < B; b0 += kRows * warps) {
+        int n[kRows], most = 0;
+#pragma unroll
+        for (int i = 0; i < kRows; i++) {
+            n[i] = b0 + i * warps < B ? count(b0 + i * warps) : 0;
+            most = max(most, n[i]);
+        }
+        for (int j = lane; j < most; j += 32) {
+            int id[kRows];
+#pragma unroll
+            for (int i = 0; i < kRows; i++) id[i] = j < n[i] ? load(b0 + i * warps, j) : 0;
+#pragma unroll
+            for (int i = 0; i < kRows; i++)
+                if (j < n[i]) use(b0 + i * warps, j, id[i]);
+        }
     }
 }
 
@@ -81,7 +95,7 @@ __device__ __forceinline__ int blocks_of(int n, int shift) { return (int)(((long
 // length, and its copy's place among them; then the running sums'.
 size_t fork_smem(int B) { return (size_t)B * 5 * 4 + 64 * 4; }
 
-__global__ void __cluster_dims__(kPageCtas, 1, 1) __launch_bounds__(kPageThreads) lm_fork_kernel(const LmForkArgs a)
+__global__ void __launch_bounds__(kPageThreads) lm_fork_kernel(const LmForkArgs a)
 {
     extern __shared__ int sm[];
     int* parent = sm;
@@ -91,7 +105,8 @@ __global__ void __cluster_dims__(kPageCtas, 1, 1) __launch_bounds__(kPageThreads
     int* copy = len + a.B;          // -1: it makes none
     int* scan = copy + a.B;
     __shared__ int freed;
-    const int tid = threadIdx.x, rank = blockIdx.x, most = a.table_blocks << a.bs_shift;
+    const int tid = threadIdx.x, rank = blockIdx.x, ctas = gridDim.x, all = ctas * kPageThreads;
+    const int most = a.table_blocks << a.bs_shift;
     pdl_wait();
     pdl_launch();
     const long long head = a.free_in[0], tail = a.free_in[1];
@@ -104,7 +119,7 @@ __global__ void __cluster_dims__(kPageCtas, 1, 1) __launch_bounds__(kPageThreads
     };
 
     // owners after: those before, then the changes
-    for (int i = rank * kPageThreads + tid; i < a.n_blocks; i += kAll) a.owners_out[i] = __ldg(a.owners + i);
+    for (int i = rank * kPageThreads + tid; i < a.n_blocks; i += all) a.owners_out[i] = __ldg(a.owners + i);
 
     // every CTA plans the rows for itself
     for (int b = tid; b < a.B; b += kPageThreads) {
@@ -158,10 +173,10 @@ __global__ void __cluster_dims__(kPageCtas, 1, 1) __launch_bounds__(kPageThreads
     __syncthreads();
 
     // tables of the rows that go on, and their copies
-    entries(a.B, rank, [&](int b) { return parent[b] < 0 ? 0 : blocks_of(len[parent[b]], a.bs_shift); },
-            [&](int b, int j) {
+    entries(a.B, [&](int b) { return parent[b] < 0 ? 0 : blocks_of(len[parent[b]], a.bs_shift); },
+            [&](int b, int j) { return __ldg(a.tables + (long long)parent[b] * a.table_blocks + j); },
+            [&](int b, int j, int id) {
                 const int p = parent[b];
-                int id = __ldg(a.tables + (long long)p * a.table_blocks + j);
                 if (copy[b] >= 0 && j == blocks_of(len[p], a.bs_shift) - 1) {
                     const int fresh = a.free_list[ring(head_at, copy[b])];
                     a.copy_src[copy[b]] = id;
@@ -173,13 +188,13 @@ __global__ void __cluster_dims__(kPageCtas, 1, 1) __launch_bounds__(kPageThreads
     cluster_barrier();              // owners_out holds the numbers before
 
     // a row's blocks have as many holders more as it has children beyond one
-    entries(a.B, rank, [&](int r) { return len[r] <= 0 || children[r] == 1 ? 0 : blocks_of(len[r], a.bs_shift); },
-            [&](int r, int j) {
+    entries(a.B, [&](int r) { return len[r] <= 0 || children[r] == 1 ? 0 : blocks_of(len[r], a.bs_shift); },
+            [&](int r, int j) { return __ldg(a.tables + (long long)r * a.table_blocks + j); },
+            [&](int r, int j, int id) {
                 if (j < a.shared_blocks) return;
                 const bool last = unfilled(r) && j == blocks_of(len[r], a.bs_shift) - 1;
                 const int more = (last ? min(children[r], 1) : children[r]) - 1;
                 if (more == 0) return;
-                const int id = __ldg(a.tables + (long long)r * a.table_blocks + j);
                 if (id < 0 || id >= a.n_blocks) {
                     atomicOr(a.err, CODEC_LM_ERR_BLOCK);
                     return;
@@ -189,7 +204,7 @@ __global__ void __cluster_dims__(kPageCtas, 1, 1) __launch_bounds__(kPageThreads
     cluster_barrier();
 
     // blocks without a holder, in ascending order: the CTAs have consecutive parts
-    const int span = (a.n_blocks + kPageCtas - 1) / kPageCtas;
+    const int span = (a.n_blocks + ctas - 1) / ctas;
     const int lo = (int)min((long long)a.n_blocks, (long long)rank * span), hi = (int)min((long long)a.n_blocks, (long long)lo + span);
     int mine = 0;
     for (int i = lo + tid; i < hi; i += kPageThreads) mine += __ldcg(a.owners_out + i) < 0;
@@ -197,13 +212,13 @@ __global__ void __cluster_dims__(kPageCtas, 1, 1) __launch_bounds__(kPageThreads
     cta_incl(mine, scan, total);
     if (tid == 0) freed = total;
     cluster_barrier();
-    int ahead = 0, all = 0;
-    for (int r = 0; r < kPageCtas; r++) {
+    int ahead = 0, freed_all = 0;
+    for (int r = 0; r < ctas; r++) {
         const int n = theirs(&freed, r);
         if (r < rank) ahead += n;
-        all += n;
+        freed_all += n;
     }
-    const int given = ring_ok ? min(all, a.n_blocks - n_free) : 0;
+    const int given = ring_ok ? min(freed_all, a.n_blocks - n_free) : 0;
     for (int base = lo; base < hi; base += kPageThreads) {
         const int i = base + tid;
         const int n = i < hi ? __ldcg(a.owners_out + i) : 0;
@@ -224,16 +239,16 @@ __global__ void __cluster_dims__(kPageCtas, 1, 1) __launch_bounds__(kPageThreads
 
 // ---- compact ----------------------------------------------------------------
 
-__global__ void __cluster_dims__(kPageCtas, 1, 1) __launch_bounds__(kPageThreads)
+__global__ void __launch_bounds__(kPageThreads)
     lm_compact_kernel(const LmCompactArgs a)
 {
     __shared__ int scan[64];
     __shared__ int counts[3];
-    const int tid = threadIdx.x, rank = blockIdx.x;
+    const int tid = threadIdx.x, rank = blockIdx.x, ctas = gridDim.x, all = ctas * kPageThreads;
     const long long most = (long long)a.table_blocks << a.bs_shift;
     pdl_wait();
     pdl_launch();
-    for (int i = rank * kPageThreads + tid; i < a.n_blocks; i += kAll) a.map[i] = 0;
+    for (int i = rank * kPageThreads + tid; i < a.n_blocks; i += all) a.map[i] = 0;
     cluster_barrier();
     auto held = [&](int b) {
         int n = __ldg(a.len + b);
@@ -247,10 +262,11 @@ __global__ void __cluster_dims__(kPageCtas, 1, 1) __launch_bounds__(kPageThreads
         else
             a.map[id] = 1;
     };
-    entries(a.B, rank, held, [&](int b, int j) {
-        if (j >= a.shared_blocks) mark(__ldg(a.tables + (long long)b * a.table_blocks + j));
-    });
-    for (int j = rank * kPageThreads + tid; j < a.shared_blocks; j += kAll) mark(__ldg(a.shared_table + j));
+    entries(a.B, held, [&](int b, int j) { return __ldg(a.tables + (long long)b * a.table_blocks + j); },
+            [&](int b, int j, int id) {
+                if (j >= a.shared_blocks) mark(id);
+            });
+    for (int j = rank * kPageThreads + tid; j < a.shared_blocks; j += all) mark(__ldg(a.shared_table + j));
     if (rank == 0)
         for (int b = tid; b < a.B; b += kPageThreads) {
             int n = __ldg(a.len + b);
@@ -258,7 +274,7 @@ __global__ void __cluster_dims__(kPageCtas, 1, 1) __launch_bounds__(kPageThreads
         }
     cluster_barrier();
 
-    const int span = (a.n_blocks + kPageCtas - 1) / kPageCtas;
+    const int span = (a.n_blocks + ctas - 1) / ctas;
     const int lo = (int)min((long long)a.n_blocks, (long long)rank * span), hi = (int)min((long long)a.n_blocks, (long long)lo + span);
     int mine = 0, total;
     for (int i = lo + tid; i < hi; i += kPageThreads) mine += __ldcg(a.map + i);
@@ -266,7 +282,7 @@ __global__ void __cluster_dims__(kPageCtas, 1, 1) __launch_bounds__(kPageThreads
     if (tid == 0) counts[0] = total;
     cluster_barrier();
     int used = 0;
-    for (int r = 0; r < kPageCtas; r++) used += theirs(&counts[0], r);
+    for (int r = 0; r < ctas; r++) used += theirs(&counts[0], r);
 
     // of this CTA's ids: those in use that lie behind, those free that lie before
     int away = 0, room = 0;
@@ -284,7 +300,7 @@ __global__ void __cluster_dims__(kPageCtas, 1, 1) __launch_bounds__(kPageThreads
     }
     cluster_barrier();
     int before = 0, before_room = 0, moves = 0;
-    for (int r = 0; r < kPageCtas; r++) {
+    for (int r = 0; r < ctas; r++) {
         const int n = theirs(&counts[1], r);
         if (r < rank) {
             before += n;
@@ -303,7 +319,7 @@ __global__ void __cluster_dims__(kPageCtas, 1, 1) __launch_bounds__(kPageThreads
         if (out) a.copy_src[k] = i;
         if (in) a.copy_dst[m] = i;
     }
-    for (int i = rank * kPageThreads + tid; i < a.n_blocks - used; i += kAll) a.free_list[i] = used + i;
+    for (int i = rank * kPageThreads + tid; i < a.n_blocks - used; i += all) a.free_list[i] = used + i;
     if (rank == 0 && tid == 0) {
         a.copies[0] = moves;
         a.free_out[0] = 0;
@@ -313,25 +329,26 @@ __global__ void __cluster_dims__(kPageCtas, 1, 1) __launch_bounds__(kPageThreads
     // where blocks go: owners (marks below the number in use are not written any
     // more), and map for those that move
     if (a.owners) {
-        for (int i = rank * kPageThreads + tid; i < a.n_blocks; i += kAll) {
+        for (int i = rank * kPageThreads + tid; i < a.n_blocks; i += all) {
             if (i >= used)
                 a.owners_out[i] = 0;
             else if (__ldcg(a.map + i))
                 a.owners_out[i] = __ldg(a.owners + i);
         }
     }
-    for (int k = rank * kPageThreads + tid; k < moves; k += kAll) {
+    for (int k = rank * kPageThreads + tid; k < moves; k += all) {
         const int from = __ldcg(a.copy_src + k), to = __ldcg(a.copy_dst + k);
         a.map[from] = to;
         if (a.owners) a.owners_out[to] = __ldg(a.owners + from);
     }
     cluster_barrier();
     auto moved = [&](int id) { return id >= used && id < a.n_blocks ? __ldcg(a.map + id) : id; };
-    entries(a.B, rank, held, [&](int b, int j) {
-        const long long at = (long long)b * a.table_blocks + j;
-        a.tables_out[at] = moved(__ldg(j < a.shared_blocks ? a.shared_table + j : a.tables + at));
-    });
-    for (int j = rank * kPageThreads + tid; j < a.shared_blocks; j += kAll)
+    entries(a.B, held,
+            [&](int b, int j) {
+                return moved(__ldg(j < a.shared_blocks ? a.shared_table + j : a.tables + (long long)b * a.table_blocks + j));
+            },
+            [&](int b, int j, int id) { a.tables_out[(long long)b * a.table_blocks + j] = id; });
+    for (int j = rank * kPageThreads + tid; j < a.shared_blocks; j += all)
         a.shared_out[j] = moved(__ldg(a.shared_table + j));
 }
 
@@ -378,14 +395,34 @@ cudaError_t configure_lm_pages()
                                 (int)fork_smem(kLmMaxRequests));
 }
 
+// One cluster of `ctas` CTAs.
+template <typename A>
+static cudaError_t launch_cluster(void (*kernel)(const A), int ctas, size_t smem, cudaStream_t s, const A& a)
+{
+    cudaLaunchAttribute at[2];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    at[1].id = cudaLaunchAttributeClusterDimension;
+    at[1].val.clusterDim.x = ctas;
+    at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(ctas);
+    cfg.blockDim = dim3(kPageThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cfg.attrs = at;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, kernel, a);
+}
+
 cudaError_t launch_lm_fork(const LmForkArgs& a, cudaStream_t s)
 {
-    return launch_pdl(lm_fork_kernel, dim3(kPageCtas), dim3(kPageThreads), fork_smem(a.B), s, a);
+    return launch_cluster(lm_fork_kernel, kPageCtas, fork_smem(a.B), s, a);
 }
 
 cudaError_t launch_lm_compact(const LmCompactArgs& a, cudaStream_t s)
 {
-    return launch_pdl(lm_compact_kernel, dim3(kPageCtas), dim3(kPageThreads), 0, s, a);
+    return launch_cluster(lm_compact_kernel, kPageCtas, 0, s, a);
 }
 
 cudaError_t launch_lm_copy(const LmCopyArgs& a, cudaStream_t s)
