@@ -148,7 +148,7 @@ codec_status codec_lm_create(const codec_lm_config* cfg, codec_lm_t** out)
         sp.chunk_q4 *= 2;
     if (heads >= 3 * 152 && positions <= 2 * sp.chunk_q4) sp.chunk_q4 *= 2;
     sp.max_splits_q4 = (int)((positions + sp.chunk_q4 - 1) / sp.chunk_q4);
-    const size_t most_splits = std::max(sp.max_splits, sp.max_splits_q4);
+    const size_t most_splits = std::max(sp.max_splits, sp.max_splits_q4 + 1);
     // The shared part's splits: by the largest batch, so that the actual one changes no bits.
     const int tokens = 2 * (128 / (c.q_heads / c.kv_heads));
     const int64_t pairs = (c.max_requests + tokens - 1) / tokens;

@@ -19,8 +19,9 @@
 // warp's: it takes units from a counter, keeps a ring of stages of 32 keys in
 // flight across them by bulk copies of its own, and shares nothing with other
 // warps, so there is no barrier but the one that a stage's copies complete.
-// Partial results are joined in order by a kernel of its own.  A long part that all requests share is first turned into halves and then
-// the prompt kernel's work, as over a cache of 16 bits.
+// Partial results are joined in order by a kernel of its own.  A part that all requests
+// share is units of its own, whose columns are the heads of several requests; a long one
+// is first turned into halves and then the prompt kernel's work, as over a cache of 16 bits.
 #include <algorithm>
 #include <type_traits>
 
@@ -56,12 +57,14 @@ struct Params {
     int table_blocks, bs_shift, n_blocks;
     const int* lead;                    // blocks of the first lead_len positions of every request
     int lead_len;
-    int shared_len, n_pre;              // part of its own: length, partial results of it
+    int shared_len;                     // positions of them worked on apart from the requests' own
+    int n_pre;                          // partial results of these from another kernel (in pre), or
+    int n_shared, sets;                 // splits of these among the units, and sets of columns
     int chunk, max_splits;
     int stages;
     int after_shared;                   // the shared part's kernel is running: nothing here needs its results
     float c;                            // scale x log2 e
-    float* part;                        // [B][max_splits][hq][D]
+    float* part;                        // [B][max_splits + 1][hq][D], a request's own behind the shared ones
     float* part_lse;
     const float* pre;                   // [n_pre][B][hq][D]
     const float* pre_lse;
@@ -136,46 +139,62 @@ __device__ __forceinline__ void each(F f)
     if constexpr (N == 2) f(std::integral_constant<int, 1>());
 }
 
-struct Unit {
-    int b, hk, split, n_splits;
-    int key0, keys;                 // first position, positions of the split
-    bool empty;                     // the request has no position at all
-};
-
-// The unit of index u: units run over the requests' splits, K/V heads innermost.
-// first, lens: the requests' first units and lengths.  A whole warp: 32 places
-// are looked at at once.
-__device__ __forceinline__ Unit unit_at(const Params& p, const int* first, const int* lens, int u)
+// Splits of the shared part among the units that a request of len positions takes
+// results of.  One that ends inside that part reads its own positions of it, so that
+// what lies behind them never touches it.
+__device__ __forceinline__ int shared_of(const Params& p, int len)
 {
-    Unit n;
-    const int x = u / p.sh.hk;
-    n.hk = u - x * p.sh.hk;
-    const int lane = threadIdx.x & 31;
-    int lo = 0;
-    for (int step = p.B <= 32 ? 1 : p.B <= 1024 ? 32 : 1024; step > 0; step >>= 5) {
-        const int at = lo + lane * step;
-        lo += (__popc(__ballot_sync(0xffffffffu, at < p.B && first[at] <= x)) - 1) * step;
-    }
-    n.b = lo;
-    n.split = x - first[lo];
-    n.n_splits = first[lo + 1] - first[lo];
-    const int len = lens[lo];
-    n.empty = len == 0;
-    n.key0 = p.shared_len + n.split * p.chunk;
-    n.keys = min(max(len - n.key0, 0), p.chunk);
-    return n;
+    return len >= p.shared_len ? p.n_shared : 0;
 }
 
+// Positions before a request's own units, and how many of these it has: one at least.
+__device__ __forceinline__ int start_of(const Params& p, int len)
+{
+    return p.n_shared > 0 && len < p.shared_len ? 0 : p.shared_len;
+}
 __device__ __forceinline__ int splits_of(const Params& p, int len)
 {
-    return max(1, (max(0, len - p.shared_len) + p.chunk - 1) / p.chunk);
+    return max(1, (max(0, len - start_of(p, len)) + p.chunk - 1) / p.chunk);
 }
 
-// The warps' stages, the stages' units and barriers, flags, the requests' first units and lengths.
+// A unit in shared memory: x the request, or the set of columns of all requests with
+// kShared (kEmpty: the request has no position at all; -1: no more units), y the K/V
+// head, z the place of its results among the request's and how many these are << 16,
+// w positions.
+constexpr int kEmpty = 1 << 30, kShared = 1 << 29;
+
+__device__ __forceinline__ int request_of(int4 unit) { return unit.x & (kShared - 1); }
+
+// The unit of index u and its first position: units run over the requests' splits,
+// K/V heads innermost.  first, lens: the requests' first units and lengths.  A whole
+// warp: 32 places are looked at at once.
+__device__ __forceinline__ int4 unit_at(const Params& p, const int* first, const int* lens, int u, int& key0)
+{
+    int x = u / p.sh.hk;
+    const int hk = u - x * p.sh.hk;
+    if (x < p.n_shared * p.sets) {
+        const int split = x / p.sets;
+        key0 = split * p.chunk;
+        return make_int4((x - split * p.sets) | kShared, hk, split | (p.n_shared + 1) << 16, min(p.shared_len - key0, p.chunk));
+    }
+    x -= p.n_shared * p.sets;
+    const int lane = threadIdx.x & 31;
+    int b = 0;
+    for (int step = p.B <= 32 ? 1 : p.B <= 1024 ? 32 : 1024; step > 0; step >>= 5) {
+        const int at = b + lane * step;
+        b += (__popc(__ballot_sync(0xffffffffu, at < p.B && first[at] <= x)) - 1) * step;
+    }
+    const int len = lens[b], split = x - first[b], before = shared_of(p, len);
+    key0 = start_of(p, len) + split * p.chunk;
+    return make_int4(b | (len == 0 ? kEmpty : 0), hk, (before + split) | (before + first[b + 1] - first[b]) << 16,
+                     min(max(len - key0, 0), p.chunk));
+}
+
+// The warps' stages, the stages' units and barriers, a unit of each warp, flags, the requests' first units and lengths.
 template <int D>
 size_t smem_bytes(int stages, int B)
 {
-    return 128 + (size_t)kWarps * stages * (2 * kTiles * Q4Tile<D>::kBytes + 16 + 8) + 16 + (2 * (size_t)B + 1) * 4;
+    return 128 + (size_t)kWarps * stages * (2 * kTiles * Q4Tile<D>::kBytes + 16 + 8) + kWarps * 16 + 16 + (2 * (size_t)B + 1) * 4;
 }
 
 __device__ __forceinline__ void store2(const Params& p, void* row, int i, float a, float b)
@@ -193,7 +212,7 @@ __device__ __forceinline__ void join_parts(const Params& p, int b, int h, int n_
 {
     constexpr int kE = D / 32;
     const int parts = empty ? 0 : p.n_pre + n_splits;
-    const long long shared_row = (long long)b * p.sh.hq + h, own_row = (long long)b * p.max_splits * p.sh.hq + h;
+    const long long shared_row = (long long)b * p.sh.hq + h, own_row = (long long)b * (p.max_splits + 1) * p.sh.hq + h;
     auto row_of = [&](int i) {
         return i < p.n_pre ? (long long)i * p.B * p.sh.hq + shared_row : (long long)(i - p.n_pre) * p.sh.hq + own_row;
     };
@@ -223,7 +242,7 @@ __global__ void __launch_bounds__(kJoinThreads) lm_join_q4_kernel(const __grid_c
     if (b >= p.B) return;
     int len = __ldg(p.kv_len + b);
     lm_clamp_len(len, (long long)p.table_blocks << p.bs_shift);
-    const int n = splits_of(p, len);
+    const int n = shared_of(p, len) + splits_of(p, len);
     if (n == 1 && p.n_pre == 0) return;         // written by its unit
     join_parts<D, 16>(p, b, h, n, len == 0, threadIdx.x & 31);
 }
@@ -240,10 +259,11 @@ __global__ void __launch_bounds__(kThreads, kCtas<D, NT>) lm_step_q4_kernel(cons
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, S = p.stages;
     constexpr uint32_t kStage = 2 * kTiles * kTile;
     uint8_t* ring = smem + (size_t)warp * S * kStage;
-    // the unit whose first keys a stage holds: request (-1: no more), K/V head, split and splits << 16, positions
-    int4* unit_of = reinterpret_cast<int4*>(smem + (size_t)kWarps * S * kStage) + warp * S;
-    uint64_t* full = reinterpret_cast<uint64_t*>(smem + (size_t)kWarps * S * (kStage + 16)) + warp * S;
-    int* flags = reinterpret_cast<int*>(smem + (size_t)kWarps * S * (kStage + 24));  // abort
+    int4* units_of = reinterpret_cast<int4*>(smem + (size_t)kWarps * S * kStage);
+    int4* unit_of = units_of + warp * S;                        // the unit whose first keys a stage holds
+    int4* now = units_of + kWarps * S + warp;                   // the unit that is worked on
+    uint64_t* full = reinterpret_cast<uint64_t*>(units_of + kWarps * (S + 1)) + warp * S;
+    int* flags = reinterpret_cast<int*>(reinterpret_cast<uint64_t*>(units_of + kWarps * (S + 1)) + kWarps * S);  // abort
     uint64_t* never = reinterpret_cast<uint64_t*>(flags + 2);   // nothing arrives (see LmShape::unarrived)
     int* first = flags + 4;
     int* lens = first + p.B + 1;
@@ -290,14 +310,14 @@ __global__ void __launch_bounds__(kThreads, kCtas<D, NT>) lm_step_q4_kernel(cons
         }
         __syncthreads();
     }
-    const int units = first[p.B] * p.sh.hk;
+    const int units = (p.n_shared * p.sets + first[p.B]) * p.sh.hk;
 
     // ---- copies ----
     // Lane i has what stage i of the next 32 of a unit takes, and issues it.
     int from = 0, end = 0, turn = 0, issued = 0;    // positions; the lane whose stage is next
-    long long src[2] = {-1, -1};                // of the two tiles in the cache, bytes; -1: zeros
+    int tile[kTiles] = {-1, -1};                // the two tiles in the cache; -1: zeros
+    int copied = 0;                             // the request, and the K/V head << 16
     bool last_out = false;                      // the stage that says so is out
-    Unit ahead{};
     auto issue = [&](int st) {
         if (last_out) return;
         issued++;
@@ -315,29 +335,27 @@ __global__ void __launch_bounds__(kThreads, kCtas<D, NT>) lm_step_q4_kernel(cons
                 next += gridDim.x * kWarps;
             else if (lane == 0)
                 next = atomicAdd(p.taken, 1);   // needed when this unit's copies are out
-            ahead = unit_at(p, first, lens, u);
-            from = ahead.key0;
-            end = from + ahead.keys;
+            const int4 unit = unit_at(p, first, lens, u, from);
+            end = from + unit.w;
             turn = 32;
-            if (lane == 0)
-                unit_of[st] = make_int4(ahead.b | (ahead.empty ? 1 << 30 : 0), ahead.hk, ahead.split | ahead.n_splits << 16, ahead.keys);
-            if (ahead.keys == 0) {              // takes a stage without copies
+            copied = (unit.x & 0xffff) | unit.y << 16;          // (a set's tables are not looked at)
+            if (lane == 0) unit_of[st] = unit;
+            if (unit.w == 0) {                  // takes a stage without copies
                 if (lane == 0) mbar_arrive(&full[st]);
                 return;
             }
         }
         if (turn == 32) {
             turn = 0;
-            const int* table = p.tables + (long long)ahead.b * p.table_blocks;
+            const int* table = p.tables + (long long)(copied & 0xffff) * p.table_blocks;
 #pragma unroll
             for (int i = 0; i < kTiles; i++) {
                 const int pos = from + lane * kKeys + i * 16, j = pos >> p.bs_shift;
-                src[i] = -1;
+                tile[i] = -1;
                 if (pos < end) {
                     const int id = __ldcg((pos < p.lead_len ? p.lead : table) + j);
                     if (id >= 0 && id < p.n_blocks)
-                        src[i] = ((((long long)id * p.sh.hk + ahead.hk) << (p.bs_shift - 4)) +
-                                  ((pos & ((1 << p.bs_shift) - 1)) >> 4)) * kTile;
+                        tile[i] = ((id * p.sh.hk + (copied >> 16)) << (p.bs_shift - 4)) + ((pos & ((1 << p.bs_shift) - 1)) >> 4);
                     else
                         atomicOr(p.sh.err, CODEC_LM_ERR_BLOCK);
                 }
@@ -348,17 +366,25 @@ __global__ void __launch_bounds__(kThreads, kCtas<D, NT>) lm_step_q4_kernel(cons
             const bool both = end - from > 16, apart = both && p.bs_shift == 4;
             const uint32_t bytes = both && !apart ? 2 * kTile : kTile;
             mbar_expect_tx(&full[st], both ? 4 * kTile : 2 * kTile);
-            bulk_load(dst, src[0] >= 0 ? p.k + src[0] : p.zeros, &full[st], bytes);
-            bulk_load(dst + kTiles * kTile, src[0] >= 0 ? p.v + src[0] : p.zeros, &full[st], bytes);
+            bulk_load(dst, tile[0] >= 0 ? p.k + tile[0] * (long long)kTile : p.zeros, &full[st], bytes);
+            bulk_load(dst + kTiles * kTile, tile[0] >= 0 ? p.v + tile[0] * (long long)kTile : p.zeros, &full[st], bytes);
             if (apart) {
-                bulk_load(dst + kTile, src[1] >= 0 ? p.k + src[1] : p.zeros, &full[st], kTile);
-                bulk_load(dst + (kTiles + 1) * kTile, src[1] >= 0 ? p.v + src[1] : p.zeros, &full[st], kTile);
+                bulk_load(dst + kTile, tile[1] >= 0 ? p.k + tile[1] * (long long)kTile : p.zeros, &full[st], kTile);
+                bulk_load(dst + (kTiles + 1) * kTile, tile[1] >= 0 ? p.v + tile[1] * (long long)kTile : p.zeros, &full[st], kTile);
             }
         }
         turn++;
         from += kKeys;
     };
     for (int i = 0; i < S; i++) issue(i);
+
+    // Request and head of its group of a unit's column c; a head behind the last for one that
+    // nobody reads.
+    auto column = [&](int4 unit, int c) {
+        if (!(unit.x & kShared)) return make_int2(request_of(unit), c);
+        const int j = request_of(unit) * 8 * NT + c, b = j / p.sh.group;
+        return b < p.B && lens[b] >= p.shared_len ? make_int2(b, j - b * p.sh.group) : make_int2(min(b, p.B - 1), p.sh.group);
+    };
 
     // ---- products ----
     const int r = lane >> 2, t = lane & 3;      // row (and + 8) and column pair of a fragment
@@ -379,14 +405,9 @@ __global__ void __launch_bounds__(kThreads, kCtas<D, NT>) lm_step_q4_kernel(cons
             done++;
             break;
         }
-        Unit n;
-        n.b = unit.x & 0xffff;
-        n.hk = unit.y;
-        n.split = unit.z & 0xffff;
-        n.n_splits = unit.z >> 16;
-        n.keys = unit.w;
-        n.empty = unit.x >> 30;
-        const int group = p.sh.group;
+        __syncwarp();
+        if (lane == 0) *now = unit;
+        const int keys = unit.w;
         uint32_t qf[NT][G][4], ql[NT];          // queries and their groups' sums
         float cf[NT][2];                        // of this lane's columns: what makes a score (log2) of an accumulator
         float acc[NT][G][2][4], low[NT][4];
@@ -408,8 +429,9 @@ __global__ void __launch_bounds__(kThreads, kCtas<D, NT>) lm_step_q4_kernel(cons
         // power of two.  Columns behind the last repeat it: nobody reads them.
 #pragma unroll
         for (int x = 0; x < NT; x++) {
-            const uint16_t* row = static_cast<const uint16_t*>(p.q) + n.b * p.qs +
-                                  ((long long)n.hk * group + min(8 * x + r, group - 1)) * D + t * 8;
+            const int2 col = column(unit, 8 * x + r);
+            const uint16_t* row = static_cast<const uint16_t*>(p.q) + col.x * p.qs +
+                                  ((long long)unit.y * p.sh.group + min(col.y, p.sh.group - 1)) * D + t * 8;
             uint4 w[G];
 #pragma unroll
             for (int g = 0; g < G; g++) w[g] = __ldcg(reinterpret_cast<const uint4*>(row + g * 32));
@@ -456,17 +478,17 @@ __global__ void __launch_bounds__(kThreads, kCtas<D, NT>) lm_step_q4_kernel(cons
         }
         int grown = 0;                          // scales are below 2^(1 + grown)
 #pragma unroll 1
-        for (int at = 0; at == 0 || at < n.keys; at += kKeys) {
+        for (int at = 0; at == 0 || at < keys; at += kKeys) {
             if (at > 0) {
                 // (unarrived: one warp's second stage of a unit of more than 64 positions never comes)
-                gave_up = !__all_sync(0xffffffffu, p.sh.unarrived && warp == 0 && n.keys > 64
+                gave_up = !__all_sync(0xffffffffu, p.sh.unarrived && warp == 0 && keys > 64
                                                        ? mbar_wait(never, 0, abort_flag, p.sh.unarrived)
                                                        : mbar_wait(&full[st], ph, abort_flag, kLmPolls));
                 if (gave_up) break;
             }
-            if (n.keys > 0) {
+            if (keys > 0) {
 #pragma unroll 1
-                for (int w = 0; w < kTiles && at + 16 * w < n.keys; w += kAt) {
+                for (int w = 0; w < kTiles && at + 16 * w < keys; w += kAt) {
                     const int here = at + 16 * w;
                     const uint32_t kt = base + (uint32_t)st * kStage + w * kTile;
                     float s[kAt][NT][4];
@@ -515,11 +537,11 @@ __global__ void __launch_bounds__(kThreads, kCtas<D, NT>) lm_step_q4_kernel(cons
                         lds<2, kP + D>(kt + vl_at, vl[i]);
                         if (r >= G) vl[i][0] = vl[i][1] = 0u;
                     });
-                    if (here + 16 * kAt > n.keys) {
+                    if (here + 16 * kAt > keys) {
                         // what lies behind the last key may be anything
 #pragma unroll
                         for (int i = 0; i < kAt; i++) {
-                            const int left = n.keys - here - 16 * i;
+                            const int left = keys - here - 16 * i;
 #pragma unroll
                             for (int x = 0; x < NT; x++)
 #pragma unroll
@@ -630,7 +652,8 @@ __global__ void __launch_bounds__(kThreads, kCtas<D, NT>) lm_step_q4_kernel(cons
         if (gave_up) break;
         // Results: sums of codes are 2^-24 of what they stand for, and 2^-20 for a
         // group's elements 1 and 3 of four; this lane has elements 4 r .. of each group.
-        const bool alone = n.n_splits == 1 && p.n_pre == 0;
+        const int4 was = *now;
+        const bool alone = was.z >> 16 == 1 && p.n_pre == 0;
 #pragma unroll
         for (int x = 0; x < NT; x++)
 #pragma unroll
@@ -639,10 +662,11 @@ __global__ void __launch_bounds__(kThreads, kCtas<D, NT>) lm_step_q4_kernel(cons
                 sum += __shfl_xor_sync(0xffffffffu, sum, 4);
                 sum += __shfl_xor_sync(0xffffffffu, sum, 8);
                 sum += __shfl_xor_sync(0xffffffffu, sum, 16);
-                const int col = 8 * x + c0 + h, b = n.b, head = n.hk * group + col;
-                const bool there = col < group, none = n.keys == 0;
+                const int2 col = column(was, 8 * x + c0 + h);
+                const int b = col.x, head = was.y * p.sh.group + col.y;
+                const bool there = col.y < p.sh.group, none = keys == 0;
                 const float inv = none ? 0.f : 1.f / sum, lse = none ? -INFINITY : (log2f(sum) - bias[x][h]) * 0.6931471805599453f;
-                const long long at = ((long long)b * p.max_splits + n.split) * p.sh.hq + head;
+                const long long at = ((long long)b * (p.max_splits + 1) + (was.z & 0xffff)) * p.sh.hq + head;
 #pragma unroll
                 for (int g = 0; g < G; g++) {
                     const float add = __shfl_sync(0xffffffffu, low[x][h], g * 4 + t);
@@ -718,12 +742,24 @@ cudaError_t launch(const LmShape& sh, const LmStepArgs& a, cudaStream_t s)
     p.lse = a.lse;
     p.lead = a.shared_table;
     p.lead_len = p.shared_len;
-    // A long shared part is worked on for all requests at once, as for 16 bits; what of
-    // it does not fit the workspace, and a short one, is read by every request.
-    const long long most_short = p.shared_len <= 256 ? 65536 : p.shared_len <= 1024 ? 32768 : 0;
-    if (a.ws.heads == sh.hk || a.ws.heads * p.shared_len <= most_short) p.shared_len = 0;
-    p.shared_len = std::min(p.shared_len, a.ws.shared_q4);
-    if (p.shared_len > 0) {
+    // The shared part, by its length and the largest batch, so that the actual one changes
+    // no bits.  Up to 64 positions every request reads it in front of its own (32 before
+    // 64 x 16 heads of 64: 18.7 us, as units 23.4, by the prompt kernel 30.4; 128: 27.5,
+    // 24.0, 30.9).  Up to 16,384 tiles of 16 keys x 8 columns (16 in groups beyond 8) it is
+    // units of this kernel, whose columns are the heads of eight requests and more (64 of
+    // 500 to 4,000 behind 1,024, 32 / 8 of 128, 16,384 tiles: 65.5, 55.7, 62.4 us; 256 of
+    // 1 to 500 behind 256, as many: 53.3, 44.8, 49.5).  Beyond, it is turned into halves
+    // and the prompt kernel's (behind 4,096, 64 x 16 heads, 32,768 tiles: 113, 39.4, 36.7;
+    // 256 behind 8,192: 484, 269, 82.4); what of it does not fit the workspace every
+    // request reads.
+    const int wide = sh.group > 8 ? 2 : 1;
+    const long long tiles = a.ws.heads * sh.group / (8 * wide) * (p.shared_len / 16);
+    if (a.ws.heads == sh.hk || p.shared_len <= 64) p.shared_len = 0;
+    if (p.shared_len > 0 && tiles <= 16384) {
+        p.n_shared = (p.shared_len + p.chunk - 1) / p.chunk;
+        p.sets = (a.B * sh.group + 8 * wide - 1) / (8 * wide);
+    } else if (p.shared_len > 0) {
+        p.shared_len = std::min(p.shared_len, a.ws.shared_q4);
         const int blocks = p.shared_len >> ks.bs_shift;
         const LmHalvesArgs h{ks.k, ks.v, a.shared_table, blocks, ks.bs_shift, ks.n_blocks, a.q, a.qs, a.B, a.ws.k16, a.ws.v16,
                              a.ws.q16, a.ws.row_c};
@@ -745,16 +781,15 @@ cudaError_t launch(const LmShape& sh, const LmStepArgs& a, cudaStream_t s)
         e = launch_lm_shared(halves, c, s);
         if (e != cudaSuccess) return e;
     }
-    const bool wide = sh.group > 8;
     int per_sm = 1;
-    fit<D>(p, wide ? kCtas<D, 2> : kCtas<D, 1>, per_sm);
+    fit<D>(p, wide == 2 ? kCtas<D, 2> : kCtas<D, 1>, per_sm);
     // a unit per request and head at least, and no more CTAs than the SMs hold at once
-    const long long most = (long long)a.B * p.max_splits * sh.hk;
+    const long long most = ((long long)a.B * p.max_splits + (long long)p.n_shared * p.sets) * sh.hk;
     const unsigned ctas = (unsigned)std::min<long long>(152 * per_sm, (most + kWarps - 1) / kWarps);
-    const bool two = p.n_pre > 0 || p.max_splits > 1;
+    const bool two = p.n_pre + p.n_shared > 0 || p.max_splits > 1;
     // from the counter where a warp has more than one
     p.taken = two && most > (long long)ctas * kWarps ? a.ws.taken : nullptr;
-    auto kernel = wide ? lm_step_q4_kernel<D, 2> : lm_step_q4_kernel<D, 1>;
+    auto kernel = wide == 2 ? lm_step_q4_kernel<D, 2> : lm_step_q4_kernel<D, 1>;
     const cudaError_t e = launch_pdl(kernel, dim3(ctas), dim3(kThreads), smem_bytes<D>(p.stages, a.B), s, p);
     if (e != cudaSuccess || !two) return e;
     return launch_pdl(lm_join_q4_kernel<D>, dim3((unsigned)(((long long)a.B * sh.hq + kJoinThreads / 32 - 1) / (kJoinThreads / 32))),

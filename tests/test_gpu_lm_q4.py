@@ -144,17 +144,18 @@ def cache_q4(seed, lens, hk, d, bs, sh=0, v_mul=1.0):
     return kc, vc, tables, shared, n_blocks, width
 
 
-def as_halves(most, hk, shared_len):
+def as_halves(most, hq, hk, shared_len):
     """Positions of the shared part that the batch has in common as halves: none
-    where every request reads it itself (a short one, or an object for one request)."""
-    short = 65536 if shared_len <= 256 else 32768 if shared_len <= 1024 else 0
-    return 0 if most == 1 or most * hk * shared_len <= short else min(shared_len, 32768)
+    where it is units of the step's own kernel (by tiles of 16 keys x 8 or 16
+    columns of an object for `most` requests) or read by every request."""
+    wide = 16 if hq // hk > 8 else 8
+    return 0 if most == 1 or most * hq // wide * (shared_len // 16) <= 16384 else min(shared_len, 32768)
 
 
 def step_reference(q, kc, vc, tables, lens, shared, hk, d, bs, scale=None, most=1):
     sh = len(shared)
     parts = [Q.values(c.cpu().numpy(), bs, d, keys, parts=True) for c, keys in ((kc, True), (vc, False))]
-    halves = as_halves(most, hk, sh * bs)
+    halves = as_halves(most, q.shape[1], hk, sh * bs)
 
     def keys_of(b):
         n = lens[b]
@@ -198,6 +199,11 @@ def test_step(hq, hk, d, bs):
     check_step([1, 0, 17, 128, 129, 260], 0, hq, hk, d, dt, bs)
     # behind a shared part: nothing, one, several blocks; shorter than the shared part; idle
     check_step([2 * bs, 2 * bs + 1, 2 * bs + 70, 0, bs + 3, 1], 2, hq, hk, d, dt, bs, seed=1)
+    # the same behind more of it, for a few and for many requests
+    lens = [11 * bs, 11 * bs + 1, 11 * bs + 70, 0, 11 * bs - 1, bs + 3, 1]
+    check_step(lens, 11, hq, hk, d, dt, bs, seed=2)
+    assert as_halves(4096, hq, hk, 11 * bs)
+    check_step(lens, 11, hq, hk, d, dt, bs, seed=3, most=4096)
 
 
 @pytest.mark.parametrize("n", [1, 2, 15, 16, 17, 31, 33, 63, 64, 65, 127, 255, 257, 500])
@@ -404,17 +410,18 @@ def test_step_graph_follows_the_lengths():
         assert not o.isnan().any()
 
 
-def test_step_waits_are_bounded():
+@pytest.mark.parametrize("most,sh", [(256, 0), (256, 40), (2048, 40)])
+def test_step_waits_are_bounded(most, sh):
     """With one warp waiting for nothing the call stops, reports it, and is right again."""
-    lens, sh = [900, 300, 1500, 1200], 40
-    lm, q, kc, vc, own, shared, o = check_step(lens, sh, 8, 2, 128, "bf16", 16, seed=11)
+    lens = [900, 300, 1500, 1200]
+    lm, q, kc, vc, own, shared, o = check_step(lens, sh, 8, 2, 128, "bf16", 16, seed=11, most=most)
     lm.set_unarrived_wait(2000)
     lm.step_q4(q, kc, vc, i32(own), i32(lens), torch.zeros(o.shape, dtype=o.dtype, device="cuda"),
-               shared_table=i32(shared))
-    assert lm.errors() in (0, C.LM_ERR_TIMEOUT)
+               shared_table=i32(shared) if sh else None)
+    assert lm.errors() == C.LM_ERR_TIMEOUT
     lm.set_unarrived_wait(0)
     o2 = torch.zeros(o.shape, dtype=o.dtype, device="cuda")
-    lm.step_q4(q, kc, vc, i32(own), i32(lens), o2, shared_table=i32(shared))
+    lm.step_q4(q, kc, vc, i32(own), i32(lens), o2, shared_table=i32(shared) if sh else None)
     assert lm.errors() == 0 and torch.equal(o2, o)
 
 
