@@ -704,7 +704,7 @@ CODEC_API codec_status codec_lm_errors(codec_lm_t* lm, uint32_t* bits, int32_t c
  * codec_lm_errors has cleared it the next calls are right again.  This verifies
  * that path: with polls != 0, in the calls made from here on one warp of each CTA
  * waits that many polls (2^20 at most) for a barrier that no role arrives on
- * (codec_lm_step: in units of more than 64 positions), so the kernels give up on
+ * (codec_lm_step, codec_lm_step_q4: in units of more than 64 positions), so the kernels give up on
  * any input and the outputs are not valid.  0: off.  Captured graphs keep what they were
  * captured with.  Errors: CODEC_ERR_NULL. */
 CODEC_API codec_status codec_lm_set_unarrived_wait(codec_lm_t* lm, uint32_t polls);
@@ -868,8 +868,14 @@ CODEC_API codec_status codec_lm_load_q4(codec_lm_t* lm, const void* k_cache, con
                                         void* stream);
 
 /* codec_lm_step over the cache in 4 bits.  Queries and outputs are of the
- * object's type; scores, sums and the codes' products are fp32, probabilities
- * (with a value group's scale) fp16.  Errors as codec_lm_step. */
+ * object's type.  Scores, their maxima and all sums are fp32; queries enter the
+ * products as fp16 times a power of two of each head's own, probabilities (times a
+ * value group's scale) as fp16.  Up to 64 positions of a shared part are read by
+ * every request; a long one (by max_requests, the heads and its length: from about
+ * 16,384 tiles of 16 keys and 8 query heads) is turned into fp16 keys and values
+ * first, in a workspace of at most 32,768 positions of one layer, and what is
+ * behind these is read by every request.  A group that stands for NaN makes what
+ * it takes part in NaN.  Errors as codec_lm_step. */
 CODEC_API codec_status codec_lm_step_q4(codec_lm_t* lm, const void* q, int64_t q_stride, int32_t B,
                                         const void* k_cache, const void* v_cache, const int32_t* tables,
                                         const int32_t* kv_len, const int32_t* shared_table, int32_t shared_blocks,
@@ -889,11 +895,11 @@ CODEC_API codec_status codec_lm_step_q4(codec_lm_t* lm, const void* q, int64_t q
  *              sum -inf, parent -1, token -1, ended 1.
  * -inf is a logit like others; a beam whose sum is not finite, or whose logits
  * hold a NaN, +inf or nothing but -inf, offers nothing, and neither does a
- * candidate of -inf.  Outputs are not inputs.
+ * candidate of -inf.
  * Errors: CODEC_ERR_NULL, CODEC_ERR_ARG (groups < 1, beams outside [1, 32], vocab
  * outside [2, 2^24], stride < vocab or above 2^32, in_type none of the three, logits not on
- * its size, end_token outside [-1, vocab); -1: none ends), CODEC_ERR_CAPACITY (rows
- * above max_requests), CODEC_ERR_CUDA.
+ * its size, end_token outside [-1, vocab); -1: none ends; an output that is another of the
+ * arrays), CODEC_ERR_CAPACITY (rows above max_requests), CODEC_ERR_CUDA.
  */
 CODEC_API codec_status codec_lm_beams(codec_lm_t* lm, const void* logits, int64_t stride, int32_t in_type,
                                       int32_t groups, int32_t beams, int32_t vocab, const float* sums,
@@ -927,7 +933,7 @@ CODEC_API codec_status codec_lm_beams(codec_lm_t* lm, const void* logits, int64_
  * shrink, and end by codec_lm_fork.  All arrays device memory; no array is another.
  * A repeated call with the same inputs writes the same outputs.
  * Errors: CODEC_ERR_NULL, CODEC_ERR_ARG (B < 1, shared_blocks outside [0, table_blocks],
- * an output that is an input), CODEC_ERR_CAPACITY, CODEC_ERR_CUDA.
+ * an output that is another of the arrays), CODEC_ERR_CAPACITY, CODEC_ERR_CUDA.
  */
 CODEC_API codec_status codec_lm_fork(codec_lm_t* lm, const int32_t* parents, const int32_t* len, int32_t B,
                                      const int32_t* tables, int32_t* tables_out, int32_t shared_blocks,

@@ -134,10 +134,10 @@ struct LmStepSpace {
     int max_splits;                 // splits of a full table
     int shared_ctas;                // of each split of the shared part, with max_requests
     long long heads;                // max_requests x kv_heads
-    float *part, *part_lse;         // [max_requests][max_splits][hq][D], [..][hq]
+    float *part, *part_lse;         // [max_requests][max_splits][hq][D], [..][hq]; in 4 bits max_splits_q4 + 1
     float *pre, *pre_lse;           // [pre_max][max_requests][hq][D], [..][hq]
     int* done;                      // [max_requests][hk], zero between calls
-    int* taken;                     // the same (behind done), of own and of shared parts in 4 bits
+    int* taken;                     // the same (behind done)
     int chunk_q4, max_splits_q4;    // chunk and max_splits over the cache in 4 bits
     unsigned char* zeros;           // two tiles of 16 positions in 4 bits that stand for zero
     // A shared part in 4 bits, as halves: at most shared_q4 positions [shared_q4][hk][D],

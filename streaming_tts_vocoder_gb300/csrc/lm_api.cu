@@ -1,6 +1,7 @@
 // The codec LM's attention operators: object, argument checks, launches.
 #include <algorithm>
 #include <cmath>
+#include <initializer_list>
 #include <new>
 
 #include "lm.h"
@@ -64,6 +65,17 @@ void lm_free(codec_lm_s* lm)
     cudaFree(lm->beam.best);
     cudaFree(lm->block_map);
     delete lm;
+}
+
+// Each output an array of its own.
+bool apart(std::initializer_list<const void*> outputs, std::initializer_list<const void*> inputs)
+{
+    for (const void* const* o = outputs.begin(); o != outputs.end(); o++) {
+        if (!*o) continue;
+        if (std::find(o + 1, outputs.end(), *o) != outputs.end()) return false;
+        if (std::find(inputs.begin(), inputs.end(), *o) != inputs.end()) return false;
+    }
+    return true;
 }
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
@@ -180,7 +192,7 @@ codec_status codec_lm_create(const codec_lm_config* cfg, codec_lm_t** out)
         cudaMalloc(&sp.q16, 2 * row * c.head_dim) != cudaSuccess ||
         cudaMalloc(&sp.row_c, sizeof(float) * row) != cudaSuccess ||
         cudaMalloc(&sp.count, sizeof(int) * (sp.shared_q4 / c.block_size)) != cudaSuccess ||
-        cudaMalloc(&sp.done, sizeof(int) * ((size_t)c.max_requests * c.kv_heads + 2)) != cudaSuccess) {
+        cudaMalloc(&sp.done, sizeof(int) * ((size_t)c.max_requests * c.kv_heads + 1)) != cudaSuccess) {
         cudaGetLastError();
         lm_free(lm);
         return CODEC_ERR_OOM;
@@ -188,8 +200,9 @@ codec_status codec_lm_create(const codec_lm_config* cfg, codec_lm_t** out)
     sp.taken = sp.done + (size_t)c.max_requests * c.kv_heads;
     lm->shape = LmShape{c.type, c.q_heads, c.kv_heads, c.q_heads / c.kv_heads, c.head_dim, c.scale, lm->err, 0};
     if (configure_lm_plan() != cudaSuccess || configure_lm_prompt() != cudaSuccess ||
-        configure_lm_step() != cudaSuccess || configure_lm_step_q4() != cudaSuccess || configure_lm_pages() != cudaSuccess || configure_lm_beams() != cudaSuccess ||
-        cudaMemset(sp.done, 0, sizeof(int) * ((size_t)c.max_requests * c.kv_heads + 2)) != cudaSuccess ||
+        configure_lm_step() != cudaSuccess || configure_lm_step_q4() != cudaSuccess ||
+        configure_lm_pages() != cudaSuccess || configure_lm_beams() != cudaSuccess ||
+        cudaMemset(sp.done, 0, sizeof(int) * ((size_t)c.max_requests * c.kv_heads + 1)) != cudaSuccess ||
         cudaMemset(sp.zeros, 0, kLmZeroBytes) != cudaSuccess ||
         launch_lm_count(sp.count, sp.shared_q4 / c.block_size, nullptr) != cudaSuccess ||
         cudaMemset(lm->err, 0, sizeof(unsigned)) != cudaSuccess ||
@@ -218,7 +231,7 @@ codec_status codec_lm_errors(codec_lm_t* lm, uint32_t* bits, int32_t clear, void
     if (!on.ok || cudaMemcpyAsync(bits, lm->err, sizeof(uint32_t), cudaMemcpyDeviceToHost, cs) != cudaSuccess ||
         (clear && (cudaMemsetAsync(lm->err, 0, sizeof(uint32_t), cs) != cudaSuccess ||
                    // a call that gave up may have left its counts of finished units
-                   cudaMemsetAsync(lm->step.done, 0, sizeof(int) * ((size_t)lm->cfg.max_requests * lm->cfg.kv_heads + 2),
+                   cudaMemsetAsync(lm->step.done, 0, sizeof(int) * ((size_t)lm->cfg.max_requests * lm->cfg.kv_heads + 1),
                                    cs) != cudaSuccess)) ||
         cudaStreamSynchronize(cs) != cudaSuccess)
         return CODEC_ERR_CUDA;
@@ -410,7 +423,7 @@ codec_status codec_lm_beams(codec_lm_t* lm, const void* logits, int64_t stride, 
     const uintptr_t size = in_type == CODEC_LM_FP32 ? 4 : 2;
     if (!typed || groups < 1 || beams < 1 || beams > kLmMaxBeams || vocab < 2 || vocab > (1 << 24) || stride < vocab ||
         stride > (1LL << 32) || reinterpret_cast<uintptr_t>(logits) % size || end_token < -1 || end_token >= vocab ||
-        sums_out == sums || ended_out == ended || parents == ended || tokens == ended)
+        !apart({sums_out, parents, tokens, ended_out}, {logits, sums, ended}))
         return CODEC_ERR_ARG;
     if ((int64_t)groups * beams > c.max_requests) return CODEC_ERR_CAPACITY;
     OnDevice on(lm->device);
@@ -430,8 +443,9 @@ codec_status codec_lm_fork(codec_lm_t* lm, const int32_t* parents, const int32_t
         !free_out || !kv_len || !status || !copy_src || !copy_dst || !copies)
         return CODEC_ERR_NULL;
     const codec_lm_config& c = lm->cfg;
-    if (B < 1 || shared_blocks < 0 || shared_blocks > c.table_blocks || tables == tables_out || owners == owners_out ||
-        free_in == free_out || kv_len == len || kv_len == parents || status == len || status == parents)
+    if (B < 1 || shared_blocks < 0 || shared_blocks > c.table_blocks ||
+        !apart({tables_out, owners_out, free_list, free_out, kv_len, status, copy_src, copy_dst, copies},
+               {parents, len, tables, owners, free_in}))
         return CODEC_ERR_ARG;
     if (B > c.max_requests) return CODEC_ERR_CAPACITY;
     OnDevice on(lm->device);
@@ -451,8 +465,9 @@ codec_status codec_lm_compact(codec_lm_t* lm, const int32_t* len, int32_t B, con
         !free_out || (lm->cfg.n_blocks > 1 && (!copy_src || !copy_dst)) || !copies || !owners != !owners_out)
         return CODEC_ERR_NULL;
     const codec_lm_config& c = lm->cfg;
-    if (B < 1 || shared_blocks < 0 || shared_blocks > c.table_blocks || tables == tables_out ||
-        (owners && owners == owners_out) || (shared_blocks > 0 && shared_table == shared_out))
+    if (B < 1 || shared_blocks < 0 || shared_blocks > c.table_blocks ||
+        !apart({tables_out, shared_out, owners_out, free_list, free_out, copy_src, copy_dst, copies},
+               {len, tables, shared_table, owners}))
         return CODEC_ERR_ARG;
     if (B > c.max_requests) return CODEC_ERR_CAPACITY;
     OnDevice on(lm->device);

@@ -259,13 +259,33 @@ def test_step_queries_of_any_size():
     zero = torch.zeros_like(q)
     lm.step_q4(zero, kc, vc, i32(tables), i32(lens), outs[0])      # every key alike
     Q.assert_step(outs[0], None, step_reference(zero, kc, vc, tables, lens, [], hk, d, bs), "bf16", d, 6.0)
+    # the same behind a shared part, as units and as halves
+    lens = [500, 420]
+    kc, vc, tables, shared, n_blocks, width = cache_q4(6, lens, hk, d, bs, 25)
+    for most in (2, 4096):
+        outs = []
+        for e in (-60, 0, 60):
+            lm = C.Lm(hq, hk, d, "bf16", block_size=bs, n_blocks=n_blocks, table_blocks=width, max_requests=most,
+                      max_rows=2, scale=0.125 * 2.0 ** -e)
+            outs.append(torch.zeros_like(q))
+            lm.step_q4(q * 2.0 ** e, kc, vc, i32(tables), i32(lens), outs[-1], shared_table=i32(shared))
+        assert torch.equal(outs[0], outs[1]) and torch.equal(outs[2], outs[1])
+        # a query that is not finite stays its own row's and head's
+        for what in (NAN, INF, -INF):
+            bad, o = q.clone(), torch.zeros_like(q)
+            bad[1, 4, 9] = what
+            lm.step_q4((bad * 2.0 ** 60), kc, vc, i32(tables), i32(lens), o, shared_table=i32(shared))
+            rest = torch.ones(2, hq, dtype=torch.bool, device="cuda")
+            rest[1, 4] = False
+            assert torch.equal(o[rest], outs[1][rest]) and o[1, 4].isnan().all() and lm.errors() == 0
 
 
 def test_step_result_does_not_depend_on_the_batch():
-    for hq, hk, d, dt, sh, mul in ((8, 2, 128, "bf16", 2, 1.0), (8, 2, 128, "bf16", 66, 8.0), (4, 4, 64, "fp16", 66, 8.0),
-                                   (16, 1, 64, "fp16", 66, 4.0)):
+    for hq, hk, d, dt, sh, mul, most in (
+            (8, 2, 128, "bf16", 2, 1.0, None), (8, 2, 128, "bf16", 66, 8.0, None), (4, 4, 64, "fp16", 66, 8.0, None),
+            (16, 1, 64, "fp16", 66, 4.0, None), (8, 2, 128, "bf16", 66, 8.0, 1024), (16, 1, 64, "fp16", 66, 4.0, 1024)):
         lens = [sh * 16 + 3 + 37 * i for i in range(20)] + [sh * 8, 0, 3]
-        lm, q, kc, vc, own, shared, o = check_step(lens, sh, hq, hk, d, dt, 16, seed=7, mul=mul)
+        lm, q, kc, vc, own, shared, o = check_step(lens, sh, hq, hk, d, dt, 16, seed=7, mul=mul, most=most)
         for b in (0, 7, 19, 20, 22):
             o1 = torch.zeros(1, hq, d, dtype=q.dtype, device="cuda")
             lm.step_q4(q[b:b + 1], kc, vc, i32(own[b:b + 1]), i32(lens[b:b + 1]), o1, shared_table=i32(shared))
@@ -281,6 +301,8 @@ def test_step_many_requests():
     rng = random.Random(1)
     check_step([rng.choice([0, 1, 7, 90]) for _ in range(600)], 0, 2, 1, 64, "bf16", 16)
     check_step([32 + rng.choice([0, 1, 7, 90]) for _ in range(1500)], 2, 2, 1, 64, "fp16", 16)
+    check_step([96 + rng.choice([-96, -50, 0, 1, 7, 90]) for _ in range(4096)], 6, 3, 1, 64, "bf16", 16)
+    check_step([400 + rng.choice([-400, -50, 0, 1, 7, 90]) for _ in range(1000)], 25, 12, 1, 128, "bf16", 16)
     check_step([40, 700, 3], 0, 8, 2, 128, "bf16", 16, most=4096)
 
 
@@ -423,6 +445,32 @@ def test_step_waits_are_bounded(most, sh):
     o2 = torch.zeros(o.shape, dtype=o.dtype, device="cuda")
     lm.step_q4(q, kc, vc, i32(own), i32(lens), o2, shared_table=i32(shared) if sh else None)
     assert lm.errors() == 0 and torch.equal(o2, o)
+
+
+@pytest.mark.parametrize("most", [6, 4096])
+def test_two_objects_at_once(most):
+    """Objects of their own on streams of their own, calls behind one another on each."""
+    hq, hk, d, bs, sh, lens = 8, 2, 128, 16, 40, [700, 640, 900, 1500, 0, 641]
+    lm, q, kc, vc, own, shared, want = check_step(lens, sh, hq, hk, d, "bf16", bs, seed=4, most=most)
+    n, width = kc.shape[0], len(own[0])
+    lms = [C.Lm(hq, hk, d, block_size=bs, n_blocks=n, table_blocks=width, max_requests=most, max_rows=8) for _ in range(3)]
+    streams = [torch.cuda.Stream() for _ in lms]
+    outs = [[torch.zeros(want.shape, dtype=q.dtype, device="cuda") for _ in range(20)] for _ in lms]
+    x, rows = logits(2, 24, 30001, "bf16"), 24
+    sums, ended = torch.zeros(rows, device="cuda"), i32([0] * rows)
+    picks = [[[torch.zeros(rows, device="cuda"), *(i32([0] * rows) for _ in range(3))] for _ in range(20)] for _ in lms]
+    own, lens, shared = i32(own), i32(lens), i32(shared)
+    big = [C.Lm(1, 1, 64, max_requests=rows) for _ in lms]
+    torch.cuda.synchronize()
+    for turn in range(20):
+        for i, s in enumerate(streams):
+            lms[i].step_q4(q, kc, vc, own, lens, outs[i][turn], shared_table=shared, stream=s)
+            big[i].beams(x, 8, sums, ended, 1, *picks[i][turn], stream=s)
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, want) for of in outs for o in of)
+    assert all(torch.equal(a, b) for of in picks for got in of for a, b in zip(got, picks[0][0]))
+    assert picks[0][0][1].tolist() == Q.beams(f64(x), 8, np.zeros(rows), [0] * rows, 1)["parents"]
+    assert all(l.errors() == 0 for l in lms + big)
 
 
 def test_streams_and_cache_beyond_32_bits():
@@ -635,7 +683,7 @@ def logits(seed, rows, vocab, dt, spread=2.5, pad=0, at=0):
 @pytest.mark.parametrize("groups,k,vocab,dt,pad,at", [
     (1, 1, 2, "fp32", 0, 0), (3, 2, 5, "bf16", 3, 1), (2, 4, 33, "fp16", 0, 0), (4, 4, 2048, "fp32", 0, 0),
     (3, 8, 2047, "bf16", 0, 0), (2, 32, 1025, "fp16", 7, 3), (1, 32, 70001, "bf16", 0, 0), (5, 5, 4099, "fp32", 1, 1),
-    (70, 4, 513, "bf16", 0, 0), (2, 3, 131072, "fp16", 0, 0), (1, 17, 9000, "fp32", 0, 0), (1, 4, 1000003, "bf16", 0, 0),
+    (70, 4, 513, "bf16", 0, 0), (1, 1, 1000003, "fp32", 1, 1), (128, 32, 40, "fp16", 0, 0), (40, 32, 3001, "bf16", 1, 0), (2, 3, 131072, "fp16", 0, 0), (1, 17, 9000, "fp32", 0, 0), (1, 4, 1000003, "bf16", 0, 0),
 ])
 def test_beams(groups, k, vocab, dt, pad, at):
     rows = groups * k
@@ -897,6 +945,9 @@ def test_refusals():
     refused(E, lm.beams, x, 2, s, e, -2, *out())
     refused(E, lm.beams, x[:, :1], 2, s, e, 0, *out())
     refused(E, lm.beams, x, 2, s, e, 1, s, *out()[1:])
+    refused(E, lm.beams, x, 2, s, e, 1, out()[0], e, *out()[2:])
+    refused(E, lm.beams, x, 2, s, e, 1, *out()[:2], *[i32([0, 0])] * 2)
+    refused(E, lm.beams, x[:1].expand(2, 9), 2, s, e, 1, *out())            # both rows in one place
     refused(E, lm.beams, torch.zeros(4, 9, device="cuda"), 2, torch.zeros(4, device="cuda"), i32([0] * 4), 1,
             torch.zeros(4, device="cuda"), i32([0] * 4), i32([0] * 4), i32([0] * 4))     # more rows than requests
     f2 = lambda: torch.zeros(2, dtype=torch.int64, device="cuda")
@@ -909,6 +960,13 @@ def test_refusals():
     refused(E, fork, tables_out=tb)
     refused(E, fork, owners_out=ow)
     refused(E, fork, kv_out=kv)
+    two = i32([0, 0])
+    for pair in (("parents", "status"), ("parents", "copy_src"), ("kv_out", "status"), ("copy_src", "copy_dst"),
+                 ("kv_len", "copy_dst")):
+        refused(E, fork, **{name: two for name in pair})
+    refused(E, fork, owners=ring)
+    refused(E, fork, owners_out=ring)
+    refused(E, fork, **(lambda t: dict(free_in=t, free_out=t))(f2()))
     refused(E, fork, shared_blocks=4)
     refused(E, fork, shared_blocks=-1)
     refused(V, fork, owners=ow[:3])
@@ -919,6 +977,9 @@ def test_refusals():
                                              copies=one), **kw})
     comp()
     refused(E, comp, tables_out=tb)
+    refused(E, comp, copy_src=two, copy_dst=two)
+    refused(E, comp, kv_len=two, copy_dst=two)
+    refused(E, comp, owners=ring)
     refused(E, comp, owners=None)
     refused(V, comp, copy_src=i32([0]))
     refused(V, comp, shared_table=i32([1]), shared_out=i32([1, 2]))
