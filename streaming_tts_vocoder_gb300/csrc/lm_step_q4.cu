@@ -361,16 +361,21 @@ __global__ void __launch_bounds__(kThreads, kCtas<D, NT>) lm_step_q4_kernel(cons
                 }
             }
         }
-        if (lane == turn) {
+        // (by one lane that the compiler knows to be one: the copies' operands are uniform)
+        const int first_tile = __shfl_sync(0xffffffffu, tile[0], turn);
+        const bool both = end - from > 16, apart = both && p.bs_shift == 4;
+        const int second = apart ? __shfl_sync(0xffffffffu, tile[1], turn) : -1;
+        if (elect_one()) {
             uint8_t* dst = ring + st * kStage;
-            const bool both = end - from > 16, apart = both && p.bs_shift == 4;
             const uint32_t bytes = both && !apart ? 2 * kTile : kTile;
             mbar_expect_tx(&full[st], both ? 4 * kTile : 2 * kTile);
-            bulk_load(dst, tile[0] >= 0 ? p.k + tile[0] * (long long)kTile : p.zeros, &full[st], bytes);
-            bulk_load(dst + kTiles * kTile, tile[0] >= 0 ? p.v + tile[0] * (long long)kTile : p.zeros, &full[st], bytes);
+            const long long at = first_tile * (long long)kTile;
+            bulk_load(dst, first_tile >= 0 ? p.k + at : p.zeros, &full[st], bytes);
+            bulk_load(dst + kTiles * kTile, first_tile >= 0 ? p.v + at : p.zeros, &full[st], bytes);
             if (apart) {
-                bulk_load(dst + kTile, tile[1] >= 0 ? p.k + tile[1] * (long long)kTile : p.zeros, &full[st], kTile);
-                bulk_load(dst + (kTiles + 1) * kTile, tile[1] >= 0 ? p.v + tile[1] * (long long)kTile : p.zeros, &full[st], kTile);
+                const long long at1 = second * (long long)kTile;
+                bulk_load(dst + kTile, second >= 0 ? p.k + at1 : p.zeros, &full[st], kTile);
+                bulk_load(dst + (kTiles + 1) * kTile, second >= 0 ? p.v + at1 : p.zeros, &full[st], kTile);
             }
         }
         turn++;
