@@ -29,7 +29,7 @@ struct Q4Tile {
 };
 
 // Queries as halves: times 2^lift, which brings a head's largest element to 2^14 ..
-// 2^15, so exact but for what lies 2^34 below (what is not finite stays so); and
+// 2^15, so exact but for what lies 2^24 below (what is not finite stays so); and
 // the factor that undoes it with the scale.
 __device__ __forceinline__ int q4_query_lift(float top)
 {

@@ -19,9 +19,25 @@
 // warp's: it takes units from a counter, keeps a ring of stages of 32 keys in
 // flight across them by bulk copies of its own, and shares nothing with other
 // warps, so there is no barrier but the one that a stage's copies complete.
-// Partial results are joined in order by a kernel of its own.  A part that all requests
-// share is units of its own, whose columns are the heads of several requests; a long one
-// is first turned into halves and then the prompt kernel's work, as over a cache of 16 bits.
+// Partial results are joined in order by a kernel of its own.  A part that all
+// requests share is units of its own, whose columns are the heads of several requests;
+// a long one is first turned into halves and then the prompt kernel's work, as over a
+// cache of 16 bits.
+//
+// Roundings: queries to halves after the power of two (exact but for elements below
+// 2^-24 of the head's largest), probabilities times a scale to halves, by 2^-11: what a
+// 16-bit operand holds of them, and what the results are rounded to is coarser (bf16)
+// or as coarse (fp16).
+//
+// What bounds it: instructions and their latency, not the memory.  A tile of 16 keys and
+// values of 128 takes 252 instructions (80 make operands of codes, 18 are MMAs), a unit
+// 1,140 more, and accumulators and operands leave room for 12 warps an SM, which use 42 %
+// of the issue slots: 64 requests of 2,000 positions (32 / 8 heads of 128) 50 us, 3.4
+// TB/s; 64 of 750 (16 heads of 64) 31 us.  256 of 500 to 4,000 behind 8,192: 162 us,
+// where 16 bits take 277.  Measured and slower: one tile at a time and four CTAs (184 us
+// against 164), four CTAs at width 64 (34.6 against 31.8), the next unit's blocks or
+// queries asked for ahead (170; registers spill), each request's last chunk in quarters
+// (170: a unit costs its warp about 6 us), results joined in this kernel (spills).
 #include <algorithm>
 #include <type_traits>
 
