@@ -246,8 +246,10 @@ __global__ void __launch_bounds__(kRowThreads, 8) lm_beam_rows_kernel(const LmBe
             bad = true;
             break;
         }
-        // The first warp takes the window's (lane, chunk) with the largest values first,
-        // until none can hold one that belongs into the list.
+        // The first warp takes the window's places (lane, chunk) with the largest values first,
+        // until none can hold one that belongs into the list: K of them at a time, whose
+        // last one's largest is below the list's last already, so that of their values, read
+        // together, few are put in.
         float mx[kRowWarps];                    // of this lane's chunks of each warp, and which
         int of[kRowWarps];
         auto look = [&](int w) {
@@ -270,52 +272,79 @@ __global__ void __launch_bounds__(kRowThreads, 8) lm_beam_rows_kernel(const LmBe
 #pragma unroll
             for (int w = 0; w < kRowWarps; w++) look(w);
         }
-        for (int turn = 0; turn < 32 * kRowWarps * kWindow && warp == 0; turn++) {
-            float mine = mx[0];
-            int at_w = 0, at_j = of[0];
+        constexpr int kPlaces = 32 * kRowWarps * kWindow;
+        bool more = warp == 0;
+        for (int round = 0; round <= kPlaces && more; round++) {
+            int n = 0, place = 0;               // lane i: the i-th place
+            float y = 0.f;
+            for (int turn = 0; turn <= kPlaces && n < K; turn++) {
+                float mine = mx[0];
+                int at_w = 0, at_j = of[0];
 #pragma unroll
-            for (int w = 1; w < kRowWarps; w++) {
-                at_j = mx[w] > mine ? of[w] : at_j;
-                at_w = mx[w] > mine ? w : at_w;
-                mine = fmaxf(mine, mx[w]);
-            }
-            const int key = ordered(mine), k = __reduce_max_sync(0xffffffffu, key);
-            const float y = __int_as_float(k >= 0 ? k : k ^ 0x7fffffff);
-            if (y == -INFINITY || y < least) break;
-            const int from = __ffs(__ballot_sync(0xffffffffu, key == k)) - 1;
-            const int w = __shfl_sync(0xffffffffu, at_w, from), j0 = __shfl_sync(0xffffffffu, at_j, from);
-            const int c = c0 + w + kRowWarps * j0;
-            if (lane == from) {
-                tops[w][j0][lane] = -INFINITY;
-                look(w);
-            }
-            __syncwarp();
-            if (y == least && c * kChunk - lead > least_i) continue;    // equal ones only before those of the list
-            // its values: V::N / 4 for each lane
-            constexpr int kE = V::N / 4;
-            const int at = c * kChunk + ((lane >> 2) * 32 + from) * V::N + (lane & 3) * kE;
-            float z[kE];
-#pragma unroll
-            for (int j = 0; j < kE; j++) z[j] = at + j >= lead && at + j < end ? to_float(base[at + j]) : -INFINITY;
-#pragma unroll
-            for (int j = 0; j < kE; j++) {
-                unsigned in = __ballot_sync(0xffffffffu, z[j] > -INFINITY && ahead(z[j], at + j - lead, least, least_i));
-                if (in == 0) continue;
-                while (in) {
-                    const int who = __ffs(in) - 1;
-                    in &= in - 1;
-                    const float nx = __shfl_sync(0xffffffffu, z[j], who);
-                    const int ni = __shfl_sync(0xffffffffu, at + j - lead, who);
-                    const int place = __popc(__ballot_sync(0xffffffffu, ahead(best_x, best_i, nx, ni)));
-                    const float ux = __shfl_up_sync(0xffffffffu, best_x, 1);
-                    const int ui = __shfl_up_sync(0xffffffffu, best_i, 1);
-                    if (lane >= place) {
-                        best_x = lane == place ? nx : ux;
-                        best_i = lane == place ? ni : ui;
-                    }
+                for (int w = 1; w < kRowWarps; w++) {
+                    at_j = mx[w] > mine ? of[w] : at_j;
+                    at_w = mx[w] > mine ? w : at_w;
+                    mine = fmaxf(mine, mx[w]);
                 }
-                least = __shfl_sync(0xffffffffu, best_x, K - 1);
-                least_i = __shfl_sync(0xffffffffu, best_i, K - 1);
+                const int key = ordered(mine), k = __reduce_max_sync(0xffffffffu, key);
+                y = __int_as_float(k >= 0 ? k : k ^ 0x7fffffff);
+                more = y > -INFINITY && y >= least;
+                if (!more) break;
+                const int from = __ffs(__ballot_sync(0xffffffffu, key == k)) - 1;
+                const int w = __shfl_sync(0xffffffffu, at_w, from), j0 = __shfl_sync(0xffffffffu, at_j, from);
+                const int c = c0 + w + kRowWarps * j0;
+                if (lane == from) {
+                    tops[w][j0][lane] = -INFINITY;
+                    look(w);
+                }
+                __syncwarp();
+                if (y == least && c * kChunk - lead > least_i) continue;    // equal ones only before those of the list
+                if (lane == n) place = c * 32 + from;
+                n++;
+            }
+            if (n == K && y > least) {          // K values are as large
+                least = y;
+                least_i = INT_MAX;
+            }
+            // their values: V::N / 4 for each lane, of kRead places at once
+            constexpr int kE = V::N / 4, kRead = 4;
+            for (int first = 0; first < n; first += kRead) {
+                float z[kRead][kE];
+                int at[kRead];
+#pragma unroll
+                for (int q = 0; q < kRead; q++) {
+                    const int pl = __shfl_sync(0xffffffffu, place, min(first + q, n - 1));
+                    at[q] = pl / 32 * kChunk + ((lane >> 2) * 32 + pl % 32) * V::N + (lane & 3) * kE;
+#pragma unroll
+                    for (int j = 0; j < kE; j++)
+                        z[q][j] = first + q < n && at[q] + j >= lead && at[q] + j < end ? to_float(base[at[q] + j]) : -INFINITY;
+                }
+#pragma unroll
+                for (int q = 0; q < kRead; q++)
+#pragma unroll
+                    for (int j = 0; j < kE; j++) {
+                        unsigned in = __ballot_sync(0xffffffffu, z[q][j] > -INFINITY && ahead(z[q][j], at[q] + j - lead, least, least_i));
+                        if (in == 0) continue;
+                        while (in) {
+                            const int who = __ffs(in) - 1;
+                            in &= in - 1;
+                            const float nx = __shfl_sync(0xffffffffu, z[q][j], who);
+                            const int ni = __shfl_sync(0xffffffffu, at[q] + j - lead, who);
+                            const int to = __popc(__ballot_sync(0xffffffffu, ahead(best_x, best_i, nx, ni)));
+                            const float ux = __shfl_up_sync(0xffffffffu, best_x, 1);
+                            const int ui = __shfl_up_sync(0xffffffffu, best_i, 1);
+                            if (lane >= to) {
+                                best_x = lane == to ? nx : ux;
+                                best_i = lane == to ? ni : ui;
+                            }
+                        }
+                        const float kx = __shfl_sync(0xffffffffu, best_x, K - 1);
+                        const int ki = __shfl_sync(0xffffffffu, best_i, K - 1);
+                        if (ahead(kx, ki, least, least_i)) {
+                            least = kx;
+                            least_i = ki;
+                        }
+                    }
             }
         }
         __syncthreads();                        // tops are written again
