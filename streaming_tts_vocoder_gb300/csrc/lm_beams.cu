@@ -161,7 +161,7 @@ __global__ void __launch_bounds__(kRowThreads, 8) lm_beam_rows_kernel(const LmBe
     using V = Vector<T>;
     constexpr int kChunk = kVectors * 32 * V::N;
     constexpr float kLog2e = 1.4426950408889634f;
-    __shared__ float tops[kRowWarps][kWindow][32];
+    __shared__ float tops[kRowWarps][kWindow][33];      // (33: a lane's of all chunks lie in different banks)
     __shared__ float part_hi[kRowWarps], part_lo[kRowWarps], part_top[kRowWarps];
     __shared__ int part_c[kRowWarps];
     const int row = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, K = a.beams;
@@ -252,26 +252,20 @@ __global__ void __launch_bounds__(kRowThreads, 8) lm_beam_rows_kernel(const LmBe
         // together, few are put in.
         float mx[kRowWarps];                    // of this lane's chunks of each warp, and which
         int of[kRowWarps];
-        auto look = [&](int w) {
-            float m = tops[w][0][lane];
-            int which = 0;
-#pragma unroll
-            for (int j = 1; j < kWindow; j++) {
-                const float y = tops[w][j][lane];
-                which = y > m ? j : which;
-                m = fmaxf(m, y);
-            }
-#pragma unroll
-            for (int j = 0; j < kRowWarps; j++)
-                if (j == w) {
-                    mx[j] = m;
-                    of[j] = which;
-                }
-        };
         if (warp == 0) {
 #pragma unroll
-            for (int w = 0; w < kRowWarps; w++) look(w);
+            for (int w = 0; w < kRowWarps; w++) {
+                mx[w] = tops[w][0][lane];
+                of[w] = 0;
+#pragma unroll
+                for (int j = 1; j < kWindow; j++) {
+                    const float y = tops[w][j][lane];
+                    of[w] = y > mx[w] ? j : of[w];
+                    mx[w] = fmaxf(mx[w], y);
+                }
+            }
         }
+        __syncwarp();
         constexpr int kPlaces = 32 * kRowWarps * kWindow;
         bool more = warp == 0;
         for (int round = 0; round <= kPlaces && more; round++) {
@@ -293,11 +287,18 @@ __global__ void __launch_bounds__(kRowThreads, 8) lm_beam_rows_kernel(const LmBe
                 const int from = __ffs(__ballot_sync(0xffffffffu, key == k)) - 1;
                 const int w = __shfl_sync(0xffffffffu, at_w, from), j0 = __shfl_sync(0xffffffffu, at_j, from);
                 const int c = c0 + w + kRowWarps * j0;
-                if (lane == from) {
-                    tops[w][j0][lane] = -INFINITY;
-                    look(w);
-                }
-                __syncwarp();
+                // that lane's next one of the warp's chunks: a chunk a lane
+                float left = lane < kWindow && lane != j0 ? tops[w][lane][from] : -INFINITY;
+                if (lane == j0) tops[w][j0][from] = -INFINITY;
+                const int left_key = ordered(left), left_k = __reduce_max_sync(0xffffffffu, left_key);
+                const int left_j = __ffs(__ballot_sync(0xffffffffu, left_key == left_k)) - 1;
+                left = __int_as_float(left_k >= 0 ? left_k : left_k ^ 0x7fffffff);
+#pragma unroll
+                for (int i = 0; i < kRowWarps; i++)
+                    if (i == w && lane == from) {
+                        mx[i] = left;
+                        of[i] = left_j;
+                    }
                 if (y == least && c * kChunk - lead > least_i) continue;    // equal ones only before those of the list
                 if (lane == n) place = c * 32 + from;
                 n++;
