@@ -16,11 +16,12 @@
 // the first left out) come from different rows and lie closer, the logarithms
 // of those rows are worked out again to about 1e-9, and the choice is made once more.
 //
-// 1,024 rows of 65,537 in bf16 (60 of them ended): 43 us, 3 TB/s.  Neither the memory
-// (43 %) nor the issue slots (34 %) bound it: a chunk's loads, maxima and sums follow one
-// another in each warp, and all rows are one wave of CTAs, whose last stretch is the
-// search.  The next chunk in registers meanwhile (spills), a search that looks one place
-// ahead (44 us) were no faster.  4 x 4 of 2,048: 12 us, two launches and the second one's
+// 1,024 rows of 65,537 in bf16 (60 of them ended): 37.6 us, 3.4 TB/s; 30 of it before the
+// search.  Neither the memory nor the issue slots bound it: a chunk's loads, maxima and
+// sums follow one another in each warp, and all rows are one wave of CTAs, whose last
+// stretch is the search.  The next chunk in registers meanwhile (spills), prefetches two
+// chunks ahead (+1.5 us), six CTAs an SM (two waves, 54 us), ten (48), twice as many parts
+// of a row (43) were slower.  4 x 4 of 2,048: 9.4 us, two launches and the second one's
 // chain of steps.
 #include <climits>
 
