@@ -869,13 +869,15 @@ CODEC_API codec_status codec_lm_load_q4(codec_lm_t* lm, const void* k_cache, con
 
 /* codec_lm_step over the cache in 4 bits.  Queries and outputs are of the
  * object's type.  Scores, their maxima and all sums are fp32; queries enter the
- * products as fp16 times a power of two of each head's own, probabilities (times a
- * value group's scale) as fp16.  Up to 64 positions of a shared part are read by
- * every request; a long one (by max_requests, the heads and its length: from about
- * 16,384 tiles of 16 keys and 8 query heads) is turned into fp16 keys and values
- * first, in a workspace of at most 32,768 positions of one layer, and what is
- * behind these is read by every request.  A group that stands for NaN makes what
- * it takes part in NaN.  Errors as codec_lm_step. */
+ * products as fp16 times a power of two of each head's own, probabilities (and these
+ * times a value group's scale) as fp16, for fp16 results as two of them.  Up to 64
+ * positions of a shared part are read by every request.  For bf16 a long one (by
+ * max_requests, the heads and its length: from about 16,384 tiles of 16 keys and 8
+ * query heads) is turned into fp16 keys and values first, in a workspace of at most
+ * 32,768 positions of one layer, and what is behind these is read by every request;
+ * for fp16, whose results would show that rounding, it never is, which costs up to
+ * three times as much behind many thousand positions.  A group that stands for NaN
+ * makes what it takes part in NaN.  Errors as codec_lm_step. */
 CODEC_API codec_status codec_lm_step_q4(codec_lm_t* lm, const void* q, int64_t q_stride, int32_t B,
                                         const void* k_cache, const void* v_cache, const int32_t* tables,
                                         const int32_t* kv_len, const int32_t* shared_table, int32_t shared_blocks,

@@ -140,7 +140,7 @@ struct LmStepSpace {
     int* taken;                     // the same (behind done)
     int chunk_q4, max_splits_q4;    // chunk and max_splits over the cache in 4 bits
     unsigned char* zeros;           // two tiles of 16 positions in 4 bits that stand for zero
-    // A shared part in 4 bits, as halves: at most shared_q4 positions [shared_q4][hk][D],
+    // A shared part in 4 bits, as halves (bf16): at most shared_q4 positions [shared_q4][hk][D],
     // the queries [max_requests][hq][D] and their factors, and the numbers 0, 1, ..
     int shared_q4;
     void *k16, *v16, *q16;
@@ -189,7 +189,7 @@ struct LmLoadQ4Args {
 cudaError_t launch_lm_load_q4(const LmShape& sh, const LmLoadQ4Args& a, cudaStream_t s);
 
 // Blocks 0 .. n - 1 of table in halves to k16, v16 [n][block][hk][D] (zeros for an id
-// out of range), and queries [B][hq][D] of the object's type in halves to q16, each
+// out of range), and queries [B][hq][D], bf16, in halves to q16, each
 // head times a power of two, with scale log2(e) / that in row_c.
 struct LmHalvesArgs {
     const void *k_cache, *v_cache;

@@ -167,7 +167,7 @@ codec_status codec_lm_create(const codec_lm_config* cfg, codec_lm_t** out)
     sp.shared_ctas = (int)(pairs * c.kv_heads);
     sp.heads = heads;
     const int pre_max = lm_shared_splits(sp.shared_ctas, positions);
-    sp.shared_q4 = (int)std::min<int64_t>(positions, kLmSharedQ4);
+    sp.shared_q4 = c.type == CODEC_LM_BF16 ? (int)std::min<int64_t>(positions, kLmSharedQ4) : 0;
     LmBeamSpace& bm = lm->beam;
     bm.parts = lm_beam_parts(c.max_requests);
     LmPromptSpace& pr = lm->prompt;
@@ -204,7 +204,7 @@ codec_status codec_lm_create(const codec_lm_config* cfg, codec_lm_t** out)
         configure_lm_pages() != cudaSuccess || configure_lm_beams() != cudaSuccess ||
         cudaMemset(sp.done, 0, sizeof(int) * ((size_t)c.max_requests * c.kv_heads + 1)) != cudaSuccess ||
         cudaMemset(sp.zeros, 0, kLmZeroBytes) != cudaSuccess ||
-        launch_lm_count(sp.count, sp.shared_q4 / c.block_size, nullptr) != cudaSuccess ||
+        (sp.shared_q4 > 0 && launch_lm_count(sp.count, sp.shared_q4 / c.block_size, nullptr) != cudaSuccess) ||
         cudaMemset(lm->err, 0, sizeof(unsigned)) != cudaSuccess ||
         launch_lm_turn_table(lm->turn, c.max_positions, c.head_dim, c.rope_theta, nullptr) != cudaSuccess ||
         cudaDeviceSynchronize() != cudaSuccess) {

@@ -274,8 +274,7 @@ __global__ void __launch_bounds__(kThreads) lm_load_q4_kernel(const LoadArgs a)
 
 // See LmHalvesArgs.  blockIdx.y: keys, values, queries (a warp per row and head).
 template <int D>
-__global__ void __launch_bounds__(kThreads) lm_halves_q4_kernel(const LmHalvesArgs a, int hq, int hk, int bf16, float scale,
-                                                             unsigned* err)
+__global__ void __launch_bounds__(kThreads) lm_halves_q4_kernel(const LmHalvesArgs a, int hq, int hk, float scale, unsigned* err)
 {
     __shared__ uint4 buf[kThreads / 32][Q4Tile<D>::kBytes / 16];
     const int lane = threadIdx.x & 31;
@@ -308,7 +307,7 @@ __global__ void __launch_bounds__(kThreads) lm_halves_q4_kernel(const LmHalvesAr
 #pragma unroll
         for (int e = 0; e < kE / 2; e++) {
             const uint32_t u = row[e];
-            x[e] = bf16 ? unpack2(u, static_cast<const __nv_bfloat16*>(nullptr)) : unpack2(u, static_cast<const __half*>(nullptr));
+            x[e] = unpack2(u, static_cast<const __nv_bfloat16*>(nullptr));
             top = fmaxf(top, fmaxf(fabsf(x[e].x), fabsf(x[e].y)));
         }
 #pragma unroll
@@ -375,7 +374,7 @@ cudaError_t launch_lm_halves_q4(const LmShape& sh, const LmHalvesArgs& a, cudaSt
     const long long warps = std::max(((long long)a.n * sh.hk) << (a.bs_shift - 4), (long long)a.B * sh.hq);
     const dim3 grid((unsigned)std::min<long long>((warps + kThreads / 32 - 1) / (kThreads / 32), 152 * 16), 3);
     return launch_pdl(sh.D == 128 ? lm_halves_q4_kernel<128> : lm_halves_q4_kernel<64>, grid, dim3(kThreads), 0, s, a, sh.hq,
-                      sh.hk, (int)(sh.type == CODEC_LM_BF16), (float)(sh.scale * 1.4426950408889634), sh.err);
+                      sh.hk, (float)(sh.scale * 1.4426950408889634), sh.err);
 }
 
 cudaError_t launch_lm_count(int* count, int n, cudaStream_t s)

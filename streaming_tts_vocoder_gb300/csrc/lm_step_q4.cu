@@ -25,9 +25,8 @@
 // cache of 16 bits.
 //
 // Roundings: queries to halves after the power of two (exact but for elements below
-// 2^-24 of the head's largest), probabilities times a scale to halves, by 2^-11: what a
-// 16-bit operand holds of them, and what the results are rounded to is coarser (bf16)
-// or as coarse (fp16).
+// 2^-24 of the head's largest); probabilities, and these times a scale, to halves, by
+// 2^-11, where results are bf16, and to two halves, by 2^-21, where they are fp16.
 //
 // What bounds it: instructions and their latency, not the memory.  A tile of 16 keys and
 // values of 128 takes 252 instructions (80 make operands of codes, 18 are MMAs), a unit
@@ -129,6 +128,20 @@ __device__ __forceinline__ float low_half(uint32_t w) { return __half2float(__us
 __device__ __forceinline__ uint32_t times(uint32_t a, uint32_t b)
 {
     const __half2 v = __hmul2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
+    return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+// What rounding a and b to the halves of ab left off.
+__device__ __forceinline__ uint32_t left_off(float a, float b, uint32_t ab)
+{
+    const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&ab));
+    return pack(a - v.x, b - v.y);
+}
+// (a + e) s - as, with as the rounded a s.
+__device__ __forceinline__ uint32_t times_left(uint32_t a, uint32_t e, uint32_t s, uint32_t as)
+{
+    auto half2 = [](const uint32_t& x) { return *reinterpret_cast<const __half2*>(&x); };
+    const __half2 v = __hfma2(half2(e), half2(s), __hfma2(half2(a), half2(s), __hneg2(half2(as))));
     return *reinterpret_cast<const uint32_t*>(&v);
 }
 
@@ -263,8 +276,11 @@ __global__ void __launch_bounds__(kJoinThreads) lm_join_q4_kernel(const __grid_c
     join_parts<D, 16>(p, b, h, n, len == 0, threadIdx.x & 31);
 }
 
-// NT: sets of eight columns.
-template <int D, int NT>
+// NT: sets of eight columns.  kFine: a probability, and its product with a scale, is two
+// halves, what is rounded and what that leaves off (2^-21 in all).  Rounded to one half
+// each they put a result off by 0.0003 of it, where its own rounding to fp16 does by 0.0002
+// and to bf16 by 0.0017: fp16 results have it, for 15 % more instructions.
+template <int D, int NT, bool kFine>
 __global__ void __launch_bounds__(kThreads, kCtas<D, NT>) lm_step_q4_kernel(const __grid_constant__ Params p)
 {
     using Tile = Q4Tile<D>;
@@ -635,7 +651,7 @@ __global__ void __launch_bounds__(kThreads, kCtas<D, NT>) lm_step_q4_kernel(cons
                     }
                     each<kAt>([&](auto I) {
                         constexpr int i = I, kOff = (kTiles + i) * kTile;
-                        uint32_t va[G], vb[G], f0[NT], f1[NT];
+                        uint32_t va[G], vb[G], f0[NT], f1[NT], e0[NT], e1[NT];
                         lds<G, kOff>(kt + v_at, va);
                         lds<G, kOff + 4 * D>(kt + v_at, vb);
 #pragma unroll
@@ -644,9 +660,16 @@ __global__ void __launch_bounds__(kThreads, kCtas<D, NT>) lm_step_q4_kernel(cons
                             const float p2 = exp2_fast(fmaf(s[i][x][2], cf[x][0], bias[x][0])), p3 = exp2_fast(fmaf(s[i][x][3], cf[x][1], bias[x][1]));
                             l[x][0] += p0 + p2;
                             l[x][1] += p1 + p3;
-                            f0[x] = transposed(pack(p0, p1));
-                            f1[x] = transposed(pack(p2, p3));
+                            f0[x] = pack(p0, p1);
+                            f1[x] = pack(p2, p3);
+                            if constexpr (kFine) {
+                                e0[x] = transposed(left_off(p0, p1, f0[x]));
+                                e1[x] = transposed(left_off(p2, p3, f1[x]));
+                            }
+                            f0[x] = transposed(f0[x]);
+                            f1[x] = transposed(f1[x]);
                             mma(low[x], vl[i][0], 0u, vl[i][1], 0u, f0[x], f1[x]);
+                            if constexpr (kFine) mma(low[x], vl[i][0], 0u, vl[i][1], 0u, e0[x], e1[x]);
                         }
 #pragma unroll
                         for (int g = 0; g < G; g++) {
@@ -657,6 +680,11 @@ __global__ void __launch_bounds__(kThreads, kCtas<D, NT>) lm_step_q4_kernel(cons
                                 const uint32_t g0 = times(f0[x], sc[i][2 * g]), g1 = times(f1[x], sc[i][2 * g + 1]);
                                 mma(acc[x][g][0], a0, a1, b0, b1, g0, g1);
                                 mma(acc[x][g][1], a2, a3, b2, b3, g0, g1);
+                                if constexpr (kFine) {
+                                    const uint32_t h0 = times_left(f0[x], e0[x], sc[i][2 * g], g0), h1 = times_left(f1[x], e1[x], sc[i][2 * g + 1], g1);
+                                    mma(acc[x][g][0], a0, a1, b0, b1, h0, h1);
+                                    mma(acc[x][g][1], a2, a3, b2, b3, h0, h1);
+                                }
                             }
                         }
                     });
@@ -772,11 +800,12 @@ cudaError_t launch(const LmShape& sh, const LmStepArgs& a, cudaStream_t s)
     // 1 to 500 behind 256, as many: 53.3, 44.8, 49.5).  Beyond, it is turned into halves
     // and the prompt kernel's (behind 4,096, 64 x 16 heads, 32,768 tiles: 113, 39.4, 36.7;
     // 256 behind 8,192: 484, 269, 82.4); what of it does not fit the workspace every
-    // request reads.
+    // request reads.  Not for fp16: keys rounded to halves put its results off by 0.00054
+    // of them, where they are by 0.0002 when they are rounded alone.
     const int wide = sh.group > 8 ? 2 : 1;
     const long long tiles = a.ws.heads * sh.group / (8 * wide) * (p.shared_len / 16);
     if (a.ws.heads == sh.hk || p.shared_len <= 64) p.shared_len = 0;
-    if (p.shared_len > 0 && tiles <= 16384) {
+    if (p.shared_len > 0 && (tiles <= 16384 || !p.bf16)) {
         p.n_shared = (p.shared_len + p.chunk - 1) / p.chunk;
         p.sets = (a.B * sh.group + 8 * wide - 1) / (8 * wide);
     } else if (p.shared_len > 0) {
@@ -810,7 +839,8 @@ cudaError_t launch(const LmShape& sh, const LmStepArgs& a, cudaStream_t s)
     const bool two = p.n_pre + p.n_shared > 0 || p.max_splits > 1;
     // from the counter where a warp has more than one
     p.taken = two && most > (long long)ctas * kWarps ? a.ws.taken : nullptr;
-    auto kernel = wide == 2 ? lm_step_q4_kernel<D, 2> : lm_step_q4_kernel<D, 1>;
+    auto kernel = p.bf16 ? (wide == 2 ? lm_step_q4_kernel<D, 2, false> : lm_step_q4_kernel<D, 1, false>)
+                         : (wide == 2 ? lm_step_q4_kernel<D, 2, true> : lm_step_q4_kernel<D, 1, true>);
     const cudaError_t e = launch_pdl(kernel, dim3(ctas), dim3(kThreads), smem_bytes<D>(p.stages, a.B), s, p);
     if (e != cudaSuccess || !two) return e;
     return launch_pdl(lm_join_q4_kernel<D>, dim3((unsigned)(((long long)a.B * sh.hq + kJoinThreads / 32 - 1) / (kJoinThreads / 32))),
@@ -820,7 +850,8 @@ cudaError_t launch(const LmShape& sh, const LmStepArgs& a, cudaStream_t s)
 template <int D>
 cudaError_t configure()
 {
-    const void* kernels[] = {(const void*)lm_step_q4_kernel<D, 1>, (const void*)lm_step_q4_kernel<D, 2>};
+    const void* kernels[] = {(const void*)lm_step_q4_kernel<D, 1, false>, (const void*)lm_step_q4_kernel<D, 2, false>,
+                             (const void*)lm_step_q4_kernel<D, 1, true>, (const void*)lm_step_q4_kernel<D, 2, true>};
     for (const void* k : kernels) {
         const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
         if (e != cudaSuccess) return e;

@@ -89,10 +89,12 @@ def values(cache, bs, d, keys, parts=False):
     t = cache.reshape(n, hk, bs // 16, 10 * d)
     c = t[..., code]
     c = np.where(upper == 1, c >> 4, c & 15).astype(np.float64)
-    pick = lambda at: np.ascontiguousarray(t[..., np.stack([at, at + 1], -1)]).view(np.float16)[..., 0].astype(np.float64)
-    sc, lo = (np.repeat(pick(at), 32, -1) for at in (scale, low))
+    with np.errstate(invalid="ignore"):
+        pick = lambda at: np.ascontiguousarray(t[..., np.stack([at, at + 1], -1)]).view(np.float16)[..., 0].astype(np.float64)
+        sc, lo = (np.repeat(pick(at), 32, -1) for at in (scale, low))
     put = lambda x: np.moveaxis(x, 1, 3).reshape(n, bs, hk, d)
-    return (put(lo), put(sc * c)) if parts else put(lo + sc * c)
+    with np.errstate(invalid="ignore"):
+        return (put(lo), put(sc * c)) if parts else put(lo + sc * c)
 
 
 # ---- attention --------------------------------------------------------------
@@ -131,13 +133,18 @@ def assert_step(got, got_lse, ref, dtype, d, v_max):
     truncate at each of their steps of 16 keys.  Probabilities are held as multiples
     of 2^-24 with the row's largest at 2^6 at least (2^6 / v_max where scales pass 2),
     so each, and each product with a scale, may be off by 2^-31 of it, times a code
-    of 15 or a low."""
+    of 15 or a low.
+    fp16: a probability is two halves, what is rounded and what that leaves off, rounded:
+    2^-22 of it.  Its product with a scale as well: the rounded product's rest is exact,
+    the second half's product and their sum are rounded (2^-22 and 2^-21).  Sums take
+    two steps for 16 keys."""
     o, lse, al, ac, s, n = ref
     half = torch.finfo(DTYPES[dtype]).eps / 2
     ds = (4 * d * 2.0 ** -23 * (s + 1))[..., None]
     n = n[:, None, None]
-    a = al + ac
-    tol = half * np.abs(o) * 1.01 + al * 2.0 ** -11 * 1.01 + ac * 2.0 ** -10 * 1.01 + a * (2 * ds + (n / 8 + 16) * 2.0 ** -23)
+    a, fine = al + ac, dtype == "fp16"
+    tol = half * np.abs(o) * 1.01 + (al * 2.0 ** -11 + ac * 2.0 ** -10) * (2.0 ** -10 if fine else 1.01)
+    tol = tol + a * (2 * ds + (n / (4 if fine else 8) + 16) * 2.0 ** -23)
     tol = tol + n * 2.0 ** -31 * (15 + 2 * v_max) * max(1.0, v_max) + 2.0 ** -25 * (dtype == "fp16") + 1e-30
     g = got.detach().cpu().double().numpy()
     bad = ~(np.abs(g - o) <= tol)

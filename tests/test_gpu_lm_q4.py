@@ -144,18 +144,18 @@ def cache_q4(seed, lens, hk, d, bs, sh=0, v_mul=1.0):
     return kc, vc, tables, shared, n_blocks, width
 
 
-def as_halves(most, hq, hk, shared_len):
+def as_halves(dt, most, hq, hk, shared_len):
     """Positions of the shared part that the batch has in common as halves: none
-    where it is units of the step's own kernel (by tiles of 16 keys x 8 or 16
-    columns of an object for `most` requests) or read by every request."""
+    where it is units of the step's own kernel (fp16, or by tiles of 16 keys x 8 or
+    16 columns of an object for `most` requests) or read by every request."""
     wide = 16 if hq // hk > 8 else 8
-    return 0 if most == 1 or most * hq // wide * (shared_len // 16) <= 16384 else min(shared_len, 32768)
+    return 0 if dt != torch.bfloat16 or most == 1 or most * hq // wide * (shared_len // 16) <= 16384 else min(shared_len, 32768)
 
 
 def step_reference(q, kc, vc, tables, lens, shared, hk, d, bs, scale=None, most=1):
     sh = len(shared)
     parts = [Q.values(c.cpu().numpy(), bs, d, keys, parts=True) for c, keys in ((kc, True), (vc, False))]
-    halves = as_halves(most, q.shape[1], hk, sh * bs)
+    halves = as_halves(q.dtype, most, q.shape[1], hk, sh * bs)
 
     def keys_of(b):
         n = lens[b]
@@ -202,7 +202,7 @@ def test_step(hq, hk, d, bs):
     # the same behind more of it, for a few and for many requests
     lens = [11 * bs, 11 * bs + 1, 11 * bs + 70, 0, 11 * bs - 1, bs + 3, 1]
     check_step(lens, 11, hq, hk, d, dt, bs, seed=2)
-    assert as_halves(4096, hq, hk, 11 * bs)
+    assert as_halves(T["bf16"], 4096, hq, hk, 11 * bs)
     check_step(lens, 11, hq, hk, d, dt, bs, seed=3, most=4096)
 
 
