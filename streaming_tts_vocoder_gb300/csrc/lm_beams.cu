@@ -35,6 +35,10 @@ constexpr int kThreads = 256;
 // A row's logarithm is off by 2^-22 at most for ex2, 2^-24 for each of 16 additions
 // and of the product with log2 e (times up to 20); of either sign, they come to 1e-7.
 constexpr float kNear = 2e-6f;
+// A row whose largest logit is as far from zero (one masked by its type's lowest value
+// from end to end) has its logarithm worked out from the differences to that one: the
+// powers' whole numbers would not hold it.
+constexpr float kFar = 1048576.f;
 constexpr double kLog2eOff = 1.4426950408889634f / 1.4426950408889634074 - 1.;    // of log2 e as a float, relative
 constexpr int kLists = 256;                 // of a group: beams x parts of a row
 
@@ -405,8 +409,8 @@ __device__ __forceinline__ double log_of(double s, const float2* table)
     return (double)y + off * (1. - 0.5 * off);
 }
 
-// log(sum(exp(x))) of a row to about 1e-9, by the whole CTA: terms added with their
-// rounding errors kept.
+// log(sum(exp(x - top))) of a row to about 1e-9, by the whole CTA: terms added with
+// their rounding errors kept.
 template <typename T>
 __device__ double exact_log_sum(const T* x, int n, float top, const float2* table, double* sm)
 {
@@ -432,7 +436,7 @@ __device__ double exact_log_sum(const T* x, int n, float top, const float2* tabl
     __syncthreads();
     sum = 0.;
     for (int w = 0; w < kThreads / 32; w++) sum += sm[w];
-    return (double)top + log_of(sum, table);
+    return log_of(sum, table);
 }
 
 // One group.  Dynamic shared memory: the lists' scores as whole numbers of the same
@@ -441,14 +445,14 @@ template <typename T>
 __global__ void __launch_bounds__(kThreads) lm_beam_pick_kernel(const LmBeamArgs a, int parts)
 {
     extern __shared__ unsigned long long keys[];
-    __shared__ double base[kLmMaxBeams];        // sums - log(sum(exp)), or the sum of an ended beam
+    __shared__ double base[kLmMaxBeams];        // sums - log(sum(exp(x - top))), or the sum of an ended beam
     __shared__ float top[kLmMaxBeams];
     __shared__ int power[kLmMaxBeams];
     __shared__ int kind[kLmMaxBeams];           // 0: offers nothing, 1: tokens, 2: itself
     __shared__ double sums[kThreads / 32], got[kLmMaxBeams + 1];
     __shared__ int got_i[kLmMaxBeams + 1];
     __shared__ float2 table[64];
-    __shared__ unsigned again;
+    __shared__ unsigned again, far;
     const int K = a.beams, row0 = blockIdx.x * K, lists = K * parts;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     int* index = reinterpret_cast<int*>(keys + lists * K);
@@ -486,7 +490,7 @@ __global__ void __launch_bounds__(kThreads) lm_beam_pick_kernel(const LmBeamArgs
             power[r] = most;
         }
     }
-    if (tid == 0) again = 0;
+    if (tid == 0) again = far = 0;
     __syncthreads();
     if (tid < K) {
         const float m = top[tid];
@@ -494,9 +498,21 @@ __global__ void __launch_bounds__(kThreads) lm_beam_pick_kernel(const LmBeamArgs
         kind[tid] = !there ? 0 : itself ? 2 : fabsf(m) < INFINITY ? 1 : 0;
         // sums of 2^(x log2 e - c), with a log2 e that is 1.33e-8 of itself too small or large
         base[tid] = kind[tid] != 1 ? (double)sum
-                                   : (double)sum - ((log_of(base[tid], table) + power[tid] * 0.69314718055994531) - kLog2eOff * (double)m);
+                                   : (double)sum - ((log_of(base[tid], table) + power[tid] * 0.69314718055994531) -
+                                                    kLog2eOff * (double)m - (double)m);
+        if (kind[tid] == 1 && fabsf(m) >= kFar) atomicOr(&far, 1u << tid);
     }
     __syncthreads();
+    auto work_out = [&](unsigned rows) {
+        for (int q = 0; q < K; q++)
+            if (rows >> q & 1 && kind[q] == 1) {
+                const double l = exact_log_sum(static_cast<const T*>(a.logits) + (row0 + q) * a.stride, a.vocab, top[q],
+                                               table, sums);
+                if (tid == 0) base[q] = (double)__ldg(a.sums + row0 + q) - l;
+            }
+        __syncthreads();
+    };
+    if (far != 0) work_out(far);
     for (int round = 0; round < 2; round++) {
         for (int e = tid; e < lists * K; e += kThreads) {
             const uint2 c = e == tid ? ahead_of : __ldcg(best + e);
@@ -505,7 +521,7 @@ __global__ void __launch_bounds__(kThreads) lm_beam_pick_kernel(const LmBeamArgs
             int i = INT_MAX;
             double s = 0.;
             if (kind[r] == 1 && x > -INFINITY) {
-                s = base[r] + (double)x;
+                s = base[r] + ((double)x - (double)top[r]);
                 i = r * a.vocab + (int)c.y;
             } else if (kind[r] == 2 && e == r * parts * K) {
                 s = base[r];
@@ -571,17 +587,11 @@ __global__ void __launch_bounds__(kThreads) lm_beam_pick_kernel(const LmBeamArgs
         // and all that lie as near to the last one
         for (int e = tid; e < lists * K; e += kThreads) {
             const int row = e / K / parts;
-            if (kind[row] == 1 && fabs(base[row] + (double)__uint_as_float(__ldcg(best + e).x) - got[K - 1]) < kNear)
+            if (kind[row] == 1 && fabs(base[row] + ((double)__uint_as_float(__ldcg(best + e).x) - (double)top[row]) - got[K - 1]) < kNear)
                 atomicOr(&again, 1u << row);
         }
         __syncthreads();
-        for (int q = 0; q < K; q++)
-            if (again >> q & 1 && kind[q] == 1) {
-                const double l = exact_log_sum(static_cast<const T*>(a.logits) + (row0 + q) * a.stride, a.vocab, top[q],
-                                               table, sums);
-                if (tid == 0) base[q] = (double)__ldg(a.sums + row0 + q) - l;
-            }
-        __syncthreads();
+        work_out(again);
     }
     if (tid < K) {
         const int c = got_i[tid], row = row0 + tid;

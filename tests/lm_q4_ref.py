@@ -246,10 +246,10 @@ def beams(logits, k, sums, ended, end):
             if np.isnan(x).any() or not np.isfinite(x.max()):
                 continue
             m = x.max()
-            base = float(sums[r]) - (m + np.log(np.exp(x - m).sum()))
+            base = float(sums[r]) - np.log(np.exp(x - m).sum())
             for v in np.argsort(-x, kind="stable")[:k]:
                 if x[v] > -np.inf:
-                    got.append((-(base + x[v]), r, int(v), False))
+                    got.append((-(base + (x[v] - m)), r, int(v), False))
         got.sort(key=lambda c: c[:3])
         for i in range(k):
             s, r, v, itself = got[i] if i < len(got) else (np.inf, -1, -1, False)

@@ -708,6 +708,26 @@ def test_beams_ties_go_to_the_lowest(dt):
         check_beams(torch.full_like(x, -3.0), k, [-1.0] * (2 * k), [1] * k + [0] * k, 7)
 
 
+@pytest.mark.parametrize("dt", ["bf16", "fp16", "fp32"])
+def test_beams_masked_by_the_lowest_value(dt):
+    """The type's lowest value, and others far from zero, in places, in whole rows, in
+    whole stretches of a row; zeros of both signs are equal."""
+    k, vocab = 4, 9001
+    low = torch.finfo(T[dt]).min
+    x = logits(8, 4 * k, vocab, dt)
+    x[0], x[1, 3:], x[2, ::2], x[3, 4000:] = low, low, low, low
+    for b, far in enumerate([-1e9, -3e10, 1e10, 1e30]):
+        far = max(min(far, 6e4), -6e4) if dt == "fp16" else far
+        x[4 + b, 20:7000] = far
+        x[8 + b] = far
+        x[8 + b, 5 + b] = far + abs(far) / 16
+    x[12:] = 0.0
+    x[12:, ::3] = -0.0
+    sums = -np.arange(4 * k) / 7.0
+    check_beams(x, k, sums, [0] * (4 * k), 3)
+    check_beams(x, k, [0.0] * (4 * k), [0] * (4 * k), 3, most=4096)
+
+
 def test_beams_infinities_and_nan():
     k, vocab = 4, 3001
     x = logits(5, 3 * k, vocab, "fp32")
