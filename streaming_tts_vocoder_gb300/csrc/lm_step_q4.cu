@@ -261,17 +261,17 @@ constexpr int kJoinThreads = 128;
 template <int D>
 __global__ void __launch_bounds__(kJoinThreads) lm_join_q4_kernel(const __grid_constant__ Params p)
 {
-    pdl_wait();
-    pdl_launch();
-    if (blockIdx.x == 0 && threadIdx.x == 0) {
-        if (p.taken) *p.taken = 0;
-    }
+    // A length was complete before the units' kernel passed its own wait, so it need not
+    // wait for that kernel's end; from L2, as there.
     const long long w = blockIdx.x * (kJoinThreads / 32LL) + (threadIdx.x >> 5);
     const int b = (int)(w / p.sh.hq), h = (int)(w - (long long)b * p.sh.hq);
-    if (b >= p.B) return;
-    int len = __ldg(p.kv_len + b);
+    int len = b < p.B ? __ldcg(p.kv_len + b) : 0;
     lm_clamp_len(len, (long long)p.table_blocks << p.bs_shift);
     const int n = shared_of(p, len) + splits_of(p, len);
+    pdl_wait();
+    pdl_launch();
+    if (p.taken && blockIdx.x == 0 && threadIdx.x == 0) *p.taken = 0;
+    if (b >= p.B) return;
     if (n == 1 && p.n_pre == 0) return;         // written by its unit
     join_parts<D, 16>(p, b, h, n, len == 0, threadIdx.x & 31);
 }

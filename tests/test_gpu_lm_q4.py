@@ -219,6 +219,12 @@ def test_step_long(lens, sh, bs):
     check_step(lens, sh, 4, 1, 64, "fp16", bs, seed=2, mul=8.0)
 
 
+@pytest.mark.parametrize("dt,sh", [("bf16", 0), ("fp16", 0), ("fp16", 520), ("bf16", 520)])
+def test_step_units_of_many_positions(dt, sh):
+    """Tables of more than 65,536 positions: units of 2,048, looked up in more than one turn."""
+    check_step([68000, 66561, 0] if sh else [68000, 2049], sh, 2, 1, 64, dt, 128, seed=5)
+
+
 @pytest.mark.parametrize("v_mul", [3e-4, 40.0, 4000.0])
 def test_step_values_of_other_sizes(v_mul):
     check_step([300, 40, 1], 0, 4, 2, 128, "bf16", 32, seed=3, v_mul=v_mul)
@@ -614,6 +620,21 @@ def test_compact(seed, B, bs, sh, width, free):
                    t["copies"], shared_table=i32(shared) if sh else None, shared_out=t["shared_out"] if sh else None)
     assert lm.errors() == 0
     same({k: v.tolist() for k, v in t.items()}, Q.compact(lens, tables, [[-3] * width] * B, shared, owners, ring, bs))
+
+
+def test_one_block():
+    lm = C.Lm(2, 2, 64, n_blocks=1, table_blocks=1, max_requests=2, max_rows=8)
+    got = run_fork(lm, [0, 0], [5, 0], [[0], [-1]], [0], [0], (1, 1), 0, 1)       # no block for the copy
+    same(got, Q.fork([0, 0], [5, 0], [[0], [-1]], [[-3]] * 2, [0], [0], (1, 1), 16, 0))
+    got = run_fork(lm, [1, -1], [5, 0], [[0], [-1]], [0], [0], (1, 1), 0, 1)      # it is given back
+    same(got, Q.fork([1, -1], [5, 0], [[0], [-1]], [[-3]] * 2, [0], [0], (1, 1), 16, 0))
+    assert got["free_out"] == [1, 2] and got["free_list"] == [0]
+    none, t = i32([]), [i32([[-3]] * 2), i32([-3]), i32([0]), torch.zeros(2, dtype=torch.int64, device="cuda")]
+    for lens, want in (([16, 0], [0, 0]), ([0, 0], [0, 1])):
+        count = i32([-3])
+        lm.compact(i32(lens), i32([[0], [-1]]), t[0], i32([0]), t[1], t[2], t[3], none, none.clone(), count)
+        assert t[3].tolist() == want and count.item() == 0 and t[1].item() == 0
+    assert t[0].tolist() == [[0], [-3]] and lm.errors() == 0
 
 
 def test_compact_wrong_blocks_and_lengths():
