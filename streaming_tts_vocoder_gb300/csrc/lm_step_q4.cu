@@ -30,9 +30,9 @@
 //
 // What bounds it: instructions and their latency, not the memory.  A tile of 16 keys and
 // values of 128 takes 252 instructions (80 make operands of codes, 18 are MMAs), a unit
-// 1,140 more, and accumulators and operands leave room for 12 warps an SM, which use 42 %
-// of the issue slots: 64 requests of 2,000 positions (32 / 8 heads of 128) 50 us, 3.4
-// TB/s; 64 of 750 (16 heads of 64) 31 us.  256 of 500 to 4,000 behind 8,192: 162 us,
+// 980 more, and accumulators and operands leave room for 12 warps an SM, which use 42 %
+// of the issue slots: 64 requests of 2,000 positions (32 / 8 heads of 128) 49 us, 3.4
+// TB/s; 64 of 750 (16 heads of 64) 31 us.  256 of 500 to 4,000 behind 8,192: 159 us,
 // where 16 bits take 277.  Measured and slower: one tile at a time and four CTAs (184 us
 // against 164), four CTAs at width 64 (34.6 against 31.8), the next unit's blocks or
 // queries asked for ahead (170; registers spill), each request's last chunk in quarters
@@ -116,6 +116,19 @@ __device__ __forceinline__ float exp2_fast(float x)
 {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+__device__ __forceinline__ float log2_fast(float x)
+{
+    float y;
+    asm("lg2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float reciprocal(float x)
+{
+    float y;
+    asm("rcp.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
 
@@ -478,8 +491,8 @@ __global__ void __launch_bounds__(kThreads, kCtas<D, NT>) lm_step_q4_kernel(cons
                 const uint32_t u[4] = {w[g].x, w[g].y, w[g].z, w[g].w};
 #pragma unroll
                 for (int e = 0; e < 4; e++) {
-                    const float2 y = p.bf16 ? __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&u[e]))
-                                            : __half22float2(*reinterpret_cast<const __half2*>(&u[e]));
+                    const float2 y = kFine ? __half22float2(*reinterpret_cast<const __half2*>(&u[e]))
+                                           : __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&u[e]));
                     f[g][2 * e] = y.x;
                     f[g][2 * e + 1] = y.y;
                     top = fmaxf(top, fmaxf(fabsf(y.x), fabsf(y.y)));
@@ -488,20 +501,17 @@ __global__ void __launch_bounds__(kThreads, kCtas<D, NT>) lm_step_q4_kernel(cons
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
             const int lift = q4_query_lift(top);
-            const float m = __int_as_float((127 + lift) << 23);
+            const float m = __int_as_float((127 + lift) << 23), m16 = m * 0.0625f;
             float mine = 0.f;
 #pragma unroll
             for (int g = 0; g < G; g++) {
-                float sum = 0.f;
 #pragma unroll
-                for (int e = 0; e < 8; e++) {
-                    f[g][e] *= m;
-                    sum += f[g][e];
-                }
+                for (int e = 0; e < 8; e++) f[g][e] *= e & 1 ? m16 : m;
+                float sum = fmaf(16.f, (f[g][1] + f[g][3]) + (f[g][5] + f[g][7]), (f[g][0] + f[g][2]) + (f[g][4] + f[g][6]));
                 qf[x][g][0] = pack(f[g][0], f[g][4]);
                 qf[x][g][1] = pack(f[g][2], f[g][6]);
-                qf[x][g][2] = pack(f[g][1] * 0.0625f, f[g][5] * 0.0625f);
-                qf[x][g][3] = pack(f[g][3] * 0.0625f, f[g][7] * 0.0625f);
+                qf[x][g][2] = pack(f[g][1], f[g][5]);
+                qf[x][g][3] = pack(f[g][3], f[g][7]);
                 sum += __shfl_xor_sync(0xffffffffu, sum, 1);
                 sum += __shfl_xor_sync(0xffffffffu, sum, 2);
                 if (g == t) mine = sum;
@@ -638,6 +648,7 @@ __global__ void __launch_bounds__(kThreads, kCtas<D, NT>) lm_step_q4_kernel(cons
                                     bias[x][h] = now;
                                     most[x][h] = m + kSlack / cf[x][h];
                                 }
+                                if (here == 0) continue;        // nothing is summed yet
                                 l[x][h] *= f;
 #pragma unroll
                                 for (int g = 0; g < G; g++)
@@ -714,13 +725,15 @@ __global__ void __launch_bounds__(kThreads, kCtas<D, NT>) lm_step_q4_kernel(cons
                 const int2 col = column(was, 8 * x + c0 + h);
                 const int b = col.x, head = was.y * p.sh.group + col.y;
                 const bool there = col.y < p.sh.group, none = keys == 0;
-                const float inv = none ? 0.f : 1.f / sum, lse = none ? -INFINITY : (log2f(sum) - bias[x][h]) * 0.6931471805599453f;
+                // (both to 2^-22: the sum is 2^-9 at least)
+                const float inv = none ? 0.f : reciprocal(sum), lse = none ? -INFINITY : (log2_fast(sum) - bias[x][h]) * 0.6931471805599453f;
+                const float inv24 = inv * 0x1p24f, inv20 = inv * 0x1p20f;
                 const long long at = ((long long)b * (p.max_splits + 1) + (was.z & 0xffff)) * p.sh.hq + head;
 #pragma unroll
                 for (int g = 0; g < G; g++) {
-                    const float add = __shfl_sync(0xffffffffu, low[x][h], g * 4 + t);
-                    const float4 v = make_float4(fmaf(acc[x][g][0][h], 0x1p24f, add) * inv, fmaf(acc[x][g][0][2 + h], 0x1p20f, add) * inv,
-                                                 fmaf(acc[x][g][1][h], 0x1p24f, add) * inv, fmaf(acc[x][g][1][2 + h], 0x1p20f, add) * inv);
+                    const float add = __shfl_sync(0xffffffffu, low[x][h], g * 4 + t) * inv;
+                    const float4 v = make_float4(fmaf(acc[x][g][0][h], inv24, add), fmaf(acc[x][g][0][2 + h], inv20, add),
+                                                 fmaf(acc[x][g][1][h], inv24, add), fmaf(acc[x][g][1][2 + h], inv20, add));
                     if (!there) continue;
                     if (alone) {
                         uint16_t* row = static_cast<uint16_t*>(p.o) + b * p.os + (long long)head * D + g * 32 + r * 4;
