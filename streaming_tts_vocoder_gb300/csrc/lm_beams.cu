@@ -193,7 +193,8 @@ __global__ void __launch_bounds__(kRowThreads, 8) lm_beam_rows_kernel(const LmBe
             const int v0 = c * kChunk + lane * V::N;
             // the warp's next chunk to L2: a line of 128 bytes a lane
             if (c + kRowWarps < last)
-                asm volatile("prefetch.global.L2 [%0];" ::"l"(base + min((c + kRowWarps) * kChunk + lane * (128 / (int)sizeof(T)), end - 1)));
+                asm volatile("prefetch.global.L2 [%0];" ::"l"(
+                    base + min((c + kRowWarps) * kChunk + lane * (128 / (int)sizeof(T)), end - 1)));
             uint4 raw[kVectors];
             if (c * kChunk >= lead && (c + 1) * kChunk <= end) {
 #pragma unroll
@@ -615,8 +616,8 @@ cudaError_t launch(const LmBeamArgs& a, cudaStream_t s)
     const int parts = (int)std::max<long long>(1, std::min<long long>({152 * 8 / rows, chunks / kRowWarps, kLists / a.beams}));
     const cudaError_t e = launch_pdl(lm_beam_rows_kernel<T>, dim3(rows, parts), dim3(kRowThreads), 0, s, a);
     if (e != cudaSuccess) return e;
-    return launch_pdl(lm_beam_pick_kernel<T>, dim3(a.groups), dim3(kThreads), (sizeof(unsigned long long) + sizeof(int)) * a.beams * parts * a.beams, s, a,
-                      parts);
+    const size_t smem = (sizeof(unsigned long long) + sizeof(int)) * a.beams * parts * a.beams;
+    return launch_pdl(lm_beam_pick_kernel<T>, dim3(a.groups), dim3(kThreads), smem, s, a, parts);
 }
 
 template <typename T>

@@ -667,8 +667,10 @@ __global__ void __launch_bounds__(kThreads, kCtas<D, NT>) lm_step_q4_kernel(cons
                         lds<G, kOff + 4 * D>(kt + v_at, vb);
 #pragma unroll
                         for (int x = 0; x < NT; x++) {
-                            const float p0 = exp2_fast(fmaf(s[i][x][0], cf[x][0], bias[x][0])), p1 = exp2_fast(fmaf(s[i][x][1], cf[x][1], bias[x][1]));
-                            const float p2 = exp2_fast(fmaf(s[i][x][2], cf[x][0], bias[x][0])), p3 = exp2_fast(fmaf(s[i][x][3], cf[x][1], bias[x][1]));
+                            const float p0 = exp2_fast(fmaf(s[i][x][0], cf[x][0], bias[x][0])),
+                                        p1 = exp2_fast(fmaf(s[i][x][1], cf[x][1], bias[x][1]));
+                            const float p2 = exp2_fast(fmaf(s[i][x][2], cf[x][0], bias[x][0])),
+                                        p3 = exp2_fast(fmaf(s[i][x][3], cf[x][1], bias[x][1]));
                             l[x][0] += p0 + p2;
                             l[x][1] += p1 + p3;
                             f0[x] = pack(p0, p1);
@@ -692,7 +694,8 @@ __global__ void __launch_bounds__(kThreads, kCtas<D, NT>) lm_step_q4_kernel(cons
                                 mma(acc[x][g][0], a0, a1, b0, b1, g0, g1);
                                 mma(acc[x][g][1], a2, a3, b2, b3, g0, g1);
                                 if constexpr (kFine) {
-                                    const uint32_t h0 = times_left(f0[x], e0[x], sc[i][2 * g], g0), h1 = times_left(f1[x], e1[x], sc[i][2 * g + 1], g1);
+                                    const uint32_t h0 = times_left(f0[x], e0[x], sc[i][2 * g], g0),
+                                                   h1 = times_left(f1[x], e1[x], sc[i][2 * g + 1], g1);
                                     mma(acc[x][g][0], a0, a1, b0, b1, h0, h1);
                                     mma(acc[x][g][1], a2, a3, b2, b3, h0, h1);
                                 }
@@ -726,7 +729,8 @@ __global__ void __launch_bounds__(kThreads, kCtas<D, NT>) lm_step_q4_kernel(cons
                 const int b = col.x, head = was.y * p.sh.group + col.y;
                 const bool there = col.y < p.sh.group, none = keys == 0;
                 // (both to 2^-22: the sum is 2^-9 at least)
-                const float inv = none ? 0.f : reciprocal(sum), lse = none ? -INFINITY : (log2_fast(sum) - bias[x][h]) * 0.6931471805599453f;
+                const float inv = none ? 0.f : reciprocal(sum),
+                            lse = none ? -INFINITY : (log2_fast(sum) - bias[x][h]) * 0.6931471805599453f;
                 const float inv24 = inv * 0x1p24f, inv20 = inv * 0x1p20f;
                 const long long at = ((long long)b * (p.max_splits + 1) + (was.z & 0xffff)) * p.sh.hq + head;
 #pragma unroll

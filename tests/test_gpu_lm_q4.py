@@ -704,7 +704,8 @@ def logits(seed, rows, vocab, dt, spread=2.5, pad=0, at=0):
 @pytest.mark.parametrize("groups,k,vocab,dt,pad,at", [
     (1, 1, 2, "fp32", 0, 0), (3, 2, 5, "bf16", 3, 1), (2, 4, 33, "fp16", 0, 0), (4, 4, 2048, "fp32", 0, 0),
     (3, 8, 2047, "bf16", 0, 0), (2, 32, 1025, "fp16", 7, 3), (1, 32, 70001, "bf16", 0, 0), (5, 5, 4099, "fp32", 1, 1),
-    (70, 4, 513, "bf16", 0, 0), (1, 1, 1000003, "fp32", 1, 1), (128, 32, 40, "fp16", 0, 0), (40, 32, 3001, "bf16", 1, 0), (2, 3, 131072, "fp16", 0, 0), (1, 17, 9000, "fp32", 0, 0), (1, 4, 1000003, "bf16", 0, 0),
+    (70, 4, 513, "bf16", 0, 0), (1, 1, 1000003, "fp32", 1, 1), (128, 32, 40, "fp16", 0, 0),
+    (40, 32, 3001, "bf16", 1, 0), (2, 3, 131072, "fp16", 0, 0), (1, 17, 9000, "fp32", 0, 0), (1, 4, 1000003, "bf16", 0, 0),
 ])
 def test_beams(groups, k, vocab, dt, pad, at):
     rows = groups * k
