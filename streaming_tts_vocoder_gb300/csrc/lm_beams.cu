@@ -12,9 +12,10 @@
 // alone for each candidate, as whole numbers of the same order (three reductions).
 //
 // What decides between rows is the logarithm, and sums of exponentials in fp32
-// are off by up to kNear.  Where two neighbours of the result (or the last and
-// the first left out) come from different rows and lie closer, the logarithms
-// of those rows are worked out again to about 1e-9, and the choice is made once more.
+// are off by up to kNear.  Where two neighbours of the result come from different
+// rows and lie closer, or the last one and any candidate of another row do, the
+// logarithms of those rows are worked out again to about 1e-9, and the choice is made
+// once more.
 //
 // 1,024 rows of 65,537 in bf16 (60 of them ended): 37.6 us, 3.4 TB/s; 30 of it before the
 // search.  Neither the memory nor the issue slots bound it: a chunk's loads, maxima and
@@ -440,6 +441,17 @@ __device__ double exact_log_sum(const T* x, int n, float top, const float2* tabl
     return log_of(sum, table);
 }
 
+// A score as a whole number of the same order, and back.
+__device__ __forceinline__ unsigned long long key_of(double s)
+{
+    const long long bits = __double_as_longlong(s);
+    return bits < 0 ? ~(unsigned long long)bits : (unsigned long long)bits | 1ULL << 63;
+}
+__device__ __forceinline__ double score_of(unsigned long long key)
+{
+    return __longlong_as_double((long long)(key >> 63 ? key & ~(1ULL << 63) : ~key));
+}
+
 // One group.  Dynamic shared memory: the lists' scores as whole numbers of the same
 // order and their indexes (row of the group, token), [K x parts][K] each.
 template <typename T>
@@ -528,8 +540,7 @@ __global__ void __launch_bounds__(kThreads) lm_beam_pick_kernel(const LmBeamArgs
                 s = base[r];
                 i = r * a.vocab + max(a.end_token, 0);
             }
-            const long long bits = __double_as_longlong(s);
-            keys[e] = bits < 0 ? ~(unsigned long long)bits : (unsigned long long)bits | 1ULL << 63;
+            keys[e] = key_of(s);
             index[e] = i;
         }
         __syncthreads();
@@ -565,8 +576,7 @@ __global__ void __launch_bounds__(kThreads) lm_beam_pick_kernel(const LmBeamArgs
                 const unsigned top_lo = __reduce_max_sync(0xffffffffu, best_i != INT_MAX && hi == top_hi ? lo : 0u);
                 const int winner = __reduce_min_sync(0xffffffffu, hi == top_hi && lo == top_lo ? best_i : INT_MAX);
                 if (lane == 0) {
-                    const unsigned long long key = (unsigned long long)top_hi << 32 | top_lo;
-                    got[k] = __longlong_as_double((long long)(key >> 63 ? key & ~(1ULL << 63) : ~key));
+                    got[k] = score_of((unsigned long long)top_hi << 32 | top_lo);
                     got_i[k] = winner;
                 }
                 if (winner != INT_MAX && best_i == winner) {
@@ -583,15 +593,17 @@ __global__ void __launch_bounds__(kThreads) lm_beam_pick_kernel(const LmBeamArgs
             const int p = got_i[tid] / a.vocab, q = got_i[tid + 1] / a.vocab;
             if (p != q && got[tid] - got[tid + 1] < kNear) atomicOr(&again, 1u << p | 1u << q);
         }
-        __syncthreads();
-        if (again == 0) break;
-        // and all that lie as near to the last one
-        for (int e = tid; e < lists * K; e += kThreads) {
-            const int row = e / K / parts;
-            if (kind[row] == 1 && fabs(base[row] + ((double)__uint_as_float(__ldcg(best + e).x) - (double)top[row]) - got[K - 1]) < kNear)
-                atomicOr(&again, 1u << row);
+        // and other rows' that lie as near to the last one: what comes first behind it may be its own row's
+        if (got_i[K - 1] != INT_MAX) {
+            const int p = got_i[K - 1] / a.vocab;
+            const double cut = got[K - 1];
+            for (int e = tid; e < lists * K; e += kThreads) {
+                const int q = e / K / parts;
+                if (index[e] != INT_MAX && q != p && fabs(score_of(keys[e]) - cut) < kNear) atomicOr(&again, 1u << p | 1u << q);
+            }
         }
         __syncthreads();
+        if (again == 0) break;
         work_out(again);
     }
     if (tid < K) {

@@ -1,0 +1,84 @@
+"""Corners of the 4-bit cache and of the selection: candidates closer than 32 bits tell
+where a list ends, values past fp16's largest, values far below one, parts without
+weight, nothing to copy, and what an object allocates."""
+from __future__ import annotations
+
+import numpy as np
+import pytest
+import torch
+
+import lm_q4_ref as Q
+from streaming_tts_vocoder_gb300 import codec as C
+from test_gpu_lm_q4 import cache_q4, check_beams, f64, gpu, i32, logits, step_reference
+
+pytestmark = pytest.mark.gpu
+T = Q.DTYPES
+
+
+# ---- selection --------------------------------------------------------------
+
+def log_sums(x):
+    return torch.logsumexp(x.double(), 1).numpy()
+
+
+def test_beams_one_rows_candidates_at_the_cut():
+    """The last one chosen and the first left out are of one row, and another row's
+    candidate lies 3e-8 to 2e-7 before or behind them."""
+    k, vocab = 3, 5000
+    rng = np.random.default_rng(0)
+    for trial in range(60):
+        x = torch.from_numpy(rng.normal(size=(k, vocab)) * 2).float()
+        x[2, 40] = 30.0                                     # first by far
+        x[1, [5, 100, 2000, 4000]] = 14.0
+        x[0, [17, 1000, 1001, 1002]] = torch.tensor([14.0, 13.5, 13.5, 13.5])
+        for _ in range(20):
+            lse = log_sums(x)
+            x[0, 17] = float(14.0 - lse[1] + lse[0])
+        lse = log_sums(x)
+        off = rng.choice([-1, 1]) * rng.uniform(3e-8, 2e-7)
+        assert abs((14.0 - lse[1]) - (float(x[0, 17]) - lse[0])) < 1e-5
+        sums = [np.float32((14.0 - lse[1]) - (float(x[0, 17]) - lse[0]) + off), 0.0, 0.0]
+        got = check_beams(x.cuda(), k, sums, [0] * k, 3)
+        assert got[1] == ([2, 0, 1] if off > 0 else [2, 1, 1])
+        got = check_beams(x.flip(0).cuda(), k, sums[::-1], [0] * k, 3)
+        assert got[1] == ([0, 2, 1] if off > 0 else [0, 1, 1])
+
+
+@pytest.mark.parametrize("dt,vocab", [("fp32", 9001), ("bf16", 9001), ("fp16", 2049), ("fp32", 300)])
+@pytest.mark.parametrize("k", [2, 5, 32])
+def test_beams_rows_of_one_value(dt, vocab, k):
+    """All beams alike, all logits one constant: the first beam's first tokens."""
+    for c in np.random.default_rng(vocab + k).normal(size=24) * 4:
+        x = torch.full((k, vocab), c, dtype=T[dt], device="cuda")
+        got = check_beams(x, k, [0.0] * k, [0] * k, -1)
+        assert got[1] == [0] * k and got[2] == list(range(k))
+
+
+@pytest.mark.parametrize("dt,vocab", [("fp32", 5000), ("bf16", 9001), ("fp32", 301)])
+@pytest.mark.parametrize("k", [2, 3, 8])
+def test_beams_many_candidates_closer_than_32_bits_tell(dt, vocab, k):
+    """Rows of a few different logits whose best are a rounding of the sums apart, some
+    of them many times; an ended beam among them."""
+    rng = np.random.default_rng(vocab + k)
+    groups = 12
+    x = torch.from_numpy(rng.integers(-6, 3, size=(groups * k, vocab)) * 0.5).to(T[dt])
+    for r in range(groups * k):
+        x[r, torch.from_numpy(rng.permutation(vocab)[:rng.integers(1, 5)])] = 9.0
+    lse = log_sums(x)
+    sums, best = np.zeros(groups * k, np.float32), np.zeros(groups * k)
+    for r in rng.permutation(groups * k):               # steps of 32 bits away from the others of its group
+        mates = [i for i in range(r // k * k, r // k * k + k) if best[i] != 0.0] + [r // k * k]
+        for step in rng.permutation(np.arange(-4, 5)):
+            sums[r] = np.float32(lse[r] - 12.0)
+            sums[r] += step * np.spacing(sums[r])
+            best[r] = float(sums[r]) + 9.0 - lse[r]
+            if all(abs(best[r] - best[i]) > 2e-8 for i in mates if i != r):
+                break
+        else:
+            raise AssertionError("no room")
+    ended = [0] * (groups * k)
+    check_beams(x.cuda(), k, sums, ended, 3)
+    ended[k] = 1                                        # itself alone, as near
+    sums[k] = next(c for c in np.float32(-3.0) + np.arange(9) * np.spacing(np.float32(3.0))
+                   if np.abs(best[k + 1:2 * k] - c).min() > 2e-8)
+    check_beams(x.cuda(), k, sums, ended, 3)
