@@ -33,9 +33,14 @@ namespace codec {
 namespace {
 
 constexpr int kThreads = 256;
-// A row's logarithm is off by 2^-22 at most for ex2, 2^-24 for each of 16 additions
-// and of the product with log2 e (times up to 20); of either sign, they come to 1e-7.
-constexpr float kNear = 2e-6f;
+// A row's logarithm is off by 2.1e-6 at most, and two rows' difference by twice that; the
+// terms have one sign where few different logits fill a row, so they are added as they
+// are.  Relative to the sum: the exponent's argument rounded once, 2^-20 ln 2 where it
+// lies in 16 .. 32 below the largest (what lies further has no weight: 2^24 tokens), 6.6e-7;
+// log2 e as a float, 1.33e-8 times the 17 that such a logit lies below, 2.2e-7; ex2 2^-22,
+// 2.4e-7; up to 15 additions to one number and two that join those, 2^-24 each, 1.0e-6.
+// The rest is kept or fp64.
+constexpr float kNear = 5e-6f;
 // A row whose largest logit is as far from zero (one masked by its type's lowest value
 // from end to end) has its logarithm worked out from the differences to that one: the
 // powers' whole numbers would not hold it.

@@ -82,3 +82,16 @@ def test_beams_many_candidates_closer_than_32_bits_tell(dt, vocab, k):
     sums[k] = next(c for c in np.float32(-3.0) + np.arange(9) * np.spacing(np.float32(3.0))
                    if np.abs(best[k + 1:2 * k] - c).min() > 2e-8)
     check_beams(x.cuda(), k, sums, ended, 3)
+
+
+@pytest.mark.parametrize("dt,vocab", [("fp32", 9001), ("bf16", 9001), ("fp16", 2049), ("fp32", 300), ("fp32", 130001)])
+@pytest.mark.parametrize("k", [2, 5, 32])
+def test_beams_rows_of_a_value_each(dt, vocab, k):
+    """Rows of a constant of their own, whose roundings are all of one sign, and sums 3e-8
+    to 5e-6 apart: the best sum's tokens."""
+    rng = np.random.default_rng(vocab + k)
+    for trial in range(12):
+        x = torch.from_numpy(rng.normal(size=(k, 1)) * 4).to(T[dt]).expand(k, vocab).contiguous().cuda()
+        sums = rng.permutation((3e-8 + rng.random() * (5e-6 / k - 3e-8)) * np.arange(1, k + 1)).astype(np.float32)
+        got = check_beams(x, k, sums, [0] * k, -1)
+        assert got[1] == [int(sums.argmax())] * k and got[2] == list(range(k))
