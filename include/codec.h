@@ -891,7 +891,9 @@ CODEC_API codec_status codec_lm_step_q4(codec_lm_t* lm, const void* q, int64_t q
  * itself alone, with end_token and the sum it has.  Each group's best `beams`
  * candidates become its rows, best first; of equal ones the lower beam's, then
  * the lower token.  Candidates are compared as 64-bit arithmetic finds them
- * (within 1e-8), whatever their type.
+ * (within 1e-8), whatever their type.  That takes longer where beams lie closer than
+ * 32 bits tell, above all where several of a group are alike (8 of 65,537 logits 0.28 ms
+ * instead of 0.02): begin a search with one finite sum a group, the others -inf.
  *   sums_out float, parents (a row), tokens, ended_out (1: the token is
  *              end_token) int32 [rows].  A row that no candidate is left for:
  *              sum -inf, parent -1, token -1, ended 1.

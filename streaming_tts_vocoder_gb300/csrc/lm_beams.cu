@@ -24,6 +24,12 @@
 // chunks ahead (+1.5 us), six CTAs an SM (two waves, 54 us), ten (48), twice as many parts
 // of a row (43) were slower.  4 x 4 of 2,048: 9.4 us, two launches and the second one's
 // chain of steps.
+//
+// Logarithms that are worked out again are a CTA's for each group, a row after the other:
+// 35 us each for 65,537 logits in bf16.  Beams with the same logits and sums always need
+// it (8 of them 282 us where 8 of their own take 16, 32 1,134 and 71; 128 x 8 571 and 38;
+// 4 x 4 of 2,048 25 and 10), and so do rows masked from end to end (8 304); a search that
+// begins with one beam whose sum is finite, and the others' at -inf, does not.
 #include <climits>
 
 #include "lm.h"
@@ -609,7 +615,7 @@ __global__ void __launch_bounds__(kThreads) lm_beam_pick_kernel(const LmBeamArgs
         }
         __syncthreads();
         if (again == 0) break;
-        work_out(again);
+        work_out(again & ~far);                 // (those far from zero are done)
     }
     if (tid < K) {
         const int c = got_i[tid], row = row0 + tid;
