@@ -70,9 +70,13 @@ __device__ __forceinline__ float max_nan(float a, float b, float c)
 }
 
 // Codes of 8 values, four lanes a group.  The steps and their roundings are the
-// format's: no contraction, no approximate reciprocal.  A value beyond +-65504 needs
-// no cut of its own (its code is 0 or 15 as that one's is), and what is not finite
-// shows in the least and the largest.
+// format's: no contraction, no approximate reciprocal.  A value below -65504 needs no cut
+// of its own: low is -65504 then and its code 0 as that one's is.  One above 65504 gets no
+// code above that one's, as the steps keep the order (low may have been rounded up to
+// near it, and then that is not 15).  kPast: inputs that may lie there and need it,
+// fp32; bf16's least value of such a group is a half already, and fp16 has none.
+// What is not finite shows in the least and the largest.
+template <bool kPast>
 __device__ __forceinline__ uint32_t encode(const float* x, __half& scale, __half& low)
 {
     float lo = min_nan(min_nan(x[0], x[1], x[2]), min_nan(x[3], x[4], x[5]), min_nan(x[6], x[6], x[7]));
@@ -89,7 +93,8 @@ __device__ __forceinline__ uint32_t encode(const float* x, __half& scale, __half
     low = __float2half_rn(lo);
     const float s = __half2float(scale), l = __half2float(low);
     const float inv = __frcp_rn(s);
-    // a number of 0 .. 15 and 1.5 x 2^23 is rounded to a whole one, which then stands in
+    const float most = kPast ? fminf(__fmul_rn(__fsub_rn(65504.f, l), inv), 15.f) : 15.f;
+    // a number of 0 .. 15 plus 1.5 x 2^23 is rounded to a whole one, which then stands in
     // the last bits; what the others' bits add to the word is taken off at the end
     constexpr float kWhole = 12582912.f;
     const float2 minus = make_float2(-l, -l), by = make_float2(inv, inv), whole = make_float2(kWhole, kWhole);
@@ -97,7 +102,7 @@ __device__ __forceinline__ uint32_t encode(const float* x, __half& scale, __half
 #pragma unroll
     for (int i = 0; i < 8; i += 2) {
         float2 c = __fmul2_rn(__fadd2_rn(make_float2(x[i], x[i + 1]), minus), by);
-        c = __fadd2_rn(make_float2(fminf(fmaxf(c.x, 0.f), 15.f), fminf(fmaxf(c.y, 0.f), 15.f)), whole);
+        c = __fadd2_rn(make_float2(fminf(fmaxf(c.x, 0.f), most), fminf(fmaxf(c.y, 0.f), most)), whole);
         word += __float_as_uint(c.x) << (4 * i);
         word += __float_as_uint(c.y) << (4 * i + 4);
         rest += (0x4b400000u << (4 * i)) + (0x4b400000u << (4 * i + 4));
@@ -154,7 +159,7 @@ __global__ void __launch_bounds__(kThreads) lm_store_q4_kernel(const StoreArgs a
             float x[8];
             raw[u].get(x);
             __half scale, low;
-            const uint32_t word = encode(x, scale, low);
+            const uint32_t word = encode<sizeof(TI) == 4>(x, scale, low);
             if (h >= a.hk) continue;
             uint8_t* tile = base + h * head_bytes;
             if (!values) {

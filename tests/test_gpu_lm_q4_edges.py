@@ -95,3 +95,32 @@ def test_beams_rows_of_a_value_each(dt, vocab, k):
         sums = rng.permutation((3e-8 + rng.random() * (5e-6 / k - 3e-8)) * np.arange(1, k + 1)).astype(np.float32)
         got = check_beams(x, k, sums, [0] * k, -1)
         assert got[1] == [int(sums.argmax())] * k and got[2] == list(range(k))
+
+
+# ---- store ------------------------------------------------------------------
+
+@pytest.mark.parametrize("hk,d,dt", [(3, 128, "bf16"), (2, 64, "fp16")])
+def test_store_groups_past_the_largest_half(hk, d, dt):
+    """fp32 groups whose values lie around 65,504 on both sides of it, of either sign,
+    and far beyond: to the byte."""
+    rows, bs = 60, 16
+    rng = np.random.default_rng(d)
+    both = []
+    for _ in range(2):
+        x = rng.uniform(65300, 65503, size=(rows, hk, d // 32, 32))
+        x[:, :, :, ::3] = rng.uniform(65504, 66000, size=x[:, :, :, ::3].shape)
+        x[::4, :, :, 7] = 10.0 ** rng.uniform(4.9, 38, size=x[::4, :, :, 7].shape)
+        x[1::4, :, 0, :31], x[1::4, :, 0, 31] = 65490, 70000
+        x[2::4, :, 0, 1:], x[2::4, :, 0, 0] = 65400, 70000
+        x[3::4, :, 0, 5] = -7e4
+        x[rows // 2:] *= np.where(rng.random((rows - rows // 2, hk, 1, 1)) < 0.5, -1, 1)
+        both.append(x.reshape(rows, hk, d).astype(np.float32))
+    lm = C.Lm(hk, hk, d, dt, block_size=bs, n_blocks=4, max_rows=rows)
+    slots = rng.permutation(4 * bs)[:rows]
+    caches = [torch.zeros(4, hk, bs * d * 5 // 8, dtype=torch.uint8, device="cuda") for _ in range(2)]
+    lm.store_q4(*(gpu(x) for x in both), i32(slots.tolist()), *caches)
+    assert lm.errors() == 0
+    for x, c, keys in zip(both, caches, (True, False)):
+        want = np.zeros(c.shape, np.uint8)
+        Q.store(want, x, slots, bs, keys)
+        assert np.array_equal(c.cpu().numpy(), want)
