@@ -26,7 +26,8 @@
 //
 // Roundings: queries to halves after the power of two (exact but for elements below
 // 2^-24 of the head's largest); probabilities, and these times a scale, to halves, by
-// 2^-11, where results are bf16, and to two halves, by 2^-21, where they are fp16.
+// 2^-11, where results are bf16, and to two halves, by 2^-21, where they are fp16; both no
+// finer than halves' smallest step lets them (see kSmall).
 //
 // What bounds it: instructions and their latency, not the memory.  A tile of 16 keys and
 // values of 128 takes 252 instructions (80 make operands of codes, 18 are MMAs), a unit
@@ -59,6 +60,12 @@ template <int D, int NT> constexpr int kCtas = D == 128 && NT == 2 ? 2 : 3;    /
 // passes it by more than kSlack (both log2), so that a probability times a scale
 // below 2 stays below 2^15.
 constexpr float kLift = 6.f, kSlack = 8.f;
+// Halves' steps do not get finer below 2^-14, so where a split's scales all lie below
+// 2^(kSmall - 15) they are taken times the power of two that brings the largest to 1 .. 2
+// (2^15 at most, a multiplication without rounding).  A probability is off by 2^-31 of the
+// row's largest at most, its product with a scale by 2^-31 of the largest's with the
+// split's largest scale, 2^-25 with scales at that border.
+constexpr int kSmall = 9;
 
 struct Params {
     LmShape sh;
@@ -523,7 +530,9 @@ __global__ void __launch_bounds__(kThreads, kCtas<D, NT>) lm_step_q4_kernel(cons
             cf[x][0] = __shfl_sync(0xffffffffu, back, c0 * 4);
             cf[x][1] = __shfl_sync(0xffffffffu, back, c0 * 4 + 4);
         }
-        int grown = 0;                          // scales are below 2^(1 + grown)
+        // Scales are below 2^(1 + grown).  Beyond 0 the reference is lowered by it; below 0
+        // scales are taken times 2^-grown.
+        int grown = -15;
 #pragma unroll 1
         for (int at = 0; at == 0 || at < keys; at += kKeys) {
             if (at > 0) {
@@ -627,9 +636,12 @@ __global__ void __launch_bounds__(kThreads, kCtas<D, NT>) lm_step_q4_kernel(cons
                                 const int lo = sc[i][g] >> 10 & 31, hi = sc[i][g] >> 26 & 31;
                                 e = max(e, max(lo == 31 ? 0 : lo, hi == 31 ? 0 : hi));
                             }
-                        const int more = max(0, (int)__reduce_max_sync(0xffffffffu, e) - 15 - grown);
-                        grown += more;
+                        e = (int)__reduce_max_sync(0xffffffffu, e);
+                        const int to = max(grown, e >= kSmall ? max(e - 15, 0) : e - 15);
+                        const int more = max(to, 0) - max(grown, 0);
                         const float shrink = __int_as_float((127 - more) << 23);
+                        const float less = __int_as_float((127 + more - (to - grown)) << 23);   // of the scales
+                        grown = to;
                         // a column's reference moves for its own scores alone (times 1 changes nothing)
 #pragma unroll
                         for (int x = 0; x < NT; x++)
@@ -643,13 +655,15 @@ __global__ void __launch_bounds__(kThreads, kCtas<D, NT>) lm_step_q4_kernel(cons
                                 float f = shrink;
                                 bias[x][h] -= (float)more;
                                 if (m > most[x][h]) {
-                                    const float now = fmaf(-m, cf[x][h], kLift - (float)grown);
+                                    const float now = fmaf(-m, cf[x][h], kLift - (float)max(grown, 0));
                                     f = most[x][h] == -INFINITY ? 0.f : shrink * exp2_fast(now - bias[x][h]);
                                     bias[x][h] = now;
                                     most[x][h] = m + kSlack / cf[x][h];
                                 }
                                 if (here == 0) continue;        // nothing is summed yet
                                 l[x][h] *= f;
+                                low[x][h] *= f;
+                                f *= less;
 #pragma unroll
                                 for (int g = 0; g < G; g++)
 #pragma unroll
@@ -657,8 +671,14 @@ __global__ void __launch_bounds__(kThreads, kCtas<D, NT>) lm_step_q4_kernel(cons
                                         acc[x][g][i][h] *= f;
                                         acc[x][g][i][2 + h] *= f;
                                     }
-                                low[x][h] *= f;
                             }
+                    }
+                    if (grown < 0) {
+                        const uint32_t up = (uint32_t)(15 - grown) * 0x04000400u;
+#pragma unroll
+                        for (int i = 0; i < kAt; i++)
+#pragma unroll
+                            for (int g = 0; g < 2 * G; g++) sc[i][g] = times(sc[i][g], up);
                     }
                     each<kAt>([&](auto I) {
                         constexpr int i = I, kOff = (kTiles + i) * kTile;
@@ -731,7 +751,8 @@ __global__ void __launch_bounds__(kThreads, kCtas<D, NT>) lm_step_q4_kernel(cons
                 // (both to 2^-22: the sum is 2^-9 at least)
                 const float inv = none ? 0.f : reciprocal(sum),
                             lse = none ? -INFINITY : (log2_fast(sum) - bias[x][h]) * 0.6931471805599453f;
-                const float inv24 = inv * 0x1p24f, inv20 = inv * 0x1p20f;
+                const float down = inv * __int_as_float((127 + min(grown, 0)) << 23);
+                const float inv24 = down * 0x1p24f, inv20 = down * 0x1p20f;
                 const long long at = ((long long)b * (p.max_splits + 1) + (was.z & 0xffff)) * p.sh.hq + head;
 #pragma unroll
                 for (int g = 0; g < G; g++) {

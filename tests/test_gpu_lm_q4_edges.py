@@ -124,3 +124,53 @@ def test_store_groups_past_the_largest_half(hk, d, dt):
         want = np.zeros(c.shape, np.uint8)
         Q.store(want, x, slots, bs, keys)
         assert np.array_equal(c.cpu().numpy(), want)
+
+
+# ---- single tokens ----------------------------------------------------------
+
+def near(got, ref, dt, d, low, scale):
+    """Elementwise.  As Q.assert_step, but with what is held in fixed steps relative to the
+    values.  A split's largest probability is 2^6 at least, 2^6 / scale where its largest
+    step `scale` passes 1, and halves' steps are 2^-24: a probability is off by 2^-31 of the
+    largest, twice where it is two halves, times the largest `low`.  Its product with a step
+    is taken times the power of two that brings the split's largest below 2 where that lies
+    below 2^-6 (2^15 at most), and off by 2^-31 over that, three times (a rounding each of
+    the product, of what it leaves off, of their sum), times a code of 15."""
+    o, _, al, ac, s, n = ref
+    half = torch.finfo(T[dt]).eps / 2
+    ds = (4 * d * 2.0 ** -23 * (s + 1))[..., None]
+    n = n[:, None, None]
+    fine = dt == "fp16"
+    tol = half * np.abs(o) * 1.01 + (al * 2.0 ** -11 + ac * 2.0 ** -10) * (2.0 ** -10 if fine else 1.01)
+    tol = tol + (al + ac) * (2 * ds + (n / (4 if fine else 8) + 16) * 2.0 ** -23)
+    unit = max(scale, 2.0 ** -15) if scale < 2.0 ** -6 else max(scale, 1.0)
+    tol = tol + n * 2.0 ** -31 * (2 * low * max(scale, 1.0) + 3 * 15 * unit) + 2.0 ** -25 * fine
+    off = np.abs(f64(got) - o) / tol
+    worst = off.max()
+    assert worst <= 1, f"{worst:.3g} x the bound"
+
+
+@pytest.mark.parametrize("dt", ["fp16", "bf16"])
+@pytest.mark.parametrize("size", [3e-6, 1e-5, 1e-4, 1e-3, 0.03, 1.0, 200.0])
+@pytest.mark.parametrize("sh,most", [(0, 1), (60, 2)])
+def test_step_values_far_below_one(dt, size, sh, most):
+    """One key at the reference and, in the same split, 7,680 to 8,000 that lie 9 nats
+    below and weigh as much: values of any size come out as close, relative to them."""
+    hk, d, bs, n, width = 2, 64, 128, 8001, 4100         # splits of 8,192 positions
+    gen = torch.Generator(device="cuda").manual_seed(1)
+    r = lambda *s: torch.randn(*s, generator=gen, device="cuda")
+    lm = C.Lm(hk, hk, d, dt, block_size=bs, n_blocks=70, table_blocks=width, max_requests=most, max_rows=n)
+    kc, vc = (torch.full((70, hk, bs * d * 5 // 8), 255, dtype=torch.uint8, device="cuda") for _ in range(2))
+    ids = torch.randperm(70, generator=gen, device="cuda")[:63].int()
+    pos = torch.arange(n, device="cuda")
+    q = r(1, hk, d).to(T[dt])
+    k, v = r(n, hk, d) * 0.02, r(n, hk, d) * size
+    k[0] += q[0].float() * (9 * d ** 0.5 / q[0].float().square().sum(-1, keepdim=True))
+    lm.store_q4(k, v, (ids[pos // bs] * bs + pos % bs).int(), kc, vc)
+    tables, o = torch.full((1, width), -1, dtype=torch.int32, device="cuda"), torch.zeros_like(q)
+    tables[0, :63] = ids
+    lm.step_q4(q, kc, vc, tables, i32([n]), o, shared_table=ids[:sh].contiguous() if sh else None)
+    assert lm.errors() == 0
+    ref = step_reference(q, kc, vc, tables.tolist(), [n], ids[:sh].tolist(), hk, d, bs)
+    low, rest = (x.reshape(-1, hk, d)[:n] for x in Q.values(vc[ids.long()].cpu().numpy(), bs, d, False, parts=True))
+    near(o, ref, dt, d, np.abs(low).max(), rest.max() / 15)
