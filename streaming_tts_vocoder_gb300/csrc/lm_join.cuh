@@ -9,8 +9,10 @@ namespace codec {
 
 // lse_of(i): a part's lse; part_of(i, x): this lane's columns of a part.
 // empty: the row sees nothing (v = 0, lse = -inf).  kAhead: parts that are read
-// before their weights are known.
-template <int kE, int kAhead, typename Lse, typename Part>
+// before their weights are known.  kValues: every part has finite values or NaN, one
+// without keys zeros, so that one of no weight is added like others (0 times NaN is NaN);
+// else it is left out, whatever it holds.
+template <int kE, int kAhead, bool kValues = false, typename Lse, typename Part>
 __device__ __forceinline__ void join_row(int parts, bool empty, Lse lse_of, Part part_of, float* v, float& lse)
 {
     const int lane = threadIdx.x & 31;
@@ -38,7 +40,7 @@ __device__ __forceinline__ void join_row(int parts, bool empty, Lse lse_of, Part
     auto add = [&](float f, const float* x) {
         sum += f;
 #pragma unroll
-        for (int e = 0; e < kE; e++) v[e] = f != 0.f ? fmaf(f, x[e], v[e]) : v[e];  // a part without keys has no value
+        for (int e = 0; e < kE; e++) v[e] = kValues || f != 0.f ? fmaf(f, x[e], v[e]) : v[e];
     };
 #pragma unroll
     for (int i = 0; i < kAhead; i++) {

@@ -266,7 +266,7 @@ __device__ __forceinline__ void join_parts(const Params& p, int b, int h, int n_
         return i < p.n_pre ? (long long)i * p.B * p.sh.hq + shared_row : (long long)(i - p.n_pre) * p.sh.hq + own_row;
     };
     float v[kE], lse;
-    join_row<kE, kAhead>(
+    join_row<kE, kAhead, true>(
         parts, empty, [&](int i) { return __ldcg((i < p.n_pre ? p.pre_lse : p.part_lse) + row_of(i)); },
         [&](int i, float* x) { row_part<kE>((i < p.n_pre ? p.pre : p.part) + row_of(i) * D, x); }, v, lse);
     uint16_t* row = static_cast<uint16_t*>(p.o) + b * p.os + (long long)h * D;

@@ -174,3 +174,25 @@ def test_step_values_far_below_one(dt, size, sh, most):
     ref = step_reference(q, kc, vc, tables.tolist(), [n], ids[:sh].tolist(), hk, d, bs)
     low, rest = (x.reshape(-1, hk, d)[:n] for x in Q.values(vc[ids.long()].cpu().numpy(), bs, d, False, parts=True))
     near(o, ref, dt, d, np.abs(low).max(), rest.max() / 15)
+
+
+@pytest.mark.parametrize("dt,sh,most", [("bf16", 0, 1), ("fp16", 0, 1), ("fp16", 8, 64), ("bf16", 8, 64), ("bf16", 64, 4096)])
+def test_step_nan_of_no_weight_reaches_its_row(dt, sh, most):
+    """A group that stands for NaN among keys hundreds of nats below the rest, in the same
+    split or in another: 0 times NaN is NaN."""
+    hk, d, bs, n = 1, 64, 16, 64 * 16 + 200
+    for where, heavy in ((3, 67), (3, 4), (100, 164), (700, 5), (700, 701), (n - 1, 5)):
+        lens = [n]
+        kc, vc, tables, shared, n_blocks, width = cache_q4(3, lens, hk, d, bs, sh)
+        lm = C.Lm(hk, hk, d, dt, block_size=bs, n_blocks=n_blocks, table_blocks=width, max_requests=most, max_rows=n)
+        table = i32((shared + tables[0][sh:])[:-(-n // bs)])
+        pos = torch.arange(n, device="cuda")
+        k = torch.full((n, hk, d), -1.5, device="cuda")
+        k[heavy] = 1.5                                      # all the weight: 12 * 64 * 3 / 8 = 288 nats above
+        v = torch.randn(n, hk, d, device="cuda", generator=torch.Generator(device="cuda").manual_seed(2))
+        v[where, 0, 40] = float("nan")                      # group 1
+        lm.store_q4(k, v, (table[pos // bs] * bs + pos % bs).int(), kc, vc)
+        q, o = torch.full((1, hk, d), 12.0, dtype=T[dt], device="cuda"), torch.zeros(1, hk, d, dtype=T[dt], device="cuda")
+        lm.step_q4(q, kc, vc, i32(tables), i32(lens), o, shared_table=i32(shared) if sh else None)
+        assert lm.errors() == 0
+        assert o[0, 0, 32:].isnan().all() and o[0, 0, :32].isfinite().all(), (where, heavy)
