@@ -966,9 +966,10 @@ CODEC_API codec_status codec_lm_compact(codec_lm_t* lm, const int32_t* len, int3
 /*
  * Copies block src[i] to block dst[i], i < min(copies[0], n), in each of n_caches
  * caches (a host array of device pointers; [n_blocks][block_bytes] each, of any
- * type).  src, dst int32 [n], copies int32 [1], device; copies NULL: n.  No block is
- * both source and destination, none twice a destination.  An id out of range is
- * left out and sets CODEC_LM_ERR_BLOCK.
+ * type).  src, dst int32 [n], copies int32 [1], device; copies NULL: n.  n of 0: nothing,
+ * src and dst may be NULL (a pool of one block has no entries).  No block is both
+ * source and destination, none twice a destination.  An id out of range is left out
+ * and sets CODEC_LM_ERR_BLOCK.
  * Errors: CODEC_ERR_NULL, CODEC_ERR_ARG (n < 0, n_caches outside [1, 256], block_bytes
  * not a positive multiple of 16 or above 2^28, a cache not on 16 bytes), CODEC_ERR_CUDA.
  */

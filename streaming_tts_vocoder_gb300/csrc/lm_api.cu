@@ -481,7 +481,7 @@ codec_status codec_lm_compact(codec_lm_t* lm, const int32_t* len, int32_t B, con
 codec_status codec_lm_copy(codec_lm_t* lm, void* const* caches, int32_t n_caches, int64_t block_bytes,
                            const int32_t* src, const int32_t* dst, int32_t n, const int32_t* copies, void* stream)
 {
-    if (!lm || !caches || !src || !dst) return CODEC_ERR_NULL;
+    if (!lm || !caches || (n > 0 && (!src || !dst))) return CODEC_ERR_NULL;
     if (n < 0 || n_caches < 1 || n_caches > kLmMaxCaches || block_bytes < 16 || block_bytes % 16 ||
         block_bytes > (1LL << 28))
         return CODEC_ERR_ARG;

@@ -196,3 +196,22 @@ def test_step_nan_of_no_weight_reaches_its_row(dt, sh, most):
         lm.step_q4(q, kc, vc, i32(tables), i32(lens), o, shared_table=i32(shared) if sh else None)
         assert lm.errors() == 0
         assert o[0, 0, 32:].isnan().all() and o[0, 0, :32].isfinite().all(), (where, heavy)
+
+
+# ---- blocks -----------------------------------------------------------------
+
+def test_copy_of_nothing():
+    """No entries: nothing is copied, and what a pool of one block's compaction leaves can
+    be handed on.  Caches are looked at all the same."""
+    lm = C.Lm(2, 2, 64, n_blocks=1, table_blocks=1, max_requests=1, max_rows=8)
+    cache = torch.arange(2 * 640, device="cuda").to(torch.uint8).view(1, 2, 640)
+    want, none, count = cache.clone(), i32([]), i32([7])
+    lm.compact(i32([16]), i32([[0]]), i32([[0]]), None, None, i32([0]), torch.zeros(2, dtype=torch.int64, device="cuda"),
+               none, none.clone(), count)
+    lm.copy_blocks([cache], none, none.clone(), count)
+    lm.copy_blocks([cache, cache.clone()], none, none.clone())
+    assert torch.equal(cache, want) and lm.errors() == 0 and count.item() == 0
+    with pytest.raises(C.CodecError):
+        lm.copy_blocks([], none, none.clone())
+    with pytest.raises(ValueError):
+        lm.copy_blocks([cache], none, i32([0]))
