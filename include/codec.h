@@ -874,7 +874,8 @@ CODEC_API codec_status codec_lm_load_q4(codec_lm_t* lm, const void* k_cache, con
  * positions of a shared part are read by every request.  For bf16 a long one (by
  * max_requests, the heads and its length: from about 16,384 tiles of 16 keys and 8
  * query heads) is turned into fp16 keys and values first, in a workspace of at most
- * 32,768 positions of one layer, and what is behind these is read by every request;
+ * 32,768 positions of one layer (which only an object has whose shape can come to
+ * that), and what is behind these is read by every request;
  * for fp16, whose results would show that rounding, it never is, which costs up to
  * three times as much behind many thousand positions.  A group that stands for NaN
  * makes what it takes part in NaN.  Errors as codec_lm_step. */

@@ -140,8 +140,9 @@ struct LmStepSpace {
     int* taken;                     // the same (behind done)
     int chunk_q4, max_splits_q4;    // chunk and max_splits over the cache in 4 bits
     unsigned char* zeros;           // two tiles of 16 positions in 4 bits that stand for zero
-    // A shared part in 4 bits, as halves (bf16): at most shared_q4 positions [shared_q4][hk][D],
-    // the queries [max_requests][hq][D] and their factors, and the numbers 0, 1, ..
+    // A shared part in 4 bits, as halves: at most shared_q4 positions [shared_q4][hk][D],
+    // the queries [max_requests][hq][D] and their factors, and the numbers 0, 1, ..;
+    // nothing of it where no shared part of the object comes to that (lm_halves_q4)
     int shared_q4;
     void *k16, *v16, *q16;
     float* row_c;
@@ -149,6 +150,14 @@ struct LmStepSpace {
 };
 constexpr int kLmZeroBytes = 2 * 16 * 128 * 5 / 8;
 constexpr int kLmSharedQ4 = 32768;
+// Sets of eight columns that a unit over 4 bits has.
+inline int lm_sets_q4(int group) { return group > 8 ? 2 : 1; }
+// Whether a shared part of len positions becomes halves: of an object for heads = max_requests
+// x kv_heads, by tiles of 16 keys and a unit's columns (both sides measured at the launch).
+inline bool lm_halves_q4(int type, int max_requests, long long heads, int group, long long len)
+{
+    return type == CODEC_LM_BF16 && max_requests > 1 && heads * group / (8 * lm_sets_q4(group)) * (len / 16) > 16384;
+}
 
 struct LmStepArgs {
     const void* q;

@@ -167,7 +167,8 @@ codec_status codec_lm_create(const codec_lm_config* cfg, codec_lm_t** out)
     sp.shared_ctas = (int)(pairs * c.kv_heads);
     sp.heads = heads;
     const int pre_max = lm_shared_splits(sp.shared_ctas, positions);
-    sp.shared_q4 = c.type == CODEC_LM_BF16 ? (int)std::min<int64_t>(positions, kLmSharedQ4) : 0;
+    const bool halves = lm_halves_q4(c.type, c.max_requests, heads, c.q_heads / c.kv_heads, positions);
+    sp.shared_q4 = halves ? (int)std::min<int64_t>(positions, kLmSharedQ4) : 0;
     LmBeamSpace& bm = lm->beam;
     bm.parts = lm_beam_parts(c.max_requests);
     LmPromptSpace& pr = lm->prompt;
@@ -189,8 +190,8 @@ codec_status codec_lm_create(const codec_lm_config* cfg, codec_lm_t** out)
         cudaMalloc(&sp.zeros, kLmZeroBytes) != cudaSuccess ||
         cudaMalloc(&sp.k16, 2 * (size_t)sp.shared_q4 * c.kv_heads * c.head_dim) != cudaSuccess ||
         cudaMalloc(&sp.v16, 2 * (size_t)sp.shared_q4 * c.kv_heads * c.head_dim) != cudaSuccess ||
-        cudaMalloc(&sp.q16, 2 * row * c.head_dim) != cudaSuccess ||
-        cudaMalloc(&sp.row_c, sizeof(float) * row) != cudaSuccess ||
+        cudaMalloc(&sp.q16, halves ? 2 * row * c.head_dim : 0) != cudaSuccess ||
+        cudaMalloc(&sp.row_c, halves ? sizeof(float) * row : 0) != cudaSuccess ||
         cudaMalloc(&sp.count, sizeof(int) * (sp.shared_q4 / c.block_size)) != cudaSuccess ||
         cudaMalloc(&sp.done, sizeof(int) * ((size_t)c.max_requests * c.kv_heads + 1)) != cudaSuccess) {
         cudaGetLastError();

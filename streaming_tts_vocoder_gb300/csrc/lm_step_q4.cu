@@ -840,10 +840,9 @@ cudaError_t launch(const LmShape& sh, const LmStepArgs& a, cudaStream_t s)
     // 256 behind 8,192: 484, 269, 82.4); what of it does not fit the workspace every
     // request reads.  Not for fp16: keys rounded to halves put its results off by 0.00054
     // of them, where they are by 0.0002 when they are rounded alone.
-    const int wide = sh.group > 8 ? 2 : 1;
-    const long long tiles = a.ws.heads * sh.group / (8 * wide) * (p.shared_len / 16);
-    if (a.ws.heads == sh.hk || p.shared_len <= 64) p.shared_len = 0;
-    if (p.shared_len > 0 && (tiles <= 16384 || !p.bf16)) {
+    const int wide = lm_sets_q4(sh.group), most = (int)(a.ws.heads / sh.hk);
+    if (most == 1 || p.shared_len <= 64) p.shared_len = 0;
+    if (p.shared_len > 0 && !lm_halves_q4(sh.type, most, a.ws.heads, sh.group, p.shared_len)) {
         p.n_shared = (p.shared_len + p.chunk - 1) / p.chunk;
         p.sets = (a.B * sh.group + 8 * wide - 1) / (8 * wide);
     } else if (p.shared_len > 0) {
@@ -872,11 +871,11 @@ cudaError_t launch(const LmShape& sh, const LmStepArgs& a, cudaStream_t s)
     int per_sm = 1;
     fit<D>(p, wide == 2 ? kCtas<D, 2> : kCtas<D, 1>, per_sm);
     // a unit per request and head at least, and no more CTAs than the SMs hold at once
-    const long long most = ((long long)a.B * p.max_splits + (long long)p.n_shared * p.sets) * sh.hk;
-    const unsigned ctas = (unsigned)std::min<long long>(152 * per_sm, (most + kWarps - 1) / kWarps);
+    const long long units = ((long long)a.B * p.max_splits + (long long)p.n_shared * p.sets) * sh.hk;
+    const unsigned ctas = (unsigned)std::min<long long>(152 * per_sm, (units + kWarps - 1) / kWarps);
     const bool two = p.n_pre + p.n_shared > 0 || p.max_splits > 1;
     // from the counter where a warp has more than one
-    p.taken = two && most > (long long)ctas * kWarps ? a.ws.taken : nullptr;
+    p.taken = two && units > (long long)ctas * kWarps ? a.ws.taken : nullptr;
     auto kernel = p.bf16 ? (wide == 2 ? lm_step_q4_kernel<D, 2, false> : lm_step_q4_kernel<D, 1, false>)
                          : (wide == 2 ? lm_step_q4_kernel<D, 2, true> : lm_step_q4_kernel<D, 1, true>);
     const cudaError_t e = launch_pdl(kernel, dim3(ctas), dim3(kThreads), smem_bytes<D>(p.stages, a.B), s, p);

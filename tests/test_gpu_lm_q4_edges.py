@@ -215,3 +215,29 @@ def test_copy_of_nothing():
         lm.copy_blocks([], none, none.clone())
     with pytest.raises(ValueError):
         lm.copy_blocks([cache], none, i32([0]))
+
+
+# ---- objects ----------------------------------------------------------------
+
+def taken(**kw):
+    torch.cuda.synchronize()
+    before = torch.cuda.mem_get_info()[0]
+    lm = C.Lm(8, 8, 128, n_blocks=2, max_rows=8, **kw)
+    return before - torch.cuda.mem_get_info()[0], lm
+
+
+@pytest.mark.parametrize("kw,much", [
+    (dict(table_blocks=2048, max_requests=1), False),       # the way is closed to one request
+    (dict(table_blocks=200, max_requests=64), False),       # 64 sets of 8 columns x 200 tiles of 16 keys: below 16,384
+    (dict(table_blocks=2048, max_requests=64), True),
+])
+def test_workspace_of_a_long_shared_part(kw, much):
+    """An object has room for a long shared part as halves only where its shape can come to
+    that: one of bf16 takes what one of fp16 takes, which never does."""
+    kw = dict(block_size=16, **kw)
+    taken(dtype="fp16", **kw)
+    halves, _ = taken(dtype="fp16", **kw)
+    wide, _ = taken(dtype="bf16", **kw)
+    more = 2 * 2 * min(kw["table_blocks"] * 16, 32768) * 8 * 128
+    slack = 4 << 20                     # small arrays share what is handed out at once, 2 MB
+    assert abs(wide - halves - (more if much else 0)) <= slack, (wide, halves)
