@@ -9,7 +9,7 @@ import torch
 
 import lm_q4_ref as Q
 from streaming_tts_vocoder_gb300 import codec as C
-from test_gpu_lm_q4 import cache_q4, check_beams, f64, gpu, i32, logits, step_reference
+from test_gpu_lm_q4 import as_halves, cache_q4, check_beams, f64, gpu, i32, step_reference
 
 pytestmark = pytest.mark.gpu
 T = Q.DTYPES
@@ -196,6 +196,39 @@ def test_step_nan_of_no_weight_reaches_its_row(dt, sh, most):
         lm.step_q4(q, kc, vc, i32(tables), i32(lens), o, shared_table=i32(shared) if sh else None)
         assert lm.errors() == 0
         assert o[0, 0, 32:].isnan().all() and o[0, 0, :32].isfinite().all(), (where, heavy)
+
+
+@pytest.mark.parametrize("hq,hk,d,bs,sh,mul", [(8, 2, 128, 16, 66, 1.0), (16, 1, 64, 32, 40, 3.0), (4, 4, 128, 128, 20, 1.0)])
+def test_step_long_shared_part_against_its_own_values(hq, hk, d, bs, sh, mul):
+    """What a long shared part's halves put off, against the cache's values as they are.
+    A key rounded to fp16 moves a score by sum |q| |k| 2^-11 of scale, at most as much of
+    which is common to all keys, so a probability by twice that; a value moves by 2^-11."""
+    assert as_halves(torch.bfloat16, 4096, hq, hk, sh * bs) == sh * bs
+    lens = [sh * bs, sh * bs + 1, sh * bs + 333, sh * bs - 5, 40, 0]
+    kc, vc, tables, shared, n_blocks, width = cache_q4(21, lens, hk, d, bs, sh)
+    gen = torch.Generator(device="cuda").manual_seed(21)
+    q = (torch.randn(len(lens), hq, d, generator=gen, device="cuda") * mul).bfloat16()
+    o, lse = torch.zeros_like(q), torch.zeros(len(lens), hq, device="cuda")
+    lm = C.Lm(hq, hk, d, "bf16", block_size=bs, n_blocks=n_blocks, table_blocks=width, max_requests=4096, max_rows=8)
+    lm.step_q4(q, kc, vc, i32(tables), i32(lens), o, shared_table=i32(shared), lse=lse)
+    assert lm.errors() == 0
+    ref = step_reference(q, kc, vc, tables, lens, shared, hk, d, bs)            # nothing of it rounded
+    want, want_lse, al, ac, s, n = ref
+    moved = (s * 2.0 ** -11)[..., None]
+    ds = (4 * d * 2.0 ** -23 * (s + 1))[..., None]
+    n = n[:, None, None]
+    tol = 2.0 ** -9 * np.abs(want) * 1.01 + al * 2.0 ** -11 * 1.01 + ac * 2.0 ** -10 * 1.01
+    tol = tol + (al + ac) * (np.exp(2 * (moved + ds)) - 1 + 2.0 ** -11 + (n / 8 + 16) * 2.0 ** -23)
+    tol = tol + n * 2.0 ** -31 * (15 + 12.0) * 6.0 + 1e-30
+    off = np.abs(f64(o) - want)
+    assert (off <= tol).all(), f"{(off / tol).max():.3g} x the bound"
+    seen = ~np.isneginf(want_lse)
+    far = np.abs(f64(lse) - np.where(seen, want_lse, 0))[seen]
+    assert (far <= ((moved + ds)[..., 0] + (np.abs(np.where(seen, want_lse, 0)) + 4) * 2.0 ** -20)[seen]).all()
+    # in all: the result's own rounding is 2^-9 / sqrt(3) on average (0.0011); the keys' move a
+    # score by 2^-11 / sqrt(3) of the root of the sum of scale^2 (q k)^2, 4 at most (0.0011)
+    rel = np.linalg.norm(f64(o) - want) / np.linalg.norm(want)
+    assert rel < 2.0 ** -8, rel
 
 
 # ---- blocks -----------------------------------------------------------------
