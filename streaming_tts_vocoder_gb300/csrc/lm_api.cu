@@ -151,6 +151,10 @@ codec_status codec_lm_create(const codec_lm_config* cfg, codec_lm_t** out)
     // 22.0; 1 x 9,000 39.7, 22.5, 18.6, 18.1, 23.5; 16 x 3,000 to 3,750 56.6, 39.0, 29.3,
     // 23.9, 27.2; 64 of 1 to 1,500 (16 / 16 of 64) 24.3, 17.9, 18.5, 17.2, 23.5; 256 of 500
     // to 4,000 (32 / 8) 457, 306, 216, 172, 155; 64 x 250 21.1, 19.7, 15.1, whole 13.5.
+    // 256 and 512 by positions a warp: 2,000 (64 of 500 to 7,000, 32 / 8) 62.6, 60.7; 2,260
+    // (128 of up to 4,000) 73.5, 76.8; 3,950 (128 of up to 7,000) 102, 92; 4,490 (64 of up to
+    // 8,000, 16 / 16 of 64) 87.8, 79.8; 8,430 (64 of up to 30,000) 157 both; 8,980 (256 of up
+    // to 8,000) 199, 177.
     const int64_t each = heads * positions / 1824;
     sp.chunk_q4 = 32;
     while ((sp.chunk_q4 < each && sp.chunk_q4 < (each >= 4096 ? 512 : 256)) || positions > 64LL * sp.chunk_q4 ||

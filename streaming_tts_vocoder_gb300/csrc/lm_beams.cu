@@ -17,12 +17,12 @@
 // logarithms of those rows are worked out again to about 1e-9, and the choice is made
 // once more.
 //
-// 1,024 rows of 65,537 in bf16 (60 of them ended): 37.6 us, 3.4 TB/s; 30 of it before the
+// 1,024 rows of 65,537 in bf16 (60 of them ended): 38.2 us, 3.3 TB/s; 30 of it before the
 // search.  Neither the memory nor the issue slots bound it: a chunk's loads, maxima and
 // sums follow one another in each warp, and all rows are one wave of CTAs, whose last
 // stretch is the search.  The next chunk in registers meanwhile (spills), prefetches two
 // chunks ahead (+1.5 us), six CTAs an SM (two waves, 54 us), ten (48), twice as many parts
-// of a row (43) were slower.  4 x 4 of 2,048: 9.4 us, two launches and the second one's
+// of a row (43) were slower.  4 x 4 of 2,048: 9.9 us, two launches and the second one's
 // chain of steps.
 //
 // Logarithms that are worked out again are a CTA's for each group, a row after the other:
@@ -396,8 +396,10 @@ __global__ void __launch_bounds__(kRowThreads, 8) lm_beam_rows_kernel(const LmBe
     }
 }
 
-// exp(d + e) as 2^k 2^(j / 64) (1 + p): k, the power of two of the table (two floats),
-// and p, a short series of what is left (at most ln 2 / 128).  e: a small rest of d.
+// exp(d + e) by a table and a series (P. T. P. Tang, "Table-driven implementation of the
+// exponential function in IEEE floating-point arithmetic", ACM TOMS 15, 1989) as 2^k 2^(j / 64)
+// (1 + p): k, the power of two of the table (two floats), and p, a short series of what
+// is left (at most ln 2 / 128).  e: a small rest of d.
 __device__ __forceinline__ float2 exp_parts(float d, float e, const float2* table, float& p, float& scale)
 {
     constexpr float kInv = 92.332482616893656f;             // 64 / ln 2
@@ -411,8 +413,8 @@ __device__ __forceinline__ float2 exp_parts(float d, float e, const float2* tabl
     return table[im & 63];
 }
 
-// log(s) to about 1e-9, s in 2^-64 .. 2^64: fp32's, and how far s is from its exponential
-// (log() itself takes some 2 us, fp64 being slow).
+// log(s) to about 1e-9, s in 2^-64 .. 2^64: fp32's, and how far s is from its exponential, a
+// step of Newton's method (log() itself takes some 2 us, fp64 being slow).
 __device__ __forceinline__ double log_of(double s, const float2* table)
 {
     const float y = logf((float)s);

@@ -30,10 +30,10 @@
 // finer than halves' smallest step lets them (see kSmall).
 //
 // What bounds it: instructions and their latency, not the memory.  A tile of 16 keys and
-// values of 128 takes 252 instructions (80 make operands of codes, 18 are MMAs), a unit
-// 980 more, and accumulators and operands leave room for 12 warps an SM, which use 42 %
+// values of 128 takes 247 instructions (80 make operands of codes, 18 are MMAs), a unit
+// 910 more, and accumulators and operands leave room for 12 warps an SM, which use 42 %
 // of the issue slots: 64 requests of 2,000 positions (32 / 8 heads of 128) 49 us, 3.4
-// TB/s; 64 of 750 (16 heads of 64) 31 us.  256 of 500 to 4,000 behind 8,192: 159 us,
+// TB/s; 64 of 750 (16 heads of 64) 31 us.  256 of 500 to 4,000 behind 8,192: 161 us,
 // where 16 bits take 277.  Measured and slower: one tile at a time and four CTAs (184 us
 // against 164), four CTAs at width 64 (34.6 against 31.8), the next unit's blocks or
 // queries asked for ahead (170; registers spill), each request's last chunk in quarters
@@ -838,7 +838,10 @@ cudaError_t launch(const LmShape& sh, const LmStepArgs& a, cudaStream_t s)
     // 1 to 500 behind 256, as many: 53.3, 44.8, 49.5).  Beyond, it is turned into halves
     // and the prompt kernel's (behind 4,096, 64 x 16 heads, 32,768 tiles: 113, 39.4, 36.7;
     // 256 behind 8,192: 484, 269, 82.4); what of it does not fit the workspace every
-    // request reads.  Not for fp16: keys rounded to halves put its results off by 0.00054
+    // request reads.  As units and as halves in front of 1 to 500 positions, by thousands of
+    // tiles, 64 x 32 / 8: 12 21.5, 25.1; 16 21.8, 25.2; 20 28.0, 26.0; 25 34.8, 26.4; 64 x 16 / 16 of
+    // 64: 12 25.7, 26.7; 16 28.1, 26.9; 20 29.5, 26.4; 33 30.4, 28.3; 256 x 32 / 8: 16 42.0, 47.2; 20
+    // 46.8, 47.1; 25 48.8, 47.2; 33 51.5, 49.2; 32 x 16 / 8: 16 22.3, 25.0; 33 38.4, 31.8.  Not for fp16: keys rounded to halves put its results off by 0.00054
     // of them, where they are by 0.0002 when they are rounded alone.
     const int wide = lm_sets_q4(sh.group), most = (int)(a.ws.heads / sh.hk);
     if (most == 1 || p.shared_len <= 64) p.shared_len = 0;
