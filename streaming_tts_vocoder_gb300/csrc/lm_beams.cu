@@ -454,10 +454,10 @@ __device__ double exact_log_sum(const T* x, int n, float top, const float2* tabl
     return log_of(sum, table);
 }
 
-// A score as a whole number of the same order, and back.
+// A score as a whole number of the same order, and back.  Zeros of both signs are one.
 __device__ __forceinline__ unsigned long long key_of(double s)
 {
-    const long long bits = __double_as_longlong(s);
+    const long long bits = __double_as_longlong(__dadd_rn(s, 0.));
     return bits < 0 ? ~(unsigned long long)bits : (unsigned long long)bits | 1ULL << 63;
 }
 __device__ __forceinline__ double score_of(unsigned long long key)

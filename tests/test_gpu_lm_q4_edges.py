@@ -97,6 +97,18 @@ def test_beams_rows_of_a_value_each(dt, vocab, k):
         assert got[1] == [int(sums.argmax())] * k and got[2] == list(range(k))
 
 
+@pytest.mark.parametrize("dt", ["bf16", "fp16", "fp32"])
+def test_beams_sums_of_zero_of_either_sign(dt):
+    """0 and -0 are equal: ended beams, and ones whose one token is certain, in order of beams."""
+    k, vocab = 5, 40
+    x = torch.full((2 * k, vocab), -float("inf"), dtype=T[dt], device="cuda")
+    x[:, 7], x[3, 7], x[8, 7] = 0.0, -0.0, -2.0
+    for sums in ([0.0, -0.0, 0.0, -0.0, 0.0, -0.0, 0.0, -0.0, 0.0, -0.0], [-0.0] * 3 + [0.0] * 4 + [-0.0] * 3):
+        for ended in ([0, 0, 1, 0, 1, 1, 0, 1, 0, 0], [1] * 10, [0] * 10):
+            got = check_beams(x, k, sums, ended, 7)
+            assert got[1] == list(range(2 * k))
+
+
 # ---- store ------------------------------------------------------------------
 
 @pytest.mark.parametrize("hk,d,dt", [(3, 128, "bf16"), (2, 64, "fp16")])
