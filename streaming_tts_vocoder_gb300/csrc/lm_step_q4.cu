@@ -839,10 +839,11 @@ cudaError_t launch(const LmShape& sh, const LmStepArgs& a, cudaStream_t s)
     // and the prompt kernel's (behind 4,096, 64 x 16 heads, 32,768 tiles: 113, 39.4, 36.7;
     // 256 behind 8,192: 484, 269, 82.4); what of it does not fit the workspace every
     // request reads.  As units and as halves in front of 1 to 500 positions, by thousands of
-    // tiles, 64 x 32 / 8: 12 21.5, 25.1; 16 21.8, 25.2; 20 28.0, 26.0; 25 34.8, 26.4; 64 x 16 / 16 of
-    // 64: 12 25.7, 26.7; 16 28.1, 26.9; 20 29.5, 26.4; 33 30.4, 28.3; 256 x 32 / 8: 16 42.0, 47.2; 20
-    // 46.8, 47.1; 25 48.8, 47.2; 33 51.5, 49.2; 32 x 16 / 8: 16 22.3, 25.0; 33 38.4, 31.8.  Not for fp16: keys rounded to halves put its results off by 0.00054
-    // of them, where they are by 0.0002 when they are rounded alone.
+    // tiles: 64 x 32 / 8, 12 21.5, 25.1; 16 21.8, 25.2; 20 28.0, 26.0; 25 34.8, 26.4; 64 x 16 / 16
+    // of 64, 12 25.7, 26.7; 16 28.1, 26.9; 20 29.5, 26.4; 33 30.4, 28.3; 256 x 32 / 8, 16 42.0,
+    // 47.2; 20 46.8, 47.1; 25 48.8, 47.2; 33 51.5, 49.2; 32 x 16 / 8, 16 22.3, 25.0; 33 38.4, 31.8.
+    // Not for fp16: keys rounded to halves put its results off by 0.00054 of them, where they
+    // are by 0.0002 when they are rounded alone.
     const int wide = lm_sets_q4(sh.group), most = (int)(a.ws.heads / sh.hk);
     if (most == 1 || p.shared_len <= 64) p.shared_len = 0;
     if (p.shared_len > 0 && !lm_halves_q4(sh.type, most, a.ws.heads, sh.group, p.shared_len)) {
